@@ -549,6 +549,186 @@ int moe_balance_update_window(const moe_config_t* cfg, const int32_t* idx, int64
                               int64_t* ring, int32_t window, int64_t* step, float alpha,
                               float* bias, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The rest of a training block around the MoE layer.  The pages' model is 48
+ * blocks of an attention branch and a sparse MoE branch; these four operators
+ * are what a block runs beside moe_layer_forward / moe_layer_backward: the
+ * norms around each branch with the residual sum, rotary positions, causal
+ * attention over packed sequences, and the clipping of the gradients.  The
+ * conventions above hold (device pointers, no allocation, no host
+ * synchronisation, deterministic results); an empty call (T = 0, no tensors)
+ * returns MOE_OK without touching its pointers. */
+
+/* Norm after a branch, gate, residual sum, norm before the next branch:
+ *   p = b * rstd_post,  rstd_post = 1/sqrt(mean(b^2) + eps)
+ *   y = alpha * r + beta * g * (p * w_post)
+ *   n = (y * rstd_pre) * w_pre,  rstd_pre = 1/sqrt(mean(y^2) + eps)
+ * with the means over the d channels of a token, everything in fp32 and y
+ * unrounded where n is computed; each output is rounded once.
+ *   b      [T, d] bf16, the branch's output, or NULL: y = alpha * r
+ *   r      [T, d] the residual stream, bf16 (res_f32 = 0) or fp32 (1)
+ *   gate   bf16: [d], the same for every token (gate_per_token = 0), or
+ *          [T, d] (1); NULL: 1.  NULL when b is NULL.
+ *   w_post [d] bf16 (NULL exactly when b is), w_pre [d] bf16
+ *   y      [T, d] as r (out; may be r itself), NULL: not written
+ *   n      [T, d] bf16 (out; may be b itself), NULL (w_pre NULL too): no
+ *          next norm
+ *   rstd_post, rstd_pre [T] fp32 (out), what the backward reads; each NULL
+ *          when its norm is absent or no gradient is wanted
+ * d a multiple of 8, 8 <= d <= 8192. */
+typedef struct moe_norm {
+    int64_t T;
+    int32_t d;
+    int32_t res_f32;
+    int32_t gate_per_token;
+    float alpha, beta, eps;
+} moe_norm_t;
+
+int moe_norm_residual(const moe_norm_t* cfg, const uint16_t* b, const void* r,
+                      const uint16_t* gate, const uint16_t* w_post, const uint16_t* w_pre,
+                      void* y, uint16_t* n, float* rstd_post, float* rstd_pre, void* stream);
+
+/* Gradients of moe_norm_residual for dn (of n) and dy (of y; the part that
+ * reaches the residual stream past this norm).  y is computed again from r
+ * and b in fp32.  With q = y rstd_pre, m = p w_post:
+ *   du = dy + rstd_pre (dn w_pre - q mean(dn w_pre q)),  dr = alpha du
+ *   dgate = beta m du (per token, or summed over the tokens for a [d] gate)
+ *   dm = beta g du,  dp = dm w_post,  db = rstd_post (dp - p mean(dp p))
+ *   dw_post = sum_t dm p,  dw_pre = sum_t dn q
+ *   dn [T, d] bf16 (NULL: no next norm in the forward), dy [T, d] as r
+ *   (NULL: zero); not both NULL
+ *   db [T, d] bf16, dr [T, d] as r (may be dy itself), dgate [d] fp32 or
+ *   [T, d] bf16, dw_post, dw_pre [d] fp32 (all out; NULL exactly where the
+ *   forward's tensor is)
+ *   ws: scratch of moe_norm_residual_workspace bytes for the sums over the
+ *   tokens, which are taken in a fixed order. */
+int moe_norm_residual_workspace(int64_t T, int32_t d, int64_t* bytes);
+int moe_norm_residual_backward(const moe_norm_t* cfg, const uint16_t* dn, const void* dy,
+                               const uint16_t* b, const void* r, const uint16_t* gate,
+                               const uint16_t* w_post, const uint16_t* w_pre,
+                               const float* rstd_post, const float* rstd_pre, uint16_t* db,
+                               void* dr, void* dgate, float* dw_post, float* dw_pre, void* ws,
+                               int64_t ws_bytes, void* stream);
+
+/* Table of rotary angles: table[p][i] = {m cos(p f_i), m sin(p f_i)} for
+ * positions p < rows and pairs i < rot_dim / 2, f_i = base^(-2i / rot_dim),
+ * the angles and their sines in 64 bits, stored in fp32.  For contexts longer
+ * than the trained one (the pages train at 4K and extend to 262K):
+ *   scaling 0  none (factor 1)
+ *   scaling 1  linear: f_i / factor (positions interpolated)
+ *   scaling 2  base: base * factor^(rot_dim / (rot_dim - 2)), rot_dim > 2
+ *   scaling 3  by parts: with t_i = orig_len f_i / (2 pi) turns over the
+ *              trained length, f_i is kept for t_i >= beta_fast, divided by
+ *              factor for t_i <= beta_slow, and mixed linearly in t_i between
+ * m = magnitude scales both (1: a pure rotation).
+ *   table [rows, rot_dim / 2, 2] fp32 (out). */
+typedef struct moe_rotary_table {
+    int64_t rows;
+    int32_t rot_dim;
+    int32_t scaling;
+    double base, factor, orig_len, beta_fast, beta_slow, magnitude;
+} moe_rotary_table_t;
+
+int moe_rotary_make_table(const moe_rotary_table_t* cfg, float* table, void* stream);
+
+/* Rotary positions for the query and key heads: in the first rot_dim
+ * channels of every head, the pair (x1, x2) becomes
+ *   (x1 c - x2 s, x2 c + x1 s),  {c, s} = table[pos[t]][i]
+ * with s negated when inverse = 1 (the gradient's direction); the other
+ * channels are copied.  Pair i is channels (i, i + rot_dim/2), or with
+ * interleaved = 1 channels (2i, 2i + 1).
+ *   q [T, hq, D], k [T, hk, D] bf16 with the given strides (elements) between
+ *   tokens and heads, channels contiguous; outputs likewise, and each output
+ *   may be its input (same strides) but not otherwise overlap it
+ *   pos [T] int32, or NULL: pos[t] = t.  A position outside the table gives
+ *   MOE_EINVAL in status and leaves that token's outputs unwritten.
+ * D and the strides multiples of 8, rot_dim a multiple of 16, 16 <= rot_dim <=
+ * D <= 1024; hk = 0 (k NULL) allowed. */
+typedef struct moe_rotary {
+    int64_t T;
+    int32_t hq, hk, D, rot_dim, interleaved, inverse;
+    int64_t table_rows;
+    int64_t q_t, q_h, k_t, k_h;       /* input strides, elements                     */
+    int64_t qo_t, qo_h, ko_t, ko_h;   /* output strides                              */
+} moe_rotary_t;
+
+int moe_rotary(const moe_rotary_t* cfg, const uint16_t* q, const uint16_t* k,
+               const float* table, const int32_t* pos, uint16_t* q_out, uint16_t* k_out,
+               int32_t* status, void* stream);
+
+/* Causal attention over packed sequences with grouped heads: token i of a
+ * sequence attends to its tokens j <= i,
+ *   s_ij = scale q_i . k_j,  P_i = softmax_j(s_ij),  o_i = sum_j P_ij v_j
+ * query head h reading key/value head h / (n_heads / n_kv_heads).
+ * Sequence s holds tokens cu[s] .. cu[s+1) of the T packed ones, cu [n_seqs +
+ * 1] int32 on the device, non-decreasing, within [0, T] (a sequence may be
+ * empty); tokens before cu[0] and from cu[n_seqs] on belong to none: their
+ * outputs and gradients are zero, their lse -infinity.  A value that the mask
+ * hides from a token never reaches its outputs, NaN and infinities included.
+ * All tensors bf16 [T, heads, head_dim] with strides (elements, multiples of
+ * 8) between tokens and heads and contiguous channels; head_dim a multiple of
+ * 8, 8 <= head_dim <= 128; n_heads a multiple of n_kv_heads; scale > 0.
+ * Products accumulate in fp32; P and, in the backward, dS are rounded to bf16
+ * as the operands of the next product.
+ *
+ * moe_attention_workspace: bytes of the plan and of the backward's scratch.
+ * moe_attention_plan: the work lists of one batch of sequences, from cu, on
+ *   the stream (no host synchronisation), for any number of forward and
+ *   backward calls of these sizes; cu that is decreasing or out of range
+ *   gives MOE_EINVAL in status and lists without work.
+ * moe_attention_forward: out [T, n_heads, D]; lse [n_heads, T] fp32 =
+ *   ln sum_j exp(s_ij); rest (same layout as out, NULL when no gradient is
+ *   wanted) = bf16(o - out), what rounding took from out.
+ * moe_attention_backward: dq, dk, dv for the upstream gradient dout, from
+ *   the forward's inputs and out, rest, lse (D_i = dout_i . (out_i + rest_i)
+ *   needs o to more than bf16 where P_i is nearly one key's).  dk and dv are
+ *   summed over a group's query heads in fp32. */
+typedef struct moe_attention {
+    int64_t T;
+    int32_t n_seqs, n_heads, n_kv_heads, head_dim;
+    float scale;
+    int32_t reserved;                  /* must be 0                                  */
+    int64_t q_t, q_h, k_t, k_h, v_t, v_h;   /* strides between tokens and heads      */
+    int64_t o_t, o_h;                       /* out and rest                          */
+    int64_t do_t, do_h, dq_t, dq_h, dk_t, dk_h, dv_t, dv_h;   /* backward only       */
+} moe_attention_t;
+
+int moe_attention_workspace(const moe_attention_t* cfg, int64_t* plan_bytes,
+                            int64_t* backward_bytes);
+int moe_attention_plan(const moe_attention_t* cfg, const int32_t* cu, void* plan,
+                       int64_t plan_bytes, int32_t* status, void* stream);
+int moe_attention_forward(const moe_attention_t* cfg, const void* plan, const uint16_t* q,
+                          const uint16_t* k, const uint16_t* v, uint16_t* out, uint16_t* rest,
+                          float* lse, int32_t* status, void* stream);
+int moe_attention_backward(const moe_attention_t* cfg, const void* plan, const uint16_t* q,
+                           const uint16_t* k, const uint16_t* v, const uint16_t* out,
+                           const uint16_t* rest, const float* lse, const uint16_t* dout,
+                           uint16_t* dq, uint16_t* dk, uint16_t* dv, void* ws, int64_t ws_bytes,
+                           int32_t* status, void* stream);
+
+/* Global gradient norm over many tensors, and clipping:
+ *   norm = sqrt(sum over all tensors and elements of g^2)
+ *   out  = g * c,  c = min(1, max_norm / (norm + 1e-6))
+ * The sum is exact to fp32 for any finite gradients (no overflow or underflow
+ * of the squares).  When norm is not finite, c = 1: the gradients stay as
+ * they are and the caller, who reads norm, decides.
+ *   tensors: host array of n_tensors records {in, out, numel, is_bf16}; out
+ *   may be in (then nothing is written when c = 1); pointers 4-byte (bf16:
+ *   2-byte) aligned; out of a tensor overlaps no other tensor.
+ *   max_norm > 0 (infinity: the norm alone decides nothing, c = 1)
+ *   norm [1] fp32 (out)   ws: scratch of moe_grad_clip_workspace bytes. */
+typedef struct moe_grad_tensor {
+    const void* in;
+    void* out;
+    int64_t numel;
+    int32_t is_bf16;
+    int32_t reserved;
+} moe_grad_tensor_t;
+
+int moe_grad_clip_workspace(int64_t n_tensors, int64_t* bytes);
+int moe_grad_clip(const moe_grad_tensor_t* tensors, int64_t n_tensors, float max_norm,
+                  float* norm, void* ws, int64_t ws_bytes, void* stream);
+
 /* Index checks of a checked build (compiled with -DMOE_CHECK=1; the pages
  * define no such operation): every row, slot, expert and tile index the
  * kernels compute is checked before use; a failed check skips the access

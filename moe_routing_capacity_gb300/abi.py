@@ -29,7 +29,11 @@ EXPORTS = ("moe_plan", "moe_router_topk", "moe_latent_proj", "moe_route_project"
            "moe_layer_backward_ragged", "moe_combine", "moe_trace_begin", "moe_trace_mark",
            "moe_trace_end", "moe_trace_event", "moe_check_status", "moe_strerror",
            "moe_abi_version", "moe_layer_forward", "moe_host_pipe_create", "moe_host_pipe_submit",
-           "moe_host_pipe_sync", "moe_host_pipe_destroy")
+           "moe_host_pipe_sync", "moe_host_pipe_destroy",
+           "moe_norm_residual", "moe_norm_residual_workspace", "moe_norm_residual_backward",
+           "moe_rotary_make_table", "moe_rotary", "moe_attention_workspace",
+           "moe_attention_plan", "moe_attention_forward", "moe_attention_backward",
+           "moe_grad_clip_workspace", "moe_grad_clip")
 # Declared in the header too, but exported by the checked build only.
 CHECKED_ONLY = ("moe_check_set_wave_wait_limit_ns",)
 
@@ -95,6 +99,43 @@ class LayerBuffers(ctypes.Structure):
     _fields_ = [(f, ctypes.c_size_t if f.endswith("_bytes") else ctypes.c_void_p)
                 for f in LAYER_BUFFER_FIELDS]
 
+
+class Norm(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("d", ctypes.c_int32), ("res_f32", ctypes.c_int32),
+                ("gate_per_token", ctypes.c_int32), ("alpha", ctypes.c_float),
+                ("beta", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class RotaryTable(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("orig_len", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("magnitude", ctypes.c_double)]
+
+
+class Rotary(ctypes.Structure):
+    _fields_ = ([("T", ctypes.c_int64)] +
+                [(f, ctypes.c_int32) for f in ("hq", "hk", "D", "rot_dim", "interleaved",
+                                               "inverse")] +
+                [(f, ctypes.c_int64) for f in ("table_rows", "q_t", "q_h", "k_t", "k_h", "qo_t",
+                                               "qo_h", "ko_t", "ko_h")])
+
+
+class Attention(ctypes.Structure):
+    _fields_ = ([("T", ctypes.c_int64)] +
+                [(f, ctypes.c_int32) for f in ("n_seqs", "n_heads", "n_kv_heads", "head_dim")] +
+                [("scale", ctypes.c_float), ("reserved", ctypes.c_int32)] +
+                [(f, ctypes.c_int64) for f in ("q_t", "q_h", "k_t", "k_h", "v_t", "v_h", "o_t",
+                                               "o_h", "do_t", "do_h", "dq_t", "dq_h", "dk_t",
+                                               "dk_h", "dv_t", "dv_h")])
+
+
+class GradTensor(ctypes.Structure):
+    _fields_ = [("in", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("is_bf16", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -159,6 +200,19 @@ def load_library(path: str) -> ctypes.CDLL:
     L.moe_host_pipe_submit.argtypes = [vp, pb, vp, vp, vp, vp]
     L.moe_host_pipe_sync.argtypes = [vp]
     L.moe_host_pipe_destroy.argtypes = [vp]
+    pi64 = ctypes.POINTER(i64)
+    pn, pa = ctypes.POINTER(Norm), ctypes.POINTER(Attention)
+    L.moe_norm_residual.argtypes = [pn] + [vp] * 10
+    L.moe_norm_residual_workspace.argtypes = [i64, i32, pi64]
+    L.moe_norm_residual_backward.argtypes = [pn] + [vp] * 15 + [i64, vp]
+    L.moe_rotary_make_table.argtypes = [ctypes.POINTER(RotaryTable), vp, vp]
+    L.moe_rotary.argtypes = [ctypes.POINTER(Rotary)] + [vp] * 8
+    L.moe_attention_workspace.argtypes = [pa, pi64, pi64]
+    L.moe_attention_plan.argtypes = [pa, vp, vp, i64, vp, vp]
+    L.moe_attention_forward.argtypes = [pa] + [vp] * 9
+    L.moe_attention_backward.argtypes = [pa] + [vp] * 12 + [i64, vp, vp]
+    L.moe_grad_clip_workspace.argtypes = [i64, pi64]
+    L.moe_grad_clip.argtypes = [ctypes.POINTER(GradTensor), i64, ctypes.c_float, vp, vp, i64, vp]
     if hasattr(L, "moe_check_set_wave_wait_limit_ns"):
         L.moe_check_set_wave_wait_limit_ns.argtypes = [ctypes.c_ulonglong]
         L.moe_check_set_wave_wait_limit_ns.restype = ctypes.c_int
@@ -496,3 +550,249 @@ def layer_backward(cfg, tensors: dict, ws, status, stream=None):
     fn = "moe_layer_backward" if eoff is None else "moe_layer_backward_ragged"
     _check(fn, getattr(lib(), fn)(ctypes.byref(make_config(cfg)), ctypes.byref(args),
                                   _stream(stream)))
+
+
+# ---------------------------------------------------------------- training block
+
+def _rows(name, t, T, d, dtypes, allow_none=False):
+    """Device pointer of a contiguous [T, d] (or [d], with T None) tensor."""
+    if t is None and allow_none:
+        return None
+    if t is None:
+        raise ValueError(f"{name}: tensor required")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if tuple(t.shape) != ((d,) if T is None else (T,) if d is None else (T, d)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def _norm_config(r, gate, alpha, beta, eps):
+    if r.dim() != 2:
+        raise ValueError("the residual stream is [T, d]")
+    T, d = r.shape
+    per_token = gate is not None and gate.dim() == 2
+    return T, d, Norm(T, d, int(r.dtype == f32), int(per_token), alpha, beta, eps)
+
+
+def norm_residual(b, r, gate, w_post, w_pre, y, n, rstd_post=None, rstd_pre=None, alpha=1.0,
+                  beta=1.0, eps=1e-6, stream=None):
+    """y = alpha r + beta gate (norm(b) w_post), n = norm(y) w_pre, in one pass:
+    the norm after a branch (output b [T, d] bf16, or None: y = alpha r), its
+    gate ([d], [T, d] or None), the residual sum (r, y [T, d] bf16 or fp32; y
+    may be r, or None) and the norm before the next branch (n [T, d] bf16, or
+    None).  rstd_post, rstd_pre [T] fp32 receive the statistics that the
+    backward reads (None: not wanted)."""
+    T, d, c = _norm_config(r, gate, alpha, beta, eps)
+    rt = (r.dtype,)
+    _check("moe_norm_residual", lib().moe_norm_residual(
+        ctypes.byref(c), _rows("b", b, T, d, (bf16,), True), _rows("r", r, T, d, (bf16, f32)),
+        _rows("gate", gate, T if c.gate_per_token else None, d, (bf16,), True),
+        _rows("w_post", w_post, None, d, (bf16,), True),
+        _rows("w_pre", w_pre, None, d, (bf16,), True), _rows("y", y, T, d, rt, True),
+        _rows("n", n, T, d, (bf16,), True), _rows("rstd_post", rstd_post, T, None, (f32,), True),
+        _rows("rstd_pre", rstd_pre, T, None, (f32,), True), _stream(stream)))
+
+
+def norm_residual_workspace(T, d) -> int:
+    """Scratch bytes of norm_residual_backward."""
+    v = ctypes.c_int64()
+    _check("moe_norm_residual_workspace",
+           lib().moe_norm_residual_workspace(T, d, ctypes.byref(v)))
+    return v.value
+
+
+def norm_residual_backward(dn, dy, b, r, gate, w_post, w_pre, rstd_post, rstd_pre, db, dr, dgate,
+                           dw_post, dw_pre, ws, alpha=1.0, beta=1.0, stream=None):
+    """Gradients of norm_residual for dn (of n) and dy (of y, the part that
+    passes this norm by; None: zero): db, dr (may be dy), dgate ([d] fp32 for
+    a [d] gate, else [T, d] bf16), dw_post, dw_pre [d] fp32.  None exactly
+    where the forward's tensor is."""
+    shape = dr
+    T, d, c = _norm_config(shape, gate, alpha, beta, 0.0)
+    if r is not None and r.dtype != dr.dtype:
+        raise TypeError("dr has the residual stream's type")
+    rt = (dr.dtype,)
+    _check("moe_norm_residual_backward", lib().moe_norm_residual_backward(
+        ctypes.byref(c), _rows("dn", dn, T, d, (bf16,), True), _rows("dy", dy, T, d, rt, True),
+        _rows("b", b, T, d, (bf16,), True), _rows("r", r, T, d, rt, True),
+        _rows("gate", gate, T if c.gate_per_token else None, d, (bf16,), True),
+        _rows("w_post", w_post, None, d, (bf16,), True),
+        _rows("w_pre", w_pre, None, d, (bf16,), True),
+        _rows("rstd_post", rstd_post, T, None, (f32,), True),
+        _rows("rstd_pre", rstd_pre, T, None, (f32,), True), _rows("db", db, T, d, (bf16,), True),
+        _rows("dr", dr, T, d, (bf16, f32)),
+        _rows("dgate", dgate, T if c.gate_per_token else None, d,
+              (bf16,) if c.gate_per_token else (f32,), True),
+        _rows("dw_post", dw_post, None, d, (f32,), True),
+        _rows("dw_pre", dw_pre, None, d, (f32,), True), _ptr(ws, u8), ws.numel(),
+        _stream(stream)))
+
+
+ROTARY_SCALING = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
+
+
+def rotary_table(table, base=10000.0, scaling="none", factor=1.0, orig_len=0.0, beta_fast=32.0,
+                 beta_slow=1.0, magnitude=1.0, stream=None):
+    """Fill table [positions, rot_dim / 2, 2] fp32 with {cos, sin} of the
+    rotary angles (see moe_rotary_make_table for the scalings)."""
+    if table.dim() != 3 or table.shape[2] != 2:
+        raise ValueError("the table is [positions, rot_dim / 2, 2]")
+    if scaling not in ROTARY_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALING)}")
+    c = RotaryTable(table.shape[0], 2 * table.shape[1], ROTARY_SCALING[scaling], base, factor,
+                    orig_len, beta_fast, beta_slow, magnitude)
+    _check("moe_rotary_make_table", lib().moe_rotary_make_table(
+        ctypes.byref(c), _ptr(table, f32), _stream(stream)))
+
+
+def _heads(name, t, T, heads, D):
+    """(pointer, token stride, head stride) of a [T, heads, D] bf16 tensor
+    whose channels are contiguous (tokens and heads may be strided)."""
+    if t.dtype != bf16:
+        raise TypeError(f"{name}: expected {bf16}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: tensors must live on the GPU")
+    if t.dim() != 3 or tuple(t.shape) != (T, heads, D):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, heads, D)}")
+    st, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name}: channels must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), st, sh
+
+
+def rotary(q, k, table, pos, q_out, k_out, status, interleaved=False, inverse=False, stream=None):
+    """Turn the first 2 table.shape[1] channels of every head of q [T, hq, D]
+    and k [T, hk, D] (None: no keys) to the tokens' positions pos [T] int32
+    (None: 0, 1, ...), into q_out and k_out (which may be q and k).  inverse:
+    the gradient's direction.  interleaved: pairs side by side."""
+    T, hq, D = q.shape
+    hk = 0 if k is None else k.shape[1]
+    qp, qt, qh = _heads("q", q, T, hq, D)
+    qop, qot, qoh = _heads("q_out", q_out, T, hq, D)
+    kp, kt, kh = (None, 0, 0) if k is None else _heads("k", k, T, hk, D)
+    kop, kot, koh = (None, 0, 0) if k is None else _heads("k_out", k_out, T, hk, D)
+    if table.dim() != 3 or table.shape[2] != 2:
+        raise ValueError("the table is [positions, rot_dim / 2, 2]")
+    if pos is not None and tuple(pos.shape) != (T,):
+        raise ValueError("pos is [T]")
+    c = Rotary(T, hq, hk, D, 2 * table.shape[1], int(bool(interleaved)), int(bool(inverse)),
+               table.shape[0], qt, qh, kt, kh, qot, qoh, kot, koh)
+    _check("moe_rotary", lib().moe_rotary(
+        ctypes.byref(c), qp, kp, _ptr(table, f32), _ptr(pos, i32, allow_none=True), qop, kop,
+        _ptr(status, i32), _stream(stream)))
+
+
+class AttentionPlan:
+    """Work lists of one batch of packed sequences: sequence s is the tokens
+    cu_seqlens[s] .. cu_seqlens[s + 1) of T (int32 on the device, read on the
+    stream, never on the host).  It serves any number of attention and
+    attention_backward calls of these sizes; refill() takes another batch's
+    cu_seqlens of the same length.  ``status`` receives MOE_EINVAL if they
+    decrease or leave [0, T]."""
+
+    def __init__(self, cu_seqlens, T, n_heads, n_kv_heads, head_dim, status=None, stream=None):
+        self.T, self.n_heads, self.n_kv_heads, self.head_dim = T, n_heads, n_kv_heads, head_dim
+        self.n_seqs = cu_seqlens.numel() - 1
+        if cu_seqlens.dim() != 1 or self.n_seqs < 0:
+            raise ValueError("cu_seqlens is [sequences + 1]")
+        pb, bb = ctypes.c_int64(), ctypes.c_int64()
+        _check("moe_attention_workspace", lib().moe_attention_workspace(
+            ctypes.byref(self._config(1.0)), ctypes.byref(pb), ctypes.byref(bb)))
+        self.backward_ws_bytes = bb.value
+        self.status = (torch.zeros(1, dtype=i32, device=cu_seqlens.device) if status is None
+                       else status)
+        self.plan = torch.empty(pb.value, dtype=u8, device=cu_seqlens.device)
+        self.refill(cu_seqlens, stream)
+
+    def _config(self, scale):
+        c = Attention()
+        c.T, c.n_seqs, c.n_heads = self.T, self.n_seqs, self.n_heads
+        c.n_kv_heads, c.head_dim, c.scale = self.n_kv_heads, self.head_dim, scale
+        return c
+
+    def refill(self, cu_seqlens, stream=None):
+        if tuple(cu_seqlens.shape) != (self.n_seqs + 1,):
+            raise ValueError("cu_seqlens of another number of sequences")
+        _check("moe_attention_plan", lib().moe_attention_plan(
+            ctypes.byref(self._config(1.0)), _ptr(cu_seqlens, i32), _ptr(self.plan, u8),
+            self.plan.numel(), _ptr(self.status, i32), _stream(stream)))
+
+
+def _attention_config(plan, scale, **tensors):
+    c = plan._config(plan.head_dim ** -0.5 if scale is None else scale)
+    ptrs = []
+    for name, t in tensors.items():
+        heads = plan.n_kv_heads if name in ("k", "v", "dk", "dv") else plan.n_heads
+        p, st, sh = _heads(name, t, plan.T, heads, plan.head_dim)
+        key = {"out": "o", "dout": "do"}.get(name, name)
+        if key == "rest":
+            if (st, sh) != (c.o_t, c.o_h):
+                raise ValueError("rest has out's strides")
+        else:
+            setattr(c, key + "_t", st)
+            setattr(c, key + "_h", sh)
+        ptrs.append(p)
+    return c, ptrs
+
+
+def attention(plan, q, k, v, out, lse, status, scale=None, rest=None, stream=None):
+    """Causal attention within each of the plan's sequences: q, out [T,
+    n_heads, D], k, v [T, n_kv_heads, D] bf16 (strided views allowed), lse
+    [n_heads, T] fp32; scale D^-1/2 unless given.  rest (like out): what
+    rounding took from out, for attention_backward (None: no gradient)."""
+    given = dict(q=q, k=k, v=v, out=out)
+    if rest is not None:
+        given["rest"] = rest
+    c, p = _attention_config(plan, scale, **given)
+    _check("moe_attention_forward", lib().moe_attention_forward(
+        ctypes.byref(c), _ptr(plan.plan, u8), p[0], p[1], p[2], p[3],
+        p[4] if rest is not None else None, _rows("lse", lse, plan.n_heads, plan.T, (f32,)),
+        _ptr(status, i32), _stream(stream)))
+
+
+def attention_backward(plan, q, k, v, out, rest, lse, dout, dq, dk, dv, ws, status, scale=None,
+                       stream=None):
+    """dq, dk, dv of attention for the upstream gradient dout, from the
+    forward's inputs and its out, rest and lse; ws: plan.backward_ws_bytes."""
+    c, p = _attention_config(plan, scale, q=q, k=k, v=v, out=out, rest=rest, dout=dout, dq=dq,
+                             dk=dk, dv=dv)
+    _check("moe_attention_backward", lib().moe_attention_backward(
+        ctypes.byref(c), _ptr(plan.plan, u8), p[0], p[1], p[2], p[3], p[4],
+        _rows("lse", lse, plan.n_heads, plan.T, (f32,)), p[5], p[6], p[7], p[8], _ptr(ws, u8),
+        ws.numel(), _ptr(status, i32), _stream(stream)))
+
+
+class GradSet:
+    """The gradients of one model: contiguous fp32 or bf16 tensors, and where
+    the clipped ones go (``outs``; None: in place).  Holds the tensors."""
+
+    def __init__(self, tensors, outs=None):
+        outs = tensors if outs is None else outs
+        if len(tensors) != len(outs):
+            raise ValueError("one output a tensor")
+        self.tensors, self.outs = list(tensors), list(outs)
+        self.records = (GradTensor * max(1, len(self.tensors)))()
+        for r, a, b in zip(self.records, self.tensors, self.outs):
+            if a.dtype not in (bf16, f32) or b.dtype != a.dtype or b.shape != a.shape:
+                raise TypeError("fp32 or bf16 gradients, each with an output of its own type "
+                                "and shape")
+            setattr(r, "in", _ptr(a))
+            r.out = _ptr(b)
+            r.numel, r.is_bf16 = a.numel(), int(a.dtype == bf16)
+        v = ctypes.c_int64()
+        _check("moe_grad_clip_workspace",
+               lib().moe_grad_clip_workspace(len(self.tensors), ctypes.byref(v)))
+        dev = self.tensors[0].device if self.tensors else None
+        self.ws = torch.empty(max(1, v.value), dtype=u8, device=dev) if dev else None
+
+
+def grad_clip(grads, max_norm, norm, stream=None):
+    """norm[0] = the 2-norm over all tensors of the GradSet; each is scaled by
+    min(1, max_norm / (norm + 1e-6)) into its output.  A norm that is not
+    finite leaves the gradients as they are."""
+    if not grads.tensors:
+        return
+    _check("moe_grad_clip", lib().moe_grad_clip(
+        grads.records, len(grads.tensors), max_norm, _ptr(norm, f32), _ptr(grads.ws, u8),
+        grads.ws.numel(), _stream(stream)))

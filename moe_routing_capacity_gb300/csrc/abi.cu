@@ -5,21 +5,8 @@
 #include <map>
 #include <mutex>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include "internal.h"
-
-namespace {
-// One NVTX range per C-ABI compute call (a no-op unless a profiler attaches),
-// so that profiler timelines group each call's kernels under its name.
-struct NvtxRange {
-    explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-    NvtxRange(const NvtxRange&) = delete;
-    NvtxRange& operator=(const NvtxRange&) = delete;
-};
-}  // namespace
-#define MOE_NVTX_RANGE() NvtxRange moe_nvtx_range_(__func__)
+#include "nvtx_range.h"
 
 namespace moe {
 

@@ -1,0 +1,217 @@
+// attention.cuh -- what the attention kernels share: the plan's layout, TMEM
+// loads and stores, MMAs with an A operand in TMEM, and packed fp32 pairs.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+// ------------------------------------------------------------------ the plan
+// Work lists of one batch of packed sequences, in device memory:
+//   header   int32[8]: number of entries of each list (q128, kv128, q256), error
+//   q128     query blocks of 128 rows, most key blocks first
+//   kv128    key blocks of 128 rows, most query blocks first
+//   q256     query blocks of 256 rows, most key blocks first
+// An entry is {first token of the sequence, its length, block, 0}; block = -1:
+// `length` tokens from the first one that belong to no sequence.
+struct AttnPlanLayout {
+    int64_t max128, max256;             // most entries of a list
+    int64_t bins;                       // most blocks of one sequence, + 1
+    int64_t q128, kv128, q256, cursor, total;   // byte offsets
+};
+
+constexpr int kPlanHeader = 32;
+
+inline AttnPlanLayout attn_plan_layout(int64_t T, int n_seqs) {
+    AttnPlanLayout l;
+    // whole and partial blocks of the sequences and of the two gaps
+    l.max128 = T / 128 + n_seqs + 2;
+    l.max256 = T / 256 + n_seqs + 2;
+    l.bins = T / 128 + 2;
+    l.q128 = kPlanHeader;
+    l.kv128 = l.q128 + l.max128 * 16;
+    l.q256 = l.kv128 + l.max128 * 16;
+    l.cursor = l.q256 + l.max256 * 16;
+    l.total = l.cursor + 2 * l.bins * 4;
+    return l;
+}
+
+// ------------------------------------------------------------------ TMEM
+
+// 32 consecutive columns, without waiting (tmem_wait_ld before their use).
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_ld() {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(
+            r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+        "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+        "r"(r[30]), "r"(r[31]), "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: A's 128 rows are the TMEM lanes, each
+// 32-bit column holds two consecutive K values (the lower half the first).
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Descriptor of an MN-major operand stored as boxes of 128 K-rows of 64
+// contiguous M/N elements with the 128-byte swizzle: 8-row atoms of 1024 B
+// along K, the next 64 M/N elements 16 KB on.
+__device__ __forceinline__ uint64_t sdesc_mn128_sw128(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(16384 >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+// A tile of 128 tokens x D channels in shared memory is D / 64 boxes of 128
+// rows of 64 channels (16 KB each, 128-byte swizzle).  The same bytes serve
+// as a K-major operand (M/N = tokens, K = channels) and as an MN-major one
+// (M/N = channels, K = tokens).
+constexpr uint32_t kBoxBytes = 16384;
+
+// scores[tmem] = A B^T over D channels, both tiles K-major.
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t d_tmem, uint32_t a_saddr, uint32_t b_saddr) {
+    constexpr uint32_t idesc = idesc_bf16_f32(128, 128);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk / 4) * kBoxBytes + (kk % 4) * 32;
+        mma_bf16(d_tmem, sdesc_k_sw128(a_saddr + off), sdesc_k_sw128(b_saddr + off), idesc,
+                 kk > 0);
+    }
+}
+
+// acc[tmem] (+)= A B over 128 tokens: A bf16 in TMEM in two halves of 64
+// tokens (32 columns each, a1 - a0 apart), B a tile read MN-major.
+template <int D>
+__device__ __forceinline__ void mma_tokens(uint32_t d_tmem, uint32_t a0, uint32_t a1,
+                                           uint32_t b_saddr, bool accumulate) {
+    constexpr uint32_t idesc = idesc_bf16_f32(128, D, false, true);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+        const uint32_t a = (kk < 4 ? a0 : a1) + (kk % 4) * 8;
+        mma_bf16_ta(d_tmem, a, sdesc_mn128_sw128(b_saddr + kk * 2048), idesc,
+                    accumulate || kk > 0);
+    }
+}
+
+// mbar_wait by a whole warp with one answer for all its lanes: the warp-wide
+// TMEM operations that follow never run in part of a warp.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          int32_t* status) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, status));
+}
+
+// ------------------------------------------------------------------ arithmetic
+
+// 2^x (flushing denormal results): the hardware's own exponential.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ bool finite_f32(float x) { return fabsf(x) <= 3.402823466e38f; }
+
+__device__ __forceinline__ float bf16_f32(uint16_t v) {
+    return __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+
+__device__ __forceinline__ uint16_t f32_bf16(float v) {
+    return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+}  // namespace moe

@@ -1,0 +1,581 @@
+// attention_fwd.cu -- causal attention over packed sequences, forward, and
+// the plan of work lists that forward and backward share.
+//
+// One CTA holds two tiles of 128 query rows that read the same key/value
+// head of the same sequence (two query heads of a group, or two blocks of
+// rows when the group is odd) and walks the sequence's key blocks of 128:
+//   S = Q K^T (tcgen05, fp32 in TMEM); m, l = running maximum and sum;
+//   P = 2^(c S - c m) as bf16 back into S's columns; O += P V (A from TMEM).
+// Warps 0-3 and 4-7 run the softmax of the two tiles, a thread a row; warp 8
+// issues the MMAs, warp 9 the TMA loads.  While one tile's softmax runs, the
+// tensor cores work on the other's products.  TMEM: two S and two O of 128
+// columns, all 512.
+#include <cstring>
+
+#include "attention.cuh"
+#include "internal.h"
+
+namespace moe {
+
+namespace {
+
+struct FwdParams {
+    CUtensorMap mapQ, mapK, mapV;   // {head_dim, T, heads}, box {64, 128, 1}
+    const int4* tiles;
+    const int32_t* header;
+    int list;                        // which header word counts the tiles
+    int units;                       // CTAs of one tile
+    int pair_heads;                  // 1: tiles are two heads; 0: two row blocks
+    int group;
+    int D;
+    int64_t T;
+    int64_t q_t, q_h, k_t, k_h, v_t, v_h, o_t, o_h;
+    const uint16_t *q, *k, *v;
+    uint16_t *out, *rest;
+    float* lse;
+    float scale, scale_log2;
+    int32_t* status;
+};
+
+template <int D>
+struct FwdCfg {
+    static constexpr int TILE = 128 * D * 2;
+    static constexpr int STAGES = D == 128 ? 4 : 8;
+    static constexpr int SMEM = 2 * TILE + STAGES * TILE + 1024 + 256;
+};
+
+// One row by the definition on the CUDA cores, for a row whose products met
+// a non-finite value: hidden tokens are skipped instead of multiplied by 0.
+__device__ __noinline__ void fwd_row(const FwdParams& p, int64_t start, int row, int h, int kvh,
+                                     float lse) {
+    const int lane = threadIdx.x & 31;
+    const uint16_t* q = p.q + (start + row) * p.q_t + h * p.q_h;
+    const uint16_t* k = p.k + start * p.k_t + kvh * p.k_h;
+    const uint16_t* v = p.v + start * p.v_t + kvh * p.v_h;
+    float qv[4], acc[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) qv[i] = lane + 32 * i < p.D ? bf16_f32(q[lane + 32 * i]) : 0.f;
+    for (int j = 0; j <= row; ++j) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (lane + 32 * i < p.D) s += qv[i] * bf16_f32(k[j * p.k_t + lane + 32 * i]);
+        s = warp_sum(s);
+        const float w = expf(s * p.scale - lse);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (lane + 32 * i < p.D) acc[i] += w * bf16_f32(v[j * p.v_t + lane + 32 * i]);
+    }
+    const int64_t o = (start + row) * p.o_t + h * p.o_h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = lane + 32 * i;
+        if (c < p.D) {
+            const uint16_t b = f32_bf16(acc[i]);
+            p.out[o + c] = b;
+            if (p.rest) p.rest[o + c] = f32_bf16(acc[i] - bf16_f32(b));
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(384, 1) attn_fwd_kernel(const __grid_constant__ FwdParams p) {
+    using C = FwdCfg<D>;
+    const int tile = blockIdx.x / p.units;
+    if (tile >= p.header[p.list]) return;
+    const int u = blockIdx.x - tile * p.units;
+    const int4 te = p.tiles[tile];
+    const int64_t start = te.x;
+    const int len = te.y;
+    int kvh, h[2], m0[2], n[2];
+    if (p.pair_heads) {
+        const int half = p.group / 2;
+        kvh = u / half;
+        h[0] = kvh * p.group + 2 * (u - kvh * half);
+        h[1] = h[0] + 1;
+        m0[0] = m0[1] = te.z * 128;
+    } else {
+        h[0] = h[1] = u;
+        kvh = u / p.group;
+        m0[0] = te.z * 256;
+        m0[1] = m0[0] + 128;
+    }
+    if (te.z < 0) {   // tokens of no sequence
+        for (int t = 0; t < (p.pair_heads ? 2 : 1); ++t) {
+            for (int i = threadIdx.x; i < len * (p.D / 8); i += blockDim.x) {
+                const int64_t o = (start + i / (p.D / 8)) * p.o_t + h[t] * p.o_h + i % (p.D / 8) * 8;
+                *reinterpret_cast<uint4*>(p.out + o) = make_uint4(0, 0, 0, 0);
+                if (p.rest) *reinterpret_cast<uint4*>(p.rest + o) = make_uint4(0, 0, 0, 0);
+            }
+            for (int i = threadIdx.x; i < len; i += blockDim.x)
+                p.lse[h[t] * p.T + start + i] = -INFINITY;
+        }
+        return;
+    }
+    n[0] = m0[0] / 128 + 1;
+    n[1] = m0[1] < len ? m0[1] / 128 + 1 : 0;
+    const int nmax = max(n[0], n[1]);
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* sQ = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    uint8_t* sKV = sQ + 2 * C::TILE;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sKV + C::STAGES * C::TILE);
+    uint64_t* empty = full + C::STAGES;
+    uint64_t* q_full = empty + C::STAGES;
+    uint64_t* s_full = q_full + 1;    // [2] scores of a tile ready
+    uint64_t* p_full = s_full + 2;    // [2] its P written
+    uint64_t* o_full = p_full + 2;    // [2] its product with V done
+    uint64_t* done = o_full + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(q_full, 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_full[t], 128);
+            mbar_init(&o_full[t], 1);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = *tmem_slot;
+    const uint32_t tmS = tm, tmO = tm + 256;   // tile t: + 128 t
+
+    if (warp >= 8) {
+        setmaxnreg_dec<88>();
+        if (warp == 9 && lane == 0) {
+            // -------------------------------------------------------- loads
+            const uint32_t dq = smem_u32(sQ);
+            mbar_arrive_expect_tx(q_full, (n[1] ? 2 : 1) * C::TILE);
+            for (int t = 0; t < (n[1] ? 2 : 1); ++t)
+                for (int b = 0; b < D / 64; ++b)
+                    tma_load_3d(dq + t * C::TILE + b * kBoxBytes, &p.mapQ, q_full, b * 64,
+                                static_cast<int>(start) + m0[t], h[t]);
+            uint32_t st = 0, ph = 0, armed = 0, par = 0;
+            bool ok = true;
+            for (int it = 0; ok && it < 2 * nmax; ++it) {
+                if (!mbar_wait(&empty[st], ph ^ 1u, abort_flag, p.status)) {
+                    ok = false;
+                    break;
+                }
+                const CUtensorMap* map = (it & 1) ? &p.mapV : &p.mapK;
+                mbar_arrive_expect_tx(&full[st], C::TILE);
+                armed |= 1u << st;
+                par = (par & ~(1u << st)) | (ph << st);
+                const uint32_t dst = smem_u32(sKV) + st * C::TILE;
+                for (int b = 0; b < D / 64; ++b)
+                    tma_load_3d(dst + b * kBoxBytes, map, &full[st], b * 64,
+                                static_cast<int>(start) + (it >> 1) * 128, kvh);
+                if (++st == C::STAGES) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (!ok || *abort_flag) {   // let the armed copies land before leaving
+                volatile int no_abort = 0;
+                mbar_wait(q_full, 0, &no_abort, nullptr, 20000000ull);
+                for (int s = 0; s < C::STAGES; ++s)
+                    if (armed & (1u << s))
+                        mbar_wait(&full[s], (par >> s) & 1u, &no_abort, nullptr, 20000000ull);
+            }
+        } else if (warp == 8 && lane == 0) {
+            // -------------------------------------------------------- MMAs
+            const uint32_t aq = smem_u32(sQ), akv = smem_u32(sKV);
+            const auto stage = [](int it) { return static_cast<uint32_t>(it % C::STAGES); };
+            const auto phase = [](int it) { return static_cast<uint32_t>(it / C::STAGES) & 1u; };
+            bool ok = mbar_wait(q_full, 0, abort_flag, p.status) &&
+                      mbar_wait(&full[0], 0, abort_flag, p.status);
+            if (ok) {
+                tc_fence_after();
+                for (int t = 0; t < 2; ++t)
+                    if (n[t]) {
+                        mma_scores<D>(tmS + 128 * t, aq + t * C::TILE, akv);
+                        mma_commit(&s_full[t]);
+                    }
+                mma_commit(&empty[0]);
+            }
+            for (int j = 0; ok && j < nmax; ++j) {
+                const int iv = 2 * j + 1, ik = 2 * j + 2;
+                if (!mbar_wait(&full[stage(iv)], phase(iv), abort_flag, p.status)) break;
+                bool have_k = false;
+                for (int t = 0; ok && t < 2; ++t) {
+                    if (j >= n[t]) continue;
+                    if (!mbar_wait(&p_full[t], j & 1u, abort_flag, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    mma_tokens<D>(tmO + 128 * t, tmS + 128 * t, tmS + 128 * t + 32,
+                                  akv + stage(iv) * C::TILE, j > 0);
+                    mma_commit(&o_full[t]);
+                    if (j + 1 < n[t]) {
+                        if (!have_k) {
+                            if (!mbar_wait(&full[stage(ik)], phase(ik), abort_flag, p.status)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            have_k = true;
+                        }
+                        // runs after the product above has read P from these columns
+                        mma_scores<D>(tmS + 128 * t, aq + t * C::TILE, akv + stage(ik) * C::TILE);
+                        mma_commit(&s_full[t]);
+                    }
+                }
+                if (!ok) break;
+                mma_commit(&empty[stage(iv)]);
+                if (have_k) mma_commit(&empty[stage(ik)]);
+            }
+            // nothing of this CTA is in flight when it leaves
+            mma_commit(done);
+            volatile int no_abort = 0;
+            mbar_wait(done, 0, &no_abort, p.status);
+        }
+    } else {
+        setmaxnreg_inc<208>();
+        // ------------------------------------------------------------ softmax
+        const int t = warp >> 2;
+        const int r = threadIdx.x & 127;
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tmS + 128 * t + lane_off, to = tmO + 128 * t + lane_off;
+        const float c = p.scale_log2;
+        const float slack = 8.0f / c;   // P may reach 2^8 before O is rescaled
+        // l: sum of P, for lse; lb: sum of P as rounded to bf16, which divides O:
+        // a row that is nearly one key's then gives that key's v, not v times
+        // its weight's rounding error, and D_i of the backward depends on it
+        float m = -INFINITY, l = 0.f, lb = 0.f;
+        bool ok = true;
+        for (int j = 0; j < n[t]; ++j) {
+            if (!warp_wait(&s_full[t], j & 1u, abort_flag, p.status)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            float s[128];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                tmem_ld32_async(ts + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
+            tmem_wait_ld();
+            if (j == n[t] - 1) {   // the diagonal block: keys after the row are hidden
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    if (i > r) s[i] = -INFINITY;
+            }
+            float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int i = 4; i < 128; i += 4) {
+                mx[0] = fmaxf(mx[0], s[i]);
+                mx[1] = fmaxf(mx[1], s[i + 1]);
+                mx[2] = fmaxf(mx[2], s[i + 2]);
+                mx[3] = fmaxf(mx[3], s[i + 3]);
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            if (j == 0) {
+                m = top;
+            } else {
+                // O keeps an older maximum until a row's rises by 2^8: sums in
+                // fp32 hold the larger terms, and rescaling is rare
+                const bool rise = top > m + slack;
+                if (__any_sync(0xFFFFFFFFu, rise)) {
+                    const float f = rise ? exp2_fast((m - top) * c) : 1.0f;
+                    if (rise) m = top;
+                    l *= f;
+                    lb *= f;
+                    if (!warp_wait(&o_full[t], (j - 1) & 1u, abort_flag, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        uint32_t o[32];
+                        tmem_ld32(to + 32 * i, o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st32(to + 32 * i, o);
+                    }
+                }
+            }
+            const float2 c2 = make_float2(c, c), neg = make_float2(-m * c, -m * c);
+            float2 sum = make_float2(0.f, 0.f), sumb = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float2 x = fma2(make_float2(s[32 * i + 2 * e], s[32 * i + 2 * e + 1]), c2, neg);
+                    x.x = exp2_fast(x.x);
+                    x.y = exp2_fast(x.y);
+                    sum = add2(sum, x);
+                    pk[e] = pack_bf16x2(x.x, x.y);
+                    sumb = add2(sumb, make_float2(bf16_lo(pk[e]), bf16_hi(pk[e])));
+                }
+                tmem_st16(ts + 16 * i, pk);
+            }
+            l += sum.x + sum.y;
+            lb += sumb.x + sumb.y;
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&p_full[t]);
+        }
+        // ------------------------------------------------------------ output
+        if (ok && n[t]) {
+            ok = warp_wait(&o_full[t], (n[t] - 1) & 1u, abort_flag, p.status);
+            tc_fence_after();
+        }
+        if (ok && n[t]) {
+            const int row = m0[t] + r;
+            const bool valid = row < len;
+            const float inv = 1.0f / lb;
+            const float lse = m * p.scale + logf(l);
+            const int64_t o = (start + row) * p.o_t + h[t] * p.o_h;
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                uint32_t a[32];
+                tmem_ld32(to + 32 * i, a);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int col = 32 * i + 8 * g;
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float x = __uint_as_float(a[8 * g + 2 * e]) * inv;
+                        const float y = __uint_as_float(a[8 * g + 2 * e + 1]) * inv;
+                        bad |= !finite_f32(x) || !finite_f32(y);
+                        hi[e] = pack_bf16x2(x, y);
+                        lo[e] = pack_bf16x2(x - bf16_lo(hi[e]), y - bf16_hi(hi[e]));
+                    }
+                    if (valid && col < p.D) {
+                        *reinterpret_cast<uint4*>(p.out + o + col) =
+                            make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        if (p.rest)
+                            *reinterpret_cast<uint4*>(p.rest + o + col) =
+                                make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                }
+            }
+            if (valid) p.lse[h[t] * p.T + start + row] = lse;
+            uint32_t again = __ballot_sync(0xFFFFFFFFu, bad && valid);
+            while (again) {
+                const int src = __ffs(again) - 1;
+                again &= again - 1;
+                fwd_row(p, start, __shfl_sync(0xFFFFFFFFu, row, src), h[t], kvh,
+                        __shfl_sync(0xFFFFFFFFu, lse, src));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tm, 512);
+}
+
+// ------------------------------------------------------------------ the plan
+// Weight w = blocks a query block reads (its number + 1), or that read a key
+// block.  Entries with weight >= w of a list of sequences with b_s blocks:
+// a counting sort, heaviest first; sequence s has one entry of each weight
+// 1 .. b_s in either list.
+
+__global__ void __launch_bounds__(1024, 1)
+    attn_plan_kernel(const int32_t* cu, int n_seqs, int64_t T, int4* q128, int4* kv128, int4* q256,
+                     int32_t* header, int32_t* cursor, int bins, int32_t* status) {
+    __shared__ int part[32];
+    __shared__ int carry, bad;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) bad = 0;
+    __syncthreads();
+    for (int s = tid; s <= n_seqs; s += 1024) {
+        const int lo = s ? cu[s - 1] : 0;
+        if (cu[s] < lo || cu[s] > T) bad = 1;
+    }
+    __syncthreads();
+    if (bad) {
+        if (tid < 8) header[tid] = 0;
+        if (tid == 0) report_error(status, MOE_EINVAL);
+        return;
+    }
+    for (int pass = 0; pass < 2; ++pass) {
+        const int bs = pass ? 256 : 128;
+        for (int i = tid; i < bins; i += 1024) cursor[i] = 0;
+        if (tid == 0) carry = 0;
+        __syncthreads();
+        for (int s = tid; s < n_seqs; s += 1024) {
+            const int nb = (cu[s + 1] - cu[s] + bs - 1) / bs;
+            if (nb) atomicAdd(&cursor[nb], 1);
+        }
+        __syncthreads();
+        // sequences with at least w blocks (a suffix sum), then the first
+        // entry of weight w: the entries heavier than w
+        for (int what = 0; what < 2; ++what) {
+            if (tid == 0) carry = 0;
+            __syncthreads();
+            for (int base = bins - 1; base >= 0; base -= 1024) {
+                const int w = base - tid;
+                const int v = w >= 0 ? cursor[w] : 0;
+                int x = v;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+                    if (lane >= o) x += y;
+                }
+                if (lane == 31) part[warp] = x;
+                __syncthreads();
+                if (warp == 0) {
+                    int y = part[lane];
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int z = __shfl_up_sync(0xFFFFFFFFu, y, o);
+                        if (lane >= o) y += z;
+                    }
+                    part[lane] = y;
+                }
+                __syncthreads();
+                const int incl = carry + x + (warp ? part[warp - 1] : 0);
+                if (w >= 0) cursor[w] = what ? incl - v : incl;
+                __syncthreads();
+                if (tid == 1023) carry = incl;
+                __syncthreads();
+            }
+            if (what == 0) {
+                if (tid == 0) cursor[0] = 0;   // no entry has weight 0
+                __syncthreads();
+            }
+        }
+        const int total = carry;
+        for (int s = warp; s < n_seqs; s += 32) {
+            const int first = cu[s], len = cu[s + 1] - first, nb = (len + bs - 1) / bs;
+            for (int w = lane + 1; w <= nb; w += 32) {
+                const int at = atomicAdd(&cursor[w], 1);
+                if (pass) {
+                    q256[at] = make_int4(first, len, w - 1, 0);
+                } else {
+                    q128[at] = make_int4(first, len, w - 1, 0);
+                    kv128[at] = make_int4(first, len, nb - w, 0);
+                }
+            }
+        }
+        // tokens outside every sequence, in blocks
+        const int head = cu[0], tail = static_cast<int>(T) - cu[n_seqs];
+        const int nh = (head + bs - 1) / bs, nt = (tail + bs - 1) / bs;
+        for (int i = tid; i < nh + nt; i += 1024) {
+            const int in = i < nh ? i : i - nh;
+            const int first = (i < nh ? 0 : cu[n_seqs]) + in * bs;
+            const int len = min(bs, (i < nh ? head : static_cast<int>(T)) - first);
+            const int4 e = make_int4(first, len, -1, 0);
+            if (pass) {
+                q256[total + i] = e;
+            } else {
+                q128[total + i] = e;
+                kv128[total + i] = e;
+            }
+        }
+        if (tid == 0) {
+            if (pass) {
+                header[2] = total + nh + nt;
+            } else {
+                header[0] = header[1] = total + nh + nt;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace
+
+int64_t attention_plan_bytes(int64_t T, int n_seqs) { return attn_plan_layout(T, n_seqs).total; }
+
+int launch_attention_plan(int64_t T, int n_seqs, const int32_t* cu, void* plan, int32_t* status,
+                          cudaStream_t st) {
+    const AttnPlanLayout l = attn_plan_layout(T, n_seqs);
+    uint8_t* b = static_cast<uint8_t*>(plan);
+    attn_plan_kernel<<<1, 1024, 0, st>>>(
+        cu, n_seqs, T, reinterpret_cast<int4*>(b + l.q128), reinterpret_cast<int4*>(b + l.kv128),
+        reinterpret_cast<int4*>(b + l.q256), reinterpret_cast<int32_t*>(b),
+        reinterpret_cast<int32_t*>(b + l.cursor), static_cast<int>(l.bins), status);
+    if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
+    trace_after(st, "attn_plan");
+    return MOE_OK;
+}
+
+// {channels, tokens, heads} of a strided tensor in boxes of 64 x 128 x 1
+// with the 128-byte swizzle; channels past D and tokens past T read as zero.
+int attn_tensor_map(CUtensorMap* m, const void* base, int D, int64_t T, int heads, int64_t st_t,
+                    int64_t st_h) {
+    // an extent of one has no stride of its own: any valid one will do
+    if (T == 1) st_t = D;
+    if (heads == 1) st_h = D;
+    return tensor_map_bf16_3d(m, base, D, T, heads, st_t, st_h, 128);
+}
+
+int launch_attention_fwd(const moe_attention_t& a, const void* plan, const uint16_t* q,
+                         const uint16_t* k, const uint16_t* v, uint16_t* out, uint16_t* rest,
+                         float* lse, int32_t* status, cudaStream_t st) {
+    FwdParams p;
+    memset(&p, 0, sizeof(p));
+    const int D = a.head_dim;
+    if (attn_tensor_map(&p.mapQ, q, D, a.T, a.n_heads, a.q_t, a.q_h) ||
+        attn_tensor_map(&p.mapK, k, D, a.T, a.n_kv_heads, a.k_t, a.k_h) ||
+        attn_tensor_map(&p.mapV, v, D, a.T, a.n_kv_heads, a.v_t, a.v_h))
+        return MOE_ECUDA;
+    const AttnPlanLayout l = attn_plan_layout(a.T, a.n_seqs);
+    const uint8_t* b = static_cast<const uint8_t*>(plan);
+    p.group = a.n_heads / a.n_kv_heads;
+    p.pair_heads = p.group % 2 == 0;
+    p.header = reinterpret_cast<const int32_t*>(b);
+    p.list = p.pair_heads ? 0 : 2;
+    p.tiles = reinterpret_cast<const int4*>(b + (p.pair_heads ? l.q128 : l.q256));
+    p.units = p.pair_heads ? a.n_heads / 2 : a.n_heads;
+    p.D = D;
+    p.T = a.T;
+    p.q_t = a.q_t;
+    p.q_h = a.q_h;
+    p.k_t = a.k_t;
+    p.k_h = a.k_h;
+    p.v_t = a.v_t;
+    p.v_h = a.v_h;
+    p.o_t = a.o_t;
+    p.o_h = a.o_h;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.out = out;
+    p.rest = rest;
+    p.lse = lse;
+    p.scale = a.scale;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.status = status;
+    const int64_t grid = (p.pair_heads ? l.max128 : l.max256) * p.units;
+    if (grid >= (1ll << 31)) return MOE_EINVAL;
+    if (D <= 64) {
+        if (ensure_smem_attr(reinterpret_cast<const void*>(attn_fwd_kernel<64>), FwdCfg<64>::SMEM))
+            return MOE_ECUDA;
+        attn_fwd_kernel<64><<<static_cast<int>(grid), 384, FwdCfg<64>::SMEM, st>>>(p);
+    } else {
+        if (ensure_smem_attr(reinterpret_cast<const void*>(attn_fwd_kernel<128>),
+                             FwdCfg<128>::SMEM))
+            return MOE_ECUDA;
+        attn_fwd_kernel<128><<<static_cast<int>(grid), 384, FwdCfg<128>::SMEM, st>>>(p);
+    }
+    if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
+    trace_after(st, "attn_fwd");
+    return MOE_OK;
+}
+
+}  // namespace moe

@@ -1055,6 +1055,13 @@ static int make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* 
     return r == CUDA_SUCCESS ? MOE_OK : MOE_ECUDA;
 }
 
+int tensor_map_bf16_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                       uint64_t stride1, uint64_t stride2, uint32_t box1) {
+    const uint64_t dims[3] = {d0, d1, d2};
+    const uint64_t str[2] = {stride1, stride2};
+    return make_map(m, base, 3, dims, str, box1);
+}
+
 static int map2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t ld,
                  uint32_t box_rows) {
     const uint64_t dims[2] = {cols, rows};

@@ -3,6 +3,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "../../include/moe_pooled_wave.h"
@@ -147,6 +148,11 @@ struct GemmDesc {
 
 int gemm_launch(const GemmDesc& d, cudaStream_t stream);
 
+// bf16 tensor map of a 3-D tensor (extents innermost first, strides in
+// elements), box {64, box1, 1}, 128-byte swizzle, zero fill out of range.
+int tensor_map_bf16_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                       uint64_t stride1, uint64_t stride2, uint32_t box1);
+
 // ---------------------------------------------------------------- routing kernels
 
 int launch_topk(const float* logits, int64_t T, int E, int k, int32_t* idx, float* w,
@@ -282,5 +288,43 @@ int launch_balance_window(const int32_t* idx, int64_t n, int E, int64_t* hist, i
 // c[t] = bf16(sum over kept j of w[t,j] ypool[slot_of[t,j]]); w == nullptr: weights 1.
 int launch_combine(const uint16_t* ypool, const int32_t* slot_of, const float* w, int64_t T, int k,
                    int L, uint16_t* c, int64_t rows, cudaStream_t stream);
+
+// ---------------------------------------------------------------- training block
+
+int launch_norm_residual(const moe_norm_t& c, const uint16_t* b, const void* r,
+                         const uint16_t* gate, const uint16_t* w_post, const uint16_t* w_pre,
+                         void* y, uint16_t* n, float* rstd_post, float* rstd_pre,
+                         cudaStream_t stream);
+int64_t norm_backward_ws(int64_t T, int d);
+int launch_norm_residual_backward(const moe_norm_t& c, const uint16_t* dn, const void* dy,
+                                  const uint16_t* b, const void* r, const uint16_t* gate,
+                                  const uint16_t* w_post, const uint16_t* w_pre,
+                                  const float* rstd_post, const float* rstd_pre, uint16_t* db,
+                                  void* dr, void* dgate, float* dw_post, float* dw_pre, void* ws,
+                                  cudaStream_t stream);
+
+int launch_rotary_table(const moe_rotary_table_t& c, float* table, cudaStream_t stream);
+int launch_rotary(const moe_rotary_t& c, const uint16_t* q, const uint16_t* k, const float* table,
+                  const int32_t* pos, uint16_t* q_out, uint16_t* k_out, int32_t* status,
+                  cudaStream_t stream);
+
+int64_t attention_plan_bytes(int64_t T, int n_seqs);
+int64_t attention_backward_ws(int64_t T, int n_heads);
+int launch_attention_plan(int64_t T, int n_seqs, const int32_t* cu, void* plan, int32_t* status,
+                          cudaStream_t stream);
+int launch_attention_fwd(const moe_attention_t& a, const void* plan, const uint16_t* q,
+                         const uint16_t* k, const uint16_t* v, uint16_t* out, uint16_t* rest,
+                         float* lse, int32_t* status, cudaStream_t stream);
+int launch_attention_bwd(const moe_attention_t& a, const void* plan, const uint16_t* q,
+                         const uint16_t* k, const uint16_t* v, const uint16_t* out,
+                         const uint16_t* rest, const float* lse, const uint16_t* dout,
+                         uint16_t* dq, uint16_t* dk, uint16_t* dv, void* ws, int32_t* status,
+                         cudaStream_t stream);
+int attn_tensor_map(CUtensorMap* m, const void* base, int D, int64_t T, int heads, int64_t st_t,
+                    int64_t st_h);
+
+int64_t grad_clip_ws(int64_t n_tensors);
+int launch_grad_clip(const moe_grad_tensor_t* tensors, int64_t n, float max_norm, float* norm,
+                     void* ws, cudaStream_t stream);
 
 }  // namespace moe
