@@ -261,8 +261,9 @@ def _ptr(t, dtype=None, allow_none=False):
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:   # the current stream's handle, without building a Stream object
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _check(fn, rc):
@@ -554,17 +555,22 @@ def layer_backward(cfg, tensors: dict, ws, status, stream=None):
 
 # ---------------------------------------------------------------- training block
 
-def _rows(name, t, T, d, dtypes, allow_none=False):
-    """Device pointer of a contiguous [T, d] (or [d], with T None) tensor."""
-    if t is None and allow_none:
-        return None
+def _rows(name, t, shape, dtypes, allow_none=False):
+    """Device address of a contiguous tensor of this shape and one of these types."""
     if t is None:
+        if allow_none:
+            return None
         raise ValueError(f"{name}: tensor required")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if tuple(t.shape) != ((d,) if T is None else (T,) if d is None else (T, d)):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}")
-    return _ptr(t)
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous device tensor required")
+    return t.data_ptr()
+
+
+_BF16, _F32, _RES = (bf16,), (f32,), (bf16, f32)
 
 
 def _norm_config(r, gate, alpha, beta, eps):
@@ -572,7 +578,7 @@ def _norm_config(r, gate, alpha, beta, eps):
         raise ValueError("the residual stream is [T, d]")
     T, d = r.shape
     per_token = gate is not None and gate.dim() == 2
-    return T, d, Norm(T, d, int(r.dtype == f32), int(per_token), alpha, beta, eps)
+    return (T, d), (d,), (T,), Norm(T, d, r.dtype == f32, per_token, alpha, beta, eps)
 
 
 def norm_residual(b, r, gate, w_post, w_pre, y, n, rstd_post=None, rstd_pre=None, alpha=1.0,
@@ -583,15 +589,14 @@ def norm_residual(b, r, gate, w_post, w_pre, y, n, rstd_post=None, rstd_pre=None
     may be r, or None) and the norm before the next branch (n [T, d] bf16, or
     None).  rstd_post, rstd_pre [T] fp32 receive the statistics that the
     backward reads (None: not wanted)."""
-    T, d, c = _norm_config(r, gate, alpha, beta, eps)
-    rt = (r.dtype,)
+    rows, chan, tok, c = _norm_config(r, gate, alpha, beta, eps)
     _check("moe_norm_residual", lib().moe_norm_residual(
-        ctypes.byref(c), _rows("b", b, T, d, (bf16,), True), _rows("r", r, T, d, (bf16, f32)),
-        _rows("gate", gate, T if c.gate_per_token else None, d, (bf16,), True),
-        _rows("w_post", w_post, None, d, (bf16,), True),
-        _rows("w_pre", w_pre, None, d, (bf16,), True), _rows("y", y, T, d, rt, True),
-        _rows("n", n, T, d, (bf16,), True), _rows("rstd_post", rstd_post, T, None, (f32,), True),
-        _rows("rstd_pre", rstd_pre, T, None, (f32,), True), _stream(stream)))
+        ctypes.byref(c), _rows("b", b, rows, _BF16, True), _rows("r", r, rows, _RES),
+        _rows("gate", gate, rows if c.gate_per_token else chan, _BF16, True),
+        _rows("w_post", w_post, chan, _BF16, True), _rows("w_pre", w_pre, chan, _BF16, True),
+        _rows("y", y, rows, (r.dtype,), True), _rows("n", n, rows, _BF16, True),
+        _rows("rstd_post", rstd_post, tok, _F32, True),
+        _rows("rstd_pre", rstd_pre, tok, _F32, True), _stream(stream)))
 
 
 def norm_residual_workspace(T, d) -> int:
@@ -608,25 +613,18 @@ def norm_residual_backward(dn, dy, b, r, gate, w_post, w_pre, rstd_post, rstd_pr
     passes this norm by; None: zero): db, dr (may be dy), dgate ([d] fp32 for
     a [d] gate, else [T, d] bf16), dw_post, dw_pre [d] fp32.  None exactly
     where the forward's tensor is."""
-    shape = dr
-    T, d, c = _norm_config(shape, gate, alpha, beta, 0.0)
-    if r is not None and r.dtype != dr.dtype:
-        raise TypeError("dr has the residual stream's type")
-    rt = (dr.dtype,)
+    rows, chan, tok, c = _norm_config(dr, gate, alpha, beta, 0.0)
+    rt, at = (dr.dtype,), rows if c.gate_per_token else chan
     _check("moe_norm_residual_backward", lib().moe_norm_residual_backward(
-        ctypes.byref(c), _rows("dn", dn, T, d, (bf16,), True), _rows("dy", dy, T, d, rt, True),
-        _rows("b", b, T, d, (bf16,), True), _rows("r", r, T, d, rt, True),
-        _rows("gate", gate, T if c.gate_per_token else None, d, (bf16,), True),
-        _rows("w_post", w_post, None, d, (bf16,), True),
-        _rows("w_pre", w_pre, None, d, (bf16,), True),
-        _rows("rstd_post", rstd_post, T, None, (f32,), True),
-        _rows("rstd_pre", rstd_pre, T, None, (f32,), True), _rows("db", db, T, d, (bf16,), True),
-        _rows("dr", dr, T, d, (bf16, f32)),
-        _rows("dgate", dgate, T if c.gate_per_token else None, d,
-              (bf16,) if c.gate_per_token else (f32,), True),
-        _rows("dw_post", dw_post, None, d, (f32,), True),
-        _rows("dw_pre", dw_pre, None, d, (f32,), True), _ptr(ws, u8), ws.numel(),
-        _stream(stream)))
+        ctypes.byref(c), _rows("dn", dn, rows, _BF16, True), _rows("dy", dy, rows, rt, True),
+        _rows("b", b, rows, _BF16, True), _rows("r", r, rows, rt, True),
+        _rows("gate", gate, at, _BF16, True), _rows("w_post", w_post, chan, _BF16, True),
+        _rows("w_pre", w_pre, chan, _BF16, True), _rows("rstd_post", rstd_post, tok, _F32, True),
+        _rows("rstd_pre", rstd_pre, tok, _F32, True), _rows("db", db, rows, _BF16, True),
+        _rows("dr", dr, rows, _RES),
+        _rows("dgate", dgate, at, _BF16 if c.gate_per_token else _F32, True),
+        _rows("dw_post", dw_post, chan, _F32, True), _rows("dw_pre", dw_pre, chan, _F32, True),
+        _ptr(ws, u8), ws.numel(), _stream(stream)))
 
 
 ROTARY_SCALING = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
@@ -646,19 +644,17 @@ def rotary_table(table, base=10000.0, scaling="none", factor=1.0, orig_len=0.0, 
         ctypes.byref(c), _ptr(table, f32), _stream(stream)))
 
 
-def _heads(name, t, T, heads, D):
-    """(pointer, token stride, head stride) of a [T, heads, D] bf16 tensor
+def _heads(name, t, shape):
+    """(address, token stride, head stride) of a [T, heads, D] bf16 tensor
     whose channels are contiguous (tokens and heads may be strided)."""
     if t.dtype != bf16:
         raise TypeError(f"{name}: expected {bf16}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: tensors must live on the GPU")
-    if t.dim() != 3 or tuple(t.shape) != (T, heads, D):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, heads, D)}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
     st, sh, sd = t.stride()
-    if sd != 1:
-        raise ValueError(f"{name}: channels must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), st, sh
+    if not t.is_cuda or sd != 1:
+        raise ValueError(f"{name}: device tensor with contiguous channels required")
+    return t.data_ptr(), st, sh
 
 
 def rotary(q, k, table, pos, q_out, k_out, status, interleaved=False, inverse=False, stream=None):
@@ -668,10 +664,11 @@ def rotary(q, k, table, pos, q_out, k_out, status, interleaved=False, inverse=Fa
     the gradient's direction.  interleaved: pairs side by side."""
     T, hq, D = q.shape
     hk = 0 if k is None else k.shape[1]
-    qp, qt, qh = _heads("q", q, T, hq, D)
-    qop, qot, qoh = _heads("q_out", q_out, T, hq, D)
-    kp, kt, kh = (None, 0, 0) if k is None else _heads("k", k, T, hk, D)
-    kop, kot, koh = (None, 0, 0) if k is None else _heads("k_out", k_out, T, hk, D)
+    qs, ks = (T, hq, D), (T, hk, D)
+    qp, qt, qh = _heads("q", q, qs)
+    qop, qot, qoh = _heads("q_out", q_out, qs)
+    kp, kt, kh = (None, 0, 0) if k is None else _heads("k", k, ks)
+    kop, kot, koh = (None, 0, 0) if k is None else _heads("k_out", k_out, ks)
     if table.dim() != 3 or table.shape[2] != 2:
         raise ValueError("the table is [positions, rot_dim / 2, 2]")
     if pos is not None and tuple(pos.shape) != (T,):
@@ -698,42 +695,26 @@ class AttentionPlan:
             raise ValueError("cu_seqlens is [sequences + 1]")
         pb, bb = ctypes.c_int64(), ctypes.c_int64()
         _check("moe_attention_workspace", lib().moe_attention_workspace(
-            ctypes.byref(self._config(1.0)), ctypes.byref(pb), ctypes.byref(bb)))
+            ctypes.byref(self._config()), ctypes.byref(pb), ctypes.byref(bb)))
         self.backward_ws_bytes = bb.value
         self.status = (torch.zeros(1, dtype=i32, device=cu_seqlens.device) if status is None
                        else status)
         self.plan = torch.empty(pb.value, dtype=u8, device=cu_seqlens.device)
+        self.address = self.plan.data_ptr()
+        self.q_shape, self.k_shape = (T, n_heads, head_dim), (T, n_kv_heads, head_dim)
+        self.lse_shape = (n_heads, T)
         self.refill(cu_seqlens, stream)
 
-    def _config(self, scale):
-        c = Attention()
-        c.T, c.n_seqs, c.n_heads = self.T, self.n_seqs, self.n_heads
-        c.n_kv_heads, c.head_dim, c.scale = self.n_kv_heads, self.head_dim, scale
-        return c
+    def _config(self, scale=None):
+        return Attention(self.T, self.n_seqs, self.n_heads, self.n_kv_heads, self.head_dim,
+                         self.head_dim ** -0.5 if scale is None else scale)
 
     def refill(self, cu_seqlens, stream=None):
         if tuple(cu_seqlens.shape) != (self.n_seqs + 1,):
             raise ValueError("cu_seqlens of another number of sequences")
         _check("moe_attention_plan", lib().moe_attention_plan(
-            ctypes.byref(self._config(1.0)), _ptr(cu_seqlens, i32), _ptr(self.plan, u8),
+            ctypes.byref(self._config()), _ptr(cu_seqlens, i32), _ptr(self.plan, u8),
             self.plan.numel(), _ptr(self.status, i32), _stream(stream)))
-
-
-def _attention_config(plan, scale, **tensors):
-    c = plan._config(plan.head_dim ** -0.5 if scale is None else scale)
-    ptrs = []
-    for name, t in tensors.items():
-        heads = plan.n_kv_heads if name in ("k", "v", "dk", "dv") else plan.n_heads
-        p, st, sh = _heads(name, t, plan.T, heads, plan.head_dim)
-        key = {"out": "o", "dout": "do"}.get(name, name)
-        if key == "rest":
-            if (st, sh) != (c.o_t, c.o_h):
-                raise ValueError("rest has out's strides")
-        else:
-            setattr(c, key + "_t", st)
-            setattr(c, key + "_h", sh)
-        ptrs.append(p)
-    return c, ptrs
 
 
 def attention(plan, q, k, v, out, lse, status, scale=None, rest=None, stream=None):
@@ -741,26 +722,43 @@ def attention(plan, q, k, v, out, lse, status, scale=None, rest=None, stream=Non
     n_heads, D], k, v [T, n_kv_heads, D] bf16 (strided views allowed), lse
     [n_heads, T] fp32; scale D^-1/2 unless given.  rest (like out): what
     rounding took from out, for attention_backward (None: no gradient)."""
-    given = dict(q=q, k=k, v=v, out=out)
-    if rest is not None:
-        given["rest"] = rest
-    c, p = _attention_config(plan, scale, **given)
+    c = plan._config(scale)
+    qs, ks = plan.q_shape, plan.k_shape
+    qp, c.q_t, c.q_h = _heads("q", q, qs)
+    kp, c.k_t, c.k_h = _heads("k", k, ks)
+    vp, c.v_t, c.v_h = _heads("v", v, ks)
+    op, c.o_t, c.o_h = _heads("out", out, qs)
+    rp = None if rest is None else _rest(rest, qs, c)
     _check("moe_attention_forward", lib().moe_attention_forward(
-        ctypes.byref(c), _ptr(plan.plan, u8), p[0], p[1], p[2], p[3],
-        p[4] if rest is not None else None, _rows("lse", lse, plan.n_heads, plan.T, (f32,)),
+        ctypes.byref(c), plan.address, qp, kp, vp, op, rp, _rows("lse", lse, plan.lse_shape, _F32),
         _ptr(status, i32), _stream(stream)))
+
+
+def _rest(rest, shape, c):
+    p, st, sh = _heads("rest", rest, shape)
+    if (st, sh) != (c.o_t, c.o_h):
+        raise ValueError("rest has out's strides")
+    return p
 
 
 def attention_backward(plan, q, k, v, out, rest, lse, dout, dq, dk, dv, ws, status, scale=None,
                        stream=None):
     """dq, dk, dv of attention for the upstream gradient dout, from the
     forward's inputs and its out, rest and lse; ws: plan.backward_ws_bytes."""
-    c, p = _attention_config(plan, scale, q=q, k=k, v=v, out=out, rest=rest, dout=dout, dq=dq,
-                             dk=dk, dv=dv)
+    c = plan._config(scale)
+    qs, ks = plan.q_shape, plan.k_shape
+    qp, c.q_t, c.q_h = _heads("q", q, qs)
+    kp, c.k_t, c.k_h = _heads("k", k, ks)
+    vp, c.v_t, c.v_h = _heads("v", v, ks)
+    op, c.o_t, c.o_h = _heads("out", out, qs)
+    dop, c.do_t, c.do_h = _heads("dout", dout, qs)
+    dqp, c.dq_t, c.dq_h = _heads("dq", dq, qs)
+    dkp, c.dk_t, c.dk_h = _heads("dk", dk, ks)
+    dvp, c.dv_t, c.dv_h = _heads("dv", dv, ks)
     _check("moe_attention_backward", lib().moe_attention_backward(
-        ctypes.byref(c), _ptr(plan.plan, u8), p[0], p[1], p[2], p[3], p[4],
-        _rows("lse", lse, plan.n_heads, plan.T, (f32,)), p[5], p[6], p[7], p[8], _ptr(ws, u8),
-        ws.numel(), _ptr(status, i32), _stream(stream)))
+        ctypes.byref(c), plan.address, qp, kp, vp, op, _rest(rest, qs, c),
+        _rows("lse", lse, plan.lse_shape, _F32), dop, dqp, dkp, dvp, _ptr(ws, u8), ws.numel(),
+        _ptr(status, i32), _stream(stream)))
 
 
 class GradSet:

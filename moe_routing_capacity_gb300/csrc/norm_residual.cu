@@ -9,8 +9,8 @@
 // cp.async stages, each thread copying what it will read itself, so that the
 // loads of the next rows run under the sums of this one and no barrier
 // guards the ring.
-//   d <= 1024: a warp a row (1, 2 or 4 times 8 channels a lane), 8 rows a CTA.
-//   d >  1024: a CTA a row, d / 8 threads.
+//   d <= 256: a warp a row, 8 rows a CTA.  d > 256: a CTA a row, d / 8
+//   threads, several CTAs an SM while their registers allow.
 // The backward's sums over tokens (dw_post, dw_pre, dgate) stay in registers
 // over all of a CTA's rows; each CTA writes one partial row and a second
 // kernel adds the partials in their order: no atomics.
@@ -26,7 +26,7 @@ namespace {
 struct NormParams {
     int64_t T;
     int d, chunks;            // chunks = d / 8
-    int stages, slots;        // ring depth; 16-byte slots of a thread and chunk
+    int stages;               // ring depth
     float alpha, beta, eps, inv_d;
     const uint16_t *b, *gate, *w_post, *w_pre, *dn;
     const void *r, *dy;
@@ -35,28 +35,27 @@ struct NormParams {
     uint16_t *n, *db;
     float *rstd_post, *rstd_pre;          // forward: out
     const float *in_post, *in_pre;        // backward: in
-    float* part;                           // [CTAs, 3, d]
+    float* part;                           // [CTAs, 2, d]
 };
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf16_lo(w[i]);
-        f[2 * i + 1] = bf16_hi(w[i]);
-    }
+// Eight channels as four pairs.
+__device__ __forceinline__ void unpack8(const uint4& v, float2 (&f)[4]) {
+    f[0] = bf16x2_f32(v.x);
+    f[1] = bf16x2_f32(v.y);
+    f[2] = bf16x2_f32(v.z);
+    f[3] = bf16x2_f32(v.w);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
+    return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
+                      pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
 }
 
-__device__ __forceinline__ void as_floats(const uint4& a, const uint4& b, float (&f)[8]) {
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+__device__ __forceinline__ float2 as_float2(uint32_t a, uint32_t b) {
+    return make_float2(__uint_as_float(a), __uint_as_float(b));
 }
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 __device__ __forceinline__ float sum32(float v) {
 #pragma unroll
@@ -87,19 +86,24 @@ __device__ __forceinline__ void wait_stage(int stages) {
 
 // A residual-stream chunk: one slot of bf16 or two of fp32.
 template <bool F32>
-__device__ __forceinline__ void load_res(const uint4* slot, int pitch, float (&f)[8]) {
-    if (F32)
-        as_floats(slot[0], slot[pitch], f);
-    else
+__device__ __forceinline__ void load_res(const uint4* slot, int pitch, float2 (&f)[4]) {
+    if (F32) {
+        const uint4 a = slot[0], b = slot[pitch];
+        f[0] = as_float2(a.x, a.y);
+        f[1] = as_float2(a.z, a.w);
+        f[2] = as_float2(b.x, b.y);
+        f[3] = as_float2(b.z, b.w);
+    } else {
         unpack8(slot[0], f);
+    }
 }
 
 template <bool F32>
-__device__ __forceinline__ void store_res(void* base, int64_t at, const float (&f)[8]) {
+__device__ __forceinline__ void store_res(void* base, int64_t at, const float2 (&f)[4]) {
     if (F32) {
         float4* o = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
-        o[0] = make_float4(f[0], f[1], f[2], f[3]);
-        o[1] = make_float4(f[4], f[5], f[6], f[7]);
+        o[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+        o[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
     } else {
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = pack8(f);
     }
@@ -117,114 +121,99 @@ __device__ __forceinline__ void copy_res(uint32_t dst, uint32_t pitch, const voi
     }
 }
 
+// beta w_post (with a gate that all tokens share: times the gate) of 8 channels.
+__device__ __forceinline__ void load_factor(const NormParams& p, bool with_gate, int c,
+                                            float2 (&G)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) G[e] = both(0.f);
+    if (!p.w_post || c >= p.chunks) return;
+    float2 g[4];
+    unpack8(*reinterpret_cast<const uint4*>(p.w_post + c * 8), G);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) G[e] = mul2(G[e], both(p.beta));
+    if (!with_gate || p.gate_mode != 1) return;
+    unpack8(*reinterpret_cast<const uint4*>(p.gate + c * 8), g);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) G[e] = mul2(G[e], g[e]);
+}
+
 // ------------------------------------------------------------------ forward
 
-// Slots of a thread and chunk: b, gate (if per token), r (1 or 2).
-template <bool F32, bool WARP, int CH, int NT, int OCC>
+// Slots of a thread and chunk: b, gate (TOKEN), r (1 or 2).  TOKEN: a gate
+// value for each token and channel; otherwise beta, the gate and w_post are
+// one factor a channel, held in fp32 over all rows.
+template <bool F32, bool TOKEN, bool WARP, int NT, int OCC>
 __global__ void __launch_bounds__(NT, OCC) norm_fwd_kernel(const NormParams p) {
     extern __shared__ uint4 ring[];
     __shared__ float red[4][32];
+    constexpr int SLOTS = 1 + TOKEN + (F32 ? 2 : 1);
     const int nt = blockDim.x;
     const int lane = WARP ? threadIdx.x & 31 : threadIdx.x;
-    const int gs = WARP ? 32 : nt;
     const int rows = WARP ? nt / 32 : 1;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows + (WARP ? threadIdx.x >> 5 : 0);
     const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
+    const int col = lane * 8;               // this thread's channels
+    const bool in = lane < p.chunks;
     const bool has_b = p.b != nullptr, has_n = p.n != nullptr;
-    const int s_gate = 1, s_r = p.gate_mode == 2 ? 2 : 1;
-    const auto slot = [&](int stage, int i, int k) {
-        return ((stage * CH + i) * p.slots + k) * nt + static_cast<int>(threadIdx.x);
+    const auto slot = [&](int stage, int k) {
+        return (stage * SLOTS + k) * nt + static_cast<int>(threadIdx.x);
     };
     const auto fetch = [&](int64_t row, int stage) {
-        if (row < p.T) {
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int c = lane + gs * i;
-                if (c < p.chunks) {
-                    const int64_t at = row * p.d + c * 8;
-                    if (has_b) cp_async_16(smem_u32(ring + slot(stage, i, 0)), p.b + at, 16);
-                    if (p.gate_mode == 2)
-                        cp_async_16(smem_u32(ring + slot(stage, i, s_gate)), p.gate + at, 16);
-                    copy_res<F32>(smem_u32(ring + slot(stage, i, s_r)), nt * 16, p.r, at);
-                }
-            }
+        if (in && row < p.T) {
+            const int64_t at = row * p.d + col;
+            if (has_b) cp_async_16(smem_u32(ring + slot(stage, 0)), p.b + at, 16);
+            if (TOKEN) cp_async_16(smem_u32(ring + slot(stage, 1)), p.gate + at, 16);
+            copy_res<F32>(smem_u32(ring + slot(stage, 1 + TOKEN)), nt * 16, p.r, at);
         }
         cp_async_commit();
     };
     for (int s = 0; s < p.stages; ++s) fetch(row0 + s * step, s);
 
-    uint4 wq[CH], wp[CH], wg[CH];
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        const int c = lane + gs * i;
-        wq[i] = wp[i] = wg[i] = make_uint4(0, 0, 0, 0);
-        if (c < p.chunks) {
-            if (has_b) wq[i] = *reinterpret_cast<const uint4*>(p.w_post + c * 8);
-            if (has_n) wp[i] = *reinterpret_cast<const uint4*>(p.w_pre + c * 8);
-            if (p.gate_mode == 1) wg[i] = *reinterpret_cast<const uint4*>(p.gate + c * 8);
-        }
-    }
+    float2 G[4];
+    load_factor(p, !TOKEN, lane, G);
+    uint4 wp = make_uint4(0, 0, 0, 0);
+    if (in && has_n) wp = *reinterpret_cast<const uint4*>(p.w_pre + col);
     int stage = 0, par = 0;
     for (int64_t row = row0; row < p.T; row += step) {
         wait_stage(p.stages);
-        float b[CH][8], y[CH][8];
-        uint4 gt[CH];
-        float ss = 0.f;
+        float2 b[4], y[4], ss = both(0.f);
+        float2 g[4];
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
+        for (int e = 0; e < 4; ++e) b[e] = y[e] = g[e] = both(0.f);
+        if (in) {
+            if (has_b) unpack8(ring[slot(stage, 0)], b);
+            if (TOKEN) unpack8(ring[slot(stage, 1)], g);
+            load_res<F32>(ring + slot(stage, 1 + TOKEN), nt, y);
+        }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) b[i][e] = y[i][e] = 0.f;
-            gt[i] = wg[i];
-            if (lane + gs * i < p.chunks) {
-                if (has_b) unpack8(ring[slot(stage, i, 0)], b[i]);
-                if (p.gate_mode == 2) gt[i] = ring[slot(stage, i, s_gate)];
-                load_res<F32>(ring + slot(stage, i, s_r), nt, y[i]);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                ss += b[i][e] * b[i][e];
-                y[i][e] *= p.alpha;
-            }
+        for (int e = 0; e < 4; ++e) {
+            ss = fma2(b[e], b[e], ss);
+            y[e] = mul2(y[e], both(p.alpha));
+            if (TOKEN) b[e] = mul2(b[e], g[e]);
         }
         fetch(row + p.stages * step, stage);   // this thread has read the slots
         if (++stage == p.stages) stage = 0;
         if (has_b) {
-            const float rb = rsqrtf(row_sum<WARP>(ss, red[par]) * p.inv_d + p.eps);
+            const float rb = rsqrtf(row_sum<WARP>(ss.x + ss.y, red[par]) * p.inv_d + p.eps);
             if (lane == 0 && p.rstd_post) p.rstd_post[row] = rb;
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                float w[8], g[8];
-                unpack8(wq[i], w);
-                unpack8(gt[i], g);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float u = p.beta * (b[i][e] * rb * w[e]);
-                    y[i][e] += p.gate_mode ? u * g[e] : u;
-                }
-            }
+            for (int e = 0; e < 4; ++e)
+                y[e] = fma2(G[e], mul2(b[e], both(rb)), y[e]);
         }
-        if (p.y)
-#pragma unroll
-            for (int i = 0; i < CH; ++i)
-                if (lane + gs * i < p.chunks)
-                    store_res<F32>(p.y, row * p.d + (lane + gs * i) * 8, y[i]);
+        if (p.y && in)
+            store_res<F32>(p.y, row * p.d + col, y);
         if (has_n) {
-            ss = 0.f;
+            ss = both(0.f);
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss += y[i][e] * y[i][e];
-            const float ry = rsqrtf(row_sum<WARP>(ss, red[2 + par]) * p.inv_d + p.eps);
+            for (int e = 0; e < 4; ++e) ss = fma2(y[e], y[e], ss);
+            const float ry = rsqrtf(row_sum<WARP>(ss.x + ss.y, red[2 + par]) * p.inv_d + p.eps);
             if (lane == 0 && p.rstd_pre) p.rstd_pre[row] = ry;
+            float2 w[4];
+            unpack8(wp, w);
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                float w[8];
-                unpack8(wp[i], w);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] *= y[i][e] * ry;
-                if (lane + gs * i < p.chunks)
-                    *reinterpret_cast<uint4*>(p.n + row * p.d + (lane + gs * i) * 8) = pack8(w);
-            }
+            for (int e = 0; e < 4; ++e) w[e] = mul2(w[e], mul2(y[e], both(ry)));
+            if (in)
+                *reinterpret_cast<uint4*>(p.n + row * p.d + col) = pack8(w);
         }
         par ^= 1;
     }
@@ -232,149 +221,124 @@ __global__ void __launch_bounds__(NT, OCC) norm_fwd_kernel(const NormParams p) {
 
 // ------------------------------------------------------------------ backward
 
-// Slots of a thread and chunk: b, dn, gate (if per token), r, dy (1 or 2 each).
-template <bool F32, bool WARP, int CH, int NT, int OCC>
+// Slots of a thread and chunk: b, dn, gate (TOKEN), r, dy (1 or 2 each).
+// Two sums over the tokens: dw_pre = sum dn q, and S = sum p du (TOKEN: sum
+// g p du), from which dw_post = beta g S and dgate = beta w_post S follow a
+// channel at the end, for a gate that all tokens share.
+template <bool F32, bool TOKEN, bool WARP, int NT, int OCC>
 __global__ void __launch_bounds__(NT, OCC) norm_bwd_kernel(const NormParams p) {
     extern __shared__ uint4 ring[];
     __shared__ float red[4][32];
+    constexpr int R = F32 ? 2 : 1, SLOTS = 2 + TOKEN + 2 * R;
+    constexpr int s_dn = 1, s_gate = 2, s_r = 2 + TOKEN, s_dy = s_r + R;
     const int nt = blockDim.x;
     const int lane = WARP ? threadIdx.x & 31 : threadIdx.x;
-    const int gs = WARP ? 32 : nt;
     const int rows = WARP ? nt / 32 : 1;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows + (WARP ? threadIdx.x >> 5 : 0);
     const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
+    const int col = lane * 8;               // this thread's channels
+    const bool in = lane < p.chunks;
     const bool has_b = p.b != nullptr, has_n = p.dn != nullptr, has_y = p.dy != nullptr;
-    const int s_dn = 1, s_gate = 2, s_r = p.gate_mode == 2 ? 3 : 2, s_dy = s_r + (F32 ? 2 : 1);
-    const auto slot = [&](int stage, int i, int k) {
-        return ((stage * CH + i) * p.slots + k) * nt + static_cast<int>(threadIdx.x);
+    const auto slot = [&](int stage, int k) {
+        return (stage * SLOTS + k) * nt + static_cast<int>(threadIdx.x);
     };
     const auto fetch = [&](int64_t row, int stage) {
-        if (row < p.T) {
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int c = lane + gs * i;
-                if (c < p.chunks) {
-                    const int64_t at = row * p.d + c * 8;
-                    if (has_b) cp_async_16(smem_u32(ring + slot(stage, i, 0)), p.b + at, 16);
-                    if (has_n) {
-                        cp_async_16(smem_u32(ring + slot(stage, i, s_dn)), p.dn + at, 16);
-                        copy_res<F32>(smem_u32(ring + slot(stage, i, s_r)), nt * 16, p.r, at);
-                    }
-                    if (p.gate_mode == 2)
-                        cp_async_16(smem_u32(ring + slot(stage, i, s_gate)), p.gate + at, 16);
-                    if (has_y)
-                        copy_res<F32>(smem_u32(ring + slot(stage, i, s_dy)), nt * 16, p.dy, at);
-                }
+        if (in && row < p.T) {
+            const int64_t at = row * p.d + col;
+            if (has_b) cp_async_16(smem_u32(ring + slot(stage, 0)), p.b + at, 16);
+            if (has_n) {
+                cp_async_16(smem_u32(ring + slot(stage, s_dn)), p.dn + at, 16);
+                copy_res<F32>(smem_u32(ring + slot(stage, s_r)), nt * 16, p.r, at);
             }
+            if (TOKEN) cp_async_16(smem_u32(ring + slot(stage, s_gate)), p.gate + at, 16);
+            if (has_y) copy_res<F32>(smem_u32(ring + slot(stage, s_dy)), nt * 16, p.dy, at);
         }
         cp_async_commit();
     };
     for (int s = 0; s < p.stages; ++s) fetch(row0 + s * step, s);
 
-    uint4 wq[CH], wp[CH], wg[CH];
-    float a_post[CH][8], a_pre[CH][8], a_gate[CH][8];
+    float2 G[4], S[4], a_pre[4];
+    load_factor(p, !TOKEN, lane, G);
+    uint4 wp = make_uint4(0, 0, 0, 0);
+    if (in && has_n) wp = *reinterpret_cast<const uint4*>(p.w_pre + col);
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        const int c = lane + gs * i;
-        wq[i] = wp[i] = wg[i] = make_uint4(0, 0, 0, 0);
-        if (c < p.chunks) {
-            if (has_b) wq[i] = *reinterpret_cast<const uint4*>(p.w_post + c * 8);
-            if (has_n) wp[i] = *reinterpret_cast<const uint4*>(p.w_pre + c * 8);
-            if (p.gate_mode == 1) wg[i] = *reinterpret_cast<const uint4*>(p.gate + c * 8);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a_post[i][e] = a_pre[i][e] = a_gate[i][e] = 0.f;
-    }
+    for (int e = 0; e < 4; ++e) S[e] = a_pre[e] = both(0.f);
     const auto stat = [&](const float* s, int64_t row) { return s && row < p.T ? s[row] : 0.f; };
     float rb = stat(p.in_post, row0), ry = stat(p.in_pre, row0);
     int stage = 0, par = 0;
     for (int64_t row = row0; row < p.T; row += step) {
         const float rb_next = stat(p.in_post, row + step), ry_next = stat(p.in_pre, row + step);
         wait_stage(p.stages);
-        // pv: p; du: first dy, then dL/dy
-        float pv[CH][8], q[CH][8], t[CH][8], du[CH][8];
-        uint4 gt[CH];
-        float s1 = 0.f;
+        // pv: p; du: first dy, then dL/dy, then dL/dp; gt: the token's gate
+        float2 pv[4], q[4], t[4], du[4], s1 = both(0.f);
+        float2 g[4], w[4];
+        uint4 dn = make_uint4(0, 0, 0, 0), gt = dn;
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            float dn[8], w[8], g[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) pv[i][e] = q[i][e] = du[i][e] = dn[e] = 0.f;
-            gt[i] = wg[i];
-            if (lane + gs * i < p.chunks) {
-                if (has_b) unpack8(ring[slot(stage, i, 0)], pv[i]);
-                if (p.gate_mode == 2) gt[i] = ring[slot(stage, i, s_gate)];
-                if (has_n) {
-                    unpack8(ring[slot(stage, i, s_dn)], dn);
-                    load_res<F32>(ring + slot(stage, i, s_r), nt, q[i]);
-                }
-                if (has_y) load_res<F32>(ring + slot(stage, i, s_dy), nt, du[i]);
+        for (int e = 0; e < 4; ++e) pv[e] = q[e] = du[e] = both(0.f);
+        if (in) {
+            if (has_b) unpack8(ring[slot(stage, 0)], pv);
+            if (TOKEN) gt = ring[slot(stage, s_gate)];
+            if (has_n) {
+                dn = ring[slot(stage, s_dn)];
+                load_res<F32>(ring + slot(stage, s_r), nt, q);
             }
-            unpack8(wq[i], w);
-            unpack8(gt[i], g);
+            if (has_y) load_res<F32>(ring + slot(stage, s_dy), nt, du);
+        }
+        if (TOKEN) unpack8(gt, g);
+        unpack8(wp, w);
+        unpack8(dn, t);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                pv[i][e] *= rb;
-                const float u = p.beta * (pv[i][e] * w[e]);
-                q[i][e] = (p.alpha * q[i][e] + (p.gate_mode ? u * g[e] : u)) * ry;
-            }
-            unpack8(wp[i], w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                a_pre[i][e] += dn[e] * q[i][e];
-                t[i][e] = dn[e] * w[e];
-                s1 += t[i][e] * q[i][e];
-            }
+        for (int e = 0; e < 4; ++e) {
+            pv[e] = mul2(pv[e], both(rb));
+            float2 m = mul2(pv[e], G[e]);
+            if (TOKEN) m = mul2(m, g[e]);
+            q[e] = mul2(fma2(q[e], both(p.alpha), m), both(ry));
+            a_pre[e] = fma2(t[e], q[e], a_pre[e]);
+            t[e] = mul2(t[e], w[e]);
+            s1 = fma2(t[e], q[e], s1);
         }
         fetch(row + p.stages * step, stage);   // this thread has read the slots
         if (++stage == p.stages) stage = 0;
-        const float k1 = has_n ? row_sum<WARP>(s1, red[par]) * p.inv_d : 0.f;
-        float s2 = 0.f;
+        const float k1 = has_n ? row_sum<WARP>(s1.x + s1.y, red[par]) * p.inv_d : 0.f;
+        float2 s2 = both(0.f);
+        float2 o[4];
+        const int64_t at = row * p.d + col;
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            float w[8], g[8], o[8];
-            unpack8(wq[i], w);
-            unpack8(gt[i], g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                du[i][e] += ry * (t[i][e] - q[i][e] * k1);
-                o[e] = p.alpha * du[i][e];
-            }
-            const bool in = lane + gs * i < p.chunks;
-            const int64_t at = row * p.d + (lane + gs * i) * 8;
-            if (in) store_res<F32>(p.dr, at, o);
-            if (has_b) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float v = p.beta * du[i][e];
-                    o[e] = v * (pv[i][e] * w[e]);                // the gate's gradient
-                    const float dm = p.gate_mode ? v * g[e] : v;
-                    a_gate[i][e] += o[e];
-                    a_post[i][e] += dm * pv[i][e];
-                    du[i][e] = dm * w[e];                        // dL/dp
-                    s2 += du[i][e] * pv[i][e];
-                }
-                if (p.gate_mode == 2 && in)
-                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dgate) + at) = pack8(o);
-            }
+        for (int e = 0; e < 4; ++e) {
+            du[e] = fma2(both(ry), fma2(q[e], both(-k1), t[e]), du[e]);
+            o[e] = mul2(du[e], both(p.alpha));
         }
-        if (has_b) {
-            const float k2 = row_sum<WARP>(s2, red[2 + par]) * p.inv_d;
+        if (in) store_res<F32>(p.dr, at, o);
+        if (TOKEN) unpack8(gt, g);
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                float o[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = rb * (du[i][e] - pv[i][e] * k2);
-                if (lane + gs * i < p.chunks)
-                    *reinterpret_cast<uint4*>(p.db + row * p.d + (lane + gs * i) * 8) = pack8(o);
+        for (int e = 0; e < 4; ++e) {
+            const float2 pd = mul2(pv[e], du[e]);
+            du[e] = mul2(du[e], G[e]);
+            if (TOKEN) {
+                o[e] = mul2(pd, G[e]);
+                S[e] = fma2(pd, g[e], S[e]);
+                du[e] = mul2(du[e], g[e]);
+            } else {
+                S[e] = add2(S[e], pd);
             }
+            s2 = fma2(du[e], pv[e], s2);
+        }
+        if (TOKEN && in)
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dgate) + at) = pack8(o);
+        if (has_b) {
+            const float k2 = row_sum<WARP>(s2.x + s2.y, red[2 + par]) * p.inv_d;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[e] = mul2(both(rb), fma2(pv[e], both(-k2), du[e]));
+            if (in)
+                *reinterpret_cast<uint4*>(p.db + row * p.d + col) = pack8(o);
         }
         par ^= 1;
         rb = rb_next;
         ry = ry_next;
     }
-    // this CTA's partial sums over its tokens: post, pre, gate
-    float* part = p.part + static_cast<int64_t>(blockIdx.x) * 3 * p.d;
+    // this CTA's partial sums over its tokens: S, then dw_pre
+    float* part = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.d;
     float* acc = reinterpret_cast<float*>(ring);
     const int turns = WARP ? rows : 1;
     if (WARP) {
@@ -384,21 +348,19 @@ __global__ void __launch_bounds__(NT, OCC) norm_bwd_kernel(const NormParams p) {
     for (int w = 0; w < turns; ++w) {
         if (!WARP || static_cast<int>(threadIdx.x >> 5) == w) {
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int c = lane + gs * i;
-                if (c >= p.chunks) continue;
+            for (int k = 0; k < 2; ++k) {
+                const float2* v = k ? a_pre : S;
+                float4* to = reinterpret_cast<float4*>((w + 1 < turns ? acc : part) + k * p.d + col);
+                const float4* was = reinterpret_cast<const float4*>(acc + k * p.d + col);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float v[3] = {a_post[i][e], a_pre[i][e], a_gate[i][e]};
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        const int at = k * p.d + c * 8 + e;
-                        const float sum = w ? acc[at] + v[k] : v[k];
-                        if (w + 1 < turns)
-                            acc[at] = sum;
-                        else
-                            part[at] = sum;
+                for (int e = 0; e < 2; ++e) {
+                    if (!in) break;
+                    float4 x = make_float4(v[2 * e].x, v[2 * e].y, v[2 * e + 1].x, v[2 * e + 1].y);
+                    if (w) {
+                        const float4 y = was[e];
+                        x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
                     }
+                    to[e] = x;
                 }
             }
         }
@@ -406,64 +368,75 @@ __global__ void __launch_bounds__(NT, OCC) norm_bwd_kernel(const NormParams p) {
     }
 }
 
-// out_k[c] = sum over the partial rows, in a fixed order: 32 columns a CTA,
-// eight threads a column over an eighth of the rows each.
-__global__ void __launch_bounds__(256) norm_sums_kernel(const float* part, int n, int d, float* o0,
-                                                        float* o1, float* o2) {
+// The sums over the partial rows in a fixed order (32 columns a CTA, eight
+// threads a column over an eighth of the rows each), and what follows from S.
+__global__ void __launch_bounds__(256) norm_sums_kernel(const NormParams p, int n, float* dw_post,
+                                                        float* dw_pre, float* dgate) {
     __shared__ float s[8][32];
     const int x = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + x;
+    const bool in = col < 2ll * p.d;
     float v = 0.f;
-    if (col < 3ll * d)
+    if (in)
 #pragma unroll 8
-        for (int i = g; i < n; i += 8) v += part[static_cast<int64_t>(i) * 3 * d + col];
+        for (int i = g; i < n; i += 8) v += p.part[static_cast<int64_t>(i) * 2 * p.d + col];
     s[g][x] = v;
     __syncthreads();
-    if (g == 0 && col < 3ll * d) {
+    if (g == 0 && in) {
 #pragma unroll
         for (int i = 1; i < 8; ++i) v += s[i][x];
-        const int k = static_cast<int>(col / d);
-        float* o = k == 0 ? o0 : k == 1 ? o1 : o2;
-        if (o) o[col - static_cast<int64_t>(k) * d] = v;
+        if (col >= p.d) {
+            if (dw_pre) dw_pre[col - p.d] = v;
+            return;
+        }
+        v *= p.beta;
+        const auto bf = [](const uint16_t* t, int64_t i) {
+            return __uint_as_float(static_cast<uint32_t>(t[i]) << 16);
+        };
+        if (dw_post) dw_post[col] = p.gate_mode == 1 ? v * bf(p.gate, col) : v;
+        if (dgate) dgate[col] = v * bf(p.w_post, col);
     }
 }
 
-// One launch shape for a width: threads, chunks a thread, CTAs an SM.
+// The launch shape for a width: threads and rows of a CTA, CTAs an SM (as
+// many as the kernels' registers allow; 80 a thread backward).
 struct Shape {
     int threads, rows, occ, grid, stages, smem;
 };
 
+constexpr int ctas_per_sm(int threads, bool bwd) {
+    return threads <= 64    ? (bwd ? 12 : 16)
+           : threads <= 128 ? (bwd ? 6 : 8)
+           : threads <= 256 ? (bwd ? 3 : 4)
+           : threads <= 512 ? (bwd ? 1 : 2)
+                            : 1;
+}
+
+constexpr int kWarpRowsBackward = 2;   // rows of a warp: a few more registers
+
 // ring budget of an SM; a CTA's share keeps room for its 512 bytes of sums
-constexpr int kRingBytes = 220 * 1024;
+constexpr int kRingBytes = 212 * 1024;
 
 Shape norm_shape(int64_t T, int d, int slots, int sms, bool bwd) {
     Shape s;
     const int chunks = d / 8;
-    int per_thread = 1;
-    if (chunks <= 128) {
-        s.threads = 256;
-        s.rows = 8;
-        per_thread = chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4;
-        s.occ = per_thread == 4 ? (bwd ? 1 : 2) : (bwd ? 2 : 4);
-    } else {
-        s.threads = (chunks + 31) / 32 * 32;
-        s.rows = 1;
-        s.occ = s.threads <= 256 ? (bwd ? 2 : 4) : s.threads <= 512 ? (bwd ? 1 : 2) : 1;
-    }
-    const int stage_bytes = s.threads * per_thread * slots * 16;
+    s.rows = chunks <= 32 ? 8 : 1;
+    s.threads = chunks <= 32 ? 256 : (chunks + 31) / 32 * 32;
+    s.occ = s.rows > 1 && bwd ? kWarpRowsBackward : ctas_per_sm(s.threads, bwd);
+    const int stage_bytes = s.threads * slots * 16;
     s.stages = kRingBytes / s.occ / stage_bytes;
     s.stages = s.stages > 4 ? 4 : s.stages < 2 ? 2 : s.stages;
     s.smem = s.stages * stage_bytes;
-    if (bwd && s.rows > 1 && s.smem < 3 * d * 4) s.smem = 3 * d * 4;   // the warps' sums
     const int64_t want = (T + s.rows - 1) / s.rows;
     s.grid = static_cast<int>(want < static_cast<int64_t>(s.occ) * sms ? want : s.occ * sms);
     return s;
 }
 
-template <bool F32, bool WARP, int CH, int NT, int OF, int OB>
+template <bool F32, bool TOKEN, bool WARP, int NT>
 int launch_norm(const NormParams& p, const Shape& s, bool bwd, cudaStream_t st) {
-    const auto f = norm_fwd_kernel<F32, WARP, CH, NT, OF>;
-    const auto b = norm_bwd_kernel<F32, WARP, CH, NT, OB>;
+    const auto f = norm_fwd_kernel<F32, TOKEN, WARP, NT, ctas_per_sm(NT, false)>;
+    const auto b = norm_bwd_kernel<F32, TOKEN, WARP, NT,
+                                   WARP ? kWarpRowsBackward : ctas_per_sm(NT, true)>;
     if (ensure_smem_attr(bwd ? reinterpret_cast<const void*>(b) : reinterpret_cast<const void*>(f),
                          s.smem))
         return MOE_ECUDA;
@@ -476,15 +449,21 @@ int launch_norm(const NormParams& p, const Shape& s, bool bwd, cudaStream_t st) 
     return MOE_OK;
 }
 
-template <bool F32>
+template <bool F32, bool TOKEN>
 int launch_width(const NormParams& p, const Shape& s, bool bwd, cudaStream_t st) {
-    if (p.chunks <= 32) return launch_norm<F32, true, 1, 256, 4, 2>(p, s, bwd, st);
-    if (p.chunks <= 64) return launch_norm<F32, true, 2, 256, 4, 2>(p, s, bwd, st);
-    if (p.chunks <= 128) return launch_norm<F32, true, 4, 256, 2, 1>(p, s, bwd, st);
-    if (p.chunks <= 256) return launch_norm<F32, false, 1, 256, 4, 2>(p, s, bwd, st);
-    if (p.chunks <= 512) return launch_norm<F32, false, 1, 512, 2, 1>(p, s, bwd, st);
-    if (p.chunks <= 768) return launch_norm<F32, false, 1, 768, 1, 1>(p, s, bwd, st);
-    return launch_norm<F32, false, 1, 1024, 1, 1>(p, s, bwd, st);
+    if (s.rows > 1) return launch_norm<F32, TOKEN, true, 256>(p, s, bwd, st);
+    if (s.threads <= 64) return launch_norm<F32, TOKEN, false, 64>(p, s, bwd, st);
+    if (s.threads <= 128) return launch_norm<F32, TOKEN, false, 128>(p, s, bwd, st);
+    if (s.threads <= 256) return launch_norm<F32, TOKEN, false, 256>(p, s, bwd, st);
+    if (s.threads <= 512) return launch_norm<F32, TOKEN, false, 512>(p, s, bwd, st);
+    if (s.threads <= 768) return launch_norm<F32, TOKEN, false, 768>(p, s, bwd, st);
+    return launch_norm<F32, TOKEN, false, 1024>(p, s, bwd, st);
+}
+
+int launch_any(const NormParams& p, const Shape& s, bool f32, bool bwd, cudaStream_t st) {
+    const bool token = p.gate_mode == 2;
+    if (f32) return token ? launch_width<true, true>(p, s, bwd, st) : launch_width<true, false>(p, s, bwd, st);
+    return token ? launch_width<false, true>(p, s, bwd, st) : launch_width<false, false>(p, s, bwd, st);
 }
 
 NormParams norm_params(const moe_norm_t& c, const uint16_t* b, const void* r, const uint16_t* gate,
@@ -520,17 +499,17 @@ int launch_norm_residual(const moe_norm_t& c, const uint16_t* b, const void* r,
     p.n = n;
     p.rstd_post = rstd_post;
     p.rstd_pre = rstd_pre;
-    p.slots = 1 + (p.gate_mode == 2) + (c.res_f32 ? 2 : 1);
-    const Shape s = norm_shape(c.T, c.d, p.slots, sms, false);
+    const int slots = 1 + (p.gate_mode == 2) + (c.res_f32 ? 2 : 1);
+    const Shape s = norm_shape(c.T, c.d, slots, sms, false);
     p.stages = s.stages;
-    return c.res_f32 ? launch_width<true>(p, s, false, st) : launch_width<false>(p, s, false, st);
+    return launch_any(p, s, c.res_f32, false, st);
 }
 
-// Partial rows for the most CTAs of any device this runs on, two an SM.
-constexpr int64_t kMaxPartRows = 2 * 160;
+// Partial rows: the most CTAs of a launch, on a device of 160 SMs at most.
+constexpr int64_t kMaxPartRows = ctas_per_sm(64, true) * 160;
 
 int64_t norm_backward_ws(int64_t T, int d) {
-    return (T < kMaxPartRows ? T : kMaxPartRows) * 3 * d * 4;
+    return (T < kMaxPartRows ? T : kMaxPartRows) * 2 * d * 4;
 }
 
 int launch_norm_residual_backward(const moe_norm_t& c, const uint16_t* dn, const void* dy,
@@ -550,15 +529,12 @@ int launch_norm_residual_backward(const moe_norm_t& c, const uint16_t* dn, const
     p.in_post = rstd_post;
     p.in_pre = rstd_pre;
     p.part = static_cast<float*>(ws);
-    p.slots = 2 + (p.gate_mode == 2) + (c.res_f32 ? 4 : 2);
-    const Shape s = norm_shape(c.T, c.d, p.slots, sms < 160 ? sms : 160, true);
+    const int slots = 2 + (p.gate_mode == 2) + (c.res_f32 ? 4 : 2);
+    const Shape s = norm_shape(c.T, c.d, slots, sms < 160 ? sms : 160, true);
     p.stages = s.stages;
-    const int rc = c.res_f32 ? launch_width<true>(p, s, true, st)
-                             : launch_width<false>(p, s, true, st);
-    if (rc != MOE_OK) return rc;
-    norm_sums_kernel<<<(3 * c.d + 31) / 32, 256, 0, st>>>(
-        p.part, s.grid, c.d, dw_post, dw_pre,
-        p.gate_mode == 1 ? static_cast<float*>(dgate) : nullptr);
+    if (const int rc = launch_any(p, s, c.res_f32, true, st)) return rc;
+    norm_sums_kernel<<<(2 * c.d + 31) / 32, 256, 0, st>>>(
+        p, s.grid, dw_post, dw_pre, p.gate_mode == 1 ? static_cast<float*>(dgate) : nullptr);
     if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
     trace_after(st, "norm_sums");
     return MOE_OK;

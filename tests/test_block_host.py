@@ -78,7 +78,7 @@ def test_norm_refuses_nothing_to_do_and_short_scratch():
     assert L.moe_norm_residual(norm(), None, P, None, None, None, P, None, None, None, None) == abi.MOE_EINVAL
     assert L.moe_norm_residual(norm(), P, P, None, P, None, None, None, None, None, None) == abi.MOE_EINVAL
     need = abi.norm_residual_workspace(4, 64)
-    assert need == 4 * 3 * 64 * 4
+    assert need == 4 * 2 * 64 * 4
     args = [P, P, P, P, None, P, P, P, P, P, P, None, P, P, P]
     assert L.moe_norm_residual_backward(norm(), *args, need - 1, None) == abi.MOE_ENOSPC
     for i in (2, 5, 7, 9, 10, 12, 13, 14):      # a tensor that belongs to the call is missing
