@@ -149,6 +149,17 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, status));
 }
 
+// One half of mma_tokens: tokens 64 half .. 64 half + 63.
+template <int D>
+__device__ __forceinline__ void mma_tokens_half(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_saddr,
+                                                int half, bool accumulate) {
+    constexpr uint32_t idesc = idesc_bf16_f32(128, D, false, true);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+        mma_bf16_ta(d_tmem, a_tmem + kk * 8, sdesc_mn128_sw128(b_saddr + (4 * half + kk) * 2048),
+                    idesc, accumulate || kk > 0);
+}
+
 // ------------------------------------------------------------------ arithmetic
 
 // 2^x (flushing denormal results): the hardware's own exponential.

@@ -1,9 +1,10 @@
 // attention_fwd.cu -- causal attention over packed sequences, forward, and
 // the plan of work lists that forward and backward share.
 //
-// One CTA holds two tiles of 128 query rows that read the same key/value
-// head of the same sequence (two query heads of a group, or two blocks of
-// rows when the group is odd) and walks the sequence's key blocks of 128:
+// One CTA an SM works through the batch, heaviest work first.  A piece of
+// work is two tiles of 128 query rows that read the same key/value head of
+// the same sequence (two query heads of a group, or two blocks of rows when
+// the group is odd), over the sequence's key blocks of 128:
 //   S = Q K^T (tcgen05, fp32 in TMEM); m, l = running maximum and sum;
 //   P = 2^(c S - c m) as bf16 back into S's columns; O += P V (A from TMEM).
 // Warps 0-3 and 4-7 run the softmax of the two tiles, a thread a row; warp 8
@@ -78,44 +79,49 @@ __device__ __noinline__ void fwd_row(const FwdParams& p, int64_t start, int row,
     }
 }
 
+// One piece of work: two tiles of query rows over one key/value head.
+struct FwdWork {
+    int64_t start;
+    int len, kvh, block;
+    int h[2], m0[2], n[2];   // query head, first row, key blocks (0: no tile)
+    __device__ FwdWork(const FwdParams& p, int item) {
+        const int tile = item / p.units, u = item - tile * p.units;
+        const int4 te = p.tiles[tile];
+        start = te.x;
+        len = te.y;
+        block = te.z;
+        if (p.pair_heads) {
+            const int half = p.group / 2;
+            kvh = u / half;
+            h[0] = kvh * p.group + 2 * (u - kvh * half);
+            h[1] = h[0] + 1;
+            m0[0] = m0[1] = block * 128;
+        } else {
+            h[0] = h[1] = u;
+            kvh = u / p.group;
+            m0[0] = block * 256;
+            m0[1] = m0[0] + 128;
+        }
+        n[0] = m0[0] / 128 + 1;
+        n[1] = m0[1] < len ? m0[1] / 128 + 1 : 0;
+    }
+};
+
+// The items of this CTA, heaviest first: dealt out to the CTAs in turn, every
+// other round from the other end, so that a CTA's early heavy item meets a
+// lighter one in the next round.  f(work) for each; false ends the walk.
+template <class F>
+__device__ __forceinline__ void each_item(const FwdParams& p, F f) {
+    const int total = p.header[p.list] * p.units, g = gridDim.x;
+    for (int r = 0; r * g < total; ++r) {
+        const int item = r * g + static_cast<int>((r & 1) ? g - 1 - blockIdx.x : blockIdx.x);
+        if (item < total && !f(FwdWork(p, item))) return;
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(384, 1) attn_fwd_kernel(const __grid_constant__ FwdParams p) {
     using C = FwdCfg<D>;
-    const int tile = blockIdx.x / p.units;
-    if (tile >= p.header[p.list]) return;
-    const int u = blockIdx.x - tile * p.units;
-    const int4 te = p.tiles[tile];
-    const int64_t start = te.x;
-    const int len = te.y;
-    int kvh, h[2], m0[2], n[2];
-    if (p.pair_heads) {
-        const int half = p.group / 2;
-        kvh = u / half;
-        h[0] = kvh * p.group + 2 * (u - kvh * half);
-        h[1] = h[0] + 1;
-        m0[0] = m0[1] = te.z * 128;
-    } else {
-        h[0] = h[1] = u;
-        kvh = u / p.group;
-        m0[0] = te.z * 256;
-        m0[1] = m0[0] + 128;
-    }
-    if (te.z < 0) {   // tokens of no sequence
-        for (int t = 0; t < (p.pair_heads ? 2 : 1); ++t) {
-            for (int i = threadIdx.x; i < len * (p.D / 8); i += blockDim.x) {
-                const int64_t o = (start + i / (p.D / 8)) * p.o_t + h[t] * p.o_h + i % (p.D / 8) * 8;
-                *reinterpret_cast<uint4*>(p.out + o) = make_uint4(0, 0, 0, 0);
-                if (p.rest) *reinterpret_cast<uint4*>(p.rest + o) = make_uint4(0, 0, 0, 0);
-            }
-            for (int i = threadIdx.x; i < len; i += blockDim.x)
-                p.lse[h[t] * p.T + start + i] = -INFINITY;
-        }
-        return;
-    }
-    n[0] = m0[0] / 128 + 1;
-    n[1] = m0[1] < len ? m0[1] / 128 + 1 : 0;
-    const int nmax = max(n[0], n[1]);
-
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* sQ = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -123,10 +129,12 @@ __global__ void __launch_bounds__(384, 1) attn_fwd_kernel(const __grid_constant_
     uint64_t* full = reinterpret_cast<uint64_t*>(sKV + C::STAGES * C::TILE);
     uint64_t* empty = full + C::STAGES;
     uint64_t* q_full = empty + C::STAGES;
-    uint64_t* s_full = q_full + 1;    // [2] scores of a tile ready
-    uint64_t* p_full = s_full + 2;    // [2] its P written
-    uint64_t* o_full = p_full + 2;    // [2] its product with V done
-    uint64_t* done = o_full + 2;
+    uint64_t* q_empty = q_full + 1;
+    uint64_t* s_full = q_empty + 1;   // [2] scores of a tile ready
+    uint64_t* p_full = s_full + 2;    // [2][2] a half of its P written
+    uint64_t* o_full = p_full + 4;    // [2] its product with V done
+    uint64_t* o_empty = o_full + 2;   // [2] its O read by the epilogue
+    uint64_t* done = o_empty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -138,10 +146,13 @@ __global__ void __launch_bounds__(384, 1) attn_fwd_kernel(const __grid_constant_
             mbar_init(&empty[s], 1);
         }
         mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
-            mbar_init(&p_full[t], 128);
+            mbar_init(&p_full[2 * t], 4);
+            mbar_init(&p_full[2 * t + 1], 4);
             mbar_init(&o_full[t], 1);
+            mbar_init(&o_empty[t], 4);
         }
         mbar_init(done, 1);
         *abort_flag = 0;
@@ -158,38 +169,46 @@ __global__ void __launch_bounds__(384, 1) attn_fwd_kernel(const __grid_constant_
     const uint32_t tmS = tm, tmO = tm + 256;   // tile t: + 128 t
 
     if (warp >= 8) {
-        setmaxnreg_dec<88>();
+        setmaxnreg_dec<56>();
         if (warp == 9 && lane == 0) {
             // -------------------------------------------------------- loads
-            const uint32_t dq = smem_u32(sQ);
-            mbar_arrive_expect_tx(q_full, (n[1] ? 2 : 1) * C::TILE);
-            for (int t = 0; t < (n[1] ? 2 : 1); ++t)
-                for (int b = 0; b < D / 64; ++b)
-                    tma_load_3d(dq + t * C::TILE + b * kBoxBytes, &p.mapQ, q_full, b * 64,
-                                static_cast<int>(start) + m0[t], h[t]);
-            uint32_t st = 0, ph = 0, armed = 0, par = 0;
+            tma_prefetch_map(&p.mapQ);
+            tma_prefetch_map(&p.mapK);
+            tma_prefetch_map(&p.mapV);
+            const uint32_t aq = smem_u32(sQ), akv = smem_u32(sKV);
+            uint32_t st = 0, ph = 0, armed = 0, par = 0, items = 0;
             bool ok = true;
-            for (int it = 0; ok && it < 2 * nmax; ++it) {
-                if (!mbar_wait(&empty[st], ph ^ 1u, abort_flag, p.status)) {
-                    ok = false;
-                    break;
+            each_item(p, [&](const FwdWork& w) {
+                if (w.block < 0) return true;
+                const int tiles = w.n[1] ? 2 : 1, blocks = max(w.n[0], w.n[1]);
+                const int tok = static_cast<int>(w.start);
+                if (items && !(ok = mbar_wait(q_empty, (items - 1) & 1u, abort_flag, p.status)))
+                    return false;
+                ++items;
+                mbar_arrive_expect_tx(q_full, tiles * C::TILE);
+                for (int t = 0; t < tiles; ++t)
+                    for (int b = 0; b < D / 64; ++b)
+                        tma_load_3d(aq + t * C::TILE + b * kBoxBytes, &p.mapQ, q_full, b * 64,
+                                    tok + w.m0[t], w.h[t]);
+                for (int it = 0; it < 2 * blocks; ++it) {
+                    if (!(ok = mbar_wait(&empty[st], ph ^ 1u, abort_flag, p.status))) return false;
+                    mbar_arrive_expect_tx(&full[st], C::TILE);
+                    armed |= 1u << st;
+                    par = (par & ~(1u << st)) | (ph << st);
+                    for (int b = 0; b < D / 64; ++b)
+                        tma_load_3d(akv + st * C::TILE + b * kBoxBytes,
+                                    (it & 1) ? &p.mapV : &p.mapK, &full[st], b * 64,
+                                    tok + (it >> 1) * 128, w.kvh);
+                    if (++st == C::STAGES) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
                 }
-                const CUtensorMap* map = (it & 1) ? &p.mapV : &p.mapK;
-                mbar_arrive_expect_tx(&full[st], C::TILE);
-                armed |= 1u << st;
-                par = (par & ~(1u << st)) | (ph << st);
-                const uint32_t dst = smem_u32(sKV) + st * C::TILE;
-                for (int b = 0; b < D / 64; ++b)
-                    tma_load_3d(dst + b * kBoxBytes, map, &full[st], b * 64,
-                                static_cast<int>(start) + (it >> 1) * 128, kvh);
-                if (++st == C::STAGES) {
-                    st = 0;
-                    ph ^= 1u;
-                }
-            }
+                return true;
+            });
             if (!ok || *abort_flag) {   // let the armed copies land before leaving
                 volatile int no_abort = 0;
-                mbar_wait(q_full, 0, &no_abort, nullptr, 20000000ull);
+                if (items) mbar_wait(q_full, (items - 1) & 1u, &no_abort, nullptr, 20000000ull);
                 for (int s = 0; s < C::STAGES; ++s)
                     if (armed & (1u << s))
                         mbar_wait(&full[s], (par >> s) & 1u, &no_abort, nullptr, 20000000ull);
@@ -197,58 +216,65 @@ __global__ void __launch_bounds__(384, 1) attn_fwd_kernel(const __grid_constant_
         } else if (warp == 8 && lane == 0) {
             // -------------------------------------------------------- MMAs
             const uint32_t aq = smem_u32(sQ), akv = smem_u32(sKV);
-            const auto stage = [](int it) { return static_cast<uint32_t>(it % C::STAGES); };
-            const auto phase = [](int it) { return static_cast<uint32_t>(it / C::STAGES) & 1u; };
-            bool ok = mbar_wait(q_full, 0, abort_flag, p.status) &&
-                      mbar_wait(&full[0], 0, abort_flag, p.status);
-            if (ok) {
+            uint32_t it = 0;                // tiles taken from the ring so far
+            uint32_t items = 0, ps[2] = {0, 0}, tiles[2] = {0, 0};
+            const auto wait = [&](uint64_t* bar, uint32_t parity) {
+                const bool got = mbar_wait(bar, parity, abort_flag, p.status);
                 tc_fence_after();
+                return got;
+            };
+            const auto ready = [&](uint32_t i) {
+                return wait(&full[i % C::STAGES], (i / C::STAGES) & 1u);
+            };
+            const auto at = [&](uint32_t i) { return akv + i % C::STAGES * C::TILE; };
+            each_item(p, [&](const FwdWork& w) {
+                if (w.block < 0) return true;
+                const int blocks = max(w.n[0], w.n[1]);
+                if (!wait(q_full, items++ & 1u) || !ready(it)) return false;
                 for (int t = 0; t < 2; ++t)
-                    if (n[t]) {
-                        mma_scores<D>(tmS + 128 * t, aq + t * C::TILE, akv);
+                    if (w.n[t]) {
+                        mma_scores<D>(tmS + 128 * t, aq + t * C::TILE, at(it));
                         mma_commit(&s_full[t]);
                     }
-                mma_commit(&empty[0]);
-            }
-            for (int j = 0; ok && j < nmax; ++j) {
-                const int iv = 2 * j + 1, ik = 2 * j + 2;
-                if (!mbar_wait(&full[stage(iv)], phase(iv), abort_flag, p.status)) break;
-                bool have_k = false;
-                for (int t = 0; ok && t < 2; ++t) {
-                    if (j >= n[t]) continue;
-                    if (!mbar_wait(&p_full[t], j & 1u, abort_flag, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    mma_tokens<D>(tmO + 128 * t, tmS + 128 * t, tmS + 128 * t + 32,
-                                  akv + stage(iv) * C::TILE, j > 0);
-                    mma_commit(&o_full[t]);
-                    if (j + 1 < n[t]) {
-                        if (!have_k) {
-                            if (!mbar_wait(&full[stage(ik)], phase(ik), abort_flag, p.status)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
+                mma_commit(&empty[it % C::STAGES]);
+                if (blocks == 1) mma_commit(q_empty);
+                for (int j = 0; j < blocks; ++j) {
+                    const uint32_t iv = it + 2 * j + 1, ik = iv + 1;
+                    if (!ready(iv)) return false;
+                    bool have_k = false;
+                    for (int t = 0; t < 2; ++t) {
+                        if (j >= w.n[t]) continue;
+                        const uint32_t dS = tmS + 128 * t, dO = tmO + 128 * t;
+                        // the last item's O has been read
+                        if (j == 0 && tiles[t]++ && !wait(&o_empty[t], (tiles[t] - 2) & 1u))
+                            return false;
+                        if (!wait(&p_full[2 * t], ps[t] & 1u)) return false;
+                        mma_tokens_half<D>(dO, dS, at(iv), 0, j > 0);
+                        if (!wait(&p_full[2 * t + 1], ps[t]++ & 1u)) return false;
+                        mma_tokens_half<D>(dO, dS + 32, at(iv), 1, true);
+                        mma_commit(&o_full[t]);
+                        if (j + 1 < w.n[t]) {
+                            if (!have_k && !ready(ik)) return false;
                             have_k = true;
+                            // runs after the product above has read P from these columns
+                            mma_scores<D>(dS, aq + t * C::TILE, at(ik));
+                            mma_commit(&s_full[t]);
                         }
-                        // runs after the product above has read P from these columns
-                        mma_scores<D>(tmS + 128 * t, aq + t * C::TILE, akv + stage(ik) * C::TILE);
-                        mma_commit(&s_full[t]);
                     }
+                    mma_commit(&empty[iv % C::STAGES]);
+                    if (have_k) mma_commit(&empty[ik % C::STAGES]);
+                    if (j == blocks - 2) mma_commit(q_empty);   // its last scores are issued
                 }
-                if (!ok) break;
-                mma_commit(&empty[stage(iv)]);
-                if (have_k) mma_commit(&empty[stage(ik)]);
-            }
+                it += 2 * blocks;
+                return true;
+            });
             // nothing of this CTA is in flight when it leaves
             mma_commit(done);
             volatile int no_abort = 0;
             mbar_wait(done, 0, &no_abort, p.status);
         }
     } else {
-        setmaxnreg_inc<208>();
+        setmaxnreg_inc<224>();
         // ------------------------------------------------------------ softmax
         const int t = warp >> 2;
         const int r = threadIdx.x & 127;
@@ -256,101 +282,119 @@ __global__ void __launch_bounds__(384, 1) attn_fwd_kernel(const __grid_constant_
         const uint32_t ts = tmS + 128 * t + lane_off, to = tmO + 128 * t + lane_off;
         const float c = p.scale_log2;
         const float slack = 8.0f / c;   // P may reach 2^8 before O is rescaled
-        // l: sum of P, for lse; lb: sum of P as rounded to bf16, which divides O:
-        // a row that is nearly one key's then gives that key's v, not v times
-        // its weight's rounding error, and D_i of the backward depends on it
-        float m = -INFINITY, l = 0.f, lb = 0.f;
-        bool ok = true;
-        for (int j = 0; j < n[t]; ++j) {
-            if (!warp_wait(&s_full[t], j & 1u, abort_flag, p.status)) {
-                ok = false;
-                break;
+        uint32_t blocks = 0;            // key blocks of this tile so far
+        each_item(p, [&](const FwdWork& w) {
+            const int h = t ? w.h[1] : w.h[0], n = t ? w.n[1] : w.n[0];
+            if (w.block < 0) {   // tokens of no sequence
+                if (t && !p.pair_heads) return true;
+                for (int i = r; i < w.len * (p.D / 8); i += 128) {
+                    const int64_t o = (w.start + i / (p.D / 8)) * p.o_t + h * p.o_h + i % (p.D / 8) * 8;
+                    *reinterpret_cast<uint4*>(p.out + o) = make_uint4(0, 0, 0, 0);
+                    if (p.rest) *reinterpret_cast<uint4*>(p.rest + o) = make_uint4(0, 0, 0, 0);
+                }
+                for (int i = r; i < w.len; i += 128) p.lse[h * p.T + w.start + i] = -INFINITY;
+                return true;
             }
-            tc_fence_after();
-            float s[128];
+            if (!n) return true;
+            // l: sum of P, for lse; lb: sum of P as rounded to bf16, which
+            // divides O: a row that is nearly one key's then gives that key's
+            // v, not v times its weight's rounding error, and D_i of the
+            // backward depends on it
+            float m = -INFINITY, l = 0.f, lb = 0.f;
+            for (int j = 0; j < n; ++j, ++blocks) {
+                if (!warp_wait(&s_full[t], blocks & 1u, abort_flag, p.status)) return false;
+                tc_fence_after();
+                float s[128];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                tmem_ld32_async(ts + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
-            tmem_wait_ld();
-            if (j == n[t] - 1) {   // the diagonal block: keys after the row are hidden
+                for (int i = 0; i < 4; ++i)
+                    tmem_ld32_async(ts + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
+                tmem_wait_ld();
+                if (j == n - 1) {   // the diagonal block: keys after the row are hidden
 #pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    if (i > r) s[i] = -INFINITY;
-            }
-            float mx[4] = {s[0], s[1], s[2], s[3]};
+                    for (int i = 0; i < 128; ++i)
+                        if (i > r) s[i] = -INFINITY;
+                }
+                float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int i = 4; i < 128; i += 4) {
-                mx[0] = fmaxf(mx[0], s[i]);
-                mx[1] = fmaxf(mx[1], s[i + 1]);
-                mx[2] = fmaxf(mx[2], s[i + 2]);
-                mx[3] = fmaxf(mx[3], s[i + 3]);
-            }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            if (j == 0) {
-                m = top;
-            } else {
-                // O keeps an older maximum until a row's rises by 2^8: sums in
-                // fp32 hold the larger terms, and rescaling is rare
-                const bool rise = top > m + slack;
-                if (__any_sync(0xFFFFFFFFu, rise)) {
-                    const float f = rise ? exp2_fast((m - top) * c) : 1.0f;
-                    if (rise) m = top;
-                    l *= f;
-                    lb *= f;
-                    if (!warp_wait(&o_full[t], (j - 1) & 1u, abort_flag, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                for (int i = 4; i < 124; i += 8)
 #pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        uint32_t o[32];
-                        tmem_ld32(to + 32 * i, o);
+                    for (int e = 0; e < 4; ++e)
+                        mx[e] = fmaxf(fmaxf(mx[e], s[i + e]), s[i + 4 + e]);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st32(to + 32 * i, o);
+                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[124 + e]);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if (j == 0) {
+                    m = top;
+                } else {
+                    // O keeps an older maximum until a row's rises by 2^8: sums
+                    // in fp32 hold the larger terms, and rescaling is rare
+                    const bool rise = top > m + slack;
+                    if (__any_sync(0xFFFFFFFFu, rise)) {
+                        const float f = rise ? exp2_fast((m - top) * c) : 1.0f;
+                        if (rise) m = top;
+                        l *= f;
+                        lb *= f;
+                        if (!warp_wait(&o_full[t], (blocks - 1) & 1u, abort_flag, p.status))
+                            return false;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int i = 0; i < D / 16; ++i) {
+                            uint32_t o[16];
+                            tmem_ld16(to + 16 * i, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16(to + 16 * i, o);
+                        }
                     }
                 }
-            }
-            const float2 c2 = make_float2(c, c), neg = make_float2(-m * c, -m * c);
-            float2 sum = make_float2(0.f, 0.f), sumb = make_float2(0.f, 0.f);
+                const float2 c2 = make_float2(c, c), neg = make_float2(-m * c, -m * c);
+                uint32_t pk[64];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t pk[16];
+                for (int i = 0; i < 4; ++i) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float2 x = fma2(make_float2(s[32 * i + 2 * e], s[32 * i + 2 * e + 1]), c2, neg);
-                    x.x = exp2_fast(x.x);
-                    x.y = exp2_fast(x.y);
-                    sum = add2(sum, x);
-                    pk[e] = pack_bf16x2(x.x, x.y);
-                    sumb = add2(sumb, make_float2(bf16_lo(pk[e]), bf16_hi(pk[e])));
+                    for (int e = 16 * i; e < 16 * i + 16; ++e) {
+                        const float2 x = fma2(make_float2(s[2 * e], s[2 * e + 1]), c2, neg);
+                        s[2 * e] = exp2_fast(x.x);
+                        s[2 * e + 1] = exp2_fast(x.y);
+                        pk[e] = pack_bf16x2(s[2 * e], s[2 * e + 1]);
+                    }
+                    tmem_st16(ts + 16 * i, pk + 16 * i);
+                    if (i & 1) {   // the product with V starts on this half
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&p_full[2 * t + (i >> 1)]);
+                    }
                 }
-                tmem_st16(ts + 16 * i, pk);
+                // the sums, while the products run
+                float2 sum = make_float2(0.f, 0.f), sumb = sum;
+#pragma unroll
+                for (int e = 0; e < 64; ++e) {
+                    sum = add2(sum, make_float2(s[2 * e], s[2 * e + 1]));
+                    sumb = add2(sumb, bf16x2_f32(pk[e]));
+                }
+                l += sum.x + sum.y;
+                lb += sumb.x + sumb.y;
             }
-            l += sum.x + sum.y;
-            lb += sumb.x + sumb.y;
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&p_full[t]);
-        }
-        // ------------------------------------------------------------ output
-        if (ok && n[t]) {
-            ok = warp_wait(&o_full[t], (n[t] - 1) & 1u, abort_flag, p.status);
+            // ------------------------------------------------------------ output
+            if (!warp_wait(&o_full[t], (blocks - 1) & 1u, abort_flag, p.status)) return false;
             tc_fence_after();
-        }
-        if (ok && n[t]) {
-            const int row = m0[t] + r;
-            const bool valid = row < len;
+            const int row = (t ? w.m0[1] : w.m0[0]) + r;
+            const bool valid = row < w.len;
             const float inv = 1.0f / lb;
             const float lse = m * p.scale + logf(l);
-            const int64_t o = (start + row) * p.o_t + h[t] * p.o_h;
+            const int64_t o = (w.start + row) * p.o_t + h * p.o_h;
             bool bad = false;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 uint32_t a[32];
                 tmem_ld32(to + 32 * i, a);
+                if (i == D / 32 - 1) {   // O may be overwritten from here on
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&o_empty[t]);
+                }
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const int col = 32 * i + 8 * g;
@@ -372,15 +416,16 @@ __global__ void __launch_bounds__(384, 1) attn_fwd_kernel(const __grid_constant_
                     }
                 }
             }
-            if (valid) p.lse[h[t] * p.T + start + row] = lse;
+            if (valid) p.lse[h * p.T + w.start + row] = lse;
             uint32_t again = __ballot_sync(0xFFFFFFFFu, bad && valid);
             while (again) {
                 const int src = __ffs(again) - 1;
                 again &= again - 1;
-                fwd_row(p, start, __shfl_sync(0xFFFFFFFFu, row, src), h[t], kvh,
+                fwd_row(p, w.start, __shfl_sync(0xFFFFFFFFu, row, src), h, w.kvh,
                         __shfl_sync(0xFFFFFFFFu, lse, src));
             }
-        }
+            return true;
+        });
     }
     tc_fence_before();
     __syncthreads();
@@ -561,17 +606,21 @@ int launch_attention_fwd(const moe_attention_t& a, const void* plan, const uint1
     p.scale = a.scale;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.status = status;
-    const int64_t grid = (p.pair_heads ? l.max128 : l.max256) * p.units;
-    if (grid >= (1ll << 31)) return MOE_EINVAL;
+    // one CTA an SM, or fewer where the batch has less work than that
+    const int64_t most = (p.pair_heads ? l.max128 : l.max256) * p.units;
+    if (most >= (1ll << 31) - 1024) return MOE_EINVAL;
+    int dev = 0, sms = 0;
+    if (const int rc = current_device(&dev, &sms)) return rc;
+    const int grid = static_cast<int>(most < sms ? most : sms);
     if (D <= 64) {
         if (ensure_smem_attr(reinterpret_cast<const void*>(attn_fwd_kernel<64>), FwdCfg<64>::SMEM))
             return MOE_ECUDA;
-        attn_fwd_kernel<64><<<static_cast<int>(grid), 384, FwdCfg<64>::SMEM, st>>>(p);
+        attn_fwd_kernel<64><<<grid, 384, FwdCfg<64>::SMEM, st>>>(p);
     } else {
         if (ensure_smem_attr(reinterpret_cast<const void*>(attn_fwd_kernel<128>),
                              FwdCfg<128>::SMEM))
             return MOE_ECUDA;
-        attn_fwd_kernel<128><<<static_cast<int>(grid), 384, FwdCfg<128>::SMEM, st>>>(p);
+        attn_fwd_kernel<128><<<grid, 384, FwdCfg<128>::SMEM, st>>>(p);
     }
     if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
     trace_after(st, "attn_fwd");

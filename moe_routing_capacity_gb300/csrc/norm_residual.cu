@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(NT, OCC) norm_fwd_kernel(const NormParams p) {
 // Two sums over the tokens: dw_pre = sum dn q, and S = sum p du (TOKEN: sum
 // g p du), from which dw_post = beta g S and dgate = beta w_post S follow a
 // channel at the end, for a gate that all tokens share.
-template <bool F32, bool TOKEN, bool WARP, int NT, int OCC>
+template <bool F32, bool TOKEN, bool WARP, int CH, int NT, int OCC>
 __global__ void __launch_bounds__(NT, OCC) norm_bwd_kernel(const NormParams p) {
     extern __shared__ uint4 ring[];
     __shared__ float red[4][32];
@@ -236,102 +236,124 @@ __global__ void __launch_bounds__(NT, OCC) norm_bwd_kernel(const NormParams p) {
     const int rows = WARP ? nt / 32 : 1;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows + (WARP ? threadIdx.x >> 5 : 0);
     const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
-    const int col = lane * 8;               // this thread's channels
-    const bool in = lane < p.chunks;
     const bool has_b = p.b != nullptr, has_n = p.dn != nullptr, has_y = p.dy != nullptr;
-    const auto slot = [&](int stage, int k) {
-        return (stage * SLOTS + k) * nt + static_cast<int>(threadIdx.x);
+    // this thread's chunks are lane + nt i
+    const auto in = [&](int i) { return lane + nt * i < p.chunks; };
+    const auto slot = [&](int stage, int i, int k) {
+        return ((stage * CH + i) * SLOTS + k) * nt + static_cast<int>(threadIdx.x);
     };
     const auto fetch = [&](int64_t row, int stage) {
-        if (in && row < p.T) {
-            const int64_t at = row * p.d + col;
-            if (has_b) cp_async_16(smem_u32(ring + slot(stage, 0)), p.b + at, 16);
-            if (has_n) {
-                cp_async_16(smem_u32(ring + slot(stage, s_dn)), p.dn + at, 16);
-                copy_res<F32>(smem_u32(ring + slot(stage, s_r)), nt * 16, p.r, at);
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+            if (row < p.T && in(i)) {
+                const int64_t at = row * p.d + (lane + nt * i) * 8;
+                if (has_b) cp_async_16(smem_u32(ring + slot(stage, i, 0)), p.b + at, 16);
+                if (has_n) {
+                    cp_async_16(smem_u32(ring + slot(stage, i, s_dn)), p.dn + at, 16);
+                    copy_res<F32>(smem_u32(ring + slot(stage, i, s_r)), nt * 16, p.r, at);
+                }
+                if (TOKEN)
+                    cp_async_16(smem_u32(ring + slot(stage, i, s_gate)), p.gate + at, 16);
+                if (has_y)
+                    copy_res<F32>(smem_u32(ring + slot(stage, i, s_dy)), nt * 16, p.dy, at);
             }
-            if (TOKEN) cp_async_16(smem_u32(ring + slot(stage, s_gate)), p.gate + at, 16);
-            if (has_y) copy_res<F32>(smem_u32(ring + slot(stage, s_dy)), nt * 16, p.dy, at);
-        }
         cp_async_commit();
     };
+    // slots that no copy fills (absent tensors, channels past d) read as zero
+    for (int s = 0; s < p.stages * CH * SLOTS; ++s) ring[slot(0, 0, s)] = make_uint4(0, 0, 0, 0);
     for (int s = 0; s < p.stages; ++s) fetch(row0 + s * step, s);
 
-    float2 G[4], S[4], a_pre[4];
-    load_factor(p, !TOKEN, lane, G);
-    uint4 wp = make_uint4(0, 0, 0, 0);
-    if (in && has_n) wp = *reinterpret_cast<const uint4*>(p.w_pre + col);
+    float2 G[CH][4], S[CH][4], a_pre[CH][4];
+    uint4 wp[CH];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) S[e] = a_pre[e] = both(0.f);
-    const auto stat = [&](const float* s, int64_t row) { return s && row < p.T ? s[row] : 0.f; };
+    for (int i = 0; i < CH; ++i) {
+        load_factor(p, !TOKEN, lane + nt * i, G[i]);
+        wp[i] = make_uint4(0, 0, 0, 0);
+        if (in(i) && has_n)
+            wp[i] = *reinterpret_cast<const uint4*>(p.w_pre + (lane + nt * i) * 8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[i][e] = a_pre[i][e] = both(0.f);
+    }
+    // a row ahead of its use; volatile, or the load sinks to the use and every
+    // row waits for it
+    const auto stat = [&](const float* s, int64_t row) {
+        float v = 0.f;
+        if (s && row < p.T) asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(s + row));
+        return v;
+    };
     float rb = stat(p.in_post, row0), ry = stat(p.in_pre, row0);
     int stage = 0, par = 0;
     for (int64_t row = row0; row < p.T; row += step) {
         const float rb_next = stat(p.in_post, row + step), ry_next = stat(p.in_pre, row + step);
         wait_stage(p.stages);
         // pv: p; du: first dy, then dL/dy, then dL/dp; gt: the token's gate
-        float2 pv[4], q[4], t[4], du[4], s1 = both(0.f);
-        float2 g[4], w[4];
-        uint4 dn = make_uint4(0, 0, 0, 0), gt = dn;
+        float2 pv[CH][4], q[CH][4], t[CH][4], du[CH][4], s1 = both(0.f);
+        uint4 gt[CH];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) pv[e] = q[e] = du[e] = both(0.f);
-        if (in) {
-            if (has_b) unpack8(ring[slot(stage, 0)], pv);
-            if (TOKEN) gt = ring[slot(stage, s_gate)];
-            if (has_n) {
-                dn = ring[slot(stage, s_dn)];
-                load_res<F32>(ring + slot(stage, s_r), nt, q);
+        for (int i = 0; i < CH; ++i) {
+            float2 g[4], w[4];
+            unpack8(ring[slot(stage, i, 0)], pv[i]);
+            unpack8(ring[slot(stage, i, s_dn)], t[i]);
+            load_res<F32>(ring + slot(stage, i, s_r), nt, q[i]);
+            load_res<F32>(ring + slot(stage, i, s_dy), nt, du[i]);
+            if (TOKEN) {
+                gt[i] = ring[slot(stage, i, s_gate)];
+                unpack8(gt[i], g);
             }
-            if (has_y) load_res<F32>(ring + slot(stage, s_dy), nt, du);
-        }
-        if (TOKEN) unpack8(gt, g);
-        unpack8(wp, w);
-        unpack8(dn, t);
+            unpack8(wp[i], w);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            pv[e] = mul2(pv[e], both(rb));
-            float2 m = mul2(pv[e], G[e]);
-            if (TOKEN) m = mul2(m, g[e]);
-            q[e] = mul2(fma2(q[e], both(p.alpha), m), both(ry));
-            a_pre[e] = fma2(t[e], q[e], a_pre[e]);
-            t[e] = mul2(t[e], w[e]);
-            s1 = fma2(t[e], q[e], s1);
+            for (int e = 0; e < 4; ++e) {
+                pv[i][e] = mul2(pv[i][e], both(rb));
+                float2 m = mul2(pv[i][e], G[i][e]);
+                if (TOKEN) m = mul2(m, g[e]);
+                q[i][e] = mul2(fma2(q[i][e], both(p.alpha), m), both(ry));
+                a_pre[i][e] = fma2(t[i][e], q[i][e], a_pre[i][e]);
+                t[i][e] = mul2(t[i][e], w[e]);
+                s1 = fma2(t[i][e], q[i][e], s1);
+            }
         }
         fetch(row + p.stages * step, stage);   // this thread has read the slots
         if (++stage == p.stages) stage = 0;
         const float k1 = has_n ? row_sum<WARP>(s1.x + s1.y, red[par]) * p.inv_d : 0.f;
         float2 s2 = both(0.f);
-        float2 o[4];
-        const int64_t at = row * p.d + col;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            du[e] = fma2(both(ry), fma2(q[e], both(-k1), t[e]), du[e]);
-            o[e] = mul2(du[e], both(p.alpha));
-        }
-        if (in) store_res<F32>(p.dr, at, o);
-        if (TOKEN) unpack8(gt, g);
+        for (int i = 0; i < CH; ++i) {
+            float2 o[4], g[4];
+            const int64_t at = row * p.d + (lane + nt * i) * 8;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 pd = mul2(pv[e], du[e]);
-            du[e] = mul2(du[e], G[e]);
-            if (TOKEN) {
-                o[e] = mul2(pd, G[e]);
-                S[e] = fma2(pd, g[e], S[e]);
-                du[e] = mul2(du[e], g[e]);
-            } else {
-                S[e] = add2(S[e], pd);
+            for (int e = 0; e < 4; ++e) {
+                du[i][e] = fma2(both(ry), fma2(q[i][e], both(-k1), t[i][e]), du[i][e]);
+                o[e] = mul2(du[i][e], both(p.alpha));
             }
-            s2 = fma2(du[e], pv[e], s2);
+            if (in(i)) store_res<F32>(p.dr, at, o);
+            if (TOKEN) unpack8(gt[i], g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 pd = mul2(pv[i][e], du[i][e]);
+                du[i][e] = mul2(du[i][e], G[i][e]);
+                if (TOKEN) {
+                    o[e] = mul2(pd, G[i][e]);
+                    S[i][e] = fma2(pd, g[e], S[i][e]);
+                    du[i][e] = mul2(du[i][e], g[e]);
+                } else {
+                    S[i][e] = add2(S[i][e], pd);
+                }
+                s2 = fma2(du[i][e], pv[i][e], s2);
+            }
+            if (TOKEN && in(i))
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dgate) + at) = pack8(o);
         }
-        if (TOKEN && in)
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dgate) + at) = pack8(o);
         if (has_b) {
             const float k2 = row_sum<WARP>(s2.x + s2.y, red[2 + par]) * p.inv_d;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                o[e] = mul2(both(rb), fma2(pv[e], both(-k2), du[e]));
-            if (in)
-                *reinterpret_cast<uint4*>(p.db + row * p.d + col) = pack8(o);
+            for (int i = 0; i < CH; ++i) {
+                float2 o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[e] = mul2(both(rb), fma2(pv[i][e], both(-k2), du[i][e]));
+                if (in(i))
+                    *reinterpret_cast<uint4*>(p.db + row * p.d + (lane + nt * i) * 8) = pack8(o);
+            }
         }
         par ^= 1;
         rb = rb_next;
@@ -348,19 +370,24 @@ __global__ void __launch_bounds__(NT, OCC) norm_bwd_kernel(const NormParams p) {
     for (int w = 0; w < turns; ++w) {
         if (!WARP || static_cast<int>(threadIdx.x >> 5) == w) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float2* v = k ? a_pre : S;
-                float4* to = reinterpret_cast<float4*>((w + 1 < turns ? acc : part) + k * p.d + col);
-                const float4* was = reinterpret_cast<const float4*>(acc + k * p.d + col);
+            for (int i = 0; i < CH; ++i) {
+                if (!in(i)) continue;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (!in) break;
-                    float4 x = make_float4(v[2 * e].x, v[2 * e].y, v[2 * e + 1].x, v[2 * e + 1].y);
-                    if (w) {
-                        const float4 y = was[e];
-                        x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                for (int k = 0; k < 2; ++k) {
+                    const float2(&v)[4] = k ? a_pre[i] : S[i];
+                    const int at = k * p.d + (lane + nt * i) * 8;
+                    float4* to = reinterpret_cast<float4*>((w + 1 < turns ? acc : part) + at);
+                    const float4* was = reinterpret_cast<const float4*>(acc + at);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float4 x = make_float4(v[2 * e].x, v[2 * e].y, v[2 * e + 1].x,
+                                               v[2 * e + 1].y);
+                        if (w) {
+                            const float4 y = was[e];
+                            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                        }
+                        to[e] = x;
                     }
-                    to[e] = x;
                 }
             }
         }
@@ -398,21 +425,19 @@ __global__ void __launch_bounds__(256) norm_sums_kernel(const NormParams p, int 
     }
 }
 
-// The launch shape for a width: threads and rows of a CTA, CTAs an SM (as
-// many as the kernels' registers allow; 80 a thread backward).
+// The launch shape for a width: threads and rows of a CTA, chunks of a
+// thread, CTAs an SM (as many as the kernels' registers allow).
 struct Shape {
-    int threads, rows, occ, grid, stages, smem;
+    int threads, rows, per_thread, occ, grid, stages, smem;
 };
 
-constexpr int ctas_per_sm(int threads, bool bwd) {
-    return threads <= 64    ? (bwd ? 12 : 16)
-           : threads <= 128 ? (bwd ? 6 : 8)
-           : threads <= 256 ? (bwd ? 3 : 4)
-           : threads <= 512 ? (bwd ? 1 : 2)
-                            : 1;
+constexpr int fwd_occ(int threads) {
+    return threads <= 64 ? 16 : threads <= 128 ? 8 : threads <= 256 ? 4 : threads <= 512 ? 2 : 1;
 }
-
-constexpr int kWarpRowsBackward = 2;   // rows of a warp: a few more registers
+// backward: 16 channels a thread past 512 channels, up to 168 registers
+constexpr int bwd_occ(int threads) {
+    return threads <= 64 ? 8 : threads <= 128 ? 3 : threads <= 256 ? 2 : 1;
+}
 
 // ring budget of an SM; a CTA's share keeps room for its 512 bytes of sums
 constexpr int kRingBytes = 212 * 1024;
@@ -421,9 +446,11 @@ Shape norm_shape(int64_t T, int d, int slots, int sms, bool bwd) {
     Shape s;
     const int chunks = d / 8;
     s.rows = chunks <= 32 ? 8 : 1;
-    s.threads = chunks <= 32 ? 256 : (chunks + 31) / 32 * 32;
-    s.occ = s.rows > 1 && bwd ? kWarpRowsBackward : ctas_per_sm(s.threads, bwd);
-    const int stage_bytes = s.threads * slots * 16;
+    s.per_thread = bwd && chunks > 64 ? 2 : 1;
+    s.threads = chunks <= 32 ? 256 : (chunks / s.per_thread + 31) / 32 * 32;
+    s.occ = bwd ? bwd_occ(s.threads) : fwd_occ(s.threads);
+    const int stage_bytes = s.threads * s.per_thread * slots * 16;
+    while (s.occ > 1 && kRingBytes / s.occ / stage_bytes < 2) --s.occ;
     s.stages = kRingBytes / s.occ / stage_bytes;
     s.stages = s.stages > 4 ? 4 : s.stages < 2 ? 2 : s.stages;
     s.smem = s.stages * stage_bytes;
@@ -432,32 +459,45 @@ Shape norm_shape(int64_t T, int d, int slots, int sms, bool bwd) {
     return s;
 }
 
-template <bool F32, bool TOKEN, bool WARP, int NT>
-int launch_norm(const NormParams& p, const Shape& s, bool bwd, cudaStream_t st) {
-    const auto f = norm_fwd_kernel<F32, TOKEN, WARP, NT, ctas_per_sm(NT, false)>;
-    const auto b = norm_bwd_kernel<F32, TOKEN, WARP, NT,
-                                   WARP ? kWarpRowsBackward : ctas_per_sm(NT, true)>;
-    if (ensure_smem_attr(bwd ? reinterpret_cast<const void*>(b) : reinterpret_cast<const void*>(f),
-                         s.smem))
-        return MOE_ECUDA;
-    if (bwd)
-        b<<<s.grid, s.threads, s.smem, st>>>(p);
-    else
-        f<<<s.grid, s.threads, s.smem, st>>>(p);
+template <class K>
+int launch_kernel(K kern, const NormParams& p, const Shape& s, const char* name, cudaStream_t st) {
+    if (ensure_smem_attr(reinterpret_cast<const void*>(kern), s.smem)) return MOE_ECUDA;
+    kern<<<s.grid, s.threads, s.smem, st>>>(p);
     if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
-    trace_after(st, bwd ? "norm_residual_bwd" : "norm_residual");
+    trace_after(st, name);
     return MOE_OK;
+}
+
+template <bool F32, bool TOKEN, bool WARP, int NT>
+int launch_fwd(const NormParams& p, const Shape& s, cudaStream_t st) {
+    return launch_kernel(norm_fwd_kernel<F32, TOKEN, WARP, NT, fwd_occ(NT)>, p, s,
+                         "norm_residual", st);
+}
+
+template <bool F32, bool TOKEN, bool WARP, int CH, int NT>
+int launch_bwd(const NormParams& p, const Shape& s, cudaStream_t st) {
+    return launch_kernel(norm_bwd_kernel<F32, TOKEN, WARP, CH, NT, bwd_occ(NT)>, p, s,
+                         "norm_residual_bwd", st);
 }
 
 template <bool F32, bool TOKEN>
 int launch_width(const NormParams& p, const Shape& s, bool bwd, cudaStream_t st) {
-    if (s.rows > 1) return launch_norm<F32, TOKEN, true, 256>(p, s, bwd, st);
-    if (s.threads <= 64) return launch_norm<F32, TOKEN, false, 64>(p, s, bwd, st);
-    if (s.threads <= 128) return launch_norm<F32, TOKEN, false, 128>(p, s, bwd, st);
-    if (s.threads <= 256) return launch_norm<F32, TOKEN, false, 256>(p, s, bwd, st);
-    if (s.threads <= 512) return launch_norm<F32, TOKEN, false, 512>(p, s, bwd, st);
-    if (s.threads <= 768) return launch_norm<F32, TOKEN, false, 768>(p, s, bwd, st);
-    return launch_norm<F32, TOKEN, false, 1024>(p, s, bwd, st);
+    if (bwd) {
+        if (s.rows > 1) return launch_bwd<F32, TOKEN, true, 1, 256>(p, s, st);
+        if (s.per_thread == 1) return launch_bwd<F32, TOKEN, false, 1, 64>(p, s, st);
+        if (s.threads <= 64) return launch_bwd<F32, TOKEN, false, 2, 64>(p, s, st);
+        if (s.threads <= 128) return launch_bwd<F32, TOKEN, false, 2, 128>(p, s, st);
+        if (s.threads <= 256) return launch_bwd<F32, TOKEN, false, 2, 256>(p, s, st);
+        if (s.threads <= 384) return launch_bwd<F32, TOKEN, false, 2, 384>(p, s, st);
+        return launch_bwd<F32, TOKEN, false, 2, 512>(p, s, st);
+    }
+    if (s.rows > 1) return launch_fwd<F32, TOKEN, true, 256>(p, s, st);
+    if (s.threads <= 64) return launch_fwd<F32, TOKEN, false, 64>(p, s, st);
+    if (s.threads <= 128) return launch_fwd<F32, TOKEN, false, 128>(p, s, st);
+    if (s.threads <= 256) return launch_fwd<F32, TOKEN, false, 256>(p, s, st);
+    if (s.threads <= 512) return launch_fwd<F32, TOKEN, false, 512>(p, s, st);
+    if (s.threads <= 768) return launch_fwd<F32, TOKEN, false, 768>(p, s, st);
+    return launch_fwd<F32, TOKEN, false, 1024>(p, s, st);
 }
 
 int launch_any(const NormParams& p, const Shape& s, bool f32, bool bwd, cudaStream_t st) {
@@ -506,7 +546,7 @@ int launch_norm_residual(const moe_norm_t& c, const uint16_t* b, const void* r,
 }
 
 // Partial rows: the most CTAs of a launch, on a device of 160 SMs at most.
-constexpr int64_t kMaxPartRows = ctas_per_sm(64, true) * 160;
+constexpr int64_t kMaxPartRows = bwd_occ(64) * 160;
 
 int64_t norm_backward_ws(int64_t T, int d) {
     return (T < kMaxPartRows ? T : kMaxPartRows) * 2 * d * 4;
