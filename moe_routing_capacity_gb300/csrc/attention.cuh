@@ -85,61 +85,94 @@ __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]: A's 128 rows are the TMEM lanes, each
-// 32-bit column holds two consecutive K values (the lower half the first).
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                            uint32_t idesc, uint32_t accumulate) {
+// The MMA warp runs converged (its waits answer for the whole warp) so that
+// addresses and descriptors live in uniform registers; one elected lane
+// issues.  Issued from inside `if (lane == 0)`, every MMA first moved its
+// operands to uniform registers, about 90 cycles each against the 64 that
+// a 128 x 128 x 16 product runs.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t e;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e;
+}
+
+// D[tmem] (+)= A[smem] B[smem]^T, by the elected lane.
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d_tmem, uint64_t adesc,
+                                       uint64_t bdesc, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(leader)
         : "memory");
 }
 
-// Descriptor of an MN-major operand stored as boxes of 128 K-rows of 64
-// contiguous M/N elements with the 128-byte swizzle: 8-row atoms of 1024 B
-// along K, the next 64 M/N elements 16 KB on.
-__device__ __forceinline__ uint64_t sdesc_mn128_sw128(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(16384 >> 4) << 16;
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
+// D[tmem] (+)= A[tmem] B[smem]: A's 128 rows are the TMEM lanes, each 32-bit
+// column holds two consecutive K values (the lower half the first).
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem,
+                                       uint64_t bdesc, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(leader)
+        : "memory");
+}
+
+// Arrive once on `bar` when every MMA the elected lane has issued is done.
+__device__ __forceinline__ void commit(uint32_t leader, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"(leader)
+        : "memory");
 }
 
 // A tile of 128 tokens x D channels in shared memory is D / 64 boxes of 128
-// rows of 64 channels (16 KB each, 128-byte swizzle).  The same bytes serve
-// as a K-major operand (M/N = tokens, K = channels) and as an MN-major one
-// (M/N = channels, K = tokens).
+// rows of 64 channels (16 KB each, 128-byte swizzle, 8-row atoms of 1 KB).
+// The same bytes serve as a K-major operand (M/N = tokens, K = channels) and
+// as an MN-major one (M/N = channels, 64 of them a box; K = tokens).  The
+// descriptors below are those of the tile's start; a step of 16 along K adds
+// 32 bytes (within a box) or 2 KB.
 constexpr uint32_t kBoxBytes = 16384;
+constexpr uint64_t kDescBase = (static_cast<uint64_t>(1024 >> 4) << 32) |
+                               (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
+    return kDescBase | (static_cast<uint64_t>(1) << 16) | (saddr >> 4);
+}
+
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
+    return kDescBase | (static_cast<uint64_t>(kBoxBytes >> 4) << 16) | (saddr >> 4);
+}
 
 // scores[tmem] = A B^T over D channels, both tiles K-major.
 template <int D>
-__device__ __forceinline__ void mma_scores(uint32_t d_tmem, uint32_t a_saddr, uint32_t b_saddr) {
+__device__ __forceinline__ void mma_scores(uint32_t leader, uint32_t d_tmem, uint64_t a,
+                                           uint64_t b) {
     constexpr uint32_t idesc = idesc_bf16_f32(128, 128);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk / 4) * kBoxBytes + (kk % 4) * 32;
-        mma_bf16(d_tmem, sdesc_k_sw128(a_saddr + off), sdesc_k_sw128(b_saddr + off), idesc,
-                 kk > 0);
+        const uint32_t off = ((kk / 4) * kBoxBytes + (kk % 4) * 32) >> 4;
+        mma_ss(leader, d_tmem, a + off, b + off, idesc, kk > 0);
     }
 }
 
-// acc[tmem] (+)= A B over 128 tokens: A bf16 in TMEM in two halves of 64
-// tokens (32 columns each, a1 - a0 apart), B a tile read MN-major.
+// acc[tmem] (+)= A B over tokens 64 half .. 64 half + 63: A bf16 in 32
+// columns of TMEM, B a tile read MN-major.
 template <int D>
-__device__ __forceinline__ void mma_tokens(uint32_t d_tmem, uint32_t a0, uint32_t a1,
-                                           uint32_t b_saddr, bool accumulate) {
+__device__ __forceinline__ void mma_tokens(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem,
+                                           uint64_t b, int half, bool accumulate) {
     constexpr uint32_t idesc = idesc_bf16_f32(128, D, false, true);
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk) {
-        const uint32_t a = (kk < 4 ? a0 : a1) + (kk % 4) * 8;
-        mma_bf16_ta(d_tmem, a, sdesc_mn128_sw128(b_saddr + kk * 2048), idesc,
-                    accumulate || kk > 0);
-    }
+    for (int kk = 0; kk < 4; ++kk)
+        mma_ts(leader, d_tmem, a_tmem + kk * 8, b + (((4 * half + kk) * 2048) >> 4), idesc,
+               accumulate || kk > 0);
 }
 
 // mbar_wait by a whole warp with one answer for all its lanes: the warp-wide
@@ -147,17 +180,6 @@ __device__ __forceinline__ void mma_tokens(uint32_t d_tmem, uint32_t a0, uint32_
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                           int32_t* status) {
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, status));
-}
-
-// One half of mma_tokens: tokens 64 half .. 64 half + 63.
-template <int D>
-__device__ __forceinline__ void mma_tokens_half(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_saddr,
-                                                int half, bool accumulate) {
-    constexpr uint32_t idesc = idesc_bf16_f32(128, D, false, true);
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-        mma_bf16_ta(d_tmem, a_tmem + kk * 8, sdesc_mn128_sw128(b_saddr + (4 * half + kk) * 2048),
-                    idesc, accumulate || kk > 0);
 }
 
 // ------------------------------------------------------------------ arithmetic

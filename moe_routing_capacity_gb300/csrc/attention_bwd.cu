@@ -331,48 +331,53 @@ __global__ void __launch_bounds__(384, 1) attn_dkv_kernel(const __grid_constant_
                     if (armed & (1u << s))
                         mbar_wait(&sm.full[s], (par >> s) & 1u, &no_abort, nullptr, 20000000ull);
             }
-        } else if (warp == 8 && lane == 0) {
+        } else if (warp == 8) {
             // -------------------------------------------------------- MMAs
-            const uint32_t aK = smem_u32(sm.res), aV = aK + C::TILE, ag = smem_u32(sm.ring);
+            const uint32_t one = elect_lane();
+            const uint32_t aK = smem_u32(sm.res), ag = smem_u32(sm.ring);
+            const uint64_t dK = desc_k(aK), dV = desc_k(aK + C::TILE);
             const auto stage = [](int it) { return static_cast<uint32_t>(it % C::STAGES); };
             const auto phase = [](int it) { return static_cast<uint32_t>(it / C::STAGES) & 1u; };
+            const auto at = [&](int it) { return ag + stage(it) * C::TILE; };
             const auto wait = [&](uint64_t* bar, uint32_t parity) {
-                const bool got = mbar_wait(bar, parity, sm.abort_flag, p.status);
+                const bool got = warp_wait(bar, parity, sm.abort_flag, p.status);
                 tc_fence_after();
                 return got;
             };
             bool ok = wait(sm.res_full, 0) && wait(&sm.full[0], 0);
             if (ok) {
-                mma_scores<D>(tmS, aK, ag);
-                mma_commit(sm.s_full);
+                mma_scores<D>(one, tmS, dK, desc_k(at(0)));
+                commit(one, sm.s_full);
                 ok = wait(&sm.full[1], 0);
             }
             if (ok) {
-                mma_scores<D>(tmP, aV, ag + C::TILE);
-                mma_commit(sm.dp_full);
+                mma_scores<D>(one, tmP, dV, desc_k(at(1)));
+                commit(one, sm.dp_full);
             }
             for (int it = 0; ok && it < n; ++it) {
                 const int iq = 2 * it, io = iq + 1;
                 if (!(ok = wait(sm.p_full, it & 1u))) break;
-                mma_tokens<D>(tmV, tmS, tmS + 64, ag + stage(io) * C::TILE, it > 0);
-                mma_commit(&sm.empty[stage(io)]);
+                mma_tokens<D>(one, tmV, tmS, desc_mn(at(io)), 0, it > 0);
+                mma_tokens<D>(one, tmV, tmS + 64, desc_mn(at(io)), 1, true);
+                commit(one, &sm.empty[stage(io)]);
                 if (it + 1 < n) {
                     if (!(ok = wait(&sm.full[stage(iq + 2)], phase(iq + 2)))) break;
                     // runs after the product above has read P from these columns
-                    mma_scores<D>(tmS, aK, ag + stage(iq + 2) * C::TILE);
-                    mma_commit(sm.s_full);
+                    mma_scores<D>(one, tmS, dK, desc_k(at(iq + 2)));
+                    commit(one, sm.s_full);
                 }
                 if (!(ok = wait(sm.ds_full, it & 1u))) break;
-                mma_tokens<D>(tmK, tmP, tmP + 64, ag + stage(iq) * C::TILE, it > 0);
-                mma_commit(&sm.empty[stage(iq)]);
+                mma_tokens<D>(one, tmK, tmP, desc_mn(at(iq)), 0, it > 0);
+                mma_tokens<D>(one, tmK, tmP + 64, desc_mn(at(iq)), 1, true);
+                commit(one, &sm.empty[stage(iq)]);
                 if (it + 1 < n) {
                     if (!(ok = wait(&sm.full[stage(io + 2)], phase(io + 2)))) break;
-                    mma_scores<D>(tmP, aV, ag + stage(io + 2) * C::TILE);
-                    mma_commit(sm.dp_full);
+                    mma_scores<D>(one, tmP, dV, desc_k(at(io + 2)));
+                    commit(one, sm.dp_full);
                 }
             }
-            if (ok) mma_commit(sm.acc_full);
-            mma_commit(sm.done);
+            if (ok) commit(one, sm.acc_full);
+            commit(one, sm.done);
             volatile int no_abort = 0;
             mbar_wait(sm.done, 0, &no_abort, p.status);
         }
@@ -567,26 +572,29 @@ __global__ void __launch_bounds__(384, 1) attn_dq_kernel(const __grid_constant__
                     if (armed & (1u << s))
                         mbar_wait(&sm.full[s], (par >> s) & 1u, &no_abort, nullptr, 20000000ull);
             }
-        } else if (warp == 8 && lane == 0) {
+        } else if (warp == 8) {
             // -------------------------------------------------------- MMAs
-            const uint32_t aQ = smem_u32(sm.res), aO = aQ + C::TILE, ag = smem_u32(sm.ring);
+            const uint32_t one = elect_lane();
+            const uint32_t aQ = smem_u32(sm.res), ag = smem_u32(sm.ring);
+            const uint64_t dQ = desc_k(aQ), dO = desc_k(aQ + C::TILE);
             const auto stage = [](int it) { return static_cast<uint32_t>(it % C::STAGES); };
             const auto phase = [](int it) { return static_cast<uint32_t>(it / C::STAGES) & 1u; };
+            const auto at = [&](int it) { return ag + stage(it) * C::TILE; };
             const auto wait = [&](uint64_t* bar, uint32_t parity) {
-                const bool got = mbar_wait(bar, parity, sm.abort_flag, p.status);
+                const bool got = warp_wait(bar, parity, sm.abort_flag, p.status);
                 tc_fence_after();
                 return got;
             };
             bool ok = wait(sm.res_full, 0) && wait(&sm.full[0], 0);
             if (ok) {
-                mma_scores<D>(tm, aQ, ag);
-                mma_commit(sm.s_full);
+                mma_scores<D>(one, tm, dQ, desc_k(at(0)));
+                commit(one, sm.s_full);
                 ok = wait(&sm.full[1], 0);
             }
             if (ok) {
-                mma_scores<D>(tmP, aO, ag + C::TILE);
-                mma_commit(sm.dp_full);
-                mma_commit(&sm.empty[1]);
+                mma_scores<D>(one, tmP, dO, desc_k(at(1)));
+                commit(one, sm.dp_full);
+                commit(one, &sm.empty[1]);
             }
             for (int j = 0; ok && j < n; ++j) {
                 const int ik = 2 * j;
@@ -594,21 +602,22 @@ __global__ void __launch_bounds__(384, 1) attn_dq_kernel(const __grid_constant__
                     // into the other S: its last scores were read before dS of
                     // block j - 1 was written
                     if (!(ok = wait(&sm.full[stage(ik + 2)], phase(ik + 2)))) break;
-                    mma_scores<D>(tm + 128 * ((j + 1) & 1), aQ, ag + stage(ik + 2) * C::TILE);
-                    mma_commit(sm.s_full);
+                    mma_scores<D>(one, tm + 128 * ((j + 1) & 1), dQ, desc_k(at(ik + 2)));
+                    commit(one, sm.s_full);
                 }
                 if (!(ok = wait(sm.ds_full, j & 1u))) break;
-                mma_tokens<D>(tmQ, tmP, tmP + 64, ag + stage(ik) * C::TILE, j > 0);
-                mma_commit(&sm.empty[stage(ik)]);
+                mma_tokens<D>(one, tmQ, tmP, desc_mn(at(ik)), 0, j > 0);
+                mma_tokens<D>(one, tmQ, tmP + 64, desc_mn(at(ik)), 1, true);
+                commit(one, &sm.empty[stage(ik)]);
                 if (j + 1 < n) {
                     if (!(ok = wait(&sm.full[stage(ik + 3)], phase(ik + 3)))) break;
-                    mma_scores<D>(tmP, aO, ag + stage(ik + 3) * C::TILE);
-                    mma_commit(sm.dp_full);
-                    mma_commit(&sm.empty[stage(ik + 3)]);
+                    mma_scores<D>(one, tmP, dO, desc_k(at(ik + 3)));
+                    commit(one, sm.dp_full);
+                    commit(one, &sm.empty[stage(ik + 3)]);
                 }
             }
-            if (ok) mma_commit(sm.acc_full);
-            mma_commit(sm.done);
+            if (ok) commit(one, sm.acc_full);
+            commit(one, sm.done);
             volatile int no_abort = 0;
             mbar_wait(sm.done, 0, &no_abort, p.status);
         }

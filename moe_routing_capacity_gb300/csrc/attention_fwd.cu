@@ -7,8 +7,8 @@
 // the group is odd), over the sequence's key blocks of 128:
 //   S = Q K^T (tcgen05, fp32 in TMEM); m, l = running maximum and sum;
 //   P = 2^(c S - c m) as bf16 back into S's columns; O += P V (A from TMEM).
-// Warps 0-3 and 4-7 run the softmax of the two tiles, a thread a row; warp 8
-// issues the MMAs, warp 9 the TMA loads.  While one tile's softmax runs, the
+// Warps 0-7 and 8-15 run the softmax of the two tiles, two threads a row
+// (64 keys of a block each); warp 16 issues the MMAs, warp 17 the TMA loads.  While one tile's softmax runs, the
 // tensor cores work on the other's products.  TMEM: two S and two O of 128
 // columns, all 512.
 #include <cstring>
@@ -42,7 +42,7 @@ template <int D>
 struct FwdCfg {
     static constexpr int TILE = 128 * D * 2;
     static constexpr int STAGES = D == 128 ? 4 : 8;
-    static constexpr int SMEM = 2 * TILE + STAGES * TILE + 1024 + 256;
+    static constexpr int SMEM = 2 * TILE + STAGES * TILE + 1024 + 4096 + 256;
 };
 
 // One row by the definition on the CUDA cores, for a row whose products met
@@ -120,13 +120,14 @@ __device__ __forceinline__ void each_item(const FwdParams& p, F f) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(384, 1) attn_fwd_kernel(const __grid_constant__ FwdParams p) {
+__global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant__ FwdParams p) {
     using C = FwdCfg<D>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* sQ = smem_raw + (((raw + 1023u) & ~1023u) - raw);
     uint8_t* sKV = sQ + 2 * C::TILE;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sKV + C::STAGES * C::TILE);
+    float* rows = reinterpret_cast<float*>(sKV + C::STAGES * C::TILE);   // [2][2][256]
+    uint64_t* full = reinterpret_cast<uint64_t*>(rows + 1024);
     uint64_t* empty = full + C::STAGES;
     uint64_t* q_full = empty + C::STAGES;
     uint64_t* q_empty = q_full + 1;
@@ -152,13 +153,13 @@ __global__ void __launch_bounds__(384, 1) attn_fwd_kernel(const __grid_constant_
             mbar_init(&p_full[2 * t], 4);
             mbar_init(&p_full[2 * t + 1], 4);
             mbar_init(&o_full[t], 1);
-            mbar_init(&o_empty[t], 4);
+            mbar_init(&o_empty[t], 8);
         }
         mbar_init(done, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 8) {
+    if (warp == 16) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
@@ -168,9 +169,9 @@ __global__ void __launch_bounds__(384, 1) attn_fwd_kernel(const __grid_constant_
     const uint32_t tm = *tmem_slot;
     const uint32_t tmS = tm, tmO = tm + 256;   // tile t: + 128 t
 
-    if (warp >= 8) {
-        setmaxnreg_dec<56>();
-        if (warp == 9 && lane == 0) {
+    if (warp >= 16) {
+        setmaxnreg_dec<64>();
+        if (warp == 17 && lane == 0) {
             // -------------------------------------------------------- loads
             tma_prefetch_map(&p.mapQ);
             tma_prefetch_map(&p.mapK);
@@ -213,35 +214,46 @@ __global__ void __launch_bounds__(384, 1) attn_fwd_kernel(const __grid_constant_
                     if (armed & (1u << s))
                         mbar_wait(&full[s], (par >> s) & 1u, &no_abort, nullptr, 20000000ull);
             }
-        } else if (warp == 8 && lane == 0) {
+        } else if (warp == 16) {
             // -------------------------------------------------------- MMAs
+            const uint32_t one = elect_lane();
             const uint32_t aq = smem_u32(sQ), akv = smem_u32(sKV);
-            uint32_t it = 0;                // tiles taken from the ring so far
+            uint32_t st = 0, ph = 0;        // next tile of the ring
             uint32_t items = 0, ps[2] = {0, 0}, tiles[2] = {0, 0};
             const auto wait = [&](uint64_t* bar, uint32_t parity) {
-                const bool got = mbar_wait(bar, parity, abort_flag, p.status);
+                const bool got = warp_wait(bar, parity, abort_flag, p.status);
                 tc_fence_after();
                 return got;
             };
-            const auto ready = [&](uint32_t i) {
-                return wait(&full[i % C::STAGES], (i / C::STAGES) & 1u);
+            const auto next = [&] {         // its stage, once it has landed; then the one after
+                const uint32_t s = st;
+                if (!wait(&full[st], ph)) return ~0u;
+                if (++st == C::STAGES) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+                return s;
             };
-            const auto at = [&](uint32_t i) { return akv + i % C::STAGES * C::TILE; };
             each_item(p, [&](const FwdWork& w) {
                 if (w.block < 0) return true;
                 const int blocks = max(w.n[0], w.n[1]);
-                if (!wait(q_full, items++ & 1u) || !ready(it)) return false;
+                if (!wait(q_full, items++ & 1u)) return false;
+                uint32_t sk = next();
+                if (sk == ~0u) return false;
                 for (int t = 0; t < 2; ++t)
                     if (w.n[t]) {
-                        mma_scores<D>(tmS + 128 * t, aq + t * C::TILE, at(it));
-                        mma_commit(&s_full[t]);
+                        mma_scores<D>(one, tmS + 128 * t, desc_k(aq + t * C::TILE),
+                                      desc_k(akv + sk * C::TILE));
+                        commit(one, &s_full[t]);
                     }
-                mma_commit(&empty[it % C::STAGES]);
-                if (blocks == 1) mma_commit(q_empty);
+                commit(one, &empty[sk]);
+                if (blocks == 1) commit(one, q_empty);
                 for (int j = 0; j < blocks; ++j) {
-                    const uint32_t iv = it + 2 * j + 1, ik = iv + 1;
-                    if (!ready(iv)) return false;
+                    const uint32_t sv = next();
+                    if (sv == ~0u) return false;
+                    const uint64_t dv = desc_mn(akv + sv * C::TILE);
                     bool have_k = false;
+#pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         if (j >= w.n[t]) continue;
                         const uint32_t dS = tmS + 128 * t, dO = tmO + 128 * t;
@@ -249,50 +261,58 @@ __global__ void __launch_bounds__(384, 1) attn_fwd_kernel(const __grid_constant_
                         if (j == 0 && tiles[t]++ && !wait(&o_empty[t], (tiles[t] - 2) & 1u))
                             return false;
                         if (!wait(&p_full[2 * t], ps[t] & 1u)) return false;
-                        mma_tokens_half<D>(dO, dS, at(iv), 0, j > 0);
+                        mma_tokens<D>(one, dO, dS, dv, 0, j > 0);
                         if (!wait(&p_full[2 * t + 1], ps[t]++ & 1u)) return false;
-                        mma_tokens_half<D>(dO, dS + 32, at(iv), 1, true);
-                        mma_commit(&o_full[t]);
+                        mma_tokens<D>(one, dO, dS + 64, dv, 1, true);
+                        commit(one, &o_full[t]);
                         if (j + 1 < w.n[t]) {
-                            if (!have_k && !ready(ik)) return false;
+                            if (!have_k && (sk = next()) == ~0u) return false;
                             have_k = true;
                             // runs after the product above has read P from these columns
-                            mma_scores<D>(dS, aq + t * C::TILE, at(ik));
-                            mma_commit(&s_full[t]);
+                            mma_scores<D>(one, dS, desc_k(aq + t * C::TILE),
+                                          desc_k(akv + sk * C::TILE));
+                            commit(one, &s_full[t]);
                         }
                     }
-                    mma_commit(&empty[iv % C::STAGES]);
-                    if (have_k) mma_commit(&empty[ik % C::STAGES]);
-                    if (j == blocks - 2) mma_commit(q_empty);   // its last scores are issued
+                    commit(one, &empty[sv]);
+                    if (have_k) commit(one, &empty[sk]);
+                    if (j == blocks - 2) commit(one, q_empty);   // its last scores are issued
                 }
-                it += 2 * blocks;
                 return true;
             });
             // nothing of this CTA is in flight when it leaves
-            mma_commit(done);
+            commit(one, done);
             volatile int no_abort = 0;
             mbar_wait(done, 0, &no_abort, p.status);
         }
     } else {
-        setmaxnreg_inc<224>();
+        setmaxnreg_inc<104>();
         // ------------------------------------------------------------ softmax
-        const int t = warp >> 2;
+        // a thread: row r of tile t, key columns [64 half, 64 half + 64)
+        const int t = warp >> 3, half = (warp >> 2) & 1;
         const int r = threadIdx.x & 127;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t ts = tmS + 128 * t + lane_off, to = tmO + 128 * t + lane_off;
+        const uint32_t ts = tmS + 128 * t + lane_off + 64 * half;
+        const uint32_t to = tmO + 128 * t + lane_off + (D / 2) * half;
+        float* mine = rows + (2 * t + half) * 256 + r;          // what this half of the
+        const float* other = rows + (2 * t + 1 - half) * 256 + r;   // row tells the other
         const float c = p.scale_log2;
         const float slack = 8.0f / c;   // P may reach 2^8 before O is rescaled
         uint32_t blocks = 0;            // key blocks of this tile so far
+        // a warp that has given up (ok false) still meets the others at every
+        // barrier of the tile, and does nothing else
+        bool ok = true;
         each_item(p, [&](const FwdWork& w) {
             const int h = t ? w.h[1] : w.h[0], n = t ? w.n[1] : w.n[0];
             if (w.block < 0) {   // tokens of no sequence
                 if (t && !p.pair_heads) return true;
-                for (int i = r; i < w.len * (p.D / 8); i += 128) {
+                for (int i = r + 128 * half; i < w.len * (p.D / 8); i += 256) {
                     const int64_t o = (w.start + i / (p.D / 8)) * p.o_t + h * p.o_h + i % (p.D / 8) * 8;
                     *reinterpret_cast<uint4*>(p.out + o) = make_uint4(0, 0, 0, 0);
                     if (p.rest) *reinterpret_cast<uint4*>(p.rest + o) = make_uint4(0, 0, 0, 0);
                 }
-                for (int i = r; i < w.len; i += 128) p.lse[h * p.T + w.start + i] = -INFINITY;
+                for (int i = r + 128 * half; i < w.len; i += 256)
+                    p.lse[h * p.T + w.start + i] = -INFINITY;
                 return true;
             }
             if (!n) return true;
@@ -302,75 +322,80 @@ __global__ void __launch_bounds__(384, 1) attn_fwd_kernel(const __grid_constant_
             // backward depends on it
             float m = -INFINITY, l = 0.f, lb = 0.f;
             for (int j = 0; j < n; ++j, ++blocks) {
-                if (!warp_wait(&s_full[t], blocks & 1u, abort_flag, p.status)) return false;
-                tc_fence_after();
-                float s[128];
+                float s[64], top = -INFINITY;
+                ok = ok && warp_wait(&s_full[t], blocks & 1u, abort_flag, p.status);
+                if (ok) {
+                    tc_fence_after();
+                    tmem_ld32_async(ts, reinterpret_cast<uint32_t*>(s));
+                    tmem_ld32_async(ts + 32, reinterpret_cast<uint32_t*>(s) + 32);
+                    tmem_wait_ld();
+                    if (j == n - 1) {   // the diagonal block: keys after the row are hidden
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    tmem_ld32_async(ts + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
-                tmem_wait_ld();
-                if (j == n - 1) {   // the diagonal block: keys after the row are hidden
+                        for (int i = 0; i < 64; ++i)
+                            if (64 * half + i > r) s[i] = -INFINITY;
+                    }
+                    float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                    for (int i = 0; i < 128; ++i)
-                        if (i > r) s[i] = -INFINITY;
+                    for (int i = 4; i < 60; i += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            mx[e] = fmaxf(fmaxf(mx[e], s[i + e]), s[i + 4 + e]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[60 + e]);
+                    top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 }
-                float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                for (int i = 4; i < 124; i += 8)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mx[e] = fmaxf(fmaxf(mx[e], s[i + e]), s[i + 4 + e]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[124 + e]);
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                if (j == 0) {
-                    m = top;
-                } else {
-                    // O keeps an older maximum until a row's rises by 2^8: sums
-                    // in fp32 hold the larger terms, and rescaling is rare
-                    const bool rise = top > m + slack;
-                    if (__any_sync(0xFFFFFFFFu, rise)) {
-                        const float f = rise ? exp2_fast((m - top) * c) : 1.0f;
-                        if (rise) m = top;
-                        l *= f;
-                        lb *= f;
-                        if (!warp_wait(&o_full[t], (blocks - 1) & 1u, abort_flag, p.status))
-                            return false;
-                        tc_fence_after();
+                // O keeps an older maximum until a row's rises by 2^8: sums in
+                // fp32 hold the larger terms, and rescaling is rare
+                if (named_bar_or(1 + t, 256, j == 0 || top > m + slack)) {
+                    *mine = top;
+                    named_bar_sync(1 + t, 256);
+                    top = fmaxf(top, *other);
+                    if (j == 0) {
+                        m = top;
+                    } else {
+                        ok = ok && warp_wait(&o_full[t], (blocks - 1) & 1u, abort_flag, p.status);
+                        if (ok) {
+                            const bool rise = top > m + slack;
+                            const float f = rise ? exp2_fast((m - top) * c) : 1.0f;
+                            if (rise) m = top;
+                            l *= f;
+                            lb *= f;
+                            tc_fence_after();
 #pragma unroll 1
-                        for (int i = 0; i < D / 16; ++i) {
-                            uint32_t o[16];
-                            tmem_ld16(to + 16 * i, o);
+                            for (int i = 0; i < D / 32; ++i) {
+                                uint32_t o[16];
+                                tmem_ld16(to + 16 * i, o);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st16(to + 16 * i, o);
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st16(to + 16 * i, o);
+                            }
+                            tmem_wait_st();
+                            tc_fence_before();
                         }
+                        // the product with V may start on the first half's P
+                        named_bar_sync(1 + t, 256);
                     }
                 }
+                if (!ok) continue;
                 const float2 c2 = make_float2(c, c), neg = make_float2(-m * c, -m * c);
-                uint32_t pk[64];
+                uint32_t pk[32];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                    for (int e = 16 * i; e < 16 * i + 16; ++e) {
-                        const float2 x = fma2(make_float2(s[2 * e], s[2 * e + 1]), c2, neg);
-                        s[2 * e] = exp2_fast(x.x);
-                        s[2 * e + 1] = exp2_fast(x.y);
-                        pk[e] = pack_bf16x2(s[2 * e], s[2 * e + 1]);
-                    }
-                    tmem_st16(ts + 16 * i, pk + 16 * i);
-                    if (i & 1) {   // the product with V starts on this half
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&p_full[2 * t + (i >> 1)]);
-                    }
+                for (int e = 0; e < 32; ++e) {
+                    const float2 x = fma2(make_float2(s[2 * e], s[2 * e + 1]), c2, neg);
+                    s[2 * e] = exp2_fast(x.x);
+                    s[2 * e + 1] = exp2_fast(x.y);
+                    pk[e] = pack_bf16x2(s[2 * e], s[2 * e + 1]);
                 }
+                tmem_st32(ts, pk);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
                 // the sums, while the products run
                 float2 sum = make_float2(0.f, 0.f), sumb = sum;
 #pragma unroll
-                for (int e = 0; e < 64; ++e) {
+                for (int e = 0; e < 32; ++e) {
                     sum = add2(sum, make_float2(s[2 * e], s[2 * e + 1]));
                     sumb = add2(sumb, bf16x2_f32(pk[e]));
                 }
@@ -378,46 +403,57 @@ __global__ void __launch_bounds__(384, 1) attn_fwd_kernel(const __grid_constant_
                 lb += sumb.x + sumb.y;
             }
             // ------------------------------------------------------------ output
-            if (!warp_wait(&o_full[t], (blocks - 1) & 1u, abort_flag, p.status)) return false;
+            ok = ok && warp_wait(&o_full[t], (blocks - 1) & 1u, abort_flag, p.status);
             tc_fence_after();
+            mine[0] = l;
+            mine[128] = lb;
+            named_bar_sync(1 + t, 256);
+            l += other[0];
+            lb += other[128];
             const int row = (t ? w.m0[1] : w.m0[0]) + r;
             const bool valid = row < w.len;
             const float inv = 1.0f / lb;
             const float lse = m * p.scale + logf(l);
-            const int64_t o = (w.start + row) * p.o_t + h * p.o_h;
-            bool bad = false;
+            uint32_t again = 0;
+            if (ok) {
+                const int64_t o = (w.start + row) * p.o_t + h * p.o_h + (D / 2) * half;
+                bool bad = false;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                uint32_t a[32];
-                tmem_ld32(to + 32 * i, a);
-                if (i == D / 32 - 1) {   // O may be overwritten from here on
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&o_empty[t]);
-                }
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int col = 32 * i + 8 * g;
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float x = __uint_as_float(a[8 * g + 2 * e]) * inv;
-                        const float y = __uint_as_float(a[8 * g + 2 * e + 1]) * inv;
-                        bad |= !finite_f32(x) || !finite_f32(y);
-                        hi[e] = pack_bf16x2(x, y);
-                        lo[e] = pack_bf16x2(x - bf16_lo(hi[e]), y - bf16_hi(hi[e]));
+                for (int i = 0; i < D / 64; ++i) {
+                    uint32_t a[32];
+                    tmem_ld32(to + 32 * i, a);
+                    if (i == D / 64 - 1) {   // O may be overwritten from here on
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&o_empty[t]);
                     }
-                    if (valid && col < p.D) {
-                        *reinterpret_cast<uint4*>(p.out + o + col) =
-                            make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        if (p.rest)
-                            *reinterpret_cast<uint4*>(p.rest + o + col) =
-                                make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const int col = 32 * i + 8 * g;
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float x = __uint_as_float(a[8 * g + 2 * e]) * inv;
+                            const float y = __uint_as_float(a[8 * g + 2 * e + 1]) * inv;
+                            bad |= !finite_f32(x) || !finite_f32(y);
+                            hi[e] = pack_bf16x2(x, y);
+                            lo[e] = pack_bf16x2(x - bf16_lo(hi[e]), y - bf16_hi(hi[e]));
+                        }
+                        if (valid && (D / 2) * half + col < p.D) {
+                            *reinterpret_cast<uint4*>(p.out + o + col) =
+                                make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            if (p.rest)
+                                *reinterpret_cast<uint4*>(p.rest + o + col) =
+                                    make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        }
                     }
                 }
+                if (valid && half == 0) p.lse[h * p.T + w.start + row] = lse;
+                again = __ballot_sync(0xFFFFFFFFu, bad && valid);
             }
-            if (valid) p.lse[h * p.T + w.start + row] = lse;
-            uint32_t again = __ballot_sync(0xFFFFFFFFu, bad && valid);
+            // both halves of a row are stored before one is written whole
+            // again, and the sums' exchange is read before its next use
+            named_bar_sync(1 + t, 256);
             while (again) {
                 const int src = __ffs(again) - 1;
                 again &= again - 1;
@@ -429,7 +465,7 @@ __global__ void __launch_bounds__(384, 1) attn_fwd_kernel(const __grid_constant_
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) tmem_dealloc(tm, 512);
+    if (warp == 16) tmem_dealloc(tm, 512);
 }
 
 // ------------------------------------------------------------------ the plan
@@ -615,12 +651,12 @@ int launch_attention_fwd(const moe_attention_t& a, const void* plan, const uint1
     if (D <= 64) {
         if (ensure_smem_attr(reinterpret_cast<const void*>(attn_fwd_kernel<64>), FwdCfg<64>::SMEM))
             return MOE_ECUDA;
-        attn_fwd_kernel<64><<<grid, 384, FwdCfg<64>::SMEM, st>>>(p);
+        attn_fwd_kernel<64><<<grid, 640, FwdCfg<64>::SMEM, st>>>(p);
     } else {
         if (ensure_smem_attr(reinterpret_cast<const void*>(attn_fwd_kernel<128>),
                              FwdCfg<128>::SMEM))
             return MOE_ECUDA;
-        attn_fwd_kernel<128><<<grid, 384, FwdCfg<128>::SMEM, st>>>(p);
+        attn_fwd_kernel<128><<<grid, 640, FwdCfg<128>::SMEM, st>>>(p);
     }
     if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
     trace_after(st, "attn_fwd");
