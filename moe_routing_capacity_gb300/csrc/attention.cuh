@@ -191,6 +191,53 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+// Four lanes of a quad hold a row each, in four 16-byte pieces; afterwards a
+// lane holds its own piece of each of the four rows, so that a quad's store
+// covers 64 contiguous bytes of a row instead of 16 bytes of four rows.
+__device__ __forceinline__ void quad_transpose(uint4 (&v)[4]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int s = 1; s <= 2; s <<= 1) {
+        const bool up = lane & s;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & s) continue;
+            uint4 &a = v[i], &b = v[i + s];
+            const uint4 x = up ? a : b;
+            uint4 y;
+            y.x = __shfl_xor_sync(0xFFFFFFFFu, x.x, s);
+            y.y = __shfl_xor_sync(0xFFFFFFFFu, x.y, s);
+            y.z = __shfl_xor_sync(0xFFFFFFFFu, x.z, s);
+            y.w = __shfl_xor_sync(0xFFFFFFFFu, x.w, s);
+            if (up)
+                a = y;
+            else
+                b = y;
+        }
+    }
+}
+
+// 32 columns [col, col + 32) of the warp's 32 rows to global memory as bf16:
+// v is this thread's row in four pieces, base the address of the warp's first
+// row, rows how many of them exist, D how many columns.
+__device__ __forceinline__ void store_quad(uint4 (&v)[4], uint16_t* base, int64_t stride, int rows,
+                                           int col, int D) {
+    const int lane = threadIdx.x & 31;
+    quad_transpose(v);
+    const int c = col + 8 * (lane & 3);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int r = (lane & ~3) + k;
+        if (r < rows && c < D) *reinterpret_cast<uint4*>(base + r * stride + c) = v[k];
+    }
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ bool finite_f32(float x) { return fabsf(x) <= 3.402823466e38f; }
 
 __device__ __forceinline__ float bf16_f32(uint16_t v) {

@@ -172,32 +172,34 @@ __device__ __forceinline__ void zero_rows(uint16_t* base, int64_t st_t, int D, i
             make_uint4(0, 0, 0, 0);
 }
 
-// Columns [c0, c0 + N) of an accumulator row, times `f`, as bf16 to global
-// memory; returns whether a value was not finite.
+// Columns [c0, c0 + N) of the warp's 32 accumulator rows, times `f`, as bf16
+// to global memory (base: its first row; rows: how many exist); returns
+// whether a value of this thread's row was not finite.
 template <int N>
-__device__ __forceinline__ bool store_row(uint32_t taddr, int c0, int D, float f, uint16_t* o,
-                                          bool valid) {
-    bool bad = false;
+__device__ __forceinline__ bool store_rows(uint32_t taddr, int c0, int D, float f, uint16_t* base,
+                                           int64_t stride, int rows) {
+    float2 sick = make_float2(0.f, 0.f);   // NaN once a value is not finite
 #pragma unroll
     for (int i = 0; i < N / 32; ++i) {
         uint32_t a[32];
         tmem_ld32(taddr + c0 + 32 * i, a);
+        uint4 v[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            const int col = c0 + 32 * i + 8 * g;
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float x = __uint_as_float(a[8 * g + 2 * e]) * f;
-                const float y = __uint_as_float(a[8 * g + 2 * e + 1]) * f;
-                bad |= !finite_f32(x) || !finite_f32(y);
-                w[e] = pack_bf16x2(x, y);
+                const float2 x = mul2(make_float2(__uint_as_float(a[8 * g + 2 * e]),
+                                                  __uint_as_float(a[8 * g + 2 * e + 1])),
+                                      make_float2(f, f));
+                sick = fma2(x, make_float2(0.f, 0.f), sick);
+                w[e] = pack_bf16x2(x.x, x.y);
             }
-            if (valid && col < D)
-                *reinterpret_cast<uint4*>(o + col) = make_uint4(w[0], w[1], w[2], w[3]);
+            v[g] = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        store_quad(v, base, stride, rows, c0 + 32 * i, D);
     }
-    return bad;
+    return !(sick.x + sick.y == 0.f);
 }
 
 template <int D>
@@ -489,10 +491,12 @@ __global__ void __launch_bounds__(384, 1) attn_dkv_kernel(const __grid_constant_
         if (ok) {   // warps 0-3 write dV, warps 4-7 dK
             const int row = nb * 128 + r;
             const bool valid = row < len;
-            uint16_t* o = half ? p.dk + (start + row) * p.dk_t + kvh * p.dk_h
-                               : p.dv + (start + row) * p.dv_t + kvh * p.dv_h;
-            const bool bad = store_row<D>((half ? tmK : tmV) + lane_off, 0, p.D,
-                                          half ? p.scale : 1.0f, o, valid);
+            const int64_t st_t = half ? p.dk_t : p.dv_t;
+            uint16_t* o = (half ? p.dk + kvh * p.dk_h : p.dv + kvh * p.dv_h) +
+                          (start + row - lane) * st_t;
+            const bool bad = store_rows<D>((half ? tmK : tmV) + lane_off, 0, p.D,
+                                           half ? p.scale : 1.0f, o, st_t, len - (row - lane));
+            __syncwarp();   // a row's pieces come from four lanes
             uint32_t again = __ballot_sync(0xFFFFFFFFu, bad && valid);
             while (again) {
                 const int s = __ffs(again) - 1;
@@ -703,9 +707,9 @@ __global__ void __launch_bounds__(384, 1) attn_dq_kernel(const __grid_constant__
         tc_fence_after();
         uint32_t again = 0;
         if (ok) {
-            uint16_t* o = p.dq + (start + row) * p.dq_t + h * p.dq_h;
-            const bool bad = store_row<D / 2>(tmQ + lane_off, half * (D / 2), p.D, p.scale, o,
-                                              valid);
+            uint16_t* o = p.dq + (start + row - lane) * p.dq_t + h * p.dq_h;
+            const bool bad = store_rows<D / 2>(tmQ + lane_off, half * (D / 2), p.D, p.scale, o,
+                                               p.dq_t, len - (row - lane));
             again = __ballot_sync(0xFFFFFFFFu, bad && valid);
         }
         // either half of a row may have met the value: the warps of the other

@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
                     for (int i = 4; i < 60; i += 8)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            mx[e] = fmaxf(fmaxf(mx[e], s[i + e]), s[i + 4 + e]);
+                            mx[e] = max3(mx[e], s[i + e], s[i + 4 + e]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[60 + e]);
                     top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
@@ -381,13 +381,16 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
                 const float2 c2 = make_float2(c, c), neg = make_float2(-m * c, -m * c);
                 uint32_t pk[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float2 x = fma2(make_float2(s[2 * e], s[2 * e + 1]), c2, neg);
-                    s[2 * e] = exp2_fast(x.x);
-                    s[2 * e + 1] = exp2_fast(x.y);
-                    pk[e] = pack_bf16x2(s[2 * e], s[2 * e + 1]);
+                for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                    for (int e = 16 * i; e < 16 * i + 16; ++e) {
+                        const float2 x = fma2(make_float2(s[2 * e], s[2 * e + 1]), c2, neg);
+                        s[2 * e] = exp2_fast(x.x);
+                        s[2 * e + 1] = exp2_fast(x.y);
+                        pk[e] = pack_bf16x2(s[2 * e], s[2 * e + 1]);
+                    }
+                    tmem_st16(ts + 16 * i, pk + 16 * i);
                 }
-                tmem_st32(ts, pk);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -416,8 +419,9 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
             const float lse = m * p.scale + logf(l);
             uint32_t again = 0;
             if (ok) {
-                const int64_t o = (w.start + row) * p.o_t + h * p.o_h + (D / 2) * half;
-                bool bad = false;
+                const int row0 = row - lane;          // the warp's first row
+                const int64_t o = (w.start + row0) * p.o_t + h * p.o_h;
+                float2 sick = make_float2(0.f, 0.f);  // NaN once a value is not finite
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i) {
                     uint32_t a[32];
@@ -427,27 +431,30 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&o_empty[t]);
                     }
+                    uint32_t hi[16], lo[16];
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const int col = 32 * i + 8 * g;
-                        uint32_t hi[4], lo[4];
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 x = mul2(make_float2(__uint_as_float(a[2 * e]),
+                                                          __uint_as_float(a[2 * e + 1])),
+                                              make_float2(inv, inv));
+                        sick = fma2(x, make_float2(0.f, 0.f), sick);
+                        hi[e] = pack_bf16x2(x.x, x.y);
+                        lo[e] = pack_bf16x2(x.x - bf16_lo(hi[e]), x.y - bf16_hi(hi[e]));
+                    }
+                    const int col = (D / 2) * half + 32 * i;
+                    uint4 v[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float x = __uint_as_float(a[8 * g + 2 * e]) * inv;
-                            const float y = __uint_as_float(a[8 * g + 2 * e + 1]) * inv;
-                            bad |= !finite_f32(x) || !finite_f32(y);
-                            hi[e] = pack_bf16x2(x, y);
-                            lo[e] = pack_bf16x2(x - bf16_lo(hi[e]), y - bf16_hi(hi[e]));
-                        }
-                        if (valid && (D / 2) * half + col < p.D) {
-                            *reinterpret_cast<uint4*>(p.out + o + col) =
-                                make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                            if (p.rest)
-                                *reinterpret_cast<uint4*>(p.rest + o + col) =
-                                    make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                        }
+                    for (int g = 0; g < 4; ++g)
+                        v[g] = make_uint4(hi[4 * g], hi[4 * g + 1], hi[4 * g + 2], hi[4 * g + 3]);
+                    store_quad(v, p.out + o, p.o_t, w.len - row0, col, p.D);
+                    if (p.rest) {
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            v[g] = make_uint4(lo[4 * g], lo[4 * g + 1], lo[4 * g + 2], lo[4 * g + 3]);
+                        store_quad(v, p.rest + o, p.o_t, w.len - row0, col, p.D);
                     }
                 }
+                const bool bad = !(sick.x + sick.y == 0.f);
                 if (valid && half == 0) p.lse[h * p.T + w.start + row] = lse;
                 again = __ballot_sync(0xFFFFFFFFu, bad && valid);
             }
