@@ -36,6 +36,23 @@ inline AttnPlanLayout attn_plan_layout(int64_t T, int n_seqs) {
     return l;
 }
 
+// The items of this CTA, heaviest first: dealt out to the CTAs in turn, every
+// other round from the other end, so that a CTA's early heavy item meets a
+// lighter one in the next round.
+struct AttnItems {
+    int total, round = 0;
+    __device__ explicit AttnItems(int n) : total(n) {}
+    __device__ bool next(int& item) {
+        const int g = gridDim.x;
+        while (round * g < total) {
+            item = round * g + static_cast<int>((round & 1) ? g - 1 - blockIdx.x : blockIdx.x);
+            ++round;
+            if (item < total) return true;
+        }
+        return false;
+    }
+};
+
 // ------------------------------------------------------------------ TMEM
 
 // 32 consecutive columns, without waiting (tmem_wait_ld before their use).
@@ -143,12 +160,13 @@ constexpr uint32_t kBoxBytes = 16384;
 constexpr uint64_t kDescBase = (static_cast<uint64_t>(1024 >> 4) << 32) |
                                (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 
+// (The mask: in a cluster, a shared-memory address carries the CTA's rank.)
 __device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
-    return kDescBase | (static_cast<uint64_t>(1) << 16) | (saddr >> 4);
+    return kDescBase | (static_cast<uint64_t>(1) << 16) | ((saddr & 0x3FFFFu) >> 4);
 }
 
 __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
-    return kDescBase | (static_cast<uint64_t>(kBoxBytes >> 4) << 16) | (saddr >> 4);
+    return kDescBase | (static_cast<uint64_t>(kBoxBytes >> 4) << 16) | ((saddr & 0x3FFFFu) >> 4);
 }
 
 // scores[tmem] = A B^T over D channels, both tiles K-major.
@@ -180,6 +198,23 @@ __device__ __forceinline__ void mma_tokens(uint32_t leader, uint32_t d_tmem, uin
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                           int32_t* status) {
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, status));
+}
+
+// acc[tmem] (+)= A B over 128 tokens: A bf16 in four pieces of 32 tokens (16
+// columns each, 32 columns apart), B a tile read MN-major.
+template <int D>
+__device__ __forceinline__ void mma_tokens_quarters(uint32_t leader, uint32_t d_tmem,
+                                                    uint32_t a_tmem, uint64_t b, bool accumulate) {
+    constexpr uint32_t idesc = idesc_bf16_f32(128, D, false, true);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+        mma_ts(leader, d_tmem, a_tmem + (kk / 2) * 32 + (kk % 2) * 8, b + ((kk * 2048) >> 4), idesc,
+               accumulate || kk > 0);
+}
+
+// Brings `bytes` (a multiple of 16, from a 16-byte boundary) into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 // ------------------------------------------------------------------ arithmetic

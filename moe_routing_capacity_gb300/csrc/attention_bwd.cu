@@ -4,16 +4,18 @@
 //   dV_j = sum_i P_ij dO_i                dS_ij = P_ij (dO_i . V_j - D_i)
 //   dK_j = scale sum_i dS_ij Q_i          dQ_i = scale sum_j dS_ij K_j
 //
-// Three kernels.  The first forms D (from O in two bf16 parts) and the scaled
-// lse.  The second gives one CTA 128 query rows and walks their key blocks
-// for dQ.  The third gives one CTA 128 keys of one key/value head and walks
-// the query blocks of all the group's heads, so dK and dV are summed in TMEM
-// and written once: no atomics, the same bits every time.  Both compute P and
-// dP again (seven products of 128 x 128 x D a block pair where five are
-// needed): the price of a fixed order without a pass over memory for dQ.
-// Warps 0-7 form P and dS (a thread holds 64 of the 128 columns of its TMEM
-// lane), warp 8 issues the MMAs, warp 9 the TMA loads.  P and dS return to
-// the columns of S and dP as bf16 A operands.
+// Two kernels.  The first, one CTA an SM working through the batch, takes 128
+// query rows at a time, forms their D (from O in two bf16 parts) and walks
+// their key blocks for dQ.  The second gives 128 keys of one key/value head to
+// a CTA, or to a cluster of two or four where there are few, and walks the
+// query blocks of all the group's heads, so dK and dV are summed in TMEM (a
+// cluster's parts then in their order through shared memory) and written
+// once: no atomics, the same bits every time.
+// Both compute P and dP again (seven products of 128 x 128 x D a block pair
+// where five are needed): the price of a fixed order without a pass over
+// memory for dQ.  Warps 0-15 form P and dS (a thread holds 32 of the 128
+// columns of its TMEM lane), warp 16 issues the MMAs, warp 17 the TMA loads.
+// P and dS return to the columns of S and dP as bf16 A operands.
 #include <cstring>
 
 #include "attention.cuh"
@@ -37,53 +39,13 @@ struct BwdParams {
     const uint16_t *q, *k, *v, *dout;
     int64_t dq_t, dq_h, dk_t, dk_h, dv_t, dv_h;
     uint16_t *dq, *dk, *dv;
-    const float* lse2;     // [heads, T]
-    float* delta;          // [heads, T]
+    const uint16_t *out, *rest;
+    int64_t o_t, o_h;
+    const float* lse;
+    float *lse2, *delta;   // [heads, T]: lse log2 e and D, written by the dQ kernel
     float scale, scale_log2;
     int32_t* status;
 };
-
-// ------------------------------------------------------------------ D and lse
-
-struct DeltaParams {
-    int64_t T;
-    int heads, D;
-    int64_t o_t, o_h, do_t, do_h;
-    const uint16_t *out, *rest, *dout;
-    const float* lse;
-    float *lse2, *delta;
-};
-
-// Eight lanes a row (16 bytes a load), four rows a warp.
-__global__ void __launch_bounds__(256) attn_delta_kernel(const DeltaParams p) {
-    const int64_t r = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / 8;
-    const int part = threadIdx.x & 7;
-    const int64_t rows = p.T * p.heads;
-    const int64_t t = r / p.heads;
-    const int h = static_cast<int>(r - t * p.heads);
-    float sum = 0.f;
-    if (r < rows) {
-        const int64_t o = t * p.o_t + h * p.o_h, g = t * p.do_t + h * p.do_h;
-        for (int c = part * 8; c < p.D; c += 64) {
-            const uint4 a = *reinterpret_cast<const uint4*>(p.out + o + c);
-            const uint4 b = *reinterpret_cast<const uint4*>(p.rest + o + c);
-            const uint4 d = *reinterpret_cast<const uint4*>(p.dout + g + c);
-            const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w},
-                           dv[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sum += bf16_lo(dv[i]) * (bf16_lo(av[i]) + bf16_lo(bv[i]));
-                sum += bf16_hi(dv[i]) * (bf16_hi(av[i]) + bf16_hi(bv[i]));
-            }
-        }
-    }
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (r < rows && part == 0) {
-        p.delta[h * p.T + t] = sum;
-        p.lse2[h * p.T + t] = p.lse[h * p.T + t] * kLog2e;
-    }
-}
 
 // ------------------------------------------------------------------ rows by the definition
 
@@ -136,9 +98,9 @@ __device__ __noinline__ void dq_row(const BwdParams& p, int64_t start, int row, 
             p.dq[t * p.dq_t + h * p.dq_h + lane + 32 * i] = f32_bf16(acc[i] * p.scale);
 }
 
-// which: 0 the row of dV, 1 of dK.
+// Columns [c0, c1) of the row of dV (which = 0) or dK (1).
 __device__ __noinline__ void dkv_row(const BwdParams& p, int64_t start, int len, int row, int kvh,
-                                     int which) {
+                                     int which, int c0, int c1) {
     const int lane = threadIdx.x & 31;
     const int64_t t = start + row;
     float k[4], v[4], acc[4] = {0, 0, 0, 0};
@@ -163,7 +125,8 @@ __device__ __noinline__ void dkv_row(const BwdParams& p, int64_t start, int len,
     uint16_t* o = which ? p.dk + t * p.dk_t + kvh * p.dk_h : p.dv + t * p.dv_t + kvh * p.dv_h;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < p.D) o[lane + 32 * i] = f32_bf16(which ? acc[i] * p.scale : acc[i]);
+        if (lane + 32 * i >= c0 && lane + 32 * i < min(c1, p.D))
+            o[lane + 32 * i] = f32_bf16(which ? acc[i] * p.scale : acc[i]);
 }
 
 __device__ __forceinline__ void zero_rows(uint16_t* base, int64_t st_t, int D, int rows) {
@@ -172,82 +135,93 @@ __device__ __forceinline__ void zero_rows(uint16_t* base, int64_t st_t, int D, i
             make_uint4(0, 0, 0, 0);
 }
 
-// Columns [c0, c0 + N) of the warp's 32 accumulator rows, times `f`, as bf16
+// Columns [c0, c0 + 32) of the warp's 32 accumulator rows, times `f`, as bf16
 // to global memory (base: its first row; rows: how many exist); returns
 // whether a value of this thread's row was not finite.
-template <int N>
 __device__ __forceinline__ bool store_rows(uint32_t taddr, int c0, int D, float f, uint16_t* base,
                                            int64_t stride, int rows) {
     float2 sick = make_float2(0.f, 0.f);   // NaN once a value is not finite
+    uint32_t a[32];
+    tmem_ld32(taddr + c0, a);
+    uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < N / 32; ++i) {
-        uint32_t a[32];
-        tmem_ld32(taddr + c0 + 32 * i, a);
-        uint4 v[4];
+    for (int g = 0; g < 4; ++g) {
+        uint32_t w[4];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 x = mul2(make_float2(__uint_as_float(a[8 * g + 2 * e]),
-                                                  __uint_as_float(a[8 * g + 2 * e + 1])),
-                                      make_float2(f, f));
-                sick = fma2(x, make_float2(0.f, 0.f), sick);
-                w[e] = pack_bf16x2(x.x, x.y);
-            }
-            v[g] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int e = 0; e < 4; ++e) {
+            const float2 x = mul2(make_float2(__uint_as_float(a[8 * g + 2 * e]),
+                                              __uint_as_float(a[8 * g + 2 * e + 1])),
+                                  make_float2(f, f));
+            sick = fma2(x, make_float2(0.f, 0.f), sick);
+            w[e] = pack_bf16x2(x.x, x.y);
         }
-        store_quad(v, base, stride, rows, c0 + 32 * i, D);
+        v[g] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    store_quad(v, base, stride, rows, c0, D);
     return !(sick.x + sick.y == 0.f);
 }
 
-template <int D>
+// Two resident tiles, a ring of ST streamed ones, the rows' scalars, barriers.
+template <int D, int ST>
 struct BwdCfg {
     static constexpr int TILE = 128 * D * 2;
-    static constexpr int STAGES = D == 128 ? 4 : 8;
-    static constexpr int SMEM = 2 * TILE + STAGES * TILE + 1024 + 256 + 2048;
+    static constexpr int STAGES = ST;
+    static constexpr int SMEM = 2 * TILE + STAGES * TILE + 2048 + 256;
 };
+// Warps 0-15 form P and dS; then the MMA warp, the load warp, two idle ones.
+constexpr int kBwdThreads = 640, kMmaWarp = 16, kLoadWarp = 17, kFormers = 512;
+constexpr int dkv_stages(int D) { return D == 128 ? 4 : 8; }
+constexpr int dq_stages(int D) { return D == 128 ? 5 : 8; }
 
 // Shared-memory layout and barriers of both kernels: two resident tiles, a
 // ring of streamed ones.
-template <int D>
+template <class C>
 struct BwdSmem {
     uint8_t *res, *ring;
-    float* rows;                    // dK/dV: lse2 and delta of a query block, two buffers
-    uint64_t *full, *empty, *res_full, *s_full, *dp_full, *p_full, *ds_full, *acc_full, *done;
+    float* rows;   // two buffers of 256: scalars of a query block's rows
+    uint64_t *full, *empty, *res_full, *res_empty, *s_full, *s_free, *dp_full, *p_full, *ds_full, *acc_full,
+        *acc_empty, *done, *sums_there, *sums_read;
     uint32_t* tmem_slot;
     volatile int* abort_flag;
     __device__ explicit BwdSmem(uint8_t* raw_ptr) {
-        using C = BwdCfg<D>;
-        const uint32_t raw = smem_u32(raw_ptr);
-        res = raw_ptr + (((raw + 1023u) & ~1023u) - raw);
+        res = raw_ptr;
         ring = res + 2 * C::TILE;
         rows = reinterpret_cast<float*>(ring + C::STAGES * C::TILE);
         full = reinterpret_cast<uint64_t*>(rows + 512);
         empty = full + C::STAGES;
         res_full = empty + C::STAGES;
-        s_full = res_full + 1;
-        dp_full = s_full + 1;
-        p_full = dp_full + 1;
+        res_empty = res_full + 1;
+        s_full = res_empty + 1;
+        s_free = s_full + 1;
+        dp_full = s_free + 1;
+        p_full = dp_full + 2;
         ds_full = p_full + 1;
         acc_full = ds_full + 1;
-        done = acc_full + 1;
-        tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+        acc_empty = acc_full + 1;
+        done = acc_empty + 1;
+        sums_there = done + 1;
+        sums_read = sums_there + 1;
+        tmem_slot = reinterpret_cast<uint32_t*>(sums_read + 1);
         abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     }
-    __device__ void init() {
-        for (int s = 0; s < BwdCfg<D>::STAGES; ++s) {
+    __device__ void init(int parts) {   // parts: CTAs of a cluster
+        for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         mbar_init(res_full, 1);
         mbar_init(s_full, 1);
-        mbar_init(dp_full, 1);
-        mbar_init(p_full, 256);
-        mbar_init(ds_full, 256);
+        mbar_init(s_free, 16);   // one arrival a warp
+        mbar_init(&dp_full[0], 1);   // dQ: one for each dP, since the next one may be
+        mbar_init(&dp_full[1], 1);   // ready before this one is looked for
+        mbar_init(p_full, 16);
+        mbar_init(ds_full, 16);
+        mbar_init(res_empty, 1);
         mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 16);
         mbar_init(done, 1);
+        mbar_init(sums_there, 16 * parts);   // one arrival a warp and CTA
+        mbar_init(sums_read, 16 * parts);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -262,51 +236,65 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
 
 // ------------------------------------------------------------------ dK, dV
 
-template <int D>
-__global__ void __launch_bounds__(384, 1) attn_dkv_kernel(const __grid_constant__ BwdParams p) {
-    using C = BwdCfg<D>;
-    const int tile = blockIdx.x / p.units;
+template <int D, int PARTS>
+__global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_constant__ BwdParams p) {
+    using C = BwdCfg<D, dkv_stages(D)>;
+    // the CTAs of a cluster share one block of keys: a part of its query
+    // blocks each, their sums joined through shared memory at the end
+    const uint32_t part = PARTS > 1 ? cluster_ctarank() : 0u;
+    const int item = blockIdx.x / PARTS;
+    const int tile = item / p.units;
     if (tile >= p.header[p.list]) return;
-    const int kvh = blockIdx.x - tile * p.units;
+    const int kvh = item - tile * p.units;
     const int4 te = p.tiles[tile];
     const int64_t start = te.x;
     const int len = te.y;
     if (te.z < 0) {   // tokens of no sequence
+        if (part) return;
         zero_rows(p.dk + start * p.dk_t + kvh * p.dk_h, p.dk_t, p.D, len);
         zero_rows(p.dv + start * p.dv_t + kvh * p.dv_h, p.dv_t, p.D, len);
         return;
     }
     const int nb = te.z, nblk = (len + 127) / 128;
     const int per_head = nblk - nb;          // query blocks of one head
-    const int n = p.group * per_head;
+    const int all = p.group * per_head;
+    const int first = static_cast<int>(all * part / PARTS);
+    const int n = static_cast<int>(all * (part + 1) / PARTS) - first;
 
-    extern __shared__ uint8_t smem_raw[];
-    BwdSmem<D> sm(smem_raw);
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    if (smem_u32(smem_raw) & 1023u) {   // the swizzled tiles' alignment
+        report_error(p.status, MOE_ECUDA);
+        return;
+    }
+    BwdSmem<C> sm(smem_raw);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) sm.init();
-    if (warp == 8) {
+    if (threadIdx.x == 0) sm.init(PARTS);
+    if (warp == kMmaWarp) {
         tmem_alloc(sm.tmem_slot, 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (PARTS > 1) cluster_sync();   // the others' barriers exist
     const uint32_t tm = *sm.tmem_slot;
     const uint32_t tmS = tm, tmP = tm + 128, tmV = tm + 256, tmK = tm + 384;
 
-    if (warp >= 8) {
-        setmaxnreg_dec<88>();
-        if (warp == 9 && lane == 0) {
+    if (warp >= kMmaWarp) {
+        setmaxnreg_dec<64>();
+        if (warp == kLoadWarp && lane == 0) {
             // -------------------------------------------------------- loads
             const uint32_t ar = smem_u32(sm.res), ag = smem_u32(sm.ring);
             const int tok = static_cast<int>(start);
-            mbar_arrive_expect_tx(sm.res_full, 2 * C::TILE);
-            load_tile<D>(ar, &p.mapK, sm.res_full, tok + nb * 128, kvh);
-            load_tile<D>(ar + C::TILE, &p.mapV, sm.res_full, tok + nb * 128, kvh);
+            if (n) {
+                mbar_arrive_expect_tx(sm.res_full, 2 * C::TILE);
+                load_tile<D>(ar, &p.mapK, sm.res_full, tok + nb * 128, kvh);
+                load_tile<D>(ar + C::TILE, &p.mapV, sm.res_full, tok + nb * 128, kvh);
+            }
             uint32_t st = 0, ph = 0, armed = 0, par = 0;
             bool ok = true;
-            int h = kvh * p.group, i = nb;
+            int h = kvh * p.group + first / per_head, i = nb + first % per_head;
             for (int it = 0; it < 2 * n; ++it) {
                 if (!mbar_wait(&sm.empty[st], ph ^ 1u, sm.abort_flag, p.status)) {
                     ok = false;
@@ -328,12 +316,12 @@ __global__ void __launch_bounds__(384, 1) attn_dkv_kernel(const __grid_constant_
             }
             if (!ok || *sm.abort_flag) {   // let the armed copies land before leaving
                 volatile int no_abort = 0;
-                mbar_wait(sm.res_full, 0, &no_abort, nullptr, 20000000ull);
+                if (n) mbar_wait(sm.res_full, 0, &no_abort, nullptr, 20000000ull);
                 for (int s = 0; s < C::STAGES; ++s)
                     if (armed & (1u << s))
                         mbar_wait(&sm.full[s], (par >> s) & 1u, &no_abort, nullptr, 20000000ull);
             }
-        } else if (warp == 8) {
+        } else if (warp == kMmaWarp) {
             // -------------------------------------------------------- MMAs
             const uint32_t one = elect_lane();
             const uint32_t aK = smem_u32(sm.res), ag = smem_u32(sm.ring);
@@ -346,7 +334,7 @@ __global__ void __launch_bounds__(384, 1) attn_dkv_kernel(const __grid_constant_
                 tc_fence_after();
                 return got;
             };
-            bool ok = wait(sm.res_full, 0) && wait(&sm.full[0], 0);
+            bool ok = n && wait(sm.res_full, 0) && wait(&sm.full[0], 0);
             if (ok) {
                 mma_scores<D>(one, tmS, dK, desc_k(at(0)));
                 commit(one, sm.s_full);
@@ -359,8 +347,7 @@ __global__ void __launch_bounds__(384, 1) attn_dkv_kernel(const __grid_constant_
             for (int it = 0; ok && it < n; ++it) {
                 const int iq = 2 * it, io = iq + 1;
                 if (!(ok = wait(sm.p_full, it & 1u))) break;
-                mma_tokens<D>(one, tmV, tmS, desc_mn(at(io)), 0, it > 0);
-                mma_tokens<D>(one, tmV, tmS + 64, desc_mn(at(io)), 1, true);
+                mma_tokens_quarters<D>(one, tmV, tmS, desc_mn(at(io)), it > 0);
                 commit(one, &sm.empty[stage(io)]);
                 if (it + 1 < n) {
                     if (!(ok = wait(&sm.full[stage(iq + 2)], phase(iq + 2)))) break;
@@ -369,8 +356,7 @@ __global__ void __launch_bounds__(384, 1) attn_dkv_kernel(const __grid_constant_
                     commit(one, sm.s_full);
                 }
                 if (!(ok = wait(sm.ds_full, it & 1u))) break;
-                mma_tokens<D>(one, tmK, tmP, desc_mn(at(iq)), 0, it > 0);
-                mma_tokens<D>(one, tmK, tmP + 64, desc_mn(at(iq)), 1, true);
+                mma_tokens_quarters<D>(one, tmK, tmP, desc_mn(at(iq)), it > 0);
                 commit(one, &sm.empty[stage(iq)]);
                 if (it + 1 < n) {
                     if (!(ok = wait(&sm.full[stage(io + 2)], phase(io + 2)))) break;
@@ -384,46 +370,42 @@ __global__ void __launch_bounds__(384, 1) attn_dkv_kernel(const __grid_constant_
             mbar_wait(sm.done, 0, &no_abort, p.status);
         }
     } else {
-        setmaxnreg_inc<208>();
+        setmaxnreg_inc<104>();
         // ------------------------------------------------------------ P and dS
-        // a thread: key row r, query columns [64 half, 64 half + 64)
-        const int half = warp >> 2;
+        // a thread: key row r, query columns [c0, c0 + 32)
+        const int quarter = warp >> 2, c0 = 32 * quarter;
         const int r = threadIdx.x & 127;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t ts = tmS + lane_off + 64 * half, tp = tmP + lane_off + 64 * half;
+        const uint32_t ts = tmS + lane_off + c0, tp = tmP + lane_off + c0;
         const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
-        // this thread's share of the query rows' scalars: lse2 or delta of row r
-        const float* src = half ? static_cast<const float*>(p.delta) : p.lse2;
+        // warps 0-3 and 4-7 bring the query rows' lse2 and D
+        const float* src = quarter == 0 ? p.lse2 : p.delta;
         const auto fetch = [&](int it) {
-            const int g = it / per_head, i = (nb + it - g * per_head) * 128 + r;
-            return i < len ? src[(kvh * p.group + g) * p.T + start + i] : 0.f;
+            const int g = (first + it) / per_head, i = (nb + first + it - g * per_head) * 128 + r;
+            return quarter < 2 && i < len ? src[(kvh * p.group + g) * p.T + start + i] : 0.f;
         };
-        float next = fetch(0);
+        float next = n ? fetch(0) : 0.f;
         bool ok = true;
         for (int it = 0; it < n; ++it) {
             float* rows = sm.rows + (it & 1) * 256;
-            rows[half * 128 + r] = next;
-            named_bar_sync(1, 256);
+            if (quarter < 2) rows[quarter * 128 + r] = next;
+            named_bar_sync(1, kFormers);
             if (!ok) continue;   // given up: only meets the others at the barrier
             if (it + 1 < n) next = fetch(it + 1);
-            const int qb = nb + it % per_head;
+            const int qb = nb + (first + it) % per_head;
             const int limit = min(128, len - qb * 128);   // query rows in this block
             const bool masked = qb == nb || limit < 128;
             const int lo = qb == nb ? r : 0;               // columns lo .. limit-1 count
 
-            if (!warp_wait(sm.s_full, it & 1u, sm.abort_flag, p.status)) {
-                ok = false;
-                continue;
-            }
+            if (!(ok = warp_wait(sm.s_full, it & 1u, sm.abort_flag, p.status))) continue;
             tc_fence_after();
-            float x[64];
+            float x[32];
             tmem_ld32_async(ts, reinterpret_cast<uint32_t*>(x));
-            tmem_ld32_async(ts + 32, reinterpret_cast<uint32_t*>(x) + 32);
             tmem_wait_ld();
-            uint32_t pk[32];
-            const float4* l4 = reinterpret_cast<const float4*>(rows + 64 * half);
+            uint32_t pk[16];
+            const float4* l4 = reinterpret_cast<const float4*>(rows + c0);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 const float4 l = l4[i];
                 const float2 a = fma2(make_float2(x[4 * i], x[4 * i + 1]), c2,
                                       make_float2(-l.x, -l.y));
@@ -436,30 +418,25 @@ __global__ void __launch_bounds__(384, 1) attn_dkv_kernel(const __grid_constant_
             }
             if (masked) {
 #pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    const int col = 64 * half + i;
-                    if (col < lo || col >= limit) x[i] = 0.f;
-                }
+                for (int i = 0; i < 32; ++i)
+                    if (c0 + i < lo || c0 + i >= limit) x[i] = 0.f;
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) pk[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-            tmem_st32(ts, pk);
+            for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+            tmem_st16(ts, pk);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(sm.p_full);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sm.p_full);
 
-            if (!warp_wait(sm.dp_full, it & 1u, sm.abort_flag, p.status)) {
-                ok = false;
-                continue;
-            }
+            if (!(ok = warp_wait(sm.dp_full, it & 1u, sm.abort_flag, p.status))) continue;
             tc_fence_after();
-            float d[64];
+            float d[32];
             tmem_ld32_async(tp, reinterpret_cast<uint32_t*>(d));
-            tmem_ld32_async(tp + 32, reinterpret_cast<uint32_t*>(d) + 32);
             tmem_wait_ld();
-            const float4* e4 = reinterpret_cast<const float4*>(rows + 128 + 64 * half);
+            const float4* e4 = reinterpret_cast<const float4*>(rows + 128 + c0);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 const float4 e = e4[i];
                 const float2 a = mul2(make_float2(x[4 * i], x[4 * i + 1]),
                                       add2(make_float2(d[4 * i], d[4 * i + 1]),
@@ -474,66 +451,211 @@ __global__ void __launch_bounds__(384, 1) attn_dkv_kernel(const __grid_constant_
             }
             if (masked) {   // a hidden pair's dP may be anything
 #pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    const int col = 64 * half + i;
-                    if (col < lo || col >= limit) d[i] = 0.f;
-                }
+                for (int i = 0; i < 32; ++i)
+                    if (c0 + i < lo || c0 + i >= limit) d[i] = 0.f;
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) pk[i] = pack_bf16x2(d[2 * i], d[2 * i + 1]);
-            tmem_st32(tp, pk);
+            for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(d[2 * i], d[2 * i + 1]);
+            tmem_st16(tp, pk);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(sm.ds_full);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sm.ds_full);
         }
-        if (ok) ok = warp_wait(sm.acc_full, 0, sm.abort_flag, p.status);
-        tc_fence_after();
-        if (ok) {   // warps 0-3 write dV, warps 4-7 dK
-            const int row = nb * 128 + r;
-            const bool valid = row < len;
-            const int64_t st_t = half ? p.dk_t : p.dv_t;
-            uint16_t* o = (half ? p.dk + kvh * p.dk_h : p.dv + kvh * p.dv_h) +
-                          (start + row - lane) * st_t;
-            const bool bad = store_rows<D>((half ? tmK : tmV) + lane_off, 0, p.D,
-                                           half ? p.scale : 1.0f, o, st_t, len - (row - lane));
-            __syncwarp();   // a row's pieces come from four lanes
-            uint32_t again = __ballot_sync(0xFFFFFFFFu, bad && valid);
-            while (again) {
-                const int s = __ffs(again) - 1;
-                again &= again - 1;
-                dkv_row(p, start, len, __shfl_sync(0xFFFFFFFFu, row, s), kvh, half);
+        if (n) {
+            if (ok) ok = warp_wait(sm.acc_full, 0, sm.abort_flag, p.status);
+            tc_fence_after();
+        }
+        const int row = nb * 128 + r, row0 = row - lane;
+        if (PARTS > 1) {
+            // this part's sums, [dV | dK] column by column, into the ring
+            // (every copy into it has landed, every product has read it)
+            float* sum = reinterpret_cast<float*>(sm.ring) + r;
+            for (int i = quarter; i < 2 * D / 32; i += 4) {
+                uint32_t a[32];
+                if (n) tmem_ld32((i >= D / 32 ? tmK - D : tmV) + lane_off + 32 * i, a);
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    sum[(32 * i + e) * 128] = n ? __uint_as_float(a[e]) : 0.f;
+            }
+            // the parts meet at barriers in shared memory, whose waits have a
+            // limit, unlike the cluster's own barrier
+            __syncwarp();
+            if (lane < PARTS) mbar_arrive_cluster(mapa_shared(smem_u32(sm.sums_there), lane));
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(sm.sums_there, 0, p.status)) && ok;
+            // this CTA's share of the 2 D columns, 32 at a time: the parts'
+            // sums in their order
+            const int first_row = row0;
+            for (int i = quarter; ok && i < 2 * D / 32 / PARTS; i += 4) {
+                const int at0 = (static_cast<int>(part) * (2 * D / 32 / PARTS) + i) * 32;
+                const int which = at0 >= D, col = at0 - which * D;   // of [dV | dK]
+                uint32_t at[PARTS];
+#pragma unroll
+                for (int s = 0; s < PARTS; ++s)
+                    at[s] = mapa_shared(smem_u32(sm.ring) + (at0 * 128 + r) * 4, s);
+                const float f = which ? p.scale : 1.0f;
+                float2 sick = make_float2(0.f, 0.f);
+                uint4 v[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t off = (8 * g + 2 * e) * 512;
+                        float2 x = make_float2(ld_cluster(at[0] + off), ld_cluster(at[0] + off + 512));
+#pragma unroll
+                        for (int s = 1; s < PARTS; ++s)
+                            x = add2(x, make_float2(ld_cluster(at[s] + off),
+                                                    ld_cluster(at[s] + off + 512)));
+                        x = mul2(x, make_float2(f, f));
+                        sick = fma2(x, make_float2(0.f, 0.f), sick);
+                        w[e] = pack_bf16x2(x.x, x.y);
+                    }
+                    v[g] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                const int64_t st_t = which ? p.dk_t : p.dv_t;
+                uint16_t* o = (which ? p.dk + kvh * p.dk_h : p.dv + kvh * p.dv_h) +
+                              (start + first_row) * st_t;
+                store_quad(v, o, st_t, len - first_row, col, p.D);
+                __syncwarp();
+                const bool bad = !(sick.x + sick.y == 0.f);
+                uint32_t again = __ballot_sync(0xFFFFFFFFu, bad && row < len);
+                while (again) {
+                    const int s = __ffs(again) - 1;
+                    again &= again - 1;
+                    dkv_row(p, start, len, first_row + s, kvh, which, col, col + 32);
+                }
+            }
+            // nobody leaves while its sums may still be read
+            __syncwarp();
+            if (lane < PARTS) mbar_arrive_cluster(mapa_shared(smem_u32(sm.sums_read), lane));
+            mbar_wait_cluster(sm.sums_read, 0, p.status, 4 * kWaitTimeoutNs);
+        } else if (ok) {   // 32 columns of [dV | dK] at a time
+            for (int i = quarter; i < 2 * D / 32; i += 4) {
+                const int which = i >= D / 32, col = 32 * i - which * D;
+                const int64_t st_t = which ? p.dk_t : p.dv_t;
+                uint16_t* o = (which ? p.dk + kvh * p.dk_h : p.dv + kvh * p.dv_h) +
+                              (start + row0) * st_t;
+                const bool bad = store_rows((which ? tmK : tmV) + lane_off, col, p.D,
+                                            which ? p.scale : 1.0f, o, st_t, len - row0);
+                __syncwarp();   // a row's pieces come from four lanes
+                uint32_t again = __ballot_sync(0xFFFFFFFFu, bad && row < len);
+                while (again) {
+                    const int s = __ffs(again) - 1;
+                    again &= again - 1;
+                    dkv_row(p, start, len, row0 + s, kvh, which, col, col + 32);
+                }
             }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) tmem_dealloc(tm, 512);
+    if (warp == kMmaWarp) tmem_dealloc(tm, 512);
 }
 
 // ------------------------------------------------------------------ dQ
 
+struct DqWork {
+    int64_t start;
+    int len, block, h, kvh, n;   // n: key blocks
+    __device__ DqWork() {}
+    __device__ DqWork(const BwdParams& p, int item) {
+        const int tile = item / p.units;
+        const int4 te = p.tiles[tile];
+        start = te.x;
+        len = te.y;
+        block = te.z;
+        h = item - tile * p.units;
+        kvh = h / p.group;
+        n = block + 1;
+    }
+};
+
+// D of a block of 128 query rows, D_i = dO_i . (out_i + rest_i): eight lanes a
+// row, 16 bytes a load, all loads of a block under way at once.
 template <int D>
-__global__ void __launch_bounds__(384, 1) attn_dq_kernel(const __grid_constant__ BwdParams p) {
-    using C = BwdCfg<D>;
-    const int tile = blockIdx.x / p.units;
-    if (tile >= p.header[p.list]) return;
-    const int h = blockIdx.x - tile * p.units;
-    const int kvh = h / p.group;
-    const int4 te = p.tiles[tile];
-    const int64_t start = te.x;
-    const int len = te.y;
-    if (te.z < 0) {   // tokens of no sequence
-        zero_rows(p.dq + start * p.dq_t + h * p.dq_h, p.dq_t, p.D, len);
+struct RowDots {
+    uint4 o[2][D / 64], e[2][D / 64], g[2][D / 64];
+    float lse;
+    __device__ void load(const BwdParams& p, const DqWork& w) {
+        const int tid = threadIdx.x;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int row = w.block * 128 + 64 * k + (tid >> 3);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                const int col = ((tid & 7) + 8 * c) * 8;
+                o[k][c] = e[k][c] = g[k][c] = make_uint4(0, 0, 0, 0);
+                if (w.block < 0 || row >= w.len || col >= p.D) continue;
+                const int64_t at = (w.start + row) * p.o_t + w.h * p.o_h + col;
+                o[k][c] = *reinterpret_cast<const uint4*>(p.out + at);
+                e[k][c] = *reinterpret_cast<const uint4*>(p.rest + at);
+                g[k][c] = *reinterpret_cast<const uint4*>(
+                    p.dout + (w.start + row) * p.do_t + w.h * p.do_h + col);
+            }
+        }
+        const int row = w.block * 128 + tid;
+        lse = tid < 128 && w.block >= 0 && row < w.len ? p.lse[w.h * p.T + w.start + row] : 0.f;
+    }
+    // brings the rows into L2, a row a thread
+    __device__ static void prefetch(const BwdParams& p, const DqWork& w) {
+        const int row = w.block * 128 + threadIdx.x;
+        if (threadIdx.x >= 128 || w.block < 0 || row >= w.len) return;
+        const int64_t at = (w.start + row) * p.o_t + w.h * p.o_h;
+        prefetch_l2(p.out + at, p.D * 2);
+        prefetch_l2(p.rest + at, p.D * 2);
+        prefetch_l2(p.dout + (w.start + row) * p.do_t + w.h * p.do_h, p.D * 2);
+    }
+    // D and lse log2 e of the block's rows to rows[0..127], rows[128..255] and,
+    // for the dK, dV kernel, to global memory
+    __device__ void finish(const BwdParams& p, const DqWork& w, float* rows) const {
+        const int tid = threadIdx.x;
+        const int64_t at = w.h * p.T + w.start + w.block * 128;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                const uint32_t ov[4] = {o[k][c].x, o[k][c].y, o[k][c].z, o[k][c].w};
+                const uint32_t ev[4] = {e[k][c].x, e[k][c].y, e[k][c].z, e[k][c].w};
+                const uint32_t gv[4] = {g[k][c].x, g[k][c].y, g[k][c].z, g[k][c].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sum = fma2(bf16x2_f32(gv[i]), add2(bf16x2_f32(ov[i]), bf16x2_f32(ev[i])), sum);
+            }
+            float d = sum.x + sum.y;
+#pragma unroll
+            for (int s = 4; s > 0; s >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, s);
+            const int row = 64 * k + (tid >> 3);
+            if ((tid & 7) == 0) {
+                rows[row] = d;
+                // a first block's is formed from P and dP below
+                if (w.n > 1 && w.block * 128 + row < w.len) p.delta[at + row] = d;
+            }
+        }
+        if (tid < 128) {
+            rows[128 + tid] = lse * kLog2e;
+            if (w.block * 128 + tid < w.len) p.lse2[at + tid] = lse * kLog2e;
+        }
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_constant__ BwdParams p) {
+    // keys stay for dQ, a block longer than values: a ring of its own for each,
+    // or the next values would wait behind them
+    using C = BwdCfg<D, dq_stages(D)>;
+    constexpr uint32_t VS = dq_stages(D) * 2 / 5, KS = dq_stages(D) - VS;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    if (smem_u32(smem_raw) & 1023u) {   // the swizzled tiles' alignment
+        report_error(p.status, MOE_ECUDA);
         return;
     }
-    const int n = te.z + 1;   // key blocks
-
-    extern __shared__ uint8_t smem_raw[];
-    BwdSmem<D> sm(smem_raw);
+    BwdSmem<C> sm(smem_raw);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) sm.init();
-    if (warp == 8) {
+    if (threadIdx.x == 0) sm.init(1);
+    if (warp == kMmaWarp) {
         tmem_alloc(sm.tmem_slot, 512);
         tmem_relinquish();
     }
@@ -541,212 +663,303 @@ __global__ void __launch_bounds__(384, 1) attn_dq_kernel(const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = *sm.tmem_slot;
-    const uint32_t tmP = tm + 256, tmQ = tm + 384;   // S alternates between tm and tm + 128
+    const uint32_t tmP = tm + 128, tmQ = tm + 384;   // S at tm; dP alternates: + 128
+    AttnItems items(p.header[p.list] * p.units);
+    int item;
 
-    if (warp >= 8) {
-        setmaxnreg_dec<88>();
-        if (warp == 9 && lane == 0) {
+    if (warp >= kMmaWarp) {
+        setmaxnreg_dec<64>();
+        if (warp == kLoadWarp && lane == 0) {
             // -------------------------------------------------------- loads
+            tma_prefetch_map(&p.mapQ);
+            tma_prefetch_map(&p.mapK);
+            tma_prefetch_map(&p.mapV);
+            tma_prefetch_map(&p.mapO);
             const uint32_t ar = smem_u32(sm.res), ag = smem_u32(sm.ring);
-            const int tok = static_cast<int>(start);
-            mbar_arrive_expect_tx(sm.res_full, 2 * C::TILE);
-            load_tile<D>(ar, &p.mapQ, sm.res_full, tok + te.z * 128, h);
-            load_tile<D>(ar + C::TILE, &p.mapO, sm.res_full, tok + te.z * 128, h);
-            uint32_t st = 0, ph = 0, armed = 0, par = 0;
+            uint32_t kt = 0, vt = 0, armed = 0, par = 0, done = 0;   // tiles of either ring so far
             bool ok = true;
-            for (int it = 0; it < 2 * n; ++it) {
-                if (!mbar_wait(&sm.empty[st], ph ^ 1u, sm.abort_flag, p.status)) {
-                    ok = false;
+            while (ok && items.next(item)) {
+                const DqWork w(p, item);
+                if (w.block < 0) continue;
+                const int tok = static_cast<int>(w.start);
+                if (done && !(ok = mbar_wait(sm.res_empty, (done - 1) & 1u, sm.abort_flag, p.status)))
                     break;
-                }
-                mbar_arrive_expect_tx(&sm.full[st], C::TILE);
-                armed |= 1u << st;
-                par = (par & ~(1u << st)) | (ph << st);
-                load_tile<D>(ag + st * C::TILE, (it & 1) ? &p.mapV : &p.mapK, &sm.full[st],
-                             tok + (it >> 1) * 128, kvh);
-                if (++st == C::STAGES) {
-                    st = 0;
-                    ph ^= 1u;
+                ++done;
+                mbar_arrive_expect_tx(sm.res_full, 2 * C::TILE);
+                load_tile<D>(ar, &p.mapQ, sm.res_full, tok + w.block * 128, w.h);
+                load_tile<D>(ar + C::TILE, &p.mapO, sm.res_full, tok + w.block * 128, w.h);
+                for (int it = 0; ok && it < 2 * w.n; ++it) {
+                    const bool isv = it & 1;
+                    const uint32_t t = isv ? vt++ : kt++, ring = isv ? VS : KS;
+                    const uint32_t st = t % ring + (isv ? KS : 0), ph = t / ring & 1u;
+                    if (!(ok = mbar_wait(&sm.empty[st], ph ^ 1u, sm.abort_flag, p.status))) break;
+                    mbar_arrive_expect_tx(&sm.full[st], C::TILE);
+                    armed |= 1u << st;
+                    par = (par & ~(1u << st)) | (ph << st);
+                    load_tile<D>(ag + st * C::TILE, isv ? &p.mapV : &p.mapK, &sm.full[st],
+                                 tok + (it >> 1) * 128, w.kvh);
                 }
             }
             if (!ok || *sm.abort_flag) {   // let the armed copies land before leaving
                 volatile int no_abort = 0;
-                mbar_wait(sm.res_full, 0, &no_abort, nullptr, 20000000ull);
+                if (done) mbar_wait(sm.res_full, (done - 1) & 1u, &no_abort, nullptr, 20000000ull);
                 for (int s = 0; s < C::STAGES; ++s)
                     if (armed & (1u << s))
                         mbar_wait(&sm.full[s], (par >> s) & 1u, &no_abort, nullptr, 20000000ull);
             }
-        } else if (warp == 8) {
+        } else if (warp == kMmaWarp) {
             // -------------------------------------------------------- MMAs
             const uint32_t one = elect_lane();
             const uint32_t aQ = smem_u32(sm.res), ag = smem_u32(sm.ring);
             const uint64_t dQ = desc_k(aQ), dO = desc_k(aQ + C::TILE);
-            const auto stage = [](int it) { return static_cast<uint32_t>(it % C::STAGES); };
-            const auto phase = [](int it) { return static_cast<uint32_t>(it / C::STAGES) & 1u; };
-            const auto at = [&](int it) { return ag + stage(it) * C::TILE; };
+            // key blocks whose scores, whose dS have been met, items so far
+            uint32_t cs = 0, cd = 0, done = 0;
             const auto wait = [&](uint64_t* bar, uint32_t parity) {
                 const bool got = warp_wait(bar, parity, sm.abort_flag, p.status);
                 tc_fence_after();
                 return got;
             };
-            bool ok = wait(sm.res_full, 0) && wait(&sm.full[0], 0);
-            if (ok) {
-                mma_scores<D>(one, tm, dQ, desc_k(at(0)));
+            const auto landed = [&](uint32_t t, uint32_t ring, uint32_t from) {
+                return wait(&sm.full[t % ring + from], t / ring & 1u);
+            };
+            const auto tile = [&](uint32_t st) { return ag + st * C::TILE; };
+            // S and dP of the next key block, a block ahead of its dS: S once
+            // the last one has been read, dP into the columns whose dS the
+            // product before last has read
+            const auto scores = [&](bool last) {
+                if (!landed(cs, KS, 0) || (cs && !wait(sm.s_free, (cs - 1) & 1u))) return false;
+                mma_scores<D>(one, tm, dQ, desc_k(tile(cs % KS)));
                 commit(one, sm.s_full);
-                ok = wait(&sm.full[1], 0);
-            }
-            if (ok) {
-                mma_scores<D>(one, tmP, dO, desc_k(at(1)));
-                commit(one, sm.dp_full);
-                commit(one, &sm.empty[1]);
-            }
-            for (int j = 0; ok && j < n; ++j) {
-                const int ik = 2 * j;
-                if (j + 1 < n) {
-                    // into the other S: its last scores were read before dS of
-                    // block j - 1 was written
-                    if (!(ok = wait(&sm.full[stage(ik + 2)], phase(ik + 2)))) break;
-                    mma_scores<D>(one, tm + 128 * ((j + 1) & 1), dQ, desc_k(at(ik + 2)));
-                    commit(one, sm.s_full);
+                if (!landed(cs, VS, KS)) return false;
+                mma_scores<D>(one, tmP + 128 * (cs & 1u), dO, desc_k(tile(cs % VS + KS)));
+                commit(one, &sm.dp_full[cs & 1u]);
+                commit(one, &sm.empty[cs % VS + KS]);
+                if (last) commit(one, sm.res_empty);
+                ++cs;
+                return true;
+            };
+            bool ok = true;
+            while (ok && items.next(item)) {
+                const DqWork w(p, item);
+                if (w.block < 0) continue;
+                if (!(ok = wait(sm.res_full, done++ & 1u) && scores(w.n == 1))) break;
+                for (int j = 0; j < w.n; ++j) {
+                    if (j + 1 < w.n && !(ok = scores(j + 2 == w.n))) break;
+                    if (!(ok = wait(sm.ds_full, cd & 1u))) break;
+                    // the last item's dQ has been read
+                    if (j == 0 && done > 1 && !(ok = wait(sm.acc_empty, done & 1u))) break;
+                    mma_tokens_quarters<D>(one, tmQ, tmP + 128 * (cd & 1u),
+                                           desc_mn(tile(cd % KS)), j > 0);
+                    commit(one, &sm.empty[cd++ % KS]);
                 }
-                if (!(ok = wait(sm.ds_full, j & 1u))) break;
-                mma_tokens<D>(one, tmQ, tmP, desc_mn(at(ik)), 0, j > 0);
-                mma_tokens<D>(one, tmQ, tmP + 64, desc_mn(at(ik)), 1, true);
-                commit(one, &sm.empty[stage(ik)]);
-                if (j + 1 < n) {
-                    if (!(ok = wait(&sm.full[stage(ik + 3)], phase(ik + 3)))) break;
-                    mma_scores<D>(one, tmP, dO, desc_k(at(ik + 3)));
-                    commit(one, sm.dp_full);
-                    commit(one, &sm.empty[stage(ik + 3)]);
-                }
+                if (ok) commit(one, sm.acc_full);
             }
-            if (ok) commit(one, sm.acc_full);
             commit(one, sm.done);
             volatile int no_abort = 0;
             mbar_wait(sm.done, 0, &no_abort, p.status);
         }
     } else {
-        setmaxnreg_inc<208>();
+        setmaxnreg_inc<104>();
         // ------------------------------------------------------------ P and dS
-        // a thread: query row r, key columns [64 half, 64 half + 64)
-        const int half = warp >> 2;
+        // a thread: query row r, key columns [c0, c0 + 32)
+        const int quarter = warp >> 2, c0 = 32 * quarter;
         const int r = threadIdx.x & 127;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t tp = tmP + lane_off + 64 * half;
-        const int row = te.z * 128 + r;
-        const bool valid = row < len;
-        const float lse2 = valid ? p.lse2[h * p.T + start + row] : 0.f;
-        float delta = valid ? p.delta[h * p.T + start + row] : 0.f;
+        const uint32_t ts = tm + lane_off + c0;
         const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
-        const float2 nl = make_float2(-lse2, -lse2);
+        uint32_t blocks = 0, done = 0;   // key blocks and items so far
+        // a warp that has given up (ok false) still meets the others at every
+        // barrier, and does nothing else
         bool ok = true;
-        for (int j = 0; j < n; ++j) {
-            const uint32_t ts = tm + 128 * (j & 1) + lane_off + 64 * half;
-            if (!warp_wait(sm.s_full, j & 1u, sm.abort_flag, p.status)) {
-                ok = false;
-                if (n == 1) named_bar_sync(1, 256);   // given up: meets the others
-                break;
-            }
-            tc_fence_after();
-            float x[64];
-            tmem_ld32_async(ts, reinterpret_cast<uint32_t*>(x));
-            tmem_ld32_async(ts + 32, reinterpret_cast<uint32_t*>(x) + 32);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float2 a = fma2(make_float2(x[2 * i], x[2 * i + 1]), c2, nl);
-                x[2 * i] = exp2_fast(a.x);
-                x[2 * i + 1] = exp2_fast(a.y);
-            }
-            if (!warp_wait(sm.dp_full, j & 1u, sm.abort_flag, p.status)) {
-                ok = false;
-                if (n == 1) named_bar_sync(1, 256);
-                break;
-            }
-            tc_fence_after();
-            float d[64];
-            tmem_ld32_async(tp, reinterpret_cast<uint32_t*>(d));
-            tmem_ld32_async(tp + 32, reinterpret_cast<uint32_t*>(d) + 32);
-            tmem_wait_ld();
-            if (n == 1) {
-                // the first 128 tokens of a sequence: the whole row is here,
-                // so D_i = sum_j P_ij dP_ij without the rounding of P that
-                // O's product carries, which weighs most in short rows (it
-                // falls as 1 / sqrt(row)); the next kernel reads it too
-                float part = 0.f;
-#pragma unroll
-                for (int i = 0; i < 64; ++i)
-                    part += 64 * half + i <= r ? x[i] * d[i] : 0.f;
-                sm.rows[half * 128 + r] = part;
-                named_bar_sync(1, 256);
-                delta = sm.rows[r] + sm.rows[128 + r];
-                if (valid && half == 0) p.delta[h * p.T + start + row] = delta;
-            }
-            const float2 nd = make_float2(-delta, -delta);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float2 a = mul2(make_float2(x[2 * i], x[2 * i + 1]),
-                                      add2(make_float2(d[2 * i], d[2 * i + 1]), nd));
-                d[2 * i] = a.x;
-                d[2 * i + 1] = a.y;
-            }
-            if (j == n - 1) {   // the diagonal block; a hidden pair may hold anything
-#pragma unroll
-                for (int i = 0; i < 64; ++i)
-                    if (64 * half + i > r) d[i] = 0.f;
-            }
-            uint32_t pk[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) pk[i] = pack_bf16x2(d[2 * i], d[2 * i + 1]);
-            tmem_st32(tp, pk);
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(sm.ds_full);
-        }
-        if (ok) ok = warp_wait(sm.acc_full, 0, sm.abort_flag, p.status);
-        tc_fence_after();
+        DqWork w, last;
+        // Rows of the last item that met a value that is not finite.  Written
+        // again only past a barrier: any quarter of a row may have met it, and
+        // the warps of the others have stored theirs then.
         uint32_t again = 0;
-        if (ok) {
-            uint16_t* o = p.dq + (start + row - lane) * p.dq_t + h * p.dq_h;
-            const bool bad = store_rows<D / 2>(tmQ + lane_off, half * (D / 2), p.D, p.scale, o,
-                                               p.dq_t, len - (row - lane));
-            again = __ballot_sync(0xFFFFFFFFu, bad && valid);
+        const auto repair = [&] {
+            while (again) {
+                const int s = __ffs(again) - 1;
+                again &= again - 1;
+                dq_row(p, last.start, last.block * 128 + (r - lane) + s, last.h, last.kvh);
+            }
+        };
+        while (items.next(item)) {
+            w = DqWork(p, item);
+            if (w.block < 0) {   // tokens of no sequence
+                uint16_t* o = p.dq + w.start * p.dq_t + w.h * p.dq_h;
+                for (int i = threadIdx.x; i < w.len * (p.D / 8); i += kFormers)
+                    *reinterpret_cast<uint4*>(o + (i / (p.D / 8)) * p.dq_t + i % (p.D / 8) * 8) =
+                        make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            float* rows = sm.rows + (done & 1u) * 256;
+            {
+                RowDots<D> dots;
+                dots.load(p, w);
+                dots.finish(p, w, rows);
+            }
+            named_bar_sync(1, kFormers);
+            repair();
+            {   // the next item's rows, to be read at its start, into L2
+                AttnItems ahead = items;
+                int then;
+                if (ahead.next(then)) RowDots<D>::prefetch(p, DqWork(p, then));
+            }
+            float delta = rows[r];
+            const float lse2 = rows[128 + r];
+            const int row = w.block * 128 + r, row0 = row - lane, n = w.n;
+            const bool valid = row < w.len;
+            const float2 nl = make_float2(-lse2, -lse2);
+            for (int j = 0; j < n; ++j, ++blocks) {
+                const uint32_t tp = tmP + 128 * (blocks & 1u) + lane_off + c0;
+                if (!(ok = ok && warp_wait(sm.s_full, blocks & 1u, sm.abort_flag, p.status))) {
+                    for (int i = 0; n == 1 && i < 2; ++i) named_bar_sync(1, kFormers);
+                    break;
+                }
+                tc_fence_after();
+                float x[32];
+                tmem_ld32_async(ts, reinterpret_cast<uint32_t*>(x));
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sm.s_free);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 a = fma2(make_float2(x[2 * i], x[2 * i + 1]), c2, nl);
+                    x[2 * i] = exp2_fast(a.x);
+                    x[2 * i + 1] = exp2_fast(a.y);
+                }
+                if (!(ok = warp_wait(&sm.dp_full[blocks & 1u], (blocks >> 1) & 1u, sm.abort_flag,
+                                     p.status))) {
+                    for (int i = 0; n == 1 && i < 2; ++i) named_bar_sync(1, kFormers);
+                    break;
+                }
+                tc_fence_after();
+                float d[32];
+                tmem_ld32_async(tp, reinterpret_cast<uint32_t*>(d));
+                tmem_wait_ld();
+                if (n == 1) {
+                    // the first 128 tokens of a sequence: the whole row is
+                    // here, so D_i = sum_j P_ij dP_ij without the rounding of
+                    // P that O's product carries, which weighs most in short
+                    // rows (it falls as 1 / sqrt(row)); the dK, dV kernel
+                    // reads it too
+                    float part = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) part += c0 + i <= r ? x[i] * d[i] : 0.f;
+                    float* sum = sm.rows + (~done & 1u) * 256;   // the idle buffer
+                    if (quarter < 2) sum[quarter * 128 + r] = part;
+                    named_bar_sync(1, kFormers);
+                    if (quarter >= 2) sum[(quarter - 2) * 128 + r] += part;
+                    named_bar_sync(1, kFormers);
+                    delta = sum[r] + sum[128 + r];
+                    if (valid && quarter == 0) p.delta[w.h * p.T + w.start + row] = delta;
+                }
+                const float2 nd = make_float2(-delta, -delta);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 a = mul2(make_float2(x[2 * i], x[2 * i + 1]),
+                                          add2(make_float2(d[2 * i], d[2 * i + 1]), nd));
+                    d[2 * i] = a.x;
+                    d[2 * i + 1] = a.y;
+                }
+                if (j == n - 1) {   // the diagonal block; a hidden pair may hold anything
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (c0 + i > r) d[i] = 0.f;
+                }
+                uint32_t pk[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(d[2 * i], d[2 * i + 1]);
+                tmem_st16(tp, pk);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sm.ds_full);
+            }
+            ok = ok && warp_wait(sm.acc_full, done & 1u, sm.abort_flag, p.status);
+            ++done;
+            if (ok) {
+                tc_fence_after();
+                uint16_t* o = p.dq + (w.start + row0) * p.dq_t + w.h * p.dq_h;
+                bool bad = false;
+                if (c0 < D)
+                    bad = store_rows(tmQ + lane_off, c0, p.D, p.scale, o, p.dq_t, w.len - row0);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sm.acc_empty);
+                again = __ballot_sync(0xFFFFFFFFu, bad && valid);
+            }
+            last = w;
         }
-        // either half of a row may have met the value: the warps of the other
-        // half have stored theirs before a row is written whole
-        named_bar_sync(1, 256);
-        while (again) {
-            const int s = __ffs(again) - 1;
-            again &= again - 1;
-            dq_row(p, start, __shfl_sync(0xFFFFFFFFu, row, s), h, kvh);
-        }
+        named_bar_sync(1, kFormers);
+        repair();
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) tmem_dealloc(tm, 512);
+    if (warp == kMmaWarp) tmem_dealloc(tm, 512);
+}
+
+template <int D, int PARTS>
+int launch_dkv(const BwdParams& p, int64_t items, cudaStream_t st) {
+    const auto kern = attn_dkv_kernel<D, PARTS>;
+    const int smem = BwdCfg<D, dkv_stages(D)>::SMEM;
+    if (ensure_smem_attr(reinterpret_cast<const void*>(kern), smem)) return MOE_ECUDA;
+    if (items * PARTS >= (1ll << 31)) return MOE_EINVAL;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(items * PARTS), 1, 1);
+    cfg.blockDim = dim3(kBwdThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = PARTS;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return MOE_ECUDA;
+    trace_after(st, "attn_dkv");
+    return MOE_OK;
+}
+
+// CTAs that share a block of keys.  The first keys of a sequence meet every
+// query block of the group's heads, so one CTA would run 2 / (T / 128 + 1) of
+// a head's work alone, against 1 / SMs of all the work for an even share.
+int dkv_parts(int64_t T, int group, int n_kv_heads, int sms) {
+#ifdef DKV_PARTS
+    return DKV_PARTS;
+#endif
+    const int64_t blocks = (T + 127) / 128;
+    const double share = 2.0 * sms / (static_cast<double>(n_kv_heads) * (blocks + 1));
+    int parts = share > 4.0 ? 4 : share > 1.5 ? 2 : 1;
+    while (parts > 1 && group * blocks < 4 * parts) parts /= 2;   // too few to share
+    return parts;
 }
 
 template <int D>
 int launch_pair(BwdParams& p, const AttnPlanLayout& l, const uint8_t* plan, int n_heads,
                 int n_kv_heads, cudaStream_t st) {
-    const int smem = BwdCfg<D>::SMEM;
-    if (ensure_smem_attr(reinterpret_cast<const void*>(attn_dkv_kernel<D>), smem) ||
-        ensure_smem_attr(reinterpret_cast<const void*>(attn_dq_kernel<D>), smem))
-        return MOE_ECUDA;
-    const int64_t gkv = l.max128 * n_kv_heads, gq = l.max128 * n_heads;
+    int dev = 0, sms = 0;
+    if (const int rc = current_device(&dev, &sms)) return rc;
+    const int smem = BwdCfg<D, dq_stages(D)>::SMEM;
+    if (ensure_smem_attr(reinterpret_cast<const void*>(attn_dq_kernel<D>), smem)) return MOE_ECUDA;
+    const int64_t items = l.max128 * n_heads;
+    if (items >= (1ll << 31) - 1024) return MOE_EINVAL;
     p.list = 0;
     p.tiles = reinterpret_cast<const int4*>(plan + l.q128);
     p.units = n_heads;
-    attn_dq_kernel<D><<<static_cast<int>(gq), 384, smem, st>>>(p);
+    attn_dq_kernel<D><<<static_cast<int>(items < sms ? items : sms), kBwdThreads, smem, st>>>(p);
     if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
     trace_after(st, "attn_dq");
     p.list = 1;
     p.tiles = reinterpret_cast<const int4*>(plan + l.kv128);
     p.units = n_kv_heads;
-    attn_dkv_kernel<D><<<static_cast<int>(gkv), 384, smem, st>>>(p);
-    if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
-    trace_after(st, "attn_dkv");
-    return MOE_OK;
+    const int parts = dkv_parts(p.T, p.group, n_kv_heads, sms);
+    const int64_t kv_items = l.max128 * n_kv_heads;
+    return parts == 4   ? launch_dkv<D, 4>(p, kv_items, st)
+           : parts == 2 ? launch_dkv<D, 2>(p, kv_items, st)
+                        : launch_dkv<D, 1>(p, kv_items, st);
 }
 
 }  // namespace
@@ -769,25 +982,11 @@ int launch_attention_bwd(const moe_attention_t& a, const void* plan, const uint1
         attn_tensor_map(&p.mapO, dout, D, a.T, a.n_heads, a.do_t, a.do_h))
         return MOE_ECUDA;
     const AttnPlanLayout l = attn_plan_layout(a.T, a.n_seqs);
-    const int64_t blocks = (a.T * a.n_heads + 31) / 32;
-    if (blocks >= (1ll << 31) || l.max128 * a.n_heads >= (1ll << 31)) return MOE_EINVAL;
-    DeltaParams d;
-    d.T = a.T;
-    d.heads = a.n_heads;
-    d.D = D;
-    d.o_t = a.o_t;
-    d.o_h = a.o_h;
-    d.do_t = a.do_t;
-    d.do_h = a.do_h;
-    d.out = out;
-    d.rest = rest;
-    d.dout = dout;
-    d.lse = lse;
-    d.lse2 = lse2;
-    d.delta = delta;
-    attn_delta_kernel<<<static_cast<int>(blocks), 256, 0, st>>>(d);
-    if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
-    trace_after(st, "attn_delta");
+    p.out = out;
+    p.rest = rest;
+    p.o_t = a.o_t;
+    p.o_h = a.o_h;
+    p.lse = lse;
     const uint8_t* b = static_cast<const uint8_t*>(plan);
     p.header = reinterpret_cast<const int32_t*>(b);
     p.group = a.n_heads / a.n_kv_heads;

@@ -42,7 +42,7 @@ template <int D>
 struct FwdCfg {
     static constexpr int TILE = 128 * D * 2;
     static constexpr int STAGES = D == 128 ? 4 : 8;
-    static constexpr int SMEM = 2 * TILE + STAGES * TILE + 1024 + 4096 + 256;
+    static constexpr int SMEM = 2 * TILE + STAGES * TILE + 4096 + 256;
 };
 
 // One row by the definition on the CUDA cores, for a row whose products met
@@ -107,24 +107,24 @@ struct FwdWork {
     }
 };
 
-// The items of this CTA, heaviest first: dealt out to the CTAs in turn, every
-// other round from the other end, so that a CTA's early heavy item meets a
-// lighter one in the next round.  f(work) for each; false ends the walk.
+// f(work) for each of this CTA's items; false ends the walk.
 template <class F>
 __device__ __forceinline__ void each_item(const FwdParams& p, F f) {
-    const int total = p.header[p.list] * p.units, g = gridDim.x;
-    for (int r = 0; r * g < total; ++r) {
-        const int item = r * g + static_cast<int>((r & 1) ? g - 1 - blockIdx.x : blockIdx.x);
-        if (item < total && !f(FwdWork(p, item))) return;
-    }
+    AttnItems items(p.header[p.list] * p.units);
+    int item;
+    while (items.next(item))
+        if (!f(FwdWork(p, item))) return;
 }
 
 template <int D>
 __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant__ FwdParams p) {
     using C = FwdCfg<D>;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    uint8_t* sQ = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    if (smem_u32(smem_raw) & 1023u) {   // the swizzled tiles' alignment
+        report_error(p.status, MOE_ECUDA);
+        return;
+    }
+    uint8_t* sQ = smem_raw;
     uint8_t* sKV = sQ + 2 * C::TILE;
     float* rows = reinterpret_cast<float*>(sKV + C::STAGES * C::TILE);   // [2][2][256]
     uint64_t* full = reinterpret_cast<uint64_t*>(rows + 1024);
@@ -322,28 +322,32 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
             // backward depends on it
             float m = -INFINITY, l = 0.f, lb = 0.f;
             for (int j = 0; j < n; ++j, ++blocks) {
-                float s[64], top = -INFINITY;
-                ok = ok && warp_wait(&s_full[t], blocks & 1u, abort_flag, p.status);
-                if (ok) {
-                    tc_fence_after();
-                    tmem_ld32_async(ts, reinterpret_cast<uint32_t*>(s));
-                    tmem_ld32_async(ts + 32, reinterpret_cast<uint32_t*>(s) + 32);
-                    tmem_wait_ld();
-                    if (j == n - 1) {   // the diagonal block: keys after the row are hidden
-#pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            if (64 * half + i > r) s[i] = -INFINITY;
+                if (!(ok = ok && warp_wait(&s_full[t], blocks & 1u, abort_flag, p.status))) {
+                    if (named_bar_or(1 + t, 256, j == 0)) {   // meets the others
+                        named_bar_sync(1 + t, 256);
+                        if (j) named_bar_sync(1 + t, 256);
                     }
-                    float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                    for (int i = 4; i < 60; i += 8)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mx[e] = max3(mx[e], s[i + e], s[i + 4 + e]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[60 + e]);
-                    top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    continue;
                 }
+                tc_fence_after();
+                float s[64];
+                tmem_ld32_async(ts, reinterpret_cast<uint32_t*>(s));
+                tmem_ld32_async(ts + 32, reinterpret_cast<uint32_t*>(s) + 32);
+                tmem_wait_ld();
+                if (j == n - 1) {   // the diagonal block: keys after the row are hidden
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        if (64 * half + i > r) s[i] = -INFINITY;
+                }
+                float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int i = 4; i < 60; i += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mx[e] = max3(mx[e], s[i + e], s[i + 4 + e]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[60 + e]);
+                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 // O keeps an older maximum until a row's rises by 2^8: sums in
                 // fp32 hold the larger terms, and rescaling is rare
                 if (named_bar_or(1 + t, 256, j == 0 || top > m + slack)) {
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
                     if (j == 0) {
                         m = top;
                     } else {
-                        ok = ok && warp_wait(&o_full[t], (blocks - 1) & 1u, abort_flag, p.status);
+                        ok = warp_wait(&o_full[t], (blocks - 1) & 1u, abort_flag, p.status);
                         if (ok) {
                             const bool rise = top > m + slack;
                             const float f = rise ? exp2_fast((m - top) * c) : 1.0f;

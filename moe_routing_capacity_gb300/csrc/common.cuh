@@ -388,10 +388,47 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t saddr, uint32_t rank) {
     return out;
 }
 
+// A word of shared memory of the cluster (an address from mapa_shared).
+__device__ __forceinline__ float ld_cluster(uint32_t cluster_addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
 // Every thread of both CTAs (release/acquire at cluster scope).
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
                  ::: "memory");
+}
+
+// One arrival on an mbarrier given by its cluster address, publishing this
+// warp's earlier writes (behind a __syncwarp) to the cluster.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+    asm volatile("fence.acq_rel.cluster;\n\t"
+                 "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+                 : "memory");
+}
+
+// Wait for a phase that CTAs of the cluster complete, with their writes; false
+// (and MOE_ETIMEOUT recorded) after limit_ns.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, int32_t* status,
+                                                  uint64_t limit_ns = kWaitTimeoutNs) {
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (globaltimer_ns() - t0 > limit_ns) {
+            report_error(status, MOE_ETIMEOUT);
+            return false;
+        }
+    }
 }
 
 // One arrival on an mbarrier given by its cluster address (possibly the peer's).

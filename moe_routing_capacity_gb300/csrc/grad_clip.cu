@@ -2,14 +2,14 @@
 //
 //   norm = sqrt(sum g^2),  out = g min(1, max_norm / (norm + 1e-6))
 //
-// Two passes over the data, bound by its bytes.  The tensors' pieces of
-// kChunk elements form one list; a CTA takes every gridDim-th piece.  Pass 1
-// sums squares: fp32 within a thread's share of a piece, 64 bits from there
-// on, one partial a CTA, so the result does not depend on timing.  Pass 2
-// adds the partials in order (each CTA for itself) and scales, walking the
-// list from its end: the pieces that pass 1 read last are still in L2.
-// The tensor records travel as kernel parameters: no copy to the device, and
-// the call can be captured in a graph.
+// Two passes over the data, bound by its bytes.  The tensors' pieces form one
+// list, of which a CTA takes every gridDim-th (neighbouring CTAs read
+// neighbouring memory; a run of pieces for each CTA measured slower).  Pass 1 sums squares: fp32 within a
+// thread's share of a piece, pairs of fp32 and 64 bits from there on, one
+// partial a CTA, so the result does not depend on timing.  Pass 2 adds the
+// partials in order (each CTA for itself) and scales.  The tensor records
+// travel as kernel parameters: no copy to the device, and the call can be
+// captured in a graph.
 #include <cmath>
 #include <cstring>
 
@@ -21,8 +21,11 @@ namespace moe {
 namespace {
 
 constexpr int kClipThreads = 512;
-constexpr int kChunk = 16384;
-constexpr int kMaxCtas = 2 * 160;   // CTAs of a launch, and partials of a batch
+constexpr int kCtasPerSm = 1;
+constexpr int kMaxCtas = kCtasPerSm * 160;   // CTAs of a launch, and partials of a batch
+// elements of a piece: 32 a thread (eight 16-byte loads of fp32 in flight), or
+// 4 (one load) where the larger ones would not reach every SM
+constexpr int kLargePiece = 32 * kClipThreads, kSmallPiece = 4 * kClipThreads;
 
 struct ClipTensor {
     const void* in;
@@ -36,7 +39,7 @@ struct ClipBatch {
     ClipTensor t[N];
     int32_t first[N + 1];
     uint8_t kind[N];       // bit 0: bf16, bit 1: 16-byte aligned in and out
-    int n;
+    int n, piece;
 };
 
 template <int N>
@@ -52,157 +55,219 @@ __device__ __forceinline__ int tensor_of(const ClipBatch<N>& b, int piece) {
     return lo;
 }
 
+// The tensor of `piece`, given an earlier piece's (or -1).
+template <int N>
+__device__ __forceinline__ int next_tensor(const ClipBatch<N>& b, int k, int piece) {
+    if (k < 0) return tensor_of(b, piece);
+    while (piece >= b.first[k + 1]) ++k;
+    return k;
+}
+
 __device__ __forceinline__ float value(const void* p, int64_t i, bool bf) {
     if (bf)
         return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16);
     return static_cast<const float*>(p)[i];
 }
 
-template <int N>
-__global__ void __launch_bounds__(kClipThreads)
-    clip_squares_kernel(const __grid_constant__ ClipBatch<N> b, double* part) {
-    __shared__ double red[kClipThreads / 32];
-    double total = 0.0;
-    const int pieces = b.first[b.n];
-    for (int piece = blockIdx.x; piece < pieces; piece += gridDim.x) {
-        const int k = tensor_of(b, piece);
-        const int64_t at = static_cast<int64_t>(piece - b.first[k]) * kChunk;
-        const int64_t left = b.t[k].numel - at;
-        const int n = left < kChunk ? static_cast<int>(left) : kChunk;
-        const bool bf = b.kind[k] & 1;
-        const void* in = b.t[k].in;
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        if (n == kChunk && (b.kind[k] & 2)) {
-            if (bf) {
-                const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(in) + at);
-                uint4 x[4];
+// The share of a thread in a piece of n elements from `at`: f(x, count, i) for
+// each 16 bytes (4 fp32 or 8 bf16 as x; i the element), or element by element
+// where the tensor is not aligned and for the last elements of a tensor.
+template <int LOADS, bool BF, class F>
+__device__ __forceinline__ void piece_values(const void* in, int64_t at, int n, bool aligned, F f) {
+    constexpr int V = BF ? 8 : 4;
+    const int vecs = aligned ? n / V : 0;
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(in) + at * (BF ? 2 : 4));
+    const auto values = [](const uint4& r, float (&x)[V]) {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = v[threadIdx.x + i * kClipThreads];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        s[i] += bf16_lo(w[e]) * bf16_lo(w[e]);
-                        s[i] += bf16_hi(w[e]) * bf16_hi(w[e]);
-                    }
-                }
+        for (int e = 0; e < 4; ++e) {
+            if (BF) {
+                x[2 * e] = bf16_lo(w[e]);
+                x[(2 * e + 1) % V] = bf16_hi(w[e]);
             } else {
-                const float4* v = reinterpret_cast<const float4*>(static_cast<const float*>(in) + at);
-                float4 x[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = v[threadIdx.x + i * kClipThreads];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    s[0] += x[i].x * x[i].x;
-                    s[1] += x[i].y * x[i].y;
-                    s[2] += x[i].z * x[i].z;
-                    s[3] += x[i].w * x[i].w;
-                }
-            }
-        } else {
-            for (int i = threadIdx.x; i < n; i += kClipThreads) {
-                const float x = value(in, at + i, bf);
-                s[0] += x * x;
+                x[e] = __uint_as_float(w[e]);
             }
         }
-        const float sum = (s[0] + s[1]) + (s[2] + s[3]);
-        if (sum > 1e-20f && sum < 1e30f) {
-            total += sum;
-        } else {
-            // squares near the ends of fp32's range (or all zero): the same
-            // elements' squares again, in 64 bits
-            const int per = (b.kind[k] & 2) && n == kChunk ? (bf ? 8 : 4) : 1;
-            for (int i = threadIdx.x * per; i < n; i += kClipThreads * per)
-                for (int e = 0; e < per; ++e) {
-                    const float x = value(in, at + i + e, bf);
-                    if (x != 0.f) total += static_cast<double>(x) * x;
-                }
-        }
+    };
+    uint4 r[LOADS];
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+        const int k = threadIdx.x + i * kClipThreads;
+        if (k < vecs) r[i] = src[k];
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = total;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < kClipThreads / 32; ++i) total += red[i];
-        part[blockIdx.x] = total;
+    for (int i = 0; i < LOADS; ++i) {
+        const int k = threadIdx.x + i * kClipThreads;
+        if (k < vecs) {
+            float x[V];
+            values(r[i], x);
+            f(x, V, k * V);
+        }
+    }
+    for (int i = vecs * V + threadIdx.x; i < n; i += kClipThreads) {
+        float x[V];
+        x[0] = value(in, at + i, BF);
+        f(x, 1, i);
     }
 }
 
-template <int N>
-__global__ void __launch_bounds__(kClipThreads)
+// A thread's running sum: a pair of fp32 whose sum carries about 48 bits (a
+// 64-bit addition costs 16 cycles a warp here), and 64 bits for what leaves
+// fp32's range.
+struct SquareSum {
+    float hi = 0.f, lo = 0.f;
+    double far = 0.0;
+    __device__ void add(float v) {   // the exact error of hi + v goes to lo
+        const float t = hi + v, b = t - hi;
+        lo += (hi - (t - b)) + (v - b);
+        hi = t;
+    }
+    __device__ double value() const { return far + (static_cast<double>(hi) + lo); }
+};
+
+// The same elements' squares in 64 bits, for a piece of which the first
+// `whole` elements are read 16 bytes a thread.
+template <bool BF>
+__device__ __noinline__ double far_squares(const void* in, int64_t at, int n, int whole) {
+    constexpr int V = BF ? 8 : 4;
+    double sum = 0.0;
+#pragma unroll 1
+    for (int k = threadIdx.x * V; k < whole; k += kClipThreads * V)
+#pragma unroll 1
+        for (int e = 0; e < V; ++e) {
+            const float x = value(in, at + k + e, BF);
+            if (x != 0.f) sum += static_cast<double>(x) * x;   // zeros cost no 64-bit work
+        }
+#pragma unroll 1
+    for (int i = whole + threadIdx.x; i < n; i += kClipThreads) {
+        const float x = value(in, at + i, BF);
+        sum += static_cast<double>(x) * x;
+    }
+    return sum;
+}
+
+// Squares of this thread's share: fp32 within the piece; where their sum
+// nears the ends of fp32's range, the same elements again in 64 bits.
+template <int LOADS, bool BF>
+__device__ __forceinline__ void piece_squares(const void* in, int64_t at, int n, bool aligned,
+                                              SquareSum& total) {
+    constexpr int V = BF ? 8 : 4;
+    float s[V] = {};
+    piece_values<LOADS, BF>(in, at, n, aligned, [&](const float (&x)[V], int count, int) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            if (e < count) s[e] += x[e] * x[e];
+    });
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) sum += s[e];
+    if (sum > 1e-20f && sum < 1e30f) {
+        total.add(sum);
+        return;
+    }
+    total.far += far_squares<BF>(in, at, n, aligned ? n / V * V : 0);
+}
+
+template <int N, int LOADS>
+__global__ void __launch_bounds__(kClipThreads, kCtasPerSm)
+    clip_squares_kernel(const __grid_constant__ ClipBatch<N> b, double* part) {
+    __shared__ double red[kClipThreads];
+    SquareSum total;
+    const int pieces = b.first[b.n];
+    int k = -1;
+    for (int piece = blockIdx.x; piece < pieces; piece += gridDim.x) {
+        k = next_tensor(b, k, piece);
+        const int64_t at = static_cast<int64_t>(piece - b.first[k]) * b.piece;
+        const int64_t left = b.t[k].numel - at;
+        const int n = left < b.piece ? static_cast<int>(left) : b.piece;
+        if (b.kind[k] & 1)
+            piece_squares<(LOADS + 1) / 2, true>(b.t[k].in, at, n, b.kind[k] & 2, total);
+        else
+            piece_squares<LOADS, false>(b.t[k].in, at, n, b.kind[k] & 2, total);
+    }
+    red[threadIdx.x] = total.value();
+    __syncthreads();
+    if (threadIdx.x < 32) {   // one warp's 64-bit additions instead of sixteen's
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < kClipThreads / 32; ++i) sum += red[threadIdx.x + 32 * i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (threadIdx.x == 0) part[blockIdx.x] = sum;
+    }
+}
+
+template <int LOADS, bool BF>
+__device__ __forceinline__ void piece_scale(const void* in, void* out, int64_t at, int n,
+                                            bool aligned, float c) {
+    constexpr int V = BF ? 8 : 4;
+    piece_values<LOADS, BF>(in, at, n, aligned, [&](const float (&x)[V], int count, int i) {
+        if (BF) {
+            uint16_t* o = static_cast<uint16_t*>(out) + at + i;
+            if (count == 1) {
+                *o = __bfloat16_as_ushort(__float2bfloat16_rn(x[0] * c));
+            } else {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(x[2 * e % V] * c, x[(2 * e + 1) % V] * c);
+                __stcs(reinterpret_cast<uint4*>(o), make_uint4(w[0], w[1], w[2], w[3]));
+            }
+        } else {
+            float* o = static_cast<float*>(out) + at + i;
+            if (count == 1)
+                *o = x[0] * c;
+            else
+                __stcs(reinterpret_cast<float4*>(o),
+                       make_float4(x[0] * c, x[1] * c, x[2] * c, x[3] * c));
+        }
+    });
+}
+
+template <int N, int LOADS>
+__global__ void __launch_bounds__(kClipThreads, kCtasPerSm)
     clip_scale_kernel(const __grid_constant__ ClipBatch<N> b, const double* part, int parts,
                       float max_norm, float* norm_out) {
-    __shared__ double red[kClipThreads / 32];
+    __shared__ float scale;
     asm volatile("griddepcontrol.wait;" ::: "memory");   // the partials are complete
-    double total = 0.0;
-    for (int i = threadIdx.x; i < parts; i += kClipThreads) total += part[i];
+    if (threadIdx.x < 32) {
+        double total = 0.0;
+        for (int i = threadIdx.x; i < parts; i += 32) total += part[i];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = total;
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+        if (threadIdx.x == 0) {
+            // the root in fp32 unless the sum leaves its range
+            const bool plain = total > 1e-30 && total < 1e38;
+            const float norm = plain ? sqrtf(static_cast<float>(total))
+                                     : static_cast<float>(sqrt(total));
+            if (norm_out && blockIdx.x == 0) *norm_out = norm;
+            // a norm that is not finite leaves the gradients to the caller
+            const float ratio = max_norm / (norm + 1e-6f);
+            scale = norm <= 3.402823466e38f && ratio < 1.0f ? ratio : 1.0f;
+        }
+    }
     __syncthreads();
-    total = red[0];
-    for (int i = 1; i < kClipThreads / 32; ++i) total += red[i];
-    const double root = sqrt(total);
-    const float norm = static_cast<float>(root);
-    if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
-    // a norm that is not finite leaves the gradients to the caller
-    const bool finite = norm <= 3.402823466e38f;
-    const double ratio = static_cast<double>(max_norm) / (root + 1e-6);
-    const float c = finite && ratio < 1.0 ? static_cast<float>(ratio) : 1.0f;
+    const float c = scale;
     const int pieces = b.first[b.n];
-    for (int piece = pieces - 1 - static_cast<int>(blockIdx.x); piece >= 0; piece -= gridDim.x) {
-        const int k = tensor_of(b, piece);
+    int k = -1;
+    for (int piece = blockIdx.x; piece < pieces; piece += gridDim.x) {
+        k = next_tensor(b, k, piece);
         const void* in = b.t[k].in;
         void* out = b.t[k].out;
         if (c == 1.0f && in == out) continue;
-        const int64_t at = static_cast<int64_t>(piece - b.first[k]) * kChunk;
+        const int64_t at = static_cast<int64_t>(piece - b.first[k]) * b.piece;
         const int64_t left = b.t[k].numel - at;
-        const int n = left < kChunk ? static_cast<int>(left) : kChunk;
-        const bool bf = b.kind[k] & 1;
-        if (n == kChunk && (b.kind[k] & 2)) {
-            if (bf) {
-                const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(in) + at);
-                uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
-                uint4 x[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = v[threadIdx.x + i * kClipThreads];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[e] = pack_bf16x2(bf16_lo(w[e]) * c, bf16_hi(w[e]) * c);
-                    o[threadIdx.x + i * kClipThreads] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            } else {
-                const float4* v = reinterpret_cast<const float4*>(static_cast<const float*>(in) + at);
-                float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-                float4 x[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = v[threadIdx.x + i * kClipThreads];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    o[threadIdx.x + i * kClipThreads] =
-                        make_float4(x[i].x * c, x[i].y * c, x[i].z * c, x[i].w * c);
-            }
-        } else {
-            for (int i = threadIdx.x; i < n; i += kClipThreads) {
-                const float x = value(in, at + i, bf) * c;
-                if (bf)
-                    static_cast<uint16_t*>(out)[at + i] =
-                        __bfloat16_as_ushort(__float2bfloat16_rn(x));
-                else
-                    static_cast<float*>(out)[at + i] = x;
-            }
-        }
+        const int n = left < b.piece ? static_cast<int>(left) : b.piece;
+        if (b.kind[k] & 1)
+            piece_scale<(LOADS + 1) / 2, true>(in, out, at, n, b.kind[k] & 2, c);
+        else
+            piece_scale<LOADS, false>(in, out, at, n, b.kind[k] & 2, c);
     }
 }
 
 template <int N>
-int fill(ClipBatch<N>& b, const moe_grad_tensor_t* t, int64_t n) {
+int fill(ClipBatch<N>& b, const moe_grad_tensor_t* t, int64_t n, int piece) {
     int64_t at = 0;
+    b.piece = piece;
     for (int64_t i = 0; i < n; ++i) {
         const uintptr_t both =
             reinterpret_cast<uintptr_t>(t[i].in) | reinterpret_cast<uintptr_t>(t[i].out);
@@ -211,7 +276,7 @@ int fill(ClipBatch<N>& b, const moe_grad_tensor_t* t, int64_t n) {
         b.t[i].numel = t[i].numel;
         b.kind[i] = static_cast<uint8_t>((t[i].is_bf16 ? 1 : 0) | ((both & 15) == 0 ? 2 : 0));
         b.first[i] = static_cast<int32_t>(at);
-        at += (t[i].numel + kChunk - 1) / kChunk;
+        at += (t[i].numel + piece - 1) / piece;
         if (at >= (1ll << 31) - kMaxCtas) return MOE_EINVAL;
     }
     b.first[n] = static_cast<int32_t>(at);
@@ -220,27 +285,28 @@ int fill(ClipBatch<N>& b, const moe_grad_tensor_t* t, int64_t n) {
 }
 
 int grid_for(int pieces, int sms) {
-    const int most = 2 * (sms < kMaxCtas / 2 ? sms : kMaxCtas / 2);
+    const int most = kCtasPerSm * (sms < 160 ? sms : 160);
     return pieces < most ? (pieces > 0 ? pieces : 1) : most;
 }
 
 // Tensors in batches of N: the squares of every batch, then the scaling.
-template <int N>
+template <int N, int LOADS>
 int run(const moe_grad_tensor_t* t, int64_t n, float max_norm, float* norm, double* part,
         int sms, cudaStream_t st) {
+    constexpr int piece = LOADS == 1 ? kSmallPiece : kLargePiece;
     int parts = 0;
     ClipBatch<N> b;
     for (int64_t i = 0; i < n; i += N) {
-        if (const int rc = fill(b, t + i, n - i < N ? n - i : N)) return rc;
+        if (const int rc = fill(b, t + i, n - i < N ? n - i : N, piece)) return rc;
         const int g = grid_for(b.first[b.n], sms);
-        clip_squares_kernel<N><<<g, kClipThreads, 0, st>>>(b, part + parts);
+        clip_squares_kernel<N, LOADS><<<g, kClipThreads, 0, st>>>(b, part + parts);
         if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
         trace_after(st, "clip_squares");
         parts += g;
     }
     // the last batch first: it was read last (and needs no second fill)
     for (int64_t i = (n - 1) / N * N; i >= 0; i -= N) {
-        if (i + N < n && fill(b, t + i, N)) return MOE_EINVAL;
+        if (i + N < n && fill(b, t + i, N, piece)) return MOE_EINVAL;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(grid_for(b.first[b.n], sms), 1, 1);
         cfg.blockDim = dim3(kClipThreads, 1, 1);
@@ -250,12 +316,23 @@ int run(const moe_grad_tensor_t* t, int64_t n, float max_norm, float* norm, doub
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, clip_scale_kernel<N>, b, static_cast<const double*>(part),
-                               parts, max_norm, i == 0 ? norm : nullptr) != cudaSuccess)
+        if (cudaLaunchKernelEx(&cfg, clip_scale_kernel<N, LOADS>, b,
+                               static_cast<const double*>(part), parts, max_norm,
+                               i == 0 ? norm : nullptr) != cudaSuccess)
             return MOE_ECUDA;
         trace_after(st, "clip_scale");
     }
     return MOE_OK;
+}
+
+template <int N>
+int run_any(const moe_grad_tensor_t* t, int64_t n, float max_norm, float* norm, double* part,
+            int sms, cudaStream_t st) {
+    int64_t elements = 0;
+    for (int64_t i = 0; i < n; ++i) elements += t[i].numel;
+    return elements >= static_cast<int64_t>(kLargePiece) * kCtasPerSm * sms
+               ? run<N, 8>(t, n, max_norm, norm, part, sms, st)
+               : run<N, 1>(t, n, max_norm, norm, part, sms, st);
 }
 
 }  // namespace
@@ -271,8 +348,8 @@ int launch_grad_clip(const moe_grad_tensor_t* tensors, int64_t n, float max_norm
     if (const int rc = current_device(&dev, &sms)) return rc;
     double* part = static_cast<double*>(ws);
     // few records make a small launch; many tensors few launches
-    return n <= 64 ? run<64>(tensors, n, max_norm, norm, part, sms, st)
-                   : run<512>(tensors, n, max_norm, norm, part, sms, st);
+    return n <= 64 ? run_any<64>(tensors, n, max_norm, norm, part, sms, st)
+                   : run_any<512>(tensors, n, max_norm, norm, part, sms, st);
 }
 
 }  // namespace moe

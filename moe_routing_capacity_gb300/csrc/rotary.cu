@@ -63,13 +63,35 @@ __device__ __forceinline__ uint32_t turn_pair(uint32_t w, const float2& c) {
     return pack_bf16x2(x * c.x - y * c.y, y * c.x + x * c.y);
 }
 
+#ifndef ROT_NT
+#define ROT_NT 256
+#endif
+#ifndef ROT_OCC
+#define ROT_OCC 3
+#endif
+#ifndef ROT_UN
+#define ROT_UN 4
+#endif
+#ifndef ROT_WAVES
+#define ROT_WAVES 8
+#endif
 template <bool PAIRS>
-__global__ void __launch_bounds__(256) rotary_kernel(const RotaryParams p) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    const int64_t ts = i / p.units;
-    const int u = static_cast<int>(i - ts * p.units);
-    const int64_t t = ts / p.splits;
-    const int split = static_cast<int>(ts - t * p.splits);
+__global__ void __launch_bounds__(ROT_NT, ROT_OCC) rotary_kernel(const RotaryParams p) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * ROT_NT + threadIdx.x;
+    int64_t t;
+    int u, split;
+    if (p.T * p.units * p.splits < (1ll << 31)) {   // 32-bit divisions where they do
+        const uint32_t ts = static_cast<uint32_t>(i) / p.units;
+        u = static_cast<int>(static_cast<uint32_t>(i) - ts * p.units);
+        const uint32_t t32 = ts / p.splits;
+        split = static_cast<int>(ts - t32 * p.splits);
+        t = t32;
+    } else {
+        const int64_t ts = i / p.units;
+        u = static_cast<int>(i - ts * p.units);
+        t = ts / p.splits;
+        split = static_cast<int>(ts - t * p.splits);
+    }
     if (t >= p.T) return;
     const int64_t pos = p.pos ? p.pos[t] : t;
     if (pos < 0 || pos >= p.table_rows) {
@@ -92,7 +114,7 @@ __global__ void __launch_bounds__(256) rotary_kernel(const RotaryParams p) {
             cs[2 * e + 1] = make_float2(v.z, p.inverse ? -v.w : v.w);
         }
     }
-    constexpr int UNROLL = 4;
+    constexpr int UNROLL = ROT_UN;
     for (int h0 = split; h0 < p.heads; h0 += UNROLL * p.splits) {
         uint4 a[UNROLL], b[UNROLL];
 #pragma unroll
@@ -178,18 +200,18 @@ int launch_rotary(const moe_rotary_t& c, const uint16_t* q, const uint16_t* k, c
     p.pos = pos;
     p.status = status;
     // at least 1024 threads an SM while a thread keeps four heads
-    const int64_t want = static_cast<int64_t>(sms) * 1024;
+    const int64_t want = static_cast<int64_t>(sms) * 768 * ROT_WAVES;
     const int64_t have = c.T * p.units;
     int64_t splits = (want + have - 1) / have;
-    const int most = (p.heads + 3) / 4;
+    const int most = (p.heads + ROT_UN - 1) / ROT_UN;
     if (splits > most) splits = most;
     p.splits = splits < 1 ? 1 : static_cast<int>(splits);
-    const int64_t grid = (c.T * p.splits * p.units + 255) / 256;
+    const int64_t grid = (c.T * p.splits * p.units + ROT_NT - 1) / ROT_NT;
     if (grid >= (1ll << 31)) return MOE_EINVAL;
     if (c.interleaved)
-        rotary_kernel<true><<<static_cast<int>(grid), 256, 0, st>>>(p);
+        rotary_kernel<true><<<static_cast<int>(grid), ROT_NT, 0, st>>>(p);
     else
-        rotary_kernel<false><<<static_cast<int>(grid), 256, 0, st>>>(p);
+        rotary_kernel<false><<<static_cast<int>(grid), ROT_NT, 0, st>>>(p);
     if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
     trace_after(st, "rotary");
     return MOE_OK;
