@@ -395,23 +395,28 @@ __global__ void __launch_bounds__(NT, OCC) norm_bwd_kernel(const NormParams p) {
     }
 }
 
-// The sums over the partial rows in a fixed order (32 columns a CTA, eight
-// threads a column over an eighth of the rows each), and what follows from S.
-__global__ void __launch_bounds__(256) norm_sums_kernel(const NormParams p, int n, float* dw_post,
-                                                        float* dw_pre, float* dgate) {
-    __shared__ float s[8][32];
+// The sums over the partial rows in a fixed order (32 columns a CTA, 32
+// threads a column over a part of the rows each, so that all loads of a thread
+// are under way at once), and what follows from S.
+__global__ void __launch_bounds__(1024) norm_sums_kernel(const NormParams p, int n, float* dw_post,
+                                                         float* dw_pre, float* dgate) {
+    __shared__ float s[32][33];
     const int x = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + x;
     const bool in = col < 2ll * p.d;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the partials are complete
     float v = 0.f;
     if (in)
 #pragma unroll 8
-        for (int i = g; i < n; i += 8) v += p.part[static_cast<int64_t>(i) * 2 * p.d + col];
+        for (int i = g; i < n; i += 32) v += p.part[static_cast<int64_t>(i) * 2 * p.d + col];
     s[g][x] = v;
     __syncthreads();
+    v = sum32(s[x][g]);   // column g of the CTA, its 32 parts in the warp's lanes
+    __syncthreads();
+    if (x == 0) s[0][g] = v;
+    __syncthreads();
     if (g == 0 && in) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i) v += s[i][x];
+        v = s[0][x];
         if (col >= p.d) {
             if (dw_pre) dw_pre[col - p.d] = v;
             return;
@@ -447,7 +452,7 @@ Shape norm_shape(int64_t T, int d, int slots, int sms, bool bwd) {
     const int chunks = d / 8;
     s.rows = chunks <= 32 ? 8 : 1;
     s.per_thread = bwd && chunks > 64 ? 2 : 1;
-    s.threads = chunks <= 32 ? 256 : (chunks / s.per_thread + 31) / 32 * 32;
+    s.threads = chunks <= 32 ? 256 : ((chunks + s.per_thread - 1) / s.per_thread + 31) / 32 * 32;
     s.occ = bwd ? bwd_occ(s.threads) : fwd_occ(s.threads);
     const int stage_bytes = s.threads * s.per_thread * slots * 16;
     while (s.occ > 1 && kRingBytes / s.occ / stage_bytes < 2) --s.occ;
@@ -573,9 +578,19 @@ int launch_norm_residual_backward(const moe_norm_t& c, const uint16_t* dn, const
     const Shape s = norm_shape(c.T, c.d, slots, sms < 160 ? sms : 160, true);
     p.stages = s.stages;
     if (const int rc = launch_any(p, s, c.res_f32, true, st)) return rc;
-    norm_sums_kernel<<<(2 * c.d + 31) / 32, 256, 0, st>>>(
-        p, s.grid, dw_post, dw_pre, p.gate_mode == 1 ? static_cast<float*>(dgate) : nullptr);
-    if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
+    // launched while the rows are still being worked on; it waits for them
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((2 * c.d + 31) / 32, 1, 1);
+    cfg.blockDim = dim3(1024, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, norm_sums_kernel, p, s.grid, dw_post, dw_pre,
+                           p.gate_mode == 1 ? static_cast<float*>(dgate) : nullptr) != cudaSuccess)
+        return MOE_ECUDA;
     trace_after(st, "norm_sums");
     return MOE_OK;
 }

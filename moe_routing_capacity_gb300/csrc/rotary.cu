@@ -63,21 +63,11 @@ __device__ __forceinline__ uint32_t turn_pair(uint32_t w, const float2& c) {
     return pack_bf16x2(x * c.x - y * c.y, y * c.x + x * c.y);
 }
 
-#ifndef ROT_NT
-#define ROT_NT 256
-#endif
-#ifndef ROT_OCC
-#define ROT_OCC 3
-#endif
-#ifndef ROT_UN
-#define ROT_UN 4
-#endif
-#ifndef ROT_WAVES
-#define ROT_WAVES 8
-#endif
+constexpr int kRotThreads = 256;
+constexpr int kRotHeads = 4;     // heads a thread has under way at once
 template <bool PAIRS>
-__global__ void __launch_bounds__(ROT_NT, ROT_OCC) rotary_kernel(const RotaryParams p) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * ROT_NT + threadIdx.x;
+__global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(const RotaryParams p) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kRotThreads + threadIdx.x;
     int64_t t;
     int u, split;
     if (p.T * p.units * p.splits < (1ll << 31)) {   // 32-bit divisions where they do
@@ -114,11 +104,10 @@ __global__ void __launch_bounds__(ROT_NT, ROT_OCC) rotary_kernel(const RotaryPar
             cs[2 * e + 1] = make_float2(v.z, p.inverse ? -v.w : v.w);
         }
     }
-    constexpr int UNROLL = ROT_UN;
-    for (int h0 = split; h0 < p.heads; h0 += UNROLL * p.splits) {
-        uint4 a[UNROLL], b[UNROLL];
+    for (int h0 = split; h0 < p.heads; h0 += kRotHeads * p.splits) {
+        uint4 a[kRotHeads], b[kRotHeads];
 #pragma unroll
-        for (int j = 0; j < UNROLL; ++j) {
+        for (int j = 0; j < kRotHeads; ++j) {
             const int h = h0 + j * p.splits;
             if (h < p.heads) {
                 const uint16_t* s = h < p.hq ? p.q + t * p.q_t + h * p.q_h
@@ -128,7 +117,7 @@ __global__ void __launch_bounds__(ROT_NT, ROT_OCC) rotary_kernel(const RotaryPar
             }
         }
 #pragma unroll
-        for (int j = 0; j < UNROLL; ++j) {
+        for (int j = 0; j < kRotHeads; ++j) {
             const int h = h0 + j * p.splits;
             if (h >= p.heads) continue;
             uint16_t* o = h < p.hq ? p.qo + t * p.qo_t + h * p.qo_h
@@ -199,19 +188,21 @@ int launch_rotary(const moe_rotary_t& c, const uint16_t* q, const uint16_t* k, c
     p.table = table;
     p.pos = pos;
     p.status = status;
-    // at least 1024 threads an SM while a thread keeps four heads
-    const int64_t want = static_cast<int64_t>(sms) * 768 * ROT_WAVES;
+    // eight rounds of resident CTAs while a thread keeps four heads: a short
+    // last round costs little (8192 tokens x 20 heads 20.5 -> 18.5 us against one
+    // round, 65536 x 56 291 -> 282 us)
+    const int64_t want = static_cast<int64_t>(sms) * 3 * kRotThreads * 8;
     const int64_t have = c.T * p.units;
     int64_t splits = (want + have - 1) / have;
-    const int most = (p.heads + ROT_UN - 1) / ROT_UN;
+    const int most = (p.heads + kRotHeads - 1) / kRotHeads;
     if (splits > most) splits = most;
     p.splits = splits < 1 ? 1 : static_cast<int>(splits);
-    const int64_t grid = (c.T * p.splits * p.units + ROT_NT - 1) / ROT_NT;
+    const int64_t grid = (c.T * p.splits * p.units + kRotThreads - 1) / kRotThreads;
     if (grid >= (1ll << 31)) return MOE_EINVAL;
     if (c.interleaved)
-        rotary_kernel<true><<<static_cast<int>(grid), ROT_NT, 0, st>>>(p);
+        rotary_kernel<true><<<static_cast<int>(grid), kRotThreads, 0, st>>>(p);
     else
-        rotary_kernel<false><<<static_cast<int>(grid), ROT_NT, 0, st>>>(p);
+        rotary_kernel<false><<<static_cast<int>(grid), kRotThreads, 0, st>>>(p);
     if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
     trace_after(st, "rotary");
     return MOE_OK;

@@ -554,3 +554,40 @@ def test_grad_clip_zero_and_not_finite(rng):
         for a, b, o in zip(keep, x, outs):
             assert torch.equal(a.view(torch.int16), b.view(torch.int16))
             assert torch.equal(a.isnan(), o.isnan()) and torch.equal(a[~a.isnan()], o[~o.isnan()])
+
+
+def test_norm_and_clip_in_a_graph(rng):
+    """Captured, replayed on new values: as called."""
+    T, d = 70, 2048
+    x = norm_inputs(rng, T, d, "channel", BF)
+    dn, dy = randn(rng, T, d), randn(rng, T, d)
+    st = torch.empty(2, T, device="cuda")
+    y, n, db, dr = (empty(T, d) for _ in range(4))
+    dg, dq, dp = (empty(d, dt=F32) for _ in range(3))
+    ws = torch.empty(abi.norm_residual_workspace(T, d), device="cuda", dtype=torch.uint8)
+    grads = abi.GradSet([dg, dq, dp, db])
+    norm = empty(1, dt=F32)
+
+    def step():
+        abi.norm_residual(x["b"], x["r"], x["gate"], x["w_post"], x["w_pre"], y, n, st[0], st[1])
+        abi.norm_residual_backward(dn, dy, x["b"], x["r"], x["gate"], x["w_post"], x["w_pre"],
+                                   st[0], st[1], db, dr, dg, dq, dp, ws)
+        abi.grad_clip(grads, 0.5, norm)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for t in x.values():
+        t.copy_(t * 0.75)
+    step()
+    want = [t.clone() for t in (y, n, db, dr, dg, dq, dp, norm)]
+    for t in (y, n, db, dr, dg, dq, dp, norm):
+        t.fill_(float("nan"))
+    g.replay()
+    for a, b in zip((y, n, db, dr, dg, dq, dp, norm), want):
+        assert torch.equal(a, b)
