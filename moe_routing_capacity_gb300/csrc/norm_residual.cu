@@ -27,6 +27,7 @@ struct NormParams {
     int64_t T;
     int d, chunks;            // chunks = d / 8
     int stages;               // ring depth
+    bool wide;                // fp32 output on a 32-byte boundary
     float alpha, beta, eps, inv_d;
     const uint16_t *b, *gate, *w_post, *w_pre, *dn;
     const void *r, *dy;
@@ -98,12 +99,21 @@ __device__ __forceinline__ void load_res(const uint4* slot, int pitch, float2 (&
     }
 }
 
+// An fp32 chunk is a whole 32-byte sector: written by one instruction where
+// the tensor starts on such a boundary (wide), or L2 sees two halves.
 template <bool F32>
-__device__ __forceinline__ void store_res(void* base, int64_t at, const float2 (&f)[4]) {
+__device__ __forceinline__ void store_res(void* base, int64_t at, const float2 (&f)[4], bool wide) {
     if (F32) {
-        float4* o = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
-        o[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-        o[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+        float* o = static_cast<float*>(base) + at;
+        if (wide) {
+            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o),
+                         "f"(f[0].x), "f"(f[0].y), "f"(f[1].x), "f"(f[1].y), "f"(f[2].x),
+                         "f"(f[2].y), "f"(f[3].x), "f"(f[3].y)
+                         : "memory");
+        } else {
+            reinterpret_cast<float4*>(o)[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+            reinterpret_cast<float4*>(o)[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+        }
     } else {
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = pack8(f);
     }
@@ -201,7 +211,7 @@ __global__ void __launch_bounds__(NT, OCC) norm_fwd_kernel(const NormParams p) {
                 y[e] = fma2(G[e], mul2(b[e], both(rb)), y[e]);
         }
         if (p.y && in)
-            store_res<F32>(p.y, row * p.d + col, y);
+            store_res<F32>(p.y, row * p.d + col, y, p.wide);
         if (has_n) {
             ss = both(0.f);
 #pragma unroll
@@ -325,7 +335,7 @@ __global__ void __launch_bounds__(NT, OCC) norm_bwd_kernel(const NormParams p) {
                 du[i][e] = fma2(both(ry), fma2(q[i][e], both(-k1), t[i][e]), du[i][e]);
                 o[e] = mul2(du[i][e], both(p.alpha));
             }
-            if (in(i)) store_res<F32>(p.dr, at, o);
+            if (in(i)) store_res<F32>(p.dr, at, o, p.wide);
             if (TOKEN) unpack8(gt[i], g);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -547,6 +557,7 @@ int launch_norm_residual(const moe_norm_t& c, const uint16_t* b, const void* r,
     const int slots = 1 + (p.gate_mode == 2) + (c.res_f32 ? 2 : 1);
     const Shape s = norm_shape(c.T, c.d, slots, sms, false);
     p.stages = s.stages;
+    p.wide = (reinterpret_cast<uintptr_t>(y) & 31) == 0;
     return launch_any(p, s, c.res_f32, false, st);
 }
 
@@ -577,6 +588,7 @@ int launch_norm_residual_backward(const moe_norm_t& c, const uint16_t* dn, const
     const int slots = 2 + (p.gate_mode == 2) + (c.res_f32 ? 4 : 2);
     const Shape s = norm_shape(c.T, c.d, slots, sms < 160 ? sms : 160, true);
     p.stages = s.stages;
+    p.wide = (reinterpret_cast<uintptr_t>(dr) & 31) == 0;
     if (const int rc = launch_any(p, s, c.res_f32, true, st)) return rc;
     // launched while the rows are still being worked on; it waits for them
     cudaLaunchConfig_t cfg = {};
