@@ -85,11 +85,16 @@ __device__ __forceinline__ void wait_stage(int stages) {
         cp_async_wait<3>();
 }
 
-// A residual-stream chunk: one slot of bf16 or two of fp32.
+// A residual-stream chunk: one slot of bf16, or two of fp32.  Of fp32 a thread
+// copies 16 bytes 512 apart of its warp's 1 KB instead of its own 32, so that
+// a warp's copy is whole lines; it reads its own 8 values behind a __syncwarp.
+// `slot` is this thread's place in the first slot, `pitch` the slots' distance.
 template <bool F32>
 __device__ __forceinline__ void load_res(const uint4* slot, int pitch, float2 (&f)[4]) {
     if (F32) {
-        const uint4 a = slot[0], b = slot[pitch];
+        const int wl = threadIdx.x & 31;
+        const uint4* q = slot - wl + (wl >> 4) * pitch + ((2 * wl) & 31);
+        const uint4 a = q[0], b = q[1];
         f[0] = as_float2(a.x, a.y);
         f[1] = as_float2(a.z, a.w);
         f[2] = as_float2(b.x, b.y);
@@ -119,15 +124,17 @@ __device__ __forceinline__ void store_res(void* base, int64_t at, const float2 (
     }
 }
 
+// at: the row's start; col: this thread's first channel.
 template <bool F32>
-__device__ __forceinline__ void copy_res(uint32_t dst, uint32_t pitch, const void* base,
-                                         int64_t at) {
+__device__ __forceinline__ void copy_res(uint32_t dst, uint32_t pitch, const void* base, int64_t at,
+                                         int col, int d) {
     if (F32) {
-        const float* s = static_cast<const float*>(base) + at;
-        cp_async_16(dst, s, 16);
-        cp_async_16(dst + pitch, s + 4, 16);
-    } else {
-        cp_async_16(dst, static_cast<const uint16_t*>(base) + at, 16);
+        const int wl = threadIdx.x & 31, e = col - 4 * wl;   // of the warp's first channel: + 4 wl
+        const float* s = static_cast<const float*>(base) + at + e;
+        if (e < d) cp_async_16(dst, s, 16);
+        if (e + 128 < d) cp_async_16(dst + pitch, s + 128, 16);
+    } else if (col < d) {
+        cp_async_16(dst, static_cast<const uint16_t*>(base) + at + col, 16);
     }
 }
 
@@ -169,11 +176,11 @@ __global__ void __launch_bounds__(NT, OCC) norm_fwd_kernel(const NormParams p) {
         return (stage * SLOTS + k) * nt + static_cast<int>(threadIdx.x);
     };
     const auto fetch = [&](int64_t row, int stage) {
-        if (in && row < p.T) {
-            const int64_t at = row * p.d + col;
-            if (has_b) cp_async_16(smem_u32(ring + slot(stage, 0)), p.b + at, 16);
-            if (TOKEN) cp_async_16(smem_u32(ring + slot(stage, 1)), p.gate + at, 16);
-            copy_res<F32>(smem_u32(ring + slot(stage, 1 + TOKEN)), nt * 16, p.r, at);
+        if (row < p.T) {
+            const int64_t at = row * p.d;
+            if (in && has_b) cp_async_16(smem_u32(ring + slot(stage, 0)), p.b + at + col, 16);
+            if (in && TOKEN) cp_async_16(smem_u32(ring + slot(stage, 1)), p.gate + at + col, 16);
+            copy_res<F32>(smem_u32(ring + slot(stage, 1 + TOKEN)), nt * 16, p.r, at, col, p.d);
         }
         cp_async_commit();
     };
@@ -186,6 +193,7 @@ __global__ void __launch_bounds__(NT, OCC) norm_fwd_kernel(const NormParams p) {
     int stage = 0, par = 0;
     for (int64_t row = row0; row < p.T; row += step) {
         wait_stage(p.stages);
+        if (F32) __syncwarp();   // the other lanes' copies too
         float2 b[4], y[4], ss = both(0.f);
         float2 g[4];
 #pragma unroll
@@ -201,7 +209,8 @@ __global__ void __launch_bounds__(NT, OCC) norm_fwd_kernel(const NormParams p) {
             y[e] = mul2(y[e], both(p.alpha));
             if (TOKEN) b[e] = mul2(b[e], g[e]);
         }
-        fetch(row + p.stages * step, stage);   // this thread has read the slots
+        if (F32) __syncwarp();
+        fetch(row + p.stages * step, stage);   // this thread (fp32: its warp) has read the slots
         if (++stage == p.stages) stage = 0;
         if (has_b) {
             const float rb = rsqrtf(row_sum<WARP>(ss.x + ss.y, red[par]) * p.inv_d + p.eps);
@@ -255,17 +264,20 @@ __global__ void __launch_bounds__(NT, OCC) norm_bwd_kernel(const NormParams p) {
     const auto fetch = [&](int64_t row, int stage) {
 #pragma unroll
         for (int i = 0; i < CH; ++i)
-            if (row < p.T && in(i)) {
-                const int64_t at = row * p.d + (lane + nt * i) * 8;
-                if (has_b) cp_async_16(smem_u32(ring + slot(stage, i, 0)), p.b + at, 16);
-                if (has_n) {
-                    cp_async_16(smem_u32(ring + slot(stage, i, s_dn)), p.dn + at, 16);
-                    copy_res<F32>(smem_u32(ring + slot(stage, i, s_r)), nt * 16, p.r, at);
+            if (row < p.T) {
+                const int col = (lane + nt * i) * 8;
+                const int64_t at = row * p.d;
+                if (in(i)) {
+                    if (has_b) cp_async_16(smem_u32(ring + slot(stage, i, 0)), p.b + at + col, 16);
+                    if (has_n)
+                        cp_async_16(smem_u32(ring + slot(stage, i, s_dn)), p.dn + at + col, 16);
+                    if (TOKEN)
+                        cp_async_16(smem_u32(ring + slot(stage, i, s_gate)), p.gate + at + col, 16);
                 }
-                if (TOKEN)
-                    cp_async_16(smem_u32(ring + slot(stage, i, s_gate)), p.gate + at, 16);
+                if (has_n)
+                    copy_res<F32>(smem_u32(ring + slot(stage, i, s_r)), nt * 16, p.r, at, col, p.d);
                 if (has_y)
-                    copy_res<F32>(smem_u32(ring + slot(stage, i, s_dy)), nt * 16, p.dy, at);
+                    copy_res<F32>(smem_u32(ring + slot(stage, i, s_dy)), nt * 16, p.dy, at, col, p.d);
             }
         cp_async_commit();
     };
@@ -296,6 +308,7 @@ __global__ void __launch_bounds__(NT, OCC) norm_bwd_kernel(const NormParams p) {
     for (int64_t row = row0; row < p.T; row += step) {
         const float rb_next = stat(p.in_post, row + step), ry_next = stat(p.in_pre, row + step);
         wait_stage(p.stages);
+        if (F32) __syncwarp();   // the other lanes' copies too
         // pv: p; du: first dy, then dL/dy, then dL/dp; gt: the token's gate
         float2 pv[CH][4], q[CH][4], t[CH][4], du[CH][4], s1 = both(0.f);
         uint4 gt[CH];
@@ -322,7 +335,8 @@ __global__ void __launch_bounds__(NT, OCC) norm_bwd_kernel(const NormParams p) {
                 s1 = fma2(t[i][e], q[i][e], s1);
             }
         }
-        fetch(row + p.stages * step, stage);   // this thread has read the slots
+        if (F32) __syncwarp();
+        fetch(row + p.stages * step, stage);   // this thread (fp32: its warp) has read the slots
         if (++stage == p.stages) stage = 0;
         const float k1 = has_n ? row_sum<WARP>(s1.x + s1.y, red[par]) * p.inv_d : 0.f;
         float2 s2 = both(0.f);
