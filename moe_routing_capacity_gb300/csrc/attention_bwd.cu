@@ -196,7 +196,7 @@ struct BwdSmem {
         dp_full = s_free + 1;
         p_full = dp_full + 2;
         ds_full = p_full + 1;
-        acc_full = ds_full + 1;
+        acc_full = ds_full + 2;
         acc_empty = acc_full + 1;
         done = acc_empty + 1;
         sums_there = done + 1;
@@ -215,7 +215,8 @@ struct BwdSmem {
         mbar_init(&dp_full[0], 1);   // dQ: one for each dP, since the next one may be
         mbar_init(&dp_full[1], 1);   // ready before this one is looked for
         mbar_init(p_full, 16);
-        mbar_init(ds_full, 16);
+        mbar_init(&ds_full[0], 16);   // likewise
+        mbar_init(&ds_full[1], 16);
         mbar_init(res_empty, 1);
         mbar_init(acc_full, 1);
         mbar_init(acc_empty, 16);
@@ -235,6 +236,12 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
 }
 
 // ------------------------------------------------------------------ dK, dV
+
+// Byte offset of 16-byte piece `q` of row `r` of a part's sums.
+template <int D>
+__device__ __forceinline__ uint32_t sum_at(int r, int q) {
+    return r * (2 * D * 4) + ((q ^ (r & 7)) * 16);
+}
 
 template <int D, int PARTS>
 __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_constant__ BwdParams p) {
@@ -468,15 +475,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
         }
         const int row = nb * 128 + r, row0 = row - lane;
         if (PARTS > 1) {
-            // this part's sums, [dV | dK] column by column, into the ring
-            // (every copy into it has landed, every product has read it)
-            float* sum = reinterpret_cast<float*>(sm.ring) + r;
+            // this part's sums, rows of [dV | dK], into the ring (every copy
+            // into it has landed, every product has read it): 16-byte pieces,
+            // swizzled by the row so that a warp's rows spread over the banks
             for (int i = quarter; i < 2 * D / 32; i += 4) {
                 uint32_t a[32];
                 if (n) tmem_ld32((i >= D / 32 ? tmK - D : tmV) + lane_off + 32 * i, a);
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    sum[(32 * i + e) * 128] = n ? __uint_as_float(a[e]) : 0.f;
+                for (int e = 0; e < 8; ++e)
+                    *reinterpret_cast<uint4*>(sm.ring + sum_at<D>(r, 8 * i + e)) =
+                        n ? make_uint4(a[4 * e], a[4 * e + 1], a[4 * e + 2], a[4 * e + 3])
+                          : make_uint4(0, 0, 0, 0);
             }
             // the parts meet at barriers in shared memory, whose waits have a
             // limit, unlike the cluster's own barrier
@@ -485,45 +494,53 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
             ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(sm.sums_there, 0, p.status)) && ok;
             // this CTA's share of the 2 D columns, 32 at a time: the parts'
             // sums in their order
-            const int first_row = row0;
             for (int i = quarter; ok && i < 2 * D / 32 / PARTS; i += 4) {
                 const int at0 = (static_cast<int>(part) * (2 * D / 32 / PARTS) + i) * 32;
                 const int which = at0 >= D, col = at0 - which * D;   // of [dV | dK]
-                uint32_t at[PARTS];
-#pragma unroll
-                for (int s = 0; s < PARTS; ++s)
-                    at[s] = mapa_shared(smem_u32(sm.ring) + (at0 * 128 + r) * 4, s);
                 const float f = which ? p.scale : 1.0f;
-                float2 sick = make_float2(0.f, 0.f);
-                uint4 v[4];
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t off = (8 * g + 2 * e) * 512;
-                        float2 x = make_float2(ld_cluster(at[0] + off), ld_cluster(at[0] + off + 512));
-#pragma unroll
-                        for (int s = 1; s < PARTS; ++s)
-                            x = add2(x, make_float2(ld_cluster(at[s] + off),
-                                                    ld_cluster(at[s] + off + 512)));
-                        x = mul2(x, make_float2(f, f));
-                        sick = fma2(x, make_float2(0.f, 0.f), sick);
-                        w[e] = pack_bf16x2(x.x, x.y);
-                    }
-                    v[g] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
                 const int64_t st_t = which ? p.dk_t : p.dv_t;
                 uint16_t* o = (which ? p.dk + kvh * p.dk_h : p.dv + kvh * p.dv_h) +
-                              (start + first_row) * st_t;
-                store_quad(v, o, st_t, len - first_row, col, p.D);
-                __syncwarp();
-                const bool bad = !(sick.x + sick.y == 0.f);
-                uint32_t again = __ballot_sync(0xFFFFFFFFu, bad && row < len);
+                              (start + row0) * st_t + col + 4 * (lane & 7);
+                uint32_t again = 0;
+                // eight lanes a row, four rows at a time: whole lines of the
+                // other CTAs' memory (a row a lane measured four times slower)
+#pragma unroll
+                for (int k0 = 0; k0 < 8; k0 += 2) {
+                    float4 x[PARTS][2];
+#pragma unroll
+                    for (int s = 0; s < PARTS; ++s)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            x[s][k] = ld_cluster4(mapa_shared(
+                                smem_u32(sm.ring) + sum_at<D>(32 * (warp & 3) + 4 * (k0 + k) + lane / 8,
+                                                              at0 / 4 + (lane & 7)), s));
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float2 lo = make_float2(x[0][k].x, x[0][k].y);
+                        float2 hi = make_float2(x[0][k].z, x[0][k].w);
+#pragma unroll
+                        for (int s = 1; s < PARTS; ++s) {
+                            lo = add2(lo, make_float2(x[s][k].x, x[s][k].y));
+                            hi = add2(hi, make_float2(x[s][k].z, x[s][k].w));
+                        }
+                        lo = mul2(lo, make_float2(f, f));
+                        hi = mul2(hi, make_float2(f, f));
+                        const int rr = 4 * (k0 + k) + lane / 8;
+                        if (row0 + rr < len && col + 4 * (lane & 7) < p.D)
+                            *reinterpret_cast<uint2*>(o + rr * st_t) =
+                                make_uint2(pack_bf16x2(lo.x, lo.y), pack_bf16x2(hi.x, hi.y));
+                        const float sick = fmaf(lo.x + lo.y, 0.f, (hi.x + hi.y) * 0.f);
+                        const uint32_t b = __ballot_sync(0xFFFFFFFFu, !(sick == 0.f));
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            if (b >> (8 * g) & 0xFFu) again |= 1u << (4 * (k0 + k) + g);
+                    }
+                }
+                __syncwarp();   // a row's pieces come from eight lanes
                 while (again) {
                     const int s = __ffs(again) - 1;
                     again &= again - 1;
-                    dkv_row(p, start, len, first_row + s, kvh, which, col, col + 32);
+                    if (row0 + s < len) dkv_row(p, start, len, row0 + s, kvh, which, col, col + 32);
                 }
             }
             // nobody leaves while its sums may still be read
@@ -745,7 +762,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                 if (!(ok = wait(sm.res_full, done++ & 1u) && scores(w.n == 1))) break;
                 for (int j = 0; j < w.n; ++j) {
                     if (j + 1 < w.n && !(ok = scores(j + 2 == w.n))) break;
-                    if (!(ok = wait(sm.ds_full, cd & 1u))) break;
+                    if (!(ok = wait(&sm.ds_full[cd & 1u], (cd >> 1) & 1u))) break;
                     // the last item's dQ has been read
                     if (j == 0 && done > 1 && !(ok = wait(sm.acc_empty, done & 1u))) break;
                     mma_tokens_quarters<D>(one, tmQ, tmP + 128 * (cd & 1u),
@@ -875,7 +892,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(sm.ds_full);
+                if (lane == 0) mbar_arrive(&sm.ds_full[blocks & 1u]);
             }
             ok = ok && warp_wait(sm.acc_full, done & 1u, sm.abort_flag, p.status);
             ++done;
@@ -927,9 +944,6 @@ int launch_dkv(const BwdParams& p, int64_t items, cudaStream_t st) {
 // query block of the group's heads, so one CTA would run 2 / (T / 128 + 1) of
 // a head's work alone, against 1 / SMs of all the work for an even share.
 int dkv_parts(int64_t T, int group, int n_kv_heads, int sms) {
-#ifdef DKV_PARTS
-    return DKV_PARTS;
-#endif
     const int64_t blocks = (T + 127) / 128;
     const double share = 2.0 * sms / (static_cast<double>(n_kv_heads) * (blocks + 1));
     int parts = share > 4.0 ? 4 : share > 1.5 ? 2 : 1;
