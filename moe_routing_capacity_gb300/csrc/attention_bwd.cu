@@ -135,15 +135,12 @@ __device__ __forceinline__ void zero_rows(uint16_t* base, int64_t st_t, int D, i
             make_uint4(0, 0, 0, 0);
 }
 
-// Columns [c0, c0 + 32) of the warp's 32 accumulator rows, times `f`, as bf16
-// to global memory (base: its first row; rows: how many exist); returns
-// whether a value of this thread's row was not finite.
-__device__ __forceinline__ bool store_rows(uint32_t taddr, int c0, int D, float f, uint16_t* base,
-                                           int64_t stride, int rows) {
+// Columns [c0, c0 + 32) of the warp's 32 accumulator rows, times `f`, as bf16;
+// returns whether a value of this thread's row was not finite.
+__device__ __forceinline__ bool take_rows(uint32_t taddr, int c0, float f, uint4 (&v)[4]) {
     float2 sick = make_float2(0.f, 0.f);   // NaN once a value is not finite
     uint32_t a[32];
     tmem_ld32(taddr + c0, a);
-    uint4 v[4];
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
         uint32_t w[4];
@@ -157,28 +154,32 @@ __device__ __forceinline__ bool store_rows(uint32_t taddr, int c0, int D, float 
         }
         v[g] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    store_quad(v, base, stride, rows, c0, D);
     return !(sick.x + sick.y == 0.f);
 }
 
-// Two resident tiles, a ring of ST streamed ones, the rows' scalars, barriers.
-template <int D, int ST>
+// Two resident tiles, a ring of ST streamed ones, NF of the rows' scalars, barriers.
+template <int D, int ST, int NF>
 struct BwdCfg {
+    static constexpr int SCALARS = NF;
     static constexpr int TILE = 128 * D * 2;
     static constexpr int STAGES = ST;
-    static constexpr int SMEM = 2 * TILE + STAGES * TILE + 2048 + 256;
+    static constexpr int SMEM = 2 * TILE + STAGES * TILE + SCALARS * 4 + 256;
 };
 // Warps 0-15 form P and dS; then the MMA warp, the load warp, two idle ones.
 constexpr int kBwdThreads = 640, kMmaWarp = 16, kLoadWarp = 17, kFormers = 512;
 constexpr int dkv_stages(int D) { return D == 128 ? 4 : 8; }
 constexpr int dq_stages(int D) { return D == 128 ? 5 : 8; }
+template <int D>
+using DkvCfg = BwdCfg<D, dkv_stages(D), 1024>;
+template <int D>
+using DqCfg = BwdCfg<D, dq_stages(D), 512>;
 
 // Shared-memory layout and barriers of both kernels: two resident tiles, a
 // ring of streamed ones.
 template <class C>
 struct BwdSmem {
     uint8_t *res, *ring;
-    float* rows;   // two buffers of 256: scalars of a query block's rows
+    float* rows;   // scalars of query rows: dQ two blocks of 256, dK and dV 64 a warp
     uint64_t *full, *empty, *res_full, *res_empty, *s_full, *s_free, *dp_full, *p_full, *ds_full, *acc_full,
         *acc_empty, *done, *sums_there, *sums_read;
     uint32_t* tmem_slot;
@@ -187,7 +188,7 @@ struct BwdSmem {
         res = raw_ptr;
         ring = res + 2 * C::TILE;
         rows = reinterpret_cast<float*>(ring + C::STAGES * C::TILE);
-        full = reinterpret_cast<uint64_t*>(rows + 512);
+        full = reinterpret_cast<uint64_t*>(rows + C::SCALARS);
         empty = full + C::STAGES;
         res_full = empty + C::STAGES;
         res_empty = res_full + 1;
@@ -237,6 +238,11 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
 
 // ------------------------------------------------------------------ dK, dV
 
+// Bits i and up of 32, for any i.
+__device__ __forceinline__ uint32_t bits_from(int i) {
+    return i >= 32 ? 0u : ~0u << max(i, 0);
+}
+
 // Byte offset of 16-byte piece `q` of row `r` of a part's sums.
 template <int D>
 __device__ __forceinline__ uint32_t sum_at(int r, int q) {
@@ -245,7 +251,7 @@ __device__ __forceinline__ uint32_t sum_at(int r, int q) {
 
 template <int D, int PARTS>
 __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_constant__ BwdParams p) {
-    using C = BwdCfg<D, dkv_stages(D)>;
+    using C = DkvCfg<D>;
     // the CTAs of a cluster share one block of keys: a part of its query
     // blocks each, their sums joined through shared memory at the end
     const uint32_t part = PARTS > 1 ? cluster_ctarank() : 0u;
@@ -385,32 +391,42 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmS + lane_off + c0, tp = tmP + lane_off + c0;
         const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
-        // warps 0-3 and 4-7 bring the query rows' lse2 and D
-        const float* src = quarter == 0 ? p.lse2 : p.delta;
-        const auto fetch = [&](int it) {
-            const int g = (first + it) / per_head, i = (nb + first + it - g * per_head) * 128 + r;
-            return quarter < 2 && i < len ? src[(kvh * p.group + g) * p.T + start + i] : 0.f;
+        // Each warp brings the lse2 and D of its 32 query columns itself, a
+        // block ahead: through a barrier over all sixteen, the first to finish
+        // a block waited for the last (900 of 2490 cycles).
+        float* rows = sm.rows + warp * 64;
+        int qb = nb + first % per_head;
+        int64_t at = (kvh * p.group + first / per_head) * p.T + start + c0 + lane;   // its head's row 0
+        const auto fetch = [&](const float* src) {
+            return qb * 128 + c0 + lane < len ? src[at + qb * 128] : 0.f;
         };
-        float next = n ? fetch(0) : 0.f;
+        float l_next = n ? fetch(p.lse2) : 0.f, d_next = n ? fetch(p.delta) : 0.f;
         bool ok = true;
         for (int it = 0; it < n; ++it) {
-            float* rows = sm.rows + (it & 1) * 256;
-            if (quarter < 2) rows[quarter * 128 + r] = next;
-            named_bar_sync(1, kFormers);
-            if (!ok) continue;   // given up: only meets the others at the barrier
-            if (it + 1 < n) next = fetch(it + 1);
-            const int qb = nb + (first + it) % per_head;
+            __syncwarp();
+            rows[lane] = l_next;
+            rows[32 + lane] = d_next;
+            __syncwarp();
             const int limit = min(128, len - qb * 128);   // query rows in this block
             const bool masked = qb == nb || limit < 128;
-            const int lo = qb == nb ? r : 0;               // columns lo .. limit-1 count
+            // the columns that count: from the diagonal to the last row
+            const uint32_t seen = bits_from((qb == nb ? r : 0) - c0) & ~bits_from(limit - c0);
+            if (++qb == nblk) {
+                qb = nb;
+                at += p.T;
+            }
+            if (it + 1 < n) {
+                l_next = fetch(p.lse2);
+                d_next = fetch(p.delta);
+            }
 
-            if (!(ok = warp_wait(sm.s_full, it & 1u, sm.abort_flag, p.status))) continue;
+            if (!(ok = warp_wait(sm.s_full, it & 1u, sm.abort_flag, p.status))) break;
             tc_fence_after();
             float x[32];
             tmem_ld32_async(ts, reinterpret_cast<uint32_t*>(x));
             tmem_wait_ld();
             uint32_t pk[16];
-            const float4* l4 = reinterpret_cast<const float4*>(rows + c0);
+            const float4* l4 = reinterpret_cast<const float4*>(rows);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float4 l = l4[i];
@@ -426,7 +442,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
             if (masked) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                    if (c0 + i < lo || c0 + i >= limit) x[i] = 0.f;
+                    if (!(seen >> i & 1u)) x[i] = 0.f;
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
@@ -436,12 +452,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
             __syncwarp();
             if (lane == 0) mbar_arrive(sm.p_full);
 
-            if (!(ok = warp_wait(sm.dp_full, it & 1u, sm.abort_flag, p.status))) continue;
+            if (!(ok = warp_wait(sm.dp_full, it & 1u, sm.abort_flag, p.status))) break;
             tc_fence_after();
             float d[32];
             tmem_ld32_async(tp, reinterpret_cast<uint32_t*>(d));
             tmem_wait_ld();
-            const float4* e4 = reinterpret_cast<const float4*>(rows + 128 + c0);
+            const float4* e4 = reinterpret_cast<const float4*>(rows + 32);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float4 e = e4[i];
@@ -459,7 +475,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
             if (masked) {   // a hidden pair's dP may be anything
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                    if (c0 + i < lo || c0 + i >= limit) d[i] = 0.f;
+                    if (!(seen >> i & 1u)) d[i] = 0.f;
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(d[2 * i], d[2 * i + 1]);
@@ -553,8 +569,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                 const int64_t st_t = which ? p.dk_t : p.dv_t;
                 uint16_t* o = (which ? p.dk + kvh * p.dk_h : p.dv + kvh * p.dv_h) +
                               (start + row0) * st_t;
-                const bool bad = store_rows((which ? tmK : tmV) + lane_off, col, p.D,
-                                            which ? p.scale : 1.0f, o, st_t, len - row0);
+                uint4 v[4];
+                const bool bad = take_rows((which ? tmK : tmV) + lane_off, col,
+                                           which ? p.scale : 1.0f, v);
+                store_quad(v, o, st_t, len - row0, col, p.D);
                 __syncwarp();   // a row's pieces come from four lanes
                 uint32_t again = __ballot_sync(0xFFFFFFFFu, bad && row < len);
                 while (again) {
@@ -614,14 +632,16 @@ struct RowDots {
         const int row = w.block * 128 + tid;
         lse = tid < 128 && w.block >= 0 && row < w.len ? p.lse[w.h * p.T + w.start + row] : 0.f;
     }
-    // brings the rows into L2, a row a thread
-    __device__ static void prefetch(const BwdParams& p, const DqWork& w) {
-        const int row = w.block * 128 + threadIdx.x;
-        if (threadIdx.x >= 128 || w.block < 0 || row >= w.len) return;
-        const int64_t at = (w.start + row) * p.o_t + w.h * p.o_h;
-        prefetch_l2(p.out + at, p.D * 2);
-        prefetch_l2(p.rest + at, p.D * 2);
-        prefetch_l2(p.dout + (w.start + row) * p.do_t + w.h * p.do_h, p.D * 2);
+    // brings the rows into L2, by one warp
+    __device__ static void prefetch(const BwdParams& p, const DqWork& w, int lane) {
+        const int rows = w.block < 0 ? 0 : min(128, w.len - w.block * 128);
+        for (int i = lane; i < rows * (D / 64); i += 32) {   // a line of 64 channels
+            const int row = w.block * 128 + i / (D / 64), col = i % (D / 64) * 64;
+            const int64_t at = (w.start + row) * p.o_t + w.h * p.o_h + col;
+            prefetch_l2(p.out + at);
+            prefetch_l2(p.rest + at);
+            prefetch_l2(p.dout + (w.start + row) * p.do_t + w.h * p.do_h + col);
+        }
     }
     // D and lse log2 e of the block's rows to rows[0..127], rows[128..255] and,
     // for the dK, dV kernel, to global memory
@@ -661,7 +681,7 @@ template <int D>
 __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_constant__ BwdParams p) {
     // keys stay for dQ, a block longer than values: a ring of its own for each,
     // or the next values would wait behind them
-    using C = BwdCfg<D, dq_stages(D)>;
+    using C = DqCfg<D>;
     constexpr uint32_t VS = dq_stages(D) * 2 / 5, KS = dq_stages(D) - VS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     if (smem_u32(smem_raw) & 1023u) {   // the swizzled tiles' alignment
@@ -686,38 +706,41 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
 
     if (warp >= kMmaWarp) {
         setmaxnreg_dec<64>();
-        if (warp == kLoadWarp && lane == 0) {
+        if (warp == kLoadWarp) {
             // -------------------------------------------------------- loads
-            tma_prefetch_map(&p.mapQ);
-            tma_prefetch_map(&p.mapK);
-            tma_prefetch_map(&p.mapV);
-            tma_prefetch_map(&p.mapO);
             const uint32_t ar = smem_u32(sm.res), ag = smem_u32(sm.ring);
             uint32_t kt = 0, vt = 0, armed = 0, par = 0, done = 0;   // tiles of either ring so far
-            bool ok = true;
-            while (ok && items.next(item)) {
-                const DqWork w(p, item);
-                if (w.block < 0) continue;
+            const auto issue = [&](const DqWork& w) {   // lane 0
                 const int tok = static_cast<int>(w.start);
-                if (done && !(ok = mbar_wait(sm.res_empty, (done - 1) & 1u, sm.abort_flag, p.status)))
-                    break;
+                if (done && !mbar_wait(sm.res_empty, (done - 1) & 1u, sm.abort_flag, p.status))
+                    return false;
                 ++done;
                 mbar_arrive_expect_tx(sm.res_full, 2 * C::TILE);
                 load_tile<D>(ar, &p.mapQ, sm.res_full, tok + w.block * 128, w.h);
                 load_tile<D>(ar + C::TILE, &p.mapO, sm.res_full, tok + w.block * 128, w.h);
-                for (int it = 0; ok && it < 2 * w.n; ++it) {
+                for (int it = 0; it < 2 * w.n; ++it) {
                     const bool isv = it & 1;
                     const uint32_t t = isv ? vt++ : kt++, ring = isv ? VS : KS;
                     const uint32_t st = t % ring + (isv ? KS : 0), ph = t / ring & 1u;
-                    if (!(ok = mbar_wait(&sm.empty[st], ph ^ 1u, sm.abort_flag, p.status))) break;
+                    if (!mbar_wait(&sm.empty[st], ph ^ 1u, sm.abort_flag, p.status)) return false;
                     mbar_arrive_expect_tx(&sm.full[st], C::TILE);
                     armed |= 1u << st;
                     par = (par & ~(1u << st)) | (ph << st);
                     load_tile<D>(ag + st * C::TILE, isv ? &p.mapV : &p.mapK, &sm.full[st],
                                  tok + (it >> 1) * 128, w.kvh);
                 }
+                return true;
+            };
+            bool ok = true, more = items.next(item);
+            while (ok && more) {
+                const DqWork w(p, item);
+                if (lane == 0 && w.block >= 0) ok = issue(w);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                // this item's last tiles are under way: the next one's rows,
+                // which its D is formed from, into L2
+                if ((more = items.next(item))) RowDots<D>::prefetch(p, DqWork(p, item), lane);
             }
-            if (!ok || *sm.abort_flag) {   // let the armed copies land before leaving
+            if (lane == 0 && (!ok || *sm.abort_flag)) {   // let the armed copies land before leaving
                 volatile int no_abort = 0;
                 if (done) mbar_wait(sm.res_full, (done - 1) & 1u, &no_abort, nullptr, 20000000ull);
                 for (int s = 0; s < C::STAGES; ++s)
@@ -817,11 +840,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
             }
             named_bar_sync(1, kFormers);
             repair();
-            {   // the next item's rows, to be read at its start, into L2
-                AttnItems ahead = items;
-                int then;
-                if (ahead.next(then)) RowDots<D>::prefetch(p, DqWork(p, then));
-            }
             float delta = rows[r];
             const float lse2 = rows[128 + r];
             const int row = w.block * 128 + r, row0 = row - lane, n = w.n;
@@ -881,9 +899,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                     d[2 * i + 1] = a.y;
                 }
                 if (j == n - 1) {   // the diagonal block; a hidden pair may hold anything
+                    const uint32_t hidden = bits_from(r + 1 - c0);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (c0 + i > r) d[i] = 0.f;
+                        if (hidden >> i & 1u) d[i] = 0.f;
                 }
                 uint32_t pk[16];
 #pragma unroll
@@ -898,13 +917,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
             ++done;
             if (ok) {
                 tc_fence_after();
-                uint16_t* o = p.dq + (w.start + row0) * p.dq_t + w.h * p.dq_h;
+                uint4 v[4];
                 bool bad = false;
-                if (c0 < D)
-                    bad = store_rows(tmQ + lane_off, c0, p.D, p.scale, o, p.dq_t, w.len - row0);
+                if (c0 < D) bad = take_rows(tmQ + lane_off, c0, p.scale, v);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sm.acc_empty);
+                if (c0 < D)
+                    store_quad(v, p.dq + (w.start + row0) * p.dq_t + w.h * p.dq_h, p.dq_t,
+                               w.len - row0, c0, p.D);
                 again = __ballot_sync(0xFFFFFFFFu, bad && valid);
             }
             last = w;
@@ -920,7 +941,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
 template <int D, int PARTS>
 int launch_dkv(const BwdParams& p, int64_t items, cudaStream_t st) {
     const auto kern = attn_dkv_kernel<D, PARTS>;
-    const int smem = BwdCfg<D, dkv_stages(D)>::SMEM;
+    const int smem = DkvCfg<D>::SMEM;
     if (ensure_smem_attr(reinterpret_cast<const void*>(kern), smem)) return MOE_ECUDA;
     if (items * PARTS >= (1ll << 31)) return MOE_EINVAL;
     cudaLaunchConfig_t cfg = {};
@@ -956,7 +977,7 @@ int launch_pair(BwdParams& p, const AttnPlanLayout& l, const uint8_t* plan, int 
                 int n_kv_heads, cudaStream_t st) {
     int dev = 0, sms = 0;
     if (const int rc = current_device(&dev, &sms)) return rc;
-    const int smem = BwdCfg<D, dq_stages(D)>::SMEM;
+    const int smem = DqCfg<D>::SMEM;
     if (ensure_smem_attr(reinterpret_cast<const void*>(attn_dq_kernel<D>), smem)) return MOE_ECUDA;
     const int64_t items = l.max128 * n_heads;
     if (items >= (1ll << 31) - 1024) return MOE_EINVAL;
