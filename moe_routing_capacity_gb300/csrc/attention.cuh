@@ -220,6 +220,11 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
 
 // ------------------------------------------------------------------ arithmetic
 
+// Bits i and up of 32, for any i.
+__device__ __forceinline__ uint32_t bits_from(int i) {
+    return i >= 32 ? 0u : ~0u << max(i, 0);
+}
+
 // 2^x (flushing denormal results): the hardware's own exponential.
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;

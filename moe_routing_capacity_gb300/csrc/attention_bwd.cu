@@ -238,11 +238,6 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
 
 // ------------------------------------------------------------------ dK, dV
 
-// Bits i and up of 32, for any i.
-__device__ __forceinline__ uint32_t bits_from(int i) {
-    return i >= 32 ? 0u : ~0u << max(i, 0);
-}
-
 // Byte offset of 16-byte piece `q` of row `r` of a part's sums.
 template <int D>
 __device__ __forceinline__ uint32_t sum_at(int r, int q) {

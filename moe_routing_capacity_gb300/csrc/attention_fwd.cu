@@ -335,9 +335,13 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
                 tmem_ld32_async(ts + 32, reinterpret_cast<uint32_t*>(s) + 32);
                 tmem_wait_ld();
                 if (j == n - 1) {   // the diagonal block: keys after the row are hidden
+                    const uint32_t lo = bits_from(r + 1 - 64 * half);
+                    const uint32_t hi = bits_from(r + 1 - 64 * half - 32);
 #pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (64 * half + i > r) s[i] = -INFINITY;
+                    for (int i = 0; i < 32; ++i) {
+                        if (lo >> i & 1u) s[i] = -INFINITY;
+                        if (hi >> i & 1u) s[32 + i] = -INFINITY;
+                    }
                 }
                 float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
