@@ -150,8 +150,8 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
         mbar_init(q_empty, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
-            mbar_init(&p_full[2 * t], 4);
-            mbar_init(&p_full[2 * t + 1], 4);
+            mbar_init(&p_full[2 * t], 8);
+            mbar_init(&p_full[2 * t + 1], 8);
             mbar_init(&o_full[t], 1);
             mbar_init(&o_empty[t], 8);
         }
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
                         if (!wait(&p_full[2 * t], ps[t] & 1u)) return false;
                         mma_tokens<D>(one, dO, dS, dv, 0, j > 0);
                         if (!wait(&p_full[2 * t + 1], ps[t]++ & 1u)) return false;
-                        mma_tokens<D>(one, dO, dS + 64, dv, 1, true);
+                        mma_tokens<D>(one, dO, dS, dv, 1, true);
                         commit(one, &o_full[t]);
                         if (j + 1 < w.n[t]) {
                             if (!have_k && (sk = next()) == ~0u) return false;
@@ -296,6 +296,9 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
         const uint32_t to = tmO + 128 * t + lane_off + (D / 2) * half;
         float* mine = rows + (2 * t + half) * 256 + r;          // what this half of the
         const float* other = rows + (2 * t + 1 - half) * 256 + r;   // row tells the other
+        // a row is two threads': their warps meet at a barrier of their own, not
+        // all of a tile's
+        const int pair = 1 + 4 * t + (warp & 3);
         const float c = p.scale_log2;
         const float slack = 8.0f / c;   // P may reach 2^8 before O is rescaled
         uint32_t blocks = 0;            // key blocks of this tile so far
@@ -323,10 +326,7 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
             float m = -INFINITY, l = 0.f, lb = 0.f;
             for (int j = 0; j < n; ++j, ++blocks) {
                 if (!(ok = ok && warp_wait(&s_full[t], blocks & 1u, abort_flag, p.status))) {
-                    if (named_bar_or(1 + t, 256, j == 0)) {   // meets the others
-                        named_bar_sync(1 + t, 256);
-                        if (j) named_bar_sync(1 + t, 256);
-                    }
+                    if (named_bar_or(pair, 64, j == 0)) named_bar_sync(pair, 64);   // meets the other
                     continue;
                 }
                 tc_fence_after();
@@ -354,9 +354,9 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
                 float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 // O keeps an older maximum until a row's rises by 2^8: sums in
                 // fp32 hold the larger terms, and rescaling is rare
-                if (named_bar_or(1 + t, 256, j == 0 || top > m + slack)) {
+                if (named_bar_or(pair, 64, j == 0 || top > m + slack)) {
                     *mine = top;
-                    named_bar_sync(1 + t, 256);
+                    named_bar_sync(pair, 64);
                     top = fmaxf(top, *other);
                     if (j == 0) {
                         m = top;
@@ -381,8 +381,6 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
                             tmem_wait_st();
                             tc_fence_before();
                         }
-                        // the product with V may start on the first half's P
-                        named_bar_sync(1 + t, 256);
                     }
                 }
                 if (!ok) continue;
@@ -398,11 +396,13 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
                         pk[e] = pack_bf16x2(s[2 * e], s[2 * e + 1]);
                     }
                     tmem_st16(ts + 16 * i, pk + 16 * i);
+                    // half of either half's keys: their product with V runs
+                    // while the others are formed
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[2 * t + i]);
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
                 // the sums, while the products run
                 float2 sum = make_float2(0.f, 0.f), sumb = sum;
 #pragma unroll
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
             tc_fence_after();
             mine[0] = l;
             mine[128] = lb;
-            named_bar_sync(1 + t, 256);
+            named_bar_sync(pair, 64);
             l += other[0];
             lb += other[128];
             const int row = (t ? w.m0[1] : w.m0[0]) + r;
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
             }
             // both halves of a row are stored before one is written whole
             // again, and the sums' exchange is read before its next use
-            named_bar_sync(1 + t, 256);
+            named_bar_sync(pair, 64);
             while (again) {
                 const int src = __ffs(again) - 1;
                 again &= again - 1;
