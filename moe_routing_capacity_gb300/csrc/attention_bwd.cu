@@ -616,7 +616,7 @@ struct RowDots {
             for (int c = 0; c < D / 64; ++c) {
                 const int col = ((tid & 7) + 8 * c) * 8;
                 o[k][c] = e[k][c] = g[k][c] = make_uint4(0, 0, 0, 0);
-                if (w.block < 0 || row >= w.len || col >= p.D) continue;
+                if (w.block <= 0 || row >= w.len || col >= p.D) continue;   // a first block's: below
                 const int64_t at = (w.start + row) * p.o_t + w.h * p.o_h + col;
                 o[k][c] = *reinterpret_cast<const uint4*>(p.out + at);
                 e[k][c] = *reinterpret_cast<const uint4*>(p.rest + at);
@@ -629,7 +629,7 @@ struct RowDots {
     }
     // brings the rows into L2, by one warp
     __device__ static void prefetch(const BwdParams& p, const DqWork& w, int lane) {
-        const int rows = w.block < 0 ? 0 : min(128, w.len - w.block * 128);
+        const int rows = w.block <= 0 ? 0 : min(128, w.len - w.block * 128);
         for (int i = lane; i < rows * (D / 64); i += 32) {   // a line of 64 channels
             const int row = w.block * 128 + i / (D / 64), col = i % (D / 64) * 64;
             const int64_t at = (w.start + row) * p.o_t + w.h * p.o_h + col;
