@@ -8,9 +8,17 @@
 //   S = Q K^T (tcgen05, fp32 in TMEM); m, l = running maximum and sum;
 //   P = 2^(c S - c m) as bf16 back into S's columns; O += P V (A from TMEM).
 // Warps 0-7 and 8-15 run the softmax of the two tiles, two threads a row
-// (64 keys of a block each); warp 16 issues the MMAs, warp 17 the TMA loads.  While one tile's softmax runs, the
-// tensor cores work on the other's products.  TMEM: two S and two O of 128
-// columns, all 512.
+// (64 keys of a block each); warp 16 issues the MMAs, warp 17 the TMA loads.
+// While one tile's softmax runs, the tensor cores work on the other's products.
+// TMEM: two S and two O of 128 columns, all 512.
+//   16384 tokens in 7 sequences, 48/8 heads of 128 (0.69 TFLOP): 491 us, 1.41
+// PFLOP/s (a library product reaches 1.88).  32768 tokens in one sequence, 8/2
+// heads: 1.28 ms, 1.72 PFLOP/s; run for seconds both are held back by the power
+// limit (534 us, 1.40 ms).  What bounds it: S waits for the product that reads P
+// from its columns, so a tile's softmax (about 1800 cycles) and its products
+// (1024) follow each other and two tiles do not fill the tensor cores; beside
+// that Q and K from shared memory take its whole bandwidth while S is formed,
+// and a piece of work starts and ends with 5000 cycles without products.
 #include <cstring>
 
 #include "attention.cuh"
@@ -633,6 +641,10 @@ int launch_attention_fwd(const moe_attention_t& a, const void* plan, const uint1
     const AttnPlanLayout l = attn_plan_layout(a.T, a.n_seqs);
     const uint8_t* b = static_cast<const uint8_t*>(plan);
     p.group = a.n_heads / a.n_kv_heads;
+    // Two heads of an even group read the same keys in the same blocks; of an odd
+    // group, two blocks of rows, of which the second meets a block more.  Rows
+    // instead of heads at 48/8 heads: 516 us against 493 (16384 tokens), at 16/4
+    // 86 against 84 (8192 tokens), 14.3 against 16.4 (301 tokens).
     p.pair_heads = p.group % 2 == 0;
     p.header = reinterpret_cast<const int32_t*>(b);
     p.list = p.pair_heads ? 0 : 2;

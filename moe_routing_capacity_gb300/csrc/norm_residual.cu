@@ -14,6 +14,10 @@
 // The backward's sums over tokens (dw_post, dw_pre, dgate) stay in registers
 // over all of a CTA's rows; each CTA writes one partial row and a second
 // kernel adds the partials in their order: no atomics.
+//   16384 rows of 6144 in bf16: forward 121 us (6.65 TB/s; a copy reaches 6.78),
+// backward 182 us (6.64 TB/s).  8191 rows of 2048, fp32 stream and a gate a
+// token, backward: 67 us (5.5 TB/s; 5 us of them are the sums over tokens).
+// One row of 2048: 2.4 us on the device.
 #include <cstring>
 
 #include "common.cuh"
