@@ -167,18 +167,17 @@ __device__ __forceinline__ void mma_scores(uint32_t leader, uint32_t d_tmem, uin
     }
 }
 
-// acc[tmem] (+)= A B over tokens 32 part .. + 31 and 64 + 32 part .. + 31: A
-// bf16, 64 tokens in 32 columns and the other 64 in 32 columns 64 further on,
-// B a tile read MN-major.
+// acc[tmem] (+)= A B over tokens 64 half .. 64 half + 63: A bf16, two tokens a
+// column, B a tile read MN-major.
 template <int D>
 __device__ __forceinline__ void mma_tokens(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem,
-                                           uint64_t b, int part, bool accumulate) {
+                                           uint64_t b, int half, bool accumulate) {
     constexpr uint32_t idesc = idesc_bf16_f32(128, D, false, true);
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
-        const int k16 = 4 * (kk / 2) + 2 * part + kk % 2;   // sixteen tokens
-        mma_ts(leader, d_tmem, a_tmem + 64 * (kk / 2) + 16 * part + 8 * (kk % 2),
-               b + ((k16 * 2048) >> 4), idesc, accumulate || kk > 0);
+        const int k16 = 4 * half + kk;   // sixteen tokens
+        mma_ts(leader, d_tmem, a_tmem + 8 * k16, b + ((k16 * 2048) >> 4), idesc,
+               accumulate || kk > 0);
     }
 }
 

@@ -7,13 +7,14 @@
 // the group is odd), over the sequence's key blocks of 128:
 //   S = Q K^T (tcgen05, fp32 in TMEM); m, l = running maximum and sum;
 //   P = 2^(c S - c m) as bf16 back into S's columns; O += P V (A from TMEM).
-// Warps 0-7 and 8-15 run the softmax of the two tiles, two threads a row
-// (64 keys of a block each); warp 16 issues the MMAs, warp 17 the TMA loads.
+// Warps 0-3 and 4-7 run the softmax of the two tiles, a thread a row, so that
+// no two threads have to meet (two threads a row: 491 us against 479 below);
+// warp 8 issues the MMAs, warp 9 the TMA loads.
 // While one tile's softmax runs, the tensor cores work on the other's products.
 // TMEM: two S and two O of 128 columns, all 512.
-//   16384 tokens in 7 sequences, 48/8 heads of 128 (0.69 TFLOP): 491 us, 1.41
+//   16384 tokens in 7 sequences, 48/8 heads of 128 (0.69 TFLOP): 479 us, 1.45
 // PFLOP/s (a library product reaches 1.88).  32768 tokens in one sequence, 8/2
-// heads: 1.28 ms, 1.72 PFLOP/s; run for seconds both are held back by the power
+// heads: 1.24 ms, 1.77 PFLOP/s; run for seconds both are held back by the power
 // limit (534 us, 1.40 ms).  What bounds it: S waits for the product that reads P
 // from its columns, so a tile's softmax (about 1800 cycles) and its products
 // (1024) follow each other and two tiles do not fill the tensor cores; beside
@@ -46,11 +47,15 @@ struct FwdParams {
     int32_t* status;
 };
 
+// Warps 0-3 and 4-7 the softmax of the two tiles, a thread a row; then the MMA
+// warp, the load warp, two idle ones.
+constexpr int kFwdThreads = 384, kFwdMmaWarp = 8, kFwdLoadWarp = 9;
+
 template <int D>
 struct FwdCfg {
     static constexpr int TILE = 128 * D * 2;
     static constexpr int STAGES = D == 128 ? 4 : 8;
-    static constexpr int SMEM = 2 * TILE + STAGES * TILE + 4096 + 256;
+    static constexpr int SMEM = 2 * TILE + STAGES * TILE + 256;
 };
 
 // One row by the definition on the CUDA cores, for a row whose products met
@@ -125,7 +130,7 @@ __device__ __forceinline__ void each_item(const FwdParams& p, F f) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant__ FwdParams p) {
+__global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_constant__ FwdParams p) {
     using C = FwdCfg<D>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     if (smem_u32(smem_raw) & 1023u) {   // the swizzled tiles' alignment
@@ -134,8 +139,7 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
     }
     uint8_t* sQ = smem_raw;
     uint8_t* sKV = sQ + 2 * C::TILE;
-    float* rows = reinterpret_cast<float*>(sKV + C::STAGES * C::TILE);   // [2][2][256]
-    uint64_t* full = reinterpret_cast<uint64_t*>(rows + 1024);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sKV + C::STAGES * C::TILE);
     uint64_t* empty = full + C::STAGES;
     uint64_t* q_full = empty + C::STAGES;
     uint64_t* q_empty = q_full + 1;
@@ -158,16 +162,16 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
         mbar_init(q_empty, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
-            mbar_init(&p_full[2 * t], 8);
-            mbar_init(&p_full[2 * t + 1], 8);
+            mbar_init(&p_full[2 * t], 4);   // one arrival a warp
+            mbar_init(&p_full[2 * t + 1], 4);
             mbar_init(&o_full[t], 1);
-            mbar_init(&o_empty[t], 8);
+            mbar_init(&o_empty[t], 4);
         }
         mbar_init(done, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 16) {
+    if (warp == kFwdMmaWarp) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
@@ -177,9 +181,9 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
     const uint32_t tm = *tmem_slot;
     const uint32_t tmS = tm, tmO = tm + 256;   // tile t: + 128 t
 
-    if (warp >= 16) {
+    if (warp >= kFwdMmaWarp) {
         setmaxnreg_dec<64>();
-        if (warp == 17 && lane == 0) {
+        if (warp == kFwdLoadWarp && lane == 0) {
             // -------------------------------------------------------- loads
             tma_prefetch_map(&p.mapQ);
             tma_prefetch_map(&p.mapK);
@@ -222,7 +226,7 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
                     if (armed & (1u << s))
                         mbar_wait(&full[s], (par >> s) & 1u, &no_abort, nullptr, 20000000ull);
             }
-        } else if (warp == 16) {
+        } else if (warp == kFwdMmaWarp) {
             // -------------------------------------------------------- MMAs
             const uint32_t one = elect_lane();
             const uint32_t aq = smem_u32(sQ), akv = smem_u32(sKV);
@@ -294,36 +298,27 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
             mbar_wait(done, 0, &no_abort, p.status);
         }
     } else {
-        setmaxnreg_inc<104>();
+        setmaxnreg_inc<216>();
         // ------------------------------------------------------------ softmax
-        // a thread: row r of tile t, key columns [64 half, 64 half + 64)
-        const int t = warp >> 3, half = (warp >> 2) & 1;
+        // a thread: row r of tile t
+        const int t = warp >> 2;
         const int r = threadIdx.x & 127;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t ts = tmS + 128 * t + lane_off + 64 * half;
-        const uint32_t to = tmO + 128 * t + lane_off + (D / 2) * half;
-        float* mine = rows + (2 * t + half) * 256 + r;          // what this half of the
-        const float* other = rows + (2 * t + 1 - half) * 256 + r;   // row tells the other
-        // a row is two threads': their warps meet at a barrier of their own, not
-        // all of a tile's
-        const int pair = 1 + 4 * t + (warp & 3);
+        const uint32_t ts = tmS + 128 * t + lane_off, to = tmO + 128 * t + lane_off;
         const float c = p.scale_log2;
         const float slack = 8.0f / c;   // P may reach 2^8 before O is rescaled
         uint32_t blocks = 0;            // key blocks of this tile so far
-        // a warp that has given up (ok false) still meets the others at every
-        // barrier of the tile, and does nothing else
         bool ok = true;
         each_item(p, [&](const FwdWork& w) {
             const int h = t ? w.h[1] : w.h[0], n = t ? w.n[1] : w.n[0];
             if (w.block < 0) {   // tokens of no sequence
                 if (t && !p.pair_heads) return true;
-                for (int i = r + 128 * half; i < w.len * (p.D / 8); i += 256) {
+                for (int i = r; i < w.len * (p.D / 8); i += 128) {
                     const int64_t o = (w.start + i / (p.D / 8)) * p.o_t + h * p.o_h + i % (p.D / 8) * 8;
                     *reinterpret_cast<uint4*>(p.out + o) = make_uint4(0, 0, 0, 0);
                     if (p.rest) *reinterpret_cast<uint4*>(p.rest + o) = make_uint4(0, 0, 0, 0);
                 }
-                for (int i = r + 128 * half; i < w.len; i += 256)
-                    p.lse[h * p.T + w.start + i] = -INFINITY;
+                for (int i = r; i < w.len; i += 128) p.lse[h * p.T + w.start + i] = -INFINITY;
                 return true;
             }
             if (!n) return true;
@@ -333,162 +328,145 @@ __global__ void __launch_bounds__(640, 1) attn_fwd_kernel(const __grid_constant_
             // backward depends on it
             float m = -INFINITY, l = 0.f, lb = 0.f;
             for (int j = 0; j < n; ++j, ++blocks) {
-                if (!(ok = ok && warp_wait(&s_full[t], blocks & 1u, abort_flag, p.status))) {
-                    if (named_bar_or(pair, 64, j == 0)) named_bar_sync(pair, 64);   // meets the other
-                    continue;
-                }
+                if (!(ok = warp_wait(&s_full[t], blocks & 1u, abort_flag, p.status))) return false;
                 tc_fence_after();
-                float s[64];
-                tmem_ld32_async(ts, reinterpret_cast<uint32_t*>(s));
-                tmem_ld32_async(ts + 32, reinterpret_cast<uint32_t*>(s) + 32);
+                float s[128];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tmem_ld32_async(ts + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
                 tmem_wait_ld();
                 if (j == n - 1) {   // the diagonal block: keys after the row are hidden
-                    const uint32_t lo = bits_from(r + 1 - 64 * half);
-                    const uint32_t hi = bits_from(r + 1 - 64 * half - 32);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        if (lo >> i & 1u) s[i] = -INFINITY;
-                        if (hi >> i & 1u) s[32 + i] = -INFINITY;
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t hidden = bits_from(r + 1 - 32 * i);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (hidden >> e & 1u) s[32 * i + e] = -INFINITY;
                     }
                 }
-                float mx[4] = {s[0], s[1], s[2], s[3]};
+                float mx[8];
 #pragma unroll
-                for (int i = 4; i < 60; i += 8)
+                for (int e = 0; e < 8; ++e) mx[e] = max3(s[e], s[8 + e], s[16 + e]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mx[e] = max3(mx[e], s[i + e], s[i + 4 + e]);
+                for (int i = 24; i < 120; i += 16)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[60 + e]);
-                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    for (int e = 0; e < 8; ++e) mx[e] = max3(mx[e], s[i + e], s[i + 8 + e]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) mx[e] = fmaxf(mx[e], s[120 + e]);
+                const float top = fmaxf(max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[4]),
+                                        max3(mx[5], mx[6], mx[7]));
                 // O keeps an older maximum until a row's rises by 2^8: sums in
                 // fp32 hold the larger terms, and rescaling is rare
-                if (named_bar_or(pair, 64, j == 0 || top > m + slack)) {
-                    *mine = top;
-                    named_bar_sync(pair, 64);
-                    top = fmaxf(top, *other);
-                    if (j == 0) {
-                        m = top;
-                    } else {
-                        ok = warp_wait(&o_full[t], (blocks - 1) & 1u, abort_flag, p.status);
-                        if (ok) {
-                            const bool rise = top > m + slack;
-                            const float f = rise ? exp2_fast((m - top) * c) : 1.0f;
-                            if (rise) m = top;
-                            l *= f;
-                            lb *= f;
-                            tc_fence_after();
+                const bool rise = top > m + slack;
+                if (j == 0) {
+                    m = top;
+                } else if (__any_sync(0xFFFFFFFFu, rise)) {
+                    if (!(ok = warp_wait(&o_full[t], (blocks - 1) & 1u, abort_flag, p.status)))
+                        return false;
+                    const float f = rise ? exp2_fast((m - top) * c) : 1.0f;
+                    if (rise) m = top;
+                    l *= f;
+                    lb *= f;
+                    tc_fence_after();
 #pragma unroll 1
-                            for (int i = 0; i < D / 32; ++i) {
-                                uint32_t o[16];
-                                tmem_ld16(to + 16 * i, o);
+                    for (int i = 0; i < D / 16; ++i) {
+                        uint32_t o[16];
+                        tmem_ld16(to + 16 * i, o);
 #pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st16(to + 16 * i, o);
-                            }
-                            tmem_wait_st();
-                            tc_fence_before();
-                        }
+                        for (int e = 0; e < 16; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st16(to + 16 * i, o);
                     }
+                    tmem_wait_st();
+                    tc_fence_before();
                 }
-                if (!ok) continue;
                 const float2 c2 = make_float2(c, c), neg = make_float2(-m * c, -m * c);
-                uint32_t pk[32];
+                // half the keys: their product with V runs while the others
+                // are formed
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int half = 0; half < 2; ++half) {
+                    float* x = s + 64 * half;
+                    uint32_t pk[32];
 #pragma unroll
-                    for (int e = 16 * i; e < 16 * i + 16; ++e) {
-                        const float2 x = fma2(make_float2(s[2 * e], s[2 * e + 1]), c2, neg);
-                        s[2 * e] = exp2_fast(x.x);
-                        s[2 * e + 1] = exp2_fast(x.y);
-                        pk[e] = pack_bf16x2(s[2 * e], s[2 * e + 1]);
+                    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                        for (int e = 16 * i; e < 16 * i + 16; ++e) {
+                            const float2 v = fma2(make_float2(x[2 * e], x[2 * e + 1]), c2, neg);
+                            x[2 * e] = exp2_fast(v.x);
+                            x[2 * e + 1] = exp2_fast(v.y);
+                            pk[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+                        }
+                        tmem_st16(ts + 32 * half + 16 * i, pk + 16 * i);
                     }
-                    tmem_st16(ts + 16 * i, pk + 16 * i);
-                    // half of either half's keys: their product with V runs
-                    // while the others are formed
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[2 * t + i]);
-                }
-                // the sums, while the products run
-                float2 sum = make_float2(0.f, 0.f), sumb = sum;
+                    if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
+                    // the sums, while the products run
+                    float2 sum = make_float2(0.f, 0.f), sumb = sum;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    sum = add2(sum, make_float2(s[2 * e], s[2 * e + 1]));
-                    sumb = add2(sumb, bf16x2_f32(pk[e]));
+                    for (int e = 0; e < 32; ++e) {
+                        sum = add2(sum, make_float2(x[2 * e], x[2 * e + 1]));
+                        sumb = add2(sumb, bf16x2_f32(pk[e]));
+                    }
+                    l += sum.x + sum.y;
+                    lb += sumb.x + sumb.y;
                 }
-                l += sum.x + sum.y;
-                lb += sumb.x + sumb.y;
             }
             // ------------------------------------------------------------ output
-            ok = ok && warp_wait(&o_full[t], (blocks - 1) & 1u, abort_flag, p.status);
+            if (!(ok = warp_wait(&o_full[t], (blocks - 1) & 1u, abort_flag, p.status))) return false;
             tc_fence_after();
-            mine[0] = l;
-            mine[128] = lb;
-            named_bar_sync(pair, 64);
-            l += other[0];
-            lb += other[128];
-            const int row = (t ? w.m0[1] : w.m0[0]) + r;
+            const int row = (t ? w.m0[1] : w.m0[0]) + r, row0 = row - lane;
             const bool valid = row < w.len;
             const float inv = 1.0f / lb;
             const float lse = m * p.scale + logf(l);
-            uint32_t again = 0;
-            if (ok) {
-                const int row0 = row - lane;          // the warp's first row
-                const int64_t o = (w.start + row0) * p.o_t + h * p.o_h;
-                float2 sick = make_float2(0.f, 0.f);  // NaN once a value is not finite
+            const int64_t o = (w.start + row0) * p.o_t + h * p.o_h;
+            float2 sick = make_float2(0.f, 0.f);  // NaN once a value is not finite
 #pragma unroll
-                for (int i = 0; i < D / 64; ++i) {
-                    uint32_t a[32];
-                    tmem_ld32(to + 32 * i, a);
-                    if (i == D / 64 - 1) {   // O may be overwritten from here on
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&o_empty[t]);
-                    }
-                    uint32_t hi[16], lo[16];
+            for (int i = 0; i < D / 32; ++i) {
+                uint32_t a[32];
+                tmem_ld32(to + 32 * i, a);
+                if (i == D / 32 - 1) {   // O may be overwritten from here on
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&o_empty[t]);
+                }
+                uint32_t hi[16], lo[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 x = mul2(make_float2(__uint_as_float(a[2 * e]),
-                                                          __uint_as_float(a[2 * e + 1])),
-                                              make_float2(inv, inv));
-                        sick = fma2(x, make_float2(0.f, 0.f), sick);
-                        hi[e] = pack_bf16x2(x.x, x.y);
-                        lo[e] = pack_bf16x2(x.x - bf16_lo(hi[e]), x.y - bf16_hi(hi[e]));
-                    }
-                    const int col = (D / 2) * half + 32 * i;
-                    uint4 v[4];
+                for (int e = 0; e < 16; ++e) {
+                    const float2 x = mul2(make_float2(__uint_as_float(a[2 * e]),
+                                                      __uint_as_float(a[2 * e + 1])),
+                                          make_float2(inv, inv));
+                    sick = fma2(x, make_float2(0.f, 0.f), sick);
+                    hi[e] = pack_bf16x2(x.x, x.y);
+                    lo[e] = pack_bf16x2(x.x - bf16_lo(hi[e]), x.y - bf16_hi(hi[e]));
+                }
+                uint4 v[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    v[g] = make_uint4(hi[4 * g], hi[4 * g + 1], hi[4 * g + 2], hi[4 * g + 3]);
+                store_quad(v, p.out + o, p.o_t, w.len - row0, 32 * i, p.D);
+                if (p.rest) {
 #pragma unroll
                     for (int g = 0; g < 4; ++g)
-                        v[g] = make_uint4(hi[4 * g], hi[4 * g + 1], hi[4 * g + 2], hi[4 * g + 3]);
-                    store_quad(v, p.out + o, p.o_t, w.len - row0, col, p.D);
-                    if (p.rest) {
-#pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            v[g] = make_uint4(lo[4 * g], lo[4 * g + 1], lo[4 * g + 2], lo[4 * g + 3]);
-                        store_quad(v, p.rest + o, p.o_t, w.len - row0, col, p.D);
-                    }
+                        v[g] = make_uint4(lo[4 * g], lo[4 * g + 1], lo[4 * g + 2], lo[4 * g + 3]);
+                    store_quad(v, p.rest + o, p.o_t, w.len - row0, 32 * i, p.D);
                 }
-                const bool bad = !(sick.x + sick.y == 0.f);
-                if (valid && half == 0) p.lse[h * p.T + w.start + row] = lse;
-                again = __ballot_sync(0xFFFFFFFFu, bad && valid);
             }
-            // both halves of a row are stored before one is written whole
-            // again, and the sums' exchange is read before its next use
-            named_bar_sync(pair, 64);
+            if (valid) p.lse[h * p.T + w.start + row] = lse;
+            uint32_t again = __ballot_sync(0xFFFFFFFFu, !(sick.x + sick.y == 0.f) && valid);
+            __syncwarp();   // a row's pieces come from four lanes
             while (again) {
                 const int src = __ffs(again) - 1;
                 again &= again - 1;
-                fwd_row(p, w.start, __shfl_sync(0xFFFFFFFFu, row, src), h, w.kvh,
-                        __shfl_sync(0xFFFFFFFFu, lse, src));
+                fwd_row(p, w.start, row0 + src, h, w.kvh, __shfl_sync(0xFFFFFFFFu, lse, src));
             }
             return true;
         });
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 16) tmem_dealloc(tm, 512);
+    if (warp == kFwdMmaWarp) tmem_dealloc(tm, 512);
 }
 
 // ------------------------------------------------------------------ the plan
@@ -678,12 +656,12 @@ int launch_attention_fwd(const moe_attention_t& a, const void* plan, const uint1
     if (D <= 64) {
         if (ensure_smem_attr(reinterpret_cast<const void*>(attn_fwd_kernel<64>), FwdCfg<64>::SMEM))
             return MOE_ECUDA;
-        attn_fwd_kernel<64><<<grid, 640, FwdCfg<64>::SMEM, st>>>(p);
+        attn_fwd_kernel<64><<<grid, kFwdThreads, FwdCfg<64>::SMEM, st>>>(p);
     } else {
         if (ensure_smem_attr(reinterpret_cast<const void*>(attn_fwd_kernel<128>),
                              FwdCfg<128>::SMEM))
             return MOE_ECUDA;
-        attn_fwd_kernel<128><<<grid, 640, FwdCfg<128>::SMEM, st>>>(p);
+        attn_fwd_kernel<128><<<grid, kFwdThreads, FwdCfg<128>::SMEM, st>>>(p);
     }
     if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
     trace_after(st, "attn_fwd");
