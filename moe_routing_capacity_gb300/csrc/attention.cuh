@@ -188,6 +188,20 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, status));
 }
 
+// The same for the MMA warp: a wait that is not over at once goes on out of
+// line.  The warp shares its instruction cache with warps that run through
+// thousands of instructions a block, so its own loop has to be short.
+static __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                     int32_t* status) {
+    return mbar_wait(bar, parity, abort_flag, status);
+}
+
+__device__ __forceinline__ bool warp_wait_short(uint64_t* bar, uint32_t parity,
+                                                volatile int* abort_flag, int32_t* status) {
+    return __all_sync(0xFFFFFFFFu,
+                      mbar_try_wait(bar, parity) || wait_on(bar, parity, abort_flag, status));
+}
+
 // acc[tmem] (+)= A B over 128 tokens: A bf16 in four pieces of 32 tokens (16
 // columns each, 32 columns apart), B a tile read MN-major.
 template <int D>

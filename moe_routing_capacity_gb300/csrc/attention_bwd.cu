@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
             const auto phase = [](int it) { return static_cast<uint32_t>(it / C::STAGES) & 1u; };
             const auto at = [&](int it) { return ag + stage(it) * C::TILE; };
             const auto wait = [&](uint64_t* bar, uint32_t parity) {
-                const bool got = warp_wait(bar, parity, sm.abort_flag, p.status);
+                const bool got = warp_wait_short(bar, parity, sm.abort_flag, p.status);
                 tc_fence_after();
                 return got;
             };
@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
             // key blocks whose scores, whose dS have been met, items so far
             uint32_t cs = 0, cd = 0, done = 0;
             const auto wait = [&](uint64_t* bar, uint32_t parity) {
-                const bool got = warp_wait(bar, parity, sm.abort_flag, p.status);
+                const bool got = warp_wait_short(bar, parity, sm.abort_flag, p.status);
                 tc_fence_after();
                 return got;
             };

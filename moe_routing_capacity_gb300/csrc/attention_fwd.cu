@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
             uint32_t st = 0, ph = 0;        // next tile of the ring
             uint32_t items = 0, ps[2] = {0, 0}, tiles[2] = {0, 0};
             const auto wait = [&](uint64_t* bar, uint32_t parity) {
-                const bool got = warp_wait(bar, parity, abort_flag, p.status);
+                const bool got = warp_wait_short(bar, parity, abort_flag, p.status);
                 tc_fence_after();
                 return got;
             };
