@@ -17,7 +17,7 @@
 // columns of its TMEM lane), warp 16 issues the MMAs, warp 17 the TMA loads.
 // P and dS return to the columns of S and dP as bf16 A operands.
 //   8192 tokens in 4 sequences, 16/4 heads of 128 (one product 25 us at a library
-// product's rate): dQ 129 us, dK and dV 141 us.  dK and dV: a round of 128 x 128
+// product's rate): dQ 127 us, dK and dV 139 us.  dK and dV: a round of 128 x 128
 // pairs takes 2300 cycles, of which the tensor cores work 2048 and shared memory
 // is read and filled all of them; the CTA with the longest column has 96 rounds
 // and 8 us of start and end.  dQ: 2200 cycles a round (products 1536, the

@@ -8,18 +8,20 @@
 //   S = Q K^T (tcgen05, fp32 in TMEM); m, l = running maximum and sum;
 //   P = 2^(c S - c m) as bf16 back into S's columns; O += P V (A from TMEM).
 // Warps 0-3 and 4-7 run the softmax of the two tiles, a thread a row, so that
-// no two threads have to meet (two threads a row: 491 us against 479 below);
-// warp 8 issues the MMAs, warp 9 the TMA loads.
-// While one tile's softmax runs, the tensor cores work on the other's products.
-// TMEM: two S and two O of 128 columns, all 512.
-//   16384 tokens in 7 sequences, 48/8 heads of 128 (0.69 TFLOP): 479 us, 1.45
+// no two threads have to meet (two threads a row took 491 us where this takes
+// 479); warp 8 issues the MMAs, warp 9 the TMA loads.  While one tile's softmax
+// runs, the tensor cores work on the other's products.  TMEM: two S and two O
+// of 128 columns, all 512.
+//   16384 tokens in 7 sequences, 48/8 heads of 128 (0.69 TFLOP): 469 us, 1.48
 // PFLOP/s (a library product reaches 1.88).  32768 tokens in one sequence, 8/2
-// heads: 1.24 ms, 1.77 PFLOP/s; run for seconds both are held back by the power
-// limit (534 us, 1.40 ms).  What bounds it: S waits for the product that reads P
-// from its columns, so a tile's softmax (about 1800 cycles) and its products
-// (1024) follow each other and two tiles do not fill the tensor cores; beside
+// heads: 1.23 ms, 1.79 PFLOP/s.  Run for seconds, both meet the power limit
+// (535 us, 1.38 ms).  What bounds it: S waits for the product that reads P from
+// its columns, so a tile's softmax (about 1500 cycles) and its products (1024)
+// follow each other and two tiles do not quite fill the tensor cores; beside
 // that Q and K from shared memory take its whole bandwidth while S is formed,
-// and a piece of work starts and ends with 5000 cycles without products.
+// and a piece of work starts and ends with 4000 cycles without products.
+// (A MMA warp for each tile: 701 us, products of two issuers interleave; softmax
+// loops rolled over halves of the keys, to be shorter: 507 us.)
 #include <cstring>
 
 #include "attention.cuh"
