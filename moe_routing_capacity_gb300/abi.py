@@ -262,8 +262,8 @@ def _ptr(t, dtype=None, allow_none=False):
 
 def _stream(stream=None):
     if stream is None:   # the current stream's handle, without building a Stream object
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _check(fn, rc):
@@ -561,24 +561,26 @@ def _rows(name, t, shape, dtypes, allow_none=False):
         if allow_none:
             return None
         raise ValueError(f"{name}: tensor required")
+    # one condition where all is well: a small call's time is mostly these
+    if t.dtype in dtypes and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name}: contiguous device tensor required")
-    return t.data_ptr()
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name}: contiguous device tensor required")
 
 
 _BF16, _F32, _RES = (bf16,), (f32,), (bf16, f32)
 
 
 def _norm_config(r, gate, alpha, beta, eps):
-    if r.dim() != 2:
+    rows = r.shape
+    if len(rows) != 2:
         raise ValueError("the residual stream is [T, d]")
-    T, d = r.shape
+    T, d = rows
     per_token = gate is not None and gate.dim() == 2
-    return (T, d), (d,), (T,), Norm(T, d, r.dtype == f32, per_token, alpha, beta, eps)
+    return rows, (d,), (T,), Norm(T, d, r.dtype == f32, per_token, alpha, beta, eps)
 
 
 def norm_residual(b, r, gate, w_post, w_pre, y, n, rstd_post=None, rstd_pre=None, alpha=1.0,
@@ -647,14 +649,14 @@ def rotary_table(table, base=10000.0, scaling="none", factor=1.0, orig_len=0.0, 
 def _heads(name, t, shape):
     """(address, token stride, head stride) of a [T, heads, D] bf16 tensor
     whose channels are contiguous (tokens and heads may be strided)."""
+    if t.dtype == bf16 and t.shape == shape:
+        st, sh, sd = t.stride()
+        if sd == 1 and t.is_cuda:
+            return t.data_ptr(), st, sh
+        raise ValueError(f"{name}: device tensor with contiguous channels required")
     if t.dtype != bf16:
         raise TypeError(f"{name}: expected {bf16}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    st, sh, sd = t.stride()
-    if not t.is_cuda or sd != 1:
-        raise ValueError(f"{name}: device tensor with contiguous channels required")
-    return t.data_ptr(), st, sh
+    raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
 
 
 def rotary(q, k, table, pos, q_out, k_out, status, interleaved=False, inverse=False, stream=None):
