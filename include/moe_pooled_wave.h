@@ -675,7 +675,8 @@ int moe_rotary(const moe_rotary_t* cfg, const uint16_t* q, const uint16_t* k,
  * moe_attention_plan: the work lists of one batch of sequences, from cu, on
  *   the stream (no host synchronisation), for any number of forward and
  *   backward calls of these sizes; cu that is decreasing or out of range
- *   gives MOE_EINVAL in status and lists without work.
+ *   gives MOE_EINVAL in status and lists without work; forward and backward
+ *   calls on such a plan write nothing and give MOE_EINVAL in their status.
  * moe_attention_forward: out [T, n_heads, D]; lse [n_heads, T] fp32 =
  *   ln sum_j exp(s_ij); rest (same layout as out, NULL when no gradient is
  *   wanted) = bf16(o - out), what rounding took from out.

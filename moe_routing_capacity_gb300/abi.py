@@ -688,7 +688,8 @@ class AttentionPlan:
     stream, never on the host).  It serves any number of attention and
     attention_backward calls of these sizes; refill() takes another batch's
     cu_seqlens of the same length.  ``status`` receives MOE_EINVAL if they
-    decrease or leave [0, T]."""
+    decrease or leave [0, T]; calls on such a plan write nothing and set their
+    own status likewise."""
 
     def __init__(self, cu_seqlens, T, n_heads, n_kv_heads, head_dim, status=None, stream=None):
         self.T, self.n_heads, self.n_kv_heads, self.head_dim = T, n_heads, n_kv_heads, head_dim

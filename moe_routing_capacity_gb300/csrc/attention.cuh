@@ -8,7 +8,8 @@ namespace moe {
 
 // ------------------------------------------------------------------ the plan
 // Work lists of one batch of packed sequences, in device memory:
-//   header   int32[8]: number of entries of each list (q128, kv128, q256), error
+//   header   int32[8]: number of entries of each list (q128, kv128, q256), and
+//            whether the sequences were refused (the lists are empty then)
 //   q128     query blocks of 128 rows, most key blocks first
 //   kv128    key blocks of 128 rows, most query blocks first
 //   q256     query blocks of 256 rows, most key blocks first
@@ -21,6 +22,7 @@ struct AttnPlanLayout {
 };
 
 constexpr int kPlanHeader = 32;
+constexpr int kPlanRefused = 3;   // header word
 
 inline AttnPlanLayout attn_plan_layout(int64_t T, int n_seqs) {
     AttnPlanLayout l;
@@ -34,6 +36,11 @@ inline AttnPlanLayout attn_plan_layout(int64_t T, int n_seqs) {
     l.cursor = l.q256 + l.max256 * 16;
     l.total = l.cursor + 2 * l.bins * 4;
     return l;
+}
+
+// A call on refused sequences writes nothing and says so in its own status.
+__device__ __forceinline__ void report_refused(const int32_t* header, int32_t* status) {
+    if (blockIdx.x == 0 && threadIdx.x == 0 && header[kPlanRefused]) report_error(status, MOE_EINVAL);
 }
 
 // The items of this CTA, heaviest first: dealt out to the CTAs in turn, every

@@ -690,6 +690,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
         report_error(p.status, MOE_ECUDA);
         return;
     }
+    report_refused(p.header, p.status);
     BwdSmem<C> sm(smem_raw);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;

@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
         report_error(p.status, MOE_ECUDA);
         return;
     }
+    report_refused(p.header, p.status);
     uint8_t* sQ = smem_raw;
     uint8_t* sKV = sQ + 2 * C::TILE;
     uint64_t* full = reinterpret_cast<uint64_t*>(sKV + C::STAGES * C::TILE);
@@ -491,10 +492,11 @@ __global__ void __launch_bounds__(1024, 1)
     }
     __syncthreads();
     if (bad) {
-        if (tid < 8) header[tid] = 0;
+        if (tid < 8) header[tid] = tid == kPlanRefused;
         if (tid == 0) report_error(status, MOE_EINVAL);
         return;
     }
+    if (tid == 0) header[kPlanRefused] = 0;
     for (int pass = 0; pass < 2; ++pass) {
         const int bs = pass ? 256 : 128;
         for (int i = tid; i < bins; i += 1024) cursor[i] = 0;
