@@ -221,6 +221,20 @@ __device__ __forceinline__ void mma_tokens_quarters(uint32_t leader, uint32_t d_
                accumulate || kk > 0);
 }
 
+// Zeroes the rows from `rows` on of a tile that has landed, by a whole warp and
+// before a product may read it.
+template <int D>
+__device__ __forceinline__ void zero_tile_rows(uint32_t tile, int rows) {
+    for (uint32_t o = rows * 128 + (threadIdx.x & 31) * 16; o < kBoxBytes; o += 512)
+#pragma unroll
+        for (int b = 0; b < D / 64; ++b)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + b * kBoxBytes + o),
+                         "r"(0)
+                         : "memory");
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
 // Brings the 128-byte line at `p` into L2.  (As bulk prefetches, one a row,
 // 384 of them held their warps up for 6000 cycles.)
 __device__ __forceinline__ void prefetch_l2(const void* p) {
@@ -296,11 +310,33 @@ __device__ __forceinline__ uint16_t f32_bf16(float v) {
     return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
+// x . y over D channels, 16 bytes a load.
+__device__ __forceinline__ float dot_bf16(const uint16_t* x, const uint16_t* y, int D) {
+    float2 s = make_float2(0.f, 0.f);
+    for (int c = 0; c < D; c += 8) {
+        const uint4 a = *reinterpret_cast<const uint4*>(x + c);
+        const uint4 b = *reinterpret_cast<const uint4*>(y + c);
+        s = fma2(bf16x2_f32(a.x), bf16x2_f32(b.x), s);
+        s = fma2(bf16x2_f32(a.y), bf16x2_f32(b.y), s);
+        s = fma2(bf16x2_f32(a.z), bf16x2_f32(b.z), s);
+        s = fma2(bf16x2_f32(a.w), bf16x2_f32(b.w), s);
+    }
+    return s.x + s.y;
 }
+
+// ------------------------------------------------------------------ values that are not finite
+//
+// The products run over whole blocks: a hidden pair's P and dS are 0, but 0
+// times NaN or infinity is NaN.  Only the diagonal block has hidden pairs (the
+// rows behind a sequence's end, which dK and dV meet in every block of keys,
+// are zeroed before they are read), so a hidden value can have spoilt a row
+// only if it stands there, and at most the 128 rows of its own block.  Those rows are done again by the
+// definition on the CUDA cores, a pair a lane.  A row that sees the NaN itself
+// holds its answer already and is left as it is: one NaN at a sequence's start
+// reaches all its later rows and costs nothing more.
+
+__device__ __forceinline__ bool bf16_odd(uint32_t v) { return (v & 0x7F80u) == 0x7F80u; }
+__device__ __forceinline__ bool bf16_nan(uint32_t v) { return (v & 0x7FFFu) > 0x7F80u; }
 
 template <int N>
 __device__ __forceinline__ void setmaxnreg_inc() {

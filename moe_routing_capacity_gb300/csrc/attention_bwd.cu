@@ -56,84 +56,133 @@ struct BwdParams {
 
 // ------------------------------------------------------------------ rows by the definition
 
-// Rows whose products met a non-finite value, on the CUDA cores: pairs that
-// the mask hides are skipped instead of multiplied by 0.  One warp a row.
-struct RowPair {
-    float p, ds;
-};
+// (attention.cuh says when.)  One warp a row, 32 columns [c0, c0 + 32) of it,
+// a column a lane; the sum over the pairs takes 32 pairs, a pair a lane, then
+// their weights one after another.
 
-__device__ __forceinline__ RowPair row_pair(const BwdParams& p, const float (&a)[4],
-                                            const float (&b)[4], const uint16_t* x,
-                                            const uint16_t* y, float lse2, float delta, int lane) {
-    float s = 0.f, dp = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < p.D) {
-            s += a[i] * bf16_f32(x[lane + 32 * i]);
-            dp += b[i] * bf16_f32(y[lane + 32 * i]);
-        }
-    s = warp_sum(s);
-    dp = warp_sum(dp);
-    RowPair r;
-    r.p = exp2f(s * p.scale_log2 - lse2);
-    r.ds = r.p * (dp - delta);
-    return r;
+// The rows of the 32 from row0 on that a hidden key of the diagonal block can
+// have spoilt in these columns of dQ, as bits.
+__device__ __forceinline__ uint32_t dq_spoilt(const BwdParams& p, int64_t start, int row0, int kvh,
+                                            int c0) {
+    const int c = c0 + (threadIdx.x & 31), r0 = row0 & 127;
+    const int64_t first = start + row0 - r0;
+    const int n = static_cast<int>(min(static_cast<int64_t>(128), p.T - first));
+    int last = -1;
+    if (c < p.D)
+        for (int j = 0; j < n; ++j)
+            if (bf16_odd(p.k[(first + j) * p.k_t + kvh * p.k_h + c])) last = j;
+    last = __reduce_max_sync(0xFFFFFFFFu, last);
+    return ~bits_from(last - r0);   // rows before it
 }
 
-__device__ __noinline__ void dq_row(const BwdParams& p, int64_t start, int row, int h, int kvh) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void dq_row(const BwdParams& p, int64_t start, int row, int h, int kvh,
+                                    int c0, float lse2, float delta) {
+    const int lane = threadIdx.x & 31, c = c0 + lane;
     const int64_t t = start + row;
-    float q[4], g[4], acc[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool in = lane + 32 * i < p.D;
-        q[i] = in ? bf16_f32(p.q[t * p.q_t + h * p.q_h + lane + 32 * i]) : 0.f;
-        g[i] = in ? bf16_f32(p.dout[t * p.do_t + h * p.do_h + lane + 32 * i]) : 0.f;
+    const uint16_t* q = p.q + t * p.q_t + h * p.q_h;
+    const uint16_t* g = p.dout + t * p.do_t + h * p.do_h;
+    const uint16_t* k = p.k + start * p.k_t + kvh * p.k_h;
+    const uint16_t* v = p.v + start * p.v_t + kvh * p.v_h;
+    float acc = 0.f;
+    for (int j0 = 0; j0 <= row; j0 += 32) {
+        const int n = min(32, row + 1 - j0);
+        float ds = 0.f;
+        if (lane < n) {
+            const int j = j0 + lane;
+            ds = exp2f(dot_bf16(q, k + j * p.k_t, p.D) * p.scale_log2 - lse2) *
+                 (dot_bf16(g, v + j * p.v_t, p.D) - delta);
+        }
+#pragma unroll 4
+        for (int e = 0; e < n; ++e) {
+            const float x = __shfl_sync(0xFFFFFFFFu, ds, e);
+            if (c < p.D) acc += x * bf16_f32(k[(j0 + e) * p.k_t + c]);
+        }
     }
-    const float lse2 = p.lse2[h * p.T + t], delta = p.delta[h * p.T + t];
-    for (int j = 0; j <= row; ++j) {
-        const uint16_t* k = p.k + (start + j) * p.k_t + kvh * p.k_h;
-        const uint16_t* v = p.v + (start + j) * p.v_t + kvh * p.v_h;
-        const RowPair r = row_pair(p, q, g, k, v, lse2, delta, lane);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (lane + 32 * i < p.D) acc[i] += r.ds * bf16_f32(k[lane + 32 * i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < p.D)
-            p.dq[t * p.dq_t + h * p.dq_h + lane + 32 * i] = f32_bf16(acc[i] * p.scale);
+    if (c < p.D) p.dq[t * p.dq_t + h * p.dq_h + c] = f32_bf16(acc * p.scale);
 }
 
-// Columns [c0, c1) of the row of dV (which = 0) or dK (1).
-__device__ __noinline__ void dkv_row(const BwdParams& p, int64_t start, int len, int row, int kvh,
-                                     int which, int c0, int c1) {
-    const int lane = threadIdx.x & 31;
-    const int64_t t = start + row;
-    float k[4], v[4], acc[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool in = lane + 32 * i < p.D;
-        k[i] = in ? bf16_f32(p.k[t * p.k_t + kvh * p.k_h + lane + 32 * i]) : 0.f;
-        v[i] = in ? bf16_f32(p.v[t * p.v_t + kvh * p.v_h + lane + 32 * i]) : 0.f;
+// Those of the rows row0 + (bit of `rows`), by a warp whose lanes hold their
+// rows' lse2 and D.
+__device__ __noinline__ void dq_redo(const BwdParams& p, int64_t start, int row0, int h, int kvh,
+                                     int c0, uint32_t rows, float lse2, float delta) {
+    rows &= dq_spoilt(p, start, row0, kvh, c0);
+    for (; rows; rows &= rows - 1) {
+        const int s = __ffs(rows) - 1;
+        dq_row(p, start, row0 + s, h, kvh, c0, __shfl_sync(0xFFFFFFFFu, lse2, s),
+               __shfl_sync(0xFFFFFFFFu, delta, s));
     }
-    for (int h = kvh * p.group; h < (kvh + 1) * p.group; ++h)
-        for (int i = row; i < len; ++i) {
-            const uint16_t* q = p.q + (start + i) * p.q_t + h * p.q_h;
-            const uint16_t* g = p.dout + (start + i) * p.do_t + h * p.do_h;
-            const RowPair r = row_pair(p, k, v, q, g, p.lse2[h * p.T + start + i],
-                                       p.delta[h * p.T + start + i], lane);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (lane + 32 * e < p.D)
-                    acc[e] += which ? r.ds * bf16_f32(q[lane + 32 * e])
-                                    : r.p * bf16_f32(g[lane + 32 * e]);
+}
+
+// The rows of the 32 from key row0 on that a hidden query of the diagonal block
+// can have spoilt in these columns of dV (which = 0) or dK (1), as bits: a
+// query before the key holds a value that is not finite, and none from the key
+// on (in this block) makes the sum NaN by itself.
+__device__ __forceinline__ uint32_t dkv_spoilt(const BwdParams& p, int64_t start, int len, int row0,
+                                            int kvh, int which, int c0) {
+    const int lane = threadIdx.x & 31, c = c0 + lane, r0 = row0 & 127;
+    const int64_t first = start + row0 - r0;
+    const int n = min(128, len - (row0 - r0));
+    int first_odd = 128, last_nan = -1;
+    for (int h = kvh * p.group; h < (kvh + 1) * p.group; ++h) {
+        const uint16_t* x = which ? p.q + first * p.q_t + h * p.q_h
+                                  : p.dout + first * p.do_t + h * p.do_h;
+        const int64_t step = which ? p.q_t : p.do_t;
+        if (c < p.D)
+            for (int i = 0; i < n; ++i) {
+                const uint32_t v = x[i * step + c];
+                if (bf16_odd(v)) first_odd = min(first_odd, i);
+                if (bf16_nan(v)) last_nan = max(last_nan, i);
+            }
+        // P or dS itself NaN: every column of every key up to the query
+        int all = -1;
+        for (int i = lane; i < n; i += 32)
+            if (isnan(p.lse2[h * p.T + first + i]) || (which && isnan(p.delta[h * p.T + first + i])))
+                all = i;
+        last_nan = max(last_nan, __reduce_max_sync(0xFFFFFFFFu, all));
+    }
+    uint32_t rows = 0;
+    for (int i = 0; i < 32; ++i)
+        if (__any_sync(0xFFFFFFFFu, first_odd < r0 + i && last_nan < r0 + i)) rows |= 1u << i;
+    return rows;
+}
+
+__device__ __forceinline__ void dkv_row(const BwdParams& p, int64_t start, int len, int row, int kvh,
+                                     int which, int c0) {
+    const int lane = threadIdx.x & 31, c = c0 + lane;
+    const int64_t t = start + row;
+    const uint16_t* k = p.k + t * p.k_t + kvh * p.k_h;
+    const uint16_t* v = p.v + t * p.v_t + kvh * p.v_h;
+    float acc = 0.f;
+    for (int h = kvh * p.group; h < (kvh + 1) * p.group; ++h) {
+        const uint16_t* q = p.q + start * p.q_t + h * p.q_h;
+        const uint16_t* g = p.dout + start * p.do_t + h * p.do_h;
+        const uint16_t* x = which ? q : g;
+        const int64_t step = which ? p.q_t : p.do_t;
+        for (int i0 = row; i0 < len; i0 += 32) {
+            const int n = min(32, len - i0);
+            float w = 0.f;
+            if (lane < n) {
+                const int i = i0 + lane;
+                const int64_t at = h * p.T + start + i;
+                w = exp2f(dot_bf16(k, q + i * p.q_t, p.D) * p.scale_log2 - p.lse2[at]);
+                if (which) w *= dot_bf16(v, g + i * p.do_t, p.D) - p.delta[at];
+            }
+#pragma unroll 4
+            for (int e = 0; e < n; ++e) {
+                const float y = __shfl_sync(0xFFFFFFFFu, w, e);
+                if (c < p.D) acc += y * bf16_f32(x[(i0 + e) * step + c]);
+            }
         }
+    }
     uint16_t* o = which ? p.dk + t * p.dk_t + kvh * p.dk_h : p.dv + t * p.dv_t + kvh * p.dv_h;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i >= c0 && lane + 32 * i < min(c1, p.D))
-            o[lane + 32 * i] = f32_bf16(which ? acc[i] * p.scale : acc[i]);
+    if (c < p.D) o[c] = f32_bf16(which ? acc * p.scale : acc);
+}
+
+// Those of the rows row0 + (bit of `rows`), by a warp.
+__device__ __noinline__ void dkv_redo(const BwdParams& p, int64_t start, int len, int row0,
+                                      int kvh, int which, int c0, uint32_t rows) {
+    rows &= dkv_spoilt(p, start, len, row0, kvh, which, c0);
+    for (; rows; rows &= rows - 1) dkv_row(p, start, len, row0 + __ffs(rows) - 1, kvh, which, c0);
 }
 
 __device__ __forceinline__ void zero_rows(uint16_t* base, int64_t st_t, int D, int rows) {
@@ -170,10 +219,11 @@ struct BwdCfg {
     static constexpr int SCALARS = NF;
     static constexpr int TILE = 128 * D * 2;
     static constexpr int STAGES = ST;
-    static constexpr int SMEM = 2 * TILE + STAGES * TILE + SCALARS * 4 + 256;
+    static constexpr int SMEM = 2 * TILE + STAGES * TILE + SCALARS * 4 + 320;
 };
-// Warps 0-15 form P and dS; then the MMA warp, the load warp, two idle ones.
-constexpr int kBwdThreads = 640, kMmaWarp = 16, kLoadWarp = 17, kFormers = 512;
+// Warps 0-15 form P and dS; then the MMA warp, the load warp, the warp that
+// zeroes rows behind a sequence's end (dK and dV; idle in dQ), an idle one.
+constexpr int kBwdThreads = 640, kMmaWarp = 16, kLoadWarp = 17, kTailWarp = 18, kFormers = 512;
 constexpr int dkv_stages(int D) { return D == 128 ? 4 : 8; }
 constexpr int dq_stages(int D) { return D == 128 ? 5 : 8; }
 template <int D>
@@ -188,7 +238,7 @@ struct BwdSmem {
     uint8_t *res, *ring;
     float* rows;   // scalars of query rows: dQ two blocks of 256, dK and dV 64 a warp
     uint64_t *full, *empty, *res_full, *res_empty, *s_full, *s_free, *dp_full, *p_full, *ds_full, *acc_full,
-        *acc_empty, *done, *sums_there, *sums_read;
+        *acc_empty, *done, *sums_there, *sums_read, *tail_full;
     uint32_t* tmem_slot;
     volatile int* abort_flag;
     __device__ explicit BwdSmem(uint8_t* raw_ptr) {
@@ -209,13 +259,15 @@ struct BwdSmem {
         done = acc_empty + 1;
         sums_there = done + 1;
         sums_read = sums_there + 1;
-        tmem_slot = reinterpret_cast<uint32_t*>(sums_read + 1);
+        tail_full = sums_read + 1;
+        tmem_slot = reinterpret_cast<uint32_t*>(tail_full + C::STAGES);
         abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     }
     __device__ void init(int parts) {   // parts: CTAs of a cluster
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
+            mbar_init(&tail_full[s], 1);
         }
         mbar_init(res_full, 1);
         mbar_init(s_full, 1);
@@ -272,6 +324,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
     }
     const int nb = te.z, nblk = (len + 127) / 128;
     const int per_head = nblk - nb;          // query blocks of one head
+    const int end_rows = len - (nblk - 1) * 128;   // rows of the last one
     const int all = p.group * per_head;
     const int first = static_cast<int>(all * part / PARTS);
     const int n = static_cast<int>(all * (part + 1) / PARTS) - first;
@@ -308,6 +361,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                 load_tile<D>(ar + C::TILE, &p.mapV, sm.res_full, tok + nb * 128, kvh);
             }
             uint32_t st = 0, ph = 0, armed = 0, par = 0;
+            uint32_t tail_st = 0, tail_ph = 0;   // stages filled for the tail warp; its phases
             bool ok = true;
             int h = kvh * p.group + first / per_head, i = nb + first % per_head;
             for (int it = 0; it < 2 * n; ++it) {
@@ -315,10 +369,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                     ok = false;
                     break;
                 }
-                mbar_arrive_expect_tx(&sm.full[st], C::TILE);
+                const bool tail = end_rows < 128 && i == nblk - 1;
+                uint64_t* landed = tail ? &sm.tail_full[st] : &sm.full[st];
+                mbar_arrive_expect_tx(landed, C::TILE);
                 armed |= 1u << st;
-                par = (par & ~(1u << st)) | (ph << st);
-                load_tile<D>(ag + st * C::TILE, (it & 1) ? &p.mapO : &p.mapQ, &sm.full[st],
+                par = (par & ~(1u << st)) | ((tail ? tail_ph >> st & 1u : ph) << st);
+                tail_st = (tail_st & ~(1u << st)) | (static_cast<uint32_t>(tail) << st);
+                if (tail) tail_ph ^= 1u << st;
+                load_tile<D>(ag + st * C::TILE, (it & 1) ? &p.mapO : &p.mapQ, landed,
                              tok + i * 128, h);
                 if ((it & 1) && ++i == nblk) {
                     i = nb;
@@ -334,7 +392,27 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                 if (n) mbar_wait(sm.res_full, 0, &no_abort, nullptr, 20000000ull);
                 for (int s = 0; s < C::STAGES; ++s)
                     if (armed & (1u << s))
-                        mbar_wait(&sm.full[s], (par >> s) & 1u, &no_abort, nullptr, 20000000ull);
+                        mbar_wait(tail_st >> s & 1u ? &sm.tail_full[s] : &sm.full[s], (par >> s) & 1u,
+                                  &no_abort, nullptr, 20000000ull);
+            }
+        } else if (warp == kTailWarp && end_rows < 128) {
+            // -------------------------------------------------------- a sequence's end
+            // Its last block ends inside the tile: the rows behind it are other
+            // tokens', and what stands there (NaN, say, times P = 0) would reach
+            // every key.  Zeroed here, on the way from the copy to the products
+            // (by the MMA warp itself: 139 -> 150 us at the size above).
+            const uint32_t ag = smem_u32(sm.ring);
+            uint32_t st = 0, ph = 0;
+            int i = nb + first % per_head;
+            for (int it = 0; it < 2 * n; ++it) {
+                if (i == nblk - 1) {
+                    if (!warp_wait(&sm.tail_full[st], ph >> st & 1u, sm.abort_flag, p.status)) break;
+                    ph ^= 1u << st;
+                    zero_tile_rows<D>(ag + st * C::TILE, end_rows);
+                    if (lane == 0) mbar_arrive(&sm.full[st]);
+                }
+                if ((it & 1) && ++i == nblk) i = nb;
+                if (++st == C::STAGES) st = 0;
             }
         } else if (warp == kMmaWarp) {
             // -------------------------------------------------------- MMAs
@@ -492,7 +570,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
             tc_fence_after();
         }
         const int row = nb * 128 + r, row0 = row - lane;
-        if (PARTS > 1) {
+        if constexpr (PARTS > 1) {
             // this part's sums, rows of [dV | dK], into the ring (every copy
             // into it has landed, every product has read it): 16-byte pieces,
             // swizzled by the row so that a warp's rows spread over the banks
@@ -512,14 +590,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
             ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(sm.sums_there, 0, p.status)) && ok;
             // this CTA's share of the 2 D columns, 32 at a time: the parts'
             // sums in their order
-            for (int i = quarter; ok && i < 2 * D / 32 / PARTS; i += 4) {
-                const int at0 = (static_cast<int>(part) * (2 * D / 32 / PARTS) + i) * 32;
-                const int which = at0 >= D, col = at0 - which * D;   // of [dV | dK]
+            constexpr int PIECES = 2 * D / 32 / PARTS;
+            static_assert(PIECES <= 4, "one piece a warp at most");
+            const int at0 = (static_cast<int>(part) * PIECES + quarter) * 32;
+            const int which = at0 >= D, col = at0 - which * D;   // of [dV | dK]
+            uint32_t again = 0;
+            if (ok && quarter < PIECES) {
                 const float f = which ? p.scale : 1.0f;
                 const int64_t st_t = which ? p.dk_t : p.dv_t;
                 uint16_t* o = (which ? p.dk + kvh * p.dk_h : p.dv + kvh * p.dv_h) +
                               (start + row0) * st_t + col + 4 * (lane & 7);
-                uint32_t again = 0;
                 // eight lanes a row, four rows at a time: whole lines of the
                 // other CTAs' memory (a row a lane measured four times slower)
 #pragma unroll
@@ -554,17 +634,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                             if (b >> (8 * g) & 0xFFu) again |= 1u << (4 * (k0 + k) + g);
                     }
                 }
-                __syncwarp();   // a row's pieces come from eight lanes
-                while (again) {
-                    const int s = __ffs(again) - 1;
-                    again &= again - 1;
-                    if (row0 + s < len) dkv_row(p, start, len, row0 + s, kvh, which, col, col + 32);
-                }
             }
             // nobody leaves while its sums may still be read
-            __syncwarp();
+            __syncwarp();   // (and a row's pieces come from eight lanes)
             if (lane < PARTS) mbar_arrive_cluster(mapa_shared(smem_u32(sm.sums_read), lane));
             mbar_wait_cluster(sm.sums_read, 0, p.status, 4 * kWaitTimeoutNs);
+            __syncwarp();
+            again &= ~bits_from(len - row0);
+            if (again) dkv_redo(p, start, len, row0, kvh, which, col, again);
         } else if (ok) {   // 32 columns of [dV | dK] at a time
             for (int i = quarter; i < 2 * D / 32; i += 4) {
                 const int which = i >= D / 32, col = 32 * i - which * D;
@@ -576,12 +653,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                                            which ? p.scale : 1.0f, v);
                 store_quad(v, o, st_t, len - row0, col, p.D);
                 __syncwarp();   // a row's pieces come from four lanes
-                uint32_t again = __ballot_sync(0xFFFFFFFFu, bad && row < len);
-                while (again) {
-                    const int s = __ffs(again) - 1;
-                    again &= again - 1;
-                    dkv_row(p, start, len, row0 + s, kvh, which, col, col + 32);
-                }
+                const uint32_t again = __ballot_sync(0xFFFFFFFFu, bad && row < len);
+                if (again) dkv_redo(p, start, len, row0, kvh, which, col, again);
             }
         }
     }
@@ -814,18 +887,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
         // a warp that has given up (ok false) still meets the others at every
         // barrier, and does nothing else
         bool ok = true;
-        DqWork w, last;
-        // Rows of the last item that met a value that is not finite.  Written
-        // again only past a barrier: any quarter of a row may have met it, and
-        // the warps of the others have stored theirs then.
-        uint32_t again = 0;
-        const auto repair = [&] {
-            while (again) {
-                const int s = __ffs(again) - 1;
-                again &= again - 1;
-                dq_row(p, last.start, last.block * 128 + (r - lane) + s, last.h, last.kvh);
-            }
-        };
+        DqWork w;
         while (items.next(item)) {
             w = DqWork(p, item);
             if (w.block < 0) {   // tokens of no sequence
@@ -842,7 +904,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                 dots.finish(p, w, rows);
             }
             named_bar_sync(1, kFormers);
-            repair();
             float delta = rows[r];
             const float lse2 = rows[128 + r];
             const int row = w.block * 128 + r, row0 = row - lane, n = w.n;
@@ -929,12 +990,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                 if (c0 < D)
                     store_quad(v, p.dq + (w.start + row0) * p.dq_t + w.h * p.dq_h, p.dq_t,
                                w.len - row0, c0, p.D);
-                again = __ballot_sync(0xFFFFFFFFu, bad && valid);
+                __syncwarp();   // a row's pieces come from four lanes
+                // (with a NaN lse or D the row is NaN throughout)
+                const uint32_t again =
+                    __ballot_sync(0xFFFFFFFFu, bad && valid && !isnan(lse2) && !isnan(delta));
+                if (again) dq_redo(p, w.start, row0, w.h, w.kvh, c0, again, lse2, delta);
             }
-            last = w;
         }
-        named_bar_sync(1, kFormers);
-        repair();
     }
     tc_fence_before();
     __syncthreads();

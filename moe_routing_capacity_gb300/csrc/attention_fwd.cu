@@ -60,37 +60,78 @@ struct FwdCfg {
     static constexpr int SMEM = 2 * TILE + STAGES * TILE + 256;
 };
 
-// One row by the definition on the CUDA cores, for a row whose products met
-// a non-finite value: hidden tokens are skipped instead of multiplied by 0.
-__device__ __noinline__ void fwd_row(const FwdParams& p, int64_t start, int row, int h, int kvh,
+// Which of the 32 rows from row0 on a hidden value can have spoilt, as bits: in
+// some channel a value after the row (within the block of 128) is not finite,
+// and none up to the row is NaN.
+__device__ __forceinline__ uint32_t fwd_spoilt(const FwdParams& p, int64_t start, int row0, int kvh) {
+    const int lane = threadIdx.x & 31, r0 = row0 & 127;
+    const int64_t first = start + row0 - r0;
+    const int n = static_cast<int>(min(static_cast<int64_t>(128), p.T - first));
+    const uint16_t* v = p.v + first * p.v_t + kvh * p.v_h + 4 * lane;
+    int last_odd[4] = {-1, -1, -1, -1}, first_nan[4] = {128, 128, 128, 128};
+    if (4 * lane < p.D)
+        for (int j = 0; j < n; ++j) {
+            const uint2 w = *reinterpret_cast<const uint2*>(v + j * p.v_t);
+            const uint32_t x[4] = {w.x, w.x >> 16, w.y, w.y >> 16};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (bf16_odd(x[e])) last_odd[e] = j;
+                if (bf16_nan(x[e])) first_nan[e] = min(first_nan[e], j);
+            }
+        }
+    uint32_t rows = 0;
+    for (int i = 0; i < 32; ++i) {
+        const int r = r0 + i;
+        bool need = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) need |= last_odd[e] > r && first_nan[e] > r;
+        if (__any_sync(0xFFFFFFFFu, need)) rows |= 1u << i;
+    }
+    return rows;
+}
+
+// One row by the definition, by one warp: the weights of 32 keys, a key a
+// lane, then their sum over the values, four channels a lane.
+__device__ __forceinline__ void fwd_row(const FwdParams& p, int64_t start, int row, int h, int kvh,
                                      float lse) {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, c = 4 * lane;
     const uint16_t* q = p.q + (start + row) * p.q_t + h * p.q_h;
     const uint16_t* k = p.k + start * p.k_t + kvh * p.k_h;
     const uint16_t* v = p.v + start * p.v_t + kvh * p.v_h;
-    float qv[4], acc[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) qv[i] = lane + 32 * i < p.D ? bf16_f32(q[lane + 32 * i]) : 0.f;
-    for (int j = 0; j <= row; ++j) {
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (lane + 32 * i < p.D) s += qv[i] * bf16_f32(k[j * p.k_t + lane + 32 * i]);
-        s = warp_sum(s);
-        const float w = expf(s * p.scale - lse);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (lane + 32 * i < p.D) acc[i] += w * bf16_f32(v[j * p.v_t + lane + 32 * i]);
+    float acc[4] = {0, 0, 0, 0};
+    for (int j0 = 0; j0 <= row; j0 += 32) {
+        const int n = min(32, row + 1 - j0);
+        float w = 0.f;
+        if (lane < n) w = expf(dot_bf16(q, k + (j0 + lane) * p.k_t, p.D) * p.scale - lse);
+#pragma unroll 4
+        for (int e = 0; e < n; ++e) {
+            const float x = __shfl_sync(0xFFFFFFFFu, w, e);
+            if (c >= p.D) continue;
+            const uint2 u = *reinterpret_cast<const uint2*>(v + (j0 + e) * p.v_t + c);
+            acc[0] += x * bf16_lo(u.x);
+            acc[1] += x * bf16_hi(u.x);
+            acc[2] += x * bf16_lo(u.y);
+            acc[3] += x * bf16_hi(u.y);
+        }
     }
     const int64_t o = (start + row) * p.o_t + h * p.o_h;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int c = lane + 32 * i;
-        if (c < p.D) {
-            const uint16_t b = f32_bf16(acc[i]);
-            p.out[o + c] = b;
-            if (p.rest) p.rest[o + c] = f32_bf16(acc[i] - bf16_f32(b));
-        }
+        if (c >= p.D) break;
+        const uint16_t b = f32_bf16(acc[i]);
+        p.out[o + c + i] = b;
+        if (p.rest) p.rest[o + c + i] = f32_bf16(acc[i] - bf16_f32(b));
+    }
+}
+
+// Those of the rows row0 + (bit of `rows`), by a warp whose lanes hold their
+// rows' lse.
+__device__ __noinline__ void fwd_redo(const FwdParams& p, int64_t start, int row0, int h, int kvh,
+                                      uint32_t rows, float lse) {
+    rows &= fwd_spoilt(p, start, row0, kvh);
+    for (; rows; rows &= rows - 1) {
+        const int s = __ffs(rows) - 1;
+        fwd_row(p, start, row0 + s, h, kvh, __shfl_sync(0xFFFFFFFFu, lse, s));
     }
 }
 
@@ -457,13 +498,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
                 }
             }
             if (valid) p.lse[h * p.T + w.start + row] = lse;
-            uint32_t again = __ballot_sync(0xFFFFFFFFu, !(sick.x + sick.y == 0.f) && valid);
+            // (an lse that is not finite is that of a row which is NaN throughout)
+            const uint32_t again = __ballot_sync(
+                0xFFFFFFFFu, !(sick.x + sick.y == 0.f) && valid && lse - lse == 0.f);
             __syncwarp();   // a row's pieces come from four lanes
-            while (again) {
-                const int src = __ffs(again) - 1;
-                again &= again - 1;
-                fwd_row(p, w.start, row0 + src, h, w.kvh, __shfl_sync(0xFFFFFFFFu, lse, src));
-            }
+            if (again) fwd_redo(p, w.start, row0, h, w.kvh, again, lse);
             return true;
         });
     }

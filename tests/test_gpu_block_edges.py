@@ -71,3 +71,147 @@ def test_calls_on_refused_sequences_say_so(rng, hq, hk):
     want = R.attention(q, k, v, [200, 100], D ** -0.5, dout=dout)
     for n in ("out", "dq", "dk", "dv"):
         R.within(n, got[n], want[n][0], want[n][1] + 1e-30)
+
+
+# ------------------------------------------------------------------ values that are not finite
+
+def offsets(lens):
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    return cu
+
+
+def reference(q, k, v, lens, dout):
+    """R.attention with what its bounds leave out: D of a row past its
+    sequence's first 128 comes from the out that the rounded P gave.  With
+    weights w~ from P (1 + d), |d| <= U, the row's D is off by
+    sum (w~ - w)(dP - D) <= 2 U (1 + 2 U) sum w |dP - D|, and dS by P times it."""
+    D = q.shape[2]
+    want = R.attention(q, k, v, lens, D ** -0.5, dout=dout)
+    group, at = q.shape[1] // k.shape[1], 0
+    q, k, v, dout = (t.double() for t in (q, k, v, dout))
+    for n in lens:
+        sl = slice(at, at + n)
+        at += n
+        keep = torch.ones(n, n, dtype=torch.bool, device=q.device).tril()
+        for h in range(q.shape[1]):
+            kv = h // group
+            p = torch.softmax((q[sl, h] @ k[sl, kv].T * D ** -0.5).masked_fill(~keep, -math.inf), 1)
+            dp = dout[sl, h] @ v[sl, kv].T
+            off = (p * (dp - (p * dp).sum(1, keepdim=True)).abs()).sum(1, keepdim=True)
+            ds = 2 * R.U * (1 + 2 * R.U) ** 2 * p * off * D ** -0.5
+            want["dq"][1][sl, h] += ds @ k[sl, kv].abs()
+            want["dk"][1][sl, kv] += ds.T @ q[sl, h].abs()
+    return want
+
+
+# lengths, hq, hk, D: one CTA, two and four a block of keys in the backward;
+# second pieces of work a CTA in the last one
+NOT_FINITE = [([300, 333, 150], 4, 4, 64), ([300, 211], 2, 1, 128), ([140, 300, 50], 8, 1, 80),
+              ([1111, 1300, 900], 16, 8, 128), ([700, 1001, 1499], 9, 3, 96)]
+
+
+@pytest.mark.parametrize("lens,hq,hk,D", NOT_FINITE)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_token_that_is_not_finite(rng, lens, hq, hk, D, bad):
+    """All of one token's q, k, v and gradient: its sequence's earlier rows and
+    every other sequence have the values they would have without it (the
+    sequence before it ends inside a tile that it shares); with NaN, its own
+    row and the later ones are NaN, and so is every key that they see."""
+    T, cu = sum(lens), offsets(lens)
+    q, k, v, dout = (randn(rng, T, h, D) for h in (hq, hk, hk, hq))
+    want = reference(q, k, v, lens, dout)
+    clean, _ = attention_step(q, k, v, cu, dout)
+    for hit in (cu[1], cu[1] + lens[1] // 2):
+        x = [t.clone() for t in (q, k, v, dout)]
+        for t in x:
+            t[hit] = bad
+        got, st = attention_step(*x[:3], cu, x[3])
+        assert st == [0, 0]
+        rows = torch.ones(T, dtype=torch.bool, device="cuda")
+        rows[hit:cu[2]] = False
+        keys = torch.ones(T, dtype=torch.bool, device="cuda")
+        keys[cu[1]:cu[2]] = False
+        for n, some in (("out", rows), ("dq", rows), ("dk", keys), ("dv", keys)):
+            R.within(n, got[n][some], want[n][0][some], want[n][1][some] + 1e-30)
+            # a sequence that shares no tile with it: the same bits
+            apart = keys.clone()
+            apart[:cu[1]] = hit != cu[1]
+            assert torch.equal(got[n][apart], clean[n][apart]), n
+            if math.isnan(bad):
+                assert bool(got[n][~some].isnan().all()), n
+
+
+@pytest.mark.parametrize("lens,hq,hk,D", NOT_FINITE)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_gradient_that_is_not_finite(rng, lens, hq, hk, D, bad):
+    """It reaches its own row and the keys up to it."""
+    T, cu = sum(lens), offsets(lens)
+    q, k, v, dout = (randn(rng, T, h, D) for h in (hq, hk, hk, hq))
+    want = reference(q, k, v, lens, dout)
+    hit = cu[1] + lens[1] // 2
+    d = dout.clone()
+    d[hit] = bad
+    got, st = attention_step(q, k, v, cu, d)
+    assert st == [0, 0]
+    rows = torch.ones(T, dtype=torch.bool, device="cuda")
+    rows[hit] = False
+    keys = torch.ones(T, dtype=torch.bool, device="cuda")
+    keys[cu[1]:hit + 1] = False
+    for n, some in (("out", rows | True), ("dq", rows), ("dk", keys), ("dv", keys)):
+        R.within(n, got[n][some], want[n][0][some], want[n][1][some] + 1e-30)
+        assert not bool(got[n][~some].isfinite().any()), n
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_channel_that_is_not_finite(rng, D):
+    """NaN in one channel of every value stays in that channel of out; an
+    infinity that a row sees and one that it does not are told apart."""
+    lens, hq, hk = [300, 500], 4, 2
+    T, cu = 800, [0, 300, 800]
+    q, k, v, dout = (randn(rng, T, h, D) for h in (hq, hk, hk, hq))
+    want = R.attention(q, k, v, lens, D ** -0.5)["out"]
+    x = v.clone()
+    x[:, :, 5] = float("nan")
+    x[310, :, 7] = float("inf")      # seen by the rows from there on
+    x[340, :, 7] = float("inf")      # hidden from the rows before it
+    got, st = attention_step(q, k, x, cu, dout)
+    assert st == [0, 0]
+    assert bool(got["out"][:, :, 5].isnan().all())
+    keep = torch.ones(D, dtype=torch.bool, device="cuda")
+    keep[5] = keep[7] = False
+    R.within("out", got["out"][..., keep], want[0][..., keep], want[1][..., keep] + 1e-30)
+    R.within("before", got["out"][:310, :, 7], want[0][:310, :, 7], want[1][:310, :, 7] + 1e-30)
+    assert bool((got["out"][310:, :, 7] == float("inf")).all())
+
+
+@pytest.mark.parametrize("what", ["first value", "every value", "every gradient", "first key"])
+def test_what_is_not_finite_costs_little(rng, what):
+    """A row that sees the NaN itself is not done again: the step takes no
+    more than three times a finite one's time."""
+    T, hq, hk, D = 16384, 4, 1, 128
+    x = {n: randn(rng, T, h, D) for n, h in (("q", hq), ("k", hk), ("v", hk), ("d", hq))}
+    nan = {n: t.clone() for n, t in x.items()}
+    if what == "first value":
+        nan["v"][0] = float("nan")
+    elif what == "every value":
+        nan["v"].fill_(float("nan"))
+    elif what == "every gradient":
+        nan["d"].fill_(float("nan"))
+    else:
+        nan["k"][0] = float("nan")
+    plan = abi.AttentionPlan(ints(0, T), T, hq, hk, D)
+    times = []
+    for t in (x, nan, x, nan):
+        best = math.inf
+        for _ in range(3):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            _, st = attention_step(t["q"], t["k"], t["v"], None, t["d"], plan)
+            b.record()
+            b.synchronize()
+            assert st == [0, 0]
+            best = min(best, a.elapsed_time(b))
+        times.append(best)
+    assert min(times[1::2]) <= 3 * min(times[::2]), times
