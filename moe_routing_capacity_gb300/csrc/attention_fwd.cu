@@ -424,7 +424,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
                     tmem_wait_st();
                     tc_fence_before();
                 }
-                const float2 c2 = make_float2(c, c), neg = make_float2(-m * c, -m * c);
+                // (no key with a weight so far: -inf - -inf would be NaN)
+                const float from = m == -INFINITY ? 0.f : -m * c;
+                const float2 c2 = make_float2(c, c), neg = make_float2(from, from);
                 // half the keys: their product with V runs while the others
                 // are formed
 #pragma unroll

@@ -215,3 +215,26 @@ def test_what_is_not_finite_costs_little(rng, what):
             best = min(best, a.elapsed_time(b))
         times.append(best)
     assert min(times[1::2]) <= 3 * min(times[::2]), times
+
+
+@pytest.mark.parametrize("hq,hk", [(2, 1), (3, 1)])
+def test_keys_without_weight(rng, hq, hk):
+    """Keys whose scores are -infinity have weight 0, a sequence's first 128 or
+    more among them: the later rows are the softmax over the others."""
+    T, D, dead = 700, 64, 260
+    q, k, v = randn(rng, T, hq, D), randn(rng, T, hk, D), randn(rng, T, hk, D)
+    q[..., 0] = q[..., 0].abs() + 1
+    k[:dead, :, 0] = -math.inf
+    plan = abi.AttentionPlan(ints(0, T), T, hq, hk, D)
+    out, lse, st = empty(T, hq, D), empty(hq, T, dt=F32), status()
+    abi.attention(plan, q, k, v, out, lse, st)
+    assert int(st) == 0
+    assert bool(out[:dead].isnan().all()) and bool((lse[:, :dead] == -math.inf).all())
+    keep = torch.ones(T, T, dtype=torch.bool, device="cuda").tril()
+    for h in range(hq):
+        s = (q[dead:, h].double() @ k[:, h * hk // hq].double().T * D ** -0.5)
+        s = s.masked_fill(~keep[dead:], -math.inf)
+        p, x = torch.softmax(s, 1), v[:, h * hk // hq].double()
+        R.within("out", out[dead:, h], p @ x, (R.U + R.EPS) * (p @ x.abs()) + R.U * (p @ x).abs())
+        want = torch.logsumexp(s, 1)
+        R.within("lse", lse[h, dead:], want, 1e-5 + 1e-5 * want.abs())
