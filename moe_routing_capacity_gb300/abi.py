@@ -8,6 +8,7 @@ in the library's kernels; if the library is missing this module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -264,6 +265,13 @@ def _stream(stream=None):
     if stream is None:   # the current stream's handle, without building a Stream object
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
+
+
+def on_stream(stream=None):
+    """Context in which tensors are allocated and cleared for use on ``stream``
+    (None: the current one).  Memory taken under another stream's name may
+    still be written by work queued there."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _check(fn, rc):
@@ -700,9 +708,10 @@ class AttentionPlan:
         _check("moe_attention_workspace", lib().moe_attention_workspace(
             ctypes.byref(self._config()), ctypes.byref(pb), ctypes.byref(bb)))
         self.backward_ws_bytes = bb.value
-        self.status = (torch.zeros(1, dtype=i32, device=cu_seqlens.device) if status is None
-                       else status)
-        self.plan = torch.empty(pb.value, dtype=u8, device=cu_seqlens.device)
+        with on_stream(stream):
+            self.status = (torch.zeros(1, dtype=i32, device=cu_seqlens.device) if status is None
+                           else status)
+            self.plan = torch.empty(pb.value, dtype=u8, device=cu_seqlens.device)
         self.address = self.plan.data_ptr()
         self.q_shape, self.k_shape = (T, n_heads, head_dim), (T, n_kv_heads, head_dim)
         self.lse_shape = (n_heads, T)

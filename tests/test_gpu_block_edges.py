@@ -238,3 +238,18 @@ def test_keys_without_weight(rng, hq, hk):
         R.within("out", out[dead:, h], p @ x, (R.U + R.EPS) * (p @ x.abs()) + R.U * (p @ x).abs())
         want = torch.logsumexp(s, 1)
         R.within("lse", lse[h, dead:], want, 1e-5 + 1e-5 * want.abs())
+
+
+# ------------------------------------------------------------------ other streams
+
+def test_a_plan_on_another_stream_clears_its_status_there():
+    """Not on the current one, whose queued work would put the clear behind the
+    plan and its error."""
+    cu, side = ints(0, 50, 40), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    plan = abi.AttentionPlan(cu, 100, 2, 1, 64, stream=side)
+    side.synchronize()
+    assert int(plan.status.cpu()) == abi.MOE_EINVAL
+    torch.cuda.synchronize()
+    assert int(plan.status.cpu()) == abi.MOE_EINVAL
