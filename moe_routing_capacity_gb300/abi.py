@@ -775,9 +775,10 @@ def attention_backward(plan, q, k, v, out, rest, lse, dout, dq, dk, dv, ws, stat
 
 class GradSet:
     """The gradients of one model: contiguous fp32 or bf16 tensors, and where
-    the clipped ones go (``outs``; None: in place).  Holds the tensors."""
+    the clipped ones go (``outs``; None: in place).  Holds the tensors, and
+    scratch for calls on ``stream``."""
 
-    def __init__(self, tensors, outs=None):
+    def __init__(self, tensors, outs=None, stream=None):
         outs = tensors if outs is None else outs
         if len(tensors) != len(outs):
             raise ValueError("one output a tensor")
@@ -794,7 +795,8 @@ class GradSet:
         _check("moe_grad_clip_workspace",
                lib().moe_grad_clip_workspace(len(self.tensors), ctypes.byref(v)))
         dev = self.tensors[0].device if self.tensors else None
-        self.ws = torch.empty(max(1, v.value), dtype=u8, device=dev) if dev else None
+        with on_stream(stream):
+            self.ws = torch.empty(max(1, v.value), dtype=u8, device=dev) if dev else None
 
 
 def grad_clip(grads, max_norm, norm, stream=None):

@@ -95,12 +95,13 @@ class TrainingBlock:
         n_qkv, qd = (hq + 2 * hk) * D, hq * D
         if not hasattr(self, "g"):
             e = lambda *s, dt=F32: torch.empty(s, dtype=dt, device=self.layer.device)  # noqa: E731
-            self.g = {n: e(*t.shape) for n, t in w.items()}
-            self.g["h"] = e(T, d, dt=BF)
-            self.db, self.dh2, self.dn1 = (e(T, d, dt=BF) for _ in range(3))
-            self.datt, self.dqkv = e(T, hq, D, dt=BF), e(T, hq + 2 * hk, D, dt=BF)
-            self.ws_norm = e(abi.norm_residual_workspace(T, d), dt=torch.uint8)
-            self.ws_att = e(max(1, self.plan.backward_ws_bytes), dt=torch.uint8)
+            with abi.on_stream(stream):
+                self.g = {n: e(*t.shape) for n, t in w.items()}
+                self.g["h"] = e(T, d, dt=BF)
+                self.db, self.dh2, self.dn1 = (e(T, d, dt=BF) for _ in range(3))
+                self.datt, self.dqkv = e(T, hq, D, dt=BF), e(T, hq + 2 * hk, D, dt=BF)
+                self.ws_norm = e(abi.norm_residual_workspace(T, d), dt=torch.uint8)
+                self.ws_att = e(max(1, self.plan.backward_ws_bytes), dt=torch.uint8)
         g = self.g
         abi.norm_residual_backward(None, dh3, self.b2, None, w["gate2"], w["w_post2"], None,
                                    self.rstd[3], None, self.db, self.dh2, g["gate2"],
@@ -134,5 +135,5 @@ class TrainingBlock:
         """Scale the weights' gradients of the last backward in place to a
         global 2-norm of at most max_norm; norm [1] fp32 receives it."""
         if not hasattr(self, "grad_set"):
-            self.grad_set = abi.GradSet([t for n, t in self.g.items() if n != "h"])
+            self.grad_set = abi.GradSet([t for n, t in self.g.items() if n != "h"], stream=stream)
         abi.grad_clip(self.grad_set, max_norm, norm, stream)

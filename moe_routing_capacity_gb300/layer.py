@@ -204,12 +204,13 @@ class PooledWaveMoE:
         ns, Hs = cfg.n_shared, cfg.h_shared
         if not hasattr(self, "bwd_ws"):
             self.bwd_layout = abi.backward_plan(cfg, ragged=self.dropless)
-            self.bwd_ws = torch.empty(max(1, self.bwd_layout.total), dtype=torch.uint8, device=dev)
-            f = lambda *sh: torch.empty(sh, dtype=torch.float32, device=dev)
-            self.grads = {"x": torch.empty(T, d, dtype=torch.bfloat16, device=dev),
-                          "Wr": f(E, d), "W_ld": f(L, d), "Wg": f(E, H, L), "Wu": f(E, H, L),
-                          "Wd": f(E, L, H), "W_lu": f(d, L), "Wsg": f(ns, Hs, d),
-                          "Wsu": f(ns, Hs, d), "Wsd": f(ns, d, Hs)}
+            with abi.on_stream(stream):
+                self.bwd_ws = torch.empty(max(1, self.bwd_layout.total), dtype=torch.uint8, device=dev)
+                f = lambda *sh: torch.empty(sh, dtype=torch.float32, device=dev)
+                self.grads = {"x": torch.empty(T, d, dtype=torch.bfloat16, device=dev),
+                              "Wr": f(E, d), "W_ld": f(L, d), "Wg": f(E, H, L), "Wu": f(E, H, L),
+                              "Wd": f(E, L, H), "W_lu": f(d, L), "Wsg": f(ns, Hs, d),
+                              "Wsu": f(ns, Hs, d), "Wsd": f(ns, d, Hs)}
         hoff = self.plan.h_offset_bytes
         h_rows = self.plan.pool_rows if self.dropless else E * self.plan.c_recv
         h = self.ws_ffn[hoff:hoff + h_rows * H * 2].view(torch.bfloat16)

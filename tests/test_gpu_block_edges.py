@@ -8,6 +8,9 @@ import torch
 
 import block_reference as R
 from moe_routing_capacity_gb300 import abi
+from moe_routing_capacity_gb300 import workloads as wl
+from moe_routing_capacity_gb300.block import TrainingBlock, draw_block_weights
+from moe_routing_capacity_gb300.layer import PooledWaveMoE
 
 pytestmark = pytest.mark.gpu
 
@@ -253,3 +256,45 @@ def test_a_plan_on_another_stream_clears_its_status_there():
     assert int(plan.status.cpu()) == abi.MOE_EINVAL
     torch.cuda.synchronize()
     assert int(plan.status.cpu()) == abi.MOE_EINVAL
+
+
+def tiny_block(heads=4, kv_heads=2, D=32):
+    """A training block at the tiny layer's size, two sequences, its input."""
+    cfg = wl.TINY
+    inp = wl.make_inputs(cfg, "cpu")
+    table = empty(cfg.T, D // 2, 2, dt=F32)
+    abi.rotary_table(table)
+    blk = TrainingBlock(PooledWaveMoE(cfg, inp, "cuda"),
+                        draw_block_weights(cfg.d_model, heads, kv_heads, D, seed=5), heads,
+                        kv_heads, D, table, 2)
+    blk.set_batch(ints(0, 101, cfg.T), None)
+    return blk, inp["x"].cuda()
+
+
+def test_a_block_on_another_stream_takes_its_memory_there(rng):
+    """backward() and clip() allocate what they use on their stream: memory
+    that work queued on the current stream still writes is not theirs."""
+    runs = []
+    for side in (None, torch.cuda.Stream()):
+        blk, h = tiny_block()
+        dh = randn(torch.Generator(device="cuda").manual_seed(3), *h.shape)
+        norm = empty(1, dt=F32)
+        torch.cuda.synchronize()
+        blk.forward(h, stream=side)
+        if side:
+            # freed at once, written once the current stream gets there
+            junk = [empty(n) for t in (blk.qkv, blk.n1, blk.rstd[0], *blk.w.values())
+                    for n in {t.numel(), 2 * t.numel(), 4096}]
+            junk.append(empty(1 << 24))
+            torch.cuda.synchronize()
+            torch.cuda._sleep(200_000_000)
+            for t in junk:
+                t.fill_(float("nan"))
+            del t, junk
+        g = blk.backward(dh, stream=side)
+        blk.clip(0.5, norm, stream=side)
+        torch.cuda.synchronize()
+        assert int(blk.status) == 0
+        runs.append({n: t.clone() for n, t in g.items()} | {"norm": norm})
+    for n, t in runs[0].items():
+        assert torch.equal(t, runs[1][n]), n
