@@ -557,7 +557,8 @@ int moe_balance_update_window(const moe_config_t* cfg, const int32_t* idx, int64
  * attention over packed sequences, and the clipping of the gradients.  The
  * conventions above hold (device pointers, no allocation, no host
  * synchronisation, deterministic results); an empty call (T = 0, no tensors)
- * returns MOE_OK without touching its pointers. */
+ * returns MOE_OK without touching its pointers, but for the sums over tokens
+ * or tensors (weights' gradients, the norm): 0, where the pointer is given. */
 
 /* Norm after a branch, gate, residual sum, norm before the next branch:
  *   p = b * rstd_post,  rstd_post = 1/sqrt(mean(b^2) + eps)

@@ -803,8 +803,7 @@ def grad_clip(grads, max_norm, norm, stream=None):
     """norm[0] = the 2-norm over all tensors of the GradSet; each is scaled by
     min(1, max_norm / (norm + 1e-6)) into its output.  A norm that is not
     finite leaves the gradients as they are."""
-    if not grads.tensors:
-        return
+    ws = grads.ws
     _check("moe_grad_clip", lib().moe_grad_clip(
-        grads.records, len(grads.tensors), max_norm, _ptr(norm, f32), _ptr(grads.ws, u8),
-        grads.ws.numel(), _stream(stream)))
+        grads.records, len(grads.tensors), max_norm, _ptr(norm, f32),
+        _ptr(ws, u8, allow_none=True), 0 if ws is None else ws.numel(), _stream(stream)))

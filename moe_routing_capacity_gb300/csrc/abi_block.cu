@@ -17,6 +17,14 @@ int device_ok() {
     return moe::current_device(&dev, &sms);
 }
 
+// A sum over no terms: n floats at p (NULL: not wanted) become 0.
+int zero_sum(void* p, int64_t n, void* stream) {
+    if (!p) return MOE_OK;
+    if (const int rc = device_ok()) return rc;
+    return cudaMemsetAsync(p, 0, n * 4, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MOE_OK : MOE_ECUDA;
+}
+
 // Strides of a [T, heads, D] tensor: 16-byte steps wide enough that two rows
 // of heads never share an element (an extent of one has no stride).
 bool strides_ok(int64_t T, int64_t heads, int64_t D, int64_t st_t, int64_t st_h) {
@@ -86,7 +94,11 @@ int moe_norm_residual_backward(const moe_norm_t* cfg, const uint16_t* dn, const 
                                int64_t ws_bytes, void* stream) {
     MOE_NVTX_RANGE();
     if (const int rc = norm_ok(cfg)) return rc;
-    if (cfg->T == 0) return MOE_OK;
+    if (cfg->T == 0) {
+        if (const int rc = zero_sum(dw_post, cfg->d, stream)) return rc;
+        if (const int rc = zero_sum(dw_pre, cfg->d, stream)) return rc;
+        return zero_sum(cfg->gate_per_token ? nullptr : dgate, cfg->d, stream);
+    }
     const bool has_b = b != nullptr, has_n = dn != nullptr;
     if (!has_b && !has_n) return MOE_EINVAL;
     if (!dn && !dy) return MOE_EINVAL;
@@ -227,7 +239,7 @@ int moe_grad_clip(const moe_grad_tensor_t* tensors, int64_t n_tensors, float max
                   float* norm, void* ws, int64_t ws_bytes, void* stream) {
     MOE_NVTX_RANGE();
     if (n_tensors < 0 || n_tensors > (1 << 20) || !(max_norm > 0)) return MOE_EINVAL;
-    if (n_tensors == 0) return MOE_OK;
+    if (n_tensors == 0) return zero_sum(norm, 1, stream);
     if (!tensors || !norm || (reinterpret_cast<uintptr_t>(norm) & 3) || !given16(ws))
         return MOE_EINVAL;
     for (int64_t i = 0; i < n_tensors; ++i) {

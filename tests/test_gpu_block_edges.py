@@ -298,3 +298,29 @@ def test_a_block_on_another_stream_takes_its_memory_there(rng):
         runs.append({n: t.clone() for n, t in g.items()} | {"norm": norm})
     for n, t in runs[0].items():
         assert torch.equal(t, runs[1][n]), n
+
+
+# ------------------------------------------------------------------ nothing to sum
+
+@pytest.mark.parametrize("gate", ["none", "channel", "token"])
+def test_norm_gradients_of_no_token_are_zero(rng, gate):
+    T, d = 0, 64
+    w = randn(rng, d)
+    g = {"none": None, "channel": w, "token": empty(T, d)}[gate]
+    dgate = {"none": None, "channel": empty(d, dt=F32), "token": empty(T, d)}[gate]
+    dw_post, dw_pre = empty(d, dt=F32), empty(d, dt=F32)
+    x, s = empty(T, d), empty(T, dt=F32)
+    ws = torch.empty(max(1, abi.norm_residual_workspace(T, d)), device="cuda", dtype=torch.uint8)
+    abi.norm_residual_backward(x, x, x, x, g, w, w, s, s, empty(T, d), empty(T, d), dgate,
+                               dw_post, dw_pre, ws)
+    for t in (dw_post, dw_pre, dgate):
+        assert t is None or not t.any()
+
+
+def test_norm_of_no_gradients_is_zero():
+    norm = empty(1, dt=F32)
+    abi.grad_clip(abi.GradSet([]), 1.0, norm)
+    assert float(norm) == 0.0
+    norm = empty(1, dt=F32)
+    abi.grad_clip(abi.GradSet([empty(0, dt=F32), empty(0)]), 1.0, norm)
+    assert float(norm) == 0.0
