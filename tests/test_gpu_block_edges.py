@@ -324,3 +324,42 @@ def test_norm_of_no_gradients_is_zero():
     norm = empty(1, dt=F32)
     abi.grad_clip(abi.GradSet([empty(0, dt=F32), empty(0)]), 1.0, norm)
     assert float(norm) == 0.0
+
+
+# ------------------------------------------------------------------ gradients of zero and near it
+
+def best_ms(f, n=5):
+    best = math.inf
+    for _ in range(n):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        f()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b))
+    return best
+
+
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("size", [0.0, -0.0, 1e-11])
+def test_zero_and_small_gradients_take_no_longer(rng, dt, size):
+    """Experts that met no token have gradients of exactly zero."""
+    n = 100_000_000
+    x, out, norm = randn(rng, n, dt=dt), empty(n, dt=dt), empty(1, dt=F32)
+    small = x * size
+    sets = [abi.GradSet([t], [out]) for t in (x, small)]
+    ms = [best_ms(lambda s=s: abi.grad_clip(s, 1.0, norm)) for s in sets]
+    want = math.sqrt(float(small.double().square().sum()))
+    assert abs(float(norm) - want) <= 1e-6 * want
+    assert torch.equal(out, small)
+    assert ms[1] <= 1.2 * ms[0], ms
+
+
+@pytest.mark.parametrize("size", [1e-13, 1e-15, 1e-16, 1e-18])
+def test_norm_of_small_gradients(rng, size):
+    """About where the squares leave fp32's normal numbers."""
+    x = torch.randn(300_001, generator=rng, device="cuda") * size
+    norm = empty(1, dt=F32)
+    abi.grad_clip(abi.GradSet([x]), 1.0, norm)
+    want = math.sqrt(float(x.double().square().sum()))
+    assert abs(float(norm) - want) <= 1e-6 * want
