@@ -194,8 +194,11 @@ extern "C" {
 int moe_abi_version(void) { return 6; }
 
 int moe_check_status(void) {
-    const int v[4] = {check_status_route(), check_status_gemm(), check_status_backward(),
-                      check_status_expert_pair()};
+    const int v[9] = {check_status_route(),    check_status_gemm(),
+                      check_status_backward(), check_status_expert_pair(),
+                      check_status_norm(),     check_status_rotary(),
+                      check_status_attention_fwd(), check_status_attention_bwd(),
+                      check_status_clip()};
     for (int x : v)
         if (x) return x;
     return 0;

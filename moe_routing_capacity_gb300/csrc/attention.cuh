@@ -43,6 +43,12 @@ __device__ __forceinline__ void report_refused(const int32_t* header, int32_t* s
     if (blockIdx.x == 0 && threadIdx.x == 0 && header[kPlanRefused]) report_error(status, MOE_EINVAL);
 }
 
+// Checked builds: an entry of a list of blocks of `rows` rows is one of T tokens.
+__device__ __forceinline__ bool plan_entry_ok(const int4& e, int64_t T, int rows) {
+    return e.x >= 0 && e.y > 0 && static_cast<int64_t>(e.x) + e.y <= T &&
+           (e.z < 0 ? e.z == -1 && e.y <= rows : static_cast<int64_t>(e.z) * rows < e.y);
+}
+
 // The items of this CTA, heaviest first: dealt out to the CTAs in turn, every
 // other round from the other end, so that a CTA's early heavy item meets a
 // lighter one in the next round.
@@ -56,6 +62,12 @@ struct AttnItems {
             ++round;
             if (item < total) return true;
         }
+        return false;
+    }
+    // of a list of `rows` rows a block and `units` items an entry
+    __device__ bool next(int& item, const int4* tiles, int units, int64_t T, int rows, int site) {
+        while (next(item))
+            if (moe_check(plan_entry_ok(tiles[item / units], T, rows), site)) return true;
         return false;
     }
 };

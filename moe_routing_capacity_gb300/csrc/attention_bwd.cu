@@ -314,6 +314,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
     if (tile >= p.header[p.list]) return;
     const int kvh = item - tile * p.units;
     const int4 te = p.tiles[tile];
+    if (!moe_check(plan_entry_ok(te, p.T, 128), 1205)) return;
     const int64_t start = te.x;
     const int len = te.y;
     if (te.z < 0) {   // tokens of no sequence
@@ -779,6 +780,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
     const uint32_t tmP = tm + 128, tmQ = tm + 384;   // S at tm; dP alternates: + 128
     AttnItems items(p.header[p.list] * p.units);
     int item;
+    const auto next = [&] { return items.next(item, p.tiles, p.units, p.T, 128, 1204); };
 
     if (warp >= kMmaWarp) {
         setmaxnreg_dec<64>();
@@ -807,14 +809,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                 }
                 return true;
             };
-            bool ok = true, more = items.next(item);
+            bool ok = true, more = next();
             while (ok && more) {
                 const DqWork w(p, item);
                 if (lane == 0 && w.block >= 0) ok = issue(w);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 // this item's last tiles are under way: the next one's rows,
                 // which its D is formed from, into L2
-                if ((more = items.next(item))) RowDots<D>::prefetch(p, DqWork(p, item), lane);
+                if ((more = next())) RowDots<D>::prefetch(p, DqWork(p, item), lane);
             }
             if (lane == 0 && (!ok || *sm.abort_flag)) {   // let the armed copies land before leaving
                 volatile int no_abort = 0;
@@ -855,7 +857,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                 return true;
             };
             bool ok = true;
-            while (ok && items.next(item)) {
+            while (ok && next()) {
                 const DqWork w(p, item);
                 if (w.block < 0) continue;
                 if (!(ok = wait(sm.res_full, done++ & 1u) && scores(w.n == 1))) break;
@@ -888,7 +890,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
         // barrier, and does nothing else
         bool ok = true;
         DqWork w;
-        while (items.next(item)) {
+        while (next()) {
             w = DqWork(p, item);
             if (w.block < 0) {   // tokens of no sequence
                 uint16_t* o = p.dq + w.start * p.dq_t + w.h * p.dq_h;
@@ -1066,6 +1068,8 @@ int launch_pair(BwdParams& p, const AttnPlanLayout& l, const uint8_t* plan, int 
 }
 
 }  // namespace
+
+int check_status_attention_bwd() { return moe_check_read_reset(); }
 
 int64_t attention_backward_ws(int64_t T, int n_heads) { return 2 * T * n_heads * 4; }
 

@@ -168,7 +168,7 @@ template <class F>
 __device__ __forceinline__ void each_item(const FwdParams& p, F f) {
     AttnItems items(p.header[p.list] * p.units);
     int item;
-    while (items.next(item))
+    while (items.next(item, p.tiles, p.units, p.T, p.pair_heads ? 128 : 256, 1203))
         if (!f(FwdWork(p, item))) return;
 }
 
@@ -521,7 +521,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
 
 __global__ void __launch_bounds__(1024, 1)
     attn_plan_kernel(const int32_t* cu, int n_seqs, int64_t T, int4* q128, int4* kv128, int4* q256,
-                     int32_t* header, int32_t* cursor, int bins, int32_t* status) {
+                     int32_t* header, int32_t* cursor, int bins, int most128, int most256,
+                     int32_t* status) {
     __shared__ int part[32];
     __shared__ int carry, bad;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -590,6 +591,7 @@ __global__ void __launch_bounds__(1024, 1)
             const int first = cu[s], len = cu[s + 1] - first, nb = (len + bs - 1) / bs;
             for (int w = lane + 1; w <= nb; w += 32) {
                 const int at = atomicAdd(&cursor[w], 1);
+                if (!moe_check(at >= 0 && at < (pass ? most256 : most128), 1201)) continue;
                 if (pass) {
                     q256[at] = make_int4(first, len, w - 1, 0);
                 } else {
@@ -606,6 +608,7 @@ __global__ void __launch_bounds__(1024, 1)
             const int first = (i < nh ? 0 : cu[n_seqs]) + in * bs;
             const int len = min(bs, (i < nh ? head : static_cast<int>(T)) - first);
             const int4 e = make_int4(first, len, -1, 0);
+            if (!moe_check(total + i < (pass ? most256 : most128), 1202)) continue;
             if (pass) {
                 q256[total + i] = e;
             } else {
@@ -626,6 +629,8 @@ __global__ void __launch_bounds__(1024, 1)
 
 }  // namespace
 
+int check_status_attention_fwd() { return moe_check_read_reset(); }
+
 int64_t attention_plan_bytes(int64_t T, int n_seqs) { return attn_plan_layout(T, n_seqs).total; }
 
 int launch_attention_plan(int64_t T, int n_seqs, const int32_t* cu, void* plan, int32_t* status,
@@ -635,7 +640,8 @@ int launch_attention_plan(int64_t T, int n_seqs, const int32_t* cu, void* plan, 
     attn_plan_kernel<<<1, 1024, 0, st>>>(
         cu, n_seqs, T, reinterpret_cast<int4*>(b + l.q128), reinterpret_cast<int4*>(b + l.kv128),
         reinterpret_cast<int4*>(b + l.q256), reinterpret_cast<int32_t*>(b),
-        reinterpret_cast<int32_t*>(b + l.cursor), static_cast<int>(l.bins), status);
+        reinterpret_cast<int32_t*>(b + l.cursor), static_cast<int>(l.bins),
+        static_cast<int>(l.max128), static_cast<int>(l.max256), status);
     if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
     trace_after(st, "attn_plan");
     return MOE_OK;

@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(kClipThreads, 1)
         const int64_t at = static_cast<int64_t>(piece - b.first[k]) * kPiece;
         const int64_t left = b.t[k].numel - at;
         const int n = left < kPiece ? static_cast<int>(left) : kPiece;
+        if (!moe_check(k < b.n && at >= 0 && n > 0, 1231)) continue;
         if (b.kind[k] & 1)
             piece_squares<true>(b.t[k].in, at, n, b.kind[k] & 2, total);
         else
@@ -271,6 +272,7 @@ __global__ void __launch_bounds__(kClipThreads, 1)
         const int64_t at = static_cast<int64_t>(piece - b.first[k]) * kPiece;
         const int64_t left = b.t[k].numel - at;
         const int n = left < kPiece ? static_cast<int>(left) : kPiece;
+        if (!moe_check(k < b.n && at >= 0 && n > 0, 1232)) continue;
         if (b.kind[k] & 1)
             piece_scale<true>(in, out, at, n, b.kind[k] & 2, c);
         else
@@ -338,6 +340,8 @@ int run(const moe_grad_tensor_t* t, int64_t n, float max_norm, float* norm, doub
 }
 
 }  // namespace
+
+int check_status_clip() { return moe_check_read_reset(); }
 
 int64_t grad_clip_ws(int64_t n_tensors) {
     const int64_t batches = n_tensors <= 64 ? 1 : (n_tensors + 511) / 512;

@@ -291,6 +291,12 @@ int launch_combine(const uint16_t* ypool, const int32_t* slot_of, const float* w
 
 // ---------------------------------------------------------------- training block
 
+int check_status_norm();
+int check_status_rotary();
+int check_status_attention_fwd();
+int check_status_attention_bwd();
+int check_status_clip();
+
 int launch_norm_residual(const moe_norm_t& c, const uint16_t* b, const void* r,
                          const uint16_t* gate, const uint16_t* w_post, const uint16_t* w_pre,
                          void* y, uint16_t* n, float* rstd_post, float* rstd_pre,

@@ -41,6 +41,7 @@ struct NormParams {
     float *rstd_post, *rstd_pre;          // forward: out
     const float *in_post, *in_pre;        // backward: in
     float* part;                           // [CTAs, 2, d]
+    int64_t part_rows;                     // that the scratch has
 };
 
 // Eight channels as four pairs.
@@ -388,6 +389,7 @@ __global__ void __launch_bounds__(NT, OCC) norm_bwd_kernel(const NormParams p) {
         ry = ry_next;
     }
     // this CTA's partial sums over its tokens: S, then dw_pre
+    if (!moe_check(blockIdx.x < p.part_rows, 1211)) return;
     float* part = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.d;
     float* acc = reinterpret_cast<float*>(ring);
     const int turns = WARP ? rows : 1;
@@ -566,6 +568,8 @@ NormParams norm_params(const moe_norm_t& c, const uint16_t* b, const void* r, co
 
 }  // namespace
 
+int check_status_norm() { return moe_check_read_reset(); }
+
 int launch_norm_residual(const moe_norm_t& c, const uint16_t* b, const void* r,
                          const uint16_t* gate, const uint16_t* w_post, const uint16_t* w_pre,
                          void* y, uint16_t* n, float* rstd_post, float* rstd_pre,
@@ -608,6 +612,7 @@ int launch_norm_residual_backward(const moe_norm_t& c, const uint16_t* dn, const
     p.in_post = rstd_post;
     p.in_pre = rstd_pre;
     p.part = static_cast<float*>(ws);
+    p.part_rows = norm_backward_ws(c.T, c.d) / (8 * c.d);
     const int slots = 2 + (p.gate_mode == 2) + (c.res_f32 ? 4 : 2);
     const Shape s = norm_shape(c.T, c.d, slots, sms < 160 ? sms : 160, true);
     p.stages = s.stages;

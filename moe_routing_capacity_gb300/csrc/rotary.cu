@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(const RotaryPara
     const int c0 = rot ? (PAIRS ? 16 * u : 8 * u) : rest;
     const int c1 = rot ? (PAIRS ? c0 + 8 : c0 + p.half) : rest + 8;
     const bool two = c1 < p.D;
+    if (!moe_check(c0 + 8 <= p.D && (!two || c1 + 8 <= p.D) && split < p.splits, 1221)) return;
     float2 cs[8];
     if (rot) {
         const float4* tab = reinterpret_cast<const float4*>(p.table + (pos * p.half + 8 * u) * 2);
@@ -145,6 +146,8 @@ __global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(const RotaryPara
 }
 
 }  // namespace
+
+int check_status_rotary() { return moe_check_read_reset(); }
 
 int launch_rotary_table(const moe_rotary_table_t& c, float* table, cudaStream_t st) {
     const double base = c.scaling == 2
