@@ -363,3 +363,44 @@ def test_norm_of_small_gradients(rng, size):
     abi.grad_clip(abi.GradSet([x]), 1.0, norm)
     want = math.sqrt(float(x.double().square().sum()))
     assert abs(float(norm) - want) <= 1e-6 * want
+
+
+# ------------------------------------------------------------------ what the block hands on
+
+def test_the_moe_branch_gets_its_own_gradient(rng):
+    """The gradient that the block gives the MoE layer is the second residual
+    norm's; dx of that call, and its weights' gradients, are what it uses and
+    returns."""
+    blk, h = tiny_block()
+    dh3 = randn(rng, *h.shape)
+    blk.forward(h)
+    seen, plain = {}, blk.layer.backward
+
+    def backward(x, dout, stream=None):
+        seen.update(x=x.clone(), dout=dout.clone())
+        got = plain(x, dout, stream=stream)
+        seen["dx"] = got["x"].clone()
+        return got
+
+    blk.layer.backward = backward
+    got = {n: t.clone() for n, t in blk.backward(dh3).items()}
+    assert torch.equal(seen["x"], blk.n2)
+    w = blk.w
+    want = R.norm_backward(None, dh3, blk.b2, blk.h2, w["gate2"], w["w_post2"], None, 1.0, 1.0,
+                           1e-6)
+    # rows cancel (dp - p mean(dp p)): bounded against the tensor's size
+    R.within("db2", seen["dout"], want["db"],
+             2e-5 * float(want["db"].abs().max()) + R.U * want["db"].abs())
+    alone = plain(blk.n2, seen["dout"])
+    assert torch.equal(alone["x"], seen["dx"])
+    names = [n for n, t in alone.items() if n != "x" and t.numel()]
+    assert names and sorted("moe." + n for n in names) == sorted(n for n in got if n.startswith("moe."))
+    for n in names:
+        assert torch.equal(got["moe." + n], alone[n]), n
+    # dn2, used in the first residual norm's backward: dgate1 depends on it
+    du = R.norm_backward(seen["dx"], dh3, blk.b1, h, w["gate1"], w["w_post1"], w["w_pre2"], 1.0, 1.0,
+                         1e-6)
+    size = float(du["dgate"].abs().max())
+    # dy of that call is the stream's gradient, dh3 itself (alpha 1, no norm behind h3)
+    R.within("dgate1", got["gate1"], du["dgate"], 2e-5 * size)
+    R.within("dw_pre2", got["w_pre2"], du["dw_pre"], 2e-5 * float(du["dw_pre"].abs().max()))
