@@ -34,7 +34,7 @@ inline AttnPlanLayout attn_plan_layout(int64_t T, int n_seqs) {
     l.kv128 = l.q128 + l.max128 * 16;
     l.q256 = l.kv128 + l.max128 * 16;
     l.cursor = l.q256 + l.max256 * 16;
-    l.total = l.cursor + 2 * l.bins * 4;
+    l.total = l.cursor + l.bins * 4;
     return l;
 }
 
