@@ -233,20 +233,6 @@ __device__ __forceinline__ void mma_tokens_quarters(uint32_t leader, uint32_t d_
                accumulate || kk > 0);
 }
 
-// Zeroes the rows from `rows` on of a tile that has landed, by a whole warp and
-// before a product may read it.
-template <int D>
-__device__ __forceinline__ void zero_tile_rows(uint32_t tile, int rows) {
-    for (uint32_t o = rows * 128 + (threadIdx.x & 31) * 16; o < kBoxBytes; o += 512)
-#pragma unroll
-        for (int b = 0; b < D / 64; ++b)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + b * kBoxBytes + o),
-                         "r"(0)
-                         : "memory");
-    fence_proxy_async_smem();
-    __syncwarp();
-}
-
 // Brings the 128-byte line at `p` into L2.  (As bulk prefetches, one a row,
 // 384 of them held their warps up for 6000 cycles.)
 __device__ __forceinline__ void prefetch_l2(const void* p) {
@@ -260,7 +246,8 @@ __device__ __forceinline__ uint32_t bits_from(int i) {
     return i >= 32 ? 0u : ~0u << max(i, 0);
 }
 
-// 2^x (flushing denormal results): the hardware's own exponential.
+// 2^x (flushing denormal results): the hardware's own exponential, good to 2 units
+// of fp32's last place, 2^-14 of the rounding of P to bf16 that follows it.
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -322,33 +309,78 @@ __device__ __forceinline__ uint16_t f32_bf16(float v) {
     return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// x . y over D channels, 16 bytes a load.
-__device__ __forceinline__ float dot_bf16(const uint16_t* x, const uint16_t* y, int D) {
-    float2 s = make_float2(0.f, 0.f);
-    for (int c = 0; c < D; c += 8) {
-        const uint4 a = *reinterpret_cast<const uint4*>(x + c);
-        const uint4 b = *reinterpret_cast<const uint4*>(y + c);
-        s = fma2(bf16x2_f32(a.x), bf16x2_f32(b.x), s);
-        s = fma2(bf16x2_f32(a.y), bf16x2_f32(b.y), s);
-        s = fma2(bf16x2_f32(a.z), bf16x2_f32(b.z), s);
-        s = fma2(bf16x2_f32(a.w), bf16x2_f32(b.w), s);
-    }
-    return s.x + s.y;
-}
-
 // ------------------------------------------------------------------ values that are not finite
 //
 // The products run over whole blocks: a hidden pair's P and dS are 0, but 0
-// times NaN or infinity is NaN.  Only the diagonal block has hidden pairs (the
-// rows behind a sequence's end, which dK and dV meet in every block of keys,
-// are zeroed before they are read), so a hidden value can have spoilt a row
-// only if it stands there, and at most the 128 rows of its own block.  Those rows are done again by the
-// definition on the CUDA cores, a pair a lane.  A row that sees the NaN itself
-// holds its answer already and is left as it is: one NaN at a sequence's start
-// reaches all its later rows and costs nothing more.
+// times NaN or infinity is NaN.  Hidden pairs stand in the diagonal block (and
+// behind a sequence's end, which dK and dV meet in every block of keys).  Where
+// the operand that multiplies P or dS there (V, K, dO, Q) holds such a value,
+// it becomes 0 in shared memory before the product, and the rows that do see
+// it get it back at the end, from memory (*_visible): what a token does not
+// see changes no bit of its results, and no row is worked out a second time.
+//   The forward has a warp look at V on its way from the copy to the products
+// (8192 tokens, 16/4 heads: 80 -> 84 us; by the softmax warps 84 to 88; a second pass,
+// only where a result was not finite, 92 for the code it adds to the loops); dQ's forming warps look at K while they
+// wait for the scores; dK and dV know from the queries' lse and D, which are not
+// finite where Q or dO is not.
 
+// Bits 15 and 31: the word's bf16 halves that are NaN or infinite.
+__device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
+    return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
 __device__ __forceinline__ bool bf16_odd(uint32_t v) { return (v & 0x7F80u) == 0x7F80u; }
-__device__ __forceinline__ bool bf16_nan(uint32_t v) { return (v & 0x7FFFu) > 0x7F80u; }
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared16(uint32_t at, const uint4& v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w)
+                 : "memory");
+}
+
+// Whether this thread's share (the tid-th of `threads`) of a landed tile holds a
+// value that is not finite.
+template <int D>
+__device__ __forceinline__ bool odd_tile(uint32_t tile, int tid, int threads) {
+    uint32_t odd = 0;
+#pragma unroll 8
+    for (uint32_t o = tid * 16; o < 256 * D; o += threads * 16) {
+        const uint4 v = ld_shared16(tile + o);
+        odd |= odd_halves(v.x) | odd_halves(v.y) | odd_halves(v.z) | odd_halves(v.w);
+    }
+    return odd != 0;
+}
+
+// Such values of the share become 0, for the products too.
+template <int D>
+__device__ __noinline__ void clean_tile(uint32_t tile, int tid, int threads) {
+    const auto keep = [](uint32_t w) { return w & ~((odd_halves(w) >> 15) * 0xFFFFu); };
+#pragma unroll 1
+    for (uint32_t o = tid * 16; o < 256 * D; o += threads * 16) {
+        const uint4 v = ld_shared16(tile + o);
+        st_shared16(tile + o, make_uint4(keep(v.x), keep(v.y), keep(v.z), keep(v.w)));
+    }
+    fence_proxy_async_smem();
+}
+
+// Such values of a row of it, by a warp.
+template <int D>
+__device__ __forceinline__ void clean_row(uint32_t tile, int row) {
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b) {
+        const uint32_t at = tile + b * kBoxBytes + row * 128 + (threadIdx.x & 31) * 4;
+        uint32_t w;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+        w &= ~((odd_halves(w) >> 15) * 0xFFFFu);
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(w) : "memory");
+    }
+}
 
 template <int N>
 __device__ __forceinline__ void setmaxnreg_inc() {

@@ -17,12 +17,16 @@
 // columns of its TMEM lane), warp 16 issues the MMAs, warp 17 the TMA loads.
 // P and dS return to the columns of S and dP as bf16 A operands.
 //   8192 tokens in 4 sequences, 16/4 heads of 128 (one product 25 us at a library
-// product's rate): dQ 127 us, dK and dV 139 us.  dK and dV: a round of 128 x 128
-// pairs takes 2300 cycles, of which the tensor cores work 2048 and shared memory
-// is read and filled all of them; the CTA with the longest column has 96 rounds
-// and 8 us of start and end.  dQ: 2200 cycles a round (products 1536, the
-// operands' way through shared memory 1750, and P and dS of a block follow each
-// other), 6500 between two pieces of work (D, the store of dQ).
+// product's rate): dQ 127 us, dK and dV 141 us.  dK and dV: the longest column of
+// blocks is 104 rounds of 128 x 128 pairs (26 blocks, 4 heads) where an even share
+// would be 84, and sets the time: about 2450 cycles a round and 8 us of start and
+// end.  The products of a round are 2048 of them, and so is their operands' way
+// through shared memory (computed from the tiles' bytes; no counter shows it).
+// dQ: 2200 cycles a round (products 1536, operands 1750, computed likewise, and P
+// and dS of a block follow each other), 6500 between two pieces of work (D, the
+// store of dQ).  Head widths 72 to 120 run the products of 128: 16384 tokens in 7,
+// 48/8 heads, dQ and dK/dV of 128 790 and 891 us, of 96 784 and 877, of 80 765 and
+// 852, of 64 600 and 700.
 #include <cstring>
 
 #include "attention.cuh"
@@ -54,135 +58,40 @@ struct BwdParams {
     int32_t* status;
 };
 
-// ------------------------------------------------------------------ rows by the definition
+// ------------------------------------------------------------------ what rows see that is not finite
 
-// (attention.cuh says when.)  One warp a row, 32 columns [c0, c0 + 32) of it,
-// a column a lane; the sum over the pairs takes 32 pairs, a pair a lane, then
-// their weights one after another.
-
-// The rows of the 32 from row0 on that a hidden key of the diagonal block can
-// have spoilt in these columns of dQ, as bits.
-__device__ __forceinline__ uint32_t dq_spoilt(const BwdParams& p, int64_t start, int row0, int kvh,
-                                            int c0) {
-    const int c = c0 + (threadIdx.x & 31), r0 = row0 & 127;
-    const int64_t first = start + row0 - r0;
-    const int n = static_cast<int>(min(static_cast<int64_t>(128), p.T - first));
-    int last = -1;
-    if (c < p.D)
-        for (int j = 0; j < n; ++j)
-            if (bf16_odd(p.k[(first + j) * p.k_t + kvh * p.k_h + c])) last = j;
-    last = __reduce_max_sync(0xFFFFFFFFu, last);
-    return ~bits_from(last - r0);   // rows before it
+// Rows [row0, row0 + 32) of columns [c0, c0 + 32) of dQ: a column in which a key of
+// the row's own block that it sees is not finite is NaN (either the row's lse
+// is, or the key's weight is 0).  A column a lane.
+__device__ __noinline__ void dq_visible(const BwdParams& p, int64_t start, int len, int row0, int h,
+                                        int kvh, int c0) {
+    const int c = c0 + (threadIdx.x & 31);
+    if (c >= p.D) return;
+    bool odd = false;
+    for (int j = row0 & ~127; j < min(row0 + 32, len); ++j) {
+        odd |= bf16_odd(p.k[(start + j) * p.k_t + kvh * p.k_h + c]);
+        if (odd && j >= row0) p.dq[(start + j) * p.dq_t + h * p.dq_h + c] = 0x7FFF;
+    }
 }
 
-__device__ __forceinline__ void dq_row(const BwdParams& p, int64_t start, int row, int h, int kvh,
-                                    int c0, float lse2, float delta) {
-    const int lane = threadIdx.x & 31, c = c0 + lane;
-    const int64_t t = start + row;
-    const uint16_t* q = p.q + t * p.q_t + h * p.q_h;
-    const uint16_t* g = p.dout + t * p.do_t + h * p.do_h;
-    const uint16_t* k = p.k + start * p.k_t + kvh * p.k_h;
-    const uint16_t* v = p.v + start * p.v_t + kvh * p.v_h;
-    float acc = 0.f;
-    for (int j0 = 0; j0 <= row; j0 += 32) {
-        const int n = min(32, row + 1 - j0);
-        float ds = 0.f;
-        if (lane < n) {
-            const int j = j0 + lane;
-            ds = exp2f(dot_bf16(q, k + j * p.k_t, p.D) * p.scale_log2 - lse2) *
-                 (dot_bf16(g, v + j * p.v_t, p.D) - delta);
+// Key rows [row0, row0 + 32) of columns [c0, c0 + 32) of dV: adds what of the
+// gradients of the queries of its own block, from the key on, is not finite.
+// (dK needs nothing: such a query's lse or D is not finite, and so is its dS.)
+__device__ __noinline__ void dv_visible(const BwdParams& p, int64_t start, int len, int row0, int kvh,
+                                        int c0) {
+    const int c = c0 + (threadIdx.x & 31);
+    if (c >= p.D) return;
+    float sum = 0.f;   // of what is not finite among the queries so far
+    for (int i = min((row0 & ~127) + 128, len) - 1; i >= row0; --i) {
+        for (int h = kvh * p.group; h < (kvh + 1) * p.group; ++h) {
+            const uint16_t g = p.dout[(start + i) * p.do_t + h * p.do_h + c];
+            if (bf16_odd(g)) sum += bf16_f32(g);
         }
-#pragma unroll 4
-        for (int e = 0; e < n; ++e) {
-            const float x = __shfl_sync(0xFFFFFFFFu, ds, e);
-            if (c < p.D) acc += x * bf16_f32(k[(j0 + e) * p.k_t + c]);
+        if (sum != 0.f && i < row0 + 32) {
+            uint16_t* o = p.dv + (start + i) * p.dv_t + kvh * p.dv_h + c;
+            *o = f32_bf16(bf16_f32(*o) + sum);
         }
     }
-    if (c < p.D) p.dq[t * p.dq_t + h * p.dq_h + c] = f32_bf16(acc * p.scale);
-}
-
-// Those of the rows row0 + (bit of `rows`), by a warp whose lanes hold their
-// rows' lse2 and D.
-__device__ __noinline__ void dq_redo(const BwdParams& p, int64_t start, int row0, int h, int kvh,
-                                     int c0, uint32_t rows, float lse2, float delta) {
-    rows &= dq_spoilt(p, start, row0, kvh, c0);
-    for (; rows; rows &= rows - 1) {
-        const int s = __ffs(rows) - 1;
-        dq_row(p, start, row0 + s, h, kvh, c0, __shfl_sync(0xFFFFFFFFu, lse2, s),
-               __shfl_sync(0xFFFFFFFFu, delta, s));
-    }
-}
-
-// The rows of the 32 from key row0 on that a hidden query of the diagonal block
-// can have spoilt in these columns of dV (which = 0) or dK (1), as bits: a
-// query before the key holds a value that is not finite, and none from the key
-// on (in this block) makes the sum NaN by itself.
-__device__ __forceinline__ uint32_t dkv_spoilt(const BwdParams& p, int64_t start, int len, int row0,
-                                            int kvh, int which, int c0) {
-    const int lane = threadIdx.x & 31, c = c0 + lane, r0 = row0 & 127;
-    const int64_t first = start + row0 - r0;
-    const int n = min(128, len - (row0 - r0));
-    int first_odd = 128, last_nan = -1;
-    for (int h = kvh * p.group; h < (kvh + 1) * p.group; ++h) {
-        const uint16_t* x = which ? p.q + first * p.q_t + h * p.q_h
-                                  : p.dout + first * p.do_t + h * p.do_h;
-        const int64_t step = which ? p.q_t : p.do_t;
-        if (c < p.D)
-            for (int i = 0; i < n; ++i) {
-                const uint32_t v = x[i * step + c];
-                if (bf16_odd(v)) first_odd = min(first_odd, i);
-                if (bf16_nan(v)) last_nan = max(last_nan, i);
-            }
-        // P or dS itself NaN: every column of every key up to the query
-        int all = -1;
-        for (int i = lane; i < n; i += 32)
-            if (isnan(p.lse2[h * p.T + first + i]) || (which && isnan(p.delta[h * p.T + first + i])))
-                all = i;
-        last_nan = max(last_nan, __reduce_max_sync(0xFFFFFFFFu, all));
-    }
-    uint32_t rows = 0;
-    for (int i = 0; i < 32; ++i)
-        if (__any_sync(0xFFFFFFFFu, first_odd < r0 + i && last_nan < r0 + i)) rows |= 1u << i;
-    return rows;
-}
-
-__device__ __forceinline__ void dkv_row(const BwdParams& p, int64_t start, int len, int row, int kvh,
-                                     int which, int c0) {
-    const int lane = threadIdx.x & 31, c = c0 + lane;
-    const int64_t t = start + row;
-    const uint16_t* k = p.k + t * p.k_t + kvh * p.k_h;
-    const uint16_t* v = p.v + t * p.v_t + kvh * p.v_h;
-    float acc = 0.f;
-    for (int h = kvh * p.group; h < (kvh + 1) * p.group; ++h) {
-        const uint16_t* q = p.q + start * p.q_t + h * p.q_h;
-        const uint16_t* g = p.dout + start * p.do_t + h * p.do_h;
-        const uint16_t* x = which ? q : g;
-        const int64_t step = which ? p.q_t : p.do_t;
-        for (int i0 = row; i0 < len; i0 += 32) {
-            const int n = min(32, len - i0);
-            float w = 0.f;
-            if (lane < n) {
-                const int i = i0 + lane;
-                const int64_t at = h * p.T + start + i;
-                w = exp2f(dot_bf16(k, q + i * p.q_t, p.D) * p.scale_log2 - p.lse2[at]);
-                if (which) w *= dot_bf16(v, g + i * p.do_t, p.D) - p.delta[at];
-            }
-#pragma unroll 4
-            for (int e = 0; e < n; ++e) {
-                const float y = __shfl_sync(0xFFFFFFFFu, w, e);
-                if (c < p.D) acc += y * bf16_f32(x[(i0 + e) * step + c]);
-            }
-        }
-    }
-    uint16_t* o = which ? p.dk + t * p.dk_t + kvh * p.dk_h : p.dv + t * p.dv_t + kvh * p.dv_h;
-    if (c < p.D) o[c] = f32_bf16(which ? acc * p.scale : acc);
-}
-
-// Those of the rows row0 + (bit of `rows`), by a warp.
-__device__ __noinline__ void dkv_redo(const BwdParams& p, int64_t start, int len, int row0,
-                                      int kvh, int which, int c0, uint32_t rows) {
-    rows &= dkv_spoilt(p, start, len, row0, kvh, which, c0);
-    for (; rows; rows &= rows - 1) dkv_row(p, start, len, row0 + __ffs(rows) - 1, kvh, which, c0);
 }
 
 __device__ __forceinline__ void zero_rows(uint16_t* base, int64_t st_t, int D, int rows) {
@@ -191,10 +100,8 @@ __device__ __forceinline__ void zero_rows(uint16_t* base, int64_t st_t, int D, i
             make_uint4(0, 0, 0, 0);
 }
 
-// Columns [c0, c0 + 32) of the warp's 32 accumulator rows, times `f`, as bf16;
-// returns whether a value of this thread's row was not finite.
-__device__ __forceinline__ bool take_rows(uint32_t taddr, int c0, float f, uint4 (&v)[4]) {
-    float2 sick = make_float2(0.f, 0.f);   // NaN once a value is not finite
+// Columns [c0, c0 + 32) of the warp's 32 accumulator rows, times `f`, as bf16.
+__device__ __forceinline__ void take_rows(uint32_t taddr, int c0, float f, uint4 (&v)[4]) {
     uint32_t a[32];
     tmem_ld32(taddr + c0, a);
 #pragma unroll
@@ -205,12 +112,10 @@ __device__ __forceinline__ bool take_rows(uint32_t taddr, int c0, float f, uint4
             const float2 x = mul2(make_float2(__uint_as_float(a[8 * g + 2 * e]),
                                               __uint_as_float(a[8 * g + 2 * e + 1])),
                                   make_float2(f, f));
-            sick = fma2(x, make_float2(0.f, 0.f), sick);
             w[e] = pack_bf16x2(x.x, x.y);
         }
         v[g] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    return !(sick.x + sick.y == 0.f);
 }
 
 // Two resident tiles, a ring of ST streamed ones, NF of the rows' scalars, barriers.
@@ -219,11 +124,10 @@ struct BwdCfg {
     static constexpr int SCALARS = NF;
     static constexpr int TILE = 128 * D * 2;
     static constexpr int STAGES = ST;
-    static constexpr int SMEM = 2 * TILE + STAGES * TILE + SCALARS * 4 + 320;
+    static constexpr int SMEM = 2 * TILE + STAGES * TILE + SCALARS * 4 + 272;
 };
-// Warps 0-15 form P and dS; then the MMA warp, the load warp, the warp that
-// zeroes rows behind a sequence's end (dK and dV; idle in dQ), an idle one.
-constexpr int kBwdThreads = 640, kMmaWarp = 16, kLoadWarp = 17, kTailWarp = 18, kFormers = 512;
+// Warps 0-15 form P and dS; then the MMA warp, the load warp, two idle ones.
+constexpr int kBwdThreads = 640, kMmaWarp = 16, kLoadWarp = 17, kFormers = 512;
 constexpr int dkv_stages(int D) { return D == 128 ? 4 : 8; }
 constexpr int dq_stages(int D) { return D == 128 ? 5 : 8; }
 template <int D>
@@ -238,9 +142,9 @@ struct BwdSmem {
     uint8_t *res, *ring;
     float* rows;   // scalars of query rows: dQ two blocks of 256, dK and dV 64 a warp
     uint64_t *full, *empty, *res_full, *res_empty, *s_full, *s_free, *dp_full, *p_full, *ds_full, *acc_full,
-        *acc_empty, *done, *sums_there, *sums_read, *tail_full;
+        *acc_empty, *done, *sums_there, *sums_read;
     uint32_t* tmem_slot;
-    volatile int* abort_flag;
+    volatile int *abort_flag, *odd_flag;   // odd: a value that is not finite was met
     __device__ explicit BwdSmem(uint8_t* raw_ptr) {
         res = raw_ptr;
         ring = res + 2 * C::TILE;
@@ -259,15 +163,14 @@ struct BwdSmem {
         done = acc_empty + 1;
         sums_there = done + 1;
         sums_read = sums_there + 1;
-        tail_full = sums_read + 1;
-        tmem_slot = reinterpret_cast<uint32_t*>(tail_full + C::STAGES);
+        tmem_slot = reinterpret_cast<uint32_t*>(sums_read + 1);
         abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+        odd_flag = abort_flag + 1;
     }
     __device__ void init(int parts) {   // parts: CTAs of a cluster
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
-            mbar_init(&tail_full[s], 1);
         }
         mbar_init(res_full, 1);
         mbar_init(s_full, 1);
@@ -284,6 +187,7 @@ struct BwdSmem {
         mbar_init(sums_there, 16 * parts);   // one arrival a warp and CTA
         mbar_init(sums_read, 16 * parts);
         *abort_flag = 0;
+        *odd_flag = 0;
         fence_mbar_init();
     }
 };
@@ -325,7 +229,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
     }
     const int nb = te.z, nblk = (len + 127) / 128;
     const int per_head = nblk - nb;          // query blocks of one head
-    const int end_rows = len - (nblk - 1) * 128;   // rows of the last one
     const int all = p.group * per_head;
     const int first = static_cast<int>(all * part / PARTS);
     const int n = static_cast<int>(all * (part + 1) / PARTS) - first;
@@ -362,7 +265,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                 load_tile<D>(ar + C::TILE, &p.mapV, sm.res_full, tok + nb * 128, kvh);
             }
             uint32_t st = 0, ph = 0, armed = 0, par = 0;
-            uint32_t tail_st = 0, tail_ph = 0;   // stages filled for the tail warp; its phases
             bool ok = true;
             int h = kvh * p.group + first / per_head, i = nb + first % per_head;
             for (int it = 0; it < 2 * n; ++it) {
@@ -370,14 +272,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                     ok = false;
                     break;
                 }
-                const bool tail = end_rows < 128 && i == nblk - 1;
-                uint64_t* landed = tail ? &sm.tail_full[st] : &sm.full[st];
-                mbar_arrive_expect_tx(landed, C::TILE);
+                mbar_arrive_expect_tx(&sm.full[st], C::TILE);
                 armed |= 1u << st;
-                par = (par & ~(1u << st)) | ((tail ? tail_ph >> st & 1u : ph) << st);
-                tail_st = (tail_st & ~(1u << st)) | (static_cast<uint32_t>(tail) << st);
-                if (tail) tail_ph ^= 1u << st;
-                load_tile<D>(ag + st * C::TILE, (it & 1) ? &p.mapO : &p.mapQ, landed,
+                par = (par & ~(1u << st)) | (ph << st);
+                load_tile<D>(ag + st * C::TILE, (it & 1) ? &p.mapO : &p.mapQ, &sm.full[st],
                              tok + i * 128, h);
                 if ((it & 1) && ++i == nblk) {
                     i = nb;
@@ -393,27 +291,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                 if (n) mbar_wait(sm.res_full, 0, &no_abort, nullptr, 20000000ull);
                 for (int s = 0; s < C::STAGES; ++s)
                     if (armed & (1u << s))
-                        mbar_wait(tail_st >> s & 1u ? &sm.tail_full[s] : &sm.full[s], (par >> s) & 1u,
-                                  &no_abort, nullptr, 20000000ull);
-            }
-        } else if (warp == kTailWarp && end_rows < 128) {
-            // -------------------------------------------------------- a sequence's end
-            // Its last block ends inside the tile: the rows behind it are other
-            // tokens', and what stands there (NaN, say, times P = 0) would reach
-            // every key.  Zeroed here, on the way from the copy to the products
-            // (by the MMA warp itself: 139 -> 150 us at the size above).
-            const uint32_t ag = smem_u32(sm.ring);
-            uint32_t st = 0, ph = 0;
-            int i = nb + first % per_head;
-            for (int it = 0; it < 2 * n; ++it) {
-                if (i == nblk - 1) {
-                    if (!warp_wait(&sm.tail_full[st], ph >> st & 1u, sm.abort_flag, p.status)) break;
-                    ph ^= 1u << st;
-                    zero_tile_rows<D>(ag + st * C::TILE, end_rows);
-                    if (lane == 0) mbar_arrive(&sm.full[st]);
-                }
-                if ((it & 1) && ++i == nblk) i = nb;
-                if (++st == C::STAGES) st = 0;
+                        mbar_wait(&sm.full[s], (par >> s) & 1u, &no_abort, nullptr, 20000000ull);
             }
         } else if (warp == kMmaWarp) {
             // -------------------------------------------------------- MMAs
@@ -478,8 +356,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
         float* rows = sm.rows + warp * 64;
         int qb = nb + first % per_head;
         int64_t at = (kvh * p.group + first / per_head) * p.T + start + c0 + lane;   // its head's row 0
+        // (Behind the sequence's end too, where they tell of the rows there.)
+        const int64_t left = p.T - start;
         const auto fetch = [&](const float* src) {
-            return qb * 128 + c0 + lane < len ? src[at + qb * 128] : 0.f;
+            return qb * 128 + c0 + lane < left ? src[at + qb * 128] : 0.f;
         };
         float l_next = n ? fetch(p.lse2) : 0.f, d_next = n ? fetch(p.delta) : 0.f;
         bool ok = true;
@@ -488,8 +368,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
             rows[lane] = l_next;
             rows[32 + lane] = d_next;
             __syncwarp();
+            const bool finite = l_next - l_next == 0.f && d_next - d_next == 0.f;
             const int limit = min(128, len - qb * 128);   // query rows in this block
-            const bool masked = qb == nb || limit < 128;
+            const bool diagonal = qb == nb, masked = diagonal || limit < 128;
+            // columns whose Q or dO may not be finite, where hidden pairs are
+            uint32_t odd = 0;
+            if (masked)
+                odd = __ballot_sync(0xFFFFFFFFu, !finite) & (diagonal ? ~0u : bits_from(limit - c0));
             // the columns that count: from the diagonal to the last row
             const uint32_t seen = bits_from((qb == nb ? r : 0) - c0) & ~bits_from(limit - c0);
             if (++qb == nblk) {
@@ -501,6 +386,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                 d_next = fetch(p.delta);
             }
 
+            if (odd) {   // not before S and dP are done with the tiles
+                const uint32_t q = 2 * it, st0 = q % C::STAGES, st1 = (q + 1) % C::STAGES;
+                if (!(ok = warp_wait(sm.s_full, it & 1u, sm.abort_flag, p.status) &&
+                           warp_wait(sm.dp_full, it & 1u, sm.abort_flag, p.status) &&
+                           warp_wait(&sm.full[st0], q / C::STAGES & 1u, sm.abort_flag, p.status) &&
+                           warp_wait(&sm.full[st1], (q + 1) / C::STAGES & 1u, sm.abort_flag,
+                                     p.status)))
+                    break;
+                const uint32_t ring = smem_u32(sm.ring);
+                for (uint32_t m = odd; m; m &= m - 1) {
+                    const int e = __ffs(m) - 1;
+                    if ((e & 3) != (warp & 3)) continue;   // four warps meet these columns
+                    clean_row<D>(ring + st0 * C::TILE, c0 + e);
+                    clean_row<D>(ring + st1 * C::TILE, c0 + e);
+                }
+                fence_proxy_async_smem();
+                if (lane == 0) *sm.odd_flag = 1;
+            }
             if (!(ok = warp_wait(sm.s_full, it & 1u, sm.abort_flag, p.status))) break;
             tc_fence_after();
             float x[32];
@@ -525,6 +428,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                 for (int i = 0; i < 32; ++i)
                     if (!(seen >> i & 1u)) x[i] = 0.f;
             }
+            // P, and dS below, as bf16: what the tensor cores take beside bf16 dO
+            // and Q, with fp32's range.  A rounding of at most 2^-8 a pair.
 #pragma unroll
             for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
             tmem_st16(ts, pk);
@@ -595,7 +500,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
             static_assert(PIECES <= 4, "one piece a warp at most");
             const int at0 = (static_cast<int>(part) * PIECES + quarter) * 32;
             const int which = at0 >= D, col = at0 - which * D;   // of [dV | dK]
-            uint32_t again = 0;
             if (ok && quarter < PIECES) {
                 const float f = which ? p.scale : 1.0f;
                 const int64_t st_t = which ? p.dk_t : p.dv_t;
@@ -628,21 +532,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                         if (row0 + rr < len && col + 4 * (lane & 7) < p.D)
                             *reinterpret_cast<uint2*>(o + rr * st_t) =
                                 make_uint2(pack_bf16x2(lo.x, lo.y), pack_bf16x2(hi.x, hi.y));
-                        const float sick = fmaf(lo.x + lo.y, 0.f, (hi.x + hi.y) * 0.f);
-                        const uint32_t b = __ballot_sync(0xFFFFFFFFu, !(sick == 0.f));
-#pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            if (b >> (8 * g) & 0xFFu) again |= 1u << (4 * (k0 + k) + g);
                     }
                 }
             }
+            bool odd = false;   // any part's queries
+#pragma unroll
+            for (int s = 0; s < PARTS; ++s)
+                odd |= ld_cluster(mapa_shared(smem_u32(const_cast<int*>(sm.odd_flag)), s)) != 0;
             // nobody leaves while its sums may still be read
             __syncwarp();   // (and a row's pieces come from eight lanes)
             if (lane < PARTS) mbar_arrive_cluster(mapa_shared(smem_u32(sm.sums_read), lane));
             mbar_wait_cluster(sm.sums_read, 0, p.status, 4 * kWaitTimeoutNs);
             __syncwarp();
-            again &= ~bits_from(len - row0);
-            if (again) dkv_redo(p, start, len, row0, kvh, which, col, again);
+            if (odd && ok && quarter < PIECES && !which) dv_visible(p, start, len, row0, kvh, col);
         } else if (ok) {   // 32 columns of [dV | dK] at a time
             for (int i = quarter; i < 2 * D / 32; i += 4) {
                 const int which = i >= D / 32, col = 32 * i - which * D;
@@ -650,12 +552,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                 uint16_t* o = (which ? p.dk + kvh * p.dk_h : p.dv + kvh * p.dv_h) +
                               (start + row0) * st_t;
                 uint4 v[4];
-                const bool bad = take_rows((which ? tmK : tmV) + lane_off, col,
-                                           which ? p.scale : 1.0f, v);
+                take_rows((which ? tmK : tmV) + lane_off, col, which ? p.scale : 1.0f, v);
                 store_quad(v, o, st_t, len - row0, col, p.D);
                 __syncwarp();   // a row's pieces come from four lanes
-                const uint32_t again = __ballot_sync(0xFFFFFFFFu, bad && row < len);
-                if (again) dkv_redo(p, start, len, row0, kvh, which, col, again);
+                if (!which && *sm.odd_flag) dv_visible(p, start, len, row0, kvh, col);
             }
         }
     }
@@ -746,9 +646,10 @@ struct RowDots {
                 if (w.n > 1 && w.block * 128 + row < w.len) p.delta[at + row] = d;
             }
         }
-        if (tid < 128) {
-            rows[128 + tid] = lse * kLog2e;
-            if (w.block * 128 + tid < w.len) p.lse2[at + tid] = lse * kLog2e;
+        if (tid < 128) {   // a row without a weight has none that a number could give
+            const float lse2 = lse == -INFINITY ? NAN : lse * kLog2e;
+            rows[128 + tid] = lse2;
+            if (w.block * 128 + tid < w.len) p.lse2[at + tid] = lse2;
         }
     }
 };
@@ -897,6 +798,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                 for (int i = threadIdx.x; i < w.len * (p.D / 8); i += kFormers)
                     *reinterpret_cast<uint4*>(o + (i / (p.D / 8)) * p.dq_t + i % (p.D / 8) * 8) =
                         make_uint4(0, 0, 0, 0);
+                // dK and dV take it that these rows may hold anything
+                for (int i = threadIdx.x; i < w.len; i += kFormers)
+                    p.lse2[w.h * p.T + w.start + i] = NAN;
                 continue;
             }
             float* rows = sm.rows + (done & 1u) * 256;
@@ -913,6 +817,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
             const float2 nl = make_float2(-lse2, -lse2);
             for (int j = 0; j < n; ++j, ++blocks) {
                 const uint32_t tp = tmP + 128 * (blocks & 1u) + lane_off + c0;
+                bool odd = false;
+                const uint32_t kst = blocks % KS;
+                if (j == n - 1) {   // the diagonal block's K
+                    ok = ok && warp_wait(&sm.full[kst], blocks / KS & 1u, sm.abort_flag, p.status);
+                    odd = ok && odd_tile<D>(smem_u32(sm.ring) + kst * C::TILE, threadIdx.x, kFormers);
+                }
                 if (!(ok = ok && warp_wait(sm.s_full, blocks & 1u, sm.abort_flag, p.status))) {
                     for (int i = 0; n == 1 && i < 2; ++i) named_bar_sync(1, kFormers);
                     break;
@@ -924,6 +834,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sm.s_free);
+                if (odd) {   // S is done with K, dQ still to come
+                    clean_tile<D>(smem_u32(sm.ring) + kst * C::TILE, threadIdx.x, kFormers);
+                    *sm.odd_flag = 1;
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float2 a = fma2(make_float2(x[2 * i], x[2 * i + 1]), c2, nl);
@@ -984,8 +898,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
             if (ok) {
                 tc_fence_after();
                 uint4 v[4];
-                bool bad = false;
-                if (c0 < D) bad = take_rows(tmQ + lane_off, c0, p.scale, v);
+                if (c0 < D) take_rows(tmQ + lane_off, c0, p.scale, v);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sm.acc_empty);
@@ -993,10 +906,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                     store_quad(v, p.dq + (w.start + row0) * p.dq_t + w.h * p.dq_h, p.dq_t,
                                w.len - row0, c0, p.D);
                 __syncwarp();   // a row's pieces come from four lanes
-                // (with a NaN lse or D the row is NaN throughout)
-                const uint32_t again =
-                    __ballot_sync(0xFFFFFFFFu, bad && valid && !isnan(lse2) && !isnan(delta));
-                if (again) dq_redo(p, w.start, row0, w.h, w.kvh, c0, again, lse2, delta);
+                if (*sm.odd_flag) dq_visible(p, w.start, w.len, row0, w.h, w.kvh, c0);
             }
         }
     }
@@ -1033,7 +943,9 @@ int launch_dkv(const BwdParams& p, int64_t items, cudaStream_t st) {
 // a head's work alone, against 1 / SMs of all the work for an even share.
 // Measured with 1, 2 and 4 CTAs a block, 16/4 heads: 8192 tokens in four sequences
 // 141, 148, 197 us, in one 336, 320, 371; 4096 in four 74, 51, 76, in one 166,
-// 94, 119; 1024 in one 49, 33, 25; 8/1 heads, 1024 in four 51, 33, 25.
+// 94, 119; 1024 in one 49, 33, 25; 8/1 heads, 1024 in four 51, 33, 25.  The host
+// knows the tokens, not the sequences (they stay on the device): 8192 tokens get
+// one CTA a block, right for four sequences and 5 % too slow for one.
 int dkv_parts(int64_t T, int group, int n_kv_heads, int sms) {
     const int64_t blocks = (T + 127) / 128;
     const double share = 2.0 * sms / (static_cast<double>(n_kv_heads) * (blocks + 1));

@@ -9,13 +9,15 @@
 //   P = 2^(c S - c m) as bf16 back into S's columns; O += P V (A from TMEM).
 // Warps 0-3 and 4-7 run the softmax of the two tiles, a thread a row, so that
 // no two threads have to meet (two threads a row took 491 us where this takes
-// 479); warp 8 issues the MMAs, warp 9 the TMA loads.  While one tile's softmax
+// 479); warp 8 issues the MMAs, warp 9 the TMA loads, warp 10 looks at V where
+// keys are hidden.  While one tile's softmax
 // runs, the tensor cores work on the other's products.  TMEM: two S and two O
 // of 128 columns, all 512.
 //   16384 tokens in 7 sequences, 48/8 heads of 128 (0.69 TFLOP): 469 us, 1.48
 // PFLOP/s (a library product reaches 1.88).  32768 tokens in one sequence, 8/2
 // heads: 1.23 ms, 1.79 PFLOP/s.  Run for seconds, both meet the power limit
-// (535 us, 1.38 ms).  What bounds it: S waits for the product that reads P from
+// (535 us, 1.38 ms).  Heads of 96, 80 and 64 at the first size: 484, 477, 432 us.
+// What bounds it: S waits for the product that reads P from
 // its columns, so a tile's softmax (about 1500 cycles) and its products (1024)
 // follow each other and two tiles do not quite fill the tensor cores; beside
 // that Q and K from shared memory take its whole bandwidth while S is formed,
@@ -50,88 +52,41 @@ struct FwdParams {
 };
 
 // Warps 0-3 and 4-7 the softmax of the two tiles, a thread a row; then the MMA
-// warp, the load warp, two idle ones.
-constexpr int kFwdThreads = 384, kFwdMmaWarp = 8, kFwdLoadWarp = 9;
+// warp, the load warp, the value warp (diagonal blocks of V), an idle one.
+constexpr int kFwdThreads = 384, kFwdMmaWarp = 8, kFwdLoadWarp = 9, kFwdValueWarp = 10;
 
 template <int D>
 struct FwdCfg {
     static constexpr int TILE = 128 * D * 2;
     static constexpr int STAGES = D == 128 ? 4 : 8;
-    static constexpr int SMEM = 2 * TILE + STAGES * TILE + 256;
+    static constexpr int SMEM = 2 * TILE + STAGES * TILE + 320;
 };
 
-// Which of the 32 rows from row0 on a hidden value can have spoilt, as bits: in
-// some channel a value after the row (within the block of 128) is not finite,
-// and none up to the row is NaN.
-__device__ __forceinline__ uint32_t fwd_spoilt(const FwdParams& p, int64_t start, int row0, int kvh) {
-    const int lane = threadIdx.x & 31, r0 = row0 & 127;
-    const int64_t first = start + row0 - r0;
-    const int n = static_cast<int>(min(static_cast<int64_t>(128), p.T - first));
-    const uint16_t* v = p.v + first * p.v_t + kvh * p.v_h + 4 * lane;
-    int last_odd[4] = {-1, -1, -1, -1}, first_nan[4] = {128, 128, 128, 128};
-    if (4 * lane < p.D)
-        for (int j = 0; j < n; ++j) {
-            const uint2 w = *reinterpret_cast<const uint2*>(v + j * p.v_t);
-            const uint32_t x[4] = {w.x, w.x >> 16, w.y, w.y >> 16};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (bf16_odd(x[e])) last_odd[e] = j;
-                if (bf16_nan(x[e])) first_nan[e] = min(first_nan[e], j);
-            }
-        }
-    uint32_t rows = 0;
-    for (int i = 0; i < 32; ++i) {
-        const int r = r0 + i;
-        bool need = false;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) need |= last_odd[e] > r && first_nan[e] > r;
-        if (__any_sync(0xFFFFFFFFu, need)) rows |= 1u << i;
-    }
-    return rows;
-}
-
-// One row by the definition, by one warp: the weights of 32 keys, a key a
-// lane, then their sum over the values, four channels a lane.
-__device__ __forceinline__ void fwd_row(const FwdParams& p, int64_t start, int row, int h, int kvh,
-                                     float lse) {
+// Adds to the warp's rows [row0, row0 + 32) of out what of the values from key
+// `from` on, which were set to 0 for the product, they see: infinities and NaN,
+// whose weights are above 0.  Four channels a lane; a row whose lse is not finite
+// is NaN throughout.
+__device__ __noinline__ void fwd_visible(const FwdParams& p, int64_t start, int len, int from,
+                                         int row0, int h, int kvh, float lse) {
     const int lane = threadIdx.x & 31, c = 4 * lane;
-    const uint16_t* q = p.q + (start + row) * p.q_t + h * p.q_h;
-    const uint16_t* k = p.k + start * p.k_t + kvh * p.k_h;
-    const uint16_t* v = p.v + start * p.v_t + kvh * p.v_h;
-    float acc[4] = {0, 0, 0, 0};
-    for (int j0 = 0; j0 <= row; j0 += 32) {
-        const int n = min(32, row + 1 - j0);
-        float w = 0.f;
-        if (lane < n) w = expf(dot_bf16(q, k + (j0 + lane) * p.k_t, p.D) * p.scale - lse);
-#pragma unroll 4
-        for (int e = 0; e < n; ++e) {
-            const float x = __shfl_sync(0xFFFFFFFFu, w, e);
-            if (c >= p.D) continue;
-            const uint2 u = *reinterpret_cast<const uint2*>(v + (j0 + e) * p.v_t + c);
-            acc[0] += x * bf16_lo(u.x);
-            acc[1] += x * bf16_hi(u.x);
-            acc[2] += x * bf16_lo(u.y);
-            acc[3] += x * bf16_hi(u.y);
-        }
-    }
-    const int64_t o = (start + row) * p.o_t + h * p.o_h;
+    const bool in = c < p.D;
+    const uint16_t* v = p.v + start * p.v_t + kvh * p.v_h + c;
+    float sum[4] = {0, 0, 0, 0};   // of what is not finite among the keys so far
+    for (int j = from; j < min(row0 + 32, len); ++j) {
+        const uint2 w = in ? *reinterpret_cast<const uint2*>(v + j * p.v_t) : make_uint2(0, 0);
+        const uint32_t x[4] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (c >= p.D) break;
-        const uint16_t b = f32_bf16(acc[i]);
-        p.out[o + c + i] = b;
-        if (p.rest) p.rest[o + c + i] = f32_bf16(acc[i] - bf16_f32(b));
-    }
-}
-
-// Those of the rows row0 + (bit of `rows`), by a warp whose lanes hold their
-// rows' lse.
-__device__ __noinline__ void fwd_redo(const FwdParams& p, int64_t start, int row0, int h, int kvh,
-                                      uint32_t rows, float lse) {
-    rows &= fwd_spoilt(p, start, row0, kvh);
-    for (; rows; rows &= rows - 1) {
-        const int s = __ffs(rows) - 1;
-        fwd_row(p, start, row0 + s, h, kvh, __shfl_sync(0xFFFFFFFFu, lse, s));
+        for (int e = 0; e < 4; ++e)
+            if (bf16_odd(x[e])) sum[e] += bf16_f32(static_cast<uint16_t>(x[e]));
+        const float l = __shfl_sync(0xFFFFFFFFu, lse, j & 31);
+        if (j < row0 || !(l - l == 0.f)) continue;
+        const int64_t o = (start + j) * p.o_t + h * p.o_h + c;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (sum[e] != 0.f) {
+                p.out[o + e] = f32_bf16(bf16_f32(p.out[o + e]) + sum[e]);
+                if (p.rest) p.rest[o + e] = 0x7FFF;
+            }
     }
 }
 
@@ -161,6 +116,8 @@ struct FwdWork {
         n[0] = m0[0] / 128 + 1;
         n[1] = m0[1] < len ? m0[1] / 128 + 1 : 0;
     }
+    // key block j holds a tile's diagonal
+    __device__ bool diagonal(int j) const { return j == n[0] - 1 || j == n[1] - 1; }
 };
 
 // f(work) for each of this CTA's items; false ends the walk.
@@ -192,8 +149,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
     uint64_t* o_full = p_full + 4;    // [2] its product with V done
     uint64_t* o_empty = o_full + 2;   // [2] its O read by the epilogue
     uint64_t* done = o_empty + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    uint64_t* v_full = done + 1;      // [STAGES] a diagonal block's V, before the value warp
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_full + C::STAGES);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* odd_flag = abort_flag + 1;   // a value that is not finite was met
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -201,6 +160,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
+            mbar_init(&v_full[s], 1);
         }
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
@@ -213,6 +173,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
         }
         mbar_init(done, 1);
         *abort_flag = 0;
+        *odd_flag = 0;
         fence_mbar_init();
     }
     if (warp == kFwdMmaWarp) {
@@ -234,6 +195,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
             tma_prefetch_map(&p.mapV);
             const uint32_t aq = smem_u32(sQ), akv = smem_u32(sKV);
             uint32_t st = 0, ph = 0, armed = 0, par = 0, items = 0;
+            uint32_t via = 0, v_ph = 0;   // stages filled for the value warp; its phases
             bool ok = true;
             each_item(p, [&](const FwdWork& w) {
                 if (w.block < 0) return true;
@@ -249,12 +211,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
                                     tok + w.m0[t], w.h[t]);
                 for (int it = 0; it < 2 * blocks; ++it) {
                     if (!(ok = mbar_wait(&empty[st], ph ^ 1u, abort_flag, p.status))) return false;
-                    mbar_arrive_expect_tx(&full[st], C::TILE);
+                    const bool v = (it & 1) && w.diagonal(it >> 1);
+                    uint64_t* landed = v ? &v_full[st] : &full[st];
+                    mbar_arrive_expect_tx(landed, C::TILE);
                     armed |= 1u << st;
-                    par = (par & ~(1u << st)) | (ph << st);
+                    par = (par & ~(1u << st)) | ((v ? v_ph >> st & 1u : ph) << st);
+                    via = (via & ~(1u << st)) | (static_cast<uint32_t>(v) << st);
+                    if (v) v_ph ^= 1u << st;
                     for (int b = 0; b < D / 64; ++b)
                         tma_load_3d(akv + st * C::TILE + b * kBoxBytes,
-                                    (it & 1) ? &p.mapV : &p.mapK, &full[st], b * 64,
+                                    (it & 1) ? &p.mapV : &p.mapK, landed, b * 64,
                                     tok + (it >> 1) * 128, w.kvh);
                     if (++st == C::STAGES) {
                         st = 0;
@@ -268,8 +234,31 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
                 if (items) mbar_wait(q_full, (items - 1) & 1u, &no_abort, nullptr, 20000000ull);
                 for (int s = 0; s < C::STAGES; ++s)
                     if (armed & (1u << s))
-                        mbar_wait(&full[s], (par >> s) & 1u, &no_abort, nullptr, 20000000ull);
+                        mbar_wait(via >> s & 1u ? &v_full[s] : &full[s], (par >> s) & 1u, &no_abort,
+                                  nullptr, 20000000ull);
             }
+        } else if (warp == kFwdValueWarp) {
+            // -------------------------------------------------------- diagonal blocks of V
+            const uint32_t akv = smem_u32(sKV);
+            uint32_t st = 0, v_ph = 0;
+            each_item(p, [&](const FwdWork& w) {
+                if (w.block < 0) return true;
+                for (int it = 0; it < 2 * max(w.n[0], w.n[1]); ++it) {
+                    if ((it & 1) && w.diagonal(it >> 1)) {
+                        if (!warp_wait(&v_full[st], v_ph >> st & 1u, abort_flag, p.status))
+                            return false;
+                        v_ph ^= 1u << st;
+                        if (odd_tile<D>(akv + st * C::TILE, lane, 32)) {
+                            clean_tile<D>(akv + st * C::TILE, lane, 32);
+                            *odd_flag = 1;
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&full[st]);
+                    }
+                    if (++st == C::STAGES) st = 0;
+                }
+                return true;
+            });
         } else if (warp == kFwdMmaWarp) {
             // -------------------------------------------------------- MMAs
             const uint32_t one = elect_lane();
@@ -428,7 +417,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
                 const float from = m == -INFINITY ? 0.f : -m * c;
                 const float2 c2 = make_float2(c, c), neg = make_float2(from, from);
                 // half the keys: their product with V runs while the others
-                // are formed
+                // are formed.  P as bf16: what the tensor cores take beside a
+                // bf16 V, with fp32's range; the roundings (2^-8 at most a
+                // key) average out over a row's keys
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     float* x = s + 64 * half;
@@ -467,7 +458,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
             const float inv = 1.0f / lb;
             const float lse = m * p.scale + logf(l);
             const int64_t o = (w.start + row0) * p.o_t + h * p.o_h;
-            float2 sick = make_float2(0.f, 0.f);  // NaN once a value is not finite
+            // out, and for the backward what the rounding took: 16 bits of O
+            // together, since D from the 8 of out alone is off by as much as dS
+            // where a row is nearly one key's
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 uint32_t a[32];
@@ -483,7 +476,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
                     const float2 x = mul2(make_float2(__uint_as_float(a[2 * e]),
                                                       __uint_as_float(a[2 * e + 1])),
                                           make_float2(inv, inv));
-                    sick = fma2(x, make_float2(0.f, 0.f), sick);
                     hi[e] = pack_bf16x2(x.x, x.y);
                     lo[e] = pack_bf16x2(x.x - bf16_lo(hi[e]), x.y - bf16_hi(hi[e]));
                 }
@@ -500,11 +492,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
                 }
             }
             if (valid) p.lse[h * p.T + w.start + row] = lse;
-            // (an lse that is not finite is that of a row which is NaN throughout)
-            const uint32_t again = __ballot_sync(
-                0xFFFFFFFFu, !(sick.x + sick.y == 0.f) && valid && lse - lse == 0.f);
-            __syncwarp();   // a row's pieces come from four lanes
-            if (again) fwd_redo(p, w.start, row0, h, w.kvh, again, lse);
+            __syncwarp();    // a row's pieces come from four lanes
+            if (*odd_flag)   // (of two row blocks, the second meets the first's diagonal too)
+                fwd_visible(p, w.start, w.len, w.m0[0], row0, h, w.kvh, lse);
             return true;
         });
     }
@@ -517,7 +507,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
 // Weight w = blocks a query block reads (its number + 1), or that read a key
 // block.  Entries with weight >= w of a list of sequences with b_s blocks:
 // a counting sort, heaviest first; sequence s has one entry of each weight
-// 1 .. b_s in either list.
+// 1 .. b_s in either list.  One CTA, bound by the latency of its loads and
+// atomics one behind the other; once a batch.  5 sequences of 301 tokens 6.3 us,
+// 7 of 16384 7.7, one of 65536 12, 1024 of 16384 50, 4096 of 262144 185.
 
 __global__ void __launch_bounds__(1024, 1)
     attn_plan_kernel(const int32_t* cu, int n_seqs, int64_t T, int4* q128, int4* kv128, int4* q256,

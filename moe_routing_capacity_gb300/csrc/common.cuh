@@ -384,6 +384,12 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t cluster_addr) {
     return v;
 }
 
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t cluster_addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
 // Every thread of both CTAs (release/acquire at cluster scope).
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"

@@ -138,10 +138,7 @@ def test_a_token_that_is_not_finite(rng, lens, hq, hk, D, bad):
         keys[cu[1]:cu[2]] = False
         for n, some in (("out", rows), ("dq", rows), ("dk", keys), ("dv", keys)):
             R.within(n, got[n][some], want[n][0][some], want[n][1][some] + 1e-30)
-            # a sequence that shares no tile with it: the same bits
-            apart = keys.clone()
-            apart[:cu[1]] = hit != cu[1]
-            assert torch.equal(got[n][apart], clean[n][apart]), n
+            assert torch.equal(got[n][some], clean[n][some]), n    # not a bit of theirs
             if math.isnan(bad):
                 assert bool(got[n][~some].isnan().all()), n
 
@@ -153,6 +150,7 @@ def test_a_gradient_that_is_not_finite(rng, lens, hq, hk, D, bad):
     T, cu = sum(lens), offsets(lens)
     q, k, v, dout = (randn(rng, T, h, D) for h in (hq, hk, hk, hq))
     want = reference(q, k, v, lens, dout)
+    clean, _ = attention_step(q, k, v, cu, dout)
     hit = cu[1] + lens[1] // 2
     d = dout.clone()
     d[hit] = bad
@@ -164,6 +162,7 @@ def test_a_gradient_that_is_not_finite(rng, lens, hq, hk, D, bad):
     keys[cu[1]:hit + 1] = False
     for n, some in (("out", rows | True), ("dq", rows), ("dk", keys), ("dv", keys)):
         R.within(n, got[n][some], want[n][0][some], want[n][1][some] + 1e-30)
+        assert torch.equal(got[n][some], clean[n][some]), n
         assert not bool(got[n][~some].isfinite().any()), n
 
 
@@ -189,24 +188,32 @@ def test_a_channel_that_is_not_finite(rng, D):
     assert bool((got["out"][310:, :, 7] == float("inf")).all())
 
 
-@pytest.mark.parametrize("what", ["first value", "every value", "every gradient", "first key"])
+@pytest.mark.parametrize("what", ["first value", "every value", "every gradient", "first key",
+                                  "a token amid", "a value a block", "infinite values"])
 def test_what_is_not_finite_costs_little(rng, what):
-    """A row that sees the NaN itself is not done again: the step takes no
-    more than three times a finite one's time."""
+    """The step takes no more than three times a finite one's time."""
     T, hq, hk, D = 16384, 4, 1, 128
     x = {n: randn(rng, T, h, D) for n, h in (("q", hq), ("k", hk), ("v", hk), ("d", hq))}
-    nan = {n: t.clone() for n, t in x.items()}
+    bad = {n: t.clone() for n, t in x.items()}
     if what == "first value":
-        nan["v"][0] = float("nan")
+        bad["v"][0] = math.nan
     elif what == "every value":
-        nan["v"].fill_(float("nan"))
+        bad["v"].fill_(math.nan)
     elif what == "every gradient":
-        nan["d"].fill_(float("nan"))
+        bad["d"].fill_(math.nan)
+    elif what == "first key":
+        bad["k"][0] = math.nan
+    elif what == "a token amid":
+        for t in bad.values():
+            t[T // 2 + 64] = math.nan
+    elif what == "a value a block":
+        for i in range(64, T, 128):
+            bad["v"][i, 0, i // 128] = math.nan
     else:
-        nan["k"][0] = float("nan")
+        bad["v"].fill_(math.inf)
     plan = abi.AttentionPlan(ints(0, T), T, hq, hk, D)
     times = []
-    for t in (x, nan, x, nan):
+    for t in (x, bad, x, bad):
         best = math.inf
         for _ in range(3):
             a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
@@ -404,3 +411,53 @@ def test_the_moe_branch_gets_its_own_gradient(rng):
     # dy of that call is the stream's gradient, dh3 itself (alpha 1, no norm behind h3)
     R.within("dgate1", got["gate1"], du["dgate"], 2e-5 * size)
     R.within("dw_pre2", got["w_pre2"], du["dw_pre"], 2e-5 * float(du["dw_pre"].abs().max()))
+
+
+@pytest.mark.parametrize("hq,hk", [(4, 2), (3, 1)])
+def test_gradients_with_keys_without_weight(rng, hq, hk):
+    """Keys at -infinity in one channel: 0 times that is NaN in that channel of
+    dq, for the rows that see them, and nothing anywhere else."""
+    T, D, dead = 700, 64, 260
+    q, k, v, dout = (randn(rng, T, h, D) for h in (hq, hk, hk, hq))
+    q[..., 0] = q[..., 0].abs() + 1
+    k[:dead, :, 0] = -math.inf
+    got, st = attention_step(q, k, v, [0, T], dout)
+    assert st == [0, 0]
+    for n in ("out", "dq", "dk", "dv"):
+        assert bool(got[n][:dead].isnan().all()), n
+    assert bool(got["dq"][dead:, :, 0].isnan().all())
+    # the others' gradients: what the live keys alone give
+    live = slice(dead, T)
+    want = reference(q[live], k[live], v[live], [T - dead], dout[live])
+    for n in ("out", "dk", "dv"):
+        R.within(n, got[n][live], want[n][0], want[n][1] + 1e-30)
+    R.within("dq", got["dq"][live, :, 1:], want["dq"][0][..., 1:], want["dq"][1][..., 1:] + 1e-30)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("hq,hk", [(4, 2), (3, 1), (8, 1)])
+def test_infinities_that_are_seen_come_out(rng, hq, hk, D):
+    """Single infinite values and gradients, of either sign, some in one block and
+    some in the next: out and dv hold their signs, or NaN where both meet."""
+    T = 600
+    q, k, v, dout = (randn(rng, T, h, D) for h in (hq, hk, hk, hq))
+    clean, _ = attention_step(q, k, v, [0, T], dout)
+    x, d = v.clone(), dout.clone()
+    x[130, :, 3] = math.inf
+    x[140, :, 3] = -math.inf
+    x[300, :, 9] = -math.inf
+    got, st = attention_step(q, k, x, [0, T], dout)
+    want = clean["out"].clone()
+    want[130:, :, 3] = math.inf
+    want[140:, :, 3] = math.nan
+    want[300:, :, 9] = -math.inf
+    assert torch.equal(got["out"].nan_to_num(7e5), want.nan_to_num(7e5))
+    d[130, :, 3] = math.inf
+    d[140, :, 3] = -math.inf
+    d[300, 0, 9] = -math.inf
+    got, st = attention_step(q, k, v, [0, T], d)
+    want = clean["dv"].clone()
+    want[:141, :, 3] = -math.inf
+    want[:131, :, 3] = math.nan
+    want[:301, 0, 9] = -math.inf
+    assert torch.equal(got["dv"].nan_to_num(7e5), want.nan_to_num(7e5))
