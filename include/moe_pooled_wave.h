@@ -774,7 +774,8 @@ const char* moe_strerror(int code);
  * expert FFN; 3: the whole-layer forward and the host-memory pipeline; 4: the
  * optional bank of the dropless dispatch and expert FFN; 5: the optional bank
  * as the backward's source of X; 6: the dropless dispatch overlapped with the
- * shared experts). */
+ * shared experts, and beside it, without a change to an earlier call, the
+ * training block's). */
 int moe_abi_version(void);
 
 #ifdef __cplusplus

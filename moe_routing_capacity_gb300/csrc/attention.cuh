@@ -319,10 +319,10 @@ __device__ __forceinline__ uint16_t f32_bf16(float v) {
 // it get it back at the end, from memory (*_visible): what a token does not
 // see changes no bit of its results, and no row is worked out a second time.
 //   The forward has a warp look at V on its way from the copy to the products
-// (8192 tokens, 16/4 heads: 80 -> 84 us; by the softmax warps 84 to 88; a second pass,
-// only where a result was not finite, 92 for the code it adds to the loops); dQ's forming warps look at K while they
-// wait for the scores; dK and dV know from the queries' lse and D, which are not
-// finite where Q or dO is not.
+// (8192 tokens, 16/4 heads: 78 -> 80 us; by the softmax warps 80 to 84; a second pass,
+// only where a result was not finite, 88 for the code it adds to the loops); dQ's
+// forming warps look at K while they wait for the scores; dK and dV know from the
+// queries' lse and D, which are not finite where Q or dO is not.
 
 // Bits 15 and 31: the word's bf16 halves that are NaN or infinite.
 __device__ __forceinline__ uint32_t odd_halves(uint32_t w) {

@@ -19,14 +19,14 @@
 //   8192 tokens in 4 sequences, 16/4 heads of 128 (one product 25 us at a library
 // product's rate): dQ 127 us, dK and dV 141 us.  dK and dV: the longest column of
 // blocks is 104 rounds of 128 x 128 pairs (26 blocks, 4 heads) where an even share
-// would be 84, and sets the time: about 2450 cycles a round and 8 us of start and
+// would be 82, and sets the time: about 2450 cycles a round and 8 us of start and
 // end.  The products of a round are 2048 of them, and so is their operands' way
 // through shared memory (computed from the tiles' bytes; no counter shows it).
 // dQ: 2200 cycles a round (products 1536, operands 1750, computed likewise, and P
 // and dS of a block follow each other), 6500 between two pieces of work (D, the
 // store of dQ).  Head widths 72 to 120 run the products of 128: 16384 tokens in 7,
-// 48/8 heads, dQ and dK/dV of 128 790 and 891 us, of 96 784 and 877, of 80 765 and
-// 852, of 64 600 and 700.
+// 48/8 heads, dQ and dK/dV of 128 794 and 884 us, of 96 778 and 867, of 80 769 and
+// 844, of 64 610 and 690.
 #include <cstring>
 
 #include "attention.cuh"

@@ -10,13 +10,13 @@
 // Warps 0-3 and 4-7 run the softmax of the two tiles, a thread a row, so that
 // no two threads have to meet (two threads a row took 491 us where this takes
 // 479); warp 8 issues the MMAs, warp 9 the TMA loads, warp 10 looks at V where
-// keys are hidden.  While one tile's softmax
-// runs, the tensor cores work on the other's products.  TMEM: two S and two O
-// of 128 columns, all 512.
-//   16384 tokens in 7 sequences, 48/8 heads of 128 (0.69 TFLOP): 469 us, 1.48
-// PFLOP/s (a library product reaches 1.88).  32768 tokens in one sequence, 8/2
-// heads: 1.23 ms, 1.79 PFLOP/s.  Run for seconds, both meet the power limit
-// (535 us, 1.38 ms).  Heads of 96, 80 and 64 at the first size: 484, 477, 432 us.
+// keys are hidden.  While one tile's softmax runs, the tensor cores work on the
+// other's products.  TMEM: two S and two O of 128 columns, all 512.
+//   16384 tokens in 7 sequences, 48/8 heads of 128 (0.69 TFLOP): 498 us, 1.39
+// PFLOP/s (a library product reaches 1.88), 487 without the look at V.  32768
+// tokens in one sequence, 8/2 heads: 1.28 ms, 1.72 PFLOP/s.  Ten calls each; run for
+// seconds, both meet the power limit (530 us, 1.38 ms).  Heads of 96, 80 and 64 at
+// the first size: 492, 490, 438 us.
 // What bounds it: S waits for the product that reads P from
 // its columns, so a tile's softmax (about 1500 cycles) and its products (1024)
 // follow each other and two tiles do not quite fill the tensor cores; beside

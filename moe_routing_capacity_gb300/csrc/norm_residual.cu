@@ -17,7 +17,9 @@
 //   16384 rows of 6144 in bf16: forward 121 us (6.65 TB/s; a copy reaches 6.78),
 // backward 182 us (6.64 TB/s).  8191 rows of 2048, fp32 stream and a gate a
 // token, backward: 67 us (5.5 TB/s; 5 us of them are the sums over tokens).
-// One row of 2048: 2.4 us on the device.
+// One row of 2048: 2.4 us on the device.  Forward of 16384 rows, bf16 with a gate a
+// channel, and fp32 rows with a gate a token: 256 channels 9.4 and 9.8 us, 1024 28
+// and 44, 2048 48 and 87, 4096 89 and 165, 6144 120 and 245, 8192 182 and 282.
 #include <cstring>
 
 #include "common.cuh"
@@ -473,7 +475,11 @@ constexpr int fwd_occ(int threads) {
 }
 // Backward: 8 channels a thread up to 1024 channels, 16 past them, up to 168
 // registers.  16384 rows of 1024: 41.7 us (8) and 47.4 (16), with fp32 rows and
-// a gate a token 61 and 80; 8191 rows of 2048 64.6 either way.
+// a gate a token 61 and 80; 8191 rows of 2048 64.6 either way.  CTAs of 256 and 512
+// threads (2056 to 4096 and 6152 to 8192 channels) have 128 registers a thread and
+// spill 20 to 140 bytes: 16384 rows of 4096 and 8192 take 155 and 314 us (1.3 times
+// their bytes), with fp32 rows and a gate a token 399 and 604 (1.8 and 1.4), where
+// 6144, without spills, takes 182 (1.02) and 383 (1.17).
 constexpr int bwd_occ(int threads) {
     return threads <= 64 ? 8 : threads <= 128 ? 3 : threads <= 256 ? 2 : 1;
 }

@@ -8,8 +8,10 @@
 // covers whole 128-byte lines.  The heads of a token are split over several
 // threads when there are too few tokens to fill the machine.
 //   65536 tokens of 56 heads of 128 (1.9 GB moved): 282 us, 6.67 TB/s, what a copy
-// reaches.  8192 tokens of 20 heads (84 MB): 18.5 us, of which 12.4 are the bytes
-// at that rate; the rest is the first loads' and the last stores' way.
+// reaches.  8192 tokens of 20 heads (84 MB): 18.5 us where heads are strided (15.7
+// where they are not), of which 12.4 are the bytes at that rate.  The rest is three
+// loads one behind the other (the position, its angles, then the heads), which each of
+// 2.8 rounds of CTAs waits for again.
 #include <cmath>
 
 #include "common.cuh"
@@ -194,9 +196,10 @@ int launch_rotary(const moe_rotary_t& c, const uint16_t* q, const uint16_t* k, c
     p.table = table;
     p.pos = pos;
     p.status = status;
-    // eight rounds of resident CTAs while a thread keeps four heads: a short
-    // last round costs little (8192 tokens x 20 heads 20.5 -> 18.5 us against one
-    // round, 65536 x 56 291 -> 282 us)
+    // up to eight rounds of resident CTAs, as long as a thread keeps four heads: a
+    // short last round costs little (65536 tokens x 56 heads 291 -> 282 us against
+    // one round; 8192 x 20, where the four heads allow five splits and 2.8 rounds,
+    // 20.5 -> 18.5 us)
     const int64_t want = static_cast<int64_t>(sms) * 3 * kRotThreads * 8;
     const int64_t have = c.T * p.units;
     int64_t splits = (want + have - 1) / have;
