@@ -19,7 +19,7 @@
 //   8192 tokens in 4 sequences, 16/4 heads of 128 (one product 25 us at a library
 // product's rate): dQ 127 us, dK and dV 141 us.  dK and dV: the longest column of
 // blocks is 104 rounds of 128 x 128 pairs (26 blocks, 4 heads) where an even share
-// would be 82, and sets the time: about 2450 cycles a round and 8 us of start and
+// would be 82, and sets the time: about 2500 cycles a round and 8 us of start and
 // end.  The products of a round are 2048 of them, and so is their operands' way
 // through shared memory (computed from the tiles' bytes; no counter shows it).
 // dQ: 2200 cycles a round (products 1536, operands 1750, computed likewise, and P
