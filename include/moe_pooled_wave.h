@@ -667,7 +667,8 @@ int moe_rotary(const moe_rotary_t* cfg, const uint16_t* q, const uint16_t* k,
  * outputs and gradients are zero, their lse -infinity.  A value that the mask
  * hides from a token never reaches its outputs, NaN and infinities included.
  * All tensors bf16 [T, heads, head_dim] with strides (elements, multiples of
- * 8) between tokens and heads and contiguous channels; head_dim a multiple of
+ * 8) between tokens and heads, wide enough that no two rows share an element,
+ * and contiguous channels; head_dim a multiple of
  * 8, 8 <= head_dim <= 128; n_heads a multiple of n_kv_heads; scale > 0.
  * Products accumulate in fp32; P and, in the backward, dS are rounded to bf16
  * as the operands of the next product.

@@ -31,8 +31,8 @@ bool strides_ok(int64_t T, int64_t heads, int64_t D, int64_t st_t, int64_t st_h)
     if ((T > 1 && (st_t % 8 || st_t < D || st_t >= (1ll << 38))) ||
         (heads > 1 && (st_h % 8 || st_h < D || st_h >= (1ll << 38))))
         return false;
-    if (T > 1 && heads > 1)
-        return st_t >= st_h ? st_t >= (heads - 1) * st_h + D : st_h >= (T - 1) * st_t + D;
+    if (T > 1 && heads > 1)   // (T - 1) st_t may pass 64 bits
+        return st_t >= st_h ? st_t >= (heads - 1) * st_h + D : (st_h - D) / st_t >= T - 1;
     return true;
 }
 
