@@ -646,7 +646,7 @@ struct RowDots {
                 if (w.n > 1 && w.block * 128 + row < w.len) p.delta[at + row] = d;
             }
         }
-        if (tid < 128) {   // a row without a weight has none that a number could give
+        if (tid < 128) {   // (of scores that are all -infinity: weights of 0 / 0)
             const float lse2 = lse == -INFINITY ? NAN : lse * kLog2e;
             rows[128 + tid] = lse2;
             if (w.block * 128 + tid < w.len) p.lse2[at + tid] = lse2;
