@@ -171,6 +171,13 @@ int moe_route_project(const moe_config_t* cfg, const uint16_t* x, const uint16_t
                       const float* bias, const uint16_t* W_ld, float* logits, int32_t* idx,
                       float* w, uint8_t* tie, uint16_t* z, int32_t* status, void* stream);
 
+/* moe_route_project without the choice: logits = x Wr^T (no bias) and z, for
+ * another rule's choice from the logits (moe_router_select).  W_ld = z = NULL:
+ * the logits alone. */
+int moe_route_logits(const moe_config_t* cfg, const uint16_t* x, const uint16_t* Wr,
+                     const uint16_t* W_ld, float* logits, uint16_t* z, int32_t* status,
+                     void* stream);
+
 /* Fixed pooled-wave dispatch (lamjinlab zh-HK section 二: one fixed pool per
  * destination, W same-shape waves, expert id in the payload row, the two
  * capacity factors, drops counted separately).  Priority: token ascending,
@@ -731,6 +738,156 @@ typedef struct moe_grad_tensor {
 int moe_grad_clip_workspace(int64_t n_tensors, int64_t* bytes);
 int moe_grad_clip(const moe_grad_tensor_t* tensors, int64_t n_tensors, float max_norm,
                   float* norm, void* ws, int64_t ws_bytes, void* stream);
+
+/* Norm of every query and key head and its rotation to the token's position, in
+ * one pass over the heads: with x one head's D channels,
+ *   n = w x / sqrt(mean(x^2) + eps),  y = n with its first rot_dim channels
+ *   turned as moe_rotary turns them
+ * in fp32, y rounded once.  w_q [D] bf16 is every query head's weight, w_k
+ * every key head's.
+ *   q, k, q_out, k_out: as for moe_rotary (strides, hk = 0, in place; to keep
+ *   q and k for the gradient, write elsewhere)
+ *   table [table_rows, rot_dim / 2, 2] fp32, pos [T] int32 or NULL (pos[t] =
+ *   t); rot_dim = 0 (table NULL): the norm alone.  A position outside the table
+ *   gives MOE_EINVAL in status and leaves that token's outputs unwritten.
+ * D and the strides multiples of 8, 16 <= D <= 512, rot_dim a multiple of 16,
+ * at most D. */
+typedef struct moe_head_norm {
+    int64_t T;
+    int32_t hq, hk, D, rot_dim, interleaved;
+    float eps;
+    int64_t table_rows;
+    int64_t q_t, q_h, k_t, k_h;       /* input strides, elements                     */
+    int64_t qo_t, qo_h, ko_t, ko_h;   /* output strides                              */
+    int64_t dq_t, dq_h, dk_t, dk_h;   /* backward only: the upstream gradients'      */
+} moe_head_norm_t;
+
+int moe_head_norm_rotary(const moe_head_norm_t* cfg, const uint16_t* q, const uint16_t* k,
+                         const uint16_t* w_q, const uint16_t* w_k, const float* table,
+                         const int32_t* pos, uint16_t* q_out, uint16_t* k_out, int32_t* status,
+                         void* stream);
+
+/* Its gradients for dq, dk (of q_out, k_out), from the forward's inputs: with
+ * dn = dy turned back, r = 1 / sqrt(mean(x^2) + eps),
+ *   dx = r (w dn - x r^2 mean(w dn x)),  dw = sum over tokens and heads of dn x r
+ *   dq_out, dk_out: gradients of q and k (strides qo_*, ko_*); each may be its
+ *   dq, dk or its q, k (same strides)
+ *   dw_q, dw_k [D] fp32 (dw_k NULL exactly when k is), summed in fp32 in a
+ *   fixed order; a token whose position is outside the table adds nothing
+ *   ws: scratch of moe_head_norm_rotary_workspace bytes. */
+int moe_head_norm_rotary_workspace(int64_t T, int32_t hq, int32_t hk, int32_t D, int64_t* bytes);
+int moe_head_norm_rotary_backward(const moe_head_norm_t* cfg, const uint16_t* dq,
+                                  const uint16_t* dk, const uint16_t* q, const uint16_t* k,
+                                  const uint16_t* w_q, const uint16_t* w_k, const float* table,
+                                  const int32_t* pos, uint16_t* dq_out, uint16_t* dk_out,
+                                  float* dw_q, float* dw_k, void* ws, int64_t ws_bytes,
+                                  int32_t* status, void* stream);
+
+/* Choice of experts from router logits l [T, n_experts] fp32, another rule than
+ * moe_router_topk's: with scores s = softmax(l) (score 0) or 1 / (1 + e^-l)
+ * (score 1) and v = s + bias,
+ *   the experts stand in n_groups groups of n_experts / n_groups neighbours; a
+ *   group's value is the sum of its group_top (1 or 2) largest v; the
+ *   groups_kept groups of largest value stay open, and of their experts the
+ *   top_k with the largest v are chosen, in falling order of v;
+ *   w_j = scale s_j, or scale s_j / sum of the chosen s (renorm; 0 where that
+ *   sum is 0).
+ * The order is that of the exact values of v for the given l and bias (equal
+ * ones: the lower index first), to the precision of 64 bits.  The bias has no
+ * part in w.  NaN counts as the smallest value in the choice: idx always holds
+ * top_k different experts.
+ *   bias [n_experts] fp32 or NULL; idx [T, top_k] int32, w [T, top_k] fp32 (out)
+ * n_experts <= 1024, top_k <= 32, n_groups <= 32 and a divisor of n_experts,
+ * group_top <= n_experts / n_groups, top_k <= the experts of groups_kept
+ * groups; where groups_kept < n_groups, a group has at most 1024 / n_groups
+ * experts, n_groups taken up to the next power of two.
+ * Backward: dlogits [T, n_experts], bf16 or fp32 (grad_f32), from l, the
+ * forward's idx (different experts in a row; one outside the experts adds
+ * nothing) and dw [T, top_k] fp32: with g = scale dw, or scale (dw - sum dw_j
+ * n_j) / S for renorm (n = s / S, S the chosen's sum),
+ *   sigmoid: dl_j = g_j s_j (1 - s_j), softmax: dl_e = s_e (g_e - sum g_j s_j)
+ * where the experts that are not chosen have g = 0, and with renorm no gradient. */
+typedef struct moe_routing {
+    int64_t T;
+    int32_t n_experts, top_k, score, n_groups, groups_kept, group_top, renorm;
+    float scale;
+    int32_t grad_f32;                  /* backward only                              */
+    int32_t reserved;                  /* must be 0                                  */
+} moe_routing_t;
+
+int moe_router_select(const moe_routing_t* cfg, const float* logits, const float* bias,
+                      int32_t* idx, float* w, void* stream);
+int moe_router_select_backward(const moe_routing_t* cfg, const float* logits, const int32_t* idx,
+                               const float* dw, void* dlogits, void* stream);
+
+/* The layer's backward (moe_layer_backward, with ragged = 1
+ * moe_layer_backward_ragged) where the experts and weights came from
+ * moe_router_select: routing is that call's rule (n_experts and top_k the
+ * layer's, its T not read, grad_f32 0), logits [T, n_experts] its input. */
+int moe_layer_backward_routed(const moe_config_t* cfg, int ragged,
+                              const moe_backward_args_t* args, const moe_routing_t* routing,
+                              const float* logits, void* stream);
+
+/* Token embedding: out_t = scale table[ids_t], zeros for ids_t = -1 (padding)
+ * and, with MOE_EINVAL in status, for ids outside [0, V).
+ *   table [V, d] bf16 or fp32 (table_f32), ids [T] int32, out [T, d] bf16 or
+ *   fp32 (out_f32); rows contiguous, rounded once
+ * Gradient: dtable_v = scale sum over t with ids_t = v of dout_t, [V, d] of
+ * table_f32's type, summed in fp32 in the tokens' order and rounded once; words
+ * that do not occur become 0.  accumulate = 1: added to what dtable holds
+ * (rounded once more), words that do not occur left as they are.
+ *   plan: moe_embedding_plan's, of plan_bytes from moe_embedding_workspace, made
+ *   from ids on the stream (ids outside [0, V) but -1: MOE_EINVAL in status;
+ *   none of them has a gradient); it serves any number of calls of this T, V
+ *   and d, one after another (it holds their scratch too).
+ *   dout [T, d] of out_f32's type.
+ * d a multiple of 8, 8 <= d <= 65536; T, V < 2^31 - 256. */
+typedef struct moe_embedding {
+    int64_t T, V;
+    int32_t d, table_f32, out_f32, accumulate;
+    float scale;
+    int32_t reserved;                  /* must be 0                                  */
+} moe_embedding_t;
+
+int moe_embedding(const moe_embedding_t* cfg, const void* table, const int32_t* ids, void* out,
+                  int32_t* status, void* stream);
+int moe_embedding_workspace(int64_t T, int64_t V, int32_t d, int64_t* plan_bytes);
+int moe_embedding_plan(int64_t T, int64_t V, int32_t d, const int32_t* ids, void* plan,
+                       int64_t plan_bytes, int32_t* status, void* stream);
+int moe_embedding_backward(const moe_embedding_t* cfg, const void* plan, int64_t plan_bytes,
+                           const void* dout, void* dtable, void* stream);
+
+/* Loss of a student's logits against a teacher's top logits (with K = 1 the
+ * cross entropy of a label): with tau the temperature, p = softmax(y / tau) over
+ * a token's entries and q = softmax(z / tau) over all V,
+ *   loss_t = scale weight_t tau^2 sum_k p_k (log p_k - log q_{ids_k})
+ *   dz_v = scale weight_t tau (q_v - sum over k with ids_k = v of p_k)
+ *   z [T, V] bf16 or fp32 (z_f32), rows z_ld elements apart, at any element
+ *   ids [T, K] int32, -1 for an entry that is not there (MOE_EINVAL in status
+ *   for others outside [0, V), which count as absent); a word may stand there
+ *   twice.  teacher [T, K], y, bf16 or fp32 (teacher_f32)
+ *   weight [T] fp32 or NULL (1).  A row of weight 0, or without entries (or all
+ *   of them -infinity), has loss, lse and gradient 0, whatever its logits hold.
+ *   loss, lse [T] fp32 (out): lse = log sum_v exp(z_v / tau)
+ *   total [1] fp32 (out): the sum of the losses, in a fixed order; or NULL
+ *   dlogits (out) as z, rows dz_ld apart, or NULL; it may be z itself
+ * moe_distill_loss gives the loss and, where dlogits is given, the gradient in
+ * the same pass; moe_distill_loss_backward the gradient alone, from lse.
+ * 1 <= K <= MOE_DISTILL_MAX_ENTRIES, V < 2^31, tau > 0. */
+#define MOE_DISTILL_MAX_ENTRIES 256
+typedef struct moe_distill {
+    int64_t T, V, z_ld, dz_ld;
+    int32_t K, z_f32, teacher_f32;
+    float temperature, scale;
+    int32_t reserved;                  /* must be 0                                  */
+} moe_distill_t;
+
+int moe_distill_loss(const moe_distill_t* cfg, const void* z, const int32_t* ids,
+                     const void* teacher, const float* weight, float* loss, float* lse,
+                     float* total, void* dlogits, int32_t* status, void* stream);
+int moe_distill_loss_backward(const moe_distill_t* cfg, const void* z, const int32_t* ids,
+                              const void* teacher, const float* weight, const float* lse,
+                              void* dlogits, int32_t* status, void* stream);
 
 /* Index checks of a checked build (compiled with -DMOE_CHECK=1; the pages
  * define no such operation): every row, slot, expert and tile index the

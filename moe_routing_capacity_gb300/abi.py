@@ -34,7 +34,12 @@ EXPORTS = ("moe_plan", "moe_router_topk", "moe_latent_proj", "moe_route_project"
            "moe_norm_residual", "moe_norm_residual_workspace", "moe_norm_residual_backward",
            "moe_rotary_make_table", "moe_rotary", "moe_attention_workspace",
            "moe_attention_plan", "moe_attention_forward", "moe_attention_backward",
-           "moe_grad_clip_workspace", "moe_grad_clip")
+           "moe_grad_clip_workspace", "moe_grad_clip",
+           "moe_head_norm_rotary", "moe_head_norm_rotary_workspace",
+           "moe_head_norm_rotary_backward", "moe_router_select", "moe_router_select_backward",
+           "moe_route_logits", "moe_layer_backward_routed",
+           "moe_embedding", "moe_embedding_workspace", "moe_embedding_plan",
+           "moe_embedding_backward", "moe_distill_loss", "moe_distill_loss_backward")
 # Declared in the header too, but exported by the checked build only.
 CHECKED_ONLY = ("moe_check_set_wave_wait_limit_ns",)
 
@@ -137,6 +142,36 @@ class GradTensor(ctypes.Structure):
                 ("is_bf16", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class HeadNorm(ctypes.Structure):
+    _fields_ = ([("T", ctypes.c_int64)] +
+                [(f, ctypes.c_int32) for f in ("hq", "hk", "D", "rot_dim", "interleaved")] +
+                [("eps", ctypes.c_float)] +
+                [(f, ctypes.c_int64) for f in ("table_rows", "q_t", "q_h", "k_t", "k_h", "qo_t",
+                                               "qo_h", "ko_t", "ko_h", "dq_t", "dq_h", "dk_t",
+                                               "dk_h")])
+
+
+class RoutingConfig(ctypes.Structure):
+    _fields_ = ([("T", ctypes.c_int64)] +
+                [(f, ctypes.c_int32) for f in ("n_experts", "top_k", "score", "n_groups",
+                                               "groups_kept", "group_top", "renorm")] +
+                [("scale", ctypes.c_float), ("grad_f32", ctypes.c_int32),
+                 ("reserved", ctypes.c_int32)])
+
+
+class EmbeddingConfig(ctypes.Structure):
+    _fields_ = ([("T", ctypes.c_int64), ("V", ctypes.c_int64)] +
+                [(f, ctypes.c_int32) for f in ("d", "table_f32", "out_f32", "accumulate")] +
+                [("scale", ctypes.c_float), ("reserved", ctypes.c_int32)])
+
+
+class Distill(ctypes.Structure):
+    _fields_ = ([(f, ctypes.c_int64) for f in ("T", "V", "z_ld", "dz_ld")] +
+                [(f, ctypes.c_int32) for f in ("K", "z_f32", "teacher_f32")] +
+                [("temperature", ctypes.c_float), ("scale", ctypes.c_float),
+                 ("reserved", ctypes.c_int32)])
+
+
 _lib = None
 
 
@@ -214,6 +249,22 @@ def load_library(path: str) -> ctypes.CDLL:
     L.moe_attention_backward.argtypes = [pa] + [vp] * 12 + [i64, vp, vp]
     L.moe_grad_clip_workspace.argtypes = [i64, pi64]
     L.moe_grad_clip.argtypes = [ctypes.POINTER(GradTensor), i64, ctypes.c_float, vp, vp, i64, vp]
+    ph, pr = ctypes.POINTER(HeadNorm), ctypes.POINTER(RoutingConfig)
+    pe, pd = ctypes.POINTER(EmbeddingConfig), ctypes.POINTER(Distill)
+    L.moe_head_norm_rotary.argtypes = [ph] + [vp] * 10
+    L.moe_head_norm_rotary_workspace.argtypes = [i64, i32, i32, i32, pi64]
+    L.moe_head_norm_rotary_backward.argtypes = [ph] + [vp] * 13 + [i64, vp, vp]
+    L.moe_route_logits.argtypes = [pc] + [vp] * 7
+    L.moe_layer_backward_routed.argtypes = [pc, ctypes.c_int, ctypes.POINTER(BackwardArgs), pr,
+                                            vp, vp]
+    L.moe_router_select.argtypes = [pr] + [vp] * 5
+    L.moe_router_select_backward.argtypes = [pr] + [vp] * 5
+    L.moe_embedding.argtypes = [pe] + [vp] * 5
+    L.moe_embedding_workspace.argtypes = [i64, i64, i32, pi64]
+    L.moe_embedding_plan.argtypes = [i64, i64, i32, vp, vp, i64, vp, vp]
+    L.moe_embedding_backward.argtypes = [pe, vp, i64, vp, vp, vp]
+    L.moe_distill_loss.argtypes = [pd] + [vp] * 10
+    L.moe_distill_loss_backward.argtypes = [pd] + [vp] * 8
     if hasattr(L, "moe_check_set_wave_wait_limit_ns"):
         L.moe_check_set_wave_wait_limit_ns.argtypes = [ctypes.c_ulonglong]
         L.moe_check_set_wave_wait_limit_ns.restype = ctypes.c_int
@@ -314,6 +365,15 @@ def route_project(cfg, x, Wr, bias, W_ld, logits, idx, w, tie, z, status, stream
         ctypes.byref(make_config(cfg)), _ptr(x, bf16), _ptr(Wr, bf16),
         _ptr(bias, f32, allow_none=True), _ptr(W_ld, bf16), _ptr(logits, f32), _ptr(idx, i32),
         _ptr(w, f32), _ptr(tie, u8), _ptr(z, bf16), _ptr(status, i32), _stream(stream)))
+
+
+def route_logits(cfg, x, Wr, W_ld, logits, z, status, stream=None):
+    """logits = x Wr^T and the latent projection z in one pass over x, for
+    router_select's choice (W_ld, z None: the logits alone)."""
+    _check("moe_route_logits", lib().moe_route_logits(
+        ctypes.byref(make_config(cfg)), _ptr(x, bf16), _ptr(Wr, bf16),
+        _ptr(W_ld, bf16, allow_none=True), _ptr(logits, f32), _ptr(z, bf16, allow_none=True),
+        _ptr(status, i32), _stream(stream)))
 
 
 def dispatch_pooled(cfg, z, idx, ws, pool, slot_of, drop, expert_rows, expert_count, stats,
@@ -542,9 +602,10 @@ def backward_plan(cfg, ragged=False) -> BackwardWs:
     return w
 
 
-def layer_backward(cfg, tensors: dict, ws, status, stream=None):
+def layer_backward(cfg, tensors: dict, ws, status, stream=None, routing=None, logits=None):
     """tensors: every BackwardArgs field by name (torch tensors, or None for
-    the shared-expert ones when there are none)."""
+    the shared-expert ones when there are none).  routing, logits: the rule and
+    the input of router_select, where the experts were chosen by it."""
     args = BackwardArgs()
     for f in BWD_ARG_FIELDS:
         t = tensors.get(f)
@@ -556,6 +617,11 @@ def layer_backward(cfg, tensors: dict, ws, status, stream=None):
     args.expert_offsets = None if eoff is None else eoff.data_ptr()
     bank = tensors.get("bank")
     args.bank = None if bank is None else bank.data_ptr()
+    if routing is not None:
+        _check("moe_layer_backward_routed", lib().moe_layer_backward_routed(
+            ctypes.byref(make_config(cfg)), int(eoff is not None), ctypes.byref(args),
+            ctypes.byref(routing.config(cfg.T)), _ptr(logits, f32), _stream(stream)))
+        return
     fn = "moe_layer_backward" if eoff is None else "moe_layer_backward_ragged"
     _check(fn, getattr(lib(), fn)(ctypes.byref(make_config(cfg)), ctypes.byref(args),
                                   _stream(stream)))
@@ -579,7 +645,7 @@ def _rows(name, t, shape, dtypes, allow_none=False):
     raise ValueError(f"{name}: contiguous device tensor required")
 
 
-_BF16, _F32, _RES = (bf16,), (f32,), (bf16, f32)
+_BF16, _F32, _RES, _I32 = (bf16,), (f32,), (bf16, f32), (i32,)
 
 
 def _norm_config(r, gate, alpha, beta, eps):
@@ -807,3 +873,237 @@ def grad_clip(grads, max_norm, norm, stream=None):
     _check("moe_grad_clip", lib().moe_grad_clip(
         grads.records, len(grads.tensors), max_norm, _ptr(norm, f32),
         _ptr(ws, u8, allow_none=True), 0 if ws is None else ws.numel(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- head norms with rotation
+
+def _head_norm_config(q, k, table, pos, eps, interleaved):
+    if q.dim() != 3 or (k is not None and k.dim() != 3):
+        raise ValueError("q and k are [T, heads, D]")
+    T, hq, D = q.shape
+    rot, rows = 0, 0
+    if table is not None:
+        if table.dim() != 3 or table.shape[2] != 2:
+            raise ValueError("the table is [positions, rot_dim / 2, 2]")
+        rot, rows = 2 * table.shape[1], table.shape[0]
+    if pos is not None and pos.shape != (T,):
+        raise ValueError("pos is [T]")
+    return HeadNorm(T, hq, 0 if k is None else k.shape[1], D, rot, bool(interleaved), eps, rows)
+
+
+def head_norm_rotary(q, k, w_q, w_k, table, pos, q_out, k_out, status, eps=1e-6,
+                     interleaved=False, stream=None):
+    """The norm of every head of q [T, hq, D] (weight w_q [D]) and k [T, hk, D]
+    (w_k; None both: no keys), and its rotation as rotary's to the tokens'
+    positions pos [T] int32 (None: 0, 1, ...), in one pass into q_out and k_out
+    (which may be q and k).  table None: the norm alone."""
+    c = _head_norm_config(q, k, table, pos, eps, interleaved)
+    qs, ks, chan = (c.T, c.hq, c.D), (c.T, c.hk, c.D), (c.D,)
+    qp, c.q_t, c.q_h = _heads("q", q, qs)
+    qop, c.qo_t, c.qo_h = _heads("q_out", q_out, qs)
+    kp = kop = None
+    if k is not None:
+        kp, c.k_t, c.k_h = _heads("k", k, ks)
+        kop, c.ko_t, c.ko_h = _heads("k_out", k_out, ks)
+    _check("moe_head_norm_rotary", lib().moe_head_norm_rotary(
+        ctypes.byref(c), qp, kp, _rows("w_q", w_q, chan, _BF16),
+        _rows("w_k", w_k, chan, _BF16, k is None), _ptr(table, f32, allow_none=True),
+        _ptr(pos, i32, allow_none=True), qop, kop, _ptr(status, i32), _stream(stream)))
+
+
+def head_norm_rotary_workspace(T, hq, hk, D) -> int:
+    """Scratch bytes of head_norm_rotary_backward."""
+    v = ctypes.c_int64()
+    _check("moe_head_norm_rotary_workspace",
+           lib().moe_head_norm_rotary_workspace(T, hq, hk, D, ctypes.byref(v)))
+    return v.value
+
+
+def head_norm_rotary_backward(dq, dk, q, k, w_q, w_k, table, pos, dq_out, dk_out, dw_q, dw_k, ws,
+                              status, eps=1e-6, interleaved=False, stream=None):
+    """Gradients of head_norm_rotary for dq, dk (of q_out, k_out), from the
+    forward's q and k: dq_out, dk_out (each may be its dq, dk or q, k), dw_q,
+    dw_k [D] fp32.  None exactly where the forward's tensor is."""
+    c = _head_norm_config(q, k, table, pos, eps, interleaved)
+    qs, ks, chan = (c.T, c.hq, c.D), (c.T, c.hk, c.D), (c.D,)
+    none = k is None
+    qp, c.q_t, c.q_h = _heads("q", q, qs)
+    dqp, c.dq_t, c.dq_h = _heads("dq", dq, qs)
+    qop, c.qo_t, c.qo_h = _heads("dq_out", dq_out, qs)
+    kp = dkp = kop = None
+    if not none:
+        kp, c.k_t, c.k_h = _heads("k", k, ks)
+        dkp, c.dk_t, c.dk_h = _heads("dk", dk, ks)
+        kop, c.ko_t, c.ko_h = _heads("dk_out", dk_out, ks)
+    _check("moe_head_norm_rotary_backward", lib().moe_head_norm_rotary_backward(
+        ctypes.byref(c), dqp, dkp, qp, kp, _rows("w_q", w_q, chan, _BF16),
+        _rows("w_k", w_k, chan, _BF16, none), _ptr(table, f32, allow_none=True),
+        _ptr(pos, i32, allow_none=True), qop, kop, _rows("dw_q", dw_q, chan, _F32),
+        _rows("dw_k", dw_k, chan, _F32, none), _ptr(ws, u8), ws.numel(), _ptr(status, i32),
+        _stream(stream)))
+
+
+# ---------------------------------------------------------------- choice of experts
+
+ROUTING_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+class Routing:
+    """A rule by which tokens choose top_k of n_experts (moe_routing_t): scores
+    (softmax or sigmoid of the logits) and a bias for the choice alone, the best
+    groups_kept of n_groups groups (by their group_top largest), the largest of
+    those; weights renormalised over the chosen (renorm) and scaled."""
+
+    def __init__(self, n_experts, top_k, score="softmax", n_groups=1, groups_kept=None,
+                 group_top=1, renorm=True, scale=1.0):
+        if score not in ROUTING_SCORES:
+            raise ValueError(f"score must be one of {sorted(ROUTING_SCORES)}")
+        self.n_experts, self.top_k = n_experts, top_k
+        self.score, self.n_groups, self.group_top = ROUTING_SCORES[score], n_groups, group_top
+        self.groups_kept = n_groups if groups_kept is None else groups_kept
+        self.renorm, self.scale = bool(renorm), float(scale)
+
+    def config(self, T, grad_f32=False) -> RoutingConfig:
+        return RoutingConfig(T, self.n_experts, self.top_k, self.score, self.n_groups,
+                             self.groups_kept, self.group_top, self.renorm, self.scale, grad_f32)
+
+
+def _routing_shapes(routing, logits):
+    if logits.dim() != 2:
+        raise ValueError("logits is [T, experts]")
+    T = logits.shape[0]
+    return (T, routing.n_experts), (T, routing.top_k)
+
+
+def router_select(routing, logits, bias, idx, w, stream=None):
+    """idx [T, top_k] int32, w [T, top_k] fp32: the experts that the rule chooses
+    for logits [T, n_experts] fp32 and bias [n_experts] fp32 (or None), in
+    falling order of score + bias, and their weights."""
+    rows, chosen = _routing_shapes(routing, logits)
+    c = routing.config(rows[0])
+    _check("moe_router_select", lib().moe_router_select(
+        ctypes.byref(c), _rows("logits", logits, rows, _F32),
+        _rows("bias", bias, rows[1:], _F32, True), _rows("idx", idx, chosen, _I32),
+        _rows("w", w, chosen, _F32), _stream(stream)))
+
+
+def router_select_backward(routing, logits, idx, dw, dlogits, stream=None):
+    """dlogits [T, n_experts] (bf16 or fp32): gradient of router_select's logits
+    for dw [T, top_k] fp32 of its weights; idx as the forward gave it."""
+    rows, chosen = _routing_shapes(routing, logits)
+    c = routing.config(rows[0], dlogits.dtype == f32)
+    _check("moe_router_select_backward", lib().moe_router_select_backward(
+        ctypes.byref(c), _rows("logits", logits, rows, _F32), _rows("idx", idx, chosen, _I32),
+        _rows("dw", dw, chosen, _F32), _rows("dlogits", dlogits, rows, _RES), _stream(stream)))
+
+
+# ---------------------------------------------------------------- embedding
+
+def _embedding_config(table, out, T, scale, accumulate=False):
+    if table.dim() != 2:
+        raise ValueError("the table is [V, d]")
+    V, d = table.shape
+    return EmbeddingConfig(T, V, d, table.dtype == f32, out.dtype == f32, bool(accumulate), scale)
+
+
+def embedding(table, ids, out, status, scale=1.0, stream=None):
+    """out[t] = scale * table[ids[t]]: table [V, d], out [T, d], bf16 or fp32
+    each, ids [T] int32; -1 (padding) gives zeros."""
+    T = ids.numel()
+    c = _embedding_config(table, out, T, scale)
+    _check("moe_embedding", lib().moe_embedding(
+        ctypes.byref(c), _rows("table", table, (c.V, c.d), _RES), _rows("ids", ids, (T,), _I32),
+        _rows("out", out, (T, c.d), _RES), _ptr(status, i32), _stream(stream)))
+
+
+class EmbeddingPlan:
+    """The tokens of one batch by word, for embedding_backward: made from ids [T]
+    int32 on the device, on the stream.  It serves any number of gradients of
+    this T, vocab and d, one after another (it holds their scratch); refill()
+    takes another batch's ids.  ``status`` receives MOE_EINVAL for ids outside
+    the vocabulary other than -1; none of them has a gradient."""
+
+    def __init__(self, ids, vocab, d, status=None, stream=None):
+        if ids.dim() != 1:
+            raise ValueError("ids is [T]")
+        self.T, self.vocab, self.d = ids.numel(), vocab, d
+        pb = ctypes.c_int64()
+        _check("moe_embedding_workspace", lib().moe_embedding_workspace(
+            self.T, vocab, d, ctypes.byref(pb)))
+        with on_stream(stream):
+            self.status = (torch.zeros(1, dtype=i32, device=ids.device) if status is None
+                           else status)
+            self.plan = torch.empty(pb.value, dtype=u8, device=ids.device)
+        self.refill(ids, stream)
+
+    def refill(self, ids, stream=None):
+        _check("moe_embedding_plan", lib().moe_embedding_plan(
+            self.T, self.vocab, self.d, _rows("ids", ids, (self.T,), _I32), _ptr(self.plan, u8),
+            self.plan.numel(), _ptr(self.status, i32), _stream(stream)))
+
+
+def embedding_backward(plan, dout, dtable, scale=1.0, accumulate=False, stream=None):
+    """dtable[v] = scale * the sum of dout[t] over the plan's tokens of word v, in
+    their order; dout [T, d], dtable [vocab, d], bf16 or fp32 each.  Words that do
+    not occur become 0; accumulate: the sums are added to dtable instead."""
+    c = _embedding_config(dtable, dout, plan.T, scale, accumulate)
+    _check("moe_embedding_backward", lib().moe_embedding_backward(
+        ctypes.byref(c), plan.plan.data_ptr(), plan.plan.numel(),
+        _rows("dout", dout, (plan.T, plan.d), _RES),
+        _rows("dtable", dtable, (plan.vocab, plan.d), _RES), _stream(stream)))
+
+
+# ---------------------------------------------------------------- distillation loss
+
+def _logits(name, t, shape, dtype):
+    """(address, row stride) of [T, V] logits whose rows are contiguous."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_cuda or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: device tensor with contiguous rows required")
+    return t.data_ptr(), t.stride(0)
+
+
+def _distill_config(logits, ids, teacher, temperature, scale):
+    if logits.dim() != 2 or ids.dim() != 2 or logits.dtype not in _RES:
+        raise ValueError("logits is [T, V] bf16 or fp32, ids [T, K]")
+    (T, V), K = logits.shape, ids.shape[1]
+    return (T, K), Distill(T, V, 0, 0, K, logits.dtype == f32, teacher.dtype == f32, temperature,
+                           scale)
+
+
+def distill_loss(logits, ids, teacher, weight, loss, lse, status, total=None, dlogits=None,
+                 temperature=1.0, scale=1.0, stream=None):
+    """loss[t] = scale weight[t] temperature^2 KL(teacher || student), the teacher
+    given by its logits teacher [T, K] (bf16 or fp32) of the words ids [T, K] int32
+    (-1: no entry), the student by logits [T, V] (bf16 or fp32, rows may be
+    strided), both at that temperature; weight [T] fp32 or None.  loss, lse [T]
+    fp32; total [1] fp32 receives the losses' sum, dlogits (may be logits) their
+    gradient in the same pass.  Rows without weight or entries have loss 0."""
+    given, c = _distill_config(logits, ids, teacher, temperature, scale)
+    zp, c.z_ld = _logits("logits", logits, (c.T, c.V), logits.dtype)
+    dp = None
+    if dlogits is not None:
+        dp, c.dz_ld = _logits("dlogits", dlogits, (c.T, c.V), logits.dtype)
+    tok = given[:1]
+    _check("moe_distill_loss", lib().moe_distill_loss(
+        ctypes.byref(c), zp, _rows("ids", ids, given, _I32), _rows("teacher", teacher, given, _RES),
+        _rows("weight", weight, tok, _F32, True), _rows("loss", loss, tok, _F32),
+        _rows("lse", lse, tok, _F32), _rows("total", total, (1,), _F32, True), dp,
+        _ptr(status, i32), _stream(stream)))
+
+
+def distill_loss_backward(logits, ids, teacher, weight, lse, dlogits, status, temperature=1.0,
+                          scale=1.0, stream=None):
+    """dlogits (may be logits): gradient of distill_loss's summed loss, from the
+    forward's inputs and lse."""
+    given, c = _distill_config(logits, ids, teacher, temperature, scale)
+    zp, c.z_ld = _logits("logits", logits, (c.T, c.V), logits.dtype)
+    dp, c.dz_ld = _logits("dlogits", dlogits, (c.T, c.V), logits.dtype)
+    tok = given[:1]
+    _check("moe_distill_loss_backward", lib().moe_distill_loss_backward(
+        ctypes.byref(c), zp, _rows("ids", ids, given, _I32), _rows("teacher", teacher, given, _RES),
+        _rows("weight", weight, tok, _F32, True), _rows("lse", lse, tok, _F32), dp,
+        _ptr(status, i32), _stream(stream)))

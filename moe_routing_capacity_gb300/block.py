@@ -3,6 +3,7 @@ branch, the norms around both, and the clipping of their gradients.
 
     n1 = norm(h) w_pre1                        abi.norm_residual
     q, k, v = n1 W_qkv^T, turned               abi.matmul, abi.rotary
+                                               (with head norms: abi.head_norm_rotary)
     b1 = attention(q, k, v) W_o^T              abi.attention, abi.matmul
     h2 = h + gate1 (norm(b1) w_post1),  n2 = norm(h2) w_pre2      (one call)
     b2 = MoE(n2)                               PooledWaveMoE.forward
@@ -23,9 +24,10 @@ from .workloads import _gen, _normal_bf16
 BF, F32 = torch.bfloat16, torch.float32
 
 
-def draw_block_weights(d_model, n_heads, n_kv_heads, head_dim, device="cpu", seed=0) -> dict:
+def draw_block_weights(d_model, n_heads, n_kv_heads, head_dim, device="cpu", seed=0,
+                       head_norm=False) -> dict:
     """Seeded weights: projections N(0, 1/fan_in), norms around 1, gates
-    around 1/2, all bf16."""
+    around 1/2, all bf16; with head_norm, w_q and w_k of the heads' norms."""
     dev = torch.device(device)
     n_qkv = (n_heads + 2 * n_kv_heads) * head_dim
     w = {"W_qkv": _normal_bf16((n_qkv, d_model), d_model ** -0.5, _gen(dev, seed, "W_qkv"), dev),
@@ -34,12 +36,16 @@ def draw_block_weights(d_model, n_heads, n_kv_heads, head_dim, device="cpu", see
     for n, mean in (("w_pre1", 1.0), ("w_post1", 1.0), ("w_pre2", 1.0), ("w_post2", 1.0),
                     ("gate1", 0.5), ("gate2", 0.5)):
         w[n] = (mean + _normal_bf16((d_model,), 0.1, _gen(dev, seed, n), dev).float()).to(BF)
+    if head_norm:
+        for n in ("w_q", "w_k"):
+            w[n] = (1.0 + _normal_bf16((head_dim,), 0.1, _gen(dev, seed, n), dev).float()).to(BF)
     return w
 
 
 class TrainingBlock:
     """``layer``: the MoE branch (a PooledWaveMoE); ``weights``: as
-    draw_block_weights gives them; ``table``: rotary angles [positions,
+    draw_block_weights gives them (with w_q and w_k, every query and key head is
+    normalised before it is turned); ``table``: rotary angles [positions,
     rot_dim / 2, 2] fp32 (abi.rotary_table)."""
 
     def __init__(self, layer, weights, n_heads, n_kv_heads, head_dim, table, n_seqs,
@@ -59,6 +65,14 @@ class TrainingBlock:
         self.rstd = [e(T, dt=F32) for _ in range(4)]    # n1; b1 and n2; b2
         self.qkv = e(T, hq + 2 * hk, D)
         self.q, self.k, self.v = self.qkv[:, :hq], self.qkv[:, hq:hq + hk], self.qkv[:, hq + hk:]
+        # the heads as attention reads them: in place of the projection's, but for the head
+        # norms' gradient, which needs those
+        self.head_norm = "w_q" in self.w
+        if self.head_norm:
+            self.qk = e(T, hq + hk, D)
+            self.qa, self.ka = self.qk[:, :hq], self.qk[:, hq:]
+        else:
+            self.qa, self.ka = self.q, self.k
         self.att, self.rest, self.lse = e(T, hq, D), e(T, hq, D), e(hq, T, dt=F32)
         self.b1 = e(T, d)
 
@@ -76,9 +90,14 @@ class TrainingBlock:
                           eps=self.eps, stream=stream)
         abi.matmul(self.n1, w["W_qkv"], T, (self.hq + 2 * self.hk) * self.D, d,
                    self.qkv.view(T, -1), self.status, stream=stream)
-        abi.rotary(self.q, self.k, self.table, self.pos, self.q, self.k, self.status,
-                   interleaved=self.interleaved, stream=stream)
-        abi.attention(self.plan, self.q, self.k, self.v, self.att, self.lse, self.status,
+        if self.head_norm:
+            abi.head_norm_rotary(self.q, self.k, w["w_q"], w["w_k"], self.table, self.pos,
+                                 self.qa, self.ka, self.status, eps=self.eps,
+                                 interleaved=self.interleaved, stream=stream)
+        else:
+            abi.rotary(self.q, self.k, self.table, self.pos, self.q, self.k, self.status,
+                       interleaved=self.interleaved, stream=stream)
+        abi.attention(self.plan, self.qa, self.ka, self.v, self.att, self.lse, self.status,
                       rest=self.rest, stream=stream)
         abi.matmul(self.att.view(T, qd), w["W_o"], T, d, qd, self.b1, self.status, stream=stream)
         abi.norm_residual(self.b1, h, w["gate1"], w["w_post1"], w["w_pre2"], self.h2, self.n2,
@@ -101,6 +120,8 @@ class TrainingBlock:
                 self.db, self.dh2, self.dn1 = (e(T, d, dt=BF) for _ in range(3))
                 self.datt, self.dqkv = e(T, hq, D, dt=BF), e(T, hq + 2 * hk, D, dt=BF)
                 self.ws_norm = e(abi.norm_residual_workspace(T, d), dt=torch.uint8)
+                if self.head_norm:
+                    self.ws_heads = e(abi.head_norm_rotary_workspace(T, hq, hk, D), dt=torch.uint8)
                 self.ws_att = e(max(1, self.plan.backward_ws_bytes), dt=torch.uint8)
         g = self.g
         abi.norm_residual_backward(None, dh3, self.b2, None, w["gate2"], w["w_post2"], None,
@@ -117,10 +138,16 @@ class TrainingBlock:
         abi.matmul(self.db, self.att.view(T, qd), d, qd, T, g["W_o"], self.status, a_mn=True,
                    b_mn=True, stream=stream)
         dq, dk, dv = self.dqkv[:, :hq], self.dqkv[:, hq:hq + hk], self.dqkv[:, hq + hk:]
-        abi.attention_backward(self.plan, self.q, self.k, self.v, self.att, self.rest, self.lse,
+        abi.attention_backward(self.plan, self.qa, self.ka, self.v, self.att, self.rest, self.lse,
                                self.datt, dq, dk, dv, self.ws_att, self.status, stream=stream)
-        abi.rotary(dq, dk, self.table, self.pos, dq, dk, self.status,
-                   interleaved=self.interleaved, inverse=True, stream=stream)
+        if self.head_norm:
+            abi.head_norm_rotary_backward(dq, dk, self.q, self.k, w["w_q"], w["w_k"], self.table,
+                                          self.pos, dq, dk, g["w_q"], g["w_k"], self.ws_heads,
+                                          self.status, eps=self.eps, interleaved=self.interleaved,
+                                          stream=stream)
+        else:
+            abi.rotary(dq, dk, self.table, self.pos, dq, dk, self.status,
+                       interleaved=self.interleaved, inverse=True, stream=stream)
         flat = self.dqkv.view(T, n_qkv)
         abi.matmul(flat, w["W_qkv"], T, d, n_qkv, self.dn1, self.status, b_mn=True, stream=stream)
         abi.matmul(flat, self.n1, n_qkv, d, T, g["W_qkv"], self.status, a_mn=True, b_mn=True,

@@ -194,11 +194,13 @@ extern "C" {
 int moe_abi_version(void) { return 6; }
 
 int moe_check_status(void) {
-    const int v[9] = {check_status_route(),    check_status_gemm(),
-                      check_status_backward(), check_status_expert_pair(),
-                      check_status_norm(),     check_status_rotary(),
-                      check_status_attention_fwd(), check_status_attention_bwd(),
-                      check_status_clip()};
+    const int v[] = {check_status_route(),    check_status_gemm(),
+                     check_status_backward(), check_status_expert_pair(),
+                     check_status_norm(),     check_status_rotary(),
+                     check_status_attention_fwd(), check_status_attention_bwd(),
+                     check_status_clip(),     check_status_head_norm(),
+                     check_status_router_select(), check_status_embedding(),
+                     check_status_distill()};
     for (int x : v)
         if (x) return x;
     return 0;
@@ -276,17 +278,8 @@ int moe_plan(const moe_config_t* cfg, moe_plan_t* plan) {
     return MOE_OK;
 }
 
-int moe_router_topk(const moe_config_t* cfg, const uint16_t* x, const uint16_t* Wr,
-                    const float* bias, float* logits, int32_t* idx, float* w, uint8_t* tie,
-                    int32_t* status, void* stream) {
-    MOE_NVTX_RANGE();
-    Geom G;
-    int rc = make_geom(cfg, &G);
-    if (rc) return rc;
-    if (G.g.T == 0) return MOE_OK;
-    if (!x || !Wr || !logits || !idx || !w || !tie || !status) return MOE_EINVAL;
-    if (!aligned16(x) || !aligned16(Wr)) return MOE_EINVAL;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
+static int router_gemm(const Geom& G, const uint16_t* x, const uint16_t* Wr, const float* bias,
+                       float* logits, int32_t* status, cudaStream_t st) {
     GemmDesc d;
     std::memset(&d, 0, sizeof(d));
     d.a_mode = A_DENSE;
@@ -304,24 +297,31 @@ int moe_router_topk(const moe_config_t* cfg, const uint16_t* x, const uint16_t* 
     // the workloads' sizes); wider routers use 128 x 128 tiles
     d.bn = G.g.E <= 384 ? 384 : 128;
     d.name = "gemm_router";
-    if ((rc = gemm_launch(d, st))) return rc;
-    return launch_topk(logits, G.g.T, G.g.E, G.g.k, idx, w, tie, st);
+    return gemm_launch(d, st);
 }
 
-int moe_route_project(const moe_config_t* cfg, const uint16_t* x, const uint16_t* Wr,
-                      const float* bias, const uint16_t* W_ld, float* logits, int32_t* idx,
-                      float* w, uint8_t* tie, uint16_t* z, int32_t* status, void* stream) {
+int moe_router_topk(const moe_config_t* cfg, const uint16_t* x, const uint16_t* Wr,
+                    const float* bias, float* logits, int32_t* idx, float* w, uint8_t* tie,
+                    int32_t* status, void* stream) {
     MOE_NVTX_RANGE();
     Geom G;
     int rc = make_geom(cfg, &G);
     if (rc) return rc;
     if (G.g.T == 0) return MOE_OK;
-    if (!x || !Wr || !W_ld || !logits || !idx || !w || !tie || !z || !status) return MOE_EINVAL;
-    if (!aligned16(x) || !aligned16(Wr) || !aligned16(W_ld) || !aligned16(z)) return MOE_EINVAL;
+    if (!x || !Wr || !logits || !idx || !w || !tie || !status) return MOE_EINVAL;
+    if (!aligned16(x) || !aligned16(Wr)) return MOE_EINVAL;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (G.g.L % 256) {   // no whole latent tiles: the two separate passes
-        if ((rc = moe_router_topk(cfg, x, Wr, bias, logits, idx, w, tie, status, stream))) return rc;
-        return moe_latent_proj(x, W_ld, G.g.T, G.d, G.g.L, z, status, stream);
+    if ((rc = router_gemm(G, x, Wr, bias, logits, status, st))) return rc;
+    return launch_topk(logits, G.g.T, G.g.E, G.g.k, idx, w, tie, st);
+}
+
+// Router logits and the latent projection, one pass over x where L is in whole tiles.
+static int route_gemm(const Geom& G, const uint16_t* x, const uint16_t* Wr, const float* bias,
+                      const uint16_t* W_ld, float* logits, uint16_t* z, int32_t* status,
+                      cudaStream_t st) {
+    if (G.g.L % 256) {
+        if (const int rc = router_gemm(G, x, Wr, bias, logits, status, st)) return rc;
+        return moe_latent_proj(x, W_ld, G.g.T, G.d, G.g.L, z, status, st);
     }
     GemmDesc d;
     std::memset(&d, 0, sizeof(d));
@@ -344,8 +344,37 @@ int moe_route_project(const moe_config_t* cfg, const uint16_t* x, const uint16_t
     d.bias = bias;
     d.status = status;
     d.name = "gemm_latent_router";
-    if ((rc = gemm_launch(d, st))) return rc;
+    return gemm_launch(d, st);
+}
+
+int moe_route_project(const moe_config_t* cfg, const uint16_t* x, const uint16_t* Wr,
+                      const float* bias, const uint16_t* W_ld, float* logits, int32_t* idx,
+                      float* w, uint8_t* tie, uint16_t* z, int32_t* status, void* stream) {
+    MOE_NVTX_RANGE();
+    Geom G;
+    int rc = make_geom(cfg, &G);
+    if (rc) return rc;
+    if (G.g.T == 0) return MOE_OK;
+    if (!x || !Wr || !W_ld || !logits || !idx || !w || !tie || !z || !status) return MOE_EINVAL;
+    if (!aligned16(x) || !aligned16(Wr) || !aligned16(W_ld) || !aligned16(z)) return MOE_EINVAL;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((rc = route_gemm(G, x, Wr, bias, W_ld, logits, z, status, st))) return rc;
     return launch_topk(logits, G.g.T, G.g.E, G.g.k, idx, w, tie, st);
+}
+
+int moe_route_logits(const moe_config_t* cfg, const uint16_t* x, const uint16_t* Wr,
+                     const uint16_t* W_ld, float* logits, uint16_t* z, int32_t* status,
+                     void* stream) {
+    MOE_NVTX_RANGE();
+    Geom G;
+    const int rc = make_geom(cfg, &G);
+    if (rc) return rc;
+    if (G.g.T == 0) return MOE_OK;
+    if (!x || !Wr || !W_ld != !z || !logits || !status) return MOE_EINVAL;
+    if (!aligned16(x) || !aligned16(Wr) || !aligned16(W_ld) || !aligned16(z)) return MOE_EINVAL;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (!z) return router_gemm(G, x, Wr, nullptr, logits, status, st);
+    return route_gemm(G, x, Wr, nullptr, W_ld, logits, z, status, st);
 }
 
 int moe_latent_proj(const uint16_t* in, const uint16_t* W, int64_t M, int32_t K, int32_t N,
@@ -906,7 +935,8 @@ int moe_backward_plan_ragged(const moe_config_t* cfg, moe_backward_ws_t* layout)
     return MOE_OK;
 }
 
-static int layer_backward(const Geom& G, const moe_backward_args_t* a, void* stream) {
+static int layer_backward(const Geom& G, const moe_backward_args_t* a, void* stream,
+                          const moe_routing_t* routing = nullptr, const float* logits = nullptr) {
     if (!a) return MOE_EINVAL;
     if (G.g.T == 0) return MOE_OK;
     const void* need[] = {a->x, a->Wr, a->W_ld, a->Wg, a->Wu, a->Wd, a->W_lu, a->idx, a->w,
@@ -929,7 +959,8 @@ static int layer_backward(const Geom& G, const moe_backward_args_t* a, void* str
     if (a->ws_bytes < w.total) return MOE_ENOSPC;
     int dev, sms, rc;
     if ((rc = current_device(&dev, &sms))) return rc;
-    return launch_backward(G.g, G.d, G.H, G.Hs, G.ns, *a, static_cast<cudaStream_t>(stream));
+    return launch_backward(G.g, G.d, G.H, G.Hs, G.ns, *a, static_cast<cudaStream_t>(stream), routing,
+                           logits);
 }
 
 int moe_layer_backward(const moe_config_t* cfg, const moe_backward_args_t* a, void* stream) {
@@ -947,6 +978,19 @@ int moe_layer_backward_ragged(const moe_config_t* cfg, const moe_backward_args_t
     const int rc = make_geom_ragged(cfg, &G);
     if (rc) return rc;
     return layer_backward(G, a, stream);
+}
+
+int moe_layer_backward_routed(const moe_config_t* cfg, int ragged, const moe_backward_args_t* a,
+                              const moe_routing_t* routing, const float* logits, void* stream) {
+    MOE_NVTX_RANGE();
+    Geom G;
+    int rc = ragged ? make_geom_ragged(cfg, &G) : make_geom(cfg, &G);
+    if (rc) return rc;
+    if ((rc = routing_check(routing))) return rc;
+    if ((ragged & ~1) || routing->n_experts != G.g.E || routing->top_k != G.g.k ||
+        routing->grad_f32 || (G.g.T > 0 && !logits) || !aligned16(logits))
+        return MOE_EINVAL;
+    return layer_backward(G, a, stream, routing, logits);
 }
 
 int moe_combine(const moe_config_t* cfg, const uint16_t* ypool, const int32_t* slot_of,

@@ -1,6 +1,7 @@
 // abi_block.cu -- C entry points of the training block's operators (norm with
-// residual and gate, rotary positions, packed causal attention, gradient
-// clipping): argument checks, then the launches.
+// residual and gate, rotary positions, with and without head norms, packed causal
+// attention, gradient clipping) and of what stands before and behind the blocks (choice
+// of experts, embedding, distillation loss): argument checks, then the launches.
 #include <cmath>
 
 #include "internal.h"
@@ -53,6 +54,68 @@ int attention_ok(const moe_attention_t* c) {
     return MOE_OK;
 }
 
+// In place means the same strides (an extent of one has none).
+bool in_place_ok(const void* in, const void* out, int64_t T, int64_t heads, int64_t in_t,
+                 int64_t out_t, int64_t in_h, int64_t out_h) {
+    return in != out || ((T <= 1 || in_t == out_t) && (heads <= 1 || in_h == out_h));
+}
+
+int head_norm_ok(const moe_head_norm_t* c) {
+    if (!c || c->T < 0 || c->hq <= 0 || c->hk < 0 || c->hq > 65536 || c->hk > 65536 ||
+        c->D < 16 || c->D > 512 || c->D % 8 || c->rot_dim < 0 || c->rot_dim % 16 ||
+        c->rot_dim > c->D || (c->interleaved & ~1) || !(c->eps >= 0) || !std::isfinite(c->eps) ||
+        (c->rot_dim > 0 && c->table_rows <= 0))
+        return MOE_EINVAL;
+    if (!strides_ok(c->T, c->hq, c->D, c->q_t, c->q_h) ||
+        !strides_ok(c->T, c->hq, c->D, c->qo_t, c->qo_h) ||
+        (c->hk && (!strides_ok(c->T, c->hk, c->D, c->k_t, c->k_h) ||
+                   !strides_ok(c->T, c->hk, c->D, c->ko_t, c->ko_h))))
+        return MOE_EINVAL;
+    return MOE_OK;
+}
+
+int routing_ok(const moe_routing_t* c) {
+    if (!c || c->T < 0 || c->n_experts <= 0 || c->n_experts > 1024 || c->top_k <= 0 ||
+        c->top_k > 32 || (c->score & ~1) || c->n_groups <= 0 || c->n_groups > 32 ||
+        c->n_experts % c->n_groups || c->groups_kept <= 0 || c->groups_kept > c->n_groups ||
+        c->group_top < 1 || c->group_top > 2 || (c->renorm & ~1) || !std::isfinite(c->scale) ||
+        (c->grad_f32 & ~1) || c->reserved)
+        return MOE_EINVAL;
+    const int per = c->n_experts / c->n_groups;
+    if (c->group_top > per || c->top_k > per * c->groups_kept ||
+        (c->groups_kept < c->n_groups && per > 32 * moe::router_select_lanes(c->n_groups)))
+        return MOE_EINVAL;
+    return MOE_OK;
+}
+
+bool embedding_sizes_ok(int64_t T, int64_t V, int32_t d) {
+    return T >= 0 && T < (1ll << 31) - 256 && V > 0 && V < (1ll << 31) - 256 && d >= 8 &&
+           d <= 65536 && d % 8 == 0;
+}
+
+int embedding_ok(const moe_embedding_t* c) {
+    if (!c || !embedding_sizes_ok(c->T, c->V, c->d) || (c->table_f32 & ~1) || (c->out_f32 & ~1) ||
+        (c->accumulate & ~1) || !std::isfinite(c->scale) || c->reserved)
+        return MOE_EINVAL;
+    return MOE_OK;
+}
+
+int distill_ok(const moe_distill_t* c) {
+    if (!c || c->T < 0 || c->V <= 0 || c->V >= (1ll << 31) || c->K <= 0 ||
+        c->K > MOE_DISTILL_MAX_ENTRIES || (c->z_f32 & ~1) || (c->teacher_f32 & ~1) ||
+        !(c->temperature > 0) || !std::isfinite(c->temperature) || !std::isfinite(c->scale) ||
+        c->reserved)
+        return MOE_EINVAL;
+    if (c->T > 1 && (c->z_ld < c->V || c->z_ld >= (1ll << 38))) return MOE_EINVAL;
+    return MOE_OK;
+}
+
+bool distill_grad_ok(const moe_distill_t* c, const void* z, const void* dz) {
+    if (c->T > 1 && (c->dz_ld < c->V || c->dz_ld >= (1ll << 38))) return false;
+    return reinterpret_cast<uintptr_t>(dz) % (c->z_f32 ? 4 : 2) == 0 &&
+           (z != dz || c->T <= 1 || c->z_ld == c->dz_ld);
+}
+
 bool qkvo_strides_ok(const moe_attention_t* c) {
     return strides_ok(c->T, c->n_heads, c->head_dim, c->q_t, c->q_h) &&
            strides_ok(c->T, c->n_kv_heads, c->head_dim, c->k_t, c->k_h) &&
@@ -61,6 +124,8 @@ bool qkvo_strides_ok(const moe_attention_t* c) {
 }
 
 }  // namespace
+
+int moe::routing_check(const moe_routing_t* c) { return routing_ok(c); }
 
 extern "C" {
 
@@ -253,6 +318,164 @@ int moe_grad_clip(const moe_grad_tensor_t* tensors, int64_t n_tensors, float max
     if (const int rc = device_ok()) return rc;
     return moe::launch_grad_clip(tensors, n_tensors, max_norm, norm, ws,
                                  static_cast<cudaStream_t>(stream));
+}
+
+int moe_head_norm_rotary(const moe_head_norm_t* cfg, const uint16_t* q, const uint16_t* k,
+                         const uint16_t* w_q, const uint16_t* w_k, const float* table,
+                         const int32_t* pos, uint16_t* q_out, uint16_t* k_out, int32_t* status,
+                         void* stream) {
+    MOE_NVTX_RANGE();
+    if (const int rc = head_norm_ok(cfg)) return rc;
+    if (cfg->T == 0) return MOE_OK;
+    const bool has_k = cfg->hk > 0;
+    if (!given16(q) || !given16(w_q) || !given16(q_out) || !status || !aligned16(table) ||
+        (cfg->rot_dim > 0) != (table != nullptr) || has_k != (k != nullptr) ||
+        has_k != (w_k != nullptr) || has_k != (k_out != nullptr) || !aligned16(k) ||
+        !aligned16(w_k) || !aligned16(k_out) ||
+        !in_place_ok(q, q_out, cfg->T, cfg->hq, cfg->q_t, cfg->qo_t, cfg->q_h, cfg->qo_h) ||
+        (has_k &&
+         !in_place_ok(k, k_out, cfg->T, cfg->hk, cfg->k_t, cfg->ko_t, cfg->k_h, cfg->ko_h)))
+        return MOE_EINVAL;
+    if (const int rc = device_ok()) return rc;
+    return moe::launch_head_norm(*cfg, q, k, w_q, w_k, table, pos, q_out, k_out, status,
+                                 static_cast<cudaStream_t>(stream));
+}
+
+int moe_head_norm_rotary_workspace(int64_t T, int32_t hq, int32_t hk, int32_t D, int64_t* bytes) {
+    if (!bytes || T < 0 || hq <= 0 || hk < 0 || D < 16 || D > 512 || D % 8) return MOE_EINVAL;
+    *bytes = moe::head_norm_backward_ws(D);
+    return MOE_OK;
+}
+
+int moe_head_norm_rotary_backward(const moe_head_norm_t* cfg, const uint16_t* dq,
+                                  const uint16_t* dk, const uint16_t* q, const uint16_t* k,
+                                  const uint16_t* w_q, const uint16_t* w_k, const float* table,
+                                  const int32_t* pos, uint16_t* dq_out, uint16_t* dk_out,
+                                  float* dw_q, float* dw_k, void* ws, int64_t ws_bytes,
+                                  int32_t* status, void* stream) {
+    MOE_NVTX_RANGE();
+    if (const int rc = head_norm_ok(cfg)) return rc;
+    if (!strides_ok(cfg->T, cfg->hq, cfg->D, cfg->dq_t, cfg->dq_h) ||
+        (cfg->hk && !strides_ok(cfg->T, cfg->hk, cfg->D, cfg->dk_t, cfg->dk_h)))
+        return MOE_EINVAL;
+    if (cfg->T == 0) {
+        if (const int rc = zero_sum(dw_q, cfg->D, stream)) return rc;
+        return zero_sum(dw_k, cfg->D, stream);
+    }
+    const bool has_k = cfg->hk > 0;
+    if (!given16(dq) || !given16(q) || !given16(w_q) || !given16(dq_out) || !dw_q ||
+        !given16(ws) || !status || !aligned16(table) ||
+        (cfg->rot_dim > 0) != (table != nullptr) || has_k != (dk != nullptr) ||
+        has_k != (k != nullptr) || has_k != (w_k != nullptr) || has_k != (dk_out != nullptr) ||
+        has_k != (dw_k != nullptr) || !aligned16(dk) || !aligned16(k) || !aligned16(w_k) ||
+        !aligned16(dk_out))
+        return MOE_EINVAL;
+    if (!in_place_ok(q, dq_out, cfg->T, cfg->hq, cfg->q_t, cfg->qo_t, cfg->q_h, cfg->qo_h) ||
+        !in_place_ok(dq, dq_out, cfg->T, cfg->hq, cfg->dq_t, cfg->qo_t, cfg->dq_h, cfg->qo_h) ||
+        (has_k &&
+         (!in_place_ok(k, dk_out, cfg->T, cfg->hk, cfg->k_t, cfg->ko_t, cfg->k_h, cfg->ko_h) ||
+          !in_place_ok(dk, dk_out, cfg->T, cfg->hk, cfg->dk_t, cfg->ko_t, cfg->dk_h, cfg->ko_h))))
+        return MOE_EINVAL;
+    if (ws_bytes < moe::head_norm_backward_ws(cfg->D)) return MOE_ENOSPC;
+    if (const int rc = device_ok()) return rc;
+    return moe::launch_head_norm_backward(*cfg, dq, dk, q, k, w_q, w_k, table, pos, dq_out, dk_out,
+                                          dw_q, dw_k, ws, status,
+                                          static_cast<cudaStream_t>(stream));
+}
+
+int moe_router_select(const moe_routing_t* cfg, const float* logits, const float* bias,
+                      int32_t* idx, float* w, void* stream) {
+    MOE_NVTX_RANGE();
+    if (const int rc = routing_ok(cfg)) return rc;
+    if (cfg->T == 0) return MOE_OK;
+    if (!given16(logits) || !given16(idx) || !given16(w) || !aligned16(bias)) return MOE_EINVAL;
+    if (const int rc = device_ok()) return rc;
+    return moe::launch_router_select(*cfg, logits, bias, idx, w,
+                                     static_cast<cudaStream_t>(stream));
+}
+
+int moe_router_select_backward(const moe_routing_t* cfg, const float* logits, const int32_t* idx,
+                               const float* dw, void* dlogits, void* stream) {
+    MOE_NVTX_RANGE();
+    if (const int rc = routing_ok(cfg)) return rc;
+    if (cfg->T == 0) return MOE_OK;
+    if (!given16(logits) || !given16(idx) || !given16(dw) || !given16(dlogits)) return MOE_EINVAL;
+    if (const int rc = device_ok()) return rc;
+    return moe::launch_router_select_backward(*cfg, logits, idx, dw, dlogits,
+                                              static_cast<cudaStream_t>(stream));
+}
+
+int moe_embedding(const moe_embedding_t* cfg, const void* table, const int32_t* ids, void* out,
+                  int32_t* status, void* stream) {
+    MOE_NVTX_RANGE();
+    if (const int rc = embedding_ok(cfg)) return rc;
+    if (cfg->T == 0) return MOE_OK;
+    if (!given16(table) || !ids || !given16(out) || !status) return MOE_EINVAL;
+    if (const int rc = device_ok()) return rc;
+    return moe::launch_embedding(*cfg, table, ids, out, status, static_cast<cudaStream_t>(stream));
+}
+
+int moe_embedding_workspace(int64_t T, int64_t V, int32_t d, int64_t* plan_bytes) {
+    if (!plan_bytes || !embedding_sizes_ok(T, V, d)) return MOE_EINVAL;
+    *plan_bytes = moe::embedding_plan_bytes(T, V, d);
+    return MOE_OK;
+}
+
+int moe_embedding_plan(int64_t T, int64_t V, int32_t d, const int32_t* ids, void* plan,
+                       int64_t plan_bytes, int32_t* status, void* stream) {
+    MOE_NVTX_RANGE();
+    if (!embedding_sizes_ok(T, V, d)) return MOE_EINVAL;
+    if (T == 0) return MOE_OK;
+    if (!ids || !given16(plan) || !status) return MOE_EINVAL;
+    if (plan_bytes < moe::embedding_plan_bytes(T, V, d)) return MOE_ENOSPC;
+    if (const int rc = device_ok()) return rc;
+    return moe::launch_embedding_plan(T, V, d, ids, plan, status,
+                                      static_cast<cudaStream_t>(stream));
+}
+
+int moe_embedding_backward(const moe_embedding_t* cfg, const void* plan, int64_t plan_bytes,
+                           const void* dout, void* dtable, void* stream) {
+    MOE_NVTX_RANGE();
+    if (const int rc = embedding_ok(cfg)) return rc;
+    if (cfg->T == 0) {
+        if (cfg->accumulate) return MOE_OK;
+        return zero_sum(dtable, cfg->V * cfg->d / (cfg->table_f32 ? 1 : 2), stream);
+    }
+    if (!given16(plan) || !given16(dout) || !given16(dtable)) return MOE_EINVAL;
+    if (plan_bytes < moe::embedding_plan_bytes(cfg->T, cfg->V, cfg->d)) return MOE_ENOSPC;
+    if (const int rc = device_ok()) return rc;
+    return moe::launch_embedding_backward(*cfg, plan, dout, dtable,
+                                          static_cast<cudaStream_t>(stream));
+}
+
+int moe_distill_loss(const moe_distill_t* cfg, const void* z, const int32_t* ids,
+                     const void* teacher, const float* weight, float* loss, float* lse,
+                     float* total, void* dlogits, int32_t* status, void* stream) {
+    MOE_NVTX_RANGE();
+    if (const int rc = distill_ok(cfg)) return rc;
+    if (cfg->T == 0) return zero_sum(total, 1, stream);
+    if (!z || !ids || !teacher || !loss || !lse || !status ||
+        reinterpret_cast<uintptr_t>(z) % (cfg->z_f32 ? 4 : 2) ||
+        (dlogits && !distill_grad_ok(cfg, z, dlogits)))
+        return MOE_EINVAL;
+    if (const int rc = device_ok()) return rc;
+    return moe::launch_distill(*cfg, z, ids, teacher, weight, loss, lse, total, dlogits, status,
+                               static_cast<cudaStream_t>(stream));
+}
+
+int moe_distill_loss_backward(const moe_distill_t* cfg, const void* z, const int32_t* ids,
+                              const void* teacher, const float* weight, const float* lse,
+                              void* dlogits, int32_t* status, void* stream) {
+    MOE_NVTX_RANGE();
+    if (const int rc = distill_ok(cfg)) return rc;
+    if (cfg->T == 0) return MOE_OK;
+    if (!z || !ids || !teacher || !lse || !dlogits || !status ||
+        reinterpret_cast<uintptr_t>(z) % (cfg->z_f32 ? 4 : 2) ||
+        !distill_grad_ok(cfg, z, dlogits))
+        return MOE_EINVAL;
+    if (const int rc = device_ok()) return rc;
+    return moe::launch_distill_backward(*cfg, z, ids, teacher, weight, lse, dlogits, status,
+                                        static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

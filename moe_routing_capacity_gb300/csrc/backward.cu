@@ -8,7 +8,7 @@
 //   X_row = z_t                          -> dz_t = sum_kept dX_row (the return of the
 //                                           exchange, in reverse)
 //   z = x W_ld^T                         -> dW_ld
-//   w = softmax(selected logits)         -> dlogits, dWr
+//   w = softmax(selected logits)         -> dlogits, dWr   (or another rule's weights)
 //   x                                    -> dx
 // Every product runs on the tcgen05 GEMM engine; products over the token or
 // row axis read their operands MN-major.
@@ -305,7 +305,8 @@ BackwardWs backward_ws_layout(const DispatchGeom& g, int d, int H, int Hs, int n
 }
 
 int launch_backward(const DispatchGeom& g, int d, int H, int Hs, int ns,
-                    const moe_backward_args_t& a, cudaStream_t st) {
+                    const moe_backward_args_t& a, cudaStream_t st, const moe_routing_t* routing,
+                    const float* logits) {
     const BackwardWs L_ = backward_ws_layout(g, d, H, Hs, ns);
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
     auto bf = [&](size_t off) { return reinterpret_cast<uint16_t*>(ws + off); };
@@ -571,7 +572,11 @@ int launch_backward(const DispatchGeom& g, int d, int H, int Hs, int ns,
     q.b_rows = d; q.out = a.dW_ld; q.ldo = d;
     if ((rc = mm(q, "bwd_gemm_dW_ld"))) return rc;
     // ---- router
-    {
+    if (routing) {
+        moe_routing_t rule = *routing;
+        rule.T = T;
+        if ((rc = launch_router_select_backward(rule, logits, a.idx, dw, dl, st))) return rc;
+    } else {
         const unsigned grid = static_cast<unsigned>((T + 7) / 8);
         router_bwd_kernel<<<grid, 256, 0, st>>>(a.idx, a.w, dw, T, k, E, dl);
         if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;

@@ -1,0 +1,377 @@
+// distill.cu -- loss of a student's logits z against a teacher's top logits y, and its
+// gradient.
+//
+//     p = softmax(y / tau) over a token's given entries,  q = softmax(z / tau) over all V
+//     loss = scale w tau^2 sum_k p_k (log p_k - log q_{i_k})
+//     dz_v = scale w tau (q_v - sum over k with i_k = v of p_k)
+//
+// A team of threads takes a row.  One pass over it carries the running maximum and the sum
+// of exponentials (in base 2, the temperature folded into the factor); the entries' few
+// logits are gathered behind it; a second pass, where the gradient is wanted, writes q, and
+// the entries' places are written again behind that.  The second pass finds the row in L2.
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kMaxEntries = MOE_DISTILL_MAX_ENTRIES;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+enum Mode { kForward = 0, kStep = 1, kBackward = 2 };
+
+struct DistillParams {
+    int64_t T, V, z_ld, dz_ld;
+    int K, teacher_f32;
+    float c, inv_tau, loss_f, grad_f;   // log2(e) / tau, 1 / tau, scale tau^2, scale tau
+    const void *z, *teacher;
+    const int32_t* ids;
+    const float* weight;
+    float *loss, *lse;
+    void* dz;
+    int32_t* status;
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+__device__ __forceinline__ void put(float* o, float v) { *o = v; }
+__device__ __forceinline__ void put(uint16_t* o, float v) {
+    const __nv_bfloat16 b = __float2bfloat16_rn(v);
+    *o = *reinterpret_cast<const uint16_t*>(&b);
+}
+
+// The 16 bytes of a vector as floats.
+__device__ __forceinline__ void spread(const uint4& v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ void spread(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16_lo(w[i]);
+        f[2 * i + 1] = bf16_hi(w[i]);
+    }
+}
+__device__ __forceinline__ uint4 gather(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+}
+__device__ __forceinline__ uint4 gather(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
+// Running maximum and sum of 2^(x - maximum).  Every operation is written out, so that the
+// losses have the same bits with and without the gradient.
+struct Run {
+    float m = -INFINITY, s = 0.0f;
+    // raises the maximum to at least v; what to subtract from the exponents
+    __device__ __forceinline__ float raise(float v) {
+        if (v > m) {
+            s = __fmul_rn(s, exp2_fast(__fsub_rn(m, v)));
+            m = v;
+        }
+        return m == -INFINITY ? 0.0f : m;
+    }
+    __device__ __forceinline__ void add(float x) {
+        const float b = raise(x);
+        s = __fadd_rn(s, exp2_fast(__fsub_rn(x, b)));
+    }
+    __device__ __forceinline__ void join(float om, float os) {
+        const float b = raise(om);
+        s = __fmaf_rn(os, exp2_fast(__fsub_rn(om, b)), s);
+    }
+};
+
+template <int TEAM>
+struct Team {
+    int tid;
+    float* red;   // [3][TEAM / 32], TEAM > 32
+    __device__ __forceinline__ void sync() const {
+        if (TEAM == 32) __syncwarp();
+        else __syncthreads();
+    }
+    __device__ __forceinline__ Run join(Run r) const {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            r.join(__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o));
+        if (TEAM == 32) return r;
+        __syncthreads();
+        if ((tid & 31) == 0) {
+            red[tid >> 5] = r.m;
+            red[TEAM / 32 + (tid >> 5)] = r.s;
+        }
+        __syncthreads();
+        Run all;
+        for (int i = 0; i < TEAM / 32; ++i) all.join(red[i], red[TEAM / 32 + i]);
+        return all;
+    }
+    __device__ __forceinline__ float sum(float v) const {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (TEAM == 32) return v;
+        __syncthreads();
+        if ((tid & 31) == 0) red[tid >> 5] = v;
+        __syncthreads();
+        float s = 0.0f;
+        for (int i = 0; i < TEAM / 32; ++i) s += red[i];
+        return s;
+    }
+};
+
+constexpr int kUnroll = 4;   // vectors that a thread has under way
+
+template <typename Z, int TEAM, int MODE>
+__global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM) distill_kernel(const DistillParams p) {
+    constexpr int kTeams = TEAM == 32 ? 8 : 1;
+    constexpr int E = 16 / static_cast<int>(sizeof(Z));
+    __shared__ int s_id[kTeams][kMaxEntries];
+    __shared__ float s_p[kTeams][kMaxEntries], s_z[kTeams][kMaxEntries];
+    __shared__ float s_red[TEAM == 32 ? 1 : TEAM / 16];
+    const int which = TEAM == 32 ? static_cast<int>(threadIdx.x >> 5) : 0;
+    Team<TEAM> team{static_cast<int>(TEAM == 32 ? threadIdx.x & 31 : threadIdx.x), s_red};
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + which;
+    if (t >= p.T) return;
+    const int tid = team.tid;
+    int* id = s_id[which];
+    float *pk = s_p[which], *zk = s_z[which];
+    const Z* z = static_cast<const Z*>(p.z) + t * p.z_ld;
+    Z* dz = static_cast<Z*>(p.dz) + t * p.dz_ld;
+    // the row's run of whole vectors
+    const int64_t to_vec = ((16 - (reinterpret_cast<uintptr_t>(z) & 15)) & 15) / sizeof(Z);
+    const int64_t head = to_vec < p.V ? to_vec : p.V;
+    const int64_t nvec = (p.V - head) / E, tail = head + nvec * E;
+
+    const float w = p.weight ? p.weight[t] : 1.0f;
+    // the teacher's distribution
+    Run ty;
+    if (w != 0.0f) {
+        for (int k = tid; k < p.K; k += TEAM) {
+            const int i = p.ids[t * p.K + k];
+            const bool ok = i >= 0 && i < p.V;
+            if (!ok && i != -1) report_error(p.status, MOE_EINVAL);
+            const float y = p.teacher_f32 ? static_cast<const float*>(p.teacher)[t * p.K + k]
+                                          : to_float(static_cast<const uint16_t*>(p.teacher)[t * p.K + k]);
+            id[k] = ok ? i : -1;
+            pk[k] = ok ? __fmul_rn(y, p.c) : -INFINITY;
+            if (ok) ty.add(pk[k]);
+        }
+        ty = team.join(ty);
+    }
+    if (w == 0.0f || (ty.m == -INFINITY && ty.s == 0.0f)) {   // no weight, or no entry
+        if (MODE != kBackward && tid == 0) {
+            p.loss[t] = 0.0f;
+            p.lse[t] = 0.0f;
+        }
+        if (MODE != kForward) {
+            const int64_t d_vec = ((16 - (reinterpret_cast<uintptr_t>(dz) & 15)) & 15) / sizeof(Z);
+            const int64_t h = d_vec < p.V ? d_vec : p.V, n = (p.V - h) / E;
+            for (int64_t i = tid; i < h; i += TEAM) put(dz + i, 0.0f);
+            for (int64_t i = tid; i < n; i += TEAM)
+                reinterpret_cast<uint4*>(dz + h)[i] = make_uint4(0, 0, 0, 0);
+            for (int64_t i = h + n * E + tid; i < p.V; i += TEAM) put(dz + i, 0.0f);
+        }
+        return;
+    }
+    const uint4* zv = reinterpret_cast<const uint4*>(z + head);
+    float lse2;   // log2 of the sum of exponentials
+    if (MODE == kBackward) {
+        lse2 = p.lse[t] * kLog2e;
+    } else {
+        Run r;
+        auto take = [&](const uint4& v) {
+            float f[E];
+            spread(v, f);
+            float top = f[0];
+#pragma unroll
+            for (int e = 1; e < E; ++e) top = fmaxf(top, f[e]);
+            const float b = r.raise(__fmul_rn(top, p.c));
+#pragma unroll
+            for (int e = 0; e < E; ++e) r.s = __fadd_rn(r.s, exp2_fast(fmaf(f[e], p.c, -b)));
+        };
+        for (int64_t i = tid; i < head; i += TEAM) r.add(__fmul_rn(to_float(z[i]), p.c));
+        int64_t i = tid;
+        for (; i + (kUnroll - 1) * TEAM < nvec; i += kUnroll * TEAM) {
+            uint4 v[kUnroll];
+#pragma unroll
+            for (int j = 0; j < kUnroll; ++j) v[j] = zv[i + j * TEAM];
+#pragma unroll
+            for (int j = 0; j < kUnroll; ++j) take(v[j]);
+        }
+        for (; i < nvec; i += TEAM) take(zv[i]);
+        for (int64_t q = tail + tid; q < p.V; q += TEAM) r.add(__fmul_rn(to_float(z[q]), p.c));
+        r = team.join(r);
+        lse2 = __fadd_rn(r.m, log2f(r.s));
+    }
+    const float inv = 1.0f / ty.s, lny = __fadd_rn(log2f(ty.s), ty.m);
+    float loss = 0.0f;
+    for (int k = tid; k < p.K; k += TEAM) {
+        const float y = pk[k];
+        const float prob = y == -INFINITY ? 0.0f : __fmul_rn(exp2_fast(__fsub_rn(y, ty.m)), inv);
+        float x = 0.0f;
+        if (id[k] >= 0) x = __fmul_rn(to_float(z[id[k]]), p.c);
+        if (prob != 0.0f)
+            loss = __fmaf_rn(prob, __fsub_rn(__fsub_rn(y, lny), __fsub_rn(x, lse2)), loss);
+        pk[k] = prob;
+        zk[k] = x;
+    }
+    if (MODE != kBackward) {
+        loss = team.sum(loss);
+        if (tid == 0) {
+            p.loss[t] = loss * kLn2 * (w * p.loss_f);
+            p.lse[t] = lse2 * kLn2;
+        }
+    }
+    if (MODE == kForward) return;
+    team.sync();   // the entries' logits are read: the gradient may take their place
+    const float f = w * p.grad_f;
+    auto grad = [&](float x) { return f * exp2_fast(fmaf(x, p.c, -lse2)); };
+    for (int64_t i = tid; i < head; i += TEAM) put(dz + i, grad(to_float(z[i])));
+    if (((reinterpret_cast<uintptr_t>(z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0) {
+        uint4* dv = reinterpret_cast<uint4*>(dz + head);
+        auto give = [&](const uint4& v) {
+            float g[E];
+            spread(v, g);
+#pragma unroll
+            for (int e = 0; e < E; ++e) g[e] = grad(g[e]);
+            return gather(g);
+        };
+        int64_t i = tid;
+        for (; i + (kUnroll - 1) * TEAM < nvec; i += kUnroll * TEAM) {
+            uint4 v[kUnroll];
+#pragma unroll
+            for (int j = 0; j < kUnroll; ++j) v[j] = zv[i + j * TEAM];
+#pragma unroll
+            for (int j = 0; j < kUnroll; ++j) dv[i + j * TEAM] = give(v[j]);
+        }
+        for (; i < nvec; i += TEAM) dv[i] = give(zv[i]);
+    } else {   // rows that start at different places within 16 bytes
+        for (int64_t i = head + tid; i < tail; i += TEAM) put(dz + i, grad(to_float(z[i])));
+    }
+    for (int64_t i = tail + tid; i < p.V; i += TEAM) put(dz + i, grad(to_float(z[i])));
+    team.sync();
+    // the entries' places, each by its first entry, with all that name it
+    for (int k = tid; k < p.K; k += TEAM) {
+        const int i = id[k];
+        if (i < 0) continue;
+        float sum = 0.0f;
+        bool first = true;
+        for (int j = 0; j < p.K; ++j) {
+            if (id[j] != i) continue;
+            if (j < k) first = false;
+            sum += pk[j];
+        }
+        if (first) put(dz + i, f * (exp2_fast(zk[k] - lse2) - sum));
+    }
+}
+
+// The sum of all tokens' losses, in a fixed order.
+__global__ void __launch_bounds__(1024) distill_total_kernel(const float* loss, int64_t T,
+                                                             float* total) {
+    __shared__ float red[32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the losses are complete
+    float s = 0.0f;
+    for (int64_t t = threadIdx.x; t < T; t += 1024) s += loss[t];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        s = red[threadIdx.x];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (threadIdx.x == 0) *total = s;
+    }
+}
+
+template <typename Z, int MODE>
+int start(const DistillParams& p, cudaStream_t st) {
+    // a warp where a row is a few vectors a lane, a block where it is long
+    const int64_t bytes = p.V * static_cast<int64_t>(sizeof(Z));
+    if (bytes <= 4096) {
+        const int64_t grid = (p.T + 7) / 8;
+        if (grid >= (1ll << 31)) return MOE_EINVAL;
+        distill_kernel<Z, 32, MODE><<<static_cast<unsigned>(grid), 256, 0, st>>>(p);
+    } else if (p.T >= (1ll << 31)) {
+        return MOE_EINVAL;
+    } else if (bytes <= 32768) {
+        distill_kernel<Z, 128, MODE><<<static_cast<unsigned>(p.T), 128, 0, st>>>(p);
+    } else {
+        distill_kernel<Z, 512, MODE><<<static_cast<unsigned>(p.T), 512, 0, st>>>(p);
+    }
+    return cudaPeekAtLastError() == cudaSuccess ? MOE_OK : MOE_ECUDA;
+}
+
+DistillParams distill_params(const moe_distill_t& c, const void* z, const int32_t* ids,
+                             const void* teacher, const float* weight) {
+    DistillParams p = {};
+    p.T = c.T;
+    p.V = c.V;
+    p.z_ld = c.z_ld;
+    p.dz_ld = c.dz_ld;
+    p.K = c.K;
+    p.teacher_f32 = c.teacher_f32;
+    p.c = static_cast<float>(1.4426950408889634074 / c.temperature);
+    p.loss_f = c.scale * c.temperature * c.temperature;
+    p.grad_f = c.scale * c.temperature;
+    p.z = z;
+    p.ids = ids;
+    p.teacher = teacher;
+    p.weight = weight;
+    return p;
+}
+
+}  // namespace
+
+int check_status_distill() { return moe_check_read_reset(); }
+
+int launch_distill(const moe_distill_t& c, const void* z, const int32_t* ids, const void* teacher,
+                   const float* weight, float* loss, float* lse, float* total, void* dz,
+                   int32_t* status, cudaStream_t st) {
+    DistillParams p = distill_params(c, z, ids, teacher, weight);
+    p.loss = loss;
+    p.lse = lse;
+    p.dz = dz;
+    p.status = status;
+    const int rc = c.z_f32 ? (dz ? start<float, kStep>(p, st) : start<float, kForward>(p, st))
+                           : (dz ? start<uint16_t, kStep>(p, st) : start<uint16_t, kForward>(p, st));
+    if (rc) return rc;
+    trace_after(st, "distill");
+    if (!total) return MOE_OK;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1, 1, 1);
+    cfg.blockDim = dim3(1024, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, distill_total_kernel, static_cast<const float*>(loss), c.T,
+                           total) != cudaSuccess)
+        return MOE_ECUDA;
+    trace_after(st, "distill_total");
+    return MOE_OK;
+}
+
+int launch_distill_backward(const moe_distill_t& c, const void* z, const int32_t* ids,
+                            const void* teacher, const float* weight, const float* lse, void* dz,
+                            int32_t* status, cudaStream_t st) {
+    DistillParams p = distill_params(c, z, ids, teacher, weight);
+    p.lse = const_cast<float*>(lse);
+    p.dz = dz;
+    p.status = status;
+    const int rc = c.z_f32 ? start<float, kBackward>(p, st) : start<uint16_t, kBackward>(p, st);
+    if (rc == MOE_OK) trace_after(st, "distill_bwd");
+    return rc;
+}
+
+}  // namespace moe

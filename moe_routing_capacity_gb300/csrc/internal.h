@@ -276,8 +276,10 @@ struct BackwardWs {
         total;
 };
 BackwardWs backward_ws_layout(const DispatchGeom& g, int d, int H, int Hs, int ns);
+// routing, logits: the router's rule and its input (nullptr: softmax over the selected logits).
 int launch_backward(const DispatchGeom& g, int d, int H, int Hs, int ns,
-                    const moe_backward_args_t& a, cudaStream_t stream);
+                    const moe_backward_args_t& a, cudaStream_t stream,
+                    const moe_routing_t* routing = nullptr, const float* logits = nullptr);
 
 // Quantile-balancing bias update: hist += counts of idx; bias from hist.
 int launch_balance_update(const int32_t* idx, int64_t n, int E, int64_t* hist, float alpha,
@@ -296,6 +298,10 @@ int check_status_rotary();
 int check_status_attention_fwd();
 int check_status_attention_bwd();
 int check_status_clip();
+int check_status_head_norm();
+int check_status_router_select();
+int check_status_embedding();
+int check_status_distill();
 
 int launch_norm_residual(const moe_norm_t& c, const uint16_t* b, const void* r,
                          const uint16_t* gate, const uint16_t* w_post, const uint16_t* w_pre,
@@ -332,5 +338,40 @@ int attn_tensor_map(CUtensorMap* m, const void* base, int D, int64_t T, int head
 int64_t grad_clip_ws(int64_t n_tensors);
 int launch_grad_clip(const moe_grad_tensor_t* tensors, int64_t n, float max_norm, float* norm,
                      void* ws, cudaStream_t stream);
+
+int64_t head_norm_backward_ws(int D);
+int launch_head_norm(const moe_head_norm_t& c, const uint16_t* q, const uint16_t* k,
+                     const uint16_t* w_q, const uint16_t* w_k, const float* table,
+                     const int32_t* pos, uint16_t* q_out, uint16_t* k_out, int32_t* status,
+                     cudaStream_t stream);
+int launch_head_norm_backward(const moe_head_norm_t& c, const uint16_t* dq, const uint16_t* dk,
+                              const uint16_t* q, const uint16_t* k, const uint16_t* w_q,
+                              const uint16_t* w_k, const float* table, const int32_t* pos,
+                              uint16_t* dq_out, uint16_t* dk_out, float* dw_q, float* dw_k,
+                              void* ws, int32_t* status, cudaStream_t stream);
+
+// MOE_OK, or what moe_router_select answers for such a rule.
+int routing_check(const moe_routing_t* c);
+// Lanes of a warp that share a group of experts.
+int router_select_lanes(int groups);
+int launch_router_select(const moe_routing_t& c, const float* logits, const float* bias,
+                         int32_t* idx, float* w, cudaStream_t stream);
+int launch_router_select_backward(const moe_routing_t& c, const float* logits, const int32_t* idx,
+                                  const float* dw, void* dlogits, cudaStream_t stream);
+
+int64_t embedding_plan_bytes(int64_t T, int64_t V, int d);
+int launch_embedding(const moe_embedding_t& c, const void* table, const int32_t* ids, void* out,
+                     int32_t* status, cudaStream_t stream);
+int launch_embedding_plan(int64_t T, int64_t V, int d, const int32_t* ids, void* plan,
+                          int32_t* status, cudaStream_t stream);
+int launch_embedding_backward(const moe_embedding_t& c, const void* plan, const void* dout,
+                              void* dtable, cudaStream_t stream);
+
+int launch_distill(const moe_distill_t& c, const void* z, const int32_t* ids, const void* teacher,
+                   const float* weight, float* loss, float* lse, float* total, void* dlogits,
+                   int32_t* status, cudaStream_t stream);
+int launch_distill_backward(const moe_distill_t& c, const void* z, const int32_t* ids,
+                            const void* teacher, const float* weight, const float* lse,
+                            void* dlogits, int32_t* status, cudaStream_t stream);
 
 }  // namespace moe

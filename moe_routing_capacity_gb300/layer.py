@@ -36,19 +36,26 @@ class PooledWaveMoE:
     rows grouped by expert (``self.bank``: [E, c_recv, L] capped, [T*k, L]
     dropless in the flat row list's order), from which the expert products
     load whole tiles (either layout, except the "waves" pipeline); False
-    gathers each expert's rows from the pool instead."""
+    gathers each expert's rows from the pool instead.  ``routing``: an
+    abi.Routing; the experts and their weights then come from abi.router_select
+    (scores, groups, the router bias in the choice alone) instead of the largest
+    logits, in forward() and backward(); ``tie`` is not written."""
 
     PIPELINES = (None, "waves", "shared")
 
     def __init__(self, cfg, weights: dict, device="cuda", balance_alpha=None,
-                 dropless=False, pipeline=None, balance_window=None, expert_bank=True):
+                 dropless=False, pipeline=None, balance_window=None, expert_bank=True,
+                 routing=None):
         self.cfg = cfg
         self.dropless = dropless
         if pipeline not in self.PIPELINES:
             raise ValueError(f"pipeline must be one of {self.PIPELINES}")
         if pipeline == "waves" and dropless:
             raise ValueError("the wave pipeline is built for the capped layout")
-        self.pipeline = pipeline
+        if routing is not None and (routing.n_experts, routing.top_k) != (cfg.n_experts,
+                                                                          cfg.top_k):
+            raise ValueError("the routing rule is of other sizes than the layer")
+        self.pipeline, self.routing = pipeline, routing
         self.plan = abi.plan_ragged(cfg) if dropless else abi.plan(cfg)
         self.device = torch.device(device)
         dev = self.device
@@ -98,8 +105,18 @@ class PooledWaveMoE:
 
     # -- the five steps -------------------------------------------------
     def route(self, x, stream=None):
+        if self.routing is not None:
+            abi.route_logits(self.cfg, x, self.w["Wr"], None, self.logits, None, self.status,
+                             stream)
+            self.select(stream)
+            return
         abi.router_topk(self.cfg, x, self.w["Wr"], self.w.get("bias"), self.logits, self.idx,
                         self.gate_w, self.tie, self.status, stream)
+
+    def select(self, stream=None):
+        """The routing rule's choice from the logits."""
+        abi.router_select(self.routing, self.logits, self.w.get("bias"), self.idx, self.gate_w,
+                          stream)
 
     def latent(self, x, stream=None):
         abi.latent_proj(x, self.w["W_ld"], self.z, self.status, stream)
@@ -132,6 +149,11 @@ class PooledWaveMoE:
 
     def route_and_latent(self, x, stream=None):
         """Router top-k and latent projection in one pass over x."""
+        if self.routing is not None:
+            abi.route_logits(self.cfg, x, self.w["Wr"], self.w["W_ld"], self.logits, self.z,
+                             self.status, stream)
+            self.select(stream)
+            return
         abi.route_project(self.cfg, x, self.w["Wr"], self.w.get("bias"), self.w["W_ld"],
                           self.logits, self.idx, self.gate_w, self.tie, self.z, self.status,
                           stream)
@@ -226,7 +248,8 @@ class PooledWaveMoE:
                        dWsd=g["Wsd"] if ns else None,
                        expert_offsets=self.expert_offsets if self.dropless else None,
                        bank=None if self.dropless else self.bank)
-        abi.layer_backward(cfg, tensors, self.bwd_ws, self.status, stream)
+        abi.layer_backward(cfg, tensors, self.bwd_ws, self.status, stream, self.routing,
+                           self.logits)
         return g
 
     def backward_intermediate(self, name):
@@ -239,6 +262,8 @@ class PooledWaveMoE:
         """The layer's weights and buffers as moe_layer_buffers_t (capped layout)."""
         if self.dropless:
             raise ValueError("moe_layer_forward runs the capped layout")
+        if self.routing is not None:
+            raise ValueError("moe_layer_forward chooses by the largest logits")
         t = {k: v for k, v in self.w.items() if v is not None and v.numel() > 0}
         t.update(logits=self.logits, idx=self.idx, w=self.gate_w, tie=self.tie, z=self.z,
                  ws_dispatch=self.ws_dispatch, pool=self.pool, slot_of=self.slot_of,
