@@ -50,268 +50,412 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // Two largest of (a1 >= a2) and (b1 >= b2).
-template <typename F>
-__device__ __forceinline__ void merge2(F& a1, F& a2, F b1, F b2) {
-    if (b1 > a1) {
-        a2 = a1 > b2 ? a1 : b2;
-        a1 = b1;
-    } else if (b1 > a2) {
-        a2 = b1;
+__device__ __forceinline__ void merge2(float& a1, float& a2, float b1, float b2) {
+    a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+    a1 = fmaxf(a1, b1);
+}
+
+// A lane's experts: entry i is expert first + of(i) of the group, those with of(i) < room
+// are there.  U neighbours at a time, so that U = 4 loads 16 bytes.
+template <int U>
+struct Entries {
+    int first, room, lanes;
+    __device__ __forceinline__ Entries(const SelectParams& p, int grp, int sub)
+        : first(grp * p.per + U * sub), room(grp < p.groups ? p.per - U * sub : 0), lanes(p.lanes) {}
+    __device__ __forceinline__ int of(int i) const { return i / U * U * lanes + i % U; }
+    __device__ __forceinline__ bool has(int i) const { return of(i / U * U) < room; }   // in whole U
+    __device__ __forceinline__ int expert(int i) const { return first + of(i); }
+};
+
+template <int U, int PER>
+__device__ __forceinline__ void load(float (&v)[PER], const float* from, const Entries<U>& at) {
+#pragma unroll
+    for (int i = 0; i < PER; i += U) {
+        if constexpr (U == 4) {
+            float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            if (at.has(i)) q = __ldg(reinterpret_cast<const float4*>(from + at.expert(i)));
+            v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+        } else {
+            v[i] = at.has(i) ? __ldg(from + at.expert(i)) : -INFINITY;
+        }
     }
 }
 
-// The choice in 64 bits; lane j < k returns the j-th expert.
-template <int PER>
+// The order of x (NaN as the smallest) as a signed key.
+__device__ __forceinline__ long long order_key64(double x) {
+    long long b = __double_as_longlong(x + 0.0);
+    if ((b & 0x7fffffffffffffffll) > 0x7ff0000000000000ll) b = 0xfff0000000000000ll;
+    return b < 0 ? b ^ 0x7fffffffffffffffll : b;
+}
+
+// The choice in 64 bits; lane j < k returns the j-th expert.  A row of one value (padding)
+// leaves the choice to the bias.
+template <int PER, int U>
 __device__ __noinline__ int choose64(const SelectParams& p, int64_t t) {
     const int lane = threadIdx.x & 31, grp = lane / p.lanes, sub = lane - grp * p.lanes;
     const float* row = p.logits + t * p.E;
-    double v[PER];
+    const Entries<U> at(p, grp, sub);
+    const float l0 = __ldg(row);
+    bool same = true;
     uint32_t open = 0;   // entries that may still be chosen
-    double m = -INFINITY;
+    float m = -INFINITY;
     for (int i = 0; i < PER; ++i) {
-        const int in = sub + p.lanes * i;
-        v[i] = -INFINITY;
-        if (grp < p.groups && in < p.per) {
-            open |= 1u << i;
-            v[i] = row[grp * p.per + in];
-            m = fmax(m, v[i]);
-        }
+        if (!at.has(i)) continue;
+        open |= 1u << i;
+        const float l = __ldg(row + at.expert(i));
+        same = same && l == l0;
+        m = fmaxf(m, l);
     }
-    double sum = 0;
-    if (p.softmax) {
-        for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(kAll, m, o));
+    same = __all_sync(kAll, same);
+    m = warp_max(m);
+    double sum = 1;
+    if (p.softmax && !same) {
+        sum = 0;
         for (int i = 0; i < PER; ++i)
-            if (open >> i & 1) sum += exp(v[i] - m);
+            if (open >> i & 1) sum += exp(static_cast<double>(__ldg(row + at.expert(i))) - m);
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
     }
+    long long key[PER], k1 = order_key64(-INFINITY), k2 = k1;
     double b1 = -INFINITY, b2 = -INFINITY;
     for (int i = 0; i < PER; ++i) {
+        key[i] = 0;
         if (!(open >> i & 1)) continue;
-        const double s = p.softmax ? exp(v[i] - m) / sum : 1 / (1 + exp(-v[i]));
-        const double x = p.bias ? s + p.bias[grp * p.per + sub + p.lanes * i] : s;
-        v[i] = x != x ? -INFINITY : x;
-        merge2(b1, b2, v[i], static_cast<double>(-INFINITY));
+        const double l = __ldg(row + at.expert(i));
+        double x = same ? 0 : p.softmax ? exp(l - m) / sum : 1 / (1 + exp(-l));
+        if (p.bias) x += __ldg(p.bias + at.expert(i));
+        key[i] = order_key64(x);
+        if (key[i] > k1) {
+            k2 = k1; b2 = b1;
+            k1 = key[i]; b1 = x;
+        } else if (key[i] > k2) {
+            k2 = key[i]; b2 = x;
+        }
+        if (!p.bias && !same) key[i] = order_key64(l);   // the scores' order, without their rounding
     }
     if (p.kept < p.groups) {
-        for (int o = 1; o < p.lanes; o <<= 1)
-            merge2(b1, b2, __shfl_xor_sync(kAll, b1, o), __shfl_xor_sync(kAll, b2, o));
-        double value = p.top2 ? b1 + b2 : b1;
-        if (value != value) value = -INFINITY;
+        for (int o = 1; o < p.lanes; o <<= 1) {
+            const double o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
+            const long long q1 = order_key64(o1), q2 = order_key64(o2);
+            if (q1 > k1) {
+                if (k1 > q2) {
+                    k2 = k1; b2 = b1;
+                } else {
+                    k2 = q2; b2 = o2;
+                }
+                k1 = q1; b1 = o1;
+            } else if (q1 > k2) {
+                k2 = q1; b2 = o1;
+            }
+        }
+        const long long value = order_key64(p.top2 ? b1 + b2 : b1);
         int rank = 0;
         for (int g = 0; g < p.groups; ++g) {
-            const double other = __shfl_sync(kAll, value, g * p.lanes);
+            const long long other = __shfl_sync(kAll, value, g * p.lanes);
             rank += other > value || (other == value && g < grp);
         }
         if (rank >= p.kept) open = 0;
     }
     int mine = 0;
     for (int j = 0; j < p.k; ++j) {
-        double best = -INFINITY;
-        int e = 0x7fffffff;
-        for (int i = 0; i < PER; ++i) {
-            const int ei = grp * p.per + sub + p.lanes * i;
-            if ((open >> i & 1) && (v[i] > best || (v[i] == best && ei < e))) {
-                best = v[i];
-                e = ei;
+        long long best = 0;
+        int e = 0x7fffffff, which = -1;
+        for (int i = 0; i < PER; ++i) {   // experts ascend with i
+            if ((open >> i & 1) && (which < 0 || key[i] > best)) {
+                best = key[i];
+                which = i;
+                e = at.expert(i);
             }
         }
         const int own = e;
         for (int o = 16; o > 0; o >>= 1) {
-            const double ov = __shfl_xor_sync(kAll, best, o);
+            const long long ob = __shfl_xor_sync(kAll, best, o);
             const int oe = __shfl_xor_sync(kAll, e, o);
-            if (ov > best || (ov == best && oe < e)) {
-                best = ov;
+            if (oe != 0x7fffffff && (e == 0x7fffffff || ob > best || (ob == best && oe < e))) {
+                best = ob;
                 e = oe;
             }
         }
         if (lane == j) mine = e;
-        if (own == e) open &= ~(1u << ((e - grp * p.per) / p.lanes));
+        if (own == e) open &= ~(1u << which);
     }
     return mine;
 }
 
-// Relative error of a fast score: 2^-20 for a sigmoid and 2^-18 for a softmax (the fast
-// exponential, the division or the sum over the row), and the rounding of the exponent's
-// argument; the sum with the bias rounds once more.  What underflows is below 1e-36.
-__device__ __forceinline__ float score_error(float s, float arg, float v, bool softmax) {
-    const float rel = (softmax ? 3.8147e-6f : 9.5368e-7f) + fabsf(arg) * 1.1921e-7f;
-    return fmaf(s, rel, fmaf(fabsf(v), 1.1921e-7f, 1e-36f));
+// The largest logit and the sum of the exponentials of a row, in 64 bits.
+template <int PER, int U>
+__device__ __noinline__ double row_sum64(const SelectParams& p, int64_t t, float* largest) {
+    const int lane = threadIdx.x & 31, grp = lane / p.lanes, sub = lane - grp * p.lanes;
+    const float* row = p.logits + t * p.E;
+    const Entries<U> at(p, grp, sub);
+    float m = -INFINITY;
+    for (int i = 0; i < PER; ++i)
+        if (at.has(i)) m = fmaxf(m, __ldg(row + at.expert(i)));
+    m = warp_max(m);
+    double sum = 0;
+#pragma unroll 4
+    for (int i = 0; i < PER; ++i)
+        if (at.has(i)) sum += exp(static_cast<double>(__ldg(row + at.expert(i))) - m);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    *largest = m;
+    return sum;
+}
+
+// What expert e goes by, in 64 bits.
+__device__ __noinline__ double value64(const SelectParams& p, int64_t t, int e, float m, double sum) {
+    const double l = __ldg(p.logits + t * p.E + e);
+    const double s = p.softmax ? exp(l - m) / sum : 1 / (1 + exp(-l));
+    return p.bias ? s + __ldg(p.bias + e) : s;
+}
+
+// The experts of the set bits, one a lane, in list (at most 32; their number).
+template <int U>
+__device__ __forceinline__ int collect(uint32_t bits, const Entries<U>& at, int* list) {
+    const int lane = threadIdx.x & 31;
+    int n = 0;
+    while (const unsigned who = __ballot_sync(kAll, bits != 0)) {
+        const int to = n + __popc(who & ((1u << lane) - 1u));
+        if (bits && to < 32) list[to] = at.expert(__ffs(bits) - 1);
+        bits &= bits - 1;
+        n += __popc(who);
+        if (n > 32) break;
+    }
+    __syncwarp();
+    return n;
+}
+
+constexpr float kStep = 5.9604645e-8f;   // 2^-24
+
+// Bound of a fast score's error.  arg is the exponential's argument: its product with
+// log2(e) is off by 1.5 steps of |arg|, the exponential by 4, the sum and the division by
+// 3, the sum of a softmax's row by fewer than 48 (rounded up for both); what underflows is
+// below 1e-36.
+__device__ __forceinline__ float score_error(float s, float arg, bool softmax) {
+    return fmaf(s, (softmax ? 64.0f : 8.0f) * kStep + 1.5f * kStep * fabsf(arg), 1e-36f);
 }
 
 __device__ __forceinline__ float fast_score(float l, float m, float inv, bool softmax) {
     return softmax ? __expf(l - m) * inv : __fdividef(1.0f, 1.0f + __expf(-l));
 }
 
-template <int PER>
-__global__ void __launch_bounds__(kThreads) router_select_kernel(const SelectParams p) {
+// Steps: values and each lane's two largest; the groups; a value that k experts reach for
+// certain, from the lanes' largest; the few experts that reach it (11 of 384 for k = 8),
+// one a lane, whose ranks the lanes count.  Where a step's bounds leave it open, the few
+// experts that it hangs on are valued in 64 bits, one a lane; choose64 where they are many.
+template <int PER, int U>
+__global__ void __launch_bounds__(kThreads) router_select_kernel(const __grid_constant__ SelectParams p) {
+    __shared__ int lists[kThreads / 32][32];      // the experts left
+    __shared__ double values[kThreads / 32][32];  // their values; two floats where fp32 does
     const int lane = threadIdx.x & 31, grp = lane / p.lanes, sub = lane - grp * p.lanes;
+    int* list = lists[threadIdx.x >> 5];
+    double* wide = values[threadIdx.x >> 5];
+    float2* few = reinterpret_cast<float2*>(wide);
     const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     if (t >= p.T) return;
     const float* row = p.logits + t * p.E;
-    const int first = grp * p.per + sub;                     // this lane's first expert
-    const int count = grp < p.groups && sub < p.per ? (p.per - sub + p.lanes - 1) / p.lanes : 0;
-    if (!moe_check(count <= PER && first + (count - 1) * p.lanes < p.E, 1611)) return;
+    const Entries<U> at(p, grp, sub);
     const bool sm = p.softmax != 0, by_groups = p.kept < p.groups;
     float v[PER];
+    load<U>(v, row, at);
+    float m = 0.0f, inv = 1.0f, top = -INFINITY;   // top: the lane's largest logit
 #pragma unroll
-    for (int i = 0; i < PER; ++i) v[i] = i < count ? __ldg(row + first + p.lanes * i) : -INFINITY;
-    // a row of one value (padding) leaves the choice to the bias, and needs no score
-    const float l0 = __shfl_sync(kAll, v[0], 0);
-    bool same = true;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) same = same && (i >= count || v[i] == l0);
-    same = __all_sync(kAll, same);
-    float m = 0.0f, inv = 1.0f;
+    for (int i = 0; i < PER; ++i) top = fmaxf(top, v[i]);
     if (sm && (p.bias || by_groups || !p.renorm)) {
-        m = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) m = fmaxf(m, v[i]);
-        m = warp_max(m);
+        m = warp_max(top);
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) sum += i < count ? __expf(v[i] - m) : 0.0f;
+        for (int i = 0; i < PER; ++i) sum += __expf(v[i] - m);   // no expert: 0
         inv = 1.0f / warp_sum(sum);
     }
     // Without a bias the logits' own order is the scores'; a group's two largest scores
     // add up all the same.
-    const bool exact = !p.bias || same;
-    bool open_question = false;
-    float b1 = -INFINITY, b2 = -INFINITY, worst = 0.0f;   // two largest; the largest error
-    if (p.bias || (by_groups && p.top2)) {
+    float b1 = -INFINITY, b2 = -INFINITY;   // the lane's two largest of what the groups go by
+    if (p.bias) {
+        float b[PER];
+        load<U>(b, p.bias, at);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            if (i >= count) continue;
-            const float l = v[i], s = same ? 0.0f : fast_score(l, m, inv, sm);
-            float x = p.bias ? s + __ldg(p.bias + first + p.lanes * i) : s;
-            x = x != x ? -INFINITY : x;
-            if (by_groups) {
-                if (!same) worst = fmaxf(worst, score_error(s, sm ? l - m : l, x, sm));
-                merge2(b1, b2, x, -INFINITY);
-            }
-            v[i] = p.bias ? x : l != l ? -INFINITY : l;
+        for (int i = 0; i < PER; ++i) {   // NaN as the smallest; -infinity where there is no expert
+            v[i] = fmaxf(fast_score(v[i], m, inv, sm) + b[i], -INFINITY);
+            merge2(b1, b2, v[i], -INFINITY);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            v[i] = v[i] != v[i] ? -INFINITY : v[i];
-            b1 = fmaxf(b1, v[i]);
+            v[i] = fmaxf(v[i], -INFINITY);
+            merge2(b1, b2, v[i], -INFINITY);
         }
     }
-    bool keep = grp < p.groups;
+    bool keep = grp < p.groups, all = false;   // all: the whole row in 64 bits
+    const float high = b1;                     // the lane's largest value
+    double sum64 = 0;
     if (by_groups) {
+        float big = top;
         for (int o = 1; o < p.lanes; o <<= 1) {
             merge2(b1, b2, __shfl_xor_sync(kAll, b1, o), __shfl_xor_sync(kAll, b2, o));
-            worst = fmaxf(worst, __shfl_xor_sync(kAll, worst, o));
+            big = fmaxf(big, __shfl_xor_sync(kAll, big, o));
         }
-        float value = p.top2 ? b1 + b2 : b1;
-        value = value != value ? -INFINITY : value;
-        // whichever experts the value comes from, no error in the group is larger
-        const float err = p.top2 ? fmaf(2.0f, worst, fabsf(value) * 1.1921e-7f) : worst;
+        const float second = b2;   // without a bias, a logit
+        if (!p.bias && p.top2) {
+            b1 = fast_score(b1, m, inv, sm);
+            b2 = fast_score(b2, m, inv, sm);
+        }
+        const float value = fmaxf(p.top2 ? b1 + b2 : b1, -INFINITY);
+        // s |arg| grows with s where |arg| > 1, so the group's largest score bounds the errors
+        // of whichever experts its value comes from
+        float err = 0.0f;
+        if (p.bias || p.top2) {
+            const float arg = sm ? big - m : big;
+            err = score_error(fast_score(big, m, inv, sm), fmaxf(1.0f, fabsf(arg)), sm);
+            err = p.top2 ? fmaf(fabsf(value) + fabsf(b1) + fabsf(b2), kStep, 2.0f * err)
+                         : fmaf(fabsf(value), kStep, err);
+        }
         int rank = 0;
-        for (int g = 0; g < p.groups; ++g) {
-            const float other = __shfl_sync(kAll, value, g * p.lanes);
-            rank += other > value || (other == value && g < grp);
+        for (int g0 = 0; g0 < p.groups; g0 += p.lanes) {   // a group's lanes share the others
+            const int g = g0 + sub;
+            const float other = __shfl_sync(kAll, value, (g * p.lanes) & 31);
+            rank += g < p.groups && (other > value || (other == value && g < grp));
         }
-        keep = keep && rank < p.kept;
-        if (__any_sync(kAll, err > 0.0f)) {
+        for (int o = 1; o < p.lanes; o <<= 1) rank += __shfl_xor_sync(kAll, rank, o);
+        bool open_question = false;
+        if (p.bias || p.top2) {
             // the lowest that a kept group may be, the highest that another may
-            const uint32_t low = __reduce_min_sync(
-                kAll, keep ? order_key(value - err) : 0xffffffffu);
-            const uint32_t high = __reduce_max_sync(
-                kAll, !keep && grp < p.groups ? order_key(value + err) : 0u);
-            open_question = low <= high;
+            const uint32_t low = __reduce_min_sync(kAll, keep && rank < p.kept ? order_key(value - err) : 0xffffffffu);
+            const uint32_t over = __reduce_max_sync(kAll, keep && rank >= p.kept ? order_key(value + err) : 0u);
+            open_question = !(low > over);
         }
-    }
-    // Rounds of selection: each lane's two first entries in routing order, the largest key
-    // over the warp, the lowest expert that holds it.
-    uint32_t hk = 0, sk = 0, used = 0;
-    int hi = -1, si = -1;
-    if (keep) {
+        if (open_question) {
+            // the experts that may be among a group's largest
+            const float from = p.bias ? (p.top2 ? b2 : b1) - 4.0f * err : second;
+            uint32_t bits = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            if (i < count) {
-                const uint32_t key = order_key(v[i]);
-                if (key > hk) {
-                    sk = hk; si = hi;
-                    hk = key; hi = i;
-                } else if (key > sk) {
-                    sk = key; si = i;
-                }
-            }
-        }
-    }
-    int mine = 0, next = -1;   // lane j holds the j-th expert; the one behind the last
-    const int there = p.kept * p.per;
-    const int rounds = p.k < there ? p.k + 1 : p.k;
-    for (int rd = 0; rd < rounds; ++rd) {
-        const uint32_t top = __reduce_max_sync(kAll, hk);
-        const int he = first + p.lanes * hi;
-        const uint32_t e = __reduce_min_sync(kAll, hi >= 0 && hk == top ? static_cast<uint32_t>(he) : 0xffffffffu);
-        if (rd == p.k) {
-            next = static_cast<int>(e);
-        } else if (lane == rd) {
-            mine = static_cast<int>(e);
-        }
-        if (hi >= 0 && static_cast<uint32_t>(he) == e) {
-            used |= 1u << hi;
-            if (si >= 0) {
-                hk = sk; hi = si;
-                sk = 0; si = -1;
-            } else {
-                hk = 0; hi = -1;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    if (i < count && !(used >> i & 1u)) {
-                        const uint32_t key = order_key(v[i]);
-                        if (key > hk) {
-                            hk = key; hi = i;
-                        }
+            for (int i = 0; i < PER; ++i) bits |= at.has(i) && !(v[i] < from) ? 1u << i : 0u;
+            const int n = collect<U>(bits, at, list);
+            all = n > 32;
+            if (!all) {
+                if (sm) sum64 = row_sum64<PER, U>(p, t, &m);
+                if (lane < n) wide[lane] = value64(p, t, list[lane], m, sum64);
+                __syncwarp();
+                double w1 = -INFINITY, w2 = -INFINITY;
+                for (int j = 0; j < n; ++j) {
+                    const double x = wide[j];
+                    if (list[j] / p.per != grp) continue;
+                    if (x > w1) {
+                        w2 = w1;
+                        w1 = x;
+                    } else if (x > w2) {
+                        w2 = x;
                     }
                 }
+                const double exact = p.top2 ? w1 + w2 : w1;
+                rank = 0;
+                for (int g = 0; g < p.groups; ++g) {
+                    const double other = __shfl_sync(kAll, exact, g * p.lanes);
+                    rank += other > exact || (!(exact > other) && g < grp);
+                }
+                __syncwarp();
+            }
+        }
+        keep = keep && rank < p.kept;
+    }
+    // A value that k experts reach: the k-th largest of the lanes' largest (equal ones go
+    // together, which only lowers it).  Of 2 k lanes and more it leaves 1.4 k experts on
+    // average; with fewer, a lane goes on to its next value.
+    uint32_t key = keep && at.room > 0 ? order_key(high) : 0u, reach = 0;
+    const bool deep = 2 * p.k > __popc(__ballot_sync(kAll, key != 0));
+    for (int j = 0; j < p.k; ++j) {
+        const uint32_t best = __reduce_max_sync(kAll, key);
+        if (best == 0) break;
+        reach = best;
+        if (key == best) {
+            key = 0;
+            if (deep) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const uint32_t k2 = at.has(i) ? order_key(v[i]) : 0u;
+                    key = k2 < best && k2 > key ? k2 : key;
+                }
             }
         }
     }
-    if (!moe_check(lane >= p.k || (mine >= 0 && mine < p.E), 1612)) mine = 0;
-    float l = lane < p.k ? __ldg(row + mine) : 0.0f;
-    if (!exact) {
-        // neighbours in the order whose bounds meet
-        auto bounds = [&](int e, float le, float& x, float& err) {
-            const float s = fast_score(le, m, inv, sm);
-            x = s + __ldg(p.bias + e);
-            err = score_error(s, sm ? le - m : le, x, sm);
-            x = x != x ? -INFINITY : x;
-        };
-        float x = 0.0f, err = 0.0f, nx = 0.0f, nerr = 0.0f;
-        if (lane < p.k) bounds(mine, l, x, err);
-        if (next >= 0) bounds(next, __ldg(row + next), nx, nerr);
-        float ox = __shfl_down_sync(kAll, x, 1), oerr = __shfl_down_sync(kAll, err, 1);
-        if (lane == p.k - 1) {
-            ox = nx;
-            oerr = nerr;
+    const float least = __uint_as_float(reach & 0x80000000u ? reach & 0x7fffffffu : ~reach);
+    float from = least;
+    if (p.bias) {   // by how much values may be off
+        const float big = warp_max(keep ? top : -INFINITY);
+        const float arg = sm ? big - m : big;
+        const float off = score_error(fast_score(big, m, inv, sm), fmaxf(1.0f, fabsf(arg)), sm);
+        from = least - 4.0f * fmaf(fabsf(least), kStep, off);
+    }
+    uint32_t bits = 0;
+    if (keep) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) bits |= at.has(i) && !(v[i] < from) ? 1u << i : 0u;
+    }
+    const int n = collect<U>(bits, at, list);
+    int e = 0, rank = 32;
+    float l = 0.0f;
+    if (n > 32 || n < p.k) {
+        all = true;
+    } else if (!all) {
+        float x = -INFINITY, err = 0.0f;
+        if (lane < n) {
+            e = list[lane];
+            if (!moe_check(e >= 0 && e < p.E, 1611)) e = 0;
+            l = __ldg(row + e);
+            x = fmaxf(l, -INFINITY);
+            if (p.bias) {
+                const float s = fast_score(l, m, inv, sm);
+                x = fmaxf(s + __ldg(p.bias + e), -INFINITY);
+                err = fmaf(fabsf(x), kStep, score_error(s, sm ? l - m : l, sm));
+            }
+            few[lane] = make_float2(x, __int_as_float(e));
         }
-        const bool pair = lane < p.k - 1 || (lane == p.k - 1 && next >= 0);
-        open_question |= __any_sync(kAll, pair && !(x - ox > err + oerr));
+        // both of two neighbours within the largest error: their order is open
+        const float apart = p.bias ? 2.0f * __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(fminf(err, 3e38f))))
+                                   : 0.0f;
+        __syncwarp();
+        rank = 0;
+        bool close = false;
+        for (int j = 0; j < n; ++j) {
+            const float2 o = few[j];
+            rank += o.x > x || (o.x == x && __float_as_int(o.y) < e);
+            close |= j != lane && !(fabsf(o.x - x) > apart);
+        }
+        if (p.bias && __any_sync(kAll, lane < n && rank < p.k && close)) {
+            if (sm && sum64 == 0) sum64 = row_sum64<PER, U>(p, t, &m);
+            double exact = -INFINITY;
+            if (lane < n) {
+                exact = value64(p, t, e, m, sum64);
+                exact = exact != exact ? -INFINITY : exact;
+                wide[lane] = exact;
+            }
+            __syncwarp();
+            rank = 0;
+            for (int j = 0; j < n; ++j) rank += wide[j] > exact || (wide[j] == exact && list[j] < e);
+        }
+        if (lane >= n) rank = 32;
     }
-    if (open_question) {
-        mine = choose64<PER>(p, t);
-        l = lane < p.k ? __ldg(row + mine) : 0.0f;
+    if (all) {
+        rank = lane < p.k ? lane : 32;
+        e = choose64<PER, U>(p, t);
+        if (!moe_check(lane >= p.k || (e >= 0 && e < p.E), 1612)) e = 0;
+        l = lane < p.k ? __ldg(row + e) : 0.0f;
     }
+    const bool chosen = rank < p.k;
     float s;
     if (sm && p.renorm) {   // the softmax of the chosen
-        const float top = warp_max(lane < p.k ? l : -INFINITY);
-        s = lane < p.k ? expf(l - top) : 0.0f;
+        const float big = warp_max(chosen ? l : -INFINITY);
+        s = expf(l - big);
     } else if (sm) {
         s = expf(l - m) * inv;
     } else {
-        s = lane < p.k ? 1.0f / (1.0f + expf(-l)) : 0.0f;
+        s = 1.0f / (1.0f + expf(-l));
     }
     if (p.renorm) {
-        const float sum = warp_sum(s);
+        const float sum = warp_sum(chosen ? s : 0.0f);
         s = sum == 0.0f ? 0.0f : s / sum;
     }
-    if (lane < p.k) {
-        p.idx[t * p.k + lane] = mine;
-        p.w[t * p.k + lane] = s * p.scale;
+    if (chosen) {
+        p.idx[t * p.k + rank] = e;
+        p.w[t * p.k + rank] = s * p.scale;
     }
 }
 
@@ -428,13 +572,19 @@ int launch_router_select(const moe_routing_t& c, const float* logits, const floa
     p.w = w;
     const int64_t grid = (c.T + kThreads / 32 - 1) / (kThreads / 32);
     if (grid >= (1ll << 31)) return MOE_EINVAL;
-    const int need = (p.per + p.lanes - 1) / p.lanes;
-    void (*kern)(SelectParams) = need <= 2    ? router_select_kernel<2>
-                                 : need <= 4  ? router_select_kernel<4>
-                                 : need <= 8  ? router_select_kernel<8>
-                                 : need <= 12 ? router_select_kernel<12>
-                                 : need <= 16 ? router_select_kernel<16>
-                                              : router_select_kernel<32>;
+    // four neighbours a lane where the groups and the rows are in whole fours
+    const bool four = p.per % 4 == 0;
+    const int unit = four ? 4 : 1, units = p.per / unit;
+    const int need = (units + p.lanes - 1) / p.lanes * unit;
+    void (*kern)(SelectParams) =
+        four ? (need <= 4    ? router_select_kernel<4, 4>
+                : need <= 8  ? router_select_kernel<8, 4>
+                : need <= 12 ? router_select_kernel<12, 4>
+                : need <= 16 ? router_select_kernel<16, 4>
+                             : router_select_kernel<32, 4>)
+             : (need <= 4    ? router_select_kernel<4, 1>
+                : need <= 16 ? router_select_kernel<16, 1>
+                             : router_select_kernel<32, 1>);
     kern<<<static_cast<unsigned>(grid), kThreads, 0, st>>>(p);
     if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
     trace_after(st, "router_select");
