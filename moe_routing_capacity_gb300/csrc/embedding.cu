@@ -2,9 +2,9 @@
 // sorted tokens.
 //
 // The gradient of a word's row is the sum of its tokens' gradients in the tokens' order, so
-// that it does not hang on the order in which anything runs.  A plan (one launch of one
-// cluster) groups the tokens by word and cuts each word's tokens into pieces of at most
-// kPiece; a warp sums a piece over 1024 channels.  Words of one piece are written at once,
+// that it does not hang on the order in which anything runs.  A plan groups the tokens by
+// word and cuts each word's tokens into pieces of at most
+// kPiece; a warp sums a piece over 512 channels.  Words of one piece are written at once,
 // the others' pieces go to scratch and are added up in their order by a second launch.
 #include "common.cuh"
 #include "internal.h"
@@ -23,27 +23,50 @@ struct LookupParams {
     void* out;
     int32_t* status;
     float scale;
+    bool wide;   // out on a 32-byte boundary
 };
 
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
-__device__ __forceinline__ void load8(const uint16_t* p, float (&f)[8]) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// 8 channels as they are stored.
+template <typename T>
+struct Chunk;
+template <>
+struct Chunk<uint16_t> {
+    uint4 v;
+    __device__ __forceinline__ void load(const uint16_t* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void spread(float (&f)[8]) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf16_lo(w[i]);
-        f[2 * i + 1] = bf16_hi(w[i]);
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = bf16_lo(w[i]);
+            f[2 * i + 1] = bf16_hi(w[i]);
+        }
     }
-}
-__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
+};
+template <>
+struct Chunk<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void spread(float (&f)[8]) const {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+};
+// fp32 as one sector where the tensor starts on such a boundary (wide): L2 sees two halves
+// of it otherwise.
+__device__ __forceinline__ void store8(float* p, const float (&f)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0]),
+                     "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+                     : "memory");
+        return;
+    }
     reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
-__device__ __forceinline__ void store8(uint16_t* p, const float (&f)[8]) {
+__device__ __forceinline__ void store8(uint16_t* p, const float (&f)[8], bool) {
     *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
                                               pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
@@ -53,18 +76,18 @@ constexpr int kLook = 4;   // chunks that a thread has under way
 template <typename Tab, typename Out>
 __global__ void __launch_bounds__(256) embedding_kernel(const LookupParams p) {
     const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 256 * kLook + threadIdx.x;
-    float f[kLook][8];
+    Chunk<Tab> c[kLook];
+    bool there[kLook];
 #pragma unroll
     for (int j = 0; j < kLook; ++j) {
         const int64_t i = i0 + j * 256;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[j][e] = 0.0f;
+        there[j] = false;
         if (i >= p.total) continue;
         const int64_t t = i / p.chunks;
-        const int c = static_cast<int>(i - t * p.chunks);
         const int id = __ldg(p.ids + t);
-        if (id >= 0 && id < p.V)
-            load8(static_cast<const Tab*>(p.table) + (static_cast<int64_t>(id) * p.chunks + c) * 8, f[j]);
+        there[j] = id >= 0 && id < p.V;
+        if (there[j])
+            c[j].load(static_cast<const Tab*>(p.table) + (id * static_cast<int64_t>(p.chunks) + (i - t * p.chunks)) * 8);
         else if (id != -1)
             report_error(p.status, MOE_EINVAL);
     }
@@ -72,31 +95,30 @@ __global__ void __launch_bounds__(256) embedding_kernel(const LookupParams p) {
     for (int j = 0; j < kLook; ++j) {
         const int64_t i = i0 + j * 256;
         if (i >= p.total) continue;
+        float f[8];
+        if (there[j]) c[j].spread(f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[j][e] *= p.scale;
-        store8(static_cast<Out*>(p.out) + i * 8, f[j]);
+        for (int e = 0; e < 8; ++e) f[e] = there[j] ? f[e] * p.scale : 0.0f;
+        store8(static_cast<Out*>(p.out) + i * 8, f, p.wide);
     }
 }
 
 // ------------------------------------------------------------------ plan
 
-constexpr int kPiece = 64;       // tokens of a piece
-constexpr int kCluster = 8;      // CTAs that group the tokens
-constexpr int kPlanThreads = 1024;
-constexpr int kShort = 128;      // words of at most so many tokens are put in order by counting
+constexpr int kPiece = 32;       // tokens of a piece: one a lane
+constexpr int kPlanThreads = 512;
 constexpr int kWindow = 1 << 18; // tokens whose bits a CTA holds at once
 
 struct PlanView {
     int32_t* head;    // [0] tokens placed, [1] pieces, [2] scratch rows, [3] words of several
-                      // pieces, [4] words past kShort
+                      // pieces
     int32_t* count;   // [V]
     int32_t* start;   // [V] where a word's tokens begin in order
     int32_t* rank;    // [T] a token's place among its word's as they came
     int32_t* mixed;   // [T] the tokens by word, as they came
-    int32_t* order;   // [T] the tokens by word, ascending
+    int32_t* order;   // [T] the tokens of words of several pieces, ascending
     int4* pieces;     // [T] {word, first place, tokens, scratch row or -1}
-    int4* joins;      // [T / kPiece] {word, first scratch row, rows, 0}
-    int32_t* longs;   // [T / kShort] words past kShort
+    int4* joins;      // [T / kPiece] {word, first scratch row, rows, first place}
     float* part;      // scratch rows [2 T / kPiece][d]
 };
 
@@ -118,124 +140,148 @@ int64_t plan_layout(int64_t T, int64_t V, int d, uint8_t* base, PlanView* v) {
     w.order = reinterpret_cast<int32_t*>(take(T * 4));
     w.pieces = reinterpret_cast<int4*>(take(T * 16));
     w.joins = reinterpret_cast<int4*>(take((T / kPiece + 1) * 16));
-    w.longs = reinterpret_cast<int32_t*>(take((T / kShort + 1) * 4));
     w.part = reinterpret_cast<float*>(take((2 * (T / kPiece) + 1) * d * 4));
     if (v) *v = w;
     return o;
 }
 
-__device__ __forceinline__ int lanemask_lt_count(unsigned m) {
-    unsigned lt;
-    asm("mov.u32 %0, %%lanemask_lt;" : "=r"(lt));
-    return __popc(m & lt);
+// Exclusive sum over the warp.
+__device__ __forceinline__ int warp_before(int v) {
+    const int lane = threadIdx.x & 31;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    return incl - v;
 }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads, 1)
-    embedding_plan_kernel(const PlanView v, const int32_t* ids, int64_t T, int64_t V,
-                          int32_t* status) {
-    extern __shared__ uint32_t bits[];
-    __shared__ int warp_sum[32];
-    const int64_t me = static_cast<int64_t>(cluster_ctarank()) * kPlanThreads + threadIdx.x;
-    const int64_t all = kCluster * kPlanThreads;
-    for (int64_t i = me; i < (V + 3) / 4; i += all)
-        reinterpret_cast<int4*>(v.count)[i] = make_int4(0, 0, 0, 0);   // the array is padded
-    if (me < 16) v.head[me] = 0;
-    __threadfence();
-    cluster_sync();
-    for (int64_t t = me; t < T; t += all) {
-        const int id = __ldg(ids + t);
-        int r = -1;
-        if (id >= 0 && id < V)
-            r = atomicAdd(v.count + id, 1);
-        else if (id != -1)
-            report_error(status, MOE_EINVAL);
-        v.rank[t] = r;
+// What an earlier launch wrote is read past L1, which a launch that waits for it may have
+// started with.
+//
+// The plan's four steps, a launch each: every one is a load or two and an atomic deep, and
+// runs over the whole machine.  (One launch of a cluster of 8 CTAs with barriers between the
+// steps took 17, 25, 73 and 390 us for 8191, 16384, 65536 and 262144 tokens.)
+
+// Count: a token's rank among its word's as they come.  A warp's tokens of one word ask
+// once for all of them (16384 tokens of one word: 36 -> EMB_ONE us).
+__global__ void __launch_bounds__(kPlanThreads) embedding_count_kernel(const PlanView v, const int32_t* ids,
+                                                                       int64_t T, int64_t V, int32_t* status) {
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x;
+    const int id = t < T ? __ldg(ids + t) : -1;
+    const bool in = id >= 0 && id < V;
+    if (!in && id != -1) report_error(status, MOE_EINVAL);
+    const int lane = threadIdx.x & 31;
+    const unsigned same = __match_any_sync(0xffffffffu, in ? id : -1);
+    const int leader = __ffs(same) - 1;
+    int r = 0;
+    if (in && lane == leader) r = atomicAdd(v.count + id, __popc(same));
+    r = __shfl_sync(0xffffffffu, r, leader) + __popc(same & ((1u << lane) - 1u));
+    if (t < T) v.rank[t] = in ? r : -1;
+}
+
+// A word's first token gives it its place and its pieces; a CTA asks for all its words.
+__global__ void __launch_bounds__(kPlanThreads) embedding_pieces_kernel(const PlanView v, const int32_t* ids,
+                                                                        int64_t T) {
+    constexpr int W = kPlanThreads / 32;
+    __shared__ int sums[3][W], first[3];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x;
+    const bool mine = t < T && __ldcg(v.rank + t) == 0;
+    const int id = mine ? __ldg(ids + t) : 0;
+    const int n = mine ? __ldcg(v.count + id) : 0, np = (n + kPiece - 1) / kPiece, rows = np > 1 ? np : 0;
+    int at = warp_before(n), pc = warp_before(np), row = warp_before(rows);
+    if (lane == 31) {
+        sums[0][wid] = at + n;
+        sums[1][wid] = pc + np;
+        sums[2][wid] = row + rows;
     }
-    __threadfence();
-    cluster_sync();
-    // a word's first token gives it its place and its pieces
-    for (int64_t t = me; t < T; t += all) {
-        if (v.rank[t] != 0) continue;
-        const int id = __ldg(ids + t);
-        const int n = __ldcg(v.count + id), np = (n + kPiece - 1) / kPiece;
-        const int at = atomicAdd(v.head, n);
-        const int pc = atomicAdd(v.head + 1, np);
-        if (!moe_check(at + n <= T && pc + np <= T, 1621)) continue;
-        v.start[id] = at;
-        int row = -1;
-        if (np > 1) {
-            row = atomicAdd(v.head + 2, np);
-            v.joins[atomicAdd(v.head + 3, 1)] = make_int4(id, row, np, 0);
+    __syncthreads();
+    if (threadIdx.x < 3) {
+        int all = 0;
+        for (int w = 0; w < W; ++w) {
+            const int s = sums[threadIdx.x][w];
+            sums[threadIdx.x][w] = all;
+            all += s;
         }
-        if (n > kShort) v.longs[atomicAdd(v.head + 4, 1)] = id;
-        for (int j = 0; j < np; ++j)
-            v.pieces[pc + j] = make_int4(id, at + j * kPiece, n - j * kPiece < kPiece ? n - j * kPiece : kPiece,
-                                         row < 0 ? -1 : row + j);
+        first[threadIdx.x] = all ? atomicAdd(v.head + threadIdx.x, all) : 0;
     }
-    __threadfence();
-    cluster_sync();
-    for (int64_t t = me; t < T; t += all) {
-        const int r = v.rank[t];
-        if (r < 0) continue;
-        const int id = __ldg(ids + t);
-        const int at = __ldcg(v.start + id) + r;
-        if (!moe_check(at < T, 1622)) continue;
-        v.mixed[at] = static_cast<int32_t>(t);
-    }
-    __threadfence();
-    cluster_sync();
-    // in order: a token of a short word counts those before it
-    for (int64_t t = me; t < T; t += all) {
-        if (v.rank[t] < 0) continue;
-        const int id = __ldg(ids + t);
-        const int n = __ldcg(v.count + id), at = __ldcg(v.start + id);
-        if (n > kShort) continue;
-        int before = 0;
-        for (int j = 0; j < n; ++j) before += __ldcg(v.mixed + at + j) < t;
-        if (!moe_check(at + before < T, 1623)) continue;
-        v.order[at + before] = static_cast<int32_t>(t);
-    }
-    // a long word's tokens are bits of a window of the batch, read out from its front
-    const int longs = __ldcg(v.head + 4), lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const int words = static_cast<int>((T < kWindow ? T : kWindow) + 31) / 32;
-    for (int l = static_cast<int>(cluster_ctarank()); l < longs; l += kCluster) {
-        const int id = __ldcg(v.longs + l), n = __ldcg(v.count + id), at = __ldcg(v.start + id);
+    __syncthreads();
+    at += sums[0][wid] + first[0];
+    pc += sums[1][wid] + first[1];
+    row += sums[2][wid] + first[2];
+    if (!mine || !moe_check(at + n <= T && pc + np <= T, 1621)) return;
+    v.start[id] = at;
+    if (np > 1) v.joins[atomicAdd(v.head + 3, 1)] = make_int4(id, row, np, at);
+    for (int j = 0; j < np; ++j)
+        v.pieces[pc + j] = make_int4(id, at + j * kPiece, n - j * kPiece < kPiece ? n - j * kPiece : kPiece,
+                                     np > 1 ? row + j : -1);
+}
+
+// The tokens to their words' places, as they came.
+__global__ void __launch_bounds__(kPlanThreads) embedding_place_kernel(const PlanView v, const int32_t* ids,
+                                                                       int64_t T) {
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x;
+    const int id = t < T ? __ldg(ids + t) : -1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int r = t < T ? __ldcg(v.rank + t) : -1;
+    if (r < 0) return;
+    const int at = __ldcg(v.start + id) + r;
+    if (moe_check(at < T, 1622)) v.mixed[at] = static_cast<int32_t>(t);
+}
+
+// Words of several pieces in order (a piece's own order is the gradient's affair where it
+// is the word's only one): a word's tokens as bits of a window of the batch, read out from
+// its front, 16 words of bits a thread.
+__global__ void __launch_bounds__(kPlanThreads) embedding_order_kernel(const PlanView v, int64_t T) {
+    extern __shared__ __align__(16) uint32_t bits[];
+    __shared__ int sums[kPlanThreads / 32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const int longs = __ldcg(v.head + 3);
+    const int64_t window = T < kWindow ? T : kWindow;
+    const int quads = static_cast<int>((window + 127) / 128);   // of words of bits
+    const int each = (quads + kPlanThreads - 1) / kPlanThreads;
+    const int q0 = static_cast<int>(threadIdx.x) * each, q1 = q0 + each < quads ? q0 + each : quads;
+    for (int l = blockIdx.x; l < longs; l += gridDim.x) {
+        const int4 q = __ldcg(v.joins + l);
+        const int n = __ldcg(v.count + q.x);
         int done = 0;
-        for (int64_t w0 = 0; w0 < T; w0 += kWindow) {
-            for (int i = threadIdx.x; i < words; i += kPlanThreads) bits[i] = 0;
+        for (int64_t w0 = 0; w0 < T; w0 += window) {
+            for (int i = threadIdx.x; i < quads; i += kPlanThreads)
+                reinterpret_cast<uint4*>(bits)[i] = make_uint4(0, 0, 0, 0);
             __syncthreads();
+#pragma unroll 8
             for (int j = threadIdx.x; j < n; j += kPlanThreads) {
-                const int64_t b = __ldcg(v.mixed + at + j) - w0;
-                if (b >= 0 && b < kWindow && moe_check(b / 32 < words, 1624))
+                const int64_t b = __ldcg(v.mixed + q.w + j) - w0;
+                if (b >= 0 && b < window && moe_check(b < 128ll * quads, 1623))
                     atomicOr(bits + b / 32, 1u << (b & 31));
             }
             __syncthreads();
-            for (int i0 = 0; i0 < words; i0 += kPlanThreads) {
-                const int i = i0 + threadIdx.x;
-                uint32_t b = i < words ? bits[i] : 0;
-                int incl = __popc(b);
-                const int own = incl;
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += y;
-                }
-                if (lane == 31) warp_sum[wid] = incl;
-                __syncthreads();
-                int base = done, total = 0;
-                for (int w = 0; w < 32; ++w) {
-                    if (w < wid) base += warp_sum[w];
-                    total += warp_sum[w];
-                }
-                int to = at + base + incl - own;
-                while (b) {
-                    if (moe_check(to < at + n, 1625))
+            int c = 0;
+            for (int i = q0; i < q1; ++i) {
+                const uint4 b = reinterpret_cast<const uint4*>(bits)[i];
+                c += __popc(b.x) + __popc(b.y) + __popc(b.z) + __popc(b.w);
+            }
+            const int before = warp_before(c);
+            if (lane == 31) sums[wid] = before + c;
+            __syncthreads();
+            int to = q.w + done + before;
+#pragma unroll
+            for (int w = 0; w < kPlanThreads / 32; ++w) {
+                if (w < wid) to += sums[w];
+                done += sums[w];
+            }
+            for (int i = 4 * q0; i < 4 * q1 && c; ++i) {
+                for (uint32_t b = bits[i]; b; b &= b - 1) {
+                    if (moe_check(to < q.w + n, 1624))
                         v.order[to] = static_cast<int32_t>(w0 + 32ll * i + __ffs(b) - 1);
                     ++to;
-                    b &= b - 1;
                 }
-                done += total;
-                __syncthreads();
             }
+            __syncthreads();
         }
     }
 }
@@ -247,74 +293,113 @@ struct GradParams {
     int64_t T, V;
     int d, chunks, spans;   // chunks of 8 channels; spans of 1024 channels a row
     int accumulate;
+    int zero_rows;           // rows that a warp looks at together for words that do not occur
+    bool wide, part_wide;   // dtable, the scratch rows on a 32-byte boundary
     float scale;
     const void* dout;
     void* dtable;
 };
 
-constexpr int kSpan = 4;    // chunks a lane of a warp's 1024 channels
+constexpr int kSpan = 2;    // chunks a lane of a warp's 512 channels
+template <typename In>
+constexpr int kRows = sizeof(In) == 2 ? 4 : 2;   // rows that a warp has under way
 
 template <typename Tab>
 __device__ __forceinline__ void finish(const GradParams& p, Tab* row, int c, float (&s)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) s[e] *= p.scale;
     if (p.accumulate) {
+        Chunk<Tab> was;
         float old[8];
-        load8(row + 8 * c, old);
+        was.load(row + 8 * c);
+        was.spread(old);
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[e] += old[e];
     }
-    store8(row + 8 * c, s);
+    store8(row + 8 * c, s, p.wide);
 }
 
-// Warps over the pieces' spans, then over the rows of words that do not occur.
+// One piece's sum over 512 channels.
 template <typename In, typename Tab>
-__global__ void __launch_bounds__(256) embedding_bwd_kernel(const GradParams p) {
+__device__ __forceinline__ void add_piece(const GradParams& p, const int4& q, int c0) {
     const int lane = threadIdx.x & 31;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
-    const int64_t me = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int64_t items = static_cast<int64_t>(p.v.head[1]) * p.spans;
-    const In* dout = static_cast<const In*>(p.dout);
-    Tab* dtable = static_cast<Tab*>(p.dtable);
-    for (int64_t it = me; it < items; it += warps) {
-        const int64_t pc = it / p.spans;
-        const int c0 = static_cast<int>(it - pc * p.spans) * 32 * kSpan + lane;
-        const int4 q = __ldg(p.v.pieces + pc);
-        if (!moe_check(q.x >= 0 && q.x < p.V && q.y + q.z <= p.T, 1626)) continue;
-        float s[kSpan][8];
+    int t = 0x7fffffff, at = lane;   // the lane's token, and its place among the piece's
+    if (lane < q.z) t = __ldg((q.w < 0 ? p.v.mixed : p.v.order) + q.y + lane);
+    if (q.w < 0 && q.z > 1) {   // as they came
+        at = 0;   // a lane without a token stands behind all: its t is the largest
+        for (int j = 0; j < q.z; ++j) {
+            const int other = __shfl_sync(0xffffffffu, t, j);
+            at += other < t ? 1 : 0;
+        }
+    }
+    float s[kSpan][8];
 #pragma unroll
-        for (int j = 0; j < kSpan; ++j)
+    for (int j = 0; j < kSpan; ++j)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[j][e] = 0.0f;
-        for (int r = 0; r < q.z; ++r) {
-            const int64_t t = __ldg(p.v.order + q.y + r);
-            const In* row = dout + t * p.d;
-            float f[kSpan][8];
+        for (int e = 0; e < 8; ++e) s[j][e] = 0.0f;
+    constexpr int R = kRows<In>;
+    for (int r0 = 0; r0 < q.z; r0 += R) {
+        Chunk<In> f[R][kSpan];
 #pragma unroll
-            for (int j = 0; j < kSpan; ++j)
-                if (c0 + 32 * j < p.chunks) load8(row + 8 * (c0 + 32 * j), f[j]);
+        for (int k = 0; k < R; ++k) {
+            const int who = __ffs(__ballot_sync(0xffffffffu, at == r0 + k)) - 1;
+            const int64_t row = __shfl_sync(0xffffffffu, t, who < 0 ? 0 : who);
+            if (r0 + k >= q.z || !moe_check(row < p.T, 1627)) continue;
 #pragma unroll
             for (int j = 0; j < kSpan; ++j)
                 if (c0 + 32 * j < p.chunks)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) s[j][e] += f[j][e];
+                    f[k][j].load(static_cast<const In*>(p.dout) + row * p.d + 8 * (c0 + 32 * j));
         }
 #pragma unroll
-        for (int j = 0; j < kSpan; ++j) {
-            const int c = c0 + 32 * j;
-            if (c >= p.chunks) continue;
-            if (q.w >= 0)
-                store8(p.v.part + static_cast<int64_t>(q.w) * p.d + 8 * c, s[j]);
-            else
-                finish(p, dtable + static_cast<int64_t>(q.x) * p.d, c, s[j]);
+        for (int k = 0; k < R; ++k) {
+            if (r0 + k >= q.z) break;
+#pragma unroll
+            for (int j = 0; j < kSpan; ++j) {
+                float g[8];
+                f[k][j].spread(g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[j][e] += g[e];
+            }
         }
     }
-    if (p.accumulate) return;
-    const float zero[8] = {};
-    for (int64_t id = me; id < p.V; id += warps) {
-        if (__ldg(p.v.count + id) != 0) continue;
-        Tab* row = dtable + id * p.d;
-        for (int c = lane; c < p.chunks; c += 32) store8(row + 8 * c, zero);
+#pragma unroll
+    for (int j = 0; j < kSpan; ++j) {
+        const int c = c0 + 32 * j;
+        if (c >= p.chunks) continue;
+        if (q.w >= 0)
+            store8(p.v.part + static_cast<int64_t>(q.w) * p.d + 8 * c, s[j], p.part_wide);
+        else
+            finish(p, static_cast<Tab*>(p.dtable) + static_cast<int64_t>(q.x) * p.d, c, s[j]);
+    }
+}
+
+// Warps over the pieces' spans, and over the rows of words that do not occur; every other
+// warp begins with those, so that reads and writes mix.
+template <typename In, typename Tab>
+__global__ void __launch_bounds__(256, 3) embedding_bwd_kernel(const GradParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
+    const int64_t me = static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+    const int64_t items = static_cast<int64_t>(p.v.head[1]) * p.spans;
+    for (int turn = 0; turn < 2; ++turn) {
+        if ((turn == 0) == ((threadIdx.x >> 5 & 1) == 0)) {
+            for (int64_t it = me; it < items; it += warps) {
+                const int64_t pc = it / p.spans;
+                const int4 q = __ldg(p.v.pieces + pc);
+                if (!moe_check(q.x >= 0 && q.x < p.V && q.y + q.z <= p.T && q.z <= kPiece, 1628)) continue;
+                add_piece<In, Tab>(p, q, static_cast<int>(it - pc * p.spans) * 32 * kSpan + lane);
+            }
+        } else if (!p.accumulate) {
+            for (int64_t id0 = me * p.zero_rows; id0 < p.V; id0 += warps * p.zero_rows) {
+                const bool absent = lane < p.zero_rows && id0 + lane < p.V && __ldg(p.v.count + id0 + lane) == 0;
+                for (unsigned rows = __ballot_sync(0xffffffffu, absent); rows; rows &= rows - 1) {
+                    uint4* row = reinterpret_cast<uint4*>(static_cast<Tab*>(p.dtable) + (id0 + __ffs(rows) - 1) * p.d);
+                    const int n = p.d * static_cast<int>(sizeof(Tab)) / 16;
+#pragma unroll 4
+                    for (int c = lane; c < n; c += 32) row[c] = make_uint4(0, 0, 0, 0);
+                }
+            }
+        }
     }
 }
 
@@ -333,9 +418,10 @@ __global__ void __launch_bounds__(256) embedding_join_kernel(const GradParams p)
         float s[8] = {};
         if (c < p.chunks)
             for (int j = run; j < q.z; j += 8) {
-                const float* r = p.v.part + static_cast<int64_t>(q.y + j) * p.d + 8 * c;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s[e] += r[e];
+                const float4* r = reinterpret_cast<const float4*>(p.v.part + static_cast<int64_t>(q.y + j) * p.d + 8 * c);
+                const float4 a = __ldcg(r), b = __ldcg(r + 1);
+                s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
+                s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
             }
 #pragma unroll
         for (int e = 0; e < 8; ++e) red[run][lane][e] = s[e];
@@ -370,6 +456,7 @@ int launch_embedding(const moe_embedding_t& c, const void* table, const int32_t*
     p.out = out;
     p.status = status;
     p.scale = c.scale;
+    p.wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
     const int64_t grid = (p.total + 256 * kLook - 1) / (256 * kLook);
     if (grid >= (1ll << 31)) return MOE_EINVAL;
     void (*kern)(LookupParams) =
@@ -385,10 +472,37 @@ int launch_embedding_plan(int64_t T, int64_t V, int d, const int32_t* ids, void*
                           int32_t* status, cudaStream_t st) {
     PlanView v;
     plan_layout(T, V, d, static_cast<uint8_t*>(plan), &v);
-    const int bytes = static_cast<int>((T < kWindow ? T : kWindow) + 31) / 32 * 4;
-    embedding_plan_kernel<<<kCluster, kPlanThreads, bytes, st>>>(v, ids, T, V, status);
+    int dev = 0, sms = 0;
+    if (const int rc = current_device(&dev, &sms)) return rc;
+    const int64_t counters = reinterpret_cast<uint8_t*>(v.count + V) - reinterpret_cast<uint8_t*>(v.head);
+    if (cudaMemsetAsync(v.head, 0, counters, st) != cudaSuccess) return MOE_ECUDA;
+    const unsigned grid = static_cast<unsigned>((T + kPlanThreads - 1) / kPlanThreads);
+    embedding_count_kernel<<<grid, kPlanThreads, 0, st>>>(v, ids, T, V, status);
     if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
-    trace_after(st, "embedding_plan");
+    trace_after(st, "embedding_count");
+    // each launched while the one before it still runs; it waits for it
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(kPlanThreads, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, embedding_pieces_kernel, static_cast<const PlanView>(v), ids, T) != cudaSuccess)
+        return MOE_ECUDA;
+    trace_after(st, "embedding_pieces");
+    if (cudaLaunchKernelEx(&cfg, embedding_place_kernel, static_cast<const PlanView>(v), ids, T) != cudaSuccess)
+        return MOE_ECUDA;
+    trace_after(st, "embedding_place");
+    if (T <= kPiece) return MOE_OK;   // no word has several pieces
+    const int64_t most = T / (kPiece + 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(most < 4 * sms ? (most ? most : 1) : 4 * sms), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(((T < kWindow ? T : kWindow) + 127) / 128 * 16);   // at most 32 KB
+    if (cudaLaunchKernelEx(&cfg, embedding_order_kernel, static_cast<const PlanView>(v), T) != cudaSuccess)
+        return MOE_ECUDA;
+    trace_after(st, "embedding_order");
     return MOE_OK;
 }
 
@@ -407,8 +521,13 @@ int launch_embedding_backward(const moe_embedding_t& c, const void* plan, const 
     p.scale = c.scale;
     p.dout = dout;
     p.dtable = dtable;
+    p.wide = (reinterpret_cast<uintptr_t>(dtable) & 31) == 0;
+    p.part_wide = (reinterpret_cast<uintptr_t>(p.v.part) & 31) == 0;
     int64_t need = c.T * p.spans;
-    if (!c.accumulate && need < c.V) need = c.V;
+    // 16 KB of the table a time, so that the warps' shares differ little
+    const int row_bytes = c.d * (c.table_f32 ? 4 : 2);
+    p.zero_rows = row_bytes >= 16384 ? 1 : row_bytes <= 512 ? 32 : 16384 / row_bytes;
+    if (!c.accumulate && need < (c.V + p.zero_rows - 1) / p.zero_rows) need = (c.V + p.zero_rows - 1) / p.zero_rows;
     need = (need + 7) / 8;
     const int64_t most = static_cast<int64_t>(sms) * 8;
     const unsigned grid = static_cast<unsigned>(need < most ? need : most);

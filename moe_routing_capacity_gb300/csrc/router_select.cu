@@ -476,8 +476,107 @@ __device__ __forceinline__ void put(uint16_t* o, float v) {
     *o = *reinterpret_cast<const uint16_t*>(&b);
 }
 
-// A warp a token: its row is put together in shared memory, and the block's rows, which
-// stand side by side in memory, are written as one run of 16-byte pieces.
+// The chosen logit's own part of the gradient, and for softmax without renormalisation
+// (dense) what the whole row is made from: dl_e = s_e (g_e - all).
+struct ChosenGrad {
+    int e;
+    float d;
+};
+__device__ __forceinline__ ChosenGrad chosen_grad(const SelectBwdParams& p, int64_t t, float m, float inv,
+                                                  float* all) {
+    const int lane = threadIdx.x & 31;
+    ChosenGrad c{-1, 0.0f};
+    float g = 0.0f, l = -INFINITY;
+    if (lane < p.k) {
+        c.e = __ldg(p.idx + t * p.k + lane);
+        if (c.e < 0 || c.e >= p.E) c.e = -1;
+        if (c.e >= 0) {
+            g = __ldg(p.dw + t * p.k + lane) * p.scale;
+            l = __ldg(p.logits + t * p.E + c.e);
+        }
+    }
+    if (p.softmax && !p.renorm) {
+        const float s = c.e >= 0 ? __expf(l - m) * inv : 0.0f;
+        *all = warp_sum(c.e >= 0 ? g * s : 0.0f);
+        c.d = s * (g - *all);
+        return c;
+    }
+    float s, gate = 1.0f;   // ds/dl = s gate
+    if (p.softmax) {
+        const float top = warp_max(l);
+        s = c.e >= 0 ? expf(l - top) : 0.0f;
+    } else {
+        const float x = expf(-l);
+        s = c.e >= 0 ? 1.0f / (1.0f + x) : 0.0f;
+        gate = x > 3e38f ? 1.0f : x / (1.0f + x);   // 1 - s, without the difference
+    }
+    if (p.renorm) {
+        const float sum = warp_sum(s);
+        const float n = sum == 0.0f ? 0.0f : s / sum;
+        c.d = n * gate * (g - warp_sum(c.e >= 0 ? g * n : 0.0f));
+    } else {
+        c.d = s * gate * g;
+    }
+    return c;
+}
+
+__device__ __forceinline__ void put4(float* o, const float (&v)[4]) {
+    *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void put4(uint16_t* o, const float (&v)[4]) {
+    *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+
+// A warp a token, four neighbouring experts a lane at a time; the chosen experts' places
+// are written again behind the row.
+template <int Q, typename Out>
+__global__ void __launch_bounds__(kThreads) router_select_bwd4_kernel(const SelectBwdParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    if (t >= p.T) return;
+    Out* to = static_cast<Out*>(p.dlogits) + t * p.E;
+    const int quads = p.E / 4;
+    float m = 0.0f, inv = 0.0f, all = 0.0f;
+    ChosenGrad c;
+    if (p.softmax && !p.renorm) {
+        float4 v[Q];
+        const float4* row = reinterpret_cast<const float4*>(p.logits + t * p.E);
+#pragma unroll
+        for (int i = 0; i < Q; ++i)
+            v[i] = lane + 32 * i < quads ? __ldg(row + lane + 32 * i)
+                                         : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) m = fmaxf(m, fmaxf(fmaxf(v[i].x, v[i].y), fmaxf(v[i].z, v[i].w)));
+        m = warp_max(m);
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            v[i] = make_float4(__expf(v[i].x - m), __expf(v[i].y - m), __expf(v[i].z - m), __expf(v[i].w - m));
+            sum += (v[i].x + v[i].y) + (v[i].z + v[i].w);
+        }
+        inv = 1.0f / warp_sum(sum);
+        c = chosen_grad(p, t, m, inv, &all);
+        const float f = -inv * all;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            const float o[4] = {v[i].x * f, v[i].y * f, v[i].z * f, v[i].w * f};
+            if (lane + 32 * i < quads) put4(to + 4 * (lane + 32 * i), o);
+        }
+    } else {
+        const float o[4] = {};
+#pragma unroll
+        for (int i = 0; i < Q; ++i)
+            if (lane + 32 * i < quads) put4(to + 4 * (lane + 32 * i), o);
+        c = chosen_grad(p, t, m, inv, &all);
+    }
+    __syncwarp();   // the row is written
+    if (c.e >= 0) put(to + c.e, c.d);
+}
+
+// The same for rows that are not in whole fours: a row is put together in shared memory,
+// and the block's rows, which stand side by side in memory, are written as one run of
+// 16-byte pieces.
 template <typename Out>
 __global__ void __launch_bounds__(kThreads) router_select_bwd_kernel(const SelectBwdParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -488,48 +587,20 @@ __global__ void __launch_bounds__(kThreads) router_select_bwd_kernel(const Selec
     if (t < p.T) {
         Out* mine = rows + static_cast<int64_t>(wid) * p.E;
         const float* row = p.logits + t * p.E;
-        int e = -1;
-        float g = 0.0f, l = -INFINITY;
-        if (lane < p.k) {
-            e = p.idx[t * p.k + lane];
-            if (e < 0 || e >= p.E) e = -1;
-            if (e >= 0) {
-                g = p.dw[t * p.k + lane] * p.scale;
-                l = __ldg(row + e);
-            }
-        }
-        float d;   // gradient of the lane's chosen logit
-        if (p.softmax && !p.renorm) {
-            float m = -INFINITY, sum = 0.0f;
+        float m = 0.0f, inv = 0.0f, all = 0.0f;
+        const bool dense = p.softmax && !p.renorm;
+        if (dense) {
+            m = -INFINITY;
             for (int i = lane; i < p.E; i += 32) m = fmaxf(m, __ldg(row + i));
             m = warp_max(m);
+            float sum = 0.0f;
             for (int i = lane; i < p.E; i += 32) sum += __expf(__ldg(row + i) - m);
-            const float inv = 1.0f / warp_sum(sum);
-            const float s = e >= 0 ? expf(l - m) * inv : 0.0f;
-            const float all = warp_sum(e >= 0 ? g * s : 0.0f);
-            for (int i = lane; i < p.E; i += 32) put(mine + i, -(expf(__ldg(row + i) - m) * inv) * all);
-            d = s * (g - all);
-        } else {
-            for (int i = lane; i < p.E; i += 32) put(mine + i, 0.0f);
-            float s, gate = 1.0f;   // ds/dl = s gate
-            if (p.softmax) {
-                const float top = warp_max(l);
-                s = e >= 0 ? expf(l - top) : 0.0f;
-            } else {
-                const float x = expf(-l);
-                s = e >= 0 ? 1.0f / (1.0f + x) : 0.0f;
-                gate = x > 3e38f ? 1.0f : x / (1.0f + x);   // 1 - s, without the difference
-            }
-            if (p.renorm) {
-                const float sum = warp_sum(s);
-                const float n = sum == 0.0f ? 0.0f : s / sum;
-                d = n * gate * (g - warp_sum(e >= 0 ? g * n : 0.0f));
-            } else {
-                d = s * gate * g;
-            }
+            inv = 1.0f / warp_sum(sum);
         }
+        const ChosenGrad c = chosen_grad(p, t, m, inv, &all);
+        for (int i = lane; i < p.E; i += 32) put(mine + i, dense ? -(__expf(__ldg(row + i) - m) * inv) * all : 0.0f);
         __syncwarp();
-        if (e >= 0) put(mine + e, d);
+        if (c.e >= 0) put(mine + c.e, c.d);
     }
     __syncthreads();
     const int64_t n = (p.T - t0 < W ? p.T - t0 : W) * p.E * static_cast<int64_t>(sizeof(Out));
@@ -540,6 +611,21 @@ __global__ void __launch_bounds__(kThreads) router_select_bwd_kernel(const Selec
     for (int i = full * 16 / static_cast<int>(sizeof(Out)) + threadIdx.x;
          i < static_cast<int>(n / static_cast<int64_t>(sizeof(Out))); i += kThreads)
         reinterpret_cast<Out*>(to)[i] = rows[i];
+}
+
+template <typename Out>
+void start_backward(const SelectBwdParams& p, unsigned grid, cudaStream_t st) {
+    const int need = (p.E / 4 + 31) / 32;
+    if (p.E % 4)
+        router_select_bwd_kernel<Out><<<grid, kThreads, kThreads / 32 * p.E * sizeof(Out), st>>>(p);   // 32 KB at most
+    else if (need <= 1)
+        router_select_bwd4_kernel<1, Out><<<grid, kThreads, 0, st>>>(p);
+    else if (need <= 2)
+        router_select_bwd4_kernel<2, Out><<<grid, kThreads, 0, st>>>(p);
+    else if (need <= 4)
+        router_select_bwd4_kernel<4, Out><<<grid, kThreads, 0, st>>>(p);
+    else
+        router_select_bwd4_kernel<8, Out><<<grid, kThreads, 0, st>>>(p);
 }
 
 }  // namespace
@@ -606,11 +692,10 @@ int launch_router_select_backward(const moe_routing_t& c, const float* logits, c
     p.dlogits = dlogits;
     const int64_t grid = (c.T + kThreads / 32 - 1) / (kThreads / 32);
     if (grid >= (1ll << 31)) return MOE_EINVAL;
-    const int bytes = kThreads / 32 * p.E * (c.grad_f32 ? 4 : 2);   // at most 32 KB
     if (c.grad_f32)
-        router_select_bwd_kernel<float><<<static_cast<unsigned>(grid), kThreads, bytes, st>>>(p);
+        start_backward<float>(p, static_cast<unsigned>(grid), st);
     else
-        router_select_bwd_kernel<uint16_t><<<static_cast<unsigned>(grid), kThreads, bytes, st>>>(p);
+        start_backward<uint16_t>(p, static_cast<unsigned>(grid), st);
     if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
     trace_after(st, "router_select_bwd");
     return MOE_OK;
