@@ -293,7 +293,6 @@ struct GradParams {
     int64_t T, V;
     int d, chunks, spans;   // chunks of 8 channels; spans of 1024 channels a row
     int accumulate;
-    int zero_rows;           // rows that a warp looks at together for words that do not occur
     bool wide, part_wide;   // dtable, the scratch rows on a 32-byte boundary
     float scale;
     const void* dout;
@@ -319,12 +318,17 @@ __device__ __forceinline__ void finish(const GradParams& p, Tab* row, int c, flo
     store8(row + 8 * c, s, p.wide);
 }
 
+// The lane's token of a piece; the largest number behind the last.
+__device__ __forceinline__ int piece_token(const GradParams& p, const int4& q) {
+    const int lane = threadIdx.x & 31;
+    return lane < q.z ? __ldg((q.w < 0 ? p.v.mixed : p.v.order) + q.y + lane) : 0x7fffffff;
+}
+
 // One piece's sum over 512 channels.
 template <typename In, typename Tab>
-__device__ __forceinline__ void add_piece(const GradParams& p, const int4& q, int c0) {
+__device__ __forceinline__ void add_piece(const GradParams& p, const int4& q, int t, int c0) {
     const int lane = threadIdx.x & 31;
-    int t = 0x7fffffff, at = lane;   // the lane's token, and its place among the piece's
-    if (lane < q.z) t = __ldg((q.w < 0 ? p.v.mixed : p.v.order) + q.y + lane);
+    int at = lane;   // the token's place among the piece's
     if (q.w < 0 && q.z > 1) {   // as they came
         at = 0;   // a lane without a token stands behind all: its t is the largest
         for (int j = 0; j < q.z; ++j) {
@@ -373,33 +377,54 @@ __device__ __forceinline__ void add_piece(const GradParams& p, const int4& q, in
     }
 }
 
-// Warps over the pieces' spans, and over the rows of words that do not occur; every other
-// warp begins with those, so that reads and writes mix.
+constexpr int kZeros = 8192;   // bytes of zeros that the rows of absent words are copied from
+
+// One warp of a CTA writes rows of words that do not occur, as bulk copies of zeros, a lane
+// a row; the others add up the pieces, a span a time, the next item's tokens already loaded.
 template <typename In, typename Tab>
 __global__ void __launch_bounds__(256, 3) embedding_bwd_kernel(const GradParams p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
-    const int64_t me = static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
-    const int64_t items = static_cast<int64_t>(p.v.head[1]) * p.spans;
-    for (int turn = 0; turn < 2; ++turn) {
-        if ((turn == 0) == ((threadIdx.x >> 5 & 1) == 0)) {
-            for (int64_t it = me; it < items; it += warps) {
-                const int64_t pc = it / p.spans;
-                const int4 q = __ldg(p.v.pieces + pc);
-                if (!moe_check(q.x >= 0 && q.x < p.V && q.y + q.z <= p.T && q.z <= kPiece, 1628)) continue;
-                add_piece<In, Tab>(p, q, static_cast<int>(it - pc * p.spans) * 32 * kSpan + lane);
+    __shared__ __align__(128) uint4 zeros[kZeros / 16];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, adders = p.accumulate ? 8 : 7;
+    if (!p.accumulate) {
+        for (int i = threadIdx.x; i < kZeros / 16; i += 256) zeros[i] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (wid == adders) {
+            const int64_t bytes = p.d * static_cast<int64_t>(sizeof(Tab));
+            for (int64_t id = blockIdx.x + static_cast<int64_t>(lane) * gridDim.x; id < p.V; id += 32ll * gridDim.x) {
+                if (__ldg(p.v.count + id) != 0) continue;
+                uint8_t* row = static_cast<uint8_t*>(p.dtable) + id * bytes;
+                for (int64_t o = 0; o < bytes; o += kZeros)
+                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(row + o),
+                                 "r"(smem_u32(zeros)),
+                                 "r"(static_cast<uint32_t>(bytes - o < kZeros ? bytes - o : kZeros))
+                                 : "memory");
             }
-        } else if (!p.accumulate) {
-            for (int64_t id0 = me * p.zero_rows; id0 < p.V; id0 += warps * p.zero_rows) {
-                const bool absent = lane < p.zero_rows && id0 + lane < p.V && __ldg(p.v.count + id0 + lane) == 0;
-                for (unsigned rows = __ballot_sync(0xffffffffu, absent); rows; rows &= rows - 1) {
-                    uint4* row = reinterpret_cast<uint4*>(static_cast<Tab*>(p.dtable) + (id0 + __ffs(rows) - 1) * p.d);
-                    const int n = p.d * static_cast<int>(sizeof(Tab)) / 16;
-#pragma unroll 4
-                    for (int c = lane; c < n; c += 32) row[c] = make_uint4(0, 0, 0, 0);
-                }
-            }
+            bulk_commit();
+            bulk_wait_all();   // the zeros are read, and the rows written
+            return;
         }
+    }
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * adders;
+    const int64_t items = static_cast<int64_t>(p.v.head[1]) * p.spans;
+    int64_t it = static_cast<int64_t>(wid) * gridDim.x + blockIdx.x;
+    if (it >= items) return;
+    int4 q = __ldg(p.v.pieces + it / p.spans);
+    int t = piece_token(p, q);
+    while (true) {
+        const int64_t then = it + warps;
+        int4 q2 = q;
+        int t2 = t;
+        if (then < items) {
+            q2 = __ldg(p.v.pieces + then / p.spans);
+            t2 = piece_token(p, q2);
+        }
+        if (moe_check(q.x >= 0 && q.x < p.V && q.y + q.z <= p.T && q.z <= kPiece, 1628))
+            add_piece<In, Tab>(p, q, t, static_cast<int>(it % p.spans) * 32 * kSpan + lane);
+        if (then >= items) return;
+        it = then;
+        q = q2;
+        t = t2;
     }
 }
 
@@ -524,11 +549,8 @@ int launch_embedding_backward(const moe_embedding_t& c, const void* plan, const 
     p.wide = (reinterpret_cast<uintptr_t>(dtable) & 31) == 0;
     p.part_wide = (reinterpret_cast<uintptr_t>(p.v.part) & 31) == 0;
     int64_t need = c.T * p.spans;
-    // 16 KB of the table a time, so that the warps' shares differ little
-    const int row_bytes = c.d * (c.table_f32 ? 4 : 2);
-    p.zero_rows = row_bytes >= 16384 ? 1 : row_bytes <= 512 ? 32 : 16384 / row_bytes;
-    if (!c.accumulate && need < (c.V + p.zero_rows - 1) / p.zero_rows) need = (c.V + p.zero_rows - 1) / p.zero_rows;
-    need = (need + 7) / 8;
+    need = (need + 6) / 7;
+    if (!c.accumulate && need < (c.V + 7) / 8) need = (c.V + 7) / 8;   // eight rows of zeros a CTA
     const int64_t most = static_cast<int64_t>(sms) * 8;
     const unsigned grid = static_cast<unsigned>(need < most ? need : most);
     void (*kern)(GradParams) =

@@ -22,7 +22,8 @@ constexpr unsigned kAll = 0xffffffffu;
 
 struct SelectParams {
     int64_t T;
-    int E, k, groups, kept, per, lanes;   // per: experts a group, lanes: of a warp a group
+    int E, k, groups, kept, per;   // per: experts a group
+    int lanes, log_lanes;          // lanes of a warp that share a group
     int softmax, top2, renorm;
     float scale;
     const float *logits, *bias;
@@ -92,7 +93,7 @@ __device__ __forceinline__ long long order_key64(double x) {
 // leaves the choice to the bias.
 template <int PER, int U>
 __device__ __noinline__ int choose64(const SelectParams& p, int64_t t) {
-    const int lane = threadIdx.x & 31, grp = lane / p.lanes, sub = lane - grp * p.lanes;
+    const int lane = threadIdx.x & 31, grp = lane >> p.log_lanes, sub = lane & (p.lanes - 1);
     const float* row = p.logits + t * p.E;
     const Entries<U> at(p, grp, sub);
     const float l0 = __ldg(row);
@@ -150,7 +151,7 @@ __device__ __noinline__ int choose64(const SelectParams& p, int64_t t) {
         const long long value = order_key64(p.top2 ? b1 + b2 : b1);
         int rank = 0;
         for (int g = 0; g < p.groups; ++g) {
-            const long long other = __shfl_sync(kAll, value, g * p.lanes);
+            const long long other = __shfl_sync(kAll, value, g << p.log_lanes);
             rank += other > value || (other == value && g < grp);
         }
         if (rank >= p.kept) open = 0;
@@ -184,7 +185,7 @@ __device__ __noinline__ int choose64(const SelectParams& p, int64_t t) {
 // The largest logit and the sum of the exponentials of a row, in 64 bits.
 template <int PER, int U>
 __device__ __noinline__ double row_sum64(const SelectParams& p, int64_t t, float* largest) {
-    const int lane = threadIdx.x & 31, grp = lane / p.lanes, sub = lane - grp * p.lanes;
+    const int lane = threadIdx.x & 31, grp = lane >> p.log_lanes, sub = lane & (p.lanes - 1);
     const float* row = p.logits + t * p.E;
     const Entries<U> at(p, grp, sub);
     float m = -INFINITY;
@@ -233,8 +234,15 @@ __device__ __forceinline__ float score_error(float s, float arg, bool softmax) {
     return fmaf(s, (softmax ? 64.0f : 8.0f) * kStep + 1.5f * kStep * fabsf(arg), 1e-36f);
 }
 
+// 1 / x for 1 <= x, infinity among them, off by a step.
+__device__ __forceinline__ float reciprocal(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ float fast_score(float l, float m, float inv, bool softmax) {
-    return softmax ? __expf(l - m) * inv : __fdividef(1.0f, 1.0f + __expf(-l));
+    return softmax ? __expf(l - m) * inv : reciprocal(1.0f + __expf(-l));
 }
 
 // Steps: values and each lane's two largest; the groups; a value that k experts reach for
@@ -244,11 +252,11 @@ __device__ __forceinline__ float fast_score(float l, float m, float inv, bool so
 template <int PER, int U>
 __global__ void __launch_bounds__(kThreads) router_select_kernel(const __grid_constant__ SelectParams p) {
     __shared__ int lists[kThreads / 32][32];      // the experts left
-    __shared__ double values[kThreads / 32][32];  // their values; two floats where fp32 does
-    const int lane = threadIdx.x & 31, grp = lane / p.lanes, sub = lane - grp * p.lanes;
+    __shared__ __align__(16) double values[kThreads / 32][32];   // their values, in fp32 where that does
+    const int lane = threadIdx.x & 31, grp = lane >> p.log_lanes, sub = lane & (p.lanes - 1);
     int* list = lists[threadIdx.x >> 5];
     double* wide = values[threadIdx.x >> 5];
-    float2* few = reinterpret_cast<float2*>(wide);
+    float* few = reinterpret_cast<float*>(wide);
     const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     if (t >= p.T) return;
     const float* row = p.logits + t * p.E;
@@ -277,12 +285,16 @@ __global__ void __launch_bounds__(kThreads) router_select_kernel(const __grid_co
             v[i] = fmaxf(fast_score(v[i], m, inv, sm) + b[i], -INFINITY);
             merge2(b1, b2, v[i], -INFINITY);
         }
-    } else {
+    } else if (by_groups && p.top2) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             v[i] = fmaxf(v[i], -INFINITY);
             merge2(b1, b2, v[i], -INFINITY);
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) v[i] = fmaxf(v[i], -INFINITY);
+        b1 = top;
     }
     bool keep = grp < p.groups, all = false;   // all: the whole row in 64 bits
     const float high = b1;                     // the lane's largest value
@@ -311,7 +323,7 @@ __global__ void __launch_bounds__(kThreads) router_select_kernel(const __grid_co
         int rank = 0;
         for (int g0 = 0; g0 < p.groups; g0 += p.lanes) {   // a group's lanes share the others
             const int g = g0 + sub;
-            const float other = __shfl_sync(kAll, value, (g * p.lanes) & 31);
+            const float other = __shfl_sync(kAll, value, (g << p.log_lanes) & 31);
             rank += g < p.groups && (other > value || (other == value && g < grp));
         }
         for (int o = 1; o < p.lanes; o <<= 1) rank += __shfl_xor_sync(kAll, rank, o);
@@ -348,7 +360,7 @@ __global__ void __launch_bounds__(kThreads) router_select_kernel(const __grid_co
                 const double exact = p.top2 ? w1 + w2 : w1;
                 rank = 0;
                 for (int g = 0; g < p.groups; ++g) {
-                    const double other = __shfl_sync(kAll, exact, g * p.lanes);
+                    const double other = __shfl_sync(kAll, exact, g << p.log_lanes);
                     rank += other > exact || (!(exact > other) && g < grp);
                 }
                 __syncwarp();
@@ -363,16 +375,14 @@ __global__ void __launch_bounds__(kThreads) router_select_kernel(const __grid_co
     const bool deep = 2 * p.k > __popc(__ballot_sync(kAll, key != 0));
     for (int j = 0; j < p.k; ++j) {
         const uint32_t best = __reduce_max_sync(kAll, key);
-        if (best == 0) break;
-        reach = best;
-        if (key == best) {
-            key = 0;
-            if (deep) {
+        reach = best ? best : reach;
+        const bool won = key == best;
+        key = won ? 0u : key;
+        if (deep && won) {
 #pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const uint32_t k2 = at.has(i) ? order_key(v[i]) : 0u;
-                    key = k2 < best && k2 > key ? k2 : key;
-                }
+            for (int i = 0; i < PER; ++i) {
+                const uint32_t k2 = at.has(i) ? order_key(v[i]) : 0u;
+                key = k2 < best && k2 > key ? k2 : key;
             }
         }
     }
@@ -406,30 +416,37 @@ __global__ void __launch_bounds__(kThreads) router_select_kernel(const __grid_co
                 x = fmaxf(s + __ldg(p.bias + e), -INFINITY);
                 err = fmaf(fabsf(x), kStep, score_error(s, sm ? l - m : l, sm));
             }
-            few[lane] = make_float2(x, __int_as_float(e));
         }
+        few[lane] = x;   // -infinity behind the last
         // both of two neighbours within the largest error: their order is open
         const float apart = p.bias ? 2.0f * __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(fminf(err, 3e38f))))
                                    : 0.0f;
         __syncwarp();
         rank = 0;
-        bool close = false;
-        for (int j = 0; j < n; ++j) {
-            const float2 o = few[j];
-            rank += o.x > x || (o.x == x && __float_as_int(o.y) < e);
-            close |= j != lane && !(fabsf(o.x - x) > apart);
+        int close = 0;   // how many are that near, itself among them
+        for (int j = 0; j < n; j += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(few + j);
+            rank += (o.x > x) + (o.y > x) + (o.z > x) + (o.w > x);
+            close += (fabsf(o.x - x) <= apart) + (fabsf(o.y - x) <= apart) + (fabsf(o.z - x) <= apart) +
+                     (fabsf(o.w - x) <= apart);
         }
-        if (p.bias && __any_sync(kAll, lane < n && rank < p.k && close)) {
-            if (sm && sum64 == 0) sum64 = row_sum64<PER, U>(p, t, &m);
-            double exact = -INFINITY;
-            if (lane < n) {
-                exact = value64(p, t, e, m, sum64);
-                exact = exact != exact ? -INFINITY : exact;
+        if (__any_sync(kAll, lane < n && rank < p.k && close != 1)) {
+            if (!p.bias) {   // equal logits, or infinite ones: the lower expert first
+                rank = 0;
+                for (int j = 0; j < n; ++j) rank += few[j] > x || (few[j] == x && list[j] < e);
+            } else {
+                if (sm && sum64 == 0) sum64 = row_sum64<PER, U>(p, t, &m);
+                double exact = -INFINITY;
+                if (lane < n) {
+                    exact = value64(p, t, e, m, sum64);
+                    exact = exact != exact ? -INFINITY : exact;
+                }
+                __syncwarp();
                 wide[lane] = exact;
+                __syncwarp();
+                rank = 0;
+                for (int j = 0; j < n; ++j) rank += wide[j] > exact || (wide[j] == exact && list[j] < e);
             }
-            __syncwarp();
-            rank = 0;
-            for (int j = 0; j < n; ++j) rank += wide[j] > exact || (wide[j] == exact && list[j] < e);
         }
         if (lane >= n) rank = 32;
     }
@@ -443,15 +460,13 @@ __global__ void __launch_bounds__(kThreads) router_select_kernel(const __grid_co
     float s;
     if (sm && p.renorm) {   // the softmax of the chosen
         const float big = warp_max(chosen ? l : -INFINITY);
-        s = expf(l - big);
-    } else if (sm) {
-        s = expf(l - m) * inv;
+        s = __expf(l - big);
     } else {
-        s = 1.0f / (1.0f + expf(-l));
+        s = fast_score(l, m, inv, sm);
     }
     if (p.renorm) {
         const float sum = warp_sum(chosen ? s : 0.0f);
-        s = sum == 0.0f ? 0.0f : s / sum;
+        s = sum == 0.0f ? 0.0f : __fdividef(s, sum);
     }
     if (chosen) {
         p.idx[t * p.k + rank] = e;
@@ -648,6 +663,8 @@ int launch_router_select(const moe_routing_t& c, const float* logits, const floa
     p.kept = c.groups_kept < c.n_groups ? c.groups_kept : 1;
     p.per = p.E / p.groups;
     p.lanes = router_select_lanes(p.groups);
+    p.log_lanes = 0;
+    while (1 << p.log_lanes < p.lanes) ++p.log_lanes;
     p.softmax = c.score == 0;
     p.top2 = c.group_top == 2;
     p.renorm = c.renorm;
