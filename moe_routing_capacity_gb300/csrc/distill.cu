@@ -114,59 +114,157 @@ struct Team {
         for (int i = 0; i < TEAM / 32; ++i) all.join(red[i], red[TEAM / 32 + i]);
         return all;
     }
-    __device__ __forceinline__ float sum(float v) const {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (TEAM == 32) return v;
-        __syncthreads();
-        if ((tid & 31) == 0) red[tid >> 5] = v;
-        __syncthreads();
-        float s = 0.0f;
-        for (int i = 0; i < TEAM / 32; ++i) s += red[i];
-        return s;
-    }
 };
 
 constexpr int kUnroll = 4;   // vectors that a thread has under way
+constexpr int kHeld = 8;     // vectors of a row that a thread keeps, where the team can keep all
 
-template <typename Z, int TEAM, int MODE>
+// A token's entries, by one warp: the teacher's distribution, and the student's exponents
+// at the entries' words.
+struct Entries {
+    int* id;        // [K] the word, -1: not there
+    float *p, *x;   // [K] probability, exponent of the logit
+    float* y;       // [K] log2 of the teacher's probability
+};
+
+// False where the row has none.
+template <typename Z>
+__device__ __forceinline__ bool load_entries(const DistillParams& p, int64_t t, const Z* z, const Entries& e) {
+    const int lane = threadIdx.x & 31;
+    Run ty;
+    for (int k = lane; k < p.K; k += 32) {
+        const int i = p.ids[t * p.K + k];
+        const bool ok = i >= 0 && i < p.V;
+        if (!ok && i != -1) report_error(p.status, MOE_EINVAL);
+        const float y = p.teacher_f32 ? static_cast<const float*>(p.teacher)[t * p.K + k]
+                                      : to_float(static_cast<const uint16_t*>(p.teacher)[t * p.K + k]);
+        e.id[k] = ok ? i : -1;
+        e.y[k] = ok ? __fmul_rn(y, p.c) : -INFINITY;
+        e.x[k] = ok ? __fmul_rn(to_float(z[i]), p.c) : 0.0f;
+        if (ok) ty.add(e.y[k]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        ty.join(__shfl_xor_sync(0xffffffffu, ty.m, o), __shfl_xor_sync(0xffffffffu, ty.s, o));
+    if (ty.m == -INFINITY && ty.s == 0.0f) return false;
+    const float inv = 1.0f / ty.s, lny = __fadd_rn(log2f(ty.s), ty.m);
+    for (int k = lane; k < p.K; k += 32) {
+        const float y = e.y[k];
+        e.p[k] = y == -INFINITY ? 0.0f : __fmul_rn(exp2_fast(__fsub_rn(y, ty.m)), inv);
+        e.y[k] = __fsub_rn(y, lny);
+    }
+    return true;
+}
+
+// sum_k p_k (log2 p_k - log2 q_k), by one warp.
+__device__ __forceinline__ float entries_loss(const DistillParams& p, const Entries& e, float lse2) {
+    float loss = 0.0f;
+    for (int k = threadIdx.x & 31; k < p.K; k += 32)
+        if (e.p[k] != 0.0f) loss = __fmaf_rn(e.p[k], __fsub_rn(e.y[k], __fsub_rn(e.x[k], lse2)), loss);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
+    return loss;
+}
+
+// The gradient at an entry's word, by its first entry, with all that name it; false for
+// entries that are not there or not the first.
+__device__ __forceinline__ bool entry_grad(const DistillParams& p, const Entries& e, int k, float f, float lse2,
+                                           float* g) {
+    const int i = e.id[k];
+    if (i < 0) return false;
+    float sum = 0.0f;
+    for (int j = 0; j < p.K; ++j) {
+        if (e.id[j] != i) continue;
+        if (j < k) return false;
+        sum += e.p[j];
+    }
+    *g = f * (exp2_fast(e.x[k] - lse2) - sum);
+    return true;
+}
+
+// The lowest value of a type, in every place of a vector: its exponentials are 0.
+template <typename Z>
+__device__ __forceinline__ uint4 nothing() {
+    const uint32_t w = sizeof(Z) == 2 ? 0xff80ff80u : 0xff800000u;
+    return make_uint4(w, w, w, w);
+}
+
+// HOLD: the team's registers keep the row between the passes.
+template <typename Z, int TEAM, int MODE, bool HOLD>
 __global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM) distill_kernel(const DistillParams p) {
     constexpr int kTeams = TEAM == 32 ? 8 : 1;
     constexpr int E = 16 / static_cast<int>(sizeof(Z));
     __shared__ int s_id[kTeams][kMaxEntries];
-    __shared__ float s_p[kTeams][kMaxEntries], s_z[kTeams][kMaxEntries];
+    __shared__ float s_p[kTeams][kMaxEntries], s_x[kTeams][kMaxEntries], s_y[kTeams][kMaxEntries];
     __shared__ float s_red[TEAM == 32 ? 1 : TEAM / 16];
+    __shared__ int s_none;
     const int which = TEAM == 32 ? static_cast<int>(threadIdx.x >> 5) : 0;
     Team<TEAM> team{static_cast<int>(TEAM == 32 ? threadIdx.x & 31 : threadIdx.x), s_red};
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + which;
     if (t >= p.T) return;
     const int tid = team.tid;
-    int* id = s_id[which];
-    float *pk = s_p[which], *zk = s_z[which];
+    const Entries en{s_id[which], s_p[which], s_x[which], s_y[which]};
     const Z* z = static_cast<const Z*>(p.z) + t * p.z_ld;
     Z* dz = static_cast<Z*>(p.dz) + t * p.dz_ld;
     // the row's run of whole vectors
     const int64_t to_vec = ((16 - (reinterpret_cast<uintptr_t>(z) & 15)) & 15) / sizeof(Z);
     const int64_t head = to_vec < p.V ? to_vec : p.V;
     const int64_t nvec = (p.V - head) / E, tail = head + nvec * E;
+    const uint4* zv = reinterpret_cast<const uint4*>(z + head);
 
     const float w = p.weight ? p.weight[t] : 1.0f;
-    // the teacher's distribution
-    Run ty;
-    if (w != 0.0f) {
-        for (int k = tid; k < p.K; k += TEAM) {
-            const int i = p.ids[t * p.K + k];
-            const bool ok = i >= 0 && i < p.V;
-            if (!ok && i != -1) report_error(p.status, MOE_EINVAL);
-            const float y = p.teacher_f32 ? static_cast<const float*>(p.teacher)[t * p.K + k]
-                                          : to_float(static_cast<const uint16_t*>(p.teacher)[t * p.K + k]);
-            id[k] = ok ? i : -1;
-            pk[k] = ok ? __fmul_rn(y, p.c) : -INFINITY;
-            if (ok) ty.add(pk[k]);
+    bool none = w == 0.0f;   // no weight, or no entry
+    uint4 held[HOLD ? kHeld : 1];
+    if (!none) {
+        if (HOLD) {
+#pragma unroll
+            for (int j = 0; j < kHeld; ++j) held[j] = tid + j * TEAM < nvec ? zv[tid + j * TEAM] : nothing<Z>();
         }
-        ty = team.join(ty);
+        if (tid < 32) {
+            none = !load_entries(p, t, z, en);
+            if (TEAM > 32 && tid == 0) s_none = none;
+        }
     }
-    if (w == 0.0f || (ty.m == -INFINITY && ty.s == 0.0f)) {   // no weight, or no entry
+    float lse2 = 0.0f;   // log2 of the sum of exponentials
+    if (w != 0.0f) {
+        if (MODE == kBackward) {
+            lse2 = p.lse[t] * kLog2e;
+            team.sync();
+        } else {
+            Run r;
+            for (int64_t i = tid; i < head; i += TEAM) r.add(__fmul_rn(to_float(z[i]), p.c));
+            for (int64_t q = tail + tid; q < p.V; q += TEAM) r.add(__fmul_rn(to_float(z[q]), p.c));
+            auto take = [&](const uint4& v) {
+                float f[E];
+                spread(v, f);
+                float top = f[0];
+#pragma unroll
+                for (int e = 1; e < E; ++e) top = fmaxf(top, f[e]);
+                const float b = r.raise(__fmul_rn(top, p.c));
+#pragma unroll
+                for (int e = 0; e < E; ++e) r.s = __fadd_rn(r.s, exp2_fast(__fmaf_rn(f[e], p.c, -b)));
+            };
+            if (HOLD) {
+#pragma unroll
+                for (int j = 0; j < kHeld; ++j)
+                    if (tid + j * TEAM < nvec) take(held[j]);
+            } else {
+                int64_t i = tid;
+                for (; i + (kUnroll - 1) * TEAM < nvec; i += kUnroll * TEAM) {
+                    uint4 v[kUnroll];
+#pragma unroll
+                    for (int j = 0; j < kUnroll; ++j) v[j] = zv[i + j * TEAM];
+#pragma unroll
+                    for (int j = 0; j < kUnroll; ++j) take(v[j]);
+                }
+                for (; i < nvec; i += TEAM) take(zv[i]);
+            }
+            r = team.join(r);
+            lse2 = __fadd_rn(r.m, log2f(r.s));
+        }
+        if (TEAM > 32) none = s_none;
+    }
+    if (none) {
         if (MODE != kBackward && tid == 0) {
             p.loss[t] = 0.0f;
             p.lse[t] = 0.0f;
@@ -176,100 +274,60 @@ __global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM) distill_kernel(const 
             const int64_t h = d_vec < p.V ? d_vec : p.V, n = (p.V - h) / E;
             for (int64_t i = tid; i < h; i += TEAM) put(dz + i, 0.0f);
             for (int64_t i = tid; i < n; i += TEAM)
-                reinterpret_cast<uint4*>(dz + h)[i] = make_uint4(0, 0, 0, 0);
+                __stcs(reinterpret_cast<uint4*>(dz + h) + i, make_uint4(0, 0, 0, 0));
             for (int64_t i = h + n * E + tid; i < p.V; i += TEAM) put(dz + i, 0.0f);
         }
         return;
     }
-    const uint4* zv = reinterpret_cast<const uint4*>(z + head);
-    float lse2;   // log2 of the sum of exponentials
-    if (MODE == kBackward) {
-        lse2 = p.lse[t] * kLog2e;
-    } else {
-        Run r;
-        auto take = [&](const uint4& v) {
-            float f[E];
-            spread(v, f);
-            float top = f[0];
-#pragma unroll
-            for (int e = 1; e < E; ++e) top = fmaxf(top, f[e]);
-            const float b = r.raise(__fmul_rn(top, p.c));
-#pragma unroll
-            for (int e = 0; e < E; ++e) r.s = __fadd_rn(r.s, exp2_fast(fmaf(f[e], p.c, -b)));
-        };
-        for (int64_t i = tid; i < head; i += TEAM) r.add(__fmul_rn(to_float(z[i]), p.c));
-        int64_t i = tid;
-        for (; i + (kUnroll - 1) * TEAM < nvec; i += kUnroll * TEAM) {
-            uint4 v[kUnroll];
-#pragma unroll
-            for (int j = 0; j < kUnroll; ++j) v[j] = zv[i + j * TEAM];
-#pragma unroll
-            for (int j = 0; j < kUnroll; ++j) take(v[j]);
-        }
-        for (; i < nvec; i += TEAM) take(zv[i]);
-        for (int64_t q = tail + tid; q < p.V; q += TEAM) r.add(__fmul_rn(to_float(z[q]), p.c));
-        r = team.join(r);
-        lse2 = __fadd_rn(r.m, log2f(r.s));
-    }
-    const float inv = 1.0f / ty.s, lny = __fadd_rn(log2f(ty.s), ty.m);
-    float loss = 0.0f;
-    for (int k = tid; k < p.K; k += TEAM) {
-        const float y = pk[k];
-        const float prob = y == -INFINITY ? 0.0f : __fmul_rn(exp2_fast(__fsub_rn(y, ty.m)), inv);
-        float x = 0.0f;
-        if (id[k] >= 0) x = __fmul_rn(to_float(z[id[k]]), p.c);
-        if (prob != 0.0f)
-            loss = __fmaf_rn(prob, __fsub_rn(__fsub_rn(y, lny), __fsub_rn(x, lse2)), loss);
-        pk[k] = prob;
-        zk[k] = x;
-    }
-    if (MODE != kBackward) {
-        loss = team.sum(loss);
+    if (MODE != kBackward && tid < 32) {
+        const float loss = entries_loss(p, en, lse2);
         if (tid == 0) {
             p.loss[t] = loss * kLn2 * (w * p.loss_f);
             p.lse[t] = lse2 * kLn2;
         }
     }
     if (MODE == kForward) return;
-    team.sync();   // the entries' logits are read: the gradient may take their place
+    // the entries' logits are read: the gradient may take their place
     const float f = w * p.grad_f;
     auto grad = [&](float x) { return f * exp2_fast(fmaf(x, p.c, -lse2)); };
     for (int64_t i = tid; i < head; i += TEAM) put(dz + i, grad(to_float(z[i])));
+    auto give = [&](const uint4& v) {
+        float g[E];
+        spread(v, g);
+#pragma unroll
+        for (int e = 0; e < E; ++e) g[e] = grad(g[e]);
+        return gather(g);
+    };
     if (((reinterpret_cast<uintptr_t>(z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0) {
         uint4* dv = reinterpret_cast<uint4*>(dz + head);
-        auto give = [&](const uint4& v) {
-            float g[E];
-            spread(v, g);
+        if (HOLD) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) g[e] = grad(g[e]);
-            return gather(g);
-        };
-        int64_t i = tid;
-        for (; i + (kUnroll - 1) * TEAM < nvec; i += kUnroll * TEAM) {
-            uint4 v[kUnroll];
+            for (int j = 0; j < kHeld; ++j)
+                if (tid + j * TEAM < nvec) __stcs(dv + tid + j * TEAM, give(held[j]));
+        } else {
+            // read for the last time, written for nobody here: what the first pass brought
+            // to L2 stays there longer
+            int64_t i = tid;
+            for (; i + (kUnroll - 1) * TEAM < nvec; i += kUnroll * TEAM) {
+                uint4 v[kUnroll];
 #pragma unroll
-            for (int j = 0; j < kUnroll; ++j) v[j] = zv[i + j * TEAM];
+                for (int j = 0; j < kUnroll; ++j) v[j] = MODE == kStep ? __ldcs(zv + i + j * TEAM) : zv[i + j * TEAM];
 #pragma unroll
-            for (int j = 0; j < kUnroll; ++j) dv[i + j * TEAM] = give(v[j]);
+                for (int j = 0; j < kUnroll; ++j) {
+                    if (MODE == kStep) __stcs(dv + i + j * TEAM, give(v[j]));
+                    else dv[i + j * TEAM] = give(v[j]);
+                }
+            }
+            for (; i < nvec; i += TEAM) dv[i] = give(zv[i]);
         }
-        for (; i < nvec; i += TEAM) dv[i] = give(zv[i]);
     } else {   // rows that start at different places within 16 bytes
         for (int64_t i = head + tid; i < tail; i += TEAM) put(dz + i, grad(to_float(z[i])));
     }
     for (int64_t i = tail + tid; i < p.V; i += TEAM) put(dz + i, grad(to_float(z[i])));
     team.sync();
-    // the entries' places, each by its first entry, with all that name it
     for (int k = tid; k < p.K; k += TEAM) {
-        const int i = id[k];
-        if (i < 0) continue;
-        float sum = 0.0f;
-        bool first = true;
-        for (int j = 0; j < p.K; ++j) {
-            if (id[j] != i) continue;
-            if (j < k) first = false;
-            sum += pk[j];
-        }
-        if (first) put(dz + i, f * (exp2_fast(zk[k] - lse2) - sum));
+        float g;
+        if (entry_grad(p, en, k, f, lse2, &g)) put(dz + en.id[k], g);
     }
 }
 
@@ -292,22 +350,23 @@ __global__ void __launch_bounds__(1024) distill_total_kernel(const float* loss, 
     }
 }
 
+template <typename Z, int TEAM, int MODE, bool HOLD>
+int start_team(const DistillParams& p, cudaStream_t st) {
+    const int64_t grid = TEAM == 32 ? (p.T + 7) / 8 : p.T;
+    if (grid >= (1ll << 31)) return MOE_EINVAL;
+    distill_kernel<Z, TEAM, MODE, HOLD><<<static_cast<unsigned>(grid), TEAM == 32 ? 256 : TEAM, 0, st>>>(p);
+    return cudaPeekAtLastError() == cudaSuccess ? MOE_OK : MOE_ECUDA;
+}
+
 template <typename Z, int MODE>
 int start(const DistillParams& p, cudaStream_t st) {
-    // a warp where a row is a few vectors a lane, a block where it is long
-    const int64_t bytes = p.V * static_cast<int64_t>(sizeof(Z));
-    if (bytes <= 4096) {
-        const int64_t grid = (p.T + 7) / 8;
-        if (grid >= (1ll << 31)) return MOE_EINVAL;
-        distill_kernel<Z, 32, MODE><<<static_cast<unsigned>(grid), 256, 0, st>>>(p);
-    } else if (p.T >= (1ll << 31)) {
-        return MOE_EINVAL;
-    } else if (bytes <= 32768) {
-        distill_kernel<Z, 128, MODE><<<static_cast<unsigned>(p.T), 128, 0, st>>>(p);
-    } else {
-        distill_kernel<Z, 512, MODE><<<static_cast<unsigned>(p.T), 512, 0, st>>>(p);
-    }
-    return cudaPeekAtLastError() == cudaSuccess ? MOE_OK : MOE_ECUDA;
+    // the smallest team whose registers hold the row, whether it reads it again or not: all
+    // of a row's loads are then under way at once
+    const int64_t vectors = p.V * static_cast<int64_t>(sizeof(Z)) / 16;
+    if (vectors <= 32 * kHeld) return start_team<Z, 32, MODE, true>(p, st);
+    if (vectors <= 128 * kHeld) return start_team<Z, 128, MODE, true>(p, st);
+    if (vectors <= 512 * kHeld) return start_team<Z, 512, MODE, true>(p, st);
+    return start_team<Z, 512, MODE, false>(p, st);
 }
 
 DistillParams distill_params(const moe_distill_t& c, const void* z, const int32_t* ids,
