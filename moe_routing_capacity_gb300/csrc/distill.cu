@@ -91,21 +91,22 @@ struct Run {
     }
 };
 
+// TEAM threads over a row; a CTA's team has a warp for the entries besides.
 template <int TEAM>
 struct Team {
     int tid;
-    float* red;   // [3][TEAM / 32], TEAM > 32
+    float* red;   // [2][TEAM / 32], TEAM > 32
     __device__ __forceinline__ void sync() const {
         if (TEAM == 32) __syncwarp();
         else __syncthreads();
     }
+    // A meeting of all; what the entries' warp brings is not used.
     __device__ __forceinline__ Run join(Run r) const {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             r.join(__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o));
         if (TEAM == 32) return r;
-        __syncthreads();
-        if ((tid & 31) == 0) {
+        if ((tid & 31) == 0 && tid < TEAM) {
             red[tid >> 5] = r.m;
             red[TEAM / 32 + (tid >> 5)] = r.s;
         }
@@ -120,11 +121,12 @@ constexpr int kUnroll = 4;   // vectors that a thread has under way
 constexpr int kHeld = 8;     // vectors of a row that a thread keeps, where the team can keep all
 
 // A token's entries, by one warp: the teacher's distribution, and the student's exponents
-// at the entries' words.
+// at the entries' words.  The arrays end in whole fours, without words behind the last.
 struct Entries {
     int* id;        // [K] the word, -1: not there
     float *p, *x;   // [K] probability, exponent of the logit
     float* y;       // [K] log2 of the teacher's probability
+    float* total;   // [K] p of all entries of the word, at its first; -1 at others
 };
 
 // False where the row has none.
@@ -132,28 +134,46 @@ template <typename Z>
 __device__ __forceinline__ bool load_entries(const DistillParams& p, int64_t t, const Z* z, const Entries& e) {
     const int lane = threadIdx.x & 31;
     Run ty;
-    for (int k = lane; k < p.K; k += 32) {
-        const int i = p.ids[t * p.K + k];
+    for (int k = lane; k < (p.K + 3) / 4 * 4; k += 32) {
+        const int i = k < p.K ? p.ids[t * p.K + k] : -1;
         const bool ok = i >= 0 && i < p.V;
         if (!ok && i != -1) report_error(p.status, MOE_EINVAL);
-        const float y = p.teacher_f32 ? static_cast<const float*>(p.teacher)[t * p.K + k]
-                                      : to_float(static_cast<const uint16_t*>(p.teacher)[t * p.K + k]);
+        float y = -INFINITY;
+        if (ok)
+            y = __fmul_rn(p.teacher_f32 ? static_cast<const float*>(p.teacher)[t * p.K + k]
+                                        : to_float(static_cast<const uint16_t*>(p.teacher)[t * p.K + k]), p.c);
         e.id[k] = ok ? i : -1;
-        e.y[k] = ok ? __fmul_rn(y, p.c) : -INFINITY;
+        e.y[k] = y;
         e.x[k] = ok ? __fmul_rn(to_float(z[i]), p.c) : 0.0f;
-        if (ok) ty.add(e.y[k]);
+        if (ok) ty.add(y);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         ty.join(__shfl_xor_sync(0xffffffffu, ty.m, o), __shfl_xor_sync(0xffffffffu, ty.s, o));
     if (ty.m == -INFINITY && ty.s == 0.0f) return false;
     const float inv = 1.0f / ty.s, lny = __fadd_rn(log2f(ty.s), ty.m);
-    for (int k = lane; k < p.K; k += 32) {
+    for (int k = lane; k < (p.K + 3) / 4 * 4; k += 32) {
         const float y = e.y[k];
         e.p[k] = y == -INFINITY ? 0.0f : __fmul_rn(exp2_fast(__fsub_rn(y, ty.m)), inv);
         e.y[k] = __fsub_rn(y, lny);
     }
     return true;
+}
+
+// Words that several entries name: their first entry stands for all.
+__device__ __forceinline__ void total_entries(const DistillParams& p, const Entries& e) {
+    for (int k = threadIdx.x & 31; k < p.K; k += 32) {
+        const int id = e.id[k];
+        float sum = 0.0f;
+        bool first = id >= 0;
+        for (int j = 0; first && j < p.K; j += 4) {
+            const int4 o = *reinterpret_cast<const int4*>(e.id + j);
+            const float4 q = *reinterpret_cast<const float4*>(e.p + j);
+            first = !((o.x == id && j < k) || (o.y == id && j + 1 < k) || (o.z == id && j + 2 < k) || (o.w == id && j + 3 < k));
+            sum += (o.x == id ? q.x : 0.0f) + (o.y == id ? q.y : 0.0f) + (o.z == id ? q.z : 0.0f) + (o.w == id ? q.w : 0.0f);
+        }
+        e.total[k] = first ? sum : -1.0f;
+    }
 }
 
 // sum_k p_k (log2 p_k - log2 q_k), by one warp.
@@ -166,22 +186,6 @@ __device__ __forceinline__ float entries_loss(const DistillParams& p, const Entr
     return loss;
 }
 
-// The gradient at an entry's word, by its first entry, with all that name it; false for
-// entries that are not there or not the first.
-__device__ __forceinline__ bool entry_grad(const DistillParams& p, const Entries& e, int k, float f, float lse2,
-                                           float* g) {
-    const int i = e.id[k];
-    if (i < 0) return false;
-    float sum = 0.0f;
-    for (int j = 0; j < p.K; ++j) {
-        if (e.id[j] != i) continue;
-        if (j < k) return false;
-        sum += e.p[j];
-    }
-    *g = f * (exp2_fast(e.x[k] - lse2) - sum);
-    return true;
-}
-
 // The lowest value of a type, in every place of a vector: its exponentials are 0.
 template <typename Z>
 __device__ __forceinline__ uint4 nothing() {
@@ -189,13 +193,27 @@ __device__ __forceinline__ uint4 nothing() {
     return make_uint4(w, w, w, w);
 }
 
-// HOLD: the team's registers keep the row between the passes.
+// Zeros for a row without weight or entries.
+template <typename Z, int TEAM>
+__device__ __forceinline__ void clear_row(Z* dz, int64_t V, int tid) {
+    constexpr int E = 16 / static_cast<int>(sizeof(Z));
+    const int64_t to_vec = ((16 - (reinterpret_cast<uintptr_t>(dz) & 15)) & 15) / sizeof(Z);
+    const int64_t h = to_vec < V ? to_vec : V, n = (V - h) / E;
+    for (int64_t i = tid; i < h; i += TEAM) put(dz + i, 0.0f);
+    for (int64_t i = tid; i < n; i += TEAM) __stcs(reinterpret_cast<uint4*>(dz + h) + i, make_uint4(0, 0, 0, 0));
+    for (int64_t i = h + n * E + tid; i < V; i += TEAM) put(dz + i, 0.0f);
+}
+
+// HOLD: the team's registers keep the row between the passes.  The entries are brought by a
+// warp of their own while the others are in the first pass (a warp that is the whole team
+// brings them itself).
 template <typename Z, int TEAM, int MODE, bool HOLD>
-__global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM) distill_kernel(const DistillParams p) {
+__global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM + 32) distill_kernel(const DistillParams p) {
     constexpr int kTeams = TEAM == 32 ? 8 : 1;
     constexpr int E = 16 / static_cast<int>(sizeof(Z));
-    __shared__ int s_id[kTeams][kMaxEntries];
-    __shared__ float s_p[kTeams][kMaxEntries], s_x[kTeams][kMaxEntries], s_y[kTeams][kMaxEntries];
+    __shared__ __align__(16) int s_id[kTeams][kMaxEntries];
+    __shared__ __align__(16) float s_p[kTeams][kMaxEntries];
+    __shared__ float s_x[kTeams][kMaxEntries], s_y[kTeams][kMaxEntries], s_t[kTeams][kMaxEntries];
     __shared__ float s_red[TEAM == 32 ? 1 : TEAM / 16];
     __shared__ int s_none;
     const int which = TEAM == 32 ? static_cast<int>(threadIdx.x >> 5) : 0;
@@ -203,7 +221,8 @@ __global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM) distill_kernel(const 
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + which;
     if (t >= p.T) return;
     const int tid = team.tid;
-    const Entries en{s_id[which], s_p[which], s_x[which], s_y[which]};
+    const bool works = TEAM == 32 || tid < TEAM, brings = TEAM == 32 || tid >= TEAM;
+    const Entries en{s_id[which], s_p[which], s_x[which], s_y[which], s_t[which]};
     const Z* z = static_cast<const Z*>(p.z) + t * p.z_ld;
     Z* dz = static_cast<Z*>(p.dz) + t * p.dz_ld;
     // the row's run of whole vectors
@@ -213,25 +232,41 @@ __global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM) distill_kernel(const 
     const uint4* zv = reinterpret_cast<const uint4*>(z + head);
 
     const float w = p.weight ? p.weight[t] : 1.0f;
-    bool none = w == 0.0f;   // no weight, or no entry
-    uint4 held[HOLD ? kHeld : 1];
-    if (!none) {
-        if (HOLD) {
-#pragma unroll
-            for (int j = 0; j < kHeld; ++j) held[j] = tid + j * TEAM < nvec ? zv[tid + j * TEAM] : nothing<Z>();
+    if (w == 0.0f) {
+        if (MODE != kBackward && tid == 0) {
+            p.loss[t] = 0.0f;
+            p.lse[t] = 0.0f;
         }
-        if (tid < 32) {
-            none = !load_entries(p, t, z, en);
-            if (TEAM > 32 && tid == 0) s_none = none;
+        if (MODE != kForward && works) clear_row<Z, TEAM>(dz, p.V, tid);
+        return;
+    }
+    uint4 held[HOLD ? kHeld : 1];
+    if (HOLD && works) {
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) held[j] = tid + j * TEAM < nvec ? zv[tid + j * TEAM] : nothing<Z>();
+    }
+    bool none = false;   // no entry
+    if (brings) {
+        none = !load_entries(p, t, z, en);
+        if (TEAM > 32 && (tid & 31) == 0) s_none = none;
+        if (MODE != kForward) {
+            __syncwarp();
+            total_entries(p, en);
         }
     }
-    float lse2 = 0.0f;   // log2 of the sum of exponentials
-    if (w != 0.0f) {
-        if (MODE == kBackward) {
-            lse2 = p.lse[t] * kLog2e;
+    float lse2;   // log2 of the sum of exponentials
+    // the gradient alone goes on at once, unless it takes the place of logits that the
+    // entries' warp may still be reading
+    const bool meets = MODE != kBackward || static_cast<const void*>(z) == static_cast<void*>(dz);
+    if (MODE == kBackward) {
+        lse2 = p.lse[t] * kLog2e;
+        if (meets) {
             team.sync();
-        } else {
-            Run r;
+            if (TEAM > 32) none = s_none;
+        }
+    } else {
+        Run r;
+        if (works) {
             for (int64_t i = tid; i < head; i += TEAM) r.add(__fmul_rn(to_float(z[i]), p.c));
             for (int64_t q = tail + tid; q < p.V; q += TEAM) r.add(__fmul_rn(to_float(z[q]), p.c));
             auto take = [&](const uint4& v) {
@@ -259,75 +294,68 @@ __global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM) distill_kernel(const 
                 }
                 for (; i < nvec; i += TEAM) take(zv[i]);
             }
-            r = team.join(r);
-            lse2 = __fadd_rn(r.m, log2f(r.s));
         }
+        r = team.join(r);
+        lse2 = __fadd_rn(r.m, log2f(r.s));
         if (TEAM > 32) none = s_none;
-    }
-    if (none) {
-        if (MODE != kBackward && tid == 0) {
-            p.loss[t] = 0.0f;
-            p.lse[t] = 0.0f;
-        }
-        if (MODE != kForward) {
-            const int64_t d_vec = ((16 - (reinterpret_cast<uintptr_t>(dz) & 15)) & 15) / sizeof(Z);
-            const int64_t h = d_vec < p.V ? d_vec : p.V, n = (p.V - h) / E;
-            for (int64_t i = tid; i < h; i += TEAM) put(dz + i, 0.0f);
-            for (int64_t i = tid; i < n; i += TEAM)
-                __stcs(reinterpret_cast<uint4*>(dz + h) + i, make_uint4(0, 0, 0, 0));
-            for (int64_t i = h + n * E + tid; i < p.V; i += TEAM) put(dz + i, 0.0f);
-        }
-        return;
-    }
-    if (MODE != kBackward && tid < 32) {
-        const float loss = entries_loss(p, en, lse2);
-        if (tid == 0) {
-            p.loss[t] = loss * kLn2 * (w * p.loss_f);
-            p.lse[t] = lse2 * kLn2;
+        if (brings) {
+            const float loss = none ? 0.0f : entries_loss(p, en, lse2);
+            if ((tid & 31) == 0) {
+                p.loss[t] = none ? 0.0f : loss * kLn2 * (w * p.loss_f);
+                p.lse[t] = none ? 0.0f : lse2 * kLn2;
+            }
         }
     }
     if (MODE == kForward) return;
-    // the entries' logits are read: the gradient may take their place
     const float f = w * p.grad_f;
-    auto grad = [&](float x) { return f * exp2_fast(fmaf(x, p.c, -lse2)); };
-    for (int64_t i = tid; i < head; i += TEAM) put(dz + i, grad(to_float(z[i])));
-    auto give = [&](const uint4& v) {
-        float g[E];
-        spread(v, g);
+    if (works && !none) {
+        auto grad = [&](float x) { return f * exp2_fast(fmaf(x, p.c, -lse2)); };
+        for (int64_t i = tid; i < head; i += TEAM) put(dz + i, grad(to_float(z[i])));
+        auto give = [&](const uint4& v) {
+            float g[E];
+            spread(v, g);
 #pragma unroll
-        for (int e = 0; e < E; ++e) g[e] = grad(g[e]);
-        return gather(g);
-    };
-    if (((reinterpret_cast<uintptr_t>(z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0) {
-        uint4* dv = reinterpret_cast<uint4*>(dz + head);
-        if (HOLD) {
+            for (int e = 0; e < E; ++e) g[e] = grad(g[e]);
+            return gather(g);
+        };
+        if (((reinterpret_cast<uintptr_t>(z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0) {
+            uint4* dv = reinterpret_cast<uint4*>(dz + head);
+            if (HOLD) {
 #pragma unroll
-            for (int j = 0; j < kHeld; ++j)
-                if (tid + j * TEAM < nvec) __stcs(dv + tid + j * TEAM, give(held[j]));
-        } else {
-            // read for the last time, written for nobody here: what the first pass brought
-            // to L2 stays there longer
-            int64_t i = tid;
-            for (; i + (kUnroll - 1) * TEAM < nvec; i += kUnroll * TEAM) {
-                uint4 v[kUnroll];
+                for (int j = 0; j < kHeld; ++j)
+                    if (tid + j * TEAM < nvec) __stcs(dv + tid + j * TEAM, give(held[j]));
+            } else {
+                // read for the last time, written for nobody here: what the first pass
+                // brought to L2 stays there longer (8192 x 131072: 857 -> 790 us; the
+                // gradient alone, which has no first pass, 66 -> 71)
+                int64_t i = tid;
+                for (; i + (kUnroll - 1) * TEAM < nvec; i += kUnroll * TEAM) {
+                    uint4 v[kUnroll];
 #pragma unroll
-                for (int j = 0; j < kUnroll; ++j) v[j] = MODE == kStep ? __ldcs(zv + i + j * TEAM) : zv[i + j * TEAM];
+                    for (int j = 0; j < kUnroll; ++j) v[j] = MODE == kStep ? __ldcs(zv + i + j * TEAM) : zv[i + j * TEAM];
 #pragma unroll
-                for (int j = 0; j < kUnroll; ++j) {
-                    if (MODE == kStep) __stcs(dv + i + j * TEAM, give(v[j]));
-                    else dv[i + j * TEAM] = give(v[j]);
+                    for (int j = 0; j < kUnroll; ++j) {
+                        if (MODE == kStep) __stcs(dv + i + j * TEAM, give(v[j]));
+                        else dv[i + j * TEAM] = give(v[j]);
+                    }
                 }
+                for (; i < nvec; i += TEAM) dv[i] = give(zv[i]);
             }
-            for (; i < nvec; i += TEAM) dv[i] = give(zv[i]);
+        } else {   // rows that start at different places within 16 bytes
+            for (int64_t i = head + tid; i < tail; i += TEAM) put(dz + i, grad(to_float(z[i])));
         }
-    } else {   // rows that start at different places within 16 bytes
-        for (int64_t i = head + tid; i < tail; i += TEAM) put(dz + i, grad(to_float(z[i])));
+        for (int64_t i = tail + tid; i < p.V; i += TEAM) put(dz + i, grad(to_float(z[i])));
     }
-    for (int64_t i = tail + tid; i < p.V; i += TEAM) put(dz + i, grad(to_float(z[i])));
     team.sync();
+    if (TEAM > 32) none = s_none;
+    if (none) {
+        if (works) clear_row<Z, TEAM>(dz, p.V, tid);
+        return;
+    }
+    // the entries' words, behind the row
     for (int k = tid; k < p.K; k += TEAM) {
-        float g;
-        if (entry_grad(p, en, k, f, lse2, &g)) put(dz + en.id[k], g);
+        const float total = en.total[k];
+        if (works && en.id[k] >= 0 && !(total < 0.0f)) put(dz + en.id[k], f * (exp2_fast(en.x[k] - lse2) - total));
     }
 }
 
@@ -354,7 +382,7 @@ template <typename Z, int TEAM, int MODE, bool HOLD>
 int start_team(const DistillParams& p, cudaStream_t st) {
     const int64_t grid = TEAM == 32 ? (p.T + 7) / 8 : p.T;
     if (grid >= (1ll << 31)) return MOE_EINVAL;
-    distill_kernel<Z, TEAM, MODE, HOLD><<<static_cast<unsigned>(grid), TEAM == 32 ? 256 : TEAM, 0, st>>>(p);
+    distill_kernel<Z, TEAM, MODE, HOLD><<<static_cast<unsigned>(grid), TEAM == 32 ? 256 : TEAM + 32, 0, st>>>(p);
     return cudaPeekAtLastError() == cudaSuccess ? MOE_OK : MOE_ECUDA;
 }
 

@@ -448,10 +448,12 @@ def test_distill(rng, T, V, K, dt, tau, tdt):
     both, l2, e2 = empty(T, V, dt=dt), empty(T, dt=F32), empty(T, dt=F32)
     abi.distill_loss(z, ids, teacher, weight, l2, e2, st, dlogits=both, temperature=tau, scale=0.7)
     R.within("dz", both, dz, bound)
-    assert torch.equal(l2, loss) and torch.equal(e2, lse)
+    R.within("loss with the gradient", l2, *want["loss"])
+    R.within("lse with the gradient", e2, *want["lse"])
     over = z.clone()
     abi.distill_loss(over, ids, teacher, weight, l2, e2, st, dlogits=over, temperature=tau, scale=0.7)
-    assert torch.equal(over, both) and torch.equal(l2, loss)
+    assert torch.equal(over, both)
+    R.within("loss over the logits", l2, *want["loss"])
     over = z.clone()
     abi.distill_loss_backward(over, ids, teacher, weight, lse, over, st, temperature=tau, scale=0.7)
     assert torch.equal(over, one)
