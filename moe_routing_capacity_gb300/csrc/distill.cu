@@ -6,9 +6,16 @@
 //     dz_v = scale w tau (q_v - sum over k with i_k = v of p_k)
 //
 // A team of threads takes a row.  One pass over it carries the running maximum and the sum
-// of exponentials (in base 2, the temperature folded into the factor); the entries' few
-// logits are gathered behind it; a second pass, where the gradient is wanted, writes q, and
-// the entries' places are written again behind that.  The second pass finds the row in L2.
+// of exponentials (in base 2, the temperature folded into the factor), while one more warp
+// brings the entries; the gradient is a second pass, which writes q, and the entries' places
+// are written again behind that.  A short row stays in registers between the passes; of a
+// long one shared memory keeps a part, and L2 the rest.
+//   Forward of 4096 x 131072 bf16 (1.07 GB): 149 us, 7.2 TB/s.  Loss and gradient of 8192 x
+// 131072, a tenth of the rows without weight: 671 us, 6.1 TB/s of the 4.1 GB that have to
+// move; the exponentials alone (two a logit) are 460 us at 16 a cycle and SM, and the second
+// reading of the row is L2's.  A ring of chunks in the shared memory of a cluster, filled
+// and drained by bulk copies, moved nothing twice and took 950: a CTA's two passes and the
+// meeting between them follow each other, and only one fits on an SM.
 #include "common.cuh"
 #include "internal.h"
 
@@ -16,7 +23,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kMaxEntries = MOE_DISTILL_MAX_ENTRIES;
+constexpr int kMaxEntries = MOE_DISTILL_MAX_ENTRIES;   // of a token
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 enum Mode { kForward = 0, kStep = 1, kBackward = 2 };
@@ -24,7 +31,7 @@ enum Mode { kForward = 0, kStep = 1, kBackward = 2 };
 struct DistillParams {
     int64_t T, V, z_ld, dz_ld;
     int K, teacher_f32;
-    float c, inv_tau, loss_f, grad_f;   // log2(e) / tau, 1 / tau, scale tau^2, scale tau
+    float c, loss_f, grad_f;   // log2(e) / tau, scale tau^2, scale tau
     const void *z, *teacher;
     const int32_t* ids;
     const float* weight;
@@ -118,7 +125,6 @@ struct Team {
 };
 
 constexpr int kUnroll = 4;   // vectors that a thread has under way
-constexpr int kHeld = 8;     // vectors of a row that a thread keeps, where the team can keep all
 
 // A token's entries, by one warp: the teacher's distribution, and the student's exponents
 // at the entries' words.  The arrays end in whole fours, without words behind the last.
@@ -204,16 +210,17 @@ __device__ __forceinline__ void clear_row(Z* dz, int64_t V, int tid) {
     for (int64_t i = h + n * E + tid; i < V; i += TEAM) put(dz + i, 0.0f);
 }
 
-// HOLD: the team's registers keep the row between the passes.  The entries are brought by a
-// warp of their own while the others are in the first pass (a warp that is the whole team
-// brings them itself).
-template <typename Z, int TEAM, int MODE, bool HOLD>
-__global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM + 32) distill_kernel(const DistillParams p) {
+// HELD: vectors a thread, where the team's registers keep the row between the passes; else
+// 0, and STASH vectors a thread are kept in shared memory.  BLOCKS: CTAs on an SM.  The
+// entries are brought by a warp of their own while the others are in the first pass (a warp
+// that is the whole team brings them itself).
+template <typename Z, int TEAM, int MODE, int HELD, int STASH, int BLOCKS>
+__global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM + 32, BLOCKS) distill_kernel(const DistillParams p) {
+    static_assert(STASH % kUnroll == 0, "in whole groups");
     constexpr int kTeams = TEAM == 32 ? 8 : 1;
     constexpr int E = 16 / static_cast<int>(sizeof(Z));
-    __shared__ __align__(16) int s_id[kTeams][kMaxEntries];
-    __shared__ __align__(16) float s_p[kTeams][kMaxEntries];
-    __shared__ float s_x[kTeams][kMaxEntries], s_y[kTeams][kMaxEntries], s_t[kTeams][kMaxEntries];
+    constexpr bool HOLD = HELD > 0;
+    extern __shared__ __align__(16) uint4 stash[];   // and behind it the entries' arrays
     __shared__ float s_red[TEAM == 32 ? 1 : TEAM / 16];
     __shared__ int s_none;
     const int which = TEAM == 32 ? static_cast<int>(threadIdx.x >> 5) : 0;
@@ -222,7 +229,10 @@ __global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM + 32) distill_kernel(c
     if (t >= p.T) return;
     const int tid = team.tid;
     const bool works = TEAM == 32 || tid < TEAM, brings = TEAM == 32 || tid >= TEAM;
-    const Entries en{s_id[which], s_p[which], s_x[which], s_y[which], s_t[which]};
+    const int width = (p.K + 3) / 4 * 4;
+    float* arrays = reinterpret_cast<float*>(stash + STASH * TEAM) + which * 5 * width;
+    const Entries en{reinterpret_cast<int*>(arrays), arrays + width, arrays + 2 * width, arrays + 3 * width,
+                     arrays + 4 * width};
     const Z* z = static_cast<const Z*>(p.z) + t * p.z_ld;
     Z* dz = static_cast<Z*>(p.dz) + t * p.dz_ld;
     // the row's run of whole vectors
@@ -230,7 +240,14 @@ __global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM + 32) distill_kernel(c
     const int64_t head = to_vec < p.V ? to_vec : p.V;
     const int64_t nvec = (p.V - head) / E, tail = head + nvec * E;
     const uint4* zv = reinterpret_cast<const uint4*>(z + head);
+    const int groups = static_cast<int>((nvec + kUnroll * TEAM - 1) / (kUnroll * TEAM));
+    const int full = static_cast<int>(nvec / (kUnroll * TEAM));   // without a vector behind the row's last
 
+    uint4 held[HOLD ? HELD : 1];
+    if (HOLD && works) {   // before the weight is known: a short row's time is latency
+#pragma unroll
+        for (int j = 0; j < HELD; ++j) held[j] = tid + j * TEAM < nvec ? zv[tid + j * TEAM] : nothing<Z>();
+    }
     const float w = p.weight ? p.weight[t] : 1.0f;
     if (w == 0.0f) {
         if (MODE != kBackward && tid == 0) {
@@ -239,11 +256,6 @@ __global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM + 32) distill_kernel(c
         }
         if (MODE != kForward && works) clear_row<Z, TEAM>(dz, p.V, tid);
         return;
-    }
-    uint4 held[HOLD ? kHeld : 1];
-    if (HOLD && works) {
-#pragma unroll
-        for (int j = 0; j < kHeld; ++j) held[j] = tid + j * TEAM < nvec ? zv[tid + j * TEAM] : nothing<Z>();
     }
     bool none = false;   // no entry
     if (brings) {
@@ -281,18 +293,26 @@ __global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM + 32) distill_kernel(c
             };
             if (HOLD) {
 #pragma unroll
-                for (int j = 0; j < kHeld; ++j)
+                for (int j = 0; j < HELD; ++j)
                     if (tid + j * TEAM < nvec) take(held[j]);
             } else {
-                int64_t i = tid;
-                for (; i + (kUnroll - 1) * TEAM < nvec; i += kUnroll * TEAM) {
+                for (int g = 0; g < groups; ++g) {
+                    const int64_t i = tid + static_cast<int64_t>(g) * kUnroll * TEAM;
                     uint4 v[kUnroll];
+                    if (g < full) {
 #pragma unroll
-                    for (int j = 0; j < kUnroll; ++j) v[j] = zv[i + j * TEAM];
+                        for (int j = 0; j < kUnroll; ++j) v[j] = zv[i + j * TEAM];
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < kUnroll; ++j) v[j] = i + j * TEAM < nvec ? zv[i + j * TEAM] : nothing<Z>();
+                    }
+                    if (g < STASH / kUnroll) {
+#pragma unroll
+                        for (int j = 0; j < kUnroll; ++j) stash[i + j * TEAM] = v[j];
+                    }
 #pragma unroll
                     for (int j = 0; j < kUnroll; ++j) take(v[j]);
                 }
-                for (; i < nvec; i += TEAM) take(zv[i]);
             }
         }
         r = team.join(r);
@@ -322,24 +342,32 @@ __global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM + 32) distill_kernel(c
             uint4* dv = reinterpret_cast<uint4*>(dz + head);
             if (HOLD) {
 #pragma unroll
-                for (int j = 0; j < kHeld; ++j)
+                for (int j = 0; j < HELD; ++j)
                     if (tid + j * TEAM < nvec) __stcs(dv + tid + j * TEAM, give(held[j]));
             } else {
-                // read for the last time, written for nobody here: what the first pass
-                // brought to L2 stays there longer (8192 x 131072: 857 -> 790 us; the
-                // gradient alone, which has no first pass, 66 -> 71)
-                int64_t i = tid;
-                for (; i + (kUnroll - 1) * TEAM < nvec; i += kUnroll * TEAM) {
+                // What the first pass read last is in L2 most surely, so the second goes
+                // backwards, past L2's other lines (streaming loads and stores), and ends
+                // with what shared memory holds.
+                for (int g = groups - 1; g >= 0; --g) {
+                    const int64_t i = tid + static_cast<int64_t>(g) * kUnroll * TEAM;
                     uint4 v[kUnroll];
+                    if (g < STASH / kUnroll) {
 #pragma unroll
-                    for (int j = 0; j < kUnroll; ++j) v[j] = MODE == kStep ? __ldcs(zv + i + j * TEAM) : zv[i + j * TEAM];
+                        for (int j = 0; j < kUnroll; ++j) v[j] = stash[i + j * TEAM];
+                    } else if (g < full) {
+#pragma unroll
+                        for (int j = 0; j < kUnroll; ++j) v[j] = MODE == kStep ? __ldcs(zv + i + j * TEAM) : zv[i + j * TEAM];
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < kUnroll; ++j) v[j] = i + j * TEAM < nvec ? zv[i + j * TEAM] : nothing<Z>();
+                    }
 #pragma unroll
                     for (int j = 0; j < kUnroll; ++j) {
+                        if (g >= full && i + j * TEAM >= nvec) continue;
                         if (MODE == kStep) __stcs(dv + i + j * TEAM, give(v[j]));
                         else dv[i + j * TEAM] = give(v[j]);
                     }
                 }
-                for (; i < nvec; i += TEAM) dv[i] = give(zv[i]);
             }
         } else {   // rows that start at different places within 16 bytes
             for (int64_t i = head + tid; i < tail; i += TEAM) put(dz + i, grad(to_float(z[i])));
@@ -378,23 +406,37 @@ __global__ void __launch_bounds__(1024) distill_total_kernel(const float* loss, 
     }
 }
 
-template <typename Z, int TEAM, int MODE, bool HOLD>
+template <typename Z, int TEAM, int MODE, int HELD, int STASH, int BLOCKS>
 int start_team(const DistillParams& p, cudaStream_t st) {
     const int64_t grid = TEAM == 32 ? (p.T + 7) / 8 : p.T;
     if (grid >= (1ll << 31)) return MOE_EINVAL;
-    distill_kernel<Z, TEAM, MODE, HOLD><<<static_cast<unsigned>(grid), TEAM == 32 ? 256 : TEAM + 32, 0, st>>>(p);
+    const auto kern = distill_kernel<Z, TEAM, MODE, HELD, STASH, BLOCKS>;
+    const int most = STASH * TEAM * 16 + (TEAM == 32 ? 8 : 1) * 5 * 4 * kMaxEntries;
+    const int bytes = STASH * TEAM * 16 + (TEAM == 32 ? 8 : 1) * 5 * 4 * ((p.K + 3) / 4 * 4);
+    if (const int rc = ensure_smem_attr(reinterpret_cast<const void*>(kern), most)) return rc;
+    kern<<<static_cast<unsigned>(grid), TEAM == 32 ? 256 : TEAM + 32, bytes, st>>>(p);
     return cudaPeekAtLastError() == cudaSuccess ? MOE_OK : MOE_ECUDA;
 }
 
 template <typename Z, int MODE>
 int start(const DistillParams& p, cudaStream_t st) {
-    // the smallest team whose registers hold the row, whether it reads it again or not: all
-    // of a row's loads are then under way at once
-    const int64_t vectors = p.V * static_cast<int64_t>(sizeof(Z)) / 16;
-    if (vectors <= 32 * kHeld) return start_team<Z, 32, MODE, true>(p, st);
-    if (vectors <= 128 * kHeld) return start_team<Z, 128, MODE, true>(p, st);
-    if (vectors <= 512 * kHeld) return start_team<Z, 512, MODE, true>(p, st);
-    return start_team<Z, 512, MODE, false>(p, st);
+    int dev = 0, sms = 0;
+    if (const int rc = current_device(&dev, &sms)) return rc;
+    // The smallest team whose registers hold the row, whether it reads it again or not: all
+    // of a row's loads are then under way at once (16384 rows of 3001 bf16, a warp of 12
+    // vectors 55 us, a CTA of 128 threads 79; 8192 of 16001, 256 threads 103, 512 154).
+    const int64_t bytes = p.V * static_cast<int64_t>(sizeof(Z)), vectors = bytes / 16;
+    if (vectors <= 32 * 4) return start_team<Z, 32, MODE, 4, 0, 4>(p, st);
+    if (vectors <= 32 * 8) return start_team<Z, 32, MODE, 8, 0, 3>(p, st);
+    if (vectors <= 32 * 12) return start_team<Z, 32, MODE, 12, 0, 3>(p, st);
+    if (vectors <= 128 * 8) return start_team<Z, 128, MODE, 8, 0, 8>(p, st);
+    if (vectors <= 256 * 8) return start_team<Z, 256, MODE, 8, 0, 4>(p, st);
+    if (vectors <= 480 * 8) return start_team<Z, 480, MODE, 8, 0, 3>(p, st);
+    if (MODE != kStep) return start_team<Z, 512, MODE, 0, 0, 3>(p, st);
+    // as many rows at once as half of L2 holds, and more of a longer row in shared memory
+    // (8192 rows of 128 KB: 355 us with two CTAs an SM, 313 with three; of 256 KB: 668, 742)
+    if (bytes * 3 * sms <= (64ll << 20)) return start_team<Z, 480, MODE, 0, 4, 3>(p, st);
+    return start_team<Z, 512, MODE, 0, 8, 2>(p, st);
 }
 
 DistillParams distill_params(const moe_distill_t& c, const void* z, const int32_t* ids,

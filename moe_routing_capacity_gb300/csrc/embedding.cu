@@ -165,7 +165,7 @@ __device__ __forceinline__ int warp_before(int v) {
 // steps took 17, 25, 73 and 390 us for 8191, 16384, 65536 and 262144 tokens.)
 
 // Count: a token's rank among its word's as they come.  A warp's tokens of one word ask
-// once for all of them (16384 tokens of one word: 36 -> EMB_ONE us).
+// once for all of them (16384 tokens of one word: 36 -> 31 us).
 __global__ void __launch_bounds__(kPlanThreads) embedding_count_kernel(const PlanView v, const int32_t* ids,
                                                                        int64_t T, int64_t V, int32_t* status) {
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x;
