@@ -114,6 +114,7 @@ struct PlanView {
                       // pieces
     int32_t* count;   // [V]
     int32_t* start;   // [V] where a word's tokens begin in order
+    int2* first;      // [V] its first piece and, where it has several, their first scratch row
     int32_t* rank;    // [T] a token's place among its word's as they came
     int32_t* mixed;   // [T] the tokens by word, as they came
     int32_t* order;   // [T] the tokens of words of several pieces, ascending
@@ -135,6 +136,7 @@ int64_t plan_layout(int64_t T, int64_t V, int d, uint8_t* base, PlanView* v) {
     w.head = reinterpret_cast<int32_t*>(take(64));
     w.count = reinterpret_cast<int32_t*>(take(V * 4));
     w.start = reinterpret_cast<int32_t*>(take(V * 4));
+    w.first = reinterpret_cast<int2*>(take(V * 8));
     w.rank = reinterpret_cast<int32_t*>(take(T * 4));
     w.mixed = reinterpret_cast<int32_t*>(take(T * 4));
     w.order = reinterpret_cast<int32_t*>(take(T * 4));
@@ -214,13 +216,11 @@ __global__ void __launch_bounds__(kPlanThreads) embedding_pieces_kernel(const Pl
     row += sums[2][wid] + first[2];
     if (!mine || !moe_check(at + n <= T && pc + np <= T, 1621)) return;
     v.start[id] = at;
+    v.first[id] = make_int2(pc, row);
     if (np > 1) v.joins[atomicAdd(v.head + 3, 1)] = make_int4(id, row, np, at);
-    for (int j = 0; j < np; ++j)
-        v.pieces[pc + j] = make_int4(id, at + j * kPiece, n - j * kPiece < kPiece ? n - j * kPiece : kPiece,
-                                     np > 1 ? row + j : -1);
 }
 
-// The tokens to their words' places, as they came.
+// The tokens to their words' places, as they came; every kPiece-th writes a piece.
 __global__ void __launch_bounds__(kPlanThreads) embedding_place_kernel(const PlanView v, const int32_t* ids,
                                                                        int64_t T) {
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x;
@@ -229,12 +229,18 @@ __global__ void __launch_bounds__(kPlanThreads) embedding_place_kernel(const Pla
     const int r = t < T ? __ldcg(v.rank + t) : -1;
     if (r < 0) return;
     const int at = __ldcg(v.start + id) + r;
-    if (moe_check(at < T, 1622)) v.mixed[at] = static_cast<int32_t>(t);
+    if (!moe_check(at < T, 1622)) return;
+    v.mixed[at] = static_cast<int32_t>(t);
+    if (r % kPiece) return;
+    const int n = __ldcg(v.count + id), j = r / kPiece;
+    const int2 f = __ldcg(v.first + id);
+    if (!moe_check(f.x + j < T, 1629)) return;
+    v.pieces[f.x + j] = make_int4(id, at, n - r < kPiece ? n - r : kPiece, n > kPiece ? f.y + j : -1);
 }
 
 // Words of several pieces in order (a piece's own order is the gradient's affair where it
 // is the word's only one): a word's tokens as bits of a window of the batch, read out from
-// its front, 16 words of bits a thread.
+// its front.
 __global__ void __launch_bounds__(kPlanThreads) embedding_order_kernel(const PlanView v, int64_t T) {
     extern __shared__ __align__(16) uint32_t bits[];
     __shared__ int sums[kPlanThreads / 32];
@@ -243,8 +249,8 @@ __global__ void __launch_bounds__(kPlanThreads) embedding_order_kernel(const Pla
     const int longs = __ldcg(v.head + 3);
     const int64_t window = T < kWindow ? T : kWindow;
     const int quads = static_cast<int>((window + 127) / 128);   // of words of bits
-    const int each = (quads + kPlanThreads - 1) / kPlanThreads;
-    const int q0 = static_cast<int>(threadIdx.x) * each, q1 = q0 + each < quads ? q0 + each : quads;
+    const int each = (4 * quads + kPlanThreads - 1) / kPlanThreads;   // words a thread
+    const int q0 = static_cast<int>(threadIdx.x) * each, q1 = q0 + each < 4 * quads ? q0 + each : 4 * quads;
     for (int l = blockIdx.x; l < longs; l += gridDim.x) {
         const int4 q = __ldcg(v.joins + l);
         const int n = __ldcg(v.count + q.x);
@@ -261,10 +267,7 @@ __global__ void __launch_bounds__(kPlanThreads) embedding_order_kernel(const Pla
             }
             __syncthreads();
             int c = 0;
-            for (int i = q0; i < q1; ++i) {
-                const uint4 b = reinterpret_cast<const uint4*>(bits)[i];
-                c += __popc(b.x) + __popc(b.y) + __popc(b.z) + __popc(b.w);
-            }
+            for (int i = q0; i < q1; ++i) c += __popc(bits[i]);
             const int before = warp_before(c);
             if (lane == 31) sums[wid] = before + c;
             __syncthreads();
@@ -274,12 +277,24 @@ __global__ void __launch_bounds__(kPlanThreads) embedding_order_kernel(const Pla
                 if (w < wid) to += sums[w];
                 done += sums[w];
             }
-            for (int i = 4 * q0; i < 4 * q1 && c; ++i) {
-                for (uint32_t b = bits[i]; b; b &= b - 1) {
-                    if (moe_check(to < q.w + n, 1624))
-                        v.order[to] = static_cast<int32_t>(w0 + 32ll * i + __ffs(b) - 1);
-                    ++to;
+            const bool dense = 16ll * n >= window;   // a lane a bit of a neighbour's word, else each its own
+            for (int k = 0; k < each; ++k) {
+                const int i = q0 + k;
+                uint32_t b = i < q1 ? bits[i] : 0;
+                const int32_t t = static_cast<int32_t>(w0 + 32ll * i);
+                if (!dense) {
+                    for (; b; b &= b - 1, ++to)
+                        if (moe_check(to < q.w + n, 1624)) v.order[to] = t + __ffs(b) - 1;
+                    continue;
                 }
+                for (unsigned some = __ballot_sync(0xffffffffu, b != 0); some; some &= some - 1) {
+                    const int who = __ffs(some) - 1;
+                    const uint32_t word = __shfl_sync(0xffffffffu, b, who);
+                    const int at = __shfl_sync(0xffffffffu, to, who) + __popc(word & ((1u << lane) - 1u));
+                    const int32_t first = __shfl_sync(0xffffffffu, t, who);
+                    if ((word >> lane & 1u) && moe_check(at < q.w + n, 1624)) v.order[at] = first + lane;
+                }
+                to += __popc(b);
             }
             __syncthreads();
         }
@@ -391,8 +406,13 @@ __global__ void __launch_bounds__(256, 3) embedding_bwd_kernel(const GradParams 
         __syncthreads();
         if (wid == adders) {
             const int64_t bytes = p.d * static_cast<int64_t>(sizeof(Tab));
-            for (int64_t id = blockIdx.x + static_cast<int64_t>(lane) * gridDim.x; id < p.V; id += 32ll * gridDim.x) {
-                if (__ldg(p.v.count + id) != 0) continue;
+            // short rows side by side, 32 a time, long ones from all CTAs in turn (131072 rows of
+            // 4 KB 81 us, in turn 89; of 24 KB 588 and 532)
+            const int log_run = bytes < 16384 ? 5 : 0;
+            const int64_t runs = (p.V + (1 << log_run) - 1) >> log_run;
+            for (int64_t k = lane; (k >> log_run) * gridDim.x + blockIdx.x < runs; k += 32) {
+                const int64_t id = (((k >> log_run) * gridDim.x + blockIdx.x) << log_run) + (k & ((1 << log_run) - 1));
+                if (id >= p.V || __ldg(p.v.count + id) != 0) continue;
                 uint8_t* row = static_cast<uint8_t*>(p.dtable) + id * bytes;
                 for (int64_t o = 0; o < bytes; o += kZeros)
                     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(row + o),
@@ -442,6 +462,7 @@ __global__ void __launch_bounds__(256) embedding_join_kernel(const GradParams p)
         const int4 q = __ldg(p.v.joins + w);
         float s[8] = {};
         if (c < p.chunks)
+#pragma unroll 8
             for (int j = run; j < q.z; j += 8) {
                 const float4* r = reinterpret_cast<const float4*>(p.v.part + static_cast<int64_t>(q.y + j) * p.d + 8 * c);
                 const float4 a = __ldcg(r), b = __ldcg(r + 1);
