@@ -281,9 +281,14 @@ __global__ void __launch_bounds__(kThreads) router_select_kernel(const __grid_co
         float b[PER];
         load<U>(b, p.bias, at);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {   // NaN as the smallest; -infinity where there is no expert
+        for (int i = 0; i < PER; ++i)   // NaN as the smallest; -infinity where there is no expert
             v[i] = fmaxf(fast_score(v[i], m, inv, sm) + b[i], -INFINITY);
-            merge2(b1, b2, v[i], -INFINITY);
+        if (by_groups && p.top2) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) merge2(b1, b2, v[i], -INFINITY);
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) b1 = fmaxf(b1, v[i]);
         }
     } else if (by_groups && p.top2) {
 #pragma unroll
@@ -292,8 +297,6 @@ __global__ void __launch_bounds__(kThreads) router_select_kernel(const __grid_co
             merge2(b1, b2, v[i], -INFINITY);
         }
     } else {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) v[i] = fmaxf(v[i], -INFINITY);
         b1 = top;
     }
     bool keep = grp < p.groups, all = false;   // all: the whole row in 64 bits
@@ -373,12 +376,18 @@ __global__ void __launch_bounds__(kThreads) router_select_kernel(const __grid_co
     // average; with fewer, a lane goes on to its next value.
     uint32_t key = keep && at.room > 0 ? order_key(high) : 0u, reach = 0;
     const bool deep = 2 * p.k > __popc(__ballot_sync(kAll, key != 0));
-    for (int j = 0; j < p.k; ++j) {
-        const uint32_t best = __reduce_max_sync(kAll, key);
-        reach = best ? best : reach;
-        const bool won = key == best;
-        key = won ? 0u : key;
-        if (deep && won) {
+    if (!deep) {
+        for (int j = 0; j < p.k; ++j) {
+            const uint32_t best = __reduce_max_sync(kAll, key);
+            reach = best ? best : reach;
+            key = key == best ? 0u : key;
+        }
+    } else {
+        for (int j = 0; j < p.k; ++j) {
+            const uint32_t best = __reduce_max_sync(kAll, key);
+            reach = best ? best : reach;
+            if (key != best) continue;
+            key = 0u;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const uint32_t k2 = at.has(i) ? order_key(v[i]) : 0u;
@@ -394,11 +403,13 @@ __global__ void __launch_bounds__(kThreads) router_select_kernel(const __grid_co
         const float off = score_error(fast_score(big, m, inv, sm), fmaxf(1.0f, fabsf(arg)), sm);
         from = least - 4.0f * fmaf(fabsf(least), kStep, off);
     }
+    // (absent experts are at -infinity: where that, or NaN, would do, choose64 does)
+    all = all || !(from > -INFINITY);
     uint32_t bits = 0;
-    if (keep) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) bits |= at.has(i) && !(v[i] < from) ? 1u << i : 0u;
-    }
+    for (int i = 0; i < PER; ++i)
+        if (v[i] >= from) bits |= 1u << i;
+    if (!keep) bits = 0;
     const int n = collect<U>(bits, at, list);
     int e = 0, rank = 32;
     float l = 0.0f;
