@@ -877,6 +877,13 @@ def grad_clip(grads, max_norm, norm, stream=None):
 
 # ---------------------------------------------------------------- head norms with rotation
 
+def _at(t, dtype):
+    """_ptr's checks; the plain address (None stays None)."""
+    if t is not None and t.dtype == dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _ptr(t, dtype, allow_none=True)
+
+
 def _head_norm_config(q, k, table, pos, eps, interleaved):
     if q.dim() != 3 or (k is not None and k.dim() != 3):
         raise ValueError("q and k are [T, heads, D]")
@@ -907,8 +914,8 @@ def head_norm_rotary(q, k, w_q, w_k, table, pos, q_out, k_out, status, eps=1e-6,
         kop, c.ko_t, c.ko_h = _heads("k_out", k_out, ks)
     _check("moe_head_norm_rotary", lib().moe_head_norm_rotary(
         ctypes.byref(c), qp, kp, _rows("w_q", w_q, chan, _BF16),
-        _rows("w_k", w_k, chan, _BF16, k is None), _ptr(table, f32, allow_none=True),
-        _ptr(pos, i32, allow_none=True), qop, kop, _ptr(status, i32), _stream(stream)))
+        _rows("w_k", w_k, chan, _BF16, k is None), _at(table, f32),
+        _at(pos, i32), qop, kop, _at(status, i32), _stream(stream)))
 
 
 def head_norm_rotary_workspace(T, hq, hk, D) -> int:
@@ -937,9 +944,9 @@ def head_norm_rotary_backward(dq, dk, q, k, w_q, w_k, table, pos, dq_out, dk_out
         kop, c.ko_t, c.ko_h = _heads("dk_out", dk_out, ks)
     _check("moe_head_norm_rotary_backward", lib().moe_head_norm_rotary_backward(
         ctypes.byref(c), dqp, dkp, qp, kp, _rows("w_q", w_q, chan, _BF16),
-        _rows("w_k", w_k, chan, _BF16, none), _ptr(table, f32, allow_none=True),
-        _ptr(pos, i32, allow_none=True), qop, kop, _rows("dw_q", dw_q, chan, _F32),
-        _rows("dw_k", dw_k, chan, _F32, none), _ptr(ws, u8), ws.numel(), _ptr(status, i32),
+        _rows("w_k", w_k, chan, _BF16, none), _at(table, f32),
+        _at(pos, i32), qop, kop, _rows("dw_q", dw_q, chan, _F32),
+        _rows("dw_k", dw_k, chan, _F32, none), _at(ws, u8), ws.numel(), _at(status, i32),
         _stream(stream)))
 
 
@@ -1013,7 +1020,7 @@ def embedding(table, ids, out, status, scale=1.0, stream=None):
     c = _embedding_config(table, out, T, scale)
     _check("moe_embedding", lib().moe_embedding(
         ctypes.byref(c), _rows("table", table, (c.V, c.d), _RES), _rows("ids", ids, (T,), _I32),
-        _rows("out", out, (T, c.d), _RES), _ptr(status, i32), _stream(stream)))
+        _rows("out", out, (T, c.d), _RES), _at(status, i32), _stream(stream)))
 
 
 class EmbeddingPlan:
@@ -1038,8 +1045,8 @@ class EmbeddingPlan:
 
     def refill(self, ids, stream=None):
         _check("moe_embedding_plan", lib().moe_embedding_plan(
-            self.T, self.vocab, self.d, _rows("ids", ids, (self.T,), _I32), _ptr(self.plan, u8),
-            self.plan.numel(), _ptr(self.status, i32), _stream(stream)))
+            self.T, self.vocab, self.d, _rows("ids", ids, (self.T,), _I32), _at(self.plan, u8),
+            self.plan.numel(), _at(self.status, i32), _stream(stream)))
 
 
 def embedding_backward(plan, dout, dtable, scale=1.0, accumulate=False, stream=None):
@@ -1092,7 +1099,7 @@ def distill_loss(logits, ids, teacher, weight, loss, lse, status, total=None, dl
         ctypes.byref(c), zp, _rows("ids", ids, given, _I32), _rows("teacher", teacher, given, _RES),
         _rows("weight", weight, tok, _F32, True), _rows("loss", loss, tok, _F32),
         _rows("lse", lse, tok, _F32), _rows("total", total, (1,), _F32, True), dp,
-        _ptr(status, i32), _stream(stream)))
+        _at(status, i32), _stream(stream)))
 
 
 def distill_loss_backward(logits, ids, teacher, weight, lse, dlogits, status, temperature=1.0,
@@ -1106,4 +1113,4 @@ def distill_loss_backward(logits, ids, teacher, weight, lse, dlogits, status, te
     _check("moe_distill_loss_backward", lib().moe_distill_loss_backward(
         ctypes.byref(c), zp, _rows("ids", ids, given, _I32), _rows("teacher", teacher, given, _RES),
         _rows("weight", weight, tok, _F32, True), _rows("lse", lse, tok, _F32), dp,
-        _ptr(status, i32), _stream(stream)))
+        _at(status, i32), _stream(stream)))

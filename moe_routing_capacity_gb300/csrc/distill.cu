@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(1024) distill_total_kernel(const float* loss, 
     __shared__ float red[32];
     asm volatile("griddepcontrol.wait;" ::: "memory");   // the losses are complete
     float s = 0.0f;
-    for (int64_t t = threadIdx.x; t < T; t += 1024) s += loss[t];
+    for (int64_t t = threadIdx.x; t < T; t += 1024) s += __ldcg(loss + t);   // past L1, as it started early
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;

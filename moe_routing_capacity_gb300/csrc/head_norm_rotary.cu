@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(1024) head_norm_sums_kernel(const float* part,
     float s = 0.0f;
     const bool there = c < (dw_k ? 2 : 1) * D;
     if (there)
-        for (int b = run; b < blocks; b += 32) s += part[static_cast<int64_t>(b) * 2 * D + c];
+        for (int b = run; b < blocks; b += 32) s += __ldcg(part + static_cast<int64_t>(b) * 2 * D + c);   // past L1, as it started early
     red[run][lane] = s;
     __syncthreads();
     if (run == 0 && there) {

@@ -172,11 +172,9 @@ def test_training_step(tied):
     assert all(bool(t.isfinite().all()) for t in got.values())
     assert {f"blocks.{i}.{n}" for i in (0, 1) for n in ("w_q", "w_k", "W_qkv", "moe.Wr")} <= set(got)
     assert int(m.status) == 0 and all(int(b.status) == 0 for b in m.blocks)
-    # the gradient points downhill: a short step along it lowers the loss by its square
-    norm = torch.empty(1, device="cuda")
-    before = float(m.total)
+    norm = torch.empty(1, device="cuda")          # all of them are a GradSet's tensors
     abi.grad_clip(abi.GradSet(list(got.values())), math.inf, norm)
-    assert math.isfinite(float(norm)) and float(norm) > 0 and math.isfinite(before)
+    assert math.isfinite(float(norm)) and float(norm) > 0
 
 
 def test_training_step_repeats_and_replays():
