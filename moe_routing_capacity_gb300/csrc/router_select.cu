@@ -97,17 +97,20 @@ __device__ __noinline__ int choose64(const SelectParams& p, int64_t t) {
     const float* row = p.logits + t * p.E;
     const Entries<U> at(p, grp, sub);
     const float l0 = __ldg(row);
-    bool same = true;
+    bool same = true, even = true;
     uint32_t open = 0;   // entries that may still be chosen
     float m = -INFINITY;
+#pragma unroll 4
     for (int i = 0; i < PER; ++i) {
         if (!at.has(i)) continue;
         open |= 1u << i;
         const float l = __ldg(row + at.expert(i));
         same = same && l == l0;
+        even = even && (!p.bias || __ldg(p.bias + at.expert(i)) == __ldg(p.bias));
         m = fmaxf(m, l);
     }
     same = __all_sync(kAll, same);
+    if (same && __all_sync(kAll, even)) return lane;   // nothing to choose by: the first experts
     m = warp_max(m);
     double sum = 1;
     if (p.softmax && !same) {
@@ -502,48 +505,45 @@ __device__ __forceinline__ void put(uint16_t* o, float v) {
     *o = *reinterpret_cast<const uint16_t*>(&b);
 }
 
-// The chosen logit's own part of the gradient, and for softmax without renormalisation
-// (dense) what the whole row is made from: dl_e = s_e (g_e - all).
-struct ChosenGrad {
-    int e;
-    float d;
-};
-__device__ __forceinline__ ChosenGrad chosen_grad(const SelectBwdParams& p, int64_t t, float m, float inv,
-                                                  float* all) {
-    const int lane = threadIdx.x & 31;
-    ChosenGrad c{-1, 0.0f};
+// A lane's chosen expert (-1: none), the gradient of its weight and its logit, asked for
+// before the row so that the waits overlap.
+struct Chosen {
+    int e = -1;
     float g = 0.0f, l = -INFINITY;
-    if (lane < p.k) {
-        c.e = __ldg(p.idx + t * p.k + lane);
-        if (c.e < 0 || c.e >= p.E) c.e = -1;
-        if (c.e >= 0) {
-            g = __ldg(p.dw + t * p.k + lane) * p.scale;
-            l = __ldg(p.logits + t * p.E + c.e);
-        }
+    __device__ __forceinline__ Chosen(const SelectBwdParams& p, int64_t t) {
+        const int lane = threadIdx.x & 31;
+        if (lane >= p.k) return;
+        const int i = __ldg(p.idx + t * p.k + lane);
+        const float dw = __ldg(p.dw + t * p.k + lane);
+        if (i < 0 || i >= p.E) return;
+        e = i;
+        g = dw * p.scale;
+        l = __ldg(p.logits + t * p.E + i);
     }
+};
+
+// The chosen logit's own part of the gradient, and for softmax without renormalisation
+// what the whole row is made from: dl_e = s_e (g_e - all).
+__device__ __forceinline__ float chosen_grad(const SelectBwdParams& p, const Chosen& c, float m, float inv,
+                                             float* all) {
     if (p.softmax && !p.renorm) {
-        const float s = c.e >= 0 ? __expf(l - m) * inv : 0.0f;
-        *all = warp_sum(c.e >= 0 ? g * s : 0.0f);
-        c.d = s * (g - *all);
-        return c;
+        const float s = c.e >= 0 ? __expf(c.l - m) * inv : 0.0f;
+        *all = warp_sum(c.e >= 0 ? c.g * s : 0.0f);
+        return s * (c.g - *all);
     }
     float s, gate = 1.0f;   // ds/dl = s gate
     if (p.softmax) {
-        const float top = warp_max(l);
-        s = c.e >= 0 ? expf(l - top) : 0.0f;
+        const float top = warp_max(c.l);
+        s = c.e >= 0 ? expf(c.l - top) : 0.0f;
     } else {
-        const float x = expf(-l);
+        const float x = expf(-c.l);
         s = c.e >= 0 ? 1.0f / (1.0f + x) : 0.0f;
         gate = x > 3e38f ? 1.0f : x / (1.0f + x);   // 1 - s, without the difference
     }
-    if (p.renorm) {
-        const float sum = warp_sum(s);
-        const float n = sum == 0.0f ? 0.0f : s / sum;
-        c.d = n * gate * (g - warp_sum(c.e >= 0 ? g * n : 0.0f));
-    } else {
-        c.d = s * gate * g;
-    }
-    return c;
+    if (!p.renorm) return s * gate * c.g;
+    const float sum = warp_sum(s);
+    const float n = sum == 0.0f ? 0.0f : s / sum;
+    return n * gate * (c.g - warp_sum(c.e >= 0 ? c.g * n : 0.0f));
 }
 
 __device__ __forceinline__ void put4(float* o, const float (&v)[4]) {
@@ -562,8 +562,8 @@ __global__ void __launch_bounds__(kThreads) router_select_bwd4_kernel(const Sele
     if (t >= p.T) return;
     Out* to = static_cast<Out*>(p.dlogits) + t * p.E;
     const int quads = p.E / 4;
-    float m = 0.0f, inv = 0.0f, all = 0.0f;
-    ChosenGrad c;
+    float m = 0.0f, inv = 0.0f, all = 0.0f, d;
+    const Chosen c(p, t);
     if (p.softmax && !p.renorm) {
         float4 v[Q];
         const float4* row = reinterpret_cast<const float4*>(p.logits + t * p.E);
@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(kThreads) router_select_bwd4_kernel(const Sele
             sum += (v[i].x + v[i].y) + (v[i].z + v[i].w);
         }
         inv = 1.0f / warp_sum(sum);
-        c = chosen_grad(p, t, m, inv, &all);
+        d = chosen_grad(p, c, m, inv, &all);
         const float f = -inv * all;
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
@@ -594,10 +594,10 @@ __global__ void __launch_bounds__(kThreads) router_select_bwd4_kernel(const Sele
 #pragma unroll
         for (int i = 0; i < Q; ++i)
             if (lane + 32 * i < quads) put4(to + 4 * (lane + 32 * i), o);
-        c = chosen_grad(p, t, m, inv, &all);
+        d = chosen_grad(p, c, m, inv, &all);
     }
     __syncwarp();   // the row is written
-    if (c.e >= 0) put(to + c.e, c.d);
+    if (c.e >= 0) put(to + c.e, d);
 }
 
 // The same for rows that are not in whole fours: a row is put together in shared memory,
@@ -623,10 +623,11 @@ __global__ void __launch_bounds__(kThreads) router_select_bwd_kernel(const Selec
             for (int i = lane; i < p.E; i += 32) sum += __expf(__ldg(row + i) - m);
             inv = 1.0f / warp_sum(sum);
         }
-        const ChosenGrad c = chosen_grad(p, t, m, inv, &all);
+        const Chosen c(p, t);
+        const float d = chosen_grad(p, c, m, inv, &all);
         for (int i = lane; i < p.E; i += 32) put(mine + i, dense ? -(__expf(__ldg(row + i) - m) * inv) * all : 0.0f);
         __syncwarp();
-        if (c.e >= 0) put(mine + c.e, c.d);
+        if (c.e >= 0) put(mine + c.e, d);
     }
     __syncthreads();
     const int64_t n = (p.T - t0 < W ? p.T - t0 : W) * p.E * static_cast<int64_t>(sizeof(Out));
@@ -648,6 +649,8 @@ void start_backward(const SelectBwdParams& p, unsigned grid, cudaStream_t st) {
         router_select_bwd4_kernel<1, Out><<<grid, kThreads, 0, st>>>(p);
     else if (need <= 2)
         router_select_bwd4_kernel<2, Out><<<grid, kThreads, 0, st>>>(p);
+    else if (need <= 3)
+        router_select_bwd4_kernel<3, Out><<<grid, kThreads, 0, st>>>(p);
     else if (need <= 4)
         router_select_bwd4_kernel<4, Out><<<grid, kThreads, 0, st>>>(p);
     else
