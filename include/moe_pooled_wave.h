@@ -790,8 +790,8 @@ int moe_head_norm_rotary_backward(const moe_head_norm_t* cfg, const uint16_t* dq
  *   group's value is the sum of its group_top (1 or 2) largest v; the
  *   groups_kept groups of largest value stay open, and of their experts the
  *   top_k with the largest v are chosen, in falling order of v;
- *   w_j = scale s_j, or scale s_j / sum of the chosen s (renorm; 0 where that
- *   sum is 0).
+ *   w_j = scale s_j, or scale s_j / sum of the chosen s (renorm; 0 where in 64
+ *   bits that sum is 0).
  * The order is that of the exact values of v for the given l and bias (equal
  * ones: the lower index first), to the precision of 64 bits.  The bias has no
  * part in w.  NaN counts as the smallest value in the choice: idx always holds
@@ -833,8 +833,8 @@ int moe_layer_backward_routed(const moe_config_t* cfg, int ragged,
  *   table [V, d] bf16 or fp32 (table_f32), ids [T] int32, out [T, d] bf16 or
  *   fp32 (out_f32); rows contiguous, rounded once
  * Gradient: dtable_v = scale sum over t with ids_t = v of dout_t, [V, d] of
- * table_f32's type, summed in fp32 in the tokens' order and rounded once; words
- * that do not occur become 0.  accumulate = 1: added to what dtable holds
+ * table_f32's type, summed in fp32 in an order that ids alone decide and rounded
+ * once; words that do not occur become 0.  accumulate = 1: added to what dtable holds
  * (rounded once more), words that do not occur left as they are.
  *   plan: moe_embedding_plan's, of plan_bytes from moe_embedding_workspace, made
  *   from ids on the stream (ids outside [0, V) but -1: MOE_EINVAL in status;

@@ -76,8 +76,8 @@ __device__ __forceinline__ uint4 gather(const float (&f)[8]) {
                       pack_bf16x2(f[6], f[7]));
 }
 
-// Running maximum and sum of 2^(x - maximum).  Every operation is written out, so that the
-// losses have the same bits with and without the gradient.
+// Running maximum and sum of 2^(x - maximum).  Every operation is written out, so that
+// what is contracted does not hang on what a kernel does besides.
 struct Run {
     float m = -INFINITY, s = 0.0f;
     // raises the maximum to at least v; what to subtract from the exponents

@@ -270,6 +270,37 @@ def test_router_select_values_that_are_not_finite(rng):
                 assert bool(dl[rest].isfinite().all())
 
 
+@pytest.mark.parametrize("E", [40, 41])
+@pytest.mark.parametrize("bias", [False, True])
+def test_router_select_shares_of_small_scores(rng, E, bias):
+    """Sigmoids that fp32 does not hold have shares all the same, as long as 64 bits
+    hold them, and those have gradients."""
+    T, k = 40, 6
+    rule = abi.Routing(E, k, score="sigmoid", renorm=True, scale=2.5)
+    logits = randn(rng, T, E, dt=F32) - ints(rng, 58, 62, T, 1).float()
+    logits[:20] = randn(rng, 20, E, dt=F32) - ints(rng, 85, 600, 20, 1).float()
+    logits[0] = -300.0
+    logits[1] = -1000.0                                # 0 in 64 bits as well
+    logits[2] = -float("inf")
+    b = randn(rng, E, std=0.1, dt=F32) if bias else None
+    idx, w = torch.empty(T, k, device="cuda", dtype=I32), empty(T, k, dt=F32)
+    abi.router_select(rule, logits, b, idx, w)
+    want, ww = R.select(logits, b, rule)
+    if bias:                                           # 64 bits lose s beside the bias
+        want = torch.sort(b.double().expand(T, E), dim=1, descending=True, stable=True)[1][:, :k]
+        ww = R.weights(R.scores(logits, False), want, rule)
+    assert torch.equal(idx.long(), want)
+    assert bool((w[1:3] == 0).all())
+    ok = torch.arange(T, device="cuda")
+    ok = (ok < 1) | (ok > 2)
+    R.within("w", w[ok], ww[ok], 128 * R.STEP * ww[ok])
+    dw, dl = randn(rng, T, k, dt=F32), empty(T, E, dt=F32)
+    abi.router_select_backward(rule, logits, idx, dw, dl)
+    ref, mag = R.select_backward(logits[ok], want[ok], dw[ok], rule)
+    R.within("dlogits", dl[ok], ref, (128 + E / 16) * R.STEP * (ref.abs() + mag))
+    assert bool((dl[1:3] == 0).all())
+
+
 def test_router_select_backward_skips_other_ids(rng):
     T, E, k = 9, 24, 3
     rule = abi.Routing(E, k, score="sigmoid", renorm=False)
