@@ -9,14 +9,15 @@
 // A head row is a group of G lanes, each with 16 channels: both chunks of 8 that a
 // rotation pairs, or 16 channels behind the rotated ones, so that turning a pair and both
 // means stay within a lane and log2 G exchanges.  The grid fills the machine once; a group
-// walks over (token, share of its heads), weights and angles in registers, with kStages
-// rows under way that each lane copies for itself (no barrier).  Nothing but x, dy and the
-// outputs moves, and memory bounds it:
-//   forward, 16384 x (48 + 8) x 128: 80 us, floor 69;
-//   forward, 8192 x (16 + 4) x 128: 21.3 us, floor 12.4 (a group has five items of four
-//     rows, so the start and the uneven end weigh);
-//   backward, 65536 x (48 + 8) x 128: 445 us, floor 415, 6.3 TB/s.
-// A group a row with plain loads took 33 and 590 us for the last two: too few bytes asked for.
+// walks over items (a token and a share of its heads) with a few rows under way that each
+// lane copies for itself (no barrier).  The forward folds weights and angles of an item
+// into four factors a pair, and steps pointers from row to row.
+//   Forward, 16384 x (48 + 8) x 128: 77 us, floor 69; 8192 x (16 + 4) x 128: 18.0 us, floor
+// 12.4: some 180 instructions a warp's four rows, of which the 16 warps of an SM issue 45 %
+// of the time, and the start.  Items of all their rows in registers without a ring took 20.6
+// and 92, rows of weights and angles not folded 21.5 and 80.
+//   Backward, 65536 x (48 + 8) x 128: 440 us, floor 415, 6.4 TB/s: memory.  8192 x (16 + 4):
+// 31.8, floor 18.5.  The forward's stepped pointers would spill here (492 and 34).
 #include "common.cuh"
 #include "internal.h"
 
@@ -33,6 +34,7 @@ struct HeadParams {
     int64_t T, table_rows;
     int hq, hk, D, units, rot_units, half;   // units: 16-channel pieces of a head
     int q_splits, k_splits;                  // parts of a token's query heads, key heads
+    int q_each, k_each;                      // heads of a part
     int64_t q_items, items;                  // tokens times parts: the query heads', all
     Rows x_q, x_k, dy_q, dy_k, y_q, y_k;     // inputs, upstream gradients, outputs
     const uint16_t *w_q, *w_k;
@@ -45,7 +47,8 @@ struct HeadParams {
 
 constexpr int kThreads = 256;
 constexpr int kBlocks = 2;     // resident on an SM
-constexpr int kStages = 4;     // head rows that a lane has under way
+constexpr int kStages = 4;     // head rows that a lane of the gradient has under way
+constexpr int kAhead = 3;      // and of the forward
 
 // Where this lane's two chunks of 8 channels stand in a head: half the rotated width
 // apart, or half of the rest, so that neighbouring lanes read neighbouring chunks whichever
@@ -91,7 +94,6 @@ __device__ __forceinline__ void turn(float2 (&f)[8], const float2 (&c)[4], const
         }
     }
 }
-
 
 // A lane's angles of 8 pairs in four vectors of two: the pairs' order is that of the first
 // chunk's words and then the second's where pairs are neighbours, else of the chunks' channels.
@@ -150,46 +152,20 @@ struct Walk {
     }
 };
 
-// Each lane copies the chunks that it will read itself, so that a stage needs no barrier:
-// x, for the gradient dy, and with an item's first step the angles.
-template <bool PAIRS, int G, bool BWD>
+// Each lane copies the chunks of x and dy that it will read itself, so that a stage needs
+// no barrier.
 struct Ring {
-    static constexpr bool kAngles = !BWD;
-    static constexpr int kX = BWD ? 4 : 2, kSlots = kX + (kAngles ? 4 : 0);
+    static constexpr int kSlots = 4;
     uint4* mine;   // slot k of stage s: mine[(s * kSlots + k) * kThreads]
     __device__ __forceinline__ uint4* at(int stage, int k) const { return mine + (stage * kSlots + k) * kThreads; }
 
-    // Starts the copies of a step; false where the token has no place in the table.  Chunks
-    // that a head does not have stay as they are (zero).
-    __device__ __forceinline__ bool issue(const HeadParams& p, const Place& pl, const Walk& w,
-                                          int u, int stage) const {
-        const uint16_t* x = w.row(p.x_q, p.x_k);
+    // Starts the copies of a step.  Chunks that a head does not have stay as they are (zero).
+    __device__ __forceinline__ void issue(const HeadParams& p, const Place& pl, const Walk& w, int stage) const {
+        const uint16_t *x = w.row(p.x_q, p.x_k), *dy = w.row(p.dy_q, p.dy_k);
         if (pl.one) cp_async_16(smem_u32(at(stage, 0)), x + pl.c0, 16);
         if (pl.two) cp_async_16(smem_u32(at(stage, 1)), x + pl.c1, 16);
-        if (BWD) {
-            const uint16_t* dy = w.row(p.dy_q, p.dy_k);
-            if (pl.one) cp_async_16(smem_u32(at(stage, 2)), dy + pl.c0, 16);
-            if (pl.two) cp_async_16(smem_u32(at(stage, 3)), dy + pl.c1, 16);
-        }
-        if (!kAngles || !w.first || !p.table) return true;
-        const int64_t pos = p.pos ? __ldg(p.pos + w.t) : w.t;
-        if (pos < 0 || pos >= p.table_rows) {
-            report_error(p.status, MOE_EINVAL);
-            return false;
-        }
-        if (pl.rot) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) cp_async_16(smem_u32(at(stage, kX + e)), angle<PAIRS>(p, pos, u, e), 16);
-        }
-        return true;
-    }
-    __device__ __forceinline__ void angles(int stage, float sign, float2 (&c)[4], float2 (&s)[4]) const {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float4 v = *reinterpret_cast<const float4*>(at(stage, kX + e));
-            c[e] = make_float2(v.x, v.z);
-            s[e] = make_float2(sign * v.y, sign * v.w);
-        }
+        if (pl.one) cp_async_16(smem_u32(at(stage, 2)), dy + pl.c0, 16);
+        if (pl.two) cp_async_16(smem_u32(at(stage, 3)), dy + pl.c1, 16);
     }
 };
 
@@ -200,24 +176,21 @@ __device__ __forceinline__ void load_weights(const uint16_t* w, int c0, int c1, 
            two ? __ldg(reinterpret_cast<const uint4*>(w + c1)) : none, f);
 }
 
-// One pass over the heads; BWD: the gradients, and the block's part of dw.
-template <bool PAIRS, int G, bool BWD>
-__global__ void __launch_bounds__(kThreads, kBlocks) head_norm_kernel(const __grid_constant__ HeadParams p) {
+// One pass over the heads: the gradients, and the block's part of dw.
+template <bool PAIRS, int G>
+__global__ void __launch_bounds__(kThreads, kBlocks) head_norm_bwd_kernel(const __grid_constant__ HeadParams p) {
     extern __shared__ __align__(16) uint4 smem[];
     const int lane = threadIdx.x & 31, u = lane & (G - 1), group = threadIdx.x / G;
     const unsigned mask = (G == 32 ? 0xffffffffu : ((1u << G) - 1u)) << (lane & ~(G - 1));
     const Place pl(p, u);
     if (!moe_check((!pl.one || pl.c0 + 8 <= p.D) && (!pl.two || pl.c1 + 8 <= p.D), 1601)) return;
-    using R = Ring<PAIRS, G, BWD>;
-    const R ring{smem + threadIdx.x};
+    const Ring ring{smem + threadIdx.x};
     const int64_t stride = static_cast<int64_t>(gridDim.x) * (kThreads / G);
     Walk in, at;   // what is copied next, what is worked on
     in.item = at.item = static_cast<int64_t>(blockIdx.x) * (kThreads / G) + group;
-    uint32_t skip = 0;   // bit s: stage s begins an item without a place
     auto fill = [&](int stage) {
         if (in.more(p)) {
-            const bool ok = ring.issue(p, pl, in, u, stage);
-            skip = ok ? skip & ~(1u << stage) : skip | 1u << stage;
+            ring.issue(p, pl, in, stage);
             in.next(p, stride);
         }
         cp_async_commit();
@@ -225,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) head_norm_kernel(const __gr
 #pragma unroll
     for (int i = 0; i < kStages; ++i)   // chunks that a head does not have
 #pragma unroll
-        for (int k = 0; k < R::kX; ++k)
+        for (int k = 0; k < Ring::kSlots; ++k)
             if (!(k & 1 ? pl.two : pl.one)) *ring.at(i, k) = make_uint4(0, 0, 0, 0);
     float2 w[8], c[4], s[4], dw[8];
     if (in.more(p)) {
@@ -236,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) head_norm_kernel(const __gr
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[i] = make_float2(0.0f, 0.0f);
     // the group's part of dw_q and dw_k, behind the ring
-    float2* red = reinterpret_cast<float2*>(smem + kStages * R::kSlots * kThreads) + threadIdx.x;
+    float2* red = reinterpret_cast<float2*>(smem + kStages * Ring::kSlots * kThreads) + threadIdx.x;
     const bool only_keys = at.more(p) && at.keys;
     bool mine = only_keys, gone = false;
 #pragma unroll
@@ -245,27 +218,20 @@ __global__ void __launch_bounds__(kThreads, kBlocks) head_norm_kernel(const __gr
         cp_async_wait<kStages - 1>();
         if (at.keys != mine) {   // the first key heads
             load_weights(p.w_k, pl.c0, pl.c1, pl.one, pl.two, w);
-            if (BWD) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    red[i * kThreads] = dw[i];
-                    dw[i] = make_float2(0.0f, 0.0f);
-                }
+            for (int i = 0; i < 8; ++i) {
+                red[i * kThreads] = dw[i];
+                dw[i] = make_float2(0.0f, 0.0f);
             }
             mine = true;
         }
-        if (at.first) {
-            gone = skip >> stage & 1;
-            if (!R::kAngles) {
-                if (p.table) {
-                    const int64_t pos = p.pos ? __ldg(p.pos + at.t) : at.t;
-                    gone = pos < 0 || pos >= p.table_rows;
-                    if (gone)
-                        report_error(p.status, MOE_EINVAL);
-                    else if (pl.rot)
-                        load_angles<PAIRS>(p, pos, u, -1.0f, c, s);
-                }
-            } else if (pl.rot) ring.angles(stage, BWD ? -1.0f : 1.0f, c, s);
+        if (at.first && p.table) {
+            const int64_t pos = p.pos ? __ldg(p.pos + at.t) : at.t;
+            gone = pos < 0 || pos >= p.table_rows;
+            if (gone)
+                report_error(p.status, MOE_EINVAL);
+            else if (pl.rot)
+                load_angles<PAIRS>(p, pos, u, -1.0f, c, s);
         }
         float2 f[8], ss = make_float2(0.0f, 0.0f);
         unpack(*ring.at(stage, 0), *ring.at(stage, 1), f);
@@ -273,39 +239,29 @@ __global__ void __launch_bounds__(kThreads, kBlocks) head_norm_kernel(const __gr
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fma2(f[i], f[i], ss);
         float sum = ss.x + ss.y;
-        if (!BWD) {
+        float2 d[8], dot = make_float2(0.0f, 0.0f);
+        unpack(*ring.at(stage, 2), *ring.at(stage, 3), d);
+        if (pl.rot) turn<PAIRS>(d, c, s);
 #pragma unroll
-            for (int q = G / 2; q > 0; q >>= 1) sum += __shfl_xor_sync(mask, sum, q);
-            const float r = rsqrtf(fmaf(sum, p.inv_d, p.eps));
+        for (int i = 0; i < 8; ++i) dot = fma2(mul2(w[i], d[i]), f[i], dot);
+        float along = dot.x + dot.y;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = mul2(mul2(f[i], make_float2(r, r)), w[i]);
-            if (pl.rot) turn<PAIRS>(f, c, s);
-        } else {
-            float2 d[8], dot = make_float2(0.0f, 0.0f);
-            unpack(*ring.at(stage, 2), *ring.at(stage, 3), d);
-            if (pl.rot) turn<PAIRS>(d, c, s);
+        for (int q = G / 2; q > 0; q >>= 1) {
+            sum += __shfl_xor_sync(mask, sum, q);
+            along += __shfl_xor_sync(mask, along, q);
+        }
+        const float r = rsqrtf(fmaf(sum, p.inv_d, p.eps)), back = -along * p.inv_d * r * r;
+        const float2 r2 = make_float2(r, r), back2 = make_float2(back, back);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dot = fma2(mul2(w[i], d[i]), f[i], dot);
-            float along = dot.x + dot.y;
-#pragma unroll
-            for (int q = G / 2; q > 0; q >>= 1) {
-                sum += __shfl_xor_sync(mask, sum, q);
-                along += __shfl_xor_sync(mask, along, q);
-            }
-            const float r = rsqrtf(fmaf(sum, p.inv_d, p.eps)), back = -along * p.inv_d * r * r;
-            const float2 r2 = make_float2(r, r), back2 = make_float2(back, back);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (!gone) dw[i] = fma2(d[i], mul2(f[i], r2), dw[i]);
-                f[i] = mul2(fma2(f[i], back2, mul2(w[i], d[i])), r2);
-            }
+        for (int i = 0; i < 8; ++i) {
+            if (!gone) dw[i] = fma2(d[i], mul2(f[i], r2), dw[i]);
+            f[i] = mul2(fma2(f[i], back2, mul2(w[i], d[i])), r2);
         }
         if (pl.one && !gone) *reinterpret_cast<uint4*>(o + pl.c0) = pack4(f);
         if (pl.two && !gone) *reinterpret_cast<uint4*>(o + pl.c1) = pack4(f + 4);
         fill(stage);
         at.next(p, stride);
     }
-    if (!BWD) return;
     cp_async_wait<0>();
     const int other = 8 * kThreads;
 #pragma unroll
@@ -319,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) head_norm_kernel(const __gr
     }
     __syncthreads();
     // the block's sums, its groups in their order
-    const float2* all = reinterpret_cast<const float2*>(smem + kStages * R::kSlots * kThreads);
+    const float2* all = reinterpret_cast<const float2*>(smem + kStages * Ring::kSlots * kThreads);
     for (int e = threadIdx.x; e < 2 * p.units * 8; e += kThreads) {
         const int kind = e / (p.units * 8), unit = e / 8 % p.units, i = e % 8;
         if (kind == 1 && !p.hk) break;
@@ -329,6 +285,225 @@ __global__ void __launch_bounds__(kThreads, kBlocks) head_norm_kernel(const __gr
         for (int g = 0; g < kThreads / G; ++g) sum = add2(sum, all[kind * other + i * kThreads + g * G + unit]);
         const int ch = i < 4 ? q.c0 + 2 * i : q.c1 + 2 * (i - 4);
         *reinterpret_cast<float2*>(p.part + (static_cast<int64_t>(blockIdx.x) * 2 + kind) * p.D + ch) = sum;
+    }
+}
+
+// What a lane does with its 16 channels x1, x2 (pairs of pairs): r (a x1 + b x2) and
+// r (c x1 + d x2), weights and angles in one.
+struct Coefs {
+    float2 a[4], b[4], c[4], d[4];
+};
+
+// 16 channels as the first and the second of 8 pairs, two pairs to a float2.
+template <bool PAIRS>
+__device__ __forceinline__ void split(const uint4& p, const uint4& q, float2 (&x1)[4], float2 (&x2)[4]) {
+    const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (PAIRS) {
+            x1[i] = make_float2(bf16_lo(w[2 * i]), bf16_lo(w[2 * i + 1]));
+            x2[i] = make_float2(bf16_hi(w[2 * i]), bf16_hi(w[2 * i + 1]));
+        } else {
+            x1[i] = bf16x2_f32(w[i]);
+            x2[i] = bf16x2_f32(w[i + 4]);
+        }
+    }
+}
+
+template <bool PAIRS>
+__device__ __forceinline__ void join(const float2 (&y1)[4], const float2 (&y2)[4], uint4* p, uint4* q) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (PAIRS) {
+            w[2 * i] = pack_bf16x2(y1[i].x, y2[i].x);
+            w[2 * i + 1] = pack_bf16x2(y1[i].y, y2[i].y);
+        } else {
+            w[i] = pack_bf16x2(y1[i].x, y1[i].y);
+            w[i + 4] = pack_bf16x2(y2[i].x, y2[i].y);
+        }
+    }
+    *p = make_uint4(w[0], w[1], w[2], w[3]);
+    *q = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// A group's item: a run of a token's query heads, behind all of those a run of its key
+// heads.  The lane's first chunk of the run's first head, the elements between heads, the
+// heads left.
+struct Run {
+    int64_t item, step;
+    const uint16_t* x;
+    int left;
+    int64_t pos;   // asked for a row ahead of its use
+    template <bool OUT>
+    __device__ __forceinline__ void enter(const HeadParams& p, int c0) {
+        const bool keys = item >= p.q_items;
+        const int splits = keys ? p.k_splits : p.q_splits, each = keys ? p.k_each : p.q_each;
+        const int64_t i = keys ? item - p.q_items : item;
+        int part = 0;
+        int64_t t = i;
+        if (splits > 1) {
+            if (p.items < (1ll << 31)) {   // a 32-bit division where it does
+                const uint32_t q = static_cast<uint32_t>(i) / static_cast<uint32_t>(splits);
+                t = q;
+                part = static_cast<int>(static_cast<uint32_t>(i) - q * splits);
+            } else {
+                t = i / splits;
+                part = static_cast<int>(i - t * splits);
+            }
+        }
+        const int h = part * each, n = (keys ? p.hk : p.hq) - h;
+        const Rows& r = OUT ? (keys ? p.y_k : p.y_q) : (keys ? p.x_k : p.x_q);
+        left = n < each ? n : each;
+        step = r.h;
+        x = r.base + t * r.t + h * r.h + c0;
+        if (!OUT && p.table) pos = p.pos ? __ldg(p.pos + t) : t;
+    }
+};
+
+// One pass over the heads: the norms, turned.  Each lane copies the chunks, and with an
+// item's first row the angles, that it will read itself.
+template <bool PAIRS, int G>
+__global__ void __launch_bounds__(kThreads, kBlocks) head_norm_fwd_kernel(const __grid_constant__ HeadParams p) {
+    extern __shared__ __align__(16) uint4 smem[];
+    constexpr int N = kThreads, kSlots = 6;
+    const int lane = threadIdx.x & 31, u = lane & (G - 1);
+    const unsigned mask = (G == 32 ? 0xffffffffu : ((1u << G) - 1u)) << (lane & ~(G - 1));
+    const Place pl(p, u);
+    if (!moe_check((!pl.one || pl.c0 + 8 <= p.D) && (!pl.two || pl.c1 + 8 <= p.D), 1602)) return;
+    const int apart = pl.c1 - pl.c0;
+    uint4* const mine = smem + threadIdx.x;   // slot k of stage s: mine[(s * kSlots + k) * N]
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * (N / G);
+    Run in, at;   // what is copied next, what is worked on
+    // a warp's groups side by side, the CTAs' warps in turn: the last items go to all CTAs
+    in.item = at.item = (static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x) * (32 / G) + lane / G;
+    if (in.item >= p.items) return;
+    in.enter<false>(p, pl.c0);
+    at.enter<true>(p, pl.c0);
+    bool fresh = true, more = true;   // what is copied next begins an item; there is something
+    uint32_t skip = 0;                // bit s: stage s begins an item without a place
+    auto fill = [&](int stage) {
+        if (more) {
+            uint4* to = mine + stage * (kSlots * N);
+            if (pl.one) cp_async_16(smem_u32(to), in.x, 16);
+            if (pl.two) cp_async_16(smem_u32(to + N), in.x + apart, 16);
+            if (fresh && p.table) {
+                const int64_t pos = in.pos;
+                skip &= ~(1u << stage);
+                if (pos < 0 || pos >= p.table_rows) {
+                    report_error(p.status, MOE_EINVAL);
+                    skip |= 1u << stage;
+                } else if (pl.rot) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) cp_async_16(smem_u32(to + (2 + e) * N), angle<PAIRS>(p, pos, u, e), 16);
+                }
+            }
+            in.x += in.step;
+            fresh = --in.left == 0;
+            if (fresh) {
+                in.item += stride;
+                more = in.item < p.items;
+                if (more) in.enter<false>(p, pl.c0);
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)   // chunks that a head does not have
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (!(k ? pl.two : pl.one)) mine[(i * kSlots + k) * N] = make_uint4(0, 0, 0, 0);
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    uint4 wa, wb;
+    auto weights = [&](bool keys) {
+        const uint16_t* w = keys ? p.w_k : p.w_q;
+        wa = pl.one ? __ldg(reinterpret_cast<const uint4*>(w + pl.c0)) : none;
+        wb = pl.two ? __ldg(reinterpret_cast<const uint4*>(w + pl.c1)) : none;
+    };
+    bool keys = at.item >= p.q_items, gone = false;
+    weights(keys);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fill(i);
+    Coefs k;
+    bool first = true;
+    for (int stage = 0;; stage = stage + 1 == kAhead ? 0 : stage + 1) {
+        cp_async_wait<kAhead - 1>();
+        const uint4* from = mine + stage * (kSlots * N);
+        if (first) {
+            gone = skip >> stage & 1;
+            float2 w1[4], w2[4];
+            split<PAIRS>(wa, wb, w1, w2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (pl.rot) {
+                    const float4 v = *reinterpret_cast<const float4*>(from + (2 + e) * N);
+                    const float2 c = make_float2(v.x, v.z), s = make_float2(v.y, v.w);
+                    k.a[e] = mul2(w1[e], c);
+                    k.b[e] = mul2(w2[e], make_float2(-s.x, -s.y));
+                    k.c[e] = mul2(w1[e], s);
+                    k.d[e] = mul2(w2[e], c);
+                } else {
+                    k.a[e] = w1[e];
+                    k.d[e] = w2[e];
+                }
+            }
+        }
+        float2 x1[4], x2[4], ss = make_float2(0.0f, 0.0f);
+        split<PAIRS>(from[0], from[N], x1, x2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ss = fma2(x1[i], x1[i], fma2(x2[i], x2[i], ss));
+        float sum = ss.x + ss.y;
+#pragma unroll
+        for (int q = G / 2; q > 0; q >>= 1) sum += __shfl_xor_sync(mask, sum, q);
+        const float r = rsqrtf(fmaf(sum, p.inv_d, p.eps));
+        const float2 r2 = make_float2(r, r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 z1 = mul2(x1[i], r2), z2 = mul2(x2[i], r2);
+            if (pl.rot) {
+                x1[i] = fma2(z1, k.a[i], mul2(z2, k.b[i]));
+                x2[i] = fma2(z1, k.c[i], mul2(z2, k.d[i]));
+            } else {
+                x1[i] = mul2(z1, k.a[i]);
+                x2[i] = mul2(z2, k.d[i]);
+            }
+        }
+        uint4 ya, yb;
+        join<PAIRS>(x1, x2, &ya, &yb);
+        uint16_t* o = const_cast<uint16_t*>(at.x);
+        if (pl.one && !gone) *reinterpret_cast<uint4*>(o) = ya;
+        if (pl.two && !gone) *reinterpret_cast<uint4*>(o + apart) = yb;
+        fill(stage);
+        at.x += at.step;
+        first = --at.left == 0;
+        if (first) {
+            at.item += stride;
+            if (at.item >= p.items) return;
+            at.enter<true>(p, pl.c0);
+            if (!keys && at.item >= p.q_items) {
+                keys = true;
+                weights(true);
+            }
+        }
+    }
+}
+
+template <bool PAIRS, int G>
+int begin_forward(const HeadParams& p, int sms, cudaStream_t st) {
+    constexpr int kBytes = kAhead * 6 * kThreads * 16;
+    const auto kern = head_norm_fwd_kernel<PAIRS, G>;
+    if (const int rc = ensure_smem_attr(reinterpret_cast<const void*>(kern), kBytes)) return rc;
+    const int64_t need = (p.items * G + kThreads - 1) / kThreads, most = static_cast<int64_t>(sms) * kBlocks;
+    kern<<<static_cast<unsigned>(need < most ? need : most), kThreads, kBytes, st>>>(p);
+    return cudaPeekAtLastError() == cudaSuccess ? MOE_OK : MOE_ECUDA;
+}
+
+int begin_forward_any(const HeadParams& p, bool pairs, int lanes, int sms, cudaStream_t st) {
+    switch (lanes) {
+        case 4: return pairs ? begin_forward<true, 4>(p, sms, st) : begin_forward<false, 4>(p, sms, st);
+        case 8: return pairs ? begin_forward<true, 8>(p, sms, st) : begin_forward<false, 8>(p, sms, st);
+        case 16: return pairs ? begin_forward<true, 16>(p, sms, st) : begin_forward<false, 16>(p, sms, st);
+        default: return pairs ? begin_forward<true, 32>(p, sms, st) : begin_forward<false, 32>(p, sms, st);
     }
 }
 
@@ -373,13 +548,13 @@ HeadParams head_params(const moe_head_norm_t& c) {
 int lanes_of(int units) { return units <= 4 ? 4 : units <= 8 ? 8 : units <= 16 ? 16 : 32; }
 
 // The heads of a token are split over several groups of lanes until four items fall to
-// each resident group, down to four heads an item (8192 tokens of 20 heads: 21.3 us; one
-// head an item 28.3, eight 20.0, where the gradient takes 33.8 instead of 32.3); to one
-// head where all heads are under way at once.
+// each resident group, down to eight heads an item (8192 tokens of 20 heads: 18.0 us, four
+// heads an item 19.9, sixteen 17.4; the gradient 31.8, 32.4, 31.6, but of 4096 tokens 13.9,
+// 15.1, 18.2); to one head where all heads are under way at once.
 void head_splits(HeadParams* p, int lanes, int sms) {
     const int64_t have = p->T * lanes, room = static_cast<int64_t>(sms) * kBlocks * kThreads;
     const int64_t want = (4 * room + have - 1) / have, heads = p->hq + p->hk;
-    const int least = have * heads <= room ? 1 : 4;
+    const int least = have * heads <= room ? 1 : 8;
     auto part = [&](int n) {   // the kind's share of the groups
         int64_t s = (want * n + heads - 1) / heads;
         const int64_t most = (n + least - 1) / least;
@@ -388,32 +563,33 @@ void head_splits(HeadParams* p, int lanes, int sms) {
     };
     p->q_splits = part(p->hq);
     p->k_splits = part(p->hk);
+    p->q_each = (p->hq + p->q_splits - 1) / p->q_splits;
+    p->k_each = p->hk ? (p->hk + p->k_splits - 1) / p->k_splits : 0;
     p->q_items = p->T * p->q_splits;
     p->items = p->q_items + p->T * p->k_splits;
 }
 
 constexpr int kMaxParts = kBlocks * 160;   // blocks of a backward launch, on a device of 160 SMs at most
 
-template <bool PAIRS, int G, bool BWD>
-int start(const HeadParams& p, int sms, int* grid, cudaStream_t st) {
-    constexpr int kBytes = kStages * Ring<PAIRS, G, BWD>::kSlots * kThreads * 16 + (BWD ? kThreads * 128 : 0);
-    const auto kern = head_norm_kernel<PAIRS, G, BWD>;
+template <bool PAIRS, int G>
+int begin_backward(const HeadParams& p, int sms, int* grid, cudaStream_t st) {
+    constexpr int kBytes = kStages * Ring::kSlots * kThreads * 16 + kThreads * 128;
+    const auto kern = head_norm_bwd_kernel<PAIRS, G>;
     if (const int rc = ensure_smem_attr(reinterpret_cast<const void*>(kern), kBytes)) return rc;
     const int64_t need = (p.items * G + kThreads - 1) / kThreads;
     int64_t most = static_cast<int64_t>(sms) * kBlocks;
-    if (BWD && most > kMaxParts) most = kMaxParts;
+    if (most > kMaxParts) most = kMaxParts;
     *grid = static_cast<int>(need < most ? need : most);
     kern<<<*grid, kThreads, kBytes, st>>>(p);
     return cudaPeekAtLastError() == cudaSuccess ? MOE_OK : MOE_ECUDA;
 }
 
-template <bool BWD>
-int start_any(const HeadParams& p, bool pairs, int lanes, int sms, int* grid, cudaStream_t st) {
+int begin_backward_any(const HeadParams& p, bool pairs, int lanes, int sms, int* grid, cudaStream_t st) {
     switch (lanes) {
-        case 4: return pairs ? start<true, 4, BWD>(p, sms, grid, st) : start<false, 4, BWD>(p, sms, grid, st);
-        case 8: return pairs ? start<true, 8, BWD>(p, sms, grid, st) : start<false, 8, BWD>(p, sms, grid, st);
-        case 16: return pairs ? start<true, 16, BWD>(p, sms, grid, st) : start<false, 16, BWD>(p, sms, grid, st);
-        default: return pairs ? start<true, 32, BWD>(p, sms, grid, st) : start<false, 32, BWD>(p, sms, grid, st);
+        case 4: return pairs ? begin_backward<true, 4>(p, sms, grid, st) : begin_backward<false, 4>(p, sms, grid, st);
+        case 8: return pairs ? begin_backward<true, 8>(p, sms, grid, st) : begin_backward<false, 8>(p, sms, grid, st);
+        case 16: return pairs ? begin_backward<true, 16>(p, sms, grid, st) : begin_backward<false, 16>(p, sms, grid, st);
+        default: return pairs ? begin_backward<true, 32>(p, sms, grid, st) : begin_backward<false, 32>(p, sms, grid, st);
     }
 }
 
@@ -441,8 +617,7 @@ int launch_head_norm(const moe_head_norm_t& c, const uint16_t* q, const uint16_t
     p.status = status;
     const int lanes = lanes_of(p.units);
     head_splits(&p, lanes, sms);
-    int grid = 0;
-    if (const int rc = start_any<false>(p, c.interleaved, lanes, sms, &grid, st)) return rc;
+    if (const int rc = begin_forward_any(p, c.interleaved, lanes, sms, st)) return rc;
     trace_after(st, "head_norm_rotary");
     return MOE_OK;
 }
@@ -470,7 +645,7 @@ int launch_head_norm_backward(const moe_head_norm_t& c, const uint16_t* dq, cons
     const int lanes = lanes_of(p.units);
     head_splits(&p, lanes, sms);
     int grid = 0;
-    if (const int rc = start_any<true>(p, c.interleaved, lanes, sms, &grid, st)) return rc;
+    if (const int rc = begin_backward_any(p, c.interleaved, lanes, sms, &grid, st)) return rc;
     trace_after(st, "head_norm_rotary_bwd");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((2 * c.D + 31) / 32, 1, 1);
