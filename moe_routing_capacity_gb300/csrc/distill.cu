@@ -17,6 +17,7 @@
 // and drained by bulk copies, moved nothing twice and took 950: a CTA's two passes and the
 // meeting between them follow each other, and only one fits on an SM.
 #include "common.cuh"
+#include "early.cuh"
 #include "internal.h"
 
 namespace moe {
@@ -223,6 +224,7 @@ __global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM + 32, BLOCKS) distill_
     extern __shared__ __align__(16) uint4 stash[];   // and behind it the entries' arrays
     __shared__ float s_red[TEAM == 32 ? 1 : TEAM / 16];
     __shared__ int s_none;
+    wait_earlier();
     const int which = TEAM == 32 ? static_cast<int>(threadIdx.x >> 5) : 0;
     Team<TEAM> team{static_cast<int>(TEAM == 32 ? threadIdx.x & 31 : threadIdx.x), s_red};
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + which;
@@ -391,7 +393,7 @@ __global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM + 32, BLOCKS) distill_
 __global__ void __launch_bounds__(1024) distill_total_kernel(const float* loss, int64_t T,
                                                              float* total) {
     __shared__ float red[32];
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // the losses are complete
+    wait_earlier();   // the losses are complete
     float s = 0.0f;
     for (int64_t t = threadIdx.x; t < T; t += 1024) s += __ldcg(loss + t);   // past L1, as it started early
 #pragma unroll
@@ -414,8 +416,7 @@ int start_team(const DistillParams& p, cudaStream_t st) {
     const int most = STASH * TEAM * 16 + (TEAM == 32 ? 8 : 1) * 5 * 4 * kMaxEntries;
     const int bytes = STASH * TEAM * 16 + (TEAM == 32 ? 8 : 1) * 5 * 4 * ((p.K + 3) / 4 * 4);
     if (const int rc = ensure_smem_attr(reinterpret_cast<const void*>(kern), most)) return rc;
-    kern<<<static_cast<unsigned>(grid), TEAM == 32 ? 256 : TEAM + 32, bytes, st>>>(p);
-    return cudaPeekAtLastError() == cudaSuccess ? MOE_OK : MOE_ECUDA;
+    return launch_early(kern, grid, TEAM == 32 ? 256 : TEAM + 32, static_cast<size_t>(bytes), st, p);
 }
 
 template <typename Z, int MODE>
@@ -475,18 +476,7 @@ int launch_distill(const moe_distill_t& c, const void* z, const int32_t* ids, co
     if (rc) return rc;
     trace_after(st, "distill");
     if (!total) return MOE_OK;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(1, 1, 1);
-    cfg.blockDim = dim3(1024, 1, 1);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, distill_total_kernel, static_cast<const float*>(loss), c.T,
-                           total) != cudaSuccess)
-        return MOE_ECUDA;
+    if (const int rc = launch_early(distill_total_kernel, 1, 1024, 0, st, loss, c.T, total)) return rc;
     trace_after(st, "distill_total");
     return MOE_OK;
 }

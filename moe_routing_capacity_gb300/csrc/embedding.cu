@@ -13,6 +13,7 @@
 // 50001 x 2048 from 8191 tokens with the plan: 58 us (floor 35), 12 of them the plan's four
 // launches and 4.5 the joins'.  Lookup of 16384 rows of 6144 fp32 to bf16: 47.5 us.
 #include "common.cuh"
+#include "early.cuh"
 #include "internal.h"
 
 namespace moe {
@@ -38,7 +39,7 @@ struct Chunk;
 template <>
 struct Chunk<uint16_t> {
     uint4 v;
-    __device__ __forceinline__ void load(const uint16_t* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void spread(float (&f)[8]) const {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -52,8 +53,8 @@ template <>
 struct Chunk<float> {
     float4 a, b;
     __device__ __forceinline__ void load(const float* p) {
-        a = __ldg(reinterpret_cast<const float4*>(p));
-        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        a = *reinterpret_cast<const float4*>(p);
+        b = reinterpret_cast<const float4*>(p)[1];
     }
     __device__ __forceinline__ void spread(float (&f)[8]) const {
         f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
@@ -81,6 +82,7 @@ constexpr int kLook = 4;   // chunks that a thread has under way
 
 template <typename Tab, typename Out>
 __global__ void __launch_bounds__(256) embedding_kernel(const LookupParams p) {
+    wait_earlier();
     const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 256 * kLook + threadIdx.x;
     Chunk<Tab> c[kLook];
     bool there[kLook];
@@ -90,7 +92,7 @@ __global__ void __launch_bounds__(256) embedding_kernel(const LookupParams p) {
         there[j] = false;
         if (i >= p.total) continue;
         const int64_t t = i / p.chunks;
-        const int id = __ldg(p.ids + t);
+        const int id = p.ids[t];
         there[j] = id >= 0 && id < p.V;
         if (there[j])
             c[j].load(static_cast<const Tab*>(p.table) + (id * static_cast<int64_t>(p.chunks) + (i - t * p.chunks)) * 8);
@@ -176,8 +178,9 @@ __device__ __forceinline__ int warp_before(int v) {
 // once for all of them (16384 tokens of one word: 36 -> 31 us).
 __global__ void __launch_bounds__(kPlanThreads) embedding_count_kernel(const PlanView v, const int32_t* ids,
                                                                        int64_t T, int64_t V, int32_t* status) {
+    wait_earlier();
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x;
-    const int id = t < T ? __ldg(ids + t) : -1;
+    const int id = t < T ? ids[t] : -1;
     const bool in = id >= 0 && id < V;
     if (!in && id != -1) report_error(status, MOE_EINVAL);
     const int lane = threadIdx.x & 31;
@@ -194,11 +197,11 @@ __global__ void __launch_bounds__(kPlanThreads) embedding_pieces_kernel(const Pl
                                                                         int64_t T) {
     constexpr int W = kPlanThreads / 32;
     __shared__ int sums[3][W], first[3];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_earlier();
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x;
     const bool mine = t < T && __ldcg(v.rank + t) == 0;
-    const int id = mine ? __ldg(ids + t) : 0;
+    const int id = mine ? ids[t] : 0;
     const int n = mine ? __ldcg(v.count + id) : 0, np = (n + kPiece - 1) / kPiece, rows = np > 1 ? np : 0;
     int at = warp_before(n), pc = warp_before(np), row = warp_before(rows);
     if (lane == 31) {
@@ -230,8 +233,8 @@ __global__ void __launch_bounds__(kPlanThreads) embedding_pieces_kernel(const Pl
 __global__ void __launch_bounds__(kPlanThreads) embedding_place_kernel(const PlanView v, const int32_t* ids,
                                                                        int64_t T) {
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x;
-    const int id = t < T ? __ldg(ids + t) : -1;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_earlier();
+    const int id = t < T ? ids[t] : -1;
     const int r = t < T ? __ldcg(v.rank + t) : -1;
     if (r < 0) return;
     const int at = __ldcg(v.start + id) + r;
@@ -250,7 +253,7 @@ __global__ void __launch_bounds__(kPlanThreads) embedding_place_kernel(const Pla
 __global__ void __launch_bounds__(kPlanThreads) embedding_order_kernel(const PlanView v, int64_t T) {
     extern __shared__ __align__(16) uint32_t bits[];
     __shared__ int sums[kPlanThreads / 32];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_earlier();
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int longs = __ldcg(v.head + 3);
     const int64_t window = T < kWindow ? T : kWindow;
@@ -342,7 +345,7 @@ __device__ __forceinline__ void finish(const GradParams& p, Tab* row, int c, flo
 // The lane's token of a piece; the largest number behind the last.
 __device__ __forceinline__ int piece_token(const GradParams& p, const int4& q) {
     const int lane = threadIdx.x & 31;
-    return lane < q.z ? __ldg((q.w < 0 ? p.v.mixed : p.v.order) + q.y + lane) : 0x7fffffff;
+    return lane < q.z ? (q.w < 0 ? p.v.mixed : p.v.order)[q.y + lane] : 0x7fffffff;
 }
 
 // One piece's sum over 512 channels.
@@ -410,6 +413,9 @@ __global__ void __launch_bounds__(256, 3) embedding_bwd_kernel(const GradParams 
         for (int i = threadIdx.x; i < kZeros / 16; i += 256) zeros[i] = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncthreads();
+    }
+    wait_earlier();
+    if (!p.accumulate) {
         if (wid == adders) {
             const int64_t bytes = p.d * static_cast<int64_t>(sizeof(Tab));
             // short rows side by side, 32 a time, long ones from all CTAs in turn (131072 rows of
@@ -418,7 +424,7 @@ __global__ void __launch_bounds__(256, 3) embedding_bwd_kernel(const GradParams 
             const int64_t runs = (p.V + (1 << log_run) - 1) >> log_run;
             for (int64_t k = lane; (k >> log_run) * gridDim.x + blockIdx.x < runs; k += 32) {
                 const int64_t id = (((k >> log_run) * gridDim.x + blockIdx.x) << log_run) + (k & ((1 << log_run) - 1));
-                if (id >= p.V || __ldg(p.v.count + id) != 0) continue;
+                if (id >= p.V || p.v.count[id] != 0) continue;
                 uint8_t* row = static_cast<uint8_t*>(p.dtable) + id * bytes;
                 for (int64_t o = 0; o < bytes; o += kZeros)
                     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(row + o),
@@ -435,14 +441,14 @@ __global__ void __launch_bounds__(256, 3) embedding_bwd_kernel(const GradParams 
     const int64_t items = static_cast<int64_t>(p.v.head[1]) * p.spans;
     int64_t it = static_cast<int64_t>(wid) * gridDim.x + blockIdx.x;
     if (it >= items) return;
-    int4 q = __ldg(p.v.pieces + it / p.spans);
+    int4 q = p.v.pieces[it / p.spans];
     int t = piece_token(p, q);
     while (true) {
         const int64_t then = it + warps;
         int4 q2 = q;
         int t2 = t;
         if (then < items) {
-            q2 = __ldg(p.v.pieces + then / p.spans);
+            q2 = p.v.pieces[then / p.spans];
             t2 = piece_token(p, q2);
         }
         if (moe_check(q.x >= 0 && q.x < p.V && q.y + q.z <= p.T && q.z <= kPiece, 1628))
@@ -458,14 +464,14 @@ __global__ void __launch_bounds__(256, 3) embedding_bwd_kernel(const GradParams 
 template <typename Tab>
 __global__ void __launch_bounds__(256) embedding_join_kernel(const GradParams p) {
     __shared__ float red[8][32][8];
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // the pieces' sums are complete
+    wait_earlier();   // the pieces' sums are complete
     const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
     const int wide = (p.chunks + 31) / 32;
     const int64_t items = static_cast<int64_t>(p.v.head[3]) * wide;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const int64_t w = it / wide;
         const int c = static_cast<int>(it - w * wide) * 32 + lane;
-        const int4 q = __ldg(p.v.joins + w);
+        const int4 q = p.v.joins[w];
         float s[8] = {};
         if (c < p.chunks)
 #pragma unroll 8
@@ -514,8 +520,7 @@ int launch_embedding(const moe_embedding_t& c, const void* table, const int32_t*
     void (*kern)(LookupParams) =
         c.table_f32 ? (c.out_f32 ? embedding_kernel<float, float> : embedding_kernel<float, uint16_t>)
                     : (c.out_f32 ? embedding_kernel<uint16_t, float> : embedding_kernel<uint16_t, uint16_t>);
-    kern<<<static_cast<unsigned>(grid), 256, 0, st>>>(p);
-    if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
+    if (const int rc = launch_early(kern, grid, 256, 0, st, p)) return rc;
     trace_after(st, "embedding");
     return MOE_OK;
 }
@@ -528,32 +533,17 @@ int launch_embedding_plan(int64_t T, int64_t V, int d, const int32_t* ids, void*
     if (const int rc = current_device(&dev, &sms)) return rc;
     const int64_t counters = reinterpret_cast<uint8_t*>(v.count + V) - reinterpret_cast<uint8_t*>(v.head);
     if (cudaMemsetAsync(v.head, 0, counters, st) != cudaSuccess) return MOE_ECUDA;
-    const unsigned grid = static_cast<unsigned>((T + kPlanThreads - 1) / kPlanThreads);
-    embedding_count_kernel<<<grid, kPlanThreads, 0, st>>>(v, ids, T, V, status);
-    if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
+    const int64_t grid = (T + kPlanThreads - 1) / kPlanThreads;
+    if (const int rc = launch_early(embedding_count_kernel, grid, kPlanThreads, 0, st, v, ids, T, V, status)) return rc;
     trace_after(st, "embedding_count");
-    // each launched while the one before it still runs; it waits for it
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(kPlanThreads, 1, 1);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, embedding_pieces_kernel, static_cast<const PlanView>(v), ids, T) != cudaSuccess)
-        return MOE_ECUDA;
+    if (const int rc = launch_early(embedding_pieces_kernel, grid, kPlanThreads, 0, st, v, ids, T)) return rc;
     trace_after(st, "embedding_pieces");
-    if (cudaLaunchKernelEx(&cfg, embedding_place_kernel, static_cast<const PlanView>(v), ids, T) != cudaSuccess)
-        return MOE_ECUDA;
+    if (const int rc = launch_early(embedding_place_kernel, grid, kPlanThreads, 0, st, v, ids, T)) return rc;
     trace_after(st, "embedding_place");
     if (T <= kPiece) return MOE_OK;   // no word has several pieces
-    const int64_t most = T / (kPiece + 1);
-    cfg.gridDim = dim3(static_cast<unsigned>(most < 4 * sms ? (most ? most : 1) : 4 * sms), 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(((T < kWindow ? T : kWindow) + 127) / 128 * 16);   // at most 32 KB
-    if (cudaLaunchKernelEx(&cfg, embedding_order_kernel, static_cast<const PlanView>(v), T) != cudaSuccess)
-        return MOE_ECUDA;
+    const int64_t most = T / (kPiece + 1), ctas = most < 4 * sms ? (most ? most : 1) : 4 * sms;
+    const size_t bits = static_cast<size_t>(((T < kWindow ? T : kWindow) + 127) / 128 * 16);   // at most 32 KB
+    if (const int rc = launch_early(embedding_order_kernel, ctas, kPlanThreads, bits, st, v, T)) return rc;
     trace_after(st, "embedding_order");
     return MOE_OK;
 }
@@ -583,22 +573,12 @@ int launch_embedding_backward(const moe_embedding_t& c, const void* plan, const 
     void (*kern)(GradParams) =
         c.out_f32 ? (c.table_f32 ? embedding_bwd_kernel<float, float> : embedding_bwd_kernel<float, uint16_t>)
                   : (c.table_f32 ? embedding_bwd_kernel<uint16_t, float> : embedding_bwd_kernel<uint16_t, uint16_t>);
-    kern<<<grid, 256, 0, st>>>(p);
-    if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
+    if (const int rc = launch_early(kern, grid, 256, 0, st, p)) return rc;
     trace_after(st, "embedding_bwd");
     if (c.T <= kPiece) return MOE_OK;   // no word has several pieces
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(sms) * 2, 1, 1);
-    cfg.blockDim = dim3(256, 1, 1);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = c.table_f32 ? cudaLaunchKernelEx(&cfg, embedding_join_kernel<float>, p)
-                                      : cudaLaunchKernelEx(&cfg, embedding_join_kernel<uint16_t>, p);
-    if (e != cudaSuccess) return MOE_ECUDA;
+    if (const int rc = launch_early(c.table_f32 ? embedding_join_kernel<float> : embedding_join_kernel<uint16_t>,
+                                    int64_t{2} * sms, 256, 0, st, p))
+        return rc;
     trace_after(st, "embedding_join");
     return MOE_OK;
 }

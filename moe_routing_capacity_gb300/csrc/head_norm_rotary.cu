@@ -19,6 +19,7 @@
 //   Backward, 65536 x (48 + 8) x 128: 440 us, floor 415, 6.4 TB/s: memory.  8192 x (16 + 4):
 // 31.8, floor 18.5.  The forward's stepped pointers would spill here (492 and 34).
 #include "common.cuh"
+#include "early.cuh"
 #include "internal.h"
 
 namespace moe {
@@ -108,7 +109,7 @@ __device__ __forceinline__ void load_angles(const HeadParams& p, int64_t pos, in
                                             float2 (&c)[4], float2 (&s)[4]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(angle<PAIRS>(p, pos, u, e)));
+        const float4 v = *reinterpret_cast<const float4*>(angle<PAIRS>(p, pos, u, e));
         c[e] = make_float2(v.x, v.z);
         s[e] = make_float2(sign * v.y, sign * v.w);
     }
@@ -172,14 +173,15 @@ struct Ring {
 __device__ __forceinline__ void load_weights(const uint16_t* w, int c0, int c1, bool one, bool two,
                                              float2 (&f)[8]) {
     const uint4 none = make_uint4(0, 0, 0, 0);
-    unpack(one ? __ldg(reinterpret_cast<const uint4*>(w + c0)) : none,
-           two ? __ldg(reinterpret_cast<const uint4*>(w + c1)) : none, f);
+    unpack(one ? *reinterpret_cast<const uint4*>(w + c0) : none,
+           two ? *reinterpret_cast<const uint4*>(w + c1) : none, f);
 }
 
 // One pass over the heads: the gradients, and the block's part of dw.
 template <bool PAIRS, int G>
 __global__ void __launch_bounds__(kThreads, kBlocks) head_norm_bwd_kernel(const __grid_constant__ HeadParams p) {
     extern __shared__ __align__(16) uint4 smem[];
+    wait_earlier();
     const int lane = threadIdx.x & 31, u = lane & (G - 1), group = threadIdx.x / G;
     const unsigned mask = (G == 32 ? 0xffffffffu : ((1u << G) - 1u)) << (lane & ~(G - 1));
     const Place pl(p, u);
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) head_norm_bwd_kernel(const 
             mine = true;
         }
         if (at.first && p.table) {
-            const int64_t pos = p.pos ? __ldg(p.pos + at.t) : at.t;
+            const int64_t pos = p.pos ? p.pos[at.t] : at.t;
             gone = pos < 0 || pos >= p.table_rows;
             if (gone)
                 report_error(p.status, MOE_EINVAL);
@@ -357,7 +359,7 @@ struct Run {
         left = n < each ? n : each;
         step = r.h;
         x = r.base + t * r.t + h * r.h + c0;
-        if (!OUT && p.table) pos = p.pos ? __ldg(p.pos + t) : t;
+        if (!OUT && p.table) pos = p.pos ? p.pos[t] : t;
     }
 };
 
@@ -366,6 +368,7 @@ struct Run {
 template <bool PAIRS, int G>
 __global__ void __launch_bounds__(kThreads, kBlocks) head_norm_fwd_kernel(const __grid_constant__ HeadParams p) {
     extern __shared__ __align__(16) uint4 smem[];
+    wait_earlier();
     constexpr int N = kThreads, kSlots = 6;
     const int lane = threadIdx.x & 31, u = lane & (G - 1);
     const unsigned mask = (G == 32 ? 0xffffffffu : ((1u << G) - 1u)) << (lane & ~(G - 1));
@@ -417,8 +420,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) head_norm_fwd_kernel(const 
     uint4 wa, wb;
     auto weights = [&](bool keys) {
         const uint16_t* w = keys ? p.w_k : p.w_q;
-        wa = pl.one ? __ldg(reinterpret_cast<const uint4*>(w + pl.c0)) : none;
-        wb = pl.two ? __ldg(reinterpret_cast<const uint4*>(w + pl.c1)) : none;
+        wa = pl.one ? *reinterpret_cast<const uint4*>(w + pl.c0) : none;
+        wb = pl.two ? *reinterpret_cast<const uint4*>(w + pl.c1) : none;
     };
     bool keys = at.item >= p.q_items, gone = false;
     weights(keys);
@@ -494,8 +497,7 @@ int begin_forward(const HeadParams& p, int sms, cudaStream_t st) {
     const auto kern = head_norm_fwd_kernel<PAIRS, G>;
     if (const int rc = ensure_smem_attr(reinterpret_cast<const void*>(kern), kBytes)) return rc;
     const int64_t need = (p.items * G + kThreads - 1) / kThreads, most = static_cast<int64_t>(sms) * kBlocks;
-    kern<<<static_cast<unsigned>(need < most ? need : most), kThreads, kBytes, st>>>(p);
-    return cudaPeekAtLastError() == cudaSuccess ? MOE_OK : MOE_ECUDA;
+    return launch_early(kern, need < most ? need : most, kThreads, kBytes, st, p);
 }
 
 int begin_forward_any(const HeadParams& p, bool pairs, int lanes, int sms, cudaStream_t st) {
@@ -511,7 +513,7 @@ int begin_forward_any(const HeadParams& p, bool pairs, int lanes, int sms, cudaS
 __global__ void __launch_bounds__(1024) head_norm_sums_kernel(const float* part, int blocks, int D,
                                                               float* dw_q, float* dw_k) {
     __shared__ float red[32][33];
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // the partials are complete
+    wait_earlier();   // the partials are complete
     const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float s = 0.0f;
@@ -580,8 +582,7 @@ int begin_backward(const HeadParams& p, int sms, int* grid, cudaStream_t st) {
     int64_t most = static_cast<int64_t>(sms) * kBlocks;
     if (most > kMaxParts) most = kMaxParts;
     *grid = static_cast<int>(need < most ? need : most);
-    kern<<<*grid, kThreads, kBytes, st>>>(p);
-    return cudaPeekAtLastError() == cudaSuccess ? MOE_OK : MOE_ECUDA;
+    return launch_early(kern, *grid, kThreads, kBytes, st, p);
 }
 
 int begin_backward_any(const HeadParams& p, bool pairs, int lanes, int sms, int* grid, cudaStream_t st) {
@@ -647,18 +648,9 @@ int launch_head_norm_backward(const moe_head_norm_t& c, const uint16_t* dq, cons
     int grid = 0;
     if (const int rc = begin_backward_any(p, c.interleaved, lanes, sms, &grid, st)) return rc;
     trace_after(st, "head_norm_rotary_bwd");
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((2 * c.D + 31) / 32, 1, 1);
-    cfg.blockDim = dim3(1024, 1, 1);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, head_norm_sums_kernel, static_cast<const float*>(p.part), grid,
-                           c.D, dw_q, dw_k) != cudaSuccess)
-        return MOE_ECUDA;
+    if (const int rc = launch_early(head_norm_sums_kernel, (2 * c.D + 31) / 32, 1024, 0, st, p.part,
+                                    grid, c.D, dw_q, dw_k))
+        return rc;
     trace_after(st, "head_norm_rotary_sums");
     return MOE_OK;
 }

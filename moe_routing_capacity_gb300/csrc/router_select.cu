@@ -16,6 +16,7 @@
 //   Gradient, 65536 x 384 in bf16, softmax of the row: 25.0 us, 22.9 of them memory's (the
 // logits in, the gradient out); the chosen ones looked up behind the row, 31.5.
 #include "common.cuh"
+#include "early.cuh"
 #include "internal.h"
 
 namespace moe {
@@ -82,10 +83,10 @@ __device__ __forceinline__ void load(float (&v)[PER], const float* from, const E
     for (int i = 0; i < PER; i += U) {
         if constexpr (U == 4) {
             float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-            if (at.has(i)) q = __ldg(reinterpret_cast<const float4*>(from + at.expert(i)));
+            if (at.has(i)) q = *reinterpret_cast<const float4*>(from + at.expert(i));
             v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
         } else {
-            v[i] = at.has(i) ? __ldg(from + at.expert(i)) : -INFINITY;
+            v[i] = at.has(i) ? from[at.expert(i)] : -INFINITY;
         }
     }
 }
@@ -104,7 +105,7 @@ __device__ __noinline__ int choose64(const SelectParams& p, int64_t t) {
     const int lane = threadIdx.x & 31, grp = lane >> p.log_lanes, sub = lane & (p.lanes - 1);
     const float* row = p.logits + t * p.E;
     const Entries<U> at(p, grp, sub);
-    const float l0 = __ldg(row);
+    const float l0 = *row;
     bool same = true, even = true;
     uint32_t open = 0;   // entries that may still be chosen
     float m = -INFINITY;
@@ -112,9 +113,9 @@ __device__ __noinline__ int choose64(const SelectParams& p, int64_t t) {
     for (int i = 0; i < PER; ++i) {
         if (!at.has(i)) continue;
         open |= 1u << i;
-        const float l = __ldg(row + at.expert(i));
+        const float l = row[at.expert(i)];
         same = same && l == l0;
-        even = even && (!p.bias || __ldg(p.bias + at.expert(i)) == __ldg(p.bias));
+        even = even && (!p.bias || p.bias[at.expert(i)] == *p.bias);
         m = fmaxf(m, l);
     }
     same = __all_sync(kAll, same);
@@ -124,7 +125,7 @@ __device__ __noinline__ int choose64(const SelectParams& p, int64_t t) {
     if (p.softmax && !same) {
         sum = 0;
         for (int i = 0; i < PER; ++i)
-            if (open >> i & 1) sum += exp(static_cast<double>(__ldg(row + at.expert(i))) - m);
+            if (open >> i & 1) sum += exp(static_cast<double>(row[at.expert(i)]) - m);
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
     }
     long long key[PER], k1 = order_key64(-INFINITY), k2 = k1;
@@ -132,9 +133,9 @@ __device__ __noinline__ int choose64(const SelectParams& p, int64_t t) {
     for (int i = 0; i < PER; ++i) {
         key[i] = 0;
         if (!(open >> i & 1)) continue;
-        const double l = __ldg(row + at.expert(i));
+        const double l = row[at.expert(i)];
         double x = same ? 0 : p.softmax ? exp(l - m) / sum : 1 / (1 + exp(-l));
-        if (p.bias) x += __ldg(p.bias + at.expert(i));
+        if (p.bias) x += p.bias[at.expert(i)];
         key[i] = order_key64(x);
         if (key[i] > k1) {
             k2 = k1; b2 = b1;
@@ -201,12 +202,12 @@ __device__ __noinline__ double row_sum64(const SelectParams& p, int64_t t, float
     const Entries<U> at(p, grp, sub);
     float m = -INFINITY;
     for (int i = 0; i < PER; ++i)
-        if (at.has(i)) m = fmaxf(m, __ldg(row + at.expert(i)));
+        if (at.has(i)) m = fmaxf(m, row[at.expert(i)]);
     m = warp_max(m);
     double sum = 0;
 #pragma unroll 4
     for (int i = 0; i < PER; ++i)
-        if (at.has(i)) sum += exp(static_cast<double>(__ldg(row + at.expert(i))) - m);
+        if (at.has(i)) sum += exp(static_cast<double>(row[at.expert(i)]) - m);
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
     *largest = m;
     return sum;
@@ -214,9 +215,9 @@ __device__ __noinline__ double row_sum64(const SelectParams& p, int64_t t, float
 
 // What expert e goes by, in 64 bits.
 __device__ __noinline__ double value64(const SelectParams& p, int64_t t, int e, float m, double sum) {
-    const double l = __ldg(p.logits + t * p.E + e);
+    const double l = p.logits[t * p.E + e];
     const double s = p.softmax ? exp(l - m) / sum : 1 / (1 + exp(-l));
-    return p.bias ? s + __ldg(p.bias + e) : s;
+    return p.bias ? s + p.bias[e] : s;
 }
 
 // The experts of the set bits, one a lane, in list (at most 32; their number).
@@ -264,6 +265,7 @@ template <int PER, int U>
 __global__ void __launch_bounds__(kThreads) router_select_kernel(const __grid_constant__ SelectParams p) {
     __shared__ int lists[kThreads / 32][32];      // the experts left
     __shared__ __align__(16) double values[kThreads / 32][32];   // their values, in fp32 where that does
+    wait_earlier();
     const int lane = threadIdx.x & 31, grp = lane >> p.log_lanes, sub = lane & (p.lanes - 1);
     int* list = lists[threadIdx.x >> 5];
     double* wide = values[threadIdx.x >> 5];
@@ -431,11 +433,11 @@ __global__ void __launch_bounds__(kThreads) router_select_kernel(const __grid_co
         if (lane < n) {
             e = list[lane];
             if (!moe_check(e >= 0 && e < p.E, 1611)) e = 0;
-            l = __ldg(row + e);
+            l = row[e];
             x = fmaxf(l, -INFINITY);
             if (p.bias) {
                 const float s = fast_score(l, m, inv, sm);
-                x = fmaxf(s + __ldg(p.bias + e), -INFINITY);
+                x = fmaxf(s + p.bias[e], -INFINITY);
                 err = fmaf(fabsf(x), kStep, score_error(s, sm ? l - m : l, sm));
             }
         }
@@ -476,7 +478,7 @@ __global__ void __launch_bounds__(kThreads) router_select_kernel(const __grid_co
         rank = lane < p.k ? lane : 32;
         e = choose64<PER, U>(p, t);
         if (!moe_check(lane >= p.k || (e >= 0 && e < p.E), 1612)) e = 0;
-        l = lane < p.k ? __ldg(row + e) : 0.0f;
+        l = lane < p.k ? row[e] : 0.0f;
     }
     const bool chosen = rank < p.k;
     float s;
@@ -522,12 +524,12 @@ struct Chosen {
     __device__ __forceinline__ Chosen(const SelectBwdParams& p, int64_t t) {
         const int lane = threadIdx.x & 31;
         if (lane >= p.k) return;
-        const int i = __ldg(p.idx + t * p.k + lane);
-        const float dw = __ldg(p.dw + t * p.k + lane);
+        const int i = p.idx[t * p.k + lane];
+        const float dw = p.dw[t * p.k + lane];
         if (i < 0 || i >= p.E) return;
         e = i;
         g = dw * p.scale;
-        l = __ldg(p.logits + t * p.E + i);
+        l = p.logits[t * p.E + i];
     }
 };
 
@@ -566,6 +568,7 @@ __device__ __forceinline__ void put4(uint16_t* o, const float (&v)[4]) {
 // are written again behind the row.
 template <int Q, typename Out>
 __global__ void __launch_bounds__(kThreads) router_select_bwd4_kernel(const SelectBwdParams p) {
+    wait_earlier();
     const int lane = threadIdx.x & 31;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     if (t >= p.T) return;
@@ -578,7 +581,7 @@ __global__ void __launch_bounds__(kThreads) router_select_bwd4_kernel(const Sele
         const float4* row = reinterpret_cast<const float4*>(p.logits + t * p.E);
 #pragma unroll
         for (int i = 0; i < Q; ++i)
-            v[i] = lane + 32 * i < quads ? __ldg(row + lane + 32 * i)
+            v[i] = lane + 32 * i < quads ? row[lane + 32 * i]
                                          : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         m = -INFINITY;
 #pragma unroll
@@ -615,6 +618,7 @@ __global__ void __launch_bounds__(kThreads) router_select_bwd4_kernel(const Sele
 template <typename Out>
 __global__ void __launch_bounds__(kRowThreads) router_select_bwd_kernel(const SelectBwdParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
+    wait_earlier();
     Out* rows = reinterpret_cast<Out*>(smem);
     constexpr int W = kRowThreads / 32;
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
@@ -626,15 +630,15 @@ __global__ void __launch_bounds__(kRowThreads) router_select_bwd_kernel(const Se
         const bool dense = p.softmax && !p.renorm;
         if (dense) {
             m = -INFINITY;
-            for (int i = lane; i < p.E; i += 32) m = fmaxf(m, __ldg(row + i));
+            for (int i = lane; i < p.E; i += 32) m = fmaxf(m, row[i]);
             m = warp_max(m);
             float sum = 0.0f;
-            for (int i = lane; i < p.E; i += 32) sum += __expf(__ldg(row + i) - m);
+            for (int i = lane; i < p.E; i += 32) sum += __expf(row[i] - m);
             inv = 1.0f / warp_sum(sum);
         }
         const Chosen c(p, t);
         const float d = chosen_grad(p, c, m, inv, &all);
-        for (int i = lane; i < p.E; i += 32) put(mine + i, dense ? -(__expf(__ldg(row + i) - m) * inv) * all : 0.0f);
+        for (int i = lane; i < p.E; i += 32) put(mine + i, dense ? -(__expf(row[i] - m) * inv) * all : 0.0f);
         __syncwarp();
         if (c.e >= 0) put(mine + c.e, d);
     }
@@ -650,21 +654,19 @@ __global__ void __launch_bounds__(kRowThreads) router_select_bwd_kernel(const Se
 }
 
 template <typename Out>
-void start_backward(const SelectBwdParams& p, unsigned grid, cudaStream_t st) {
-    const int need = (p.E / 4 + 31) / 32;
-    if (p.E % 4)
-        router_select_bwd_kernel<Out><<<static_cast<unsigned>((p.T + kRowThreads / 32 - 1) / (kRowThreads / 32)),
-                                        kRowThreads, kRowThreads / 32 * p.E * sizeof(Out), st>>>(p);   // 32 KB at most
-    else if (need <= 1)
-        router_select_bwd4_kernel<1, Out><<<grid, kThreads, 0, st>>>(p);
-    else if (need <= 2)
-        router_select_bwd4_kernel<2, Out><<<grid, kThreads, 0, st>>>(p);
-    else if (need <= 3)
-        router_select_bwd4_kernel<3, Out><<<grid, kThreads, 0, st>>>(p);
-    else if (need <= 4)
-        router_select_bwd4_kernel<4, Out><<<grid, kThreads, 0, st>>>(p);
-    else
-        router_select_bwd4_kernel<8, Out><<<grid, kThreads, 0, st>>>(p);
+int start_backward(const SelectBwdParams& p, cudaStream_t st) {
+    const bool four = p.E % 4 == 0;
+    const int need = (p.E / 4 + 31) / 32, threads = four ? kThreads : kRowThreads;
+    const int64_t grid = (p.T + threads / 32 - 1) / (threads / 32);
+    if (grid >= (1ll << 31)) return MOE_EINVAL;
+    void (*kern)(SelectBwdParams) =
+        !four       ? router_select_bwd_kernel<Out>
+        : need <= 1 ? router_select_bwd4_kernel<1, Out>
+        : need <= 2 ? router_select_bwd4_kernel<2, Out>
+        : need <= 3 ? router_select_bwd4_kernel<3, Out>
+        : need <= 4 ? router_select_bwd4_kernel<4, Out>
+                    : router_select_bwd4_kernel<8, Out>;
+    return launch_early(kern, grid, threads, four ? 0 : threads / 32 * p.E * sizeof(Out), st, p);   // 32 KB at most
 }
 
 }  // namespace
@@ -712,8 +714,7 @@ int launch_router_select(const moe_routing_t& c, const float* logits, const floa
              : (need <= 4    ? router_select_kernel<4, 1>
                 : need <= 16 ? router_select_kernel<16, 1>
                              : router_select_kernel<32, 1>);
-    kern<<<static_cast<unsigned>(grid), kThreads, 0, st>>>(p);
-    if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
+    if (const int rc = launch_early(kern, grid, kThreads, 0, st, p)) return rc;
     trace_after(st, "router_select");
     return MOE_OK;
 }
@@ -731,13 +732,7 @@ int launch_router_select_backward(const moe_routing_t& c, const float* logits, c
     p.dw = dw;
     p.idx = idx;
     p.dlogits = dlogits;
-    const int64_t grid = (c.T + kThreads / 32 - 1) / (kThreads / 32);
-    if (grid >= (1ll << 31)) return MOE_EINVAL;
-    if (c.grad_f32)
-        start_backward<float>(p, static_cast<unsigned>(grid), st);
-    else
-        start_backward<uint16_t>(p, static_cast<unsigned>(grid), st);
-    if (cudaPeekAtLastError() != cudaSuccess) return MOE_ECUDA;
+    if (const int rc = c.grad_f32 ? start_backward<float>(p, st) : start_backward<uint16_t>(p, st)) return rc;
     trace_after(st, "router_select_bwd");
     return MOE_OK;
 }
