@@ -8,9 +8,10 @@
 // and are added up in their order by a second launch, so that a word with half of the
 // tokens costs no more than many words (the plan of 16384 of one word: 19 us).
 //   Every row of the gradient is written once, most of them zeros: 131072 x 6144 fp32 from
-// 16384 tokens 545 us, 6.3 TB/s (floor 504); zeros go out as bulk copies from one row of
-// shared memory, so that the sums keep the load and store units (all by stores: 562).
-// 50001 x 2048 from 8191 tokens with the plan: 58 us (floor 35), 12 of them the plan's four
+// 16384 tokens 483 us, 7.1 TB/s (a fill alone 412).  The zeros come from CTAs of their own
+// that start one behind the other and write region by region; written by a warp of every
+// CTA as bulk copies, all over the table at once, the same took 540, as stores 562.
+// 50001 x 2048 from 8191 tokens with the plan: 56 us (floor 35), 12 of them the plan's four
 // launches and 4.5 the joins'.  Lookup of 16384 rows of 6144 fp32 to bf16: 47.5 us.
 #include "common.cuh"
 #include "early.cuh"
@@ -317,6 +318,7 @@ struct GradParams {
     int64_t T, V;
     int d, chunks, spans;   // chunks of 8 channels; spans of 1024 channels a row
     int accumulate;
+    int adders, run;        // CTAs that add up; rows of a CTA of zeros
     bool wide, part_wide;   // dtable, the scratch rows on a 32-byte boundary
     float scale;
     const void* dout;
@@ -326,6 +328,8 @@ struct GradParams {
 constexpr int kSpan = 2;    // chunks a lane of a warp's 512 channels
 template <typename In>
 constexpr int kRows = sizeof(In) == 2 ? 4 : 2;   // rows that a warp has under way
+template <typename In>
+constexpr bool kAhead = sizeof(In) == 2;         // an only row is asked for an item ahead (fp32 would spill)
 
 template <typename Tab>
 __device__ __forceinline__ void finish(const GradParams& p, Tab* row, int c, float (&s)[8]) {
@@ -350,7 +354,8 @@ __device__ __forceinline__ int piece_token(const GradParams& p, const int4& q) {
 
 // One piece's sum over 512 channels.
 template <typename In, typename Tab>
-__device__ __forceinline__ void add_piece(const GradParams& p, const int4& q, int t, int c0) {
+__device__ __forceinline__ void add_piece(const GradParams& p, const int4& q, int t, int c0,
+                                          const Chunk<In> (&only)[kSpan]) {
     const int lane = threadIdx.x & 31;
     int at = lane;   // the token's place among the piece's
     if (q.w < 0 && q.z > 1) {   // as they came
@@ -366,6 +371,11 @@ __device__ __forceinline__ void add_piece(const GradParams& p, const int4& q, in
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[j][e] = 0.0f;
     constexpr int R = kRows<In>;
+    if (kAhead<In> && q.z == 1) {
+#pragma unroll
+        for (int j = 0; j < kSpan; ++j)
+            if (c0 + 32 * j < p.chunks) only[j].spread(s[j]);
+    } else
     for (int r0 = 0; r0 < q.z; r0 += R) {
         Chunk<In> f[R][kSpan];
 #pragma unroll
@@ -401,62 +411,72 @@ __device__ __forceinline__ void add_piece(const GradParams& p, const int4& q, in
     }
 }
 
-constexpr int kZeros = 8192;   // bytes of zeros that the rows of absent words are copied from
+constexpr int kAdders = 3;                    // CTAs that add up, an SM
+constexpr int64_t kZeros = 128 << 10;         // bytes of rows that a CTA of zeros looks after
 
-// One warp of a CTA writes rows of words that do not occur, as bulk copies of zeros, a lane
-// a row; the others add up the pieces, a span a time, the next item's tokens already loaded.
+// The first CTAs add up the pieces, a span a time, the next item's tokens already loaded,
+// and the row where that is one.  Those behind write zeros to the words that do not occur,
+// each to a run of rows, so that the machine writes one region after the other.
 template <typename In, typename Tab>
-__global__ void __launch_bounds__(256, 3) embedding_bwd_kernel(const GradParams p) {
-    __shared__ __align__(128) uint4 zeros[kZeros / 16];
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, adders = p.accumulate ? 8 : 7;
-    if (!p.accumulate) {
-        for (int i = threadIdx.x; i < kZeros / 16; i += 256) zeros[i] = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncthreads();
-    }
+__global__ void __launch_bounds__(256, kAdders) embedding_bwd_kernel(const GradParams p) {
     wait_earlier();
-    if (!p.accumulate) {
-        if (wid == adders) {
-            const int64_t bytes = p.d * static_cast<int64_t>(sizeof(Tab));
-            // short rows side by side, 32 a time, long ones from all CTAs in turn (131072 rows of
-            // 4 KB 81 us, in turn 89; of 24 KB 588 and 532)
-            const int log_run = bytes < 16384 ? 5 : 0;
-            const int64_t runs = (p.V + (1 << log_run) - 1) >> log_run;
-            for (int64_t k = lane; (k >> log_run) * gridDim.x + blockIdx.x < runs; k += 32) {
-                const int64_t id = (((k >> log_run) * gridDim.x + blockIdx.x) << log_run) + (k & ((1 << log_run) - 1));
-                if (id >= p.V || p.v.count[id] != 0) continue;
-                uint8_t* row = static_cast<uint8_t*>(p.dtable) + id * bytes;
-                for (int64_t o = 0; o < bytes; o += kZeros)
-                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(row + o),
-                                 "r"(smem_u32(zeros)),
-                                 "r"(static_cast<uint32_t>(bytes - o < kZeros ? bytes - o : kZeros))
-                                 : "memory");
-            }
-            bulk_commit();
-            bulk_wait_all();   // the zeros are read, and the rows written
-            return;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    if (static_cast<int>(blockIdx.x) >= p.adders) {
+        __shared__ unsigned absent[kZeros / 16 / 32];
+        const int64_t r0 = static_cast<int64_t>(blockIdx.x - p.adders) * p.run;
+        const int rows = static_cast<int>(p.V - r0 < p.run ? p.V - r0 : p.run);
+        const int each = p.d * static_cast<int>(sizeof(Tab)) / 16;   // 16-byte pieces of a row
+        uint4* to = static_cast<uint4*>(p.dtable) + r0 * each;
+        for (int i = threadIdx.x; i < (rows + 31) / 32 * 32; i += 256) {
+            const unsigned some = __ballot_sync(0xffffffffu, i < rows && p.v.count[r0 + i] == 0);
+            if (lane == 0) absent[i >> 5] = some;
         }
+        __syncthreads();
+        const int dr = 256 / each, dc = 256 % each;
+        int r = static_cast<int>(threadIdx.x) / each, c = static_cast<int>(threadIdx.x) % each;
+        while (r < rows) {
+            if (absent[r >> 5] >> (r & 31) & 1) to[static_cast<int64_t>(r) * each + c] = make_uint4(0, 0, 0, 0);
+            r += dr;
+            c += dc;
+            if (c >= each) {
+                c -= each;
+                ++r;
+            }
+        }
+        return;
     }
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * adders;
+    const int64_t warps = static_cast<int64_t>(p.adders) * 8;
     const int64_t items = static_cast<int64_t>(p.v.head[1]) * p.spans;
-    int64_t it = static_cast<int64_t>(wid) * gridDim.x + blockIdx.x;
+    int64_t it = static_cast<int64_t>(wid) * p.adders + blockIdx.x;
     if (it >= items) return;
-    int4 q = p.v.pieces[it / p.spans];
-    int t = piece_token(p, q);
+    Chunk<In> row[kSpan], row2[kSpan];
+    // the tokens of an item, and its row where that is one
+    auto fetch = [&](int64_t item, int4& q, int& t, Chunk<In> (&f)[kSpan]) {
+        q = p.v.pieces[item / p.spans];
+        t = piece_token(p, q);
+        if (kAhead<In> && q.z == 1) {
+            const int64_t from = __shfl_sync(0xffffffffu, t, 0);
+            const int c0 = static_cast<int>(item % p.spans) * 32 * kSpan + lane;
+#pragma unroll
+            for (int j = 0; j < kSpan; ++j)
+                if (c0 + 32 * j < p.chunks && moe_check(from < p.T, 1627))
+                    f[j].load(static_cast<const In*>(p.dout) + from * p.d + 8 * (c0 + 32 * j));
+        }
+    };
+    int4 q, q2;
+    int t, t2;
+    fetch(it, q, t, row);
     while (true) {
         const int64_t then = it + warps;
-        int4 q2 = q;
-        int t2 = t;
-        if (then < items) {
-            q2 = p.v.pieces[then / p.spans];
-            t2 = piece_token(p, q2);
-        }
+        if (then < items) fetch(then, q2, t2, row2);
         if (moe_check(q.x >= 0 && q.x < p.V && q.y + q.z <= p.T && q.z <= kPiece, 1628))
-            add_piece<In, Tab>(p, q, t, static_cast<int>(it % p.spans) * 32 * kSpan + lane);
+            add_piece<In, Tab>(p, q, t, static_cast<int>(it % p.spans) * 32 * kSpan + lane, row);
         if (then >= items) return;
         it = then;
         q = q2;
         t = t2;
+#pragma unroll
+        for (int j = 0; j < kSpan; ++j) row[j] = row2[j];
     }
 }
 
@@ -566,10 +586,12 @@ int launch_embedding_backward(const moe_embedding_t& c, const void* plan, const 
     p.wide = (reinterpret_cast<uintptr_t>(dtable) & 31) == 0;
     p.part_wide = (reinterpret_cast<uintptr_t>(p.v.part) & 31) == 0;
     int64_t need = c.T * p.spans;
-    need = (need + 6) / 7;
-    if (!c.accumulate && need < (c.V + 7) / 8) need = (c.V + 7) / 8;   // eight rows of zeros a CTA
-    const int64_t most = static_cast<int64_t>(sms) * 8;
-    const unsigned grid = static_cast<unsigned>(need < most ? need : most);
+    need = (need + 7) / 8;
+    const int64_t most = static_cast<int64_t>(sms) * kAdders;
+    p.adders = static_cast<int>(need < most ? need : most);
+    const int64_t run = kZeros / (static_cast<int64_t>(c.d) * (c.table_f32 ? 4 : 2));
+    p.run = static_cast<int>(run < 8 ? 8 : run);
+    const int64_t grid = p.adders + (c.accumulate ? 0 : (c.V + p.run - 1) / p.run);
     void (*kern)(GradParams) =
         c.out_f32 ? (c.table_f32 ? embedding_bwd_kernel<float, float> : embedding_bwd_kernel<float, uint16_t>)
                   : (c.table_f32 ? embedding_bwd_kernel<uint16_t, float> : embedding_bwd_kernel<uint16_t, uint16_t>);
