@@ -10,10 +10,10 @@
 // value is a matter of its own lanes.  Scores are computed in fp32 together with a bound
 // of their error; where the bound leaves a comparison that matters open, the few experts
 // that it hangs on are valued in 64 bits, and the whole row where they are many.
-//   16384 tokens of 384 experts in 8 groups, 8 chosen, sigmoid with bias: 19.0 us; the
+//   16384 tokens of 384 experts in 8 groups, 8 chosen, sigmoid with bias: 18.8 us; the
 // bytes are 3.9 us; some 1000 instructions a token bound it.  With k rounds of a warp-wide
 // maximum it took 70 us.  Without groups and bias 10 us.
-//   Gradient, 65536 x 384 in bf16, softmax of the row: 25.0 us, 22.9 of them memory's (the
+//   Gradient, 65536 x 384 in bf16, softmax of the row: 24.4 us, 22.9 of them memory's (the
 // logits in, the gradient out); the chosen ones looked up behind the row, 31.5.
 #include "common.cuh"
 #include "early.cuh"
@@ -516,20 +516,23 @@ __device__ __forceinline__ void put(uint16_t* o, float v) {
     *o = *reinterpret_cast<const uint16_t*>(&b);
 }
 
-// A lane's chosen expert (-1: none), the gradient of its weight and its logit, asked for
-// before the row so that the waits overlap.
+// A lane's chosen expert (-1: none), the gradient of its weight and its logit.  Asked for
+// before the row and, as the logit waits for the expert, behind it: the waits overlap
+// (65536 x 384: 24.4 us, asked for together 26.6).
 struct Chosen {
     int e = -1;
     float g = 0.0f, l = -INFINITY;
-    __device__ __forceinline__ Chosen(const SelectBwdParams& p, int64_t t) {
+    __device__ __forceinline__ void ask(const SelectBwdParams& p, int64_t t) {
         const int lane = threadIdx.x & 31;
         if (lane >= p.k) return;
-        const int i = p.idx[t * p.k + lane];
-        const float dw = p.dw[t * p.k + lane];
-        if (i < 0 || i >= p.E) return;
-        e = i;
-        g = dw * p.scale;
-        l = p.logits[t * p.E + i];
+        e = p.idx[t * p.k + lane];
+        g = p.dw[t * p.k + lane] * p.scale;
+    }
+    __device__ __forceinline__ void logit(const SelectBwdParams& p, int64_t t) {
+        if (e < 0 || e >= p.E)
+            e = -1;
+        else
+            l = p.logits[t * p.E + e];
     }
 };
 
@@ -575,7 +578,8 @@ __global__ void __launch_bounds__(kThreads) router_select_bwd4_kernel(const Sele
     Out* to = static_cast<Out*>(p.dlogits) + t * p.E;
     const int quads = p.E / 4;
     float m = 0.0f, inv = 0.0f, all = 0.0f, d;
-    const Chosen c(p, t);
+    Chosen c;
+    c.ask(p, t);
     if (p.softmax && !p.renorm) {
         float4 v[Q];
         const float4* row = reinterpret_cast<const float4*>(p.logits + t * p.E);
@@ -583,6 +587,7 @@ __global__ void __launch_bounds__(kThreads) router_select_bwd4_kernel(const Sele
         for (int i = 0; i < Q; ++i)
             v[i] = lane + 32 * i < quads ? row[lane + 32 * i]
                                          : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        c.logit(p, t);
         m = -INFINITY;
 #pragma unroll
         for (int i = 0; i < Q; ++i) m = fmaxf(m, fmaxf(fmaxf(v[i].x, v[i].y), fmaxf(v[i].z, v[i].w)));
@@ -606,6 +611,7 @@ __global__ void __launch_bounds__(kThreads) router_select_bwd4_kernel(const Sele
 #pragma unroll
         for (int i = 0; i < Q; ++i)
             if (lane + 32 * i < quads) put4(to + 4 * (lane + 32 * i), o);
+        c.logit(p, t);
         d = chosen_grad(p, c, m, inv, &all);
     }
     __syncwarp();   // the row is written
@@ -636,7 +642,9 @@ __global__ void __launch_bounds__(kRowThreads) router_select_bwd_kernel(const Se
             for (int i = lane; i < p.E; i += 32) sum += __expf(row[i] - m);
             inv = 1.0f / warp_sum(sum);
         }
-        const Chosen c(p, t);
+        Chosen c;
+        c.ask(p, t);
+        c.logit(p, t);
         const float d = chosen_grad(p, c, m, inv, &all);
         for (int i = lane; i < p.E; i += 32) put(mine + i, dense ? -(__expf(row[i] - m) * inv) * all : 0.0f);
         __syncwarp();
