@@ -884,18 +884,21 @@ def _at(t, dtype):
     return _ptr(t, dtype, allow_none=True)
 
 
-def _head_norm_config(q, k, table, pos, eps, interleaved):
-    if q.dim() != 3 or (k is not None and k.dim() != 3):
+def _head_norm_shapes(q, k, table, pos):
+    """The shapes of q, k and the weights; what HeadNorm needs of the rotation."""
+    qs, ks = q.shape, None if k is None else k.shape
+    if len(qs) != 3 or (ks is not None and len(ks) != 3):
         raise ValueError("q and k are [T, heads, D]")
-    T, hq, D = q.shape
-    rot, rows = 0, 0
+    T, _, D = qs
+    rot = rows = 0
     if table is not None:
-        if table.dim() != 3 or table.shape[2] != 2:
+        angles = table.shape
+        if len(angles) != 3 or angles[2] != 2:
             raise ValueError("the table is [positions, rot_dim / 2, 2]")
-        rot, rows = 2 * table.shape[1], table.shape[0]
+        rows, rot = angles[0], 2 * angles[1]
     if pos is not None and pos.shape != (T,):
         raise ValueError("pos is [T]")
-    return HeadNorm(T, hq, 0 if k is None else k.shape[1], D, rot, bool(interleaved), eps, rows)
+    return qs, ks and (T, ks[1], D), (D,), rot, rows
 
 
 def head_norm_rotary(q, k, w_q, w_k, table, pos, q_out, k_out, status, eps=1e-6,
@@ -904,14 +907,16 @@ def head_norm_rotary(q, k, w_q, w_k, table, pos, q_out, k_out, status, eps=1e-6,
     (w_k; None both: no keys), and its rotation as rotary's to the tokens'
     positions pos [T] int32 (None: 0, 1, ...), in one pass into q_out and k_out
     (which may be q and k).  table None: the norm alone."""
-    c = _head_norm_config(q, k, table, pos, eps, interleaved)
-    qs, ks, chan = (c.T, c.hq, c.D), (c.T, c.hk, c.D), (c.D,)
-    qp, c.q_t, c.q_h = _heads("q", q, qs)
-    qop, c.qo_t, c.qo_h = _heads("q_out", q_out, qs)
-    kp = kop = None
+    qs, ks, chan, rot, rows = _head_norm_shapes(q, k, table, pos)
+    T, hq, D = qs
+    qp, qt, qh = _heads("q", q, qs)
+    qop, qot, qoh = _heads("q_out", q_out, qs)
+    hk, kp, kt, kh, kop, kot, koh = 0, None, 0, 0, None, 0, 0
     if k is not None:
-        kp, c.k_t, c.k_h = _heads("k", k, ks)
-        kop, c.ko_t, c.ko_h = _heads("k_out", k_out, ks)
+        hk = ks[1]
+        kp, kt, kh = _heads("k", k, ks)
+        kop, kot, koh = _heads("k_out", k_out, ks)
+    c = HeadNorm(T, hq, hk, D, rot, bool(interleaved), eps, rows, qt, qh, kt, kh, qot, qoh, kot, koh)
     _check("moe_head_norm_rotary", lib().moe_head_norm_rotary(
         ctypes.byref(c), qp, kp, _rows("w_q", w_q, chan, _BF16),
         _rows("w_k", w_k, chan, _BF16, k is None), _at(table, f32),
@@ -931,17 +936,20 @@ def head_norm_rotary_backward(dq, dk, q, k, w_q, w_k, table, pos, dq_out, dk_out
     """Gradients of head_norm_rotary for dq, dk (of q_out, k_out), from the
     forward's q and k: dq_out, dk_out (each may be its dq, dk or q, k), dw_q,
     dw_k [D] fp32.  None exactly where the forward's tensor is."""
-    c = _head_norm_config(q, k, table, pos, eps, interleaved)
-    qs, ks, chan = (c.T, c.hq, c.D), (c.T, c.hk, c.D), (c.D,)
+    qs, ks, chan, rot, rows = _head_norm_shapes(q, k, table, pos)
+    T, hq, D = qs
     none = k is None
-    qp, c.q_t, c.q_h = _heads("q", q, qs)
-    dqp, c.dq_t, c.dq_h = _heads("dq", dq, qs)
-    qop, c.qo_t, c.qo_h = _heads("dq_out", dq_out, qs)
-    kp = dkp = kop = None
+    qp, qt, qh = _heads("q", q, qs)
+    dqp, dqt, dqh = _heads("dq", dq, qs)
+    qop, qot, qoh = _heads("dq_out", dq_out, qs)
+    hk, kp, kt, kh, dkp, dkt, dkh, kop, kot, koh = 0, None, 0, 0, None, 0, 0, None, 0, 0
     if not none:
-        kp, c.k_t, c.k_h = _heads("k", k, ks)
-        dkp, c.dk_t, c.dk_h = _heads("dk", dk, ks)
-        kop, c.ko_t, c.ko_h = _heads("dk_out", dk_out, ks)
+        hk = ks[1]
+        kp, kt, kh = _heads("k", k, ks)
+        dkp, dkt, dkh = _heads("dk", dk, ks)
+        kop, kot, koh = _heads("dk_out", dk_out, ks)
+    c = HeadNorm(T, hq, hk, D, rot, bool(interleaved), eps, rows, qt, qh, kt, kh, qot, qoh, kot, koh,
+                 dqt, dqh, dkt, dkh)
     _check("moe_head_norm_rotary_backward", lib().moe_head_norm_rotary_backward(
         ctypes.byref(c), dqp, dkp, qp, kp, _rows("w_q", w_q, chan, _BF16),
         _rows("w_k", w_k, chan, _BF16, none), _at(table, f32),
