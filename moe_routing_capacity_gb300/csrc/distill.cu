@@ -8,14 +8,17 @@
 // A team of threads takes a row.  One pass over it carries the running maximum and the sum
 // of exponentials (in base 2, the temperature folded into the factor), while one more warp
 // brings the entries; the gradient is a second pass, which writes q, and the entries' places
-// are written again behind that.  A short row stays in registers between the passes; of a
-// long one shared memory keeps a part, and L2 the rest.
-//   Forward of 4096 x 131072 bf16 (1.07 GB): 149 us, 7.2 TB/s.  Loss and gradient of 8192 x
-// 131072, a tenth of the rows without weight: 671 us, 6.1 TB/s of the 4.1 GB that have to
-// move; the exponentials alone (two a logit) are 460 us at 16 a cycle and SM, and the second
-// reading of the row is L2's.  A ring of chunks in the shared memory of a cluster, filled
-// and drained by bulk copies, moved nothing twice and took 950: a CTA's two passes and the
-// meeting between them follow each other, and only one fits on an SM.
+// are written again behind that.  A row of up to 2 KB stays in a warp's registers between
+// the passes; of one of more than 64 KB shared memory keeps a part; else the second pass
+// reads L2.
+//   Forward of 4096 x 131072 bf16 (1.07 GB): 149 us, 7.2 TB/s; of 10172 x 12288: 46, floor
+// 37.  Gradient alone of 15258 x 8192: 75, floor 74.  Loss and gradient of 8192 x 131072, a
+// tenth of the rows without weight: 671 us, 6.1 TB/s of the 4.1 GB that have to move; the
+// exponentials alone (two a logit) are 460 us at 16 a cycle and SM, and the second reading
+// of the row is L2's.  A ring of chunks in the shared memory of a cluster, filled and
+// drained by bulk copies, moved nothing twice and took 950: a CTA's two passes and the
+// meeting between them follow each other, and only one fits on an SM.  Rows of 12 to 64 KB
+// kept in the registers of 128 to 480 threads took 10 to 45 % more than read again.
 #include "common.cuh"
 #include "early.cuh"
 #include "internal.h"
@@ -423,16 +426,26 @@ template <typename Z, int MODE>
 int start(const DistillParams& p, cudaStream_t st) {
     int dev = 0, sms = 0;
     if (const int rc = current_device(&dev, &sms)) return rc;
-    // The smallest team whose registers hold the row, whether it reads it again or not: all
-    // of a row's loads are then under way at once (16384 rows of 3001 bf16, a warp of 12
-    // vectors 55 us, a CTA of 128 threads 79; 8192 of 16001, 256 threads 103, 512 154).
     const int64_t bytes = p.V * static_cast<int64_t>(sizeof(Z)), vectors = bytes / 16;
-    if (vectors <= 32 * 4) return start_team<Z, 32, MODE, 4, 0, 4>(p, st);
-    if (vectors <= 32 * 8) return start_team<Z, 32, MODE, 8, 0, 3>(p, st);
-    if (vectors <= 32 * 12) return start_team<Z, 32, MODE, 12, 0, 3>(p, st);
-    if (vectors <= 128 * 8) return start_team<Z, 128, MODE, 8, 0, 8>(p, st);
-    if (vectors <= 256 * 8) return start_team<Z, 256, MODE, 8, 0, 4>(p, st);
-    if (vectors <= 480 * 8) return start_team<Z, 480, MODE, 8, 0, 3>(p, st);
+    if (vectors <= 32 * 4) return start_team<Z, 32, MODE, 4, 0, 4>(p, st);   // a warp's registers hold the row
+    // Few threads a row leave little to a row's own waits and meetings, many keep the rows
+    // that are under way few, so that what is read again is still near.  (250 MB of bf16 rows of 8,
+    // 24, 64 KB: forward with 32, 128, 256, 512 threads 28, 37, 69, 153 us; 46, 46, 60, 97;
+    // 47, 44, 44, 53.  Loss and gradient 52, 60, 101, 225; 115, 83, 97, 155; 126, 105, 87, 88.)
+    constexpr int64_t K = 1024;
+    constexpr int64_t kWarp = MODE == kForward ? 20 * K : MODE == kBackward ? 6 * K : 8 * K;
+    constexpr int64_t kSmall = MODE == kForward ? 48 * K : MODE == kBackward ? 14 * K : 28 * K;
+    constexpr int64_t kMiddle = MODE == kForward ? int64_t{1} << 62 : MODE == kBackward ? 48 * K : 64 * K;
+    int team = bytes <= kWarp ? 32 : bytes <= kSmall ? 128 : bytes <= kMiddle ? 256 : 512;
+    // as many as there is room for where the rows are few, with four vectors each (5 rows of 8
+    // KB, forward, 128 threads 2.6 us, 512 3.4)
+    const int room = p.T <= 3 * sms ? 512 : p.T <= 7 * sms ? 256 : p.T <= 12 * sms ? 128 : 32;
+    const int most = vectors >= 2048 ? 512 : vectors >= 1024 ? 256 : vectors >= 256 || p.T <= 4 * sms ? 128 : 32;
+    const int wide = room < most ? room : most;
+    team = team < wide ? wide : team;
+    if (team == 32) return start_team<Z, 32, MODE, 0, 0, 5>(p, st);
+    if (team == 128) return start_team<Z, 128, MODE, 0, 0, 12>(p, st);
+    if (team == 256) return start_team<Z, 256, MODE, 0, 0, 7>(p, st);
     if (MODE != kStep) return start_team<Z, 512, MODE, 0, 0, 3>(p, st);
     // as many rows at once as half of L2 holds, and more of a longer row in shared memory
     // (8192 rows of 128 KB: 355 us with two CTAs an SM, 313 with three; of 256 KB: 668, 742)
