@@ -386,14 +386,29 @@ __global__ void __launch_bounds__(kThreads) router_select_kernel(const __grid_co
     }
     // A value that k experts reach: the k-th largest of the lanes' largest (equal ones go
     // together, which only lowers it).  Of 2 k lanes and more it leaves 1.4 k experts on
-    // average; with fewer, a lane goes on to its next value.
+    // average; with fewer, or so many that more than 32 may be left, the lanes' largest two
+    // decide, which leave 1.1 k (16 of 384 experts, 16384 tokens: 36.0 -> 19.3 us), and where
+    // those would be too few a lane goes on to its next value.
     uint32_t key = keep && at.room > 0 ? order_key(high) : 0u, reach = 0;
-    const bool deep = 2 * p.k > __popc(__ballot_sync(kAll, key != 0));
-    if (!deep) {
+    const int some = __popc(__ballot_sync(kAll, key != 0));
+    if (2 * p.k <= some && p.k <= 10) {
         for (int j = 0; j < p.k; ++j) {
             const uint32_t best = __reduce_max_sync(kAll, key);
             reach = best ? best : reach;
             key = key == best ? 0u : key;
+        }
+    } else if (4 * p.k <= 3 * some) {
+        float h1 = -INFINITY, h2 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) merge2(h1, h2, v[i], -INFINITY);
+        uint32_t next = keep && at.has(1) ? order_key(h2) : 0u;
+        for (int j = 0; j < p.k; ++j) {
+            const uint32_t best = __reduce_max_sync(kAll, key);
+            reach = best ? best : reach;
+            if (key == best) {
+                key = next;
+                next = 0u;
+            }
         }
     } else {
         for (int j = 0; j < p.k; ++j) {
