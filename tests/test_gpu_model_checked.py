@@ -65,7 +65,8 @@ def test_checked_build_clean_and_identical(checked_lib, monkeypatch):  # noqa: F
 
 def test_a_piece_of_no_word_is_recorded_and_skipped(checked_lib, monkeypatch):  # noqa: F811
     """A plan whose pieces name a word past the vocabulary: found in the plan by their
-    values, changed there; nothing of them is written."""
+    values, changed there; nothing of them is written (to a word that no piece of a small
+    plan names zeros are)."""
     monkeypatch.setattr(abi, "_lib", checked_lib)
     V, d = 50, 64
     ids = torch.arange(4, device="cuda", dtype=torch.int32) + 7
@@ -81,8 +82,6 @@ def test_a_piece_of_no_word_is_recorded_and_skipped(checked_lib, monkeypatch):  
     torch.cuda.synchronize()
     assert abi.lib().moe_check_status() == 1628 and abi.lib().moe_check_status() == 0
     skipped = int(host[hits[0]])
-    assert bool(out[skipped].isnan().all())
-    out[skipped] = 0
     want = torch.zeros_like(out)
     want[7:11] = 1
     want[skipped] = 0

@@ -389,6 +389,25 @@ def test_embedding_backward_skewed(rng, T, V, d, kind):
     check_embedding_backward(ids, randn(rng, T, d), V, F32)
 
 
+@pytest.mark.parametrize("T", [31, 32, 33, 63, 65, 257, 1023, 1024, 1025, 1100])
+@pytest.mark.parametrize("V,kind", [(1, "even"), (3, "often"), (200, "often"), (70000, "even")])
+def test_embedding_backward_of_few_tokens(rng, T, V, kind):
+    """Plans of one launch and of several, and one refilled after the other."""
+    d, plan = 72, None
+    for ids in (ints(rng, 0, V, T) if kind == "even" else words(rng, T, V, kind),
+                ints(rng, 0, V, T), torch.full((T,), -1, device="cuda", dtype=I32)):
+        ids[T // 3] = -1
+        dout = randn(rng, T, d)
+        if plan is None:
+            plan = abi.EmbeddingPlan(ids, V, d)
+        else:
+            plan.refill(ids)
+        got = torch.full((V, d), 7.0, device="cuda")
+        abi.embedding_backward(plan, dout, got, scale=0.6)
+        want, mag, most = R.embedding_backward(ids, dout, V, 0.6)
+        R.within("dtable", got, want, (most + 4) * R.STEP * (1 + R.U) * mag + R.round_of(F32) * want.abs())
+
+
 def test_embedding_sums_are_in_the_tokens_order(rng):
     """The plan's order is ascending within each word, whichever way the words are
     found: values whose sum tells the order."""
