@@ -12,7 +12,7 @@
 // walks over items (a token and a share of its heads) with a few rows under way that each
 // lane copies for itself (no barrier).  The forward folds weights and angles of an item
 // into four factors a pair, and steps pointers from row to row.
-//   Forward, 16384 x (48 + 8) x 128: 77 us, floor 69; 8192 x (16 + 4) x 128: 18.0 us, floor
+//   Forward, 16384 x (48 + 8) x 128: 77 us, floor 69; 8192 x (16 + 4) x 128: 17.4 us, floor
 // 12.4: some 180 instructions a warp's four rows, of which the 16 warps of an SM issue 45 %
 // of the time, and the start.  Items of all their rows in registers without a ring took 20.6
 // and 92, rows of weights and angles not folded 21.5 and 80.
