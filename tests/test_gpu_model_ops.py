@@ -640,3 +640,66 @@ def test_captured_on_another_stream_and_replayed(rng):
     assert int(buf["st"]) == 0
     for n in want:
         assert torch.equal(want[n], buf[n]), n
+
+
+@pytest.mark.parametrize("T", [5, 1500, 6000])
+def test_calls_behind_one_another_see_what_came_before(rng, T):
+    """Inputs written right before a call and again right behind it, outputs that are
+    the next call's inputs, scratch that the next call takes: as with waits between."""
+    hq, hk, D, E, k, V, d, K = 6, 2, 64, 64, 4, 900, 136, 7
+    rule = abi.Routing(E, k, score="softmax", n_groups=4, groups_kept=2, group_top=2, renorm=False)
+    sets = []
+    for _ in range(2):
+        x = head_inputs(rng, T, hq, hk, D, 64)
+        z, ti, ty, wt = distill_inputs(rng, T, V, K, BF)
+        sets.append(dict(q=x["q"], pos=x["pos"], wq=x["w_q"], logits=randn(rng, T, E, dt=F32),
+                         ids=words(rng, T, V, "often"), table=randn(rng, V, d), z=z, ti=ti, ty=ty, wt=wt))
+    key, w_k, table, bias = x["k"], x["w_k"], x["table"], randn(rng, E, std=0.01, dt=F32)
+    now = {n: t.clone() for n, t in sets[0].items()}
+    buf = dict(q=empty(T, hq, D), k=empty(T, hk, D), dq=empty(T, hq, D), dk=empty(T, hk, D), dwq=empty(D, dt=F32),
+               dwk=empty(D, dt=F32), idx=torch.zeros(T, k, device="cuda", dtype=I32), w=empty(T, k, dt=F32),
+               dl=empty(T, E, dt=F32), h=empty(T, d), dt=empty(V, d, dt=F32), loss=empty(T, dt=F32),
+               lse=empty(T, dt=F32), total=empty(1, dt=F32), dz=empty(T, V), dz2=empty(T, V), st=status())
+    ws = torch.empty(abi.head_norm_rotary_workspace(T, hq, hk, D), dtype=torch.uint8, device="cuda")
+    plan = abi.EmbeddingPlan(now["ids"], V, d)
+
+    def step(values, wait):
+        n, b = now, buf
+        for name, t in values.items():
+            n[name].copy_(t)
+        wait()
+        abi.head_norm_rotary(n["q"], key, n["wq"], w_k, table, n["pos"], b["q"], b["k"], b["st"])
+        wait()
+        abi.head_norm_rotary_backward(b["q"], b["k"], n["q"], key, n["wq"], w_k, table, n["pos"], b["dq"], b["dk"],
+                                      b["dwq"], b["dwk"], ws, b["st"])
+        wait()
+        abi.router_select(rule, n["logits"], bias, b["idx"], b["w"])
+        wait()
+        abi.router_select_backward(rule, n["logits"], b["idx"], b["w"], b["dl"])
+        wait()
+        abi.embedding(n["table"], n["ids"], b["h"], b["st"])
+        wait()
+        plan.refill(n["ids"])
+        wait()
+        abi.embedding_backward(plan, b["h"], b["dt"])
+        wait()
+        abi.distill_loss(n["z"], n["ti"], n["ty"], n["wt"], b["loss"], b["lse"], b["st"], total=b["total"],
+                         dlogits=b["dz"])
+        wait()
+        abi.distill_loss_backward(b["dz"], n["ti"], n["ty"], n["wt"], b["lse"], b["dz2"], b["st"])
+        wait()
+
+    want = []
+    for values in sets:
+        step(values, torch.cuda.synchronize)
+        want.append({n: t.clone() for n, t in buf.items()})
+    got = []
+    for i in range(24):
+        step(sets[i % 2], lambda: None)
+        got.append({n: t.clone() for n, t in buf.items()} if i % 5 == 3 else None)
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        for n in g or ():
+            same = torch.equal(g[n].nan_to_num() if g[n].is_floating_point() else g[n],
+                               want[i % 2][n].nan_to_num() if g[n].is_floating_point() else want[i % 2][n])
+            assert same, (i, n)
