@@ -266,6 +266,7 @@ __global__ void __launch_bounds__(kThreads) router_select_kernel(const __grid_co
     __shared__ int lists[kThreads / 32][32];      // the experts left
     __shared__ __align__(16) double values[kThreads / 32][32];   // their values, in fp32 where that does
     wait_earlier();
+    __shared__ float open[kThreads / 32][32 * PER];
     const int lane = threadIdx.x & 31, grp = lane >> p.log_lanes, sub = lane & (p.lanes - 1);
     int* list = lists[threadIdx.x >> 5];
     double* wide = values[threadIdx.x >> 5];
@@ -387,8 +388,10 @@ __global__ void __launch_bounds__(kThreads) router_select_kernel(const __grid_co
     // A value that k experts reach: the k-th largest of the lanes' largest (equal ones go
     // together, which only lowers it).  Of 2 k lanes and more it leaves 1.4 k experts on
     // average; with fewer, or so many that more than 32 may be left, the lanes' largest two
-    // decide, which leave 1.1 k (16 of 384 experts, 16384 tokens: 36.0 -> 19.3 us), and where
-    // those would be too few a lane goes on to its next value.
+    // decide, which leave 1.1 k (16 of 384 experts, 16384 tokens: 36.0 -> 19.1 us), spread
+    // over the warp first where few lanes have experts (7 of 2 of 8 groups of 55, softmax with
+    // bias, 26467 tokens: 63.6 -> 49.2 us); and of 25 and more a lane goes on to its next
+    // value.
     uint32_t key = keep && at.room > 0 ? order_key(high) : 0u, reach = 0;
     const int some = __popc(__ballot_sync(kAll, key != 0));
     if (2 * p.k <= some && p.k <= 10) {
@@ -397,11 +400,24 @@ __global__ void __launch_bounds__(kThreads) router_select_kernel(const __grid_co
             reach = best ? best : reach;
             key = key == best ? 0u : key;
         }
-    } else if (4 * p.k <= 3 * some) {
+    } else if (p.k <= 24) {
         float h1 = -INFINITY, h2 = -INFINITY;
+        uint32_t next;
+        if (4 * p.k <= 3 * some) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) merge2(h1, h2, v[i], -INFINITY);
-        uint32_t next = keep && at.has(1) ? order_key(h2) : 0u;
+            for (int i = 0; i < PER; ++i) merge2(h1, h2, v[i], -INFINITY);
+            next = key && at.has(1) ? order_key(h2) : 0u;
+        } else {   // the open groups' values over all lanes
+            const int slot = __popc(__ballot_sync(kAll, key != 0) & ((1u << lane) - 1u)), n = some * PER;
+            float* all_open = open[threadIdx.x >> 5];
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (key) all_open[i * some + slot] = v[i];
+            __syncwarp();
+            for (int i = lane; i < n; i += 32) merge2(h1, h2, all_open[i], -INFINITY);
+            key = lane < n ? order_key(h1) : 0u;
+            next = lane + 32 < n ? order_key(h2) : 0u;
+        }
         for (int j = 0; j < p.k; ++j) {
             const uint32_t best = __reduce_max_sync(kAll, key);
             reach = best ? best : reach;
