@@ -793,7 +793,8 @@ int moe_head_norm_rotary_backward(const moe_head_norm_t* cfg, const uint16_t* dq
  *   w_j = scale s_j, or scale s_j / sum of the chosen s (renorm; 0 where in 64
  *   bits that sum is 0).
  * The order is that of the exact values of v for the given l and bias (equal
- * ones: the lower index first), to the precision of 64 bits.  The bias has no
+ * ones: the lower index first), to the precision of 64 bits; without a bias the
+ * experts, and groups by one value, go by the logits themselves.  The bias has no
  * part in w.  NaN counts as the smallest value in the choice: idx always holds
  * top_k different experts.
  *   bias [n_experts] fp32 or NULL; idx [T, top_k] int32, w [T, top_k] fp32 (out)

@@ -135,7 +135,10 @@ __device__ __noinline__ int choose64(const SelectParams& p, int64_t t) {
         if (!(open >> i & 1)) continue;
         const double l = row[at.expert(i)];
         double x = same ? 0 : p.softmax ? exp(l - m) / sum : 1 / (1 + exp(-l));
-        if (p.bias) x += p.bias[at.expert(i)];
+        if (p.bias)
+            x += p.bias[at.expert(i)];
+        else if (!p.top2 && !same)
+            x = l;   // the scores' order, without their rounding: for the groups' largest as well
         key[i] = order_key64(x);
         if (key[i] > k1) {
             k2 = k1; b2 = b1;
@@ -143,7 +146,7 @@ __device__ __noinline__ int choose64(const SelectParams& p, int64_t t) {
         } else if (key[i] > k2) {
             k2 = key[i]; b2 = x;
         }
-        if (!p.bias && !same) key[i] = order_key64(l);   // the scores' order, without their rounding
+        if (!p.bias && !same) key[i] = order_key64(l);
     }
     if (p.kept < p.groups) {
         for (int o = 1; o < p.lanes; o <<= 1) {

@@ -232,6 +232,21 @@ def test_router_select_near_ties(rng, score):
         assert float((got - want).abs().max()) <= 2.0 ** -51
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("k", [6, 32])
+def test_router_select_scores_that_64_bits_round_to_one(rng, score, k):
+    """Without a bias the logits decide, in the groups as well, also where more experts
+    than a warp has lanes reach the k-th logit (several of the same)."""
+    T, E = 300, 960
+    rule = abi.Routing(E, k, score=score, n_groups=16, groups_kept=6, group_top=1)
+    logits = (randn(rng, T, E, dt=F32) * 4).round() * 10.0
+    idx, w = torch.empty(T, k, device="cuda", dtype=I32), empty(T, k, dt=F32)
+    abi.router_select(rule, logits, None, idx, w)
+    want, want_w = R.select(logits, None, rule)
+    assert torch.equal(idx.long(), want)
+    R.within("w", w, want_w, 128 * R.STEP * want_w + 2.0 ** -120)
+
+
 def test_router_select_values_that_are_not_finite(rng):
     """Always k different experts; masked experts (-inf) come last; NaN counts as
     the smallest; the weights of rows without NaN are as ever."""
