@@ -92,9 +92,10 @@ struct Run {
         }
         return m == -INFINITY ? 0.0f : m;
     }
-    __device__ __forceinline__ void add(float x) {
-        const float b = raise(x);
-        s = __fadd_rn(s, exp2_fast(__fsub_rn(x, b)));
+    // the exponent x c in one rounding with the maximum, which for the sum is what it is
+    __device__ __forceinline__ void add(float x, float c) {
+        const float b = raise(__fmul_rn(x, c));
+        s = __fadd_rn(s, exp2_fast(__fmaf_rn(x, c, -b)));
     }
     __device__ __forceinline__ void join(float om, float os) {
         const float b = raise(om);
@@ -134,8 +135,8 @@ constexpr int kUnroll = 4;   // vectors that a thread has under way
 // at the entries' words.  The arrays end in whole fours, without words behind the last.
 struct Entries {
     int* id;        // [K] the word, -1: not there
-    float *p, *x;   // [K] probability, exponent of the logit
-    float* y;       // [K] log2 of the teacher's probability
+    float *p, *x;   // [K] probability, the student's logit
+    float* y;       // [K] the teacher's logit, then log2 of its probability
     float* total;   // [K] p of all entries of the word, at its first; -1 at others
 };
 
@@ -150,22 +151,22 @@ __device__ __forceinline__ bool load_entries(const DistillParams& p, int64_t t, 
         if (!ok && i != -1) report_error(p.status, MOE_EINVAL);
         float y = -INFINITY;
         if (ok)
-            y = __fmul_rn(p.teacher_f32 ? static_cast<const float*>(p.teacher)[t * p.K + k]
-                                        : to_float(static_cast<const uint16_t*>(p.teacher)[t * p.K + k]), p.c);
+            y = p.teacher_f32 ? static_cast<const float*>(p.teacher)[t * p.K + k]
+                              : to_float(static_cast<const uint16_t*>(p.teacher)[t * p.K + k]);
         e.id[k] = ok ? i : -1;
         e.y[k] = y;
-        e.x[k] = ok ? __fmul_rn(to_float(z[i]), p.c) : 0.0f;
-        if (ok) ty.add(y);
+        e.x[k] = ok ? to_float(z[i]) : 0.0f;
+        if (ok) ty.add(y, p.c);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         ty.join(__shfl_xor_sync(0xffffffffu, ty.m, o), __shfl_xor_sync(0xffffffffu, ty.s, o));
     if (ty.m == -INFINITY && ty.s == 0.0f) return false;
-    const float inv = 1.0f / ty.s, lny = __fadd_rn(log2f(ty.s), ty.m);
+    const float inv = 1.0f / ty.s, logs = log2f(ty.s);
     for (int k = lane; k < (p.K + 3) / 4 * 4; k += 32) {
-        const float y = e.y[k];
-        e.p[k] = y == -INFINITY ? 0.0f : __fmul_rn(exp2_fast(__fsub_rn(y, ty.m)), inv);
-        e.y[k] = __fsub_rn(y, lny);
+        const float y = e.y[k], a = __fmaf_rn(y, p.c, -ty.m);
+        e.p[k] = y == -INFINITY ? 0.0f : __fmul_rn(exp2_fast(a), inv);
+        e.y[k] = __fsub_rn(a, logs);
     }
     return true;
 }
@@ -186,11 +187,12 @@ __device__ __forceinline__ void total_entries(const DistillParams& p, const Entr
     }
 }
 
-// sum_k p_k (log2 p_k - log2 q_k), by one warp.
-__device__ __forceinline__ float entries_loss(const DistillParams& p, const Entries& e, float lse2) {
+// sum_k p_k (log2 p_k - log2 q_k), by one warp; log2 q = (x c - m) - logs, from the row's
+// maximum and not from lse, so that a word near it loses nothing to the size of the logits.
+__device__ __forceinline__ float entries_loss(const DistillParams& p, const Entries& e, float m, float logs) {
     float loss = 0.0f;
     for (int k = threadIdx.x & 31; k < p.K; k += 32)
-        if (e.p[k] != 0.0f) loss = __fmaf_rn(e.p[k], __fsub_rn(e.y[k], __fsub_rn(e.x[k], lse2)), loss);
+        if (e.p[k] != 0.0f) loss = __fmaf_rn(e.p[k], __fsub_rn(e.y[k], __fsub_rn(__fmaf_rn(e.x[k], p.c, -m), logs)), loss);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
     return loss;
@@ -271,12 +273,12 @@ __global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM + 32, BLOCKS) distill_
             total_entries(p, en);
         }
     }
-    float lse2;   // log2 of the sum of exponentials
+    float m, inv = 1.0f;   // q = 2^(x c - m) inv; the gradient alone has log2 of the sum for m
     // the gradient alone goes on at once, unless it takes the place of logits that the
     // entries' warp may still be reading
     const bool meets = MODE != kBackward || static_cast<const void*>(z) == static_cast<void*>(dz);
     if (MODE == kBackward) {
-        lse2 = p.lse[t] * kLog2e;
+        m = p.lse[t] * kLog2e;
         if (meets) {
             team.sync();
             if (TEAM > 32) none = s_none;
@@ -284,8 +286,8 @@ __global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM + 32, BLOCKS) distill_
     } else {
         Run r;
         if (works) {
-            for (int64_t i = tid; i < head; i += TEAM) r.add(__fmul_rn(to_float(z[i]), p.c));
-            for (int64_t q = tail + tid; q < p.V; q += TEAM) r.add(__fmul_rn(to_float(z[q]), p.c));
+            for (int64_t i = tid; i < head; i += TEAM) r.add(to_float(z[i]), p.c);
+            for (int64_t q = tail + tid; q < p.V; q += TEAM) r.add(to_float(z[q]), p.c);
             auto take = [&](const uint4& v) {
                 float f[E];
                 spread(v, f);
@@ -321,20 +323,21 @@ __global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM + 32, BLOCKS) distill_
             }
         }
         r = team.join(r);
-        lse2 = __fadd_rn(r.m, log2f(r.s));
+        m = r.m;
+        inv = 1.0f / r.s;
         if (TEAM > 32) none = s_none;
         if (brings) {
-            const float loss = none ? 0.0f : entries_loss(p, en, lse2);
+            const float logs = log2f(r.s), loss = none ? 0.0f : entries_loss(p, en, m, logs);
             if ((tid & 31) == 0) {
                 p.loss[t] = none ? 0.0f : loss * kLn2 * (w * p.loss_f);
-                p.lse[t] = none ? 0.0f : lse2 * kLn2;
+                p.lse[t] = none ? 0.0f : __fadd_rn(m, logs) * kLn2;
             }
         }
     }
     if (MODE == kForward) return;
-    const float f = w * p.grad_f;
+    const float f = w * p.grad_f, fq = f * inv;
     if (works && !none) {
-        auto grad = [&](float x) { return f * exp2_fast(fmaf(x, p.c, -lse2)); };
+        auto grad = [&](float x) { return fq * exp2_fast(fmaf(x, p.c, -m)); };
         for (int64_t i = tid; i < head; i += TEAM) put(dz + i, grad(to_float(z[i])));
         auto give = [&](const uint4& v) {
             float g[E];
@@ -388,7 +391,7 @@ __global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM + 32, BLOCKS) distill_
     // the entries' words, behind the row
     for (int k = tid; k < p.K; k += TEAM) {
         const float total = en.total[k];
-        if (works && en.id[k] >= 0 && !(total < 0.0f)) put(dz + en.id[k], f * (exp2_fast(en.x[k] - lse2) - total));
+        if (works && en.id[k] >= 0 && !(total < 0.0f)) put(dz + en.id[k], f * (exp2_fast(fmaf(en.x[k], p.c, -m)) * inv - total));
     }
 }
 

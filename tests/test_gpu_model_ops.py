@@ -594,6 +594,26 @@ def test_distill_gradient_is_that_of_differences(rng):
         assert abs((f(z + d) - f(z - d)) / 2e-5 - float(dz[at])) < 1e-8
 
 
+@pytest.mark.parametrize("V", [700, 5001, 40000])
+@pytest.mark.parametrize("shift", [0.0, 512.0, -1024.0])
+def test_distill_loss_does_not_feel_a_shift_of_all_logits(rng, V, shift):
+    """Logits in whole 2^-10, so that the shift is exact: what is lost is by the
+    logits' differences (at most 32 here, 47 as exponents), not by their size."""
+    T, K = 33, 4
+    z = (randn(rng, T, V, std=2.0, dt=F32) * 1024).round() / 1024
+    z[:, 5] += 12.0                                     # a word that is nearly certain
+    ids, y = ints(rng, 0, V, T, K), (randn(rng, T, K, dt=F32) * 1024).round() / 1024
+    ids[:, 0] = 5
+    y[:, 0] += 12.0
+    ref = R.distill(z, ids, y, None, 1.0, 1.0)
+    loss, lse, dz, st = empty(T, dt=F32), empty(T, dt=F32), empty(T, V, dt=F32), status()
+    abi.distill_loss(z + shift, ids, y + shift, None, loss, lse, st, dlogits=dz)
+    # differences in one rounding of 47 each, the sums' logarithms, an exponential's 4 and 1.5
+    # of its argument, sums in V / 128 + 64 roundings at most
+    assert float((loss - ref["loss"][0]).abs().max()) < (4 * 47 + 4 + 1.5 * 47 + V / 128 + 64) * R.STEP
+    assert float((dz - ref["dz"][0]).abs().max()) < 2 * (4 + 1.5 * 47 + V / 128 + 64) * R.STEP
+
+
 # ------------------------------------------------------------------ streams and graphs
 
 def test_captured_on_another_stream_and_replayed(rng):
