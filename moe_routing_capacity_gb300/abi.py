@@ -1081,12 +1081,17 @@ def _logits(name, t, shape, dtype):
     return t.data_ptr(), t.stride(0)
 
 
-def _distill_config(logits, ids, teacher, temperature, scale):
-    if logits.dim() != 2 or ids.dim() != 2 or logits.dtype not in _RES:
+def _distill_args(logits, ids, teacher, dlogits, temperature, scale):
+    """(configuration, addresses of logits and dlogits, shapes of entries and tokens)."""
+    zs, given, dt = logits.shape, ids.shape, logits.dtype
+    if len(zs) != 2 or len(given) != 2 or dt not in _RES:
         raise ValueError("logits is [T, V] bf16 or fp32, ids [T, K]")
-    (T, V), K = logits.shape, ids.shape[1]
-    return (T, K), Distill(T, V, 0, 0, K, logits.dtype == f32, teacher.dtype == f32, temperature,
-                           scale)
+    T, V = zs
+    K = given[1]
+    zp, z_ld = _logits("logits", logits, zs, dt)
+    dp, dz_ld = (None, 0) if dlogits is None else _logits("dlogits", dlogits, zs, dt)
+    c = Distill(T, V, z_ld, dz_ld, K, dt == f32, teacher.dtype == f32, temperature, scale)
+    return c, zp, dp, (T, K), (T,)
 
 
 def distill_loss(logits, ids, teacher, weight, loss, lse, status, total=None, dlogits=None,
@@ -1097,12 +1102,7 @@ def distill_loss(logits, ids, teacher, weight, loss, lse, status, total=None, dl
     strided), both at that temperature; weight [T] fp32 or None.  loss, lse [T]
     fp32; total [1] fp32 receives the losses' sum, dlogits (may be logits) their
     gradient in the same pass.  Rows without weight or entries have loss 0."""
-    given, c = _distill_config(logits, ids, teacher, temperature, scale)
-    zp, c.z_ld = _logits("logits", logits, (c.T, c.V), logits.dtype)
-    dp = None
-    if dlogits is not None:
-        dp, c.dz_ld = _logits("dlogits", dlogits, (c.T, c.V), logits.dtype)
-    tok = given[:1]
+    c, zp, dp, given, tok = _distill_args(logits, ids, teacher, dlogits, temperature, scale)
     _check("moe_distill_loss", lib().moe_distill_loss(
         ctypes.byref(c), zp, _rows("ids", ids, given, _I32), _rows("teacher", teacher, given, _RES),
         _rows("weight", weight, tok, _F32, True), _rows("loss", loss, tok, _F32),
@@ -1114,10 +1114,9 @@ def distill_loss_backward(logits, ids, teacher, weight, lse, dlogits, status, te
                           scale=1.0, stream=None):
     """dlogits (may be logits): gradient of distill_loss's summed loss, from the
     forward's inputs and lse."""
-    given, c = _distill_config(logits, ids, teacher, temperature, scale)
-    zp, c.z_ld = _logits("logits", logits, (c.T, c.V), logits.dtype)
-    dp, c.dz_ld = _logits("dlogits", dlogits, (c.T, c.V), logits.dtype)
-    tok = given[:1]
+    if dlogits is None:
+        raise ValueError("dlogits: tensor required")
+    c, zp, dp, given, tok = _distill_args(logits, ids, teacher, dlogits, temperature, scale)
     _check("moe_distill_loss_backward", lib().moe_distill_loss_backward(
         ctypes.byref(c), zp, _rows("ids", ids, given, _I32), _rows("teacher", teacher, given, _RES),
         _rows("weight", weight, tok, _F32, True), _rows("lse", lse, tok, _F32), dp,
