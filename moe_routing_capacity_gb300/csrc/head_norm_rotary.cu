@@ -104,14 +104,15 @@ __device__ __forceinline__ const float* angle(const HeadParams& p, int64_t pos, 
     return p.table + (pos * p.half + pair) * 2;
 }
 
+// The angles that turn back.
 template <bool PAIRS>
-__device__ __forceinline__ void load_angles(const HeadParams& p, int64_t pos, int u, float sign,
-                                            float2 (&c)[4], float2 (&s)[4]) {
+__device__ __forceinline__ void load_angles(const HeadParams& p, int64_t pos, int u, float2 (&c)[4],
+                                            float2 (&s)[4]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float4 v = *reinterpret_cast<const float4*>(angle<PAIRS>(p, pos, u, e));
         c[e] = make_float2(v.x, v.z);
-        s[e] = make_float2(sign * v.y, sign * v.w);
+        s[e] = make_float2(-v.y, -v.w);
     }
 }
 
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) head_norm_bwd_kernel(const 
             if (gone)
                 report_error(p.status, MOE_EINVAL);
             else if (pl.rot)
-                load_angles<PAIRS>(p, pos, u, -1.0f, c, s);
+                load_angles<PAIRS>(p, pos, u, c, s);
         }
         float2 f[8], ss = make_float2(0.0f, 0.0f);
         unpack(*ring.at(stage, 0), *ring.at(stage, 1), f);
