@@ -20,6 +20,7 @@
 // 31.8, floor 18.5.  The forward's stepped pointers would spill here (492 and 34).
 #include "common.cuh"
 #include "early.cuh"
+#include "head_split.h"
 #include "internal.h"
 
 namespace moe {
@@ -35,7 +36,7 @@ struct HeadParams {
     int64_t T, table_rows;
     int hq, hk, D, units, rot_units, half;   // units: 16-channel pieces of a head
     int q_splits, k_splits;                  // parts of a token's query heads, key heads
-    int q_each, k_each;                      // heads of a part
+    int q_each, k_each;                      // heads of a part, the last one's fewer (forward)
     int64_t q_items, items;                  // tokens times parts: the query heads', all
     Rows x_q, x_k, dy_q, dy_k, y_q, y_k;     // inputs, upstream gradients, outputs
     const uint16_t *w_q, *w_k;
@@ -355,7 +356,11 @@ struct Run {
                 part = static_cast<int>(i - t * splits);
             }
         }
-        const int h = part * each, n = (keys ? p.hk : p.hq) - h;
+        int h = part * each, n = (keys ? p.hk : p.hq) - h;
+        if (!moe_check(n > 0, 1603)) {   // the walk ends where left comes to zero
+            h = 0;
+            n = 1;
+        }
         const Rows& r = OUT ? (keys ? p.y_k : p.y_q) : (keys ? p.x_k : p.x_q);
         left = n < each ? n : each;
         step = r.h;
@@ -550,26 +555,29 @@ HeadParams head_params(const moe_head_norm_t& c) {
 
 int lanes_of(int units) { return units <= 4 ? 4 : units <= 8 ? 8 : units <= 16 ? 16 : 32; }
 
-// The heads of a token are split over several groups of lanes until four items fall to
-// each resident group, down to eight heads an item (8192 tokens of 20 heads: 18.0 us, four
-// heads an item 19.9, sixteen 17.4; the gradient 31.8, 32.4, 31.6, but of 4096 tokens 13.9,
-// 15.1, 18.2); to one head where all heads are under way at once.
-void head_splits(HeadParams* p, int lanes, int sms) {
-    const int64_t have = p->T * lanes, room = static_cast<int64_t>(sms) * kBlocks * kThreads;
-    const int64_t want = (4 * room + have - 1) / have, heads = p->hq + p->hk;
-    const int least = have * heads <= room ? 1 : 8;
-    auto part = [&](int n) {   // the kind's share of the groups
-        int64_t s = (want * n + heads - 1) / heads;
-        const int64_t most = (n + least - 1) / least;
-        s = s > most ? most : s;
-        return static_cast<int>(s < 1 ? (n > 0) : s);
-    };
-    p->q_splits = part(p->hq);
-    p->k_splits = part(p->hk);
-    p->q_each = (p->hq + p->q_splits - 1) / p->q_splits;
-    p->k_each = p->hk ? (p->hk + p->k_splits - 1) / p->k_splits : 0;
+void set_items(HeadParams* p) {
     p->q_items = p->T * p->q_splits;
     p->items = p->q_items + p->T * p->k_splits;
+}
+
+// The parts of a token's heads: of each kind every q_splits-th, k_splits-th head (the
+// gradient).
+void head_strides(HeadParams* p, int lanes, int sms) {
+    const HeadParts parts = head_parts(p->T, p->hq, p->hk, lanes, static_cast<int64_t>(sms) * kBlocks * kThreads);
+    p->q_splits = parts.q;
+    p->k_splits = parts.k;
+    set_items(p);
+}
+
+// Runs of neighbours (the forward).
+void head_neighbours(HeadParams* p, int lanes, int sms) {
+    const HeadParts parts = head_parts(p->T, p->hq, p->hk, lanes, static_cast<int64_t>(sms) * kBlocks * kThreads);
+    const HeadRuns q = head_runs(p->hq, parts.q), k = head_runs(p->hk, parts.k);
+    p->q_splits = q.runs;
+    p->q_each = q.each;
+    p->k_splits = k.runs;
+    p->k_each = k.each;
+    set_items(p);
 }
 
 constexpr int kMaxParts = kBlocks * 160;   // blocks of a backward launch, on a device of 160 SMs at most
@@ -618,7 +626,7 @@ int launch_head_norm(const moe_head_norm_t& c, const uint16_t* q, const uint16_t
     p.pos = pos;
     p.status = status;
     const int lanes = lanes_of(p.units);
-    head_splits(&p, lanes, sms);
+    head_neighbours(&p, lanes, sms);
     if (const int rc = begin_forward_any(p, c.interleaved, lanes, sms, st)) return rc;
     trace_after(st, "head_norm_rotary");
     return MOE_OK;
@@ -645,7 +653,7 @@ int launch_head_norm_backward(const moe_head_norm_t& c, const uint16_t* dq, cons
     p.part = static_cast<float*>(ws);
     p.status = status;
     const int lanes = lanes_of(p.units);
-    head_splits(&p, lanes, sms);
+    head_strides(&p, lanes, sms);
     int grid = 0;
     if (const int rc = begin_backward_any(p, c.interleaved, lanes, sms, &grid, st)) return rc;
     trace_after(st, "head_norm_rotary_bwd");
