@@ -1,4 +1,6 @@
-"""Head norms of many heads against the plain 64-bit implementation."""
+"""Head norms where a group of lanes goes from item to item (several heads an item, several
+items a group, query heads and then key heads), and of many heads, against the plain 64-bit
+implementation."""
 import pytest
 import torch
 
@@ -12,9 +14,11 @@ F32 = torch.float32
 
 #          T     hq   hk   D    rot
 # more than 80 heads: runs of neighbours that do not come out even (128 heads in 14 parts
-# of 10, 81 in 10 of 9 on 152 SMs)
+# of 10, 81 in 10 of 9 on 152 SMs); then several items a group
 ITEMS = [(2900, 128, 8, 128, 128), (1450, 128, 128, 128, 64), (4001, 81, 8, 128, 128), (300, 200, 3, 64, 64),
-         (3, 1000, 1, 64, 32)]
+         (3, 1000, 1, 64, 32), (8192, 16, 4, 128, 128), (3000, 128, 8, 128, 128), (12001, 6, 2, 128, 64),
+         (30011, 3, 1, 64, 64), (30000, 8, 8, 64, 64), (9001, 20, 0, 128, 0), (5003, 7, 5, 264, 16),
+         (2503, 9, 3, 512, 512), (20001, 2, 3, 72, 48)]
 
 
 def inputs(g, T, hq, hk, D, rot):
