@@ -273,9 +273,9 @@ constexpr float kStep = 5.9604645e-8f;   // 2^-24
 // Bound of a fast score's error.  arg is the exponential's argument: its product with
 // log2(e) is off by 1.5 steps of |arg|, the exponential by 4, the sum and the division by
 // 3, the sum of a softmax's row by fewer than 48 (rounded up for both); what underflows is
-// below 1e-36.
+// below 1e-36.  Of a logit of -infinity, whose score is 0, that alone is left, and not NaN.
 __device__ __forceinline__ float score_error(float s, float arg, bool softmax) {
-    return fmaf(s, (softmax ? 64.0f : 8.0f) * kStep + 1.5f * kStep * fabsf(arg), 1e-36f);
+    return fmaf(s, (softmax ? 64.0f : 8.0f) * kStep + 1.5f * kStep * fminf(fabsf(arg), 3e38f), 1e-36f);
 }
 
 // 1 / x for 1 <= x, infinity among them, off by a step.
