@@ -52,6 +52,7 @@ class TrainingModel:
         self.plan = abi.EmbeddingPlan(torch.full((T,), -1, dtype=torch.int32, device=dev),
                                       self.vocab, d, self.status)
         self.ids = None
+        self.batch = torch.empty(2, T, dtype=torch.int32, device=dev)   # its ids and positions
         self.h0, self.n, self.dn, self.dh = e(T, d), e(T, d), e(T, d), e(T, d)
         self.rstd = e(T, dt=F32)
         self.z = e(T, self.vocab)
@@ -61,11 +62,19 @@ class TrainingModel:
 
     def set_batch(self, ids, cu_seqlens, pos, stream=None):
         """The batch: its tokens' ids [T] int32 (-1: none), packed sequences
-        (cu_seqlens [sequences + 1]) and positions [T], int32 on the device."""
+        (cu_seqlens [sequences + 1]) and positions [T] (or None: 0, 1, ...), int32 on
+        the device.  It is copied on the stream, so that a step looks up the words
+        that its plan was made from whatever the caller's tensors hold by then."""
+        if pos is not None:
+            abi._rows("pos", pos, (self.T,), abi._I32)
         self.plan.refill(ids, stream)
-        self.ids = ids
+        with abi.on_stream(stream):
+            self.batch[0].copy_(ids)
+            if pos is not None:
+                self.batch[1].copy_(pos)
+        self.ids = self.batch[0]
         for b in self.blocks:
-            b.set_batch(cu_seqlens, pos, stream)
+            b.set_batch(cu_seqlens, None if pos is None else self.batch[1], stream)
 
     def forward(self, stream=None):
         """Logits z [T, vocab] of the batch (the buffer that step() overwrites)."""
