@@ -59,6 +59,8 @@ class TrainingModel:
         self.loss, self.lse, self.total = e(T, dt=F32), e(T, dt=F32), e(1, dt=F32)
         self.g = {n: e(*t.shape, dt=F32) for n, t in self.w.items()}
         self.ws_norm = e(abi.norm_residual_workspace(T, d), dt=torch.uint8)
+        self.made = torch.cuda.Event()   # behind what was queued so far, a plan of no words among it
+        self.made.record(torch.cuda.current_stream(dev))
 
     def set_batch(self, ids, cu_seqlens, pos, stream=None):
         """The batch: its tokens' ids [T] int32 (-1: none), packed sequences
@@ -67,6 +69,12 @@ class TrainingModel:
         that its plan was made from whatever the caller's tensors hold by then."""
         if pos is not None:
             abi._rows("pos", pos, (self.T,), abi._I32)
+        with abi.on_stream(stream):
+            # the first batch's stream may be another than the model was made on (a capture
+            # begins with the device idle)
+            if self.made is not None and not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream(self.batch.device).wait_event(self.made)
+                self.made = None
         self.plan.refill(ids, stream)
         with abi.on_stream(stream):
             self.batch[0].copy_(ids)

@@ -2,6 +2,8 @@
 import pytest
 import torch
 
+from moe_routing_capacity_gb300.model import TrainingModel
+
 from test_gpu_training_model import make_model
 
 pytestmark = pytest.mark.gpu
@@ -43,3 +45,22 @@ def test_a_batch_of_other_shapes_or_types_is_refused():
         m.set_batch(mine[:5], cu, pos)
     m.set_batch(mine, cu, None)                     # positions 0, 1, ...
     assert all(b.pos is None for b in m.blocks)
+
+
+def test_the_first_batch_on_another_stream_than_the_models():
+    """The model is made on a stream that is still busy, its first batch set and run on
+    another: what making it queued (a plan of no words, a cleared status) comes first."""
+    m, ids, entries, teacher, weight = make_model()
+    want = {n: t.clone() for n, t in m.step(entries, teacher, weight).items()}
+    mine, cu, pos = batch(m, ids)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(100_000_000)                  # some 50 ms
+    late = TrainingModel(m.blocks, m.w, embed_scale=m.embed_scale)
+    late.set_batch(mine, cu, pos, stream=side)
+    for _ in range(2):
+        got = late.step(entries, teacher, weight, stream=side)
+        torch.cuda.synchronize()
+        for n in want:
+            assert torch.equal(got[n], want[n]), n
+        assert int(late.status) == 0
