@@ -449,11 +449,14 @@ int start(const DistillParams& p, cudaStream_t st) {
     if (team == 32) return start_team<Z, 32, MODE, 0, 0, 5>(p, st);
     if (team == 128) return start_team<Z, 128, MODE, 0, 0, 12>(p, st);
     if (team == 256) return start_team<Z, 256, MODE, 0, 0, 7>(p, st);
-    if (MODE != kStep) return start_team<Z, 512, MODE, 0, 0, 3>(p, st);
-    // as many rows at once as half of L2 holds, and more of a longer row in shared memory
-    // (8192 rows of 128 KB: 355 us with two CTAs an SM, 313 with three; of 256 KB: 668, 742)
-    if (bytes * 3 * sms <= (64ll << 20)) return start_team<Z, 480, MODE, 0, 4, 3>(p, st);
-    return start_team<Z, 512, MODE, 0, 8, 2>(p, st);
+    if constexpr (MODE == kStep) {
+        // as many rows at once as half of L2 holds, and more of a longer row in shared memory
+        // (8192 rows of 128 KB: 355 us with two CTAs an SM, 313 with three; of 256 KB: 668, 742)
+        if (bytes * 3 * sms <= (64ll << 20)) return start_team<Z, 480, MODE, 0, 4, 3>(p, st);
+        return start_team<Z, 512, MODE, 0, 8, 2>(p, st);
+    } else {
+        return start_team<Z, 512, MODE, 0, 0, 3>(p, st);
+    }
 }
 
 DistillParams distill_params(const moe_distill_t& c, const void* z, const int32_t* ids,
