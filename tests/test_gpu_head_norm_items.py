@@ -8,6 +8,8 @@ import model_reference as R
 import test_gpu_model_ops as ops
 from moe_routing_capacity_gb300 import abi
 
+from test_gpu_block_checked import checked_lib  # noqa: F401
+
 pytestmark = pytest.mark.gpu
 
 F32 = torch.float32
@@ -90,3 +92,24 @@ def test_backward(T, hq, hk, D, rot, pairs, in_place):
         assert bool(same.all())
         R.within("d" + n, res[n][~out], dx[~out], dx_b[~out])
         R.within("dw_" + n, dw[n], w, w_b)
+
+
+def test_checked_build(checked_lib, monkeypatch):  # noqa: F811
+    """No check of a head fires, and the outputs are the normal build's bit for bit."""
+    def run():
+        got = []
+        for T, hq, hk, D, rot in ITEMS[:8]:
+            x, _ = inputs(torch.Generator(device="cuda").manual_seed(T), T, hq, hk, D, rot)
+            q, k, st = ops.empty(T, hq, D), ops.empty(T, hk, D), ops.status()
+            abi.head_norm_rotary(x["q"], x["k"], x["w_q"], x["w_k"], x["table"], x["pos"], q, k, st)
+            got += [q, k]
+        torch.cuda.synchronize()
+        return got, abi.lib().moe_check_status()
+
+    want, code = run()
+    assert code == 0
+    monkeypatch.setattr(abi, "_lib", checked_lib)
+    got, code = run()
+    assert code == 0, f"index check site {code} fired"
+    for a, b in zip(want, got):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
