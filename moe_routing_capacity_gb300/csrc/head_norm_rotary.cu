@@ -15,7 +15,7 @@
 //   Forward, 16384 x (48 + 8) x 128: 77 us, floor 69; 8192 x (16 + 4) x 128: 17.4 us, floor
 // 12.4: some 180 instructions a warp's four rows, of which the 16 warps of an SM issue 45 %
 // of the time, the start, and uneven shares (24576 items of 8, 8 and 4 heads over 9728 groups
-// give 5120 of them 20 rows, 1536 16 and 3072 12, where 16.8 is even).  Items of all their rows
+// give 5120 of them 20 rows, 1536 16 and the others 12, where 16.8 is even).  Items of all their rows
 // in registers without a ring took 20.6 and 92, rows of weights and angles not folded 21.5
 // and 80.
 //   Backward, 65536 x (48 + 8) x 128: 444 us, floor 415, 6.3 TB/s: memory.  8192 x (16 + 4):
